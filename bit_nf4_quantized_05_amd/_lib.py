@@ -20,6 +20,7 @@ LIB_PATH = os.path.join(_HERE, "libqlora_nf4.so")
 _c_i64 = ctypes.c_int64
 _c_int = ctypes.c_int
 _c_float = ctypes.c_float
+_c_double = ctypes.c_double
 _c_vp = ctypes.c_void_p
 
 # name -> (restype, argtypes); mirrors include/qlora_nf4.h
@@ -58,6 +59,12 @@ SIGNATURES = {
     "qlr_linear_fwd": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_int, _c_int, _c_vp, _c_vp, _c_int,
                                 _c_vp, _c_vp, _c_int, _c_float, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64,
                                 _c_vp]),
+    "qlora_adamw_blocks": (_c_i64, [_c_vp, _c_int]),
+    "qlora_adamw_table_bytes": (_c_i64, [_c_vp, _c_int]),
+    "qlora_adamw_table": (_c_i64, [_c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_int, _c_vp]),
+    "qlora_adamw_step": (_c_int, [_c_vp, _c_int, _c_i64, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp, _c_double,
+                                  _c_vp, _c_double, _c_double, _c_double, _c_double, _c_vp, ctypes.c_uint32, _c_vp]),
+    "qlora_adamw_moments": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp, _c_vp, _c_vp]),
     "qn_profile_enable": (_c_int, [_c_int]),
     "qn_profile_read": (_c_int, [_c_vp, _c_int, _c_vp, _c_vp, _c_int]),
     "qn_profile_durations": (_c_int, [ctypes.c_char_p, _c_vp, _c_int]),
@@ -456,3 +463,139 @@ def qlr_linear_fwd(q: NF4Weight, Af: QFactor, Bf: QFactor, s: float, X: torch.Te
                               ws.numel() * ws.element_size(), _stream(dev))
     _check(rc, "qlr_linear_fwd")
     return o
+
+
+# ---- AdamW over many tensors -----------------------------------------------------
+
+ADAMW_BLOCK = 256     # elements per state block
+_STATES_8, _GRAD_BF16, _PARAM_BF16 = 1, 2, 4
+
+
+@dataclass
+class AdamWState:
+    """The tensors of an AdamW step, their moments and the device table that lists them,
+    as made by ``adamw_state``. Tensor i's moments are the elements [offsets[i],
+    offsets[i] + numel) of m and v (values with bits 32, codes with bits 8: ``adamw_moments``
+    gives their values). The tensors are kept, not copied; ``set_grads`` names other
+    gradient tensors."""
+    params: list
+    grads: list
+    copies: list | None
+    bits: int
+    m: torch.Tensor                 # float32 or uint8 [256 * blocks]
+    v: torch.Tensor
+    m_scale: torch.Tensor | None    # float32 [blocks] (bits 8)
+    v_scale: torch.Tensor | None
+    offsets: list
+    blocks: int
+    flags: int
+    table: torch.Tensor             # uint8, device
+    n_chunks: int
+
+    @property
+    def device(self) -> torch.device:
+        return self.m.device
+
+    def set_grads(self, grads) -> None:
+        """Uses these gradients (same shapes and type) from the next step on; the table is
+        built again and copied to the device, so keep gradient buffers where possible."""
+        grads = list(grads)
+        if _adamw_flags(self.params, grads, self.copies, self.bits) != self.flags:
+            raise TypeError("the gradients' type must stay the same")
+        self.table, self.n_chunks = _adamw_table(self.params, grads, self.copies, self.flags, self.device)
+        self.grads = grads
+
+
+def _adamw_flags(params, grads, copies, bits) -> int:
+    if bits not in (8, 32):
+        raise ValueError("bits must be 8 or 32")
+    if not params:
+        raise ValueError("no tensors")
+    if len(grads) != len(params) or (copies is not None and len(copies) != len(params)):
+        raise ValueError("params, grads and copies must have the same length")
+    dev, pt, gt = params[0].device, params[0].dtype, grads[0].dtype
+    for t, name in ((pt, "params"), (gt, "grads")):
+        if t not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"{name}: expected float32 or bfloat16, got {t}")
+    for i, p in enumerate(params):
+        _need(p, pt, p.shape, f"params[{i}]", dev)
+        _need(grads[i], gt, p.shape, f"grads[{i}]", dev)
+        if copies is not None and copies[i] is not None:
+            _need(copies[i], torch.bfloat16, p.shape, f"copies[{i}]", dev)
+    return ((_STATES_8 if bits == 8 else 0) | (_GRAD_BF16 if gt == torch.bfloat16 else 0) |
+            (_PARAM_BF16 if pt == torch.bfloat16 else 0))
+
+
+def _adamw_table(params, grads, copies, flags, device):
+    k = len(params)
+    n = (_c_i64 * k)(*[p.numel() for p in params])
+    ptrs = [(ctypes.c_void_p * k)(*[t.data_ptr() if t is not None and t.numel() else None for t in ts])
+            for ts in (params, grads, copies if copies is not None else [None] * k)]
+    need = lib().qlora_adamw_table_bytes(ctypes.addressof(n), k)
+    if need < 0:
+        _check(int(need), "qlora_adamw_table_bytes")
+    host = torch.empty(need, dtype=torch.uint8)
+    chunks = lib().qlora_adamw_table(*[ctypes.addressof(p) for p in ptrs], ctypes.addressof(n), k, flags, _ptr(host))
+    if chunks < 0:
+        _check(int(chunks), "qlora_adamw_table")
+    return host.to(device), int(chunks)
+
+
+def adamw_state(params, grads, copies=None, bits: int = 32) -> AdamWState:
+    """State of an AdamW step over these tensors (float32 or bfloat16, contiguous; the
+    gradients of the same shapes, float32 or bfloat16), moments of 32 or 8 bits, all zero.
+    copies: bfloat16 tensors (or None entries) that receive the new parameters."""
+    params, grads = list(params), list(grads)
+    copies = list(copies) if copies is not None else None
+    flags = _adamw_flags(params, grads, copies, bits)
+    dev = params[0].device
+    offsets, blocks = [], 0
+    for p in params:
+        offsets.append(blocks * ADAMW_BLOCK)
+        blocks += -(-p.numel() // ADAMW_BLOCK)
+    dt = torch.uint8 if bits == 8 else torch.float32
+    m = torch.zeros(blocks * ADAMW_BLOCK, dtype=dt, device=dev)
+    scales = [torch.zeros(blocks, dtype=torch.float32, device=dev) for _ in range(2)] if bits == 8 else [None, None]
+    table, n_chunks = _adamw_table(params, grads, copies, flags, dev)
+    return AdamWState(params, grads, copies, bits, m, torch.zeros_like(m), *scales, offsets, blocks, flags, table,
+                      n_chunks)
+
+
+def _scalar(t: torch.Tensor, dtype, name: str, device) -> int:
+    if t.dtype != dtype or t.numel() != 1 or t.device != device:
+        raise ValueError(f"{name}: expected one {dtype} on {device}")
+    return t.data_ptr()
+
+
+def adamw_step(state: AdamWState, step, lr, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+               weight_decay: float = 0.01, grad_scale: torch.Tensor | None = None, seed: int = 0) -> None:
+    """qlora_adamw_step: one AdamW step in place over all tensors of the state. step (1 for
+    the first) and lr may be one-element device tensors (int64, float32), read when the step
+    runs, for calls captured in a graph; grad_scale is a one-element float32 device tensor
+    that multiplies the gradients."""
+    dev = state.device
+    step_dev = _scalar(step, torch.int64, "step", dev) if isinstance(step, torch.Tensor) else None
+    lr_dev = _scalar(lr, torch.float32, "lr", dev) if isinstance(lr, torch.Tensor) else None
+    gs = _scalar(grad_scale, torch.float32, "grad_scale", dev) if grad_scale is not None else None
+    s8 = state.bits == 8
+    rc = lib().qlora_adamw_step(_ptr(state.table), len(state.params), state.n_chunks, state.flags, _ptr(state.m),
+                                _ptr(state.v), _ptr(state.m_scale) if s8 else None,
+                                _ptr(state.v_scale) if s8 else None, 0 if step_dev else step, step_dev,
+                                0.0 if lr_dev else lr, lr_dev, beta1, beta2, eps, weight_decay, gs,
+                                seed & 0xFFFFFFFF, _stream(dev))
+    _check(rc, "qlora_adamw_step")
+
+
+def adamw_moments(state: AdamWState, m: torch.Tensor | None = None, v: torch.Tensor | None = None):
+    """(m, v) as float32 [256 * blocks]: the state's own tensors with bits 32, the values of
+    the codes with bits 8 (into m and v if given)."""
+    if state.bits == 32:
+        return state.m, state.v
+    n = state.blocks * ADAMW_BLOCK
+    mo = m if m is not None else torch.empty(n, dtype=torch.float32, device=state.device)
+    vo = v if v is not None else torch.empty(n, dtype=torch.float32, device=state.device)
+    _need(mo, torch.float32, (n,), "m", state.device)
+    _need(vo, torch.float32, (n,), "v", state.device)
+    _check(lib().qlora_adamw_moments(_ptr(state.m), _ptr(state.m_scale), _ptr(state.v), _ptr(state.v_scale),
+                                     state.blocks, _ptr(mo), _ptr(vo), _stream(state.device)), "qlora_adamw_moments")
+    return mo, vo

@@ -1,6 +1,6 @@
 // extern "C" entry points of libqlora_nf4: argument checks, workspace layout and
 // kernel sequencing. Every step of the layer runs in the kernels of quantize.hip,
-// prologue.hip, gemm_nt.hip, gemv.hip, skinny.hip, lora_grads.hip and factors.hip; this file does
+// prologue.hip, gemm_nt.hip, gemv.hip, skinny.hip, lora_grads.hip, factors.hip and adamw.hip; this file does
 // no arithmetic on the data.
 #include <hip/hip_runtime.h>
 
@@ -15,6 +15,7 @@
 
 #include "../../include/qlora_nf4.h"
 #include "internal.h"
+#include "multi.h"
 
 namespace {
 
@@ -693,6 +694,93 @@ int qlora_lora_grads(const uint16_t* A, const uint16_t* B, int r, float s, const
     if ((e = qn::launch_lora_grads(X, ldx, dY, lddy, tp, up, d_out, d_in, d_seq, r, gw.r_pad, part, dA, dB, st)) !=
         hipSuccess)
         return hip_fail(e, "qlora_lora_grads (reduction)");
+    return 0;
+}
+
+// ---- AdamW over many tensors --------------------------------------------------
+
+int64_t qlora_adamw_blocks(const int64_t* n, int count) {
+    if (count < 0 || (!n && count > 0)) return fail(-1, "bad tensor list");
+    int64_t b = 0;
+    for (int i = 0; i < count; ++i) {
+        if (n[i] < 0 || n[i] > (int64_t{1} << 40)) return fail(-1, "bad tensor size");
+        b += (n[i] + qn::kAdamBlock - 1) / qn::kAdamBlock;
+    }
+    return b;
+}
+
+int64_t qlora_adamw_table_bytes(const int64_t* n, int count) {
+    if (qlora_adamw_blocks(n, count) < 0) return -1;
+    int64_t chunks = 0;
+    for (int i = 0; i < count; ++i) chunks += (n[i] + qn::kAdamChunk - 1) / qn::kAdamChunk;
+    return static_cast<int64_t>(sizeof(qn::AdamTensor)) * count + static_cast<int64_t>(sizeof(qn::AdamChunk)) * chunks;
+}
+
+int64_t qlora_adamw_table(void* const* p, const void* const* g, uint16_t* const* copy, const int64_t* n, int count,
+                          int flags, void* table) {
+    if (!table && count > 0) return fail(-1, "null pointer argument");
+    if (count > 0 && (!p || !g)) return fail(-1, "null pointer argument");
+    if (flags & ~7) return fail(-1, "unknown flags");
+    if (qlora_adamw_blocks(n, count) < 0) return -1;
+    const bool gb = flags & QN_ADAMW_GRAD_BF16, pb = flags & QN_ADAMW_PARAM_BF16;
+    auto* t = static_cast<qn::AdamTensor*>(table);
+    auto* c = reinterpret_cast<qn::AdamChunk*>(t + count);
+    int64_t blocks = 0, chunks = 0;
+    for (int i = 0; i < count; ++i) {
+        uint16_t* cp = copy ? copy[i] : nullptr;
+        if (n[i] > 0 && (!p[i] || !g[i])) return fail(-1, "null pointer argument");
+        if (!aligned(p[i], pb ? 2 : 4) || !aligned(g[i], gb ? 2 : 4) || !aligned(cp, 2))
+            return fail(-1, "misaligned pointer");
+        const bool vec = aligned(p[i], pb ? 8 : 16) && aligned(g[i], gb ? 8 : 16) && aligned(cp, 8);
+        t[i] = qn::AdamTensor{p[i], g[i], cp, n[i], blocks, vec ? 1 : 0};
+        blocks += (n[i] + qn::kAdamBlock - 1) / qn::kAdamBlock;
+        const int64_t nc = (n[i] + qn::kAdamChunk - 1) / qn::kAdamChunk;
+        for (int64_t k = 0; k < nc; ++k) c[chunks + k] = qn::AdamChunk{i, static_cast<int32_t>(k)};
+        chunks += nc;
+    }
+    if (chunks > INT32_MAX) return fail(-1, "too many elements");
+    return chunks;
+}
+
+int qlora_adamw_step(const void* table, int count, int64_t n_chunks, int flags, void* m, void* v, float* m_scale,
+                     float* v_scale, int64_t step, const int64_t* step_dev, double lr, const float* lr_dev,
+                     double beta1, double beta2, double eps, double weight_decay, const float* grad_scale,
+                     uint32_t seed, void* stream) {
+    if (count < 0 || n_chunks < 0 || n_chunks > INT32_MAX) return fail(-1, "bad tensor list");
+    if (flags & ~7) return fail(-1, "unknown flags");
+    const bool s8 = flags & QN_ADAMW_STATES_8;
+    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return fail(-1, "betas must be in [0, 1)");
+    if (!(eps > 0.0)) return fail(-1, "eps must be > 0");
+    if (!step_dev && step < 1) return fail(-1, "step must be >= 1");
+    if (n_chunks == 0) return 0;
+    if (!table || !m || !v || (s8 && (!m_scale || !v_scale))) return fail(-1, "null pointer argument");
+    if (!aligned(table, 8) || !aligned(m, 16) || !aligned(v, 16) || !aligned(m_scale, 4) || !aligned(v_scale, 4) ||
+        !aligned(step_dev, 8) || !aligned(lr_dev, 4) || !aligned(grad_scale, 4))
+        return fail(-1, "misaligned pointer");
+    qn::AdamArgs a{};
+    a.tensors = static_cast<const qn::AdamTensor*>(table);
+    a.chunks = reinterpret_cast<const qn::AdamChunk*>(a.tensors + count);
+    a.m = m; a.v = v; a.m_scale = m_scale; a.v_scale = v_scale;
+    a.grad_scale = grad_scale; a.lr_dev = lr_dev; a.step_dev = step_dev;
+    a.lr = lr; a.beta1 = beta1; a.beta2 = beta2; a.weight_decay = weight_decay;
+    a.step = step; a.eps = static_cast<float>(eps); a.seed = seed;
+    hipError_t e = qn::launch_adamw(a, n_chunks, s8, flags & QN_ADAMW_GRAD_BF16, flags & QN_ADAMW_PARAM_BF16,
+                                    static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "qlora_adamw_step");
+    return 0;
+}
+
+int qlora_adamw_moments(const uint8_t* m, const float* m_scale, const uint8_t* v, const float* v_scale,
+                        int64_t blocks, float* m_out, float* v_out, void* stream) {
+    if (blocks < 0 || blocks > (int64_t{1} << 32)) return fail(-1, "bad block count");
+    if (blocks == 0) return 0;
+    if (!m || !m_scale || !v || !v_scale || !m_out || !v_out) return fail(-1, "null pointer argument");
+    if (!aligned(m, 4) || !aligned(v, 4) || !aligned(m_scale, 4) || !aligned(v_scale, 4) || !aligned(m_out, 16) ||
+        !aligned(v_out, 16))
+        return fail(-1, "misaligned pointer");
+    hipError_t e = qn::launch_adamw_moments(m, m_scale, v, v_scale, blocks, m_out, v_out,
+                                            static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "qlora_adamw_moments");
     return 0;
 }
 

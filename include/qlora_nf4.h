@@ -341,6 +341,67 @@ int qlora_lora_grads(const uint16_t* A, const uint16_t* B, int r, float s,
                      void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
+ * AdamW over many tensors in one launch, with the moments in 32 bits or in 8: the step
+ * that takes the adapter gradients (float32) to the adapters the linear calls read (bf16).
+ *   [P2 card 1: only the adapters are trained; I. Loshchilov, F. Hutter, "Decoupled Weight
+ *    Decay Regularization"; T. Dettmers et al., "8-bit Optimizers via Block-wise
+ *    Quantization", for moments kept at 8 bits with one constant per block]
+ * Per element, g being the gradient times *grad_scale (a device float, e.g. a clip factor;
+ * NULL: 1) and t the step number (1 for the first step):
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps),
+ * in float32, each operation rounded once, p rounded once to its type.
+ *
+ * The tensors of a step are described by a table, filled on the host once and copied to
+ * device memory by the caller; it is built again when a pointer changes.
+ *   p[i], g[i]   parameters and gradient of tensor i, n[i] >= 0 elements, contiguous;
+ *                float32 or bf16 as the step's flags say, aligned to their element
+ *   copy[i]      bf16 copy of the new parameters, or NULL (copy itself may be NULL)
+ * State arrays are shared by all tensors: tensor i has ceil(n[i] / 256) blocks of 256
+ * elements, after those of the tensors before it, so element e of tensor i is at
+ * 256 * (blocks before it) + e. State past a tensor's last element is kept at zero. All
+ * states start as zeros.
+ *   QN_ADAMW_STATES_32  m, v float32 [256 blocks]; m_scale, v_scale unused (NULL)
+ *   QN_ADAMW_STATES_8   m, v uint8 [256 blocks], m_scale, v_scale float32 [blocks], the
+ *     block's largest |m| (v). With k = c & 127 (m; bit 7 is the sign) or k = c (v), code c
+ *     stands for scale * L(k), L(0) = 0 and L(k) = the float32 with bit pattern
+ *     (k + 889) << 20 (m) or (k + 761) << 20 (v): 3 mantissa bits, L = 1 at the top. |x| /
+ *     scale (a product with the rounded reciprocal) is cut to L's bits after 16 random bits
+ *     are added to the part cut off, so its mean is kept; a v > 0 has at least k = 1, m and
+ *     v below a block's smallest level become 0 (v: level 1), a block whose largest value
+ *     is below 2^-126 becomes zeros. The random bits of the element at state index e are
+ *     the low (m) and high (v) halves of mix(e ^ mix(t ^ mix(seed))), mix being the 32-bit
+ *     finaliser of MurmurHash3, e and t taken mod 2^32. p is formed from m, v before that.
+ * A NaN or infinite gradient makes its element's p, m, v non-finite (with 8-bit states the
+ * moments of its whole block).
+ */
+#define QN_ADAMW_STATES_32 0
+#define QN_ADAMW_STATES_8 1     /* flags of qlora_adamw_step */
+#define QN_ADAMW_GRAD_BF16 2
+#define QN_ADAMW_PARAM_BF16 4
+
+/* Blocks of the state arrays for `count` tensors of n[i] elements (-1 on a bad count or
+ * size). Host pointer. */
+int64_t qlora_adamw_blocks(const int64_t* n, int count);
+/* Bytes of the table (-1 on a bad count or size). Host pointer. */
+int64_t qlora_adamw_table_bytes(const int64_t* n, int count);
+/* Fills `table` (host memory, qlora_adamw_table_bytes bytes) from host arrays of `count`
+ * device pointers and sizes; flags as for the step. Returns the number of chunks (what
+ * qlora_adamw_step needs), or -1 (null or misaligned pointer, bad size or flags). */
+int64_t qlora_adamw_table(void* const* p, const void* const* g, uint16_t* const* copy, const int64_t* n, int count,
+                          int flags, void* table);
+/* One step. `table` is the device copy of the table for `count` tensors and `n_chunks`
+ * chunks. step >= 1 and lr are used unless lr_dev / step_dev (device scalars, for calls
+ * captured in a HIP graph) are given; 0 <= beta < 1, eps > 0. m, v 16-byte aligned. */
+int qlora_adamw_step(const void* table, int count, int64_t n_chunks, int flags, void* m, void* v, float* m_scale,
+                     float* v_scale, int64_t step, const int64_t* step_dev, double lr, const float* lr_dev,
+                     double beta1, double beta2, double eps, double weight_decay, const float* grad_scale,
+                     uint32_t seed, void* stream);
+/* The float32 values of 8-bit moments: m_out, v_out [256 blocks] (16-byte aligned). */
+int qlora_adamw_moments(const uint8_t* m, const float* m_scale, const uint8_t* v, const float* v_scale,
+                        int64_t blocks, float* m_out, float* v_out, void* stream);
+
+/*
  * Kernel timing, off by default. While enabled, the library brackets every kernel
  * it launches with a pair of HIP events recorded on that kernel's stream, so the
  * elapsed time of each kernel is measured on the stream it runs on.

@@ -1,0 +1,142 @@
+"""AdamW without a GPU: the table and its refusals, the binding's checks, and the oracle
+against torch's own AdamW and its format's fixed points."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import bit_nf4_quantized_05_amd as qn
+from bit_nf4_quantized_05_amd import _lib
+from oracle import adamw_oracle as O
+
+FAKE = 1 << 20
+
+
+def _i64(*v):
+    return (ctypes.c_int64 * len(v))(*v)
+
+
+def _ptrs(*v):
+    return (ctypes.c_void_p * len(v))(*v)
+
+
+def _at(a):
+    return ctypes.addressof(a)
+
+
+def test_block_and_table_sizes():
+    lib = _lib.lib()
+    n = _i64(1, 256, 257, 0, 5000)
+    assert lib.qlora_adamw_blocks(_at(n), 5) == 1 + 1 + 2 + 0 + 20
+    assert lib.qlora_adamw_table_bytes(_at(n), 5) == 5 * 48 + 8 * (1 + 1 + 1 + 0 + 3)
+    assert lib.qlora_adamw_blocks(_at(_i64(-1)), 1) == -1
+    assert lib.qlora_adamw_table_bytes(None, 2) == -1
+    assert lib.qlora_adamw_blocks(None, 0) == 0
+
+
+def test_table_entries_and_refusals():
+    lib = _lib.lib()
+    n = _i64(3000, 5)
+    buf = np.zeros(lib.qlora_adamw_table_bytes(_at(n), 2), np.uint8)
+
+    def table(p, g, c=None, flags=0):
+        return lib.qlora_adamw_table(_at(p), _at(g), _at(c) if c else None, _at(n), 2, flags, buf.ctypes.data)
+
+    assert table(_ptrs(FAKE, FAKE + 4), _ptrs(FAKE, FAKE)) == 3
+    rows = buf[:96].view(np.int64).reshape(2, 6)
+    assert rows[0].tolist() == [FAKE, FAKE, 0, 3000, 0, 1]
+    assert rows[1].tolist() == [FAKE + 4, FAKE, 0, 5, 12, 0]        # 4-byte aligned: no wide accesses
+    assert buf[96:].view(np.int32).tolist() == [0, 0, 0, 1, 1, 0]
+    assert table(_ptrs(FAKE, FAKE + 2), _ptrs(FAKE, FAKE)) == -1    # float32 at an odd half
+    assert b"misaligned" in lib.qn_last_error()
+    assert table(_ptrs(FAKE, FAKE + 2), _ptrs(FAKE, FAKE), flags=4) == 3
+    assert table(_ptrs(FAKE, None), _ptrs(FAKE, FAKE)) == -1
+    assert table(_ptrs(FAKE, FAKE), _ptrs(FAKE, FAKE), flags=8) == -1
+    assert table(_ptrs(FAKE, FAKE), _ptrs(FAKE, FAKE), _ptrs(FAKE, FAKE + 1)) == -1
+
+
+def test_step_refusals_without_device_work():
+    lib = _lib.lib()
+
+    def step(**kw):
+        a = dict(table=FAKE, count=1, chunks=1, flags=0, m=FAKE, v=FAKE, ms=None, vs=None, step=1, step_dev=None,
+                 lr=1e-3, b1=0.9, b2=0.999, eps=1e-8)
+        a.update(kw)
+        return lib.qlora_adamw_step(a["table"], a["count"], a["chunks"], a["flags"], a["m"], a["v"], a["ms"], a["vs"],
+                                    a["step"], a["step_dev"], a["lr"], None, a["b1"], a["b2"], a["eps"], 0.0, None, 0,
+                                    None)
+
+    assert step(step=0) == -1
+    assert step(b1=1.0) == -1 and step(b2=-0.1) == -1 and step(b1=float("nan")) == -1
+    assert step(eps=0.0) == -1
+    assert step(m=None) == -1 and step(table=None) == -1
+    assert step(flags=1) == -1                                       # 8-bit states without scales
+    assert step(flags=16) == -1 and step(m=FAKE + 4) == -1 and step(chunks=-1) == -1
+    assert step(chunks=0) == 0                                       # nothing to do
+    assert lib.qlora_adamw_moments(FAKE, FAKE, FAKE, FAKE, 1, None, FAKE, None) == -1
+    assert lib.qlora_adamw_moments(FAKE, FAKE, FAKE, FAKE, -1, FAKE, FAKE, None) == -1
+
+
+def test_binding_refusals():
+    p, g = torch.zeros(8), torch.zeros(8)
+    with pytest.raises(ValueError):
+        qn.adamw_state([], [])
+    with pytest.raises(ValueError):
+        qn.adamw_state([p], [g, g])
+    with pytest.raises(ValueError):
+        qn.adamw_state([p], [g], bits=16)
+    with pytest.raises(TypeError):
+        qn.adamw_state([p.half()], [g])
+    with pytest.raises(TypeError):
+        qn.adamw_state([p, p.bfloat16()], [g, g])
+    with pytest.raises(ValueError):
+        qn.adamw_state([p], [torch.zeros(9)])
+    with pytest.raises(ValueError):
+        qn.adamw_state([torch.zeros(8, 2)[:, 0]], [g])
+    with pytest.raises(TypeError):
+        qn.adamw_state([p], [g], copies=[torch.zeros(8)])
+
+
+def test_oracle_step_is_torch_adamw():
+    rng = np.random.default_rng(1)
+    p = rng.standard_normal(100)
+    t = torch.nn.Parameter(torch.from_numpy(p.copy()))
+    opt = torch.optim.AdamW([t], lr=3e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.02)
+    m = v = np.zeros(100)
+    for k in range(1, 6):
+        g = rng.standard_normal(100) * 10.0 ** (k - 3)
+        t.grad = torch.from_numpy(g.copy())
+        opt.step()
+        p, m, v = O.step(p, g, m, v, k, 3e-3, eps=1e-8, weight_decay=0.02)
+        assert np.allclose(p, t.detach().numpy(), rtol=1e-12, atol=1e-15)
+
+
+def test_oracle_moment_format():
+    lv, lu = O.levels(True), O.levels(False)
+    assert lv[127] == 1.0 and lu[255] == 1.0 and lv[0] == lu[0] == 0.0
+    assert lv[1] == 1.25 * 2.0 ** -16 and lu[1] == 1.25 * 2.0 ** -32
+    assert lv[126] == 0.9375 and np.all(np.diff(lv) > 0) and np.all(np.diff(lu) > 0)
+    # every level is its own code, whatever the random part
+    x = np.zeros(256)
+    x[:127] = lv[1:]
+    for frac in (0.0, 0.999):
+        code, scale, _ = O.encode(np.concatenate([x[:128], -x[:128]]), np.full(256, frac), True)
+        assert scale[0] == 1.0
+        assert code[:127].tolist() == list(range(1, 128)) and code[128:255].tolist() == list(range(129, 256))
+        code, _, _ = O.encode(lu[np.arange(256)] * 3.0, np.full(256, frac), False)
+        assert code.tolist() == list(range(256))
+    # a value between two levels goes up with the probability of its place
+    y = np.full(256, 0.9375 + 0.25 * 0.0625)
+    y[0] = 1.0
+    ups = sum((O.encode(y, np.full(256, (f + 0.5) / 100), True)[0][1:] == 127).all() for f in range(100))
+    assert ups == 25
+
+
+def test_oracle_words_match_known_values():
+    # the mixer's published finaliser: 0 is a fixed point, 1 maps to 0x514E28B7
+    assert O.mix32(np.array([0, 1], np.uint32)).tolist() == [0, 0x514E28B7]
+    a, b = O.words(1 << 16, 7), O.words(1 << 16, 8)
+    for h in (a & 0xFFFF, a >> 16, b & 0xFFFF):
+        assert abs(float(h.mean()) - 32767.5) < 5 * 18918.6 / 256      # 5 deviations of a uniform mean
+    assert np.mean(a == b) < 1e-3

@@ -1,0 +1,224 @@
+"""The AdamW step against the float64 oracle: many tensors of awkward sizes, both moment
+formats, all type combinations, unaligned tensors, device scalars, streams and graphs.
+
+Tolerances, from the float32 operations (u = 2^-24 each, the coefficients rounded once):
+v is a sum of two positive terms of at most 4 rounded factors: 6 u relative. m's terms have
+3: 5 u (|b1 m| + |c1 g|). The update m / den adds 8 u for the root, its factor, the sum, the
+quotient and the step size; p two products and a difference: 4 u |p|. A bf16 result adds
+half a unit in its last place (2^-8 relative to the value, its own rounding being the only
+other error). An 8-bit code may be one level off only where the oracle's cut is closer to a
+level than the float32 error of the value, 16 levels a binade at most."""
+import numpy as np
+import pytest
+import torch
+
+import bit_nf4_quantized_05_amd as qn
+from oracle import adamw_oracle as O
+from parity import dev
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+LR, WD, EPS = 3e-3, 0.02, 1e-8
+SIZES = [1, 255, 256, 257, 2047, 2048, 2049, 0, 4 * 2048 + 3, 16 * 77]
+
+
+def _say(*a):
+    print(*a, flush=True)
+
+
+def _f64(t):
+    return t.detach().float().cpu().numpy().astype(np.float64).reshape(-1)
+
+
+def _flat(state, tensors):
+    """Tensors in the state's block-padded order (zeros past each)."""
+    out = np.zeros(state.blocks * O.BLOCK)
+    for a, t in zip(state.offsets, tensors):
+        out[a:a + t.numel()] = _f64(t)
+    return out
+
+
+def _make(sizes, gen, p_dtype, g_dtype, shift=0):
+    """Tensors of the given sizes; shift > 0 puts each that many elements past an aligned start."""
+    def one(n, sigma, dt):
+        return (torch.randn(n + shift, generator=gen, device=dev()) * sigma).to(dt)[shift:]
+
+    params = [one(n, 0.02, p_dtype) for n in sizes]
+    grads = [one(n, 10.0 ** (i % 5 - 4), g_dtype) for i, n in enumerate(sizes)]
+    if sizes and len(sizes) > 3:
+        grads[3].zero_()
+    return params, grads
+
+
+def _run_and_check(state, steps, grad_scale=None, seed=0, device_scalars=False):
+    s8 = state.bits == 8
+    gs = float(grad_scale.item()) if grad_scale is not None else 1.0
+    for t in steps:
+        p0 = _flat(state, state.params)
+        g0 = _flat(state, state.grads)
+        if s8:
+            m0 = O.decode(state.m.cpu().numpy(), state.m_scale.cpu().numpy(), True)
+            v0 = O.decode(state.v.cpu().numpy(), state.v_scale.cpu().numpy(), False)
+        else:
+            m0, v0 = _f64(state.m), _f64(state.v)
+        if device_scalars:
+            qn.adamw_step(state, torch.tensor([t], device=dev()), torch.tensor([LR], dtype=torch.float32, device=dev()),
+                          eps=EPS, weight_decay=WD, grad_scale=grad_scale, seed=seed)
+            lr = float(np.float32(LR))
+        else:
+            qn.adamw_step(state, t, LR, eps=EPS, weight_decay=WD, grad_scale=grad_scale, seed=seed)
+            lr = LR
+        torch.cuda.synchronize()
+        p, m, v = O.step(p0, g0, m0, v0, t, lr, eps=EPS, weight_decay=WD, grad_scale=gs)
+        m_err = 5 * U * (np.abs(0.9 * m0) + np.abs(0.1 * g0 * gs)) + 1e-44
+        v_err = 6 * U * v + 1e-44
+        upd = lr / (1 - 0.9 ** t) / (np.sqrt(v / (1 - 0.999 ** t)) + EPS)
+        p_err = 4 * U * np.abs(p0) + upd * (m_err + 8 * U * np.abs(m)) + 4 * U * np.abs(p) + 1e-44
+        got = _flat(state, state.params)
+        bf = state.params[0].dtype == torch.bfloat16
+        slack = 2.0 ** -8 * np.abs(p) + 1e-40 if bf else 0.0
+        assert np.all(np.abs(got - p) <= p_err + slack), f"p, step {t}: {np.max(np.abs(got - p) - p_err - slack)}"
+        if state.copies is not None:
+            for a, c, q in zip(state.offsets, state.copies, state.params):
+                if c is not None:
+                    assert torch.equal(c.view(torch.int16), q.to(torch.bfloat16).view(torch.int16)), f"copy, step {t}"
+        if not s8:
+            assert np.all(np.abs(_f64(state.m) - m) <= m_err), f"m, step {t}"
+            assert np.all(np.abs(_f64(state.v) - v) <= v_err), f"v, step {t}"
+            continue
+        w = O.words(m.size, t, seed)
+        for name, x, err, code, scale, frac, signed in (
+                ("m", m, m_err, state.m, state.m_scale, (w & 0xFFFF) / 65536.0, True),
+                ("v", v, v_err, state.v, state.v_scale, (w >> 16) / 65536.0, False)):
+            want, big, slack = O.encode(x, frac, signed)
+            have, big_have = code.cpu().numpy(), scale.cpu().numpy().astype(np.float64)
+            big_err = err.reshape(-1, O.BLOCK).max(1)
+            assert np.all(np.abs(big_have - big) <= big_err + 2 * U * big), f"{name} scale, step {t}"
+            rel = err / np.maximum(np.abs(x), 1e-300) + np.repeat(big_err / np.maximum(big, 1e-300), O.BLOCK) + 4 * U
+            bad = (have != want) & (slack > 16 * rel)
+            assert not bad.any(), f"{name} codes, step {t}: {bad.sum()} of {bad.size}, first {np.flatnonzero(bad)[:4]}"
+        mv, vv = qn.adamw_moments(state)
+        assert np.allclose(_f64(mv), O.decode(state.m.cpu().numpy(), state.m_scale.cpu().numpy(), True), rtol=2 * U, atol=1e-44)
+        assert np.allclose(_f64(vv), O.decode(state.v.cpu().numpy(), state.v_scale.cpu().numpy(), False), rtol=2 * U, atol=1e-44)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("p_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("g_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("shift", [0, 1])
+def test_steps_match_oracle(bits, p_dtype, g_dtype, shift):
+    _say(f"[adamw] bits={bits} p={p_dtype} g={g_dtype} shift={shift}")
+    gen = torch.Generator(device=dev()).manual_seed(bits + shift)
+    params, grads = _make(SIZES, gen, p_dtype, g_dtype, shift)
+    copies = None
+    if p_dtype == torch.float32:
+        copies = [None if i == 2 else torch.empty(p.numel() + shift, dtype=torch.bfloat16, device=dev())[shift:]
+                  for i, p in enumerate(params)]
+    st = qn.adamw_state(params, grads, copies=copies, bits=bits)
+    _run_and_check(st, [1, 2])
+    for g in grads:
+        g.copy_(torch.randn(g.shape, generator=gen, device=dev()))
+    _run_and_check(st, [3], seed=5)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_scaled_gradients_and_device_scalars(bits):
+    _say(f"[adamw] device step, lr and gradient scale, bits={bits}")
+    gen = torch.Generator(device=dev()).manual_seed(3)
+    params, grads = _make([300, 5000], gen, torch.float32, torch.float32)
+    st = qn.adamw_state(params, grads, bits=bits)
+    _run_and_check(st, [1, 2, 1000], grad_scale=torch.tensor([0.37], device=dev()), device_scalars=True)
+    _run_and_check(st, [1001], grad_scale=torch.zeros(1, device=dev()))      # zero gradients: the moments decay
+
+
+def test_guards_around_tensors_stay():
+    """Elements beside each tensor of a wider buffer are not touched."""
+    _say("[adamw] guards")
+    gen = torch.Generator(device=dev()).manual_seed(4)
+    buf = torch.randn(3000, generator=gen, device=dev())
+    cbuf = torch.randn(3000, generator=gen, device=dev()).bfloat16()
+    before, cbefore = buf.clone(), cbuf.clone()
+    spans = [(5, 6), (10, 300), (312, 2600)]
+    st = qn.adamw_state([buf[a:b] for a, b in spans], [torch.ones(b - a, device=dev()) for a, b in spans],
+                        copies=[cbuf[a:b] for a, b in spans], bits=8)
+    qn.adamw_step(st, 1, 1e-2)
+    torch.cuda.synchronize()
+    keep = torch.ones(3000, dtype=torch.bool, device=dev())
+    for a, b in spans:
+        keep[a:b] = False
+        assert not torch.equal(buf[a:b], before[a:b])
+    assert torch.equal(buf[keep], before[keep]) and torch.equal(cbuf[keep], cbefore[keep])
+
+
+def test_8bit_second_moment_follows_its_mean():
+    """Constant gradients of many sizes: v must rise as 1 - b2^t on average. Per step the
+    rounding has mean 0 and a variance of at most 1/8 * 0.001 / 4 relative, 300 steps: a
+    deviation of at most 0.1 per element, 0.001 over 16000 of them; 5 of those allowed.
+    Rounding to nearest would leave v where a step no longer reaches half a level."""
+    _say("[adamw] mean of the 8-bit second moment")
+    n, steps = 64 * 256, 300
+    g = torch.rand(n, generator=torch.Generator(device=dev()).manual_seed(5), device=dev()) * 0.9 + 0.1
+    st = qn.adamw_state([torch.zeros(n, device=dev())], [g], bits=8)
+    for t in range(1, steps + 1):
+        qn.adamw_step(st, t, 0.0)
+    _, v = qn.adamw_moments(st)
+    ratio = (v.double() / (g.double() ** 2)).mean().item() / (1 - 0.999 ** steps)
+    _say(f"[adamw] mean ratio {ratio:.5f}")
+    assert abs(ratio - 1) < 0.005
+
+
+def test_tiny_and_zero_blocks():
+    """Blocks of zeros, of values whose squares are below the normal numbers, and one huge one."""
+    _say("[adamw] tiny blocks")
+    g = torch.zeros(256 * 4, device=dev())
+    g[256:512] = 1e-25
+    g[512] = 1e15
+    g[513:768] = 1e-15
+    st = qn.adamw_state([torch.ones(256 * 4, device=dev())], [g], bits=8)
+    _run_and_check(st, [1, 2])
+    assert torch.isfinite(st.params[0]).all()
+
+
+def test_other_stream_and_graph():
+    _say("[adamw] side stream and graph replays")
+    gen = torch.Generator(device=dev()).manual_seed(6)
+    params, grads = _make([1000, 4096, 77], gen, torch.float32, torch.float32)
+    twin = [p.clone() for p in params]
+    st = qn.adamw_state(params, grads, bits=8)
+    ref = qn.adamw_state(twin, grads, bits=8)
+    t = torch.zeros(1, dtype=torch.int64, device=dev())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        t += 1
+        qn.adamw_step(st, t, LR)
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    qn.adamw_step(ref, 1, LR)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        t += 1
+        qn.adamw_step(st, t, LR)
+    for k in range(2, 6):
+        for g in grads:
+            g.copy_(torch.randn(g.shape, generator=gen, device=dev()))
+        (torch.randn(256, 256, device=dev()) @ torch.randn(256, 256, device=dev())).sum().item()
+        graph.replay()
+        torch.cuda.synchronize()
+        qn.adamw_step(ref, k, LR)
+        torch.cuda.synchronize()
+        for a, b in zip(params + [st.m, st.v, st.m_scale, st.v_scale], twin + [ref.m, ref.v, ref.m_scale, ref.v_scale]):
+            assert torch.equal(a, b), f"replay {k}"
+
+
+def test_set_grads():
+    _say("[adamw] other gradient tensors")
+    gen = torch.Generator(device=dev()).manual_seed(8)
+    params, grads = _make([500, 257], gen, torch.float32, torch.float32)
+    st = qn.adamw_state(params, grads)
+    _run_and_check(st, [1])
+    st.set_grads([torch.randn(g.shape, generator=gen, device=dev()) for g in grads])
+    _run_and_check(st, [2])
+    with pytest.raises(TypeError):
+        st.set_grads([g.bfloat16() for g in grads])
