@@ -59,6 +59,15 @@ SIGNATURES = {
     "qlr_linear_fwd": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_int, _c_int, _c_vp, _c_vp, _c_int,
                                 _c_vp, _c_vp, _c_int, _c_float, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64,
                                 _c_vp]),
+    "qlora_multi_plan_bytes": (_c_i64, [_c_i64, _c_int]),
+    "qlora_multi_plan": (_c_int, [_c_vp, _c_i64, _c_int, _c_vp, _c_i64, _c_vp]),
+    "qlora_multi_fwd_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64, _c_int, _c_int]),
+    "qlora_multi_bwd_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64, _c_int, _c_int]),
+    "qlora_multi_fwd": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_int, _c_vp, _c_vp, _c_vp, _c_int,
+                                 _c_int, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp]),
+    "qlora_multi_bwd": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_i64, _c_int, _c_vp, _c_vp, _c_vp, _c_int,
+                                 _c_int, _c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_vp, _c_i64, _c_vp, _c_vp,
+                                 _c_vp, _c_i64, _c_vp]),
     "qlora_adamw_blocks": (_c_i64, [_c_vp, _c_int]),
     "qlora_adamw_table_bytes": (_c_i64, [_c_vp, _c_int]),
     "qlora_adamw_table": (_c_i64, [_c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_int, _c_vp]),
@@ -463,6 +472,145 @@ def qlr_linear_fwd(q: NF4Weight, Af: QFactor, Bf: QFactor, s: float, X: torch.Te
                               ws.numel() * ws.element_size(), _stream(dev))
     _check(rc, "qlr_linear_fwd")
     return o
+
+
+# ---- many adapters on one layer ---------------------------------------------------
+
+MULTI_RANK_STEP = 16          # ranks of a pool come in this step
+
+
+@dataclass
+class AdapterPool:
+    """Adapters of one layer side by side: A bfloat16 [n, r, d_in], B bfloat16
+    [n, d_out, r], s float32 [n] (each adapter's LoRA scale); r a multiple of 16.
+    ``alloc_pool`` and ``set`` make one from adapters of any rank up to r."""
+    A: torch.Tensor
+    B: torch.Tensor
+    s: torch.Tensor
+
+    @property
+    def n(self) -> int:
+        return self.A.shape[0]
+
+    @property
+    def r(self) -> int:
+        return self.A.shape[1]
+
+    def set(self, i: int, A: torch.Tensor, B: torch.Tensor, s: float) -> None:
+        """Puts an adapter (A [k, d_in], B [d_out, k], k <= r, scale s) at place i; ranks
+        past k are zeros."""
+        k = A.shape[0]
+        if A.shape != (k, self.A.shape[2]) or B.shape != (self.B.shape[1], k) or not 1 <= k <= self.r:
+            raise ValueError(f"expected A [k, {self.A.shape[2]}] and B [{self.B.shape[1]}, k] with k <= {self.r}")
+        self.A[i].zero_()
+        self.B[i].zero_()
+        self.A[i, :k] = A
+        self.B[i, :, :k] = B
+        self.s[i] = s
+
+
+def alloc_pool(n: int, r: int, d_out: int, d_in: int, device) -> AdapterPool:
+    """A pool of n adapters of rank up to r (rounded up to a multiple of 16), all zero."""
+    if n < 1 or not 1 <= r <= 256:
+        raise ValueError("n must be >= 1 and r in [1, 256]")
+    rp = -(-r // MULTI_RANK_STEP) * MULTI_RANK_STEP
+    return AdapterPool(torch.zeros(n, rp, d_in, dtype=torch.bfloat16, device=device),
+                       torch.zeros(n, d_out, rp, dtype=torch.bfloat16, device=device),
+                       torch.zeros(n, dtype=torch.float32, device=device))
+
+
+@dataclass
+class MultiPlan:
+    """A batch's plan (``multi_plan``): good for every layer with n adapters in its pool."""
+    buf: torch.Tensor
+    d_seq: int
+    n: int
+
+
+def multi_plan(ids: torch.Tensor, n: int, out: MultiPlan | None = None) -> MultiPlan:
+    """qlora_multi_plan: the plan of a batch whose token t has adapter ids[t] (int32
+    [d_seq]; a value outside [0, n): none). out: a plan of the same sizes to write again."""
+    if ids.dim() != 1:
+        raise ValueError("ids must be 1-D [d_seq]")
+    d_seq = ids.shape[0]
+    _need(ids, torch.int32, (d_seq,), "ids", ids.device)
+    need = lib().qlora_multi_plan_bytes(d_seq, n)
+    if out is None:
+        out = MultiPlan(torch.empty(max(need, 1), dtype=torch.uint8, device=ids.device), d_seq, n)
+    elif (out.d_seq, out.n) != (d_seq, n) or out.buf.device != ids.device:
+        raise ValueError(f"out is a plan for {out.d_seq} tokens and {out.n} adapters")
+    _check(lib().qlora_multi_plan(_ptr(ids), d_seq, n, _ptr(out.buf), out.buf.numel(), _stream(ids.device)),
+           "qlora_multi_plan")
+    return out
+
+
+def multi_linear_fwd_workspace_bytes(d_out: int, d_in: int, d_seq: int, r: int, n: int) -> int:
+    return lib().qlora_multi_fwd_workspace_bytes(d_out, d_in, d_seq, r, n)
+
+
+def multi_linear_bwd_workspace_bytes(d_out: int, d_in: int, d_seq: int, r: int, n: int) -> int:
+    return lib().qlora_multi_bwd_workspace_bytes(d_out, d_in, d_seq, r, n)
+
+
+def _multi_check(q: NF4Weight, pool: AdapterPool, plan: MultiPlan, d_seq: int) -> None:
+    dev = q.device
+    n, r = pool.n, pool.r
+    _need(pool.A, torch.bfloat16, (n, r, q.d_in), "pool.A", dev)
+    _need(pool.B, torch.bfloat16, (n, q.d_out, r), "pool.B", dev)
+    _need(pool.s, torch.float32, (n,), "pool.s", dev)
+    if (plan.d_seq, plan.n) != (d_seq, n) or plan.buf.device != dev:
+        raise ValueError(f"the plan is for {plan.d_seq} tokens and {plan.n} adapters on {plan.buf.device}, "
+                         f"not {d_seq} and {n} on {dev}")
+
+
+def multi_linear_fwd(q: NF4Weight, pool: AdapterPool, plan: MultiPlan, X: torch.Tensor,
+                     out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """qlora_multi_fwd: Y[t] = W_hat x_t + s_a B_a (A_a x_t), a the adapter of token t in the
+    plan. X [d_seq, d_in] and out [d_seq, d_out] may be row views of wider arrays."""
+    dev = q.device
+    if X.dim() != 2 or X.shape[1] != q.d_in:
+        raise ValueError(f"input must be [d_seq, {q.d_in}]")
+    d_seq = X.shape[0]
+    _multi_check(q, pool, plan, d_seq)
+    ldx = _rows(X, torch.bfloat16, (d_seq, q.d_in), "input", dev)
+    o = out if out is not None else torch.empty(d_seq, q.d_out, dtype=torch.bfloat16, device=dev)
+    ldy = _rows(o, torch.bfloat16, (d_seq, q.d_out), "out", dev)
+    ws = workspace if workspace is not None else torch.empty(
+        max(multi_linear_fwd_workspace_bytes(q.d_out, q.d_in, d_seq, pool.r, pool.n), 1), dtype=torch.uint8, device=dev)
+    rc = lib().qlora_multi_fwd(_ptr(q.codes), _ptr(q.qconst), _ptr(q.qscale), _ptr(q.qmean), q.d_out, q.d_in,
+                               _dq_code(q.dq), _ptr(pool.A), _ptr(pool.B), _ptr(pool.s), pool.n, pool.r, _ptr(X), ldx,
+                               d_seq, _ptr(plan.buf), _ptr(o), ldy, _ptr(ws), ws.numel() * ws.element_size(),
+                               _stream(dev))
+    _check(rc, "qlora_multi_fwd")
+    return o
+
+
+def multi_linear_bwd(q: NF4Weight, pool: AdapterPool, plan: MultiPlan, X: torch.Tensor, dY: torch.Tensor,
+                     dX: torch.Tensor | None = None, dA: torch.Tensor | None = None, dB: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None):
+    """qlora_multi_bwd: (dX bfloat16 [d_seq, d_in], dA float32 [n, r, d_in], dB float32
+    [n, d_out, r]) of ``multi_linear_fwd`` for the loss gradient dY."""
+    dev = q.device
+    if X.dim() != 2 or dY.dim() != 2 or X.shape[0] != dY.shape[0]:
+        raise ValueError("X [d_seq, d_in] and dY [d_seq, d_out] must share d_seq")
+    d_seq = X.shape[0]
+    _multi_check(q, pool, plan, d_seq)
+    ldx = _rows(X, torch.bfloat16, (d_seq, q.d_in), "X", dev)
+    lddy = _rows(dY, torch.bfloat16, (d_seq, q.d_out), "dY", dev)
+    gx = dX if dX is not None else torch.empty(d_seq, q.d_in, dtype=torch.bfloat16, device=dev)
+    lddx = _rows(gx, torch.bfloat16, (d_seq, q.d_in), "dX", dev)
+    ga = dA if dA is not None else torch.empty(pool.A.shape, dtype=torch.float32, device=dev)
+    gb = dB if dB is not None else torch.empty(pool.B.shape, dtype=torch.float32, device=dev)
+    _need(ga, torch.float32, pool.A.shape, "dA", dev)
+    _need(gb, torch.float32, pool.B.shape, "dB", dev)
+    ws = workspace if workspace is not None else torch.empty(
+        max(multi_linear_bwd_workspace_bytes(q.d_out, q.d_in, d_seq, pool.r, pool.n), 1), dtype=torch.uint8, device=dev)
+    rc = lib().qlora_multi_bwd(_ptr(q.codes), _ptr(q.qconst), _ptr(q.qscale), _ptr(q.qmean), q.d_out, q.d_in,
+                               _dq_code(q.dq), _ptr(pool.A), _ptr(pool.B), _ptr(pool.s), pool.n, pool.r, _ptr(X), ldx,
+                               _ptr(dY), lddy, d_seq, _ptr(plan.buf), _ptr(gx), lddx, _ptr(ga), _ptr(gb), _ptr(ws),
+                               ws.numel() * ws.element_size(), _stream(dev))
+    _check(rc, "qlora_multi_bwd")
+    return gx, ga, gb
 
 
 # ---- AdamW over many tensors -----------------------------------------------------

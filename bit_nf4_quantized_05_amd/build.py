@@ -20,7 +20,7 @@ CALIB_SOURCES = ["calibrate.hip"]
 BUILD = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.hip", "quantize.hip", "gemm_nt.hip", "gemm_nf4.hip", "prologue.hip", "gemv.hip", "skinny.hip", "lora_grads.hip", "factors.hip",
-           "adamw.hip", "tables.cpp"]
+           "multi_plan.hip", "multi_small.hip", "gemm_multi.hip", "multi_grads.hip", "adamw.hip", "tables.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

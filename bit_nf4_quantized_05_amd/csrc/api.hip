@@ -1,6 +1,7 @@
 // extern "C" entry points of libqlora_nf4: argument checks, workspace layout and
 // kernel sequencing. Every step of the layer runs in the kernels of quantize.hip,
-// prologue.hip, gemm_nt.hip, gemv.hip, skinny.hip, lora_grads.hip, factors.hip and adamw.hip; this file does
+// prologue.hip, gemm_nt.hip, gemv.hip, skinny.hip, lora_grads.hip, factors.hip,
+// multi_plan.hip, multi_small.hip, gemm_multi.hip, multi_grads.hip and adamw.hip; this file does
 // no arithmetic on the data.
 #include <hip/hip_runtime.h>
 
@@ -694,6 +695,179 @@ int qlora_lora_grads(const uint16_t* A, const uint16_t* B, int r, float s, const
     if ((e = qn::launch_lora_grads(X, ldx, dY, lddy, tp, up, d_out, d_in, d_seq, r, gw.r_pad, part, dA, dB, st)) !=
         hipSuccess)
         return hip_fail(e, "qlora_lora_grads (reduction)");
+    return 0;
+}
+
+// ---- many adapters on one layer -------------------------------------------------
+namespace {
+
+struct MultiWs {
+    int64_t what, at, bt, pre0, pre1, t, u, gpart, grads, part, part_t, bytes;
+    int splits0, splits1;
+};
+
+// Workspace of a multi-adapter call; regions a call does not use have size 0.
+MultiWs multi_ws(int64_t d_out, int64_t d_in, int64_t M, int r, int n, bool bwd) {
+    MultiWs w{};
+    int64_t off = 0;
+    auto take = [&](int64_t bytes) { const int64_t at = off; off += align_up(bytes, 256); return at; };
+    if (!bwd && M <= qn::kSkinnyMaxTokens) {
+        w.part = take(4 * static_cast<int64_t>(qn::skinny_splits(d_in, M)) * M * d_out);    // W_hat x, K-split
+        w.part_t = take(4 * static_cast<int64_t>(qn::multi_small_splits(d_in)) * M * r);    // A x, K-split
+        w.bytes = off;
+        return w;
+    }
+    w.splits0 = qn::prepass_split(M, d_in).splits;
+    w.splits1 = qn::prepass_split(M, d_out).splits;
+    w.what = take(2 * d_out * d_in);                                                // W_hat or W_hat^T
+    w.pre0 = take(4 * static_cast<int64_t>(w.splits0) * M * r);                     // A x, K-split
+    w.t = take(2 * (bwd ? 3 : 1) * M * r);                                          // T = s A x
+    if (bwd) {
+        w.pre1 = take(4 * static_cast<int64_t>(w.splits1) * M * r);                 // B^T dy, K-split
+        w.u = take(2 * 3 * M * r);                                                  // U = s B^T dy
+        w.at = take(2 * static_cast<int64_t>(n) * r * d_in);                        // A^T, B^T of the adapters in use
+        w.bt = take(2 * static_cast<int64_t>(n) * r * d_out);
+        w.grads = take(4 * qn::multi_grads_part_floats(d_out, d_in, M, n, r));      // dA, dB partials
+    }
+    w.gpart = take(4 * (bwd ? qn::gemm_split_part_floats(M, d_in, d_out) : qn::gemm_split_part_floats(M, d_out, d_in)));
+    w.bytes = off;
+    return w;
+}
+
+bool multi_sizes_ok(int64_t d_out, int64_t d_in, int64_t d_seq, int r, int n) {
+    return linear_sizes_ok(d_out, d_in, d_seq, r) && n >= 1 && n <= QN_MULTI_MAX_ADAPTERS;
+}
+
+static_assert(QN_MULTI_MAX_ADAPTERS == qn::kMultiMaxAdapters, "adapter limit");
+
+int check_multi(const uint8_t* codes, const int8_t* qconst, const float* qscale, const float* qmean, int dq,
+                int64_t d_out, int64_t d_in, const uint16_t* A, const uint16_t* B, const float* s, int n, int r,
+                const uint16_t* X, int64_t ldx, const uint16_t* dY, int64_t lddy, int64_t d_seq, const void* plan,
+                uint16_t* out, int64_t ldo, bool bwd, void* ws, int64_t ws_bytes, MultiWs* mw, qn::BlockConsts* bc) {
+    if (int rc = make_consts(dq, codes, qconst, qscale, qmean, bc)) return rc;
+    if (!A || !B || !s || !X || (bwd && !dY) || !plan || !out || !ws) return fail(-1, "null pointer argument");
+    if (d_out < 1 || d_in < 1 || d_seq < 1) return fail(-1, "sizes must be >= 1");
+    if (n < 1) return fail(-1, "the pool must hold at least one adapter");
+    if (r < 1 || r > 256) return fail(-1, "r must be in [1, 256]");
+    const int64_t out_cols = bwd ? d_in : d_out;
+    if (ldx < d_in || ldo < out_cols || (bwd && lddy < d_out))
+        return fail(-1, "a leading dimension is smaller than its row");
+    if (ldx % 8 != 0 || ldo % 8 != 0 || (bwd && lddy % 8 != 0))
+        return fail(-1, "leading dimensions must be multiples of 8 elements");
+    if (!aligned(codes, 16) || !aligned(A, 16) || !aligned(B, 16) || !aligned(s, 4) || !aligned(X, 16) ||
+        !aligned(dY, 16) || !aligned(plan, 16) || !aligned(out, 16) || !aligned(ws, 256))
+        return fail(-1, "misaligned pointer (16 B for arrays, 256 B for the workspace)");
+    if (d_in % 64 != 0 || d_out % 64 != 0) return fail(-2, "d_in and d_out must be multiples of 64");
+    if (r % 16 != 0) return fail(-2, "the pool's rank must be a multiple of 16");
+    if (n > QN_MULTI_MAX_ADAPTERS) return fail(-2, "too many adapters in the pool");
+    if (d_in > INT32_MAX || d_out > INT32_MAX || d_seq > INT32_MAX) return fail(-2, "dimension too large");
+    int64_t cnt, n_b, n_g;
+    if (!nf4_counts(d_out, d_in, &cnt, &n_b, &n_g)) return fail(-2, "weight too large");
+    // the GEMM addresses each operand with 32-bit byte offsets
+    const int64_t kMaxBytes = int64_t{1} << 32;
+    if (2 * cnt >= kMaxBytes || 2 * d_seq * std::max<int64_t>({ldx, ldo, bwd ? lddy : 0, r}) >= kMaxBytes ||
+        2 * std::max(d_in, d_out) * r >= kMaxBytes)
+        return fail(-2, "an operand reaches 4 GiB");
+    *mw = multi_ws(d_out, d_in, d_seq, r, n, bwd);
+    if (ws_bytes < mw->bytes) return fail(-3, "workspace too small");
+    return 0;
+}
+
+}  // namespace
+
+int64_t qlora_multi_plan_bytes(int64_t d_seq, int n) {
+    if (d_seq < 1 || d_seq > INT32_MAX || n < 1 || n > QN_MULTI_MAX_ADAPTERS) return 0;
+    return 4 * qn::multi_plan_words(d_seq, n);
+}
+
+int qlora_multi_plan(const int32_t* ids, int64_t d_seq, int n, void* plan, int64_t plan_bytes, void* stream) {
+    if (!ids || !plan) return fail(-1, "null pointer argument");
+    if (d_seq < 1 || n < 1) return fail(-1, "sizes must be >= 1");
+    if (!aligned(ids, 4) || !aligned(plan, 16)) return fail(-1, "misaligned pointer");
+    if (n > QN_MULTI_MAX_ADAPTERS) return fail(-2, "too many adapters in the pool");
+    if (d_seq > INT32_MAX - 4096) return fail(-2, "dimension too large");
+    if (plan_bytes < 4 * qn::multi_plan_words(d_seq, n)) return fail(-3, "plan buffer too small");
+    hipError_t e = qn::launch_multi_plan(ids, d_seq, n, plan, static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "qlora_multi_plan");
+    return 0;
+}
+
+int64_t qlora_multi_fwd_workspace_bytes(int64_t d_out, int64_t d_in, int64_t d_seq, int r, int n) {
+    return multi_sizes_ok(d_out, d_in, d_seq, r, n) ? multi_ws(d_out, d_in, d_seq, r, n, false).bytes : 0;
+}
+
+int64_t qlora_multi_bwd_workspace_bytes(int64_t d_out, int64_t d_in, int64_t d_seq, int r, int n) {
+    return multi_sizes_ok(d_out, d_in, d_seq, r, n) ? multi_ws(d_out, d_in, d_seq, r, n, true).bytes : 0;
+}
+
+int qlora_multi_fwd(const uint8_t* codes, const int8_t* qconst, const float* qscale, const float* qmean,
+                    int64_t d_out, int64_t d_in, int dq, const uint16_t* A, const uint16_t* B, const float* s, int n,
+                    int r, const uint16_t* X, int64_t ldx, int64_t d_seq, const void* plan, uint16_t* Y, int64_t ldy,
+                    void* workspace, int64_t workspace_bytes, void* stream) {
+    MultiWs mw;
+    qn::BlockConsts bc;
+    int rc = check_multi(codes, qconst, qscale, qmean, dq, d_out, d_in, A, B, s, n, r, X, ldx, nullptr, 0, d_seq, plan,
+                         Y, ldy, false, workspace, workspace_bytes, &mw, &bc);
+    if (rc) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    auto f32 = [&](int64_t off) { return reinterpret_cast<float*>(ws + off); };
+    auto u16 = [&](int64_t off) { return reinterpret_cast<uint16_t*>(ws + off); };
+    const qn::MultiPlan pl = qn::multi_plan_at(plan, d_seq, n);
+    hipError_t e;
+    if (d_seq <= qn::kSkinnyMaxTokens) {
+        e = qn::launch_multi_small(codes, bc, d_out, d_in, qn::MultiPool{A, B, s, n, r}, X, ldx, d_seq, pl, f32(mw.part),
+                                   f32(mw.part_t), Y, ldy, st);
+        if (e != hipSuccess) return hip_fail(e, "qlora_multi_fwd (small batch)");
+        return 0;
+    }
+    if ((e = qn::launch_multi_prologue(codes, bc, d_out, d_in, false, u16(mw.what), pl, s, d_seq, n, r,
+                                       qn::MultiPre{X, ldx, d_in, A, f32(mw.pre0)}, qn::MultiPre{}, st)) != hipSuccess)
+        return hip_fail(e, "qlora_multi_fwd (prologue)");
+    if ((e = qn::launch_multi_reduce(pl, d_seq, r, 1, f32(mw.pre0), mw.splits0, u16(mw.t), nullptr, 0, nullptr, st)) !=
+        hipSuccess)
+        return hip_fail(e, "qlora_multi_fwd (A x)");
+    if ((e = qn::launch_gemm_multi(X, ldx, u16(mw.what), d_in, u16(mw.t), B, r, pl, Y, ldy, d_seq, d_out, f32(mw.gpart),
+                                   st)) != hipSuccess)
+        return hip_fail(e, "qlora_multi_fwd (gemm)");
+    return 0;
+}
+
+int qlora_multi_bwd(const uint8_t* codes, const int8_t* qconst, const float* qscale, const float* qmean,
+                    int64_t d_out, int64_t d_in, int dq, const uint16_t* A, const uint16_t* B, const float* s, int n,
+                    int r, const uint16_t* X, int64_t ldx, const uint16_t* dY, int64_t lddy, int64_t d_seq,
+                    const void* plan, uint16_t* dX, int64_t lddx, float* dA, float* dB, void* workspace,
+                    int64_t workspace_bytes, void* stream) {
+    if (!dA || !dB) return fail(-1, "null pointer argument");
+    if (!aligned(dA, 16) || !aligned(dB, 16)) return fail(-1, "misaligned pointer (16 B for arrays, 256 B for the workspace)");
+    MultiWs mw;
+    qn::BlockConsts bc;
+    int rc = check_multi(codes, qconst, qscale, qmean, dq, d_out, d_in, A, B, s, n, r, X, ldx, dY, lddy, d_seq, plan, dX,
+                         lddx, true, workspace, workspace_bytes, &mw, &bc);
+    if (rc) return rc;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    auto f32 = [&](int64_t off) { return reinterpret_cast<float*>(ws + off); };
+    auto u16 = [&](int64_t off) { return reinterpret_cast<uint16_t*>(ws + off); };
+    const qn::MultiPlan pl = qn::multi_plan_at(plan, d_seq, n);
+    hipError_t e;
+    // K-contiguous copies for the products: B^T [r, d_out] (B^T dy) and A^T [d_in, r] (dX)
+    if ((e = qn::launch_multi_transpose(pl, std::min<int64_t>(n, d_seq), A, r, d_in, u16(mw.at), B, d_out, r, u16(mw.bt),
+                                        st)) != hipSuccess)
+        return hip_fail(e, "qlora_multi_bwd (A^T, B^T)");
+    if ((e = qn::launch_multi_prologue(codes, bc, d_out, d_in, true, u16(mw.what), pl, s, d_seq, n, r,
+                                       qn::MultiPre{X, ldx, d_in, A, f32(mw.pre0)},
+                                       qn::MultiPre{dY, lddy, d_out, u16(mw.bt), f32(mw.pre1)}, st)) != hipSuccess)
+        return hip_fail(e, "qlora_multi_bwd (prologue)");
+    if ((e = qn::launch_multi_reduce(pl, d_seq, r, 3, f32(mw.pre0), mw.splits0, u16(mw.t), f32(mw.pre1), mw.splits1,
+                                     u16(mw.u), st)) != hipSuccess)
+        return hip_fail(e, "qlora_multi_bwd (A x, B^T dy)");
+    if ((e = qn::launch_gemm_multi(dY, lddy, u16(mw.what), d_out, u16(mw.u), u16(mw.at), r, pl, dX, lddx, d_seq, d_in,
+                                   f32(mw.gpart), st)) != hipSuccess)
+        return hip_fail(e, "qlora_multi_bwd (gemm)");
+    if ((e = qn::launch_multi_grads(pl, X, ldx, dY, lddy, u16(mw.t), u16(mw.u), d_out, d_in, d_seq, n, r, f32(mw.grads),
+                                    dA, dB, st)) != hipSuccess)
+        return hip_fail(e, "qlora_multi_bwd (adapter gradients)");
     return 0;
 }
 

@@ -1,0 +1,383 @@
+// BF16 MFMA contraction of the calls with many adapters on gfx950:
+//     C[order[p], :] = bf16( P[order[p], K] Q[N, K]^T + T[p, r] R_a[N, r]^T )
+// for the positions p of a batch sorted by adapter, a the adapter of position p:
+//     forward : P = X,  Q = W_hat,    T = s_a A_a x,    R_a = B_a
+//     dX      : P = dY, Q = W_hat^T,  T = s_a B_a^T dy, R_a = A_a^T
+//
+// The main K-steps are those of the single-adapter GEMM (256 x 256 tiles, 8 waves of
+// 128 x 64, K-steps of 64 double-buffered in LDS by direct loads, swizzled rows; the
+// reasons are told there); only the token rows of P are gathered and those of C scattered
+// through the plan's order, each lane loading the tokens of its 4 rows once. Sorting keeps
+// the adapters per tile few: over all tile rows there are at most (tile rows + adapters in
+// use) pairs, however the requests came in.
+//
+// Rank steps. After the last main step a tile walks the adapters with tokens in it, 64
+// ranks a step, double-buffered in the same stages (the first one's loads go out under the
+// last main step). A 32-row MFMA tile skips an adapter that has none of its rows, adds
+// straight to its accumulators when all 32 rows are the adapter's, and otherwise forms the
+// product apart and adds it where the lane's row is the adapter's. So a row only ever
+// meets its own adapter: zeros in place of the other rows would let an infinity or NaN in
+// one adapter's weights reach its neighbours' tokens, and this costs fewer MFMAs besides.
+//
+// With few tiles the K-steps are split as in the single-adapter GEMM (gemm_split), the rank
+// steps going to the last split; gemm_multi_reduce adds the partials.
+#include <hip/hip_runtime.h>
+
+#include "gemm_common.h"
+#include "internal.h"
+#include "mfma_device.h"
+#include "multi.h"
+#include "nf4_device.h"
+
+#include <algorithm>
+
+namespace qn {
+namespace {
+
+__shared__ uint4 g_st0[2 * kChunks];
+__shared__ uint4 g_st1[2 * kChunks];
+
+constexpr int kWM = 2, kWN = 4;                 // waves
+constexpr int kNT = 64 * kWM * kWN;             // threads
+
+struct MultiGemm {
+    GemmArgs g;                                 // P, Q, C, sizes, splits
+    MultiPlan plan;
+    const uint16_t* T;                          // [M, r]
+    const uint16_t* R;                          // [adapters, N, r]
+    int r;
+    uint32_t bytesT, bytesR;                    // extents of T and of one adapter's R
+};
+
+template <bool kSplit>
+__device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg) {
+    const GemmArgs& g = mg.g;
+    constexpr int TM = BM / kWM / 32;           // 4 m sub-tiles per wave
+    constexpr int TN = BN / kWN / 32;           // 2 n sub-tiles
+    constexpr int SEG = BM / (kWM * kWN) / 8;   // 4 8-row load segments per wave and operand
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wm = wave / kWN, wn = wave % kWN;
+    const int M = g.M, N = g.N;
+
+    const int bid = static_cast<int>(blockIdx.x);
+    const bool split_wg = kSplit && bid >= g.full;
+    const int T = kSplit ? g.full : g.tiles_m * g.tiles_n;
+    const int w = split_wg ? 0 : bid;
+    const int sj = split_wg ? bid - g.full : 0;
+    const int sk = split_wg ? sj / g.rem : 0;
+    const int logical = split_wg ? g.full + sj % g.rem : ((T % 8 == 0) ? (w & 7) * (T >> 3) + (w >> 3) : w);
+    int tm, tn;
+    tile_coords(g, logical, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+
+    // this tile's adapters: used[k0 .. k1), `steps` rank steps in all (last split only)
+    const int2 kr = mg.plan.tile[tm];
+    const int jsteps = (mg.r + BK - 1) / BK;
+    const int steps = !split_wg || sk == g.splits - 1 ? (kr.y - kr.x) * jsteps : 0;
+    int a_next = 0, lo_next = 0, hi_next = 0;   // adapter and positions of the step issued next
+    if (steps > 0) {
+        a_next = mg.plan.used[kr.x];
+        lo_next = mg.plan.start[a_next];
+        hi_next = mg.plan.start[a_next + 1];
+    }
+
+    const uint32_t kcE = static_cast<uint32_t>((lane & 7) ^ (lane >> 4)) * 16u;
+    const uint32_t kcO = static_cast<uint32_t>((lane & 7) ^ (4 | (lane >> 4))) * 16u;
+    uint32_t voP[SEG], voQ[SEG];
+#pragma unroll
+    for (int j = 0; j < SEG; ++j) {
+        const int rr = 8 * SEG * wave + 8 * j + (lane >> 3);
+        const uint32_t kc16 = (((SEG * wave + j) & 1) ? kcO : kcE);
+        const uint32_t rp = static_cast<uint32_t>(mg.plan.order[min(m0 + rr, M - 1)]);
+        const uint32_t rq = static_cast<uint32_t>(min(n0 + rr, N - 1));
+        voP[j] = rp * static_cast<uint32_t>(g.ldp * 2) + kc16;
+        voQ[j] = rq * static_cast<uint32_t>(g.ldq * 2) + kc16;
+    }
+    const __amdgpu_buffer_rsrc_t rsP = make_rsrc(g.P, g.bytesP);
+    const __amdgpu_buffer_rsrc_t rsQ = make_rsrc(g.Q, g.bytesQ);
+    const int kb = split_wg ? sk * g.kper : 0;
+    const int ke = split_wg ? min(kb + g.kper, g.kt1) : g.kt1;
+    const int KT = ke - kb;
+
+#define QN_ISSUE(KTV, ST)                                                                         \
+    {                                                                                             \
+        uint4* sp_ = (ST) + wave * (64 * SEG);                                                    \
+        uint4* sq_ = sp_ + kChunks;                                                               \
+        const int so_ = ((KTV) + kb) * (BK * 2);                                                  \
+        _Pragma("unroll") for (int j = 0; j < SEG; ++j) {                                         \
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsP, (lds_ptr_t)(sp_ + 64 * j), 16, voP[j], so_, 0, 0); \
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsQ, (lds_ptr_t)(sq_ + 64 * j), 16, voQ[j], so_, 0, 0); \
+        }                                                                                         \
+    }
+
+    // Rank step S into stage ST: ranks j0 .. of T's rows and of the rows of R of adapter
+    // a_next. Pieces past r re-read the last one (no MFMA reads them); the offsets are formed
+    // from an opaque copy of the lane index, so they hold no registers through the main steps.
+    auto issue_rank = [&](int s, uint4* st) {
+        const int j0 = (s % jsteps) * BK;
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
+        const uint16_t* rb = mg.R + static_cast<int64_t>(a_next) * N * mg.r;
+        const __amdgpu_buffer_rsrc_t rsT = make_rsrc(mg.T, mg.bytesT);
+        const __amdgpu_buffer_rsrc_t rsR = make_rsrc(rb, mg.bytesR);
+        uint4* sp = st + wave * (64 * SEG);
+        uint4* sq = sp + kChunks;
+        const int last = mg.r / 8 - 1 - j0 / 8;
+#pragma unroll
+        for (int j = 0; j < SEG; ++j) {
+            const int rr = 8 * SEG * wave + 8 * j + (ln >> 3);
+            const int c = min((ln & 7) ^ ((rr >> 1) & 7), last);
+            const uint32_t vp = (static_cast<uint32_t>(min(m0 + rr, M - 1)) * mg.r + 8 * c) * 2u;
+            const uint32_t vq = (static_cast<uint32_t>(min(n0 + rr, N - 1)) * mg.r + 8 * c) * 2u;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsT, (lds_ptr_t)(sp + 64 * j), 16, vp, j0 * 2, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsR, (lds_ptr_t)(sq + 64 * j), 16, vq, j0 * 2, 0, 0);
+        }
+    };
+
+    const uint32_t frow = lane & 31;
+    const uint32_t fsw = (frow >> 1) & 7;
+    const uint32_t prow = (wm * (TM * 32) + frow) * 8;
+    const uint32_t qrow = kChunks + (wn * (TN * 32) + frow) * 8;
+    uint32_t chs[4];
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) chs[kk] = (2 * kk + (lane >> 5)) ^ fsw;
+#define QN_FRAGS(ST, CH, F)                                             \
+    {                                                                   \
+        F[0] = (ST)[qrow + (CH)];                                       \
+        _Pragma("unroll") for (int i = 0; i < TM; ++i) F[TN + i] = (ST)[prow + i * 256 + (CH)]; \
+        _Pragma("unroll") for (int i = 1; i < TN; ++i) F[i] = (ST)[qrow + i * 256 + (CH)];      \
+    }
+
+    f32x16 acc[TN][TM];
+#pragma unroll
+    for (int a = 0; a < TN; ++a)
+#pragma unroll
+        for (int b = 0; b < TM; ++b) acc[a][b] = f32x16{};
+#define QN_MFMAS(F)                                                            \
+    _Pragma("unroll") for (int a = 0; a < TN; ++a)                             \
+        _Pragma("unroll") for (int b = 0; b < TM; ++b)                         \
+            acc[a][b] = mfma32(F[a], F[TN + b], acc[a][b]);
+
+    uint4 fa[TM + TN], fb[TM + TN];
+#define QN_STEP(ISSUE, CUR, NXT, NEXT_FRAGS)                                   \
+    {                                                                          \
+        ISSUE;                                                                 \
+        QN_FRAGS(CUR, chs[1], fb)                                              \
+        __builtin_amdgcn_s_setprio(1);                                         \
+        QN_MFMAS(fa)                                                           \
+        QN_INTERLEAVE_DS_MFMA((TM + TN));                                      \
+        QN_FRAGS(CUR, chs[2], fa)                                              \
+        QN_MFMAS(fb)                                                           \
+        QN_INTERLEAVE_DS_MFMA((TM + TN));                                      \
+        QN_FRAGS(CUR, chs[3], fb)                                              \
+        QN_MFMAS(fa)                                                           \
+        QN_INTERLEAVE_DS_MFMA((TM + TN));                                      \
+        __builtin_amdgcn_s_setprio(0);                                         \
+        __builtin_amdgcn_s_waitcnt(0);                                         \
+        QN_BARRIER();                                                          \
+        NEXT_FRAGS                                                             \
+        QN_MFMAS(fb)                                                           \
+        QN_INTERLEAVE_DS_MFMA((TM + TN));                                      \
+    }
+#define QN_MAIN(K, CUR, NXT) QN_STEP(QN_ISSUE((K) + 1, NXT), CUR, NXT, QN_FRAGS(NXT, chs[0], fa))
+#define QN_LAST(CUR, NXT) QN_STEP(if (steps > 0) issue_rank(0, NXT), CUR, NXT, )
+
+    QN_ISSUE(0, g_st0)
+    QN_WAIT_VM(0);
+    QN_BARRIER();
+    QN_FRAGS(g_st0, chs[0], fa)
+    // the last main step stands outside the loop, which then has no branch in it
+    int kt = 0;
+    for (; kt + 2 < KT; kt += 2) {
+        QN_MAIN(kt, g_st0, g_st1)
+        QN_MAIN(kt + 1, g_st1, g_st0)
+    }
+    if (kt + 1 < KT) QN_MAIN(kt, g_st0, g_st1)
+    {
+        const uint4* cur = (KT & 1) ? g_st0 : g_st1;
+        uint4* nxt = (KT & 1) ? g_st1 : g_st0;
+        QN_LAST(cur, nxt)
+    }
+#undef QN_LAST
+#undef QN_MAIN
+#undef QN_STEP
+#undef QN_MFMAS
+#undef QN_FRAGS
+#undef QN_ISSUE
+
+    // ---- rank steps. Step 0 is in the stage the last main step did not read, and complete
+    // (that step's wait and barrier). Each step: the next one's loads, this one's products,
+    // then every wave's loads and LDS reads are waited for before the barrier.
+    for (int s = 0; s < steps; ++s) {
+        const uint4* cur = ((KT + s) & 1) ? g_st1 : g_st0;
+        uint4* nxt = ((KT + s) & 1) ? g_st0 : g_st1;
+        const int lo = lo_next, hi = hi_next;
+        const int subs = min(BK, mg.r - (s % jsteps) * BK) / 16;
+        if (s + 1 < steps) {
+            if ((s + 1) % jsteps == 0) {
+                a_next = mg.plan.used[kr.x + (s + 1) / jsteps];
+                lo_next = mg.plan.start[a_next];
+                hi_next = mg.plan.start[a_next + 1];
+            }
+            issue_rank(s + 1, nxt);
+        }
+        uint4 q[TN][4];
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+            if (kk < subs) {
+#pragma unroll
+                for (int a = 0; a < TN; ++a) q[a][kk] = cur[qrow + a * 256 + chs[kk]];
+            }
+#pragma unroll
+        for (int b = 0; b < TM; ++b) {
+            const int p0 = m0 + wm * (TM * 32) + b * 32;             // the sub-tile's positions p0 .. p0 + 31
+            if (p0 >= hi || p0 + 32 <= lo) continue;                 // wave-uniform
+            const bool whole = p0 >= lo && p0 + 32 <= hi;
+            const bool mine = p0 + static_cast<int>(frow) >= lo && p0 + static_cast<int>(frow) < hi;
+            uint4 p[4];
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                if (kk < subs) p[kk] = cur[prow + b * 256 + chs[kk]];
+#pragma unroll
+            for (int a = 0; a < TN; ++a) {
+                if (whole) {
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        if (kk < subs) acc[a][b] = mfma32(q[a][kk], p[kk], acc[a][b]);
+                } else {
+                    f32x16 t = f32x16{};
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        if (kk < subs) t = mfma32(q[a][kk], p[kk], t);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[a][b][e] = mine ? acc[a][b][e] + t[e] : acc[a][b][e];
+                }
+            }
+        }
+        __builtin_amdgcn_s_waitcnt(0);
+        QN_BARRIER();
+    }
+
+    if (split_wg) {
+        float* pt = g.part + (static_cast<int64_t>(sk) * g.rem + sj % g.rem) * (BM * BN);
+#pragma unroll
+        for (int b = 0; b < TM; ++b) {
+            const int ml = wm * (TM * 32) + b * 32 + static_cast<int>(frow);
+#pragma unroll
+            for (int a = 0; a < TN; ++a) {
+#pragma unroll
+                for (int gq = 0; gq < 4; ++gq) {
+                    const int nl = wn * (TN * 32) + a * 32 + 8 * gq + 4 * (lane >> 5);
+                    *reinterpret_cast<float4*>(pt + ml * BN + nl) =
+                        float4{acc[a][b][4 * gq], acc[a][b][4 * gq + 1], acc[a][b][4 * gq + 2], acc[a][b][4 * gq + 3]};
+                }
+            }
+        }
+        return;
+    }
+    // ---- epilogue: the bf16 tile through LDS (conflict-free, as the single-adapter GEMM),
+    // then each row as 512 contiguous bytes to its token's row of C
+#pragma unroll
+    for (int b = 0; b < TM; ++b) {
+        const int rl = wm * (TM * 32) + b * 32 + static_cast<int>(frow);
+        uint4* arr = (rl >> 7) ? g_st1 : g_st0;
+        char* rowp = reinterpret_cast<char*>(arr) + (rl & 127) * 512;
+#pragma unroll
+        for (int a = 0; a < TN; ++a) {
+#pragma unroll
+            for (int gq = 0; gq < 4; ++gq) {
+                const int nl = wn * (TN * 32) + a * 32 + 8 * gq + 4 * (lane >> 5);
+                uint2 o;
+                o.x = pack_bf16x2(acc[a][b][4 * gq + 0], acc[a][b][4 * gq + 1]);
+                o.y = pack_bf16x2(acc[a][b][4 * gq + 2], acc[a][b][4 * gq + 3]);
+                *reinterpret_cast<uint2*>(rowp + (((nl >> 3) ^ (rl & 31)) << 4) + ((nl & 7) << 1)) = o;
+            }
+        }
+    }
+    __syncthreads();
+    const int cj = tid & 31;
+    constexpr int kRowsPerPass = kNT / 32;
+#pragma unroll 4
+    for (int i = 0; i < BM / kRowsPerPass; ++i) {
+        const int r = i * kRowsPerPass + (tid >> 5);
+        const uint4* arr = (r >> 7) ? g_st1 : g_st0;
+        const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(arr) + (r & 127) * 512 +
+                                                        ((cj ^ (r & 31)) << 4));
+        const int m = m0 + r;
+        const int n = n0 + cj * 8;
+        if (m < M && n < N)
+            *reinterpret_cast<uint4*>(g.C + static_cast<int64_t>(mg.plan.order[m]) * g.ldc + n) = v;
+    }
+}
+
+__global__ __launch_bounds__(kNT, 1)
+void gemm_multi_kernel(MultiGemm mg) {
+    gemm_multi_body<false>(mg);
+}
+
+__global__ __launch_bounds__(kNT, 1)
+void gemm_multi_split(MultiGemm mg) {
+    gemm_multi_body<true>(mg);
+}
+
+// Split tiles: C[order[m], n..n+3] = bf16(sum of the tile's partials in split order)
+template <int SP>
+__global__ __launch_bounds__(256)
+void gemm_multi_reduce(MultiGemm mg) {
+    const GemmArgs& g = mg.g;
+    const int j = static_cast<int>(blockIdx.x) / 64;
+    const int ml = (static_cast<int>(blockIdx.x) % 64) * 4 + (threadIdx.x >> 6);
+    const int nl = (threadIdx.x & 63) * 4;
+    int tm, tn;
+    tile_coords(g, g.full + j, tm, tn);
+    const int m = tm * BM + ml, n = tn * BN + nl;
+    if (m >= g.M || n >= g.N) return;
+    const float* p = g.part + static_cast<int64_t>(j) * (BM * BN) + ml * BN + nl;
+    const int64_t stride = static_cast<int64_t>(g.rem) * (BM * BN);
+    const int64_t row = mg.plan.order[m];
+    float4 v[SP];
+#pragma unroll
+    for (int s = 0; s < SP; ++s) v[s] = *reinterpret_cast<const float4*>(p + s * stride);
+    float4 t = v[0];
+#pragma unroll
+    for (int s = 1; s < SP; ++s) { t.x += v[s].x; t.y += v[s].y; t.z += v[s].z; t.w += v[s].w; }
+    *reinterpret_cast<uint2*>(g.C + row * g.ldc + n) = uint2{pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w)};
+}
+
+}  // namespace
+
+hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t K, const uint16_t* T,
+                             const uint16_t* R, int r, const MultiPlan& plan, uint16_t* C, int64_t ldc, int64_t M,
+                             int64_t N, float* part, hipStream_t st) {
+    MultiGemm mg{};
+    GemmArgs& g = mg.g;
+    g.tiles_m = static_cast<int>((M + BM - 1) / BM);
+    g.tiles_n = static_cast<int>((N + BN - 1) / BN);
+    g.P = P; g.ldp = ldp; g.Q = Q; g.ldq = K; g.kt1 = static_cast<int>(K / BK);
+    g.C = C; g.ldc = ldc; g.M = static_cast<int>(M); g.N = static_cast<int>(N);
+    g.bytesP = static_cast<uint32_t>(2 * ldp * M);
+    g.bytesQ = static_cast<uint32_t>(2 * K * N);
+    mg.plan = plan; mg.T = T; mg.R = R; mg.r = r;
+    mg.bytesT = static_cast<uint32_t>(2 * M * r);
+    mg.bytesR = static_cast<uint32_t>(2 * N * r);
+    const GemmSplit gs = gemm_split(M, N, K);
+    g.splits = gs.splits;
+    g.full = gs.full;
+    g.rem = gs.rem;
+    g.kper = (g.kt1 + g.splits - 1) / g.splits;
+    g.part = part;
+    if (g.splits <= 1) {
+        QN_LAUNCH("gemm_multi_kernel", st, gemm_multi_kernel, dim3(g.tiles_m * g.tiles_n), dim3(kNT), 0, st, mg);
+        return hipGetLastError();
+    }
+    QN_LAUNCH("gemm_multi_split", st, gemm_multi_split, dim3(g.full + g.rem * g.splits), dim3(kNT), 0, st, mg);
+    const dim3 rgrid(static_cast<unsigned>(g.rem * 64));
+    if (g.splits == 2) QN_LAUNCH("gemm_multi_reduce", st, gemm_multi_reduce<2>, rgrid, dim3(256), 0, st, mg);
+    else if (g.splits == 3) QN_LAUNCH("gemm_multi_reduce", st, gemm_multi_reduce<3>, rgrid, dim3(256), 0, st, mg);
+    else QN_LAUNCH("gemm_multi_reduce", st, gemm_multi_reduce<4>, rgrid, dim3(256), 0, st, mg);
+    return hipGetLastError();
+}
+
+}  // namespace qn

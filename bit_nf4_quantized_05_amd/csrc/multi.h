@@ -48,4 +48,83 @@ hipError_t launch_adamw(const AdamArgs& a, int64_t n_chunks, bool states8, bool 
 hipError_t launch_adamw_moments(const uint8_t* m, const float* m_scale, const uint8_t* v, const float* v_scale,
                                 int64_t blocks, float* m_out, float* v_out, hipStream_t st);
 
+// ---- multi_plan.hip ----
+// The plan of a batch: its tokens sorted (stably) by adapter, as int32 words on the device.
+// A position is an index into that order; tokens without an adapter come last.
+constexpr int kMultiMaxAdapters = 1024;
+constexpr int kMultiItem = 128;             // positions per work item at most
+constexpr int kMultiTile = 256;             // positions per GEMM tile
+
+struct MultiItem { int32_t adapter, pos, count, index; };   // index: of the item within its adapter
+struct MultiPlan {
+    const int32_t* head;                    // [0] adapters in use, [1] items, [2] positions with an adapter
+    const int32_t* order;                   // [M] token at each position
+    const int32_t* start;                   // [n + 1] first position of each adapter's tokens
+    const int32_t* first_item;              // [n] each adapter's first item (adapters in use)
+    const int32_t* used;                    // [min(n, M)] adapters in use, ascending
+    const int2* tile;                       // [ceil(M / 256)] range of `used` with tokens in the tile
+    const MultiItem* items;                 // [multi_max_items] runs of <= 128 positions of one adapter
+};
+inline int64_t multi_max_items(int64_t M, int64_t n) { return (M + kMultiItem - 1) / kMultiItem + (n < M ? n : M); }
+// the plan's parts in a buffer of multi_plan_words(M, n) int32 words (16-byte aligned)
+int64_t multi_plan_words(int64_t M, int64_t n);
+MultiPlan multi_plan_at(const void* buf, int64_t M, int64_t n);
+hipError_t launch_multi_plan(const int32_t* ids, int64_t M, int n, void* buf, hipStream_t st);
+
+// ---- the adapters of a call ----
+struct MultiPool {
+    const uint16_t* A;                      // [n, r, d_in]
+    const uint16_t* B;                      // [n, d_out, r]
+    const float* s;                         // [n]
+    int n, r;
+};
+
+// ---- prologue.hip ----
+// Pre-passes of the multi-adapter calls, one launch: for every item and K-slice the fp32
+// partial s_a P[order[pos], kslice] R_a[r, kslice]^T into part[slice][pos][r]; R is [n, r, K]
+// row-major. Up to two products (R1 null: one), and the double dequantisation of the weight
+// to what (transposed or not; null: none).
+struct MultiPre { const uint16_t* P; int64_t ldp; int64_t K; const uint16_t* R; float* part; };
+hipError_t launch_multi_prologue(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
+                                 bool transposed, uint16_t* what, const MultiPlan& plan, const float* s, int64_t M,
+                                 int n, int r, const MultiPre& p0, const MultiPre& p1, hipStream_t st);
+// T[piece][pos][r] = the slice partials added in slice order, in `pieces` bf16 terms (1:
+// rounded once; 3: the remainders too, 24 bits in all), for one or two products (part1
+// null: one)
+hipError_t launch_multi_reduce(const MultiPlan& plan, int64_t M, int r, int pieces, const float* part0, int splits0,
+                               uint16_t* T0, const float* part1, int splits1, uint16_t* T1, hipStream_t st);
+
+// ---- gemm_multi.hip ----
+// C[order[pos], :] = bf16( P[order[pos], K] Q[N, K]^T + T[pos, r] R_a[N, r]^T ), a the adapter
+// of the position (no second term without one); part as for gemm_nt.
+hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t K, const uint16_t* T,
+                             const uint16_t* R, int r, const MultiPlan& plan, uint16_t* C, int64_t ldc, int64_t M,
+                             int64_t N, float* part, hipStream_t st);
+
+// ---- skinny.hip ----
+// The W_hat x partials alone, [skinny_splits(d_in, d_seq)][d_seq][d_out] floats
+hipError_t launch_skinny_stream(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
+                                const uint16_t* X, int64_t ldx, int64_t d_seq, float* part, hipStream_t st);
+
+// ---- multi_small.hip ----
+// Forward of up to kSkinnyMaxTokens tokens from the packed codes. part holds
+// skinny_splits * M * d_out floats, part_t multi_small_splits(d_in) * M * r.
+int multi_small_splits(int64_t d_in);
+hipError_t launch_multi_small(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
+                              const MultiPool& pool, const uint16_t* X, int64_t ldx, int64_t M,
+                              const MultiPlan& plan, float* part, float* part_t, uint16_t* Y, int64_t ldy,
+                              hipStream_t st);
+
+// ---- multi_grads.hip ----
+// dst[a] [cols, rows] = src[a] [rows, cols]^T for the adapters in use (rows and cols multiples of 16)
+hipError_t launch_multi_transpose(const MultiPlan& plan, int64_t max_used, const uint16_t* src0, int64_t rows0,
+                                  int64_t cols0, uint16_t* dst0, const uint16_t* src1, int64_t rows1, int64_t cols1,
+                                  uint16_t* dst1, hipStream_t st);
+// dB[a] [d_out, r] = sum over a's positions of dY^T T, dA[a] [r, d_in] of U^T X (zeros for an
+// adapter without tokens); T, U [3][M][r]. part holds multi_grads_part_floats floats.
+int64_t multi_grads_part_floats(int64_t d_out, int64_t d_in, int64_t M, int n, int r);
+hipError_t launch_multi_grads(const MultiPlan& plan, const uint16_t* X, int64_t ldx, const uint16_t* dY, int64_t lddy,
+                              const uint16_t* T, const uint16_t* U, int64_t d_out, int64_t d_in, int64_t M, int n,
+                              int r, float* part, float* dA, float* dB, hipStream_t st);
+
 }  // namespace qn

@@ -1,12 +1,13 @@
 // Prologue of a QLoRA linear call on gfx950: the LoRA pre-pass (rank-r product of
 // the activations with A or B^T; up to two such products per launch), the adapter
 // layouts and the double dequantisation of the NF4 weight to bf16 W_hat or W_hat^T,
-// in one launch; the reduction of K-split pre-pass partials; and the small transpose
+// in one launch; the same for tokens of many adapters (multi_prologue_kernel); the reduction of K-split pre-pass partials; and the small transpose
 // of B that the input gradient uses when the pre-pass cannot read B itself.
 #include <hip/hip_runtime.h>
 
 #include "internal.h"
 #include "mfma_device.h"
+#include "multi.h"
 #include "nf4_device.h"
 
 #include <algorithm>
@@ -241,7 +242,6 @@ __device__ __forceinline__ void prepass_job(const PreJob& j, const PrologueArgs&
         }
     }
 }
-#undef QN_PRE_BARRIER
 
 // OUT[m, j] = bf16(s * sum of the slice partials in slice order) for j < r, 0 for
 // r <= j < r_pad; a thread takes 4 consecutive columns. The first `blocks0` workgroups
@@ -391,6 +391,22 @@ __device__ __forceinline__ void dequant_transposed_job(const PrologueArgs& a, in
     }
 }
 
+// Workgroup bd of the double dequantisation, with 16 KB of LDS scratch.
+__device__ __forceinline__ void dequant_jobs(const PrologueArgs& a, int bd, const NF4Tables& tab, char* lds) {
+    float* s_code = reinterpret_cast<float*>(lds);             // 16 floats
+    float* s_ahat = reinterpret_cast<float*>(lds + 64);        // up to 256 floats
+    if (threadIdx.x < 16) s_code[threadIdx.x] = tab.code[threadIdx.x];
+    if (a.transposed) {
+        // Workgroups go to the 8 XCDs in turn; a code row's 128-byte line spans several
+        // neighbouring regions, so each XCD takes a contiguous range of regions and a
+        // line is fetched into one XCD's L2 rather than into several.
+        const int bl = (a.n_deq & 7) == 0 ? (bd & 7) * (a.n_deq >> 3) + (bd >> 3) : bd;
+        dequant_transposed_job(a, bl, s_code, s_ahat, reinterpret_cast<uint16_t*>(lds + 64 + 1024));
+    } else {
+        dequant_rows_job(a, bd, s_code, s_ahat);
+    }
+}
+
 // KM0, KM1: whether pre-pass job 0 / 1 takes its R k-major
 template <int NT, bool KM0, bool KM1>
 __global__ __launch_bounds__(256)
@@ -410,19 +426,141 @@ void prologue_kernel(PrologueArgs a, NF4Tables tab) {
         adapt_job(a, b - a.n_pre);
         return;
     }
-    float* s_code = reinterpret_cast<float*>(lds);             // 16 floats
-    float* s_ahat = reinterpret_cast<float*>(lds + 64);        // up to 256 floats
-    if (threadIdx.x < 16) s_code[threadIdx.x] = tab.code[threadIdx.x];
-    const int bd = b - a.n_pre - a.n_adapt;
-    if (a.transposed) {
-        // Workgroups go to the 8 XCDs in turn; a code row's 128-byte line spans several
-        // neighbouring regions, so each XCD takes a contiguous range of regions and a
-        // line is fetched into one XCD's L2 rather than into several.
-        const int bl = (a.n_deq & 7) == 0 ? (bd & 7) * (a.n_deq >> 3) + (bd >> 3) : bd;
-        dequant_transposed_job(a, bl, s_code, s_ahat, reinterpret_cast<uint16_t*>(lds + 64 + 1024));
-    } else {
-        dequant_rows_job(a, bd, s_code, s_ahat);
+    dequant_jobs(a, b - a.n_pre - a.n_adapt, tab, lds);
+}
+
+// ---------------------------------------------------------------------------
+// Pre-passes of the calls with many adapters: T[pos] = s_a R_a P[order[pos]], the adapter
+// a of each token taken from the batch's plan. A workgroup takes one item of the plan (at
+// most 128 positions of one adapter) and one K-slice, with the stages and fragments of
+// the pre-pass above; only the token rows are gathered, each lane keeping the addresses
+// of the 4 rows it fetches. Every slice writes its fp32 partial, already times s_a, and
+// multi_reduce adds them. Work is proportional to the tokens of each adapter rounded up
+// to 128, whatever the number of adapters in the pool; items past the plan's count (the
+// grid is sized for the worst case) end at once. Bound by the reads of P (each row once)
+// and, with many adapters of few tokens, of R (each adapter once per 128 tokens).
+// ---------------------------------------------------------------------------
+struct MultiPreJob {
+    const uint16_t* P; int64_t ldp; int K;
+    const uint16_t* R;               // [n, r, K]
+    float* part;                     // [psplits][M][r]
+    int psplits, kper, n;            // K-slices, 64-wide K-chunks per slice, workgroups
+};
+
+struct MultiPrologueArgs {
+    PrologueArgs d;                  // the dequantisation's fields, M, r
+    MultiPreJob pre[2];
+    MultiPlan plan; const float* s;
+    int max_items;
+};
+
+template <int NT>
+__device__ __forceinline__ void multi_pre_job(const MultiPreJob& j, const MultiPrologueArgs& a, int b,
+                                              PreStage<NT>& s0, PreStage<NT>& s1) {
+    constexpr int kLoads = 4 + NT;
+    const int item = b % a.max_items, sp = b / a.max_items;
+    if (item >= a.plan.head[1]) return;
+    const MultiItem it = a.plan.items[item];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int r = a.d.r;
+    const int kb = sp * j.kper;
+    const int ke = min(kb + j.kper, j.K / 64);
+    const uint16_t* prow[4];                           // the lane's 16-byte pieces of P rows 32 w + 8 u + lane / 8
+    const uint16_t* rrow[NT];                          // and of R rows 8 (4 i + w) + lane / 8
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int row = 32 * wave + 8 * u + (lane >> 3);
+        const int64_t tok = a.plan.order[it.pos + min(row, it.count - 1)];
+        prow[u] = j.P + tok * j.ldp + 8 * ((lane & 7) ^ ((row >> 1) & 7));
     }
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const int row = 8 * (4 * i + wave) + (lane >> 3);
+        rrow[i] = j.R + (static_cast<int64_t>(it.adapter) * r + min(row, r - 1)) * j.K + 8 * ((lane & 7) ^ ((row >> 1) & 7));
+    }
+    auto issue = [&](PreStage<NT>& st, int kc) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) load_lds16(prow[u] + static_cast<int64_t>(kc) * 64, &st.x[(32 * wave + 8 * u) * 8]);
+#pragma unroll
+        for (int i = 0; i < NT; ++i) load_lds16(rrow[i] + static_cast<int64_t>(kc) * 64, &st.r[8 * (4 * i + wave) * 8]);
+    };
+    f32x16 acc[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[t] = f32x16{};
+    issue(s0, kb);
+    for (int kc = kb; kc < ke; kc += 2) {
+        if (kc + 1 < ke) { issue(s1, kc + 1); QN_WAIT_VM(kLoads); }
+        else QN_WAIT_VM(0);
+        QN_PRE_BARRIER();
+        pre_compute<NT, false>(s0, wave, lane, acc);
+        QN_PRE_BARRIER();
+        if (kc + 1 >= ke) break;
+        if (kc + 2 < ke) { issue(s0, kc + 2); QN_WAIT_VM(kLoads); }
+        else QN_WAIT_VM(0);
+        QN_PRE_BARRIER();
+        pre_compute<NT, false>(s1, wave, lane, acc);
+        QN_PRE_BARRIER();
+    }
+    const int row = 32 * wave + (lane & 31);
+    if (row >= it.count) return;
+    const float s = a.s[it.adapter];
+    float* out = j.part + (static_cast<int64_t>(sp) * a.d.M + it.pos + row) * r;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int gq = 0; gq < 4; ++gq) {
+            const int n = t * 32 + 8 * gq + 4 * (lane >> 5);          // r % 16 == 0: 4 ranks in or out together
+            if (n < r)
+                *reinterpret_cast<float4*>(out + n) = float4{s * acc[t][4 * gq], s * acc[t][4 * gq + 1],
+                                                             s * acc[t][4 * gq + 2], s * acc[t][4 * gq + 3]};
+        }
+    }
+}
+
+// T[piece][pos][r] = the slice partials added in slice order, as 1 or 3 bf16 terms; 4 ranks
+// per thread. The positions of a token without an adapter are not written.
+struct MultiReduceJob { const float* part; uint16_t* T; int splits; };
+
+__global__ __launch_bounds__(256)
+void multi_reduce(MultiReduceJob j0, MultiReduceJob j1, int blocks0, const int32_t* __restrict__ head, int64_t M, int r,
+                  int pieces) {
+    const bool second = static_cast<int>(blockIdx.x) >= blocks0;
+    const MultiReduceJob& jb = second ? j1 : j0;
+    const int64_t idx = (static_cast<int64_t>(second ? blockIdx.x - blocks0 : blockIdx.x) * 256 + threadIdx.x) * 4;
+    if (idx >= static_cast<int64_t>(head[2]) * r) return;
+    const int64_t total = M * r;
+    const float4 t = ordered_sum4<8>(jb.part + idx, total, jb.splits);
+    float v[4] = {t.x, t.y, t.z, t.w};
+    for (int p = 0; p < pieces; ++p) {
+        uint16_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            h[e] = bf16_bits(v[e]);
+            const float f = bf16_to_f32(h[e]);
+            v[e] = fabsf(f) < __builtin_inff() ? v[e] - f : 0.0f;      // nothing is left of an infinity or NaN
+        }
+        *reinterpret_cast<uint2*>(jb.T + p * total + idx) =
+            uint2{h[0] | (static_cast<uint32_t>(h[1]) << 16), h[2] | (static_cast<uint32_t>(h[3]) << 16)};
+    }
+}
+#undef QN_PRE_BARRIER
+
+template <int NT>
+__global__ __launch_bounds__(256)
+void multi_prologue_kernel(MultiPrologueArgs a, NF4Tables tab) {
+    __shared__ PreStage<NT> s0, s1;
+    int b = blockIdx.x;
+    if (b < a.pre[0].n) {
+        multi_pre_job<NT>(a.pre[0], a, b, s0, s1);
+        return;
+    }
+    b -= a.pre[0].n;
+    if (b < a.pre[1].n) {
+        multi_pre_job<NT>(a.pre[1], a, b, s0, s1);
+        return;
+    }
+    dequant_jobs(a.d, b - a.pre[1].n, tab, reinterpret_cast<char*>(s1.x));
 }
 
 // ---------------------------------------------------------------------------
@@ -577,6 +715,17 @@ PreJob make_job(const uint16_t* P, int64_t ldp, int64_t M, int64_t K, const uint
     return j;
 }
 
+// The dequantisation of a launch: its sizes and workgroups (none if what is null).
+void set_dequant(PrologueArgs& a, int64_t d_out, int64_t d_in, bool transposed, uint16_t* what) {
+    a.d_out = d_out; a.d_in = d_in; a.transposed = transposed ? 1 : 0; a.what = what;
+    const int64_t n = d_out * d_in;
+    a.trans_tiles = static_cast<int>(std::min<int64_t>(kTransTiles, std::max<int64_t>(1, (n / 4096) / 2048)));
+    a.n_deq = what == nullptr ? 0   // pre-pass (and adapter layout) only
+                              : static_cast<int>(transposed ? (d_in / 64 + a.trans_tiles - 1) / a.trans_tiles *
+                                                                  ((d_out + 63) / 64)
+                                                            : (n + kDeqPerWG - 1) / kDeqPerWG);
+}
+
 // Launch the prologue for a (pre[0].n, pre[1].n set; the dequant and adapter fields
 // set by the caller), then one reduction of the split pre-pass jobs.
 hipError_t launch_prologue_args(PrologueArgs& a, bool km0, bool km1, hipStream_t st) {
@@ -621,7 +770,6 @@ hipError_t launch_prologue(const uint8_t* codes, const BlockConsts& bc, int64_t 
                            int64_t acols, float* ppart, hipStream_t st) {
     PrologueArgs a{};
     a.codes = codes; a.bc = bc;
-    a.d_out = d_out; a.d_in = d_in; a.transposed = transposed ? 1 : 0; a.what = what;
     // With the adapter laid out here (r < r_pad), the K-slices of the pre-pass can each
     // take r of the r_pad columns and the adapter repeat once per slice: the GEMM's
     // LoRA K-steps then add the slice partials, and no reduction pass is needed.
@@ -633,12 +781,7 @@ hipError_t launch_prologue(const uint8_t* codes, const BlockConsts& bc, int64_t 
     a.reps = a.pre[0].cat ? a.pre[0].psplits : 1;
     const int64_t adapt_elems = adapt_mode == 0 ? 0 : (adapt_mode == 1 ? arows : acols) * r_pad;
     a.n_adapt = static_cast<int>((adapt_elems / 8 + 255) / 256);    // one 8-entry chunk per thread
-    const int64_t n = d_out * d_in;
-    a.trans_tiles = static_cast<int>(std::min<int64_t>(kTransTiles, std::max<int64_t>(1, (n / 4096) / 2048)));
-    a.n_deq = what == nullptr ? 0   // pre-pass (and adapter layout) only
-                              : static_cast<int>(transposed ? (d_in / 64 + a.trans_tiles - 1) / a.trans_tiles *
-                                                                  ((d_out + 63) / 64)
-                                                            : (n + kDeqPerWG - 1) / kDeqPerWG);
+    set_dequant(a, d_out, d_in, transposed, what);
     static_assert(64 + 1024 + 64 * kTP * sizeof(uint16_t) <= sizeof(PreStage<1>::x), "dequant scratch fits a stage");
     return launch_prologue_args(a, r_kmajor, false, st);
 }
@@ -653,6 +796,43 @@ hipError_t launch_prepass_pair(const uint16_t* P0, int64_t ldp0, int64_t K0, con
     a.M = static_cast<int>(M); a.r = r; a.s = s; a.r_pad = r_pad;
     a.n_adapt = 0; a.n_deq = 0; a.trans_tiles = 1; a.reps = 1;
     return launch_prologue_args(a, false, r1_kmajor, st);
+}
+
+hipError_t launch_multi_prologue(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
+                                 bool transposed, uint16_t* what, const MultiPlan& plan, const float* s, int64_t M,
+                                 int n, int r, const MultiPre& p0, const MultiPre& p1, hipStream_t st) {
+    MultiPrologueArgs a{};
+    a.d.codes = codes; a.d.bc = bc; a.d.M = static_cast<int>(M); a.d.r = r;
+    set_dequant(a.d, d_out, d_in, transposed, what);
+    a.plan = plan; a.s = s;
+    a.max_items = static_cast<int>(multi_max_items(M, n));
+    const MultiPre* in[2] = {&p0, &p1};
+    for (int i = 0; i < 2; ++i) {
+        if (in[i]->R == nullptr) continue;
+        const PrepassSplit ps = prepass_split(M, in[i]->K);
+        a.pre[i] = MultiPreJob{in[i]->P, in[i]->ldp, static_cast<int>(in[i]->K), in[i]->R, in[i]->part, ps.splits,
+                               ps.kper, a.max_items * ps.splits};
+    }
+    const dim3 grid(static_cast<unsigned>(a.pre[0].n + a.pre[1].n + a.d.n_deq));
+    const NF4Tables& tab = tables();
+    switch ((r + 31) / 32) {
+#define QN_PRO_CASE(T) \
+        case T: QN_LAUNCH("multi_prologue_kernel", st, multi_prologue_kernel<T>, grid, dim3(256), 0, st, a, tab); break;
+        QN_PRO_CASE(1) QN_PRO_CASE(2) QN_PRO_CASE(3) QN_PRO_CASE(4)
+        QN_PRO_CASE(5) QN_PRO_CASE(6) QN_PRO_CASE(7) QN_PRO_CASE(8)
+#undef QN_PRO_CASE
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_multi_reduce(const MultiPlan& plan, int64_t M, int r, int pieces, const float* part0, int splits0,
+                               uint16_t* T0, const float* part1, int splits1, uint16_t* T1, hipStream_t st) {
+    const int blocks = static_cast<int>((M * r / 4 + 255) / 256);
+    const MultiReduceJob j0{part0, T0, splits0}, j1{part1, T1, splits1};
+    QN_LAUNCH("multi_reduce", st, multi_reduce, dim3(static_cast<unsigned>(part1 ? 2 * blocks : blocks)), dim3(256), 0,
+              st, j0, j1, blocks, plan.head, M, r, pieces);
+    return hipGetLastError();
 }
 
 hipError_t launch_transpose_pad(const uint16_t* src, int64_t rows, int64_t cols,

@@ -27,6 +27,7 @@
 
 #include "internal.h"
 #include "mfma_device.h"
+#include "multi.h"
 #include "nf4_device.h"
 
 #include <algorithm>
@@ -365,6 +366,34 @@ int skinny_splits(int64_t d_in, int64_t d_seq) {
     return static_cast<int>(std::min<int64_t>(cap, nslices));
 }
 
+namespace {
+
+hipError_t launch_stream(const SkArgs& a, hipStream_t st) {
+    const int blocks = a.d_out / kSkRows + (a.r + kSkRows - 1) / kSkRows;
+    const dim3 grid(static_cast<unsigned>(blocks * a.splits));
+    const NF4Tables& tab = tables();
+    switch ((a.d_seq + 15) / 16) {
+        case 1: QN_LAUNCH("skinny_nf4", st, skinny_nf4<1>, grid, dim3(kSkThreads), 0, st, a, tab); break;
+        case 2: QN_LAUNCH("skinny_nf4", st, skinny_nf4<2>, grid, dim3(kSkThreads), 0, st, a, tab); break;
+        case 3: QN_LAUNCH("skinny_nf4", st, skinny_nf4<3>, grid, dim3(kSkThreads), 0, st, a, tab); break;
+        case 4: QN_LAUNCH("skinny_nf4", st, skinny_nf4<4>, grid, dim3(kSkThreads), 0, st, a, tab); break;
+        default: return hipErrorInvalidValue;
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_skinny_stream(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
+                                const uint16_t* X, int64_t ldx, int64_t d_seq, float* part, hipStream_t st) {
+    SkArgs a{};
+    a.codes = codes; a.bc = bc;
+    a.d_out = static_cast<int>(d_out); a.d_in = static_cast<int>(d_in); a.d_seq = static_cast<int>(d_seq);
+    a.splits = skinny_splits(d_in, d_seq);
+    a.X = X; a.ldx = ldx; a.part = part;
+    return launch_stream(a, st);
+}
+
 hipError_t launch_skinny_nf4(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
                              const uint16_t* X, int64_t ldx, int64_t d_seq,
                              const uint16_t* A, const uint16_t* B, int r, int r_pad, float s, float* part,
@@ -375,16 +404,8 @@ hipError_t launch_skinny_nf4(const uint8_t* codes, const BlockConsts& bc, int64_
     a.splits = skinny_splits(d_in, d_seq);
     a.r = r; a.r_pad = r_pad;
     a.X = X; a.ldx = ldx; a.A = A; a.part = part; a.part_a = part_a;
-    const int blocks = static_cast<int>(d_out / kSkRows) + (r + kSkRows - 1) / kSkRows;
-    const dim3 grid(static_cast<unsigned>(blocks * a.splits));
-    const NF4Tables& tab = tables();
-    switch ((d_seq + 15) / 16) {
-        case 1: QN_LAUNCH("skinny_nf4", st, skinny_nf4<1>, grid, dim3(kSkThreads), 0, st, a, tab); break;
-        case 2: QN_LAUNCH("skinny_nf4", st, skinny_nf4<2>, grid, dim3(kSkThreads), 0, st, a, tab); break;
-        case 3: QN_LAUNCH("skinny_nf4", st, skinny_nf4<3>, grid, dim3(kSkThreads), 0, st, a, tab); break;
-        case 4: QN_LAUNCH("skinny_nf4", st, skinny_nf4<4>, grid, dim3(kSkThreads), 0, st, a, tab); break;
-        default: return hipErrorInvalidValue;
-    }
+    const hipError_t e = launch_stream(a, st);
+    if (e != hipSuccess) return e;
     // as many partial loads per output as there are splits (4 or 8), not 8 at clamped addresses
     const dim3 rgrid(static_cast<unsigned>(d_out / kRdRows));
     const int o = static_cast<int>(d_out), t = static_cast<int>(d_seq);

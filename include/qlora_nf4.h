@@ -341,6 +341,59 @@ int qlora_lora_grads(const uint16_t* A, const uint16_t* B, int r, float s,
                      void* workspace, int64_t workspace_bytes, void* stream);
 
 /*
+ * Many adapters on one layer. A batch of tokens of which each has its own adapter (or
+ * none): requests of many users served from one quantised weight, or several adapters
+ * trained in one batch.
+ *   [P1 LoRA: y = W0 x + s B(A x), with A, B and s of the token's adapter; P2 card 1: the
+ *    4-bit weight is shared and frozen, only the adapters differ]
+ * The adapters stand in a pool: A bf16 [n, r, d_in], B bf16 [n, d_out, r], s float32 [n],
+ * 1 <= n <= 1024 (QN_MULTI_MAX_ADAPTERS). All have rank r, a multiple of 16, r <= 256
+ * (smaller ranks: pad A and B with zeros, which changes nothing).
+ *
+ * qlora_multi_plan - the batch's plan, made once and then used by every call on the batch,
+ * in every layer and both directions.
+ *   ids   int32 [d_seq]: the adapter of each token, or any value outside [0, n) for none
+ *   plan  qlora_multi_plan_bytes(d_seq, n) bytes of device memory: the tokens sorted by
+ *         adapter (stable) and the work lists of the calls below
+ * The calls below must be given a plan made for their d_seq and n.
+ */
+#define QN_MULTI_MAX_ADAPTERS 1024
+int64_t qlora_multi_plan_bytes(int64_t d_seq, int n);
+int qlora_multi_plan(const int32_t* ids, int64_t d_seq, int n, void* plan, int64_t plan_bytes, void* stream);
+
+/* Workspace bytes of the two calls (0 on bad sizes). */
+int64_t qlora_multi_fwd_workspace_bytes(int64_t d_out, int64_t d_in, int64_t d_seq, int r, int n);
+int64_t qlora_multi_bwd_workspace_bytes(int64_t d_out, int64_t d_in, int64_t d_seq, int r, int n);
+
+/*
+ * qlora_multi_fwd - Y[t] = dequant(W) x_t + s_a B_a (A_a x_t), a the token's adapter; the
+ * first term alone for a token without one. Shapes, strides, alignment and errors as
+ * qlora_linear_fwd_ex (d_in, d_out multiples of 64; -2 for r not a multiple of 16 or n over
+ * the limit). A_a x_t is rounded to bf16 once; accumulation in float32, one final rounding.
+ * A token's result depends on its own adapter only: an infinity or NaN in another's weights
+ * does not reach it. Up to 64 tokens stream the packed codes (a decode batch); more run the
+ * MFMA GEMM on W_hat dequantised into the workspace.
+ */
+int qlora_multi_fwd(const uint8_t* codes, const int8_t* qconst, const float* qscale, const float* qmean,
+                    int64_t d_out, int64_t d_in, int dq, const uint16_t* A, const uint16_t* B, const float* s, int n,
+                    int r, const uint16_t* X, int64_t ldx, int64_t d_seq, const void* plan, uint16_t* Y, int64_t ldy,
+                    void* workspace, int64_t workspace_bytes, void* stream);
+
+/*
+ * qlora_multi_bwd - the gradients of qlora_multi_fwd for the loss gradient dY:
+ *   dX[t]  = dequant(W)^T dy_t + s_a A_a^T (B_a^T dy_t)         bf16 [d_seq, d_in]
+ *   dA_a   = s_a sum over a's tokens of (B_a^T dy_t) x_t^T      float32 [n, r, d_in]
+ *   dB_a   = s_a sum over a's tokens of dy_t (A_a x_t)^T        float32 [n, d_out, r]
+ * dA, dB of an adapter without tokens are zeros. dX rounds B_a^T dy_t to bf16 once; dA and
+ * dB use the rank products to 24 bits and accumulate in float32, in a fixed order.
+ */
+int qlora_multi_bwd(const uint8_t* codes, const int8_t* qconst, const float* qscale, const float* qmean,
+                    int64_t d_out, int64_t d_in, int dq, const uint16_t* A, const uint16_t* B, const float* s, int n,
+                    int r, const uint16_t* X, int64_t ldx, const uint16_t* dY, int64_t lddy, int64_t d_seq,
+                    const void* plan, uint16_t* dX, int64_t lddx, float* dA, float* dB, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+
+/*
  * AdamW over many tensors in one launch, with the moments in 32 bits or in 8: the step
  * that takes the adapter gradients (float32) to the adapters the linear calls read (bf16).
  *   [P2 card 1: only the adapters are trained; I. Loshchilov, F. Hutter, "Decoupled Weight

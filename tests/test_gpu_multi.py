@@ -1,0 +1,333 @@
+"""Many adapters on one layer against the float64 oracle: the plan, the forward in both its
+forms (up to 64 tokens, and the GEMM), and the gradients.
+
+Tolerances. Y and dX: those of the single-adapter products (parity.py). dA, dB are float32
+sums of up to ~1500 tokens of products with rank sums over up to 1536 features: with
+u = 2^-24 per addition and independent roundings, sqrt(1500 + 1536) u = 3.3e-6 of the norm
+(5e-6 allowed), and 5 deviations of that on the largest element (2e-5 of it)."""
+import numpy as np
+import pytest
+import torch
+
+import bit_nf4_quantized_05_amd as qn
+import workloads as WL
+from oracle import multi_oracle as MO
+from oracle import nf4_oracle as O
+from parity import bf16_f64, check_close, dev, to_gpu_f32
+
+pytestmark = pytest.mark.gpu
+
+
+def _say(*a):
+    print(*a, flush=True)
+
+
+def _pool(n, r, d_out, d_in, gen, sigma=0.05):
+    return qn.AdapterPool((torch.randn(n, r, d_in, generator=gen, device=dev()) * sigma).bfloat16(),
+                          (torch.randn(n, d_out, r, generator=gen, device=dev()) * sigma).bfloat16(),
+                          torch.rand(n, generator=gen, device=dev()) + 0.5)
+
+
+def _f64(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def _ids(kind, M, n, rng):
+    if kind == "none":
+        return np.full(M, -1, np.int32)
+    if kind == "one":
+        return np.full(M, n - 1, np.int32)
+    if kind == "mixed":                                     # every token anybody's, some nobody's
+        return rng.integers(-1, n, M).astype(np.int32)
+    if kind == "outside":                                   # ids past the pool count as none
+        return rng.choice(np.array([0, n, n + 5, -7, 2 ** 31 - 1], np.int64), M).astype(np.int32)
+    # packed requests of uneven lengths
+    reqs = min(M, max(1, n + 2))
+    cuts = np.sort(rng.choice(np.arange(1, M), reqs - 1, replace=False)) if reqs > 1 else np.array([], int)
+    who = rng.integers(-1, n, reqs)
+    return np.repeat(who, np.diff(np.concatenate([[0], cuts, [M]]))).astype(np.int32)
+
+
+class Layer:
+    def __init__(self, d_out, d_in, M, r, n, kind, seed, dq="int8"):
+        self.gen = torch.Generator(device=dev()).manual_seed(seed)
+        rng = np.random.default_rng(seed)
+        w = WL.make_weight(WL.custom("m", d_out, d_in, 1, 8, seed=seed))
+        self.q = qn.quantize(to_gpu_f32(w), dq=dq)
+        self.W = bf16_f64(qn.double_dequant(self.q))
+        self.pool = _pool(n, r, d_out, d_in, self.gen)
+        self.ids_np = _ids(kind, M, n, rng)
+        self.ids = torch.from_numpy(self.ids_np).to(dev())
+        self.plan = qn.multi_plan(self.ids, n)
+        self.X = torch.randn(M, d_in, generator=self.gen, device=dev()).bfloat16()
+        self.dY = torch.randn(M, d_out, generator=self.gen, device=dev()).bfloat16()
+        self.A, self.B, self.s = _f64(self.pool.A), _f64(self.pool.B), _f64(self.pool.s)
+
+    def forward(self):
+        return MO.forward(self.W, self.A, self.B, self.s, self.ids_np, _f64(self.X))
+
+    def backward(self):
+        return MO.backward(self.W, self.A, self.B, self.s, self.ids_np, _f64(self.X), _f64(self.dY))
+
+
+def _close32(got, ref, what):
+    got = _f64(got)
+    assert np.all(np.isfinite(got)), what
+    norm = np.linalg.norm(ref)
+    if norm == 0:
+        assert np.all(got == 0), what
+        return
+    rel, big = np.linalg.norm(got - ref) / norm, np.max(np.abs(got - ref)) / np.max(np.abs(ref))
+    assert rel <= 5e-6 and big <= 2e-5, f"{what}: {rel:.2e} {big:.2e}"
+
+
+# ---- the plan -------------------------------------------------------------------------
+
+def _plan_parts(plan):
+    """(head, order, start, first_item, used, tile, items) of a plan's buffer."""
+    w = plan.buf.cpu().numpy().view(np.int32)
+    M, n = plan.d_seq, plan.n
+    up = lambda v: (v + 3) // 4 * 4  # noqa: E731
+    at, out = 4, [w[:4]]
+    for size in (M, n + 1, n, min(n, M), 2 * ((M + 255) // 256)):
+        out.append(w[at:at + size])
+        at += up(size)
+    items = w[at:at + 4 * ((M + 127) // 128 + min(n, M))].reshape(-1, 4)
+    return out + [items]
+
+
+@pytest.mark.parametrize("M,n,kind", [(1, 1, "one"), (1, 5, "none"), (63, 64, "mixed"), (64, 3, "packed"),
+                                      (65, 1, "mixed"), (1000, 7, "packed"), (1024, 7, "outside"),
+                                      (4097, 1024, "mixed"), (5000, 1000, "packed"), (20011, 33, "mixed")])
+def test_plan(M, n, kind):
+    _say(f"[multi] plan {M} tokens, {n} adapters, {kind}")
+    ids = _ids(kind, M, n, np.random.default_rng(M + n))
+    plan = qn.multi_plan(torch.from_numpy(ids).to(dev()), n)
+    torch.cuda.synchronize()
+    head, order, start, first, used, tile, items = _plan_parts(plan)
+    key = np.where((ids >= 0) & (ids < n), ids, n)
+    want = np.argsort(key, kind="stable")
+    assert np.array_equal(order, want)
+    counts = np.bincount(key, minlength=n + 1)
+    assert np.array_equal(start, np.concatenate([[0], np.cumsum(counts[:n])]))
+    act = np.flatnonzero(counts[:n])
+    assert head[0] == len(act) and np.array_equal(used[:len(act)], act) and head[2] == counts[:n].sum()
+    rows = []
+    for a in act:
+        assert first[a] == len(rows)
+        rows += [(a, start[a] + k, min(128, counts[a] - k), k // 128) for k in range(0, counts[a], 128)]
+    assert head[1] == len(rows) and np.array_equal(items[:len(rows)].reshape(-1, 4), np.array(rows, int).reshape(-1, 4))
+    for t in range((M + 255) // 256):
+        have = [a for k, a in enumerate(act) if start[a] < min(256 * t + 256, head[2]) and start[a + 1] > 256 * t]
+        k0, k1 = tile[2 * t], tile[2 * t + 1]
+        assert list(used[k0:k1]) == have, t
+    again = qn.multi_plan(torch.from_numpy(ids[::-1].copy()).to(dev()), n, out=plan)
+    assert again is plan and np.array_equal(_plan_parts(plan)[1], np.argsort(key[::-1], kind="stable"))
+
+
+# ---- forward --------------------------------------------------------------------------
+
+SMALL = [(64, 64, 1, 16, 1, "one"), (256, 320, 1, 16, 4, "none"), (512, 4096, 3, 32, 3, "mixed"),
+         (1024, 1088, 16, 16, 40, "mixed"), (320, 192, 17, 48, 2, "mixed"), (512, 2048, 33, 64, 33, "packed"),
+         (192, 11008, 64, 80, 64, "mixed"), (4096, 512, 64, 256, 5, "mixed"), (256, 256, 64, 16, 1, "one"),
+         (128, 64, 40, 128, 300, "outside")]
+LARGE = [(256, 256, 65, 16, 3, "mixed"), (320, 192, 300, 32, 5, "packed"), (512, 4096, 200, 48, 40, "mixed"),
+         (1024, 1536, 1531, 16, 7, "packed"), (256, 512, 1024, 64, 4, "packed"), (64, 64, 257, 256, 2, "mixed"),
+         (192, 128, 513, 80, 64, "outside"), (256, 320, 700, 112, 1, "one"), (256, 256, 600, 16, 9, "none"),
+         (128, 192, 2000, 16, 1000, "mixed"), (2048, 2048, 2100, 16, 3, "packed")]
+
+
+@pytest.mark.parametrize("d_out,d_in,M,r,n,kind", SMALL + LARGE)
+def test_forward(d_out, d_in, M, r, n, kind):
+    _say(f"[multi] forward {d_out}x{d_in}, {M} tokens, r={r}, {n} adapters, {kind}")
+    L = Layer(d_out, d_in, M, r, n, kind, seed=M + r)
+    Y = qn.multi_linear_fwd(L.q, L.pool, L.plan, L.X)
+    torch.cuda.synchronize()
+    check_close(_f64(Y), L.forward(), "forward")
+    again = qn.multi_linear_fwd(L.q, L.pool, L.plan, L.X)
+    assert torch.equal(Y.view(torch.int16), again.view(torch.int16))
+
+
+@pytest.mark.parametrize("dq", ["fp8", "none"])
+@pytest.mark.parametrize("M", [20, 150])
+def test_second_level_formats(dq, M):
+    _say(f"[multi] second level {dq}, {M} tokens")
+    L = Layer(256, 320, M, 16, 4, "mixed", seed=5, dq=dq)
+    check_close(_f64(qn.multi_linear_fwd(L.q, L.pool, L.plan, L.X)), L.forward(), "forward")
+    check_close(_f64(qn.multi_linear_bwd(L.q, L.pool, L.plan, L.X, L.dY)[0]), L.backward()[0], "dX")
+
+
+@pytest.mark.parametrize("M", [1, 30, 64, 65, 400])
+def test_rows_of_wider_arrays(M):
+    """Strided inputs and outputs: the contiguous call's bits, and nothing else is written."""
+    _say(f"[multi] windows, {M} tokens")
+    d_out, d_in, r, n = 320, 256, 32, 5
+    L = Layer(d_out, d_in, M, r, n, "mixed", seed=M)
+    ref = qn.multi_linear_fwd(L.q, L.pool, L.plan, L.X)
+    dX, dA, dB = qn.multi_linear_bwd(L.q, L.pool, L.plan, L.X, L.dY)
+    wide = torch.full((M, d_in + 40), 7.0, device=dev()).bfloat16()
+    wide[:, 16:16 + d_in] = L.X
+    wdy = torch.full((M, d_out + 8), 7.0, device=dev()).bfloat16()
+    wdy[:, :d_out] = L.dY
+    out = torch.full((M + 2, d_out + 24), 3.0, device=dev()).bfloat16()
+    gx = torch.full((M + 2, d_in + 24), 3.0, device=dev()).bfloat16()
+    qn.multi_linear_fwd(L.q, L.pool, L.plan, wide[:, 16:16 + d_in], out=out[1:M + 1, 8:8 + d_out])
+    _, wA, wB = qn.multi_linear_bwd(L.q, L.pool, L.plan, wide[:, 16:16 + d_in], wdy[:, :d_out], dX=gx[1:M + 1, 8:8 + d_in])
+    torch.cuda.synchronize()
+    for got, want, cols in ((out, ref, d_out), (gx, dX, d_in)):
+        assert torch.equal(got[1:M + 1, 8:8 + cols].reshape(M, cols).view(torch.int16), want.view(torch.int16))
+        got[1:M + 1, 8:8 + cols] = 3.0
+        assert torch.all(got == 3.0)
+    assert torch.equal(wA, dA) and torch.equal(wB, dB)
+
+
+@pytest.mark.parametrize("M", [48, 64, 300, 700])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_adapters_do_not_reach_each_other(M, value):
+    """An adapter of NaN or infinity leaves every other token's Y and dX, and every other
+    adapter's gradients, at the bits they have with a finite one."""
+    _say(f"[multi] isolation, {M} tokens, {value}")
+    L = Layer(192, 256, M, 16, 6, "mixed", seed=M)
+    ref = qn.multi_linear_fwd(L.q, L.pool, L.plan, L.X)
+    rX, rA, rB = qn.multi_linear_bwd(L.q, L.pool, L.plan, L.X, L.dY)
+    bad = 2
+    L.pool.A[bad, 3, 5] = value
+    L.pool.B[bad, 7, 2] = value
+    Y = qn.multi_linear_fwd(L.q, L.pool, L.plan, L.X)
+    dX, dA, dB = qn.multi_linear_bwd(L.q, L.pool, L.plan, L.X, L.dY)
+    torch.cuda.synchronize()
+    other = L.ids != bad
+    assert torch.equal(Y[other].view(torch.int16), ref[other].view(torch.int16))
+    assert torch.equal(dX[other].view(torch.int16), rX[other].view(torch.int16))
+    assert not torch.isfinite(Y[~other].float()).all() and not torch.isfinite(dX[~other].float()).all()
+    keep = [a for a in range(6) if a != bad]
+    assert torch.equal(dA[keep], rA[keep]) and torch.equal(dB[keep], rB[keep])
+
+
+@pytest.mark.parametrize("M", [50, 400])
+def test_tokens_of_nan_stay_apart(M):
+    """A token of NaN changes only its own rows and its own adapter's gradients."""
+    _say(f"[multi] NaN token, {M} tokens")
+    L = Layer(128, 192, M, 32, 4, "mixed", seed=3 + M)
+    ref = qn.multi_linear_fwd(L.q, L.pool, L.plan, L.X)
+    rX, rA, rB = qn.multi_linear_bwd(L.q, L.pool, L.plan, L.X, L.dY)
+    t = int(np.flatnonzero(L.ids_np == 1)[0])
+    L.X[t] = float("nan")
+    L.dY[t] = float("inf")
+    Y = qn.multi_linear_fwd(L.q, L.pool, L.plan, L.X)
+    dX, dA, dB = qn.multi_linear_bwd(L.q, L.pool, L.plan, L.X, L.dY)
+    torch.cuda.synchronize()
+    rows = [k for k in range(M) if k != t]
+    assert torch.equal(Y[rows].view(torch.int16), ref[rows].view(torch.int16)) and torch.isnan(Y[t]).all()
+    assert torch.equal(dX[rows].view(torch.int16), rX[rows].view(torch.int16))
+    assert torch.equal(dA[[0, 2, 3]], rA[[0, 2, 3]]) and torch.equal(dB[[0, 2, 3]], rB[[0, 2, 3]])
+
+
+def test_ranks_padded_by_the_pool():
+    """Adapters of ranks 1, 5 and 20 in one pool give what each gives by its own rank."""
+    _say("[multi] mixed ranks")
+    L = Layer(256, 192, 90, 16, 3, "mixed", seed=9)
+    pool = qn.alloc_pool(3, 20, 256, 192, dev())
+    assert pool.r == 32
+    A, B = [], []
+    for i, k in enumerate((1, 5, 20)):
+        A.append((torch.randn(k, 192, generator=L.gen, device=dev()) * 0.05).bfloat16())
+        B.append((torch.randn(256, k, generator=L.gen, device=dev()) * 0.05).bfloat16())
+        pool.set(i, A[i], B[i], 1.5 + i)
+    Y = qn.multi_linear_fwd(L.q, pool, L.plan, L.X)
+    _, dA, dB = qn.multi_linear_bwd(L.q, pool, L.plan, L.X, L.dY)
+    X, dY = _f64(L.X), _f64(L.dY)
+    ref = X @ L.W.T
+    for i, k in enumerate((1, 5, 20)):
+        t = np.flatnonzero(L.ids_np == i)
+        T = X[t] @ _f64(A[i]).T
+        ref[t] += (1.5 + i) * (T @ _f64(B[i]).T)
+        _close32(dB[i, :, :k], (1.5 + i) * (dY[t].T @ T), f"dB rank {k}")
+        assert torch.all(dB[i, :, k:] == 0) and torch.all(dA[i, k:] == 0)
+    check_close(_f64(Y), ref, "mixed ranks")
+
+
+# ---- gradients ------------------------------------------------------------------------
+
+BWD = [(64, 64, 1, 16, 2, "one"), (256, 256, 203, 16, 3, "packed"), (320, 192, 40, 48, 6, "mixed"),
+       (192, 320, 700, 32, 2, "packed"), (512, 1024, 1300, 16, 1, "one"), (128, 256, 900, 80, 5, "mixed"),
+       (256, 192, 1500, 64, 3, "packed"), (64, 128, 300, 256, 4, "mixed"), (128, 128, 500, 16, 200, "mixed"),
+       (256, 256, 130, 16, 4, "none"), (1536, 1088, 640, 128, 3, "packed")]
+
+
+@pytest.mark.parametrize("d_out,d_in,M,r,n,kind", BWD)
+def test_gradients(d_out, d_in, M, r, n, kind):
+    _say(f"[multi] gradients {d_out}x{d_in}, {M} tokens, r={r}, {n} adapters, {kind}")
+    L = Layer(d_out, d_in, M, r, n, kind, seed=M + r + 1)
+    junk = torch.full(L.pool.A.shape, float("nan"), device=dev()), torch.full(L.pool.B.shape, float("nan"), device=dev())
+    dX, dA, dB = qn.multi_linear_bwd(L.q, L.pool, L.plan, L.X, L.dY, dA=junk[0], dB=junk[1])
+    torch.cuda.synchronize()
+    wX, wA, wB = L.backward()
+    check_close(_f64(dX), wX, "dX")
+    _close32(dA, wA, "dA")
+    _close32(dB, wB, "dB")
+    again = qn.multi_linear_bwd(L.q, L.pool, L.plan, L.X, L.dY)
+    for x, y in zip((dX, dA, dB), again):
+        assert torch.equal(x, y)
+
+
+# ---- streams and graphs ---------------------------------------------------------------
+
+@pytest.mark.parametrize("M", [24, 300])
+def test_other_stream_and_graph(M):
+    _say(f"[multi] side stream and graph replays, {M} tokens")
+    L = Layer(512, 256, M, 16, 7, "mixed", seed=M)
+    Y, dX = torch.empty_like(L.dY), torch.empty_like(L.X)
+    dA, dB = (torch.empty(p.shape, dtype=torch.float32, device=dev()) for p in (L.pool.A, L.pool.B))
+    ws = torch.empty(max(qn.multi_linear_fwd_workspace_bytes(512, 256, M, 16, 7),
+                         qn.multi_linear_bwd_workspace_bytes(512, 256, M, 16, 7)), dtype=torch.uint8, device=dev())
+
+    def calls():
+        qn.multi_plan(L.ids, 7, out=L.plan)
+        qn.multi_linear_fwd(L.q, L.pool, L.plan, L.X, out=Y, workspace=ws)
+        qn.multi_linear_bwd(L.q, L.pool, L.plan, L.X, L.dY, dX=dX, dA=dA, dB=dB, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        calls()
+    rng = np.random.default_rng(M)
+    for k in range(4):
+        L.ids.copy_(torch.from_numpy(_ids("mixed" if k % 2 else "packed", M, 7, rng)))
+        L.X.copy_(torch.randn(L.X.shape, generator=L.gen, device=dev()))
+        L.dY.copy_(torch.randn(L.dY.shape, generator=L.gen, device=dev()))
+        (torch.randn(256, 256, device=dev()) @ torch.randn(256, 256, device=dev())).sum().item()
+        graph.replay()
+        torch.cuda.synchronize()
+        plan = qn.multi_plan(L.ids, 7)
+        eY = qn.multi_linear_fwd(L.q, L.pool, plan, L.X)
+        eX, eA, eB = qn.multi_linear_bwd(L.q, L.pool, plan, L.X, L.dY)
+        torch.cuda.synchronize()
+        for x, y in ((Y, eY), (dX, eX), (dA, eA), (dB, eB)):
+            assert torch.equal(x, y), f"replay {k}"
+
+
+def test_training_step_lowers_the_loss():
+    """Plan, forward, gradients and AdamW together: two adapters learn two targets."""
+    _say("[multi] training steps")
+    L = Layer(256, 256, 240, 16, 2, "mixed", seed=21)
+    L.pool.B.zero_()
+    target = torch.randn(240, 256, generator=L.gen, device=dev()) * 0.3 + (L.X @ torch.from_numpy(L.W.T).to(dev()).bfloat16()).float()
+    masters = [L.pool.A.float(), L.pool.B.float()]
+    dA, dB = (torch.empty_like(m) for m in masters)
+    opt = qn.adamw_state(masters, [dA, dB], copies=[L.pool.A, L.pool.B], bits=8)
+    losses = []
+    for step in range(1, 31):
+        Y = qn.multi_linear_fwd(L.q, L.pool, L.plan, L.X)
+        err = Y.float() - target
+        live = (L.ids >= 0)[:, None]
+        losses.append((err * live).square().sum().item())
+        dY = (err * live * (2.0 / err.numel())).bfloat16()
+        qn.multi_linear_bwd(L.q, L.pool, L.plan, L.X, dY, dA=dA, dB=dB)
+        qn.adamw_step(opt, step, 3e-3)
+    assert losses[-1] < 0.7 * losses[0], losses[::10]
