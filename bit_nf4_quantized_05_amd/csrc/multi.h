@@ -101,15 +101,14 @@ hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, 
                              const uint16_t* R, int r, const MultiPlan& plan, uint16_t* C, int64_t ldc, int64_t M,
                              int64_t N, float* part, hipStream_t st);
 
-// ---- skinny.hip ----
-// The W_hat x partials alone, [skinny_splits(d_in, d_seq)][d_seq][d_out] floats
-hipError_t launch_skinny_stream(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
-                                const uint16_t* X, int64_t ldx, int64_t d_seq, float* part, hipStream_t st);
-
-// ---- multi_small.hip ----
-// Forward of up to kSkinnyMaxTokens tokens from the packed codes. part holds
-// skinny_splits * M * d_out floats, part_t multi_small_splits(d_in) * M * r.
+// ---- skinny.hip, multi_small.hip ----
+// Forward of up to kSkinnyMaxTokens tokens from the packed codes: the W_hat x partials
+// [skinny_splits(d_in, M)][M][d_out] by token and the s_a A_a x partials
+// [multi_small_splits(d_in)][M][r] by position in one launch, then Y from both.
 int multi_small_splits(int64_t d_in);
+hipError_t launch_skinny_multi(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
+                               const MultiPool& pool, const MultiPlan& plan, const uint16_t* X, int64_t ldx,
+                               int64_t M, float* part, float* part_t, hipStream_t st);
 hipError_t launch_multi_small(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
                               const MultiPool& pool, const uint16_t* X, int64_t ldx, int64_t M,
                               const MultiPlan& plan, float* part, float* part_t, uint16_t* Y, int64_t ldy,

@@ -68,9 +68,97 @@ __device__ __forceinline__ void mma(f32x4 (&acc)[TT], const uint4* xs, const uin
     for (int t = 0; t < TT; ++t) acc[t] = mfma16(af, xs[(t * 16 + i) * 64 + (c ^ i)], acc[t]);
 }
 
-template <int TT>   // 16-token tiles
+// A x of tokens that belong to many adapters (multi_small.hip tells the whole): job b of the
+// launch takes one item of the plan (the tokens of one adapter), 16 ranks and a slice of K,
+// the 8 waves the slice's 64-wide blocks in turn. One MFMA operand is the 16
+// rank rows of the adapter, the other 16 gathered tokens, both straight from memory (a lane
+// takes 32 contiguous bytes of its row, the k order permuted alike on both sides); the waves'
+// sums are added through LDS (red: 7 TT x 64 float4) in wave order and written times s_a.
+struct MultiAx {
+    MultiPlan plan; MultiPool pool;
+    int max_items, splits, bper;        // items, K-slices and 64-wide blocks per slice
+    float* part;                        // [splits][d_seq][r], by position
+};
+
+template <int TT>
+__device__ __forceinline__ void multi_ax_job(const MultiAx& m, const SkArgs& a, int b, f32x4* red) {
+    constexpr int NW = kSkThreads / 64;
+    const int item = b % m.max_items;
+    b /= m.max_items;
+    const int sp = b % m.splits;
+    const int j0 = b / m.splits * 16;
+    if (item >= m.plan.head[1]) return;
+    const MultiItem it = m.plan.items[item];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int i = lane & 15, g = lane >> 4;
+    const int b0 = sp * m.bper, b1 = min(b0 + m.bper, a.d_in / 64);
+    const uint16_t* arow = m.pool.A + (static_cast<int64_t>(it.adapter) * m.pool.r + j0 + i) * a.d_in + 16 * g;
+    const uint16_t* xrow[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        const int64_t tok = m.plan.order[it.pos + min(16 * t + i, it.count - 1)];
+        xrow[t] = a.X + tok * a.ldx + 16 * g;
+    }
+    f32x4 acc[TT];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // U blocks k, k + 8 at a time (past the slice: k again, not added); with 3 or 4 token tiles
+    // one, or the registers would leave room for one workgroup per CU instead of two
+    constexpr int U = TT <= 2 ? 2 : 1;
+    for (int k = b0 + wave; k < b1; k += U * NW) {
+        uint4 av[U][2], xv[TT][U][2];
+        int64_t off[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            off[u] = static_cast<int64_t>(k + u * NW < b1 ? k + u * NW : k) * 64;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) av[u][h] = reinterpret_cast<const uint4*>(arow + off[u])[h];
+        }
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+            if (16 * t < it.count) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) xv[t][u][h] = reinterpret_cast<const uint4*>(xrow[t] + off[u])[h];
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (k + u * NW < b1) {
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+                    if (16 * t < it.count) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) acc[t] = mfma16(av[u][h], xv[t][u][h], acc[t]);
+                    }
+            }
+    }
+    if (wave > 0) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t) red[((wave - 1) * TT + t) * 64 + lane] = acc[t];
+    }
+    __syncthreads();
+    if (wave > 0) return;
+    const float s = m.pool.s[it.adapter];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        const int row = 16 * t + i;
+        if (row >= it.count) continue;
+        f32x4 v = acc[t];
+#pragma unroll
+        for (int q = 0; q < NW - 1; ++q) v = v + red[(q * TT + t) * 64 + lane];
+        // D of a 16 x 16 tile: lane l holds ranks 4 (l / 16) .. + 3 of token l % 16
+        float* out = m.part + (static_cast<int64_t>(sp) * a.d_seq + it.pos + row) * m.pool.r + j0 + 4 * g;
+        *reinterpret_cast<float4*>(out) = float4{s * v[0], s * v[1], s * v[2], s * v[3]};
+    }
+}
+
+// TT 16-token tiles; kMulti: the first m.n workgroups form A x of many adapters instead of
+// the rows of one A past the rows of W (a.r = 0)
+template <int TT, bool kMulti>
 __global__ __launch_bounds__(kSkThreads)
-void skinny_nf4(SkArgs a, NF4Tables tab) {
+void skinny_nf4(SkArgs a, NF4Tables tab, MultiAx m, int n_ax) {
     constexpr int KQ = kSkKq;
     constexpr int NW = 4 * KQ;                     // waves
     constexpr int NT = 64 * NW;                    // threads
@@ -83,10 +171,18 @@ void skinny_nf4(SkArgs a, NF4Tables tab) {
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int rg = wave & 3;                       // 16-row group
     const int kq = wave >> 2;                      // block pairs kq, kq + KQ, ... of each slice
+    if constexpr (kMulti) {
+        static_assert((NW - 1) * TT * 64 <= TT * 16 * kSkBlk * 8, "the sums of A x fit the x buffer");
+        if (static_cast<int>(blockIdx.x) < n_ax) {
+            multi_ax_job<TT>(m, a, static_cast<int>(blockIdx.x), reinterpret_cast<f32x4*>(xs));
+            return;
+        }
+    }
+    const int bid = static_cast<int>(blockIdx.x) - (kMulti ? n_ax : 0);
     const int row_blocks = a.d_out / kSkRows;
     const int all_blocks = row_blocks + (a.r + kSkRows - 1) / kSkRows;
-    const int rb = static_cast<int>(blockIdx.x) % all_blocks;
-    const int sp = static_cast<int>(blockIdx.x) / all_blocks;
+    const int rb = bid % all_blocks;
+    const int sp = bid / all_blocks;
     const bool lora = rb >= row_blocks;            // workgroup-uniform: rows of A
     const int ra = (rb - row_blocks) * kSkRows + rg * 16 + (threadIdx.x & 15);
     const int nb = a.d_in / 64;
@@ -368,30 +464,46 @@ int skinny_splits(int64_t d_in, int64_t d_seq) {
 
 namespace {
 
-hipError_t launch_stream(const SkArgs& a, hipStream_t st) {
+template <bool kMulti>
+hipError_t launch_stream(const SkArgs& a, const MultiAx& m, int n_ax, hipStream_t st) {
     const int blocks = a.d_out / kSkRows + (a.r + kSkRows - 1) / kSkRows;
-    const dim3 grid(static_cast<unsigned>(blocks * a.splits));
+    const dim3 grid(static_cast<unsigned>(n_ax + blocks * a.splits));
     const NF4Tables& tab = tables();
     switch ((a.d_seq + 15) / 16) {
-        case 1: QN_LAUNCH("skinny_nf4", st, skinny_nf4<1>, grid, dim3(kSkThreads), 0, st, a, tab); break;
-        case 2: QN_LAUNCH("skinny_nf4", st, skinny_nf4<2>, grid, dim3(kSkThreads), 0, st, a, tab); break;
-        case 3: QN_LAUNCH("skinny_nf4", st, skinny_nf4<3>, grid, dim3(kSkThreads), 0, st, a, tab); break;
-        case 4: QN_LAUNCH("skinny_nf4", st, skinny_nf4<4>, grid, dim3(kSkThreads), 0, st, a, tab); break;
+#define QN_SK_CASE(TT) \
+        case TT: \
+            QN_LAUNCH(kMulti ? "skinny_nf4_multi" : "skinny_nf4", st, (skinny_nf4<TT, kMulti>), grid, \
+                      dim3(kSkThreads), 0, st, a, tab, m, n_ax); \
+            break;
+        QN_SK_CASE(1) QN_SK_CASE(2) QN_SK_CASE(3) QN_SK_CASE(4)
+#undef QN_SK_CASE
         default: return hipErrorInvalidValue;
     }
     return hipGetLastError();
 }
 
+// K-slices of A x: at most 8, of at least 16 blocks (two per wave)
+int ax_blocks(int64_t d_in) { return static_cast<int>(std::max<int64_t>(16, (d_in / 64 + 7) / 8)); }
+
 }  // namespace
 
-hipError_t launch_skinny_stream(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
-                                const uint16_t* X, int64_t ldx, int64_t d_seq, float* part, hipStream_t st) {
+int multi_small_splits(int64_t d_in) { return static_cast<int>((d_in / 64 + ax_blocks(d_in) - 1) / ax_blocks(d_in)); }
+
+hipError_t launch_skinny_multi(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
+                               const MultiPool& pool, const MultiPlan& plan, const uint16_t* X, int64_t ldx,
+                               int64_t d_seq, float* part, float* part_t, hipStream_t st) {
     SkArgs a{};
     a.codes = codes; a.bc = bc;
     a.d_out = static_cast<int>(d_out); a.d_in = static_cast<int>(d_in); a.d_seq = static_cast<int>(d_seq);
     a.splits = skinny_splits(d_in, d_seq);
     a.X = X; a.ldx = ldx; a.part = part;
-    return launch_stream(a, st);
+    MultiAx m{};
+    m.plan = plan; m.pool = pool;
+    m.max_items = static_cast<int>(multi_max_items(d_seq, pool.n));
+    m.splits = multi_small_splits(d_in);
+    m.bper = ax_blocks(d_in);
+    m.part = part_t;
+    return launch_stream<true>(a, m, m.max_items * m.splits * (pool.r / 16), st);
 }
 
 hipError_t launch_skinny_nf4(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
@@ -404,7 +516,7 @@ hipError_t launch_skinny_nf4(const uint8_t* codes, const BlockConsts& bc, int64_
     a.splits = skinny_splits(d_in, d_seq);
     a.r = r; a.r_pad = r_pad;
     a.X = X; a.ldx = ldx; a.A = A; a.part = part; a.part_a = part_a;
-    const hipError_t e = launch_stream(a, st);
+    const hipError_t e = launch_stream<false>(a, MultiAx{}, 0, st);
     if (e != hipSuccess) return e;
     // as many partial loads per output as there are splits (4 or 8), not 8 at clamped addresses
     const dim3 rgrid(static_cast<unsigned>(d_out / kRdRows));
