@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from dataclasses import dataclass
+from dataclasses import dataclass, field
 
 import torch
 
@@ -479,29 +479,38 @@ def qlr_linear_fwd(q: NF4Weight, Af: QFactor, Bf: QFactor, s: float, X: torch.Te
 MULTI_RANK_STEP = 16          # ranks of a pool come in this step
 
 
-@dataclass
+@dataclass(frozen=True)
 class AdapterPool:
     """Adapters of one layer side by side: A bfloat16 [n, r, d_in], B bfloat16
-    [n, d_out, r], s float32 [n] (each adapter's LoRA scale); r a multiple of 16.
+    [n, d_out, r], s float32 [n] (each adapter's LoRA scale); r a multiple of 16. Checked
+    when it is made; the tensors' contents may change, the tensors may not be replaced.
     ``alloc_pool`` and ``set`` make one from adapters of any rank up to r."""
     A: torch.Tensor
     B: torch.Tensor
     s: torch.Tensor
+    n: int = field(init=False)
+    r: int = field(init=False)
+    d_in: int = field(init=False)
+    d_out: int = field(init=False)
+    device: torch.device = field(init=False)
 
-    @property
-    def n(self) -> int:
-        return self.A.shape[0]
-
-    @property
-    def r(self) -> int:
-        return self.A.shape[1]
+    def __post_init__(self):
+        A, B, s = self.A, self.B, self.s
+        if A.dim() != 3 or B.dim() != 3:
+            raise ValueError("expected A [n, r, d_in] and B [n, d_out, r]")
+        (n, r, d_in), d_out, dev = A.shape, B.shape[1], A.device
+        _need(A, torch.bfloat16, (n, r, d_in), "pool.A", dev)
+        _need(B, torch.bfloat16, (n, d_out, r), "pool.B", dev)
+        _need(s, torch.float32, (n,), "pool.s", dev)
+        for name, v in (("n", n), ("r", r), ("d_in", d_in), ("d_out", d_out), ("device", dev)):
+            object.__setattr__(self, name, v)
 
     def set(self, i: int, A: torch.Tensor, B: torch.Tensor, s: float) -> None:
         """Puts an adapter (A [k, d_in], B [d_out, k], k <= r, scale s) at place i; ranks
         past k are zeros."""
         k = A.shape[0]
-        if A.shape != (k, self.A.shape[2]) or B.shape != (self.B.shape[1], k) or not 1 <= k <= self.r:
-            raise ValueError(f"expected A [k, {self.A.shape[2]}] and B [{self.B.shape[1]}, k] with k <= {self.r}")
+        if A.shape != (k, self.d_in) or B.shape != (self.d_out, k) or not 1 <= k <= self.r:
+            raise ValueError(f"expected A [k, {self.d_in}] and B [{self.d_out}, k] with k <= {self.r}")
         self.A[i].zero_()
         self.B[i].zero_()
         self.A[i, :k] = A
@@ -519,7 +528,7 @@ def alloc_pool(n: int, r: int, d_out: int, d_in: int, device) -> AdapterPool:
                        torch.zeros(n, dtype=torch.float32, device=device))
 
 
-@dataclass
+@dataclass(frozen=True)
 class MultiPlan:
     """A batch's plan (``multi_plan``): good for every layer with n adapters in its pool."""
     buf: torch.Tensor
@@ -552,36 +561,38 @@ def multi_linear_bwd_workspace_bytes(d_out: int, d_in: int, d_seq: int, r: int, 
     return lib().qlora_multi_bwd_workspace_bytes(d_out, d_in, d_seq, r, n)
 
 
-def _multi_check(q: NF4Weight, pool: AdapterPool, plan: MultiPlan, d_seq: int) -> None:
-    dev = q.device
-    n, r = pool.n, pool.r
-    _need(pool.A, torch.bfloat16, (n, r, q.d_in), "pool.A", dev)
-    _need(pool.B, torch.bfloat16, (n, q.d_out, r), "pool.B", dev)
-    _need(pool.s, torch.float32, (n,), "pool.s", dev)
-    if (plan.d_seq, plan.n) != (d_seq, n) or plan.buf.device != dev:
+def _multi_check(q: NF4Weight, pool: AdapterPool, plan: MultiPlan, d_seq: int, dev) -> None:
+    if pool.d_in != q.d_in or pool.d_out != q.d_out or pool.device != dev:
+        raise ValueError(f"the pool is for a {pool.d_out} x {pool.d_in} layer on {pool.device}, "
+                         f"not {q.d_out} x {q.d_in} on {dev}")
+    if plan.d_seq != d_seq or plan.n != pool.n or plan.buf.device != dev:
         raise ValueError(f"the plan is for {plan.d_seq} tokens and {plan.n} adapters on {plan.buf.device}, "
-                         f"not {d_seq} and {n} on {dev}")
+                         f"not {d_seq} and {pool.n} on {dev}")
 
 
 def multi_linear_fwd(q: NF4Weight, pool: AdapterPool, plan: MultiPlan, X: torch.Tensor,
                      out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """qlora_multi_fwd: Y[t] = W_hat x_t + s_a B_a (A_a x_t), a the adapter of token t in the
     plan. X [d_seq, d_in] and out [d_seq, d_out] may be row views of wider arrays."""
-    dev = q.device
-    if X.dim() != 2 or X.shape[1] != q.d_in:
-        raise ValueError(f"input must be [d_seq, {q.d_in}]")
+    dev = q.codes.device
+    d_out, d_in = q.d_out, q.d_in
+    if X.dim() != 2 or X.shape[1] != d_in:
+        raise ValueError(f"input must be [d_seq, {d_in}]")
     d_seq = X.shape[0]
-    _multi_check(q, pool, plan, d_seq)
-    ldx = _rows(X, torch.bfloat16, (d_seq, q.d_in), "input", dev)
-    o = out if out is not None else torch.empty(d_seq, q.d_out, dtype=torch.bfloat16, device=dev)
-    ldy = _rows(o, torch.bfloat16, (d_seq, q.d_out), "out", dev)
+    _multi_check(q, pool, plan, d_seq, dev)
+    ldx = _rows(X, torch.bfloat16, X.shape, "input", dev)
+    if out is None:
+        o, ldy = X.new_empty((d_seq, d_out)), d_out
+    else:
+        o, ldy = out, _rows(out, torch.bfloat16, (d_seq, d_out), "out", dev)
     ws = workspace if workspace is not None else torch.empty(
-        max(multi_linear_fwd_workspace_bytes(q.d_out, q.d_in, d_seq, pool.r, pool.n), 1), dtype=torch.uint8, device=dev)
-    rc = lib().qlora_multi_fwd(_ptr(q.codes), _ptr(q.qconst), _ptr(q.qscale), _ptr(q.qmean), q.d_out, q.d_in,
-                               _dq_code(q.dq), _ptr(pool.A), _ptr(pool.B), _ptr(pool.s), pool.n, pool.r, _ptr(X), ldx,
-                               d_seq, _ptr(plan.buf), _ptr(o), ldy, _ptr(ws), ws.numel() * ws.element_size(),
-                               _stream(dev))
-    _check(rc, "qlora_multi_fwd")
+        max(multi_linear_fwd_workspace_bytes(d_out, d_in, d_seq, pool.r, pool.n), 1), dtype=torch.uint8, device=dev)
+    rc = lib().qlora_multi_fwd(q.codes.data_ptr(), q.qconst.data_ptr(), q.qscale.data_ptr(), q.qmean.data_ptr(), d_out,
+                               d_in, _dq_code(q.dq), pool.A.data_ptr(), pool.B.data_ptr(), pool.s.data_ptr(), pool.n,
+                               pool.r, X.data_ptr(), ldx, d_seq, plan.buf.data_ptr(), o.data_ptr(), ldy, ws.data_ptr(),
+                               ws.nbytes, _stream(dev))
+    if rc:
+        _check(rc, "qlora_multi_fwd")
     return o
 
 
@@ -590,26 +601,32 @@ def multi_linear_bwd(q: NF4Weight, pool: AdapterPool, plan: MultiPlan, X: torch.
                      workspace: torch.Tensor | None = None):
     """qlora_multi_bwd: (dX bfloat16 [d_seq, d_in], dA float32 [n, r, d_in], dB float32
     [n, d_out, r]) of ``multi_linear_fwd`` for the loss gradient dY."""
-    dev = q.device
+    dev = q.codes.device
+    d_out, d_in, n, r = q.d_out, q.d_in, pool.n, pool.r
     if X.dim() != 2 or dY.dim() != 2 or X.shape[0] != dY.shape[0]:
         raise ValueError("X [d_seq, d_in] and dY [d_seq, d_out] must share d_seq")
     d_seq = X.shape[0]
-    _multi_check(q, pool, plan, d_seq)
-    ldx = _rows(X, torch.bfloat16, (d_seq, q.d_in), "X", dev)
-    lddy = _rows(dY, torch.bfloat16, (d_seq, q.d_out), "dY", dev)
-    gx = dX if dX is not None else torch.empty(d_seq, q.d_in, dtype=torch.bfloat16, device=dev)
-    lddx = _rows(gx, torch.bfloat16, (d_seq, q.d_in), "dX", dev)
-    ga = dA if dA is not None else torch.empty(pool.A.shape, dtype=torch.float32, device=dev)
-    gb = dB if dB is not None else torch.empty(pool.B.shape, dtype=torch.float32, device=dev)
-    _need(ga, torch.float32, pool.A.shape, "dA", dev)
-    _need(gb, torch.float32, pool.B.shape, "dB", dev)
+    _multi_check(q, pool, plan, d_seq, dev)
+    ldx = _rows(X, torch.bfloat16, (d_seq, d_in), "X", dev)
+    lddy = _rows(dY, torch.bfloat16, (d_seq, d_out), "dY", dev)
+    if dX is None:
+        gx, lddx = X.new_empty((d_seq, d_in)), d_in
+    else:
+        gx, lddx = dX, _rows(dX, torch.bfloat16, (d_seq, d_in), "dX", dev)
+    ga = dA if dA is not None else torch.empty(n, r, d_in, dtype=torch.float32, device=dev)
+    gb = dB if dB is not None else torch.empty(n, d_out, r, dtype=torch.float32, device=dev)
+    if dA is not None:
+        _need(ga, torch.float32, (n, r, d_in), "dA", dev)
+    if dB is not None:
+        _need(gb, torch.float32, (n, d_out, r), "dB", dev)
     ws = workspace if workspace is not None else torch.empty(
-        max(multi_linear_bwd_workspace_bytes(q.d_out, q.d_in, d_seq, pool.r, pool.n), 1), dtype=torch.uint8, device=dev)
-    rc = lib().qlora_multi_bwd(_ptr(q.codes), _ptr(q.qconst), _ptr(q.qscale), _ptr(q.qmean), q.d_out, q.d_in,
-                               _dq_code(q.dq), _ptr(pool.A), _ptr(pool.B), _ptr(pool.s), pool.n, pool.r, _ptr(X), ldx,
-                               _ptr(dY), lddy, d_seq, _ptr(plan.buf), _ptr(gx), lddx, _ptr(ga), _ptr(gb), _ptr(ws),
-                               ws.numel() * ws.element_size(), _stream(dev))
-    _check(rc, "qlora_multi_bwd")
+        max(multi_linear_bwd_workspace_bytes(d_out, d_in, d_seq, r, n), 1), dtype=torch.uint8, device=dev)
+    rc = lib().qlora_multi_bwd(q.codes.data_ptr(), q.qconst.data_ptr(), q.qscale.data_ptr(), q.qmean.data_ptr(), d_out,
+                               d_in, _dq_code(q.dq), pool.A.data_ptr(), pool.B.data_ptr(), pool.s.data_ptr(), n, r,
+                               X.data_ptr(), ldx, dY.data_ptr(), lddy, d_seq, plan.buf.data_ptr(), gx.data_ptr(), lddx,
+                               ga.data_ptr(), gb.data_ptr(), ws.data_ptr(), ws.nbytes, _stream(dev))
+    if rc:
+        _check(rc, "qlora_multi_bwd")
     return gx, ga, gb
 
 

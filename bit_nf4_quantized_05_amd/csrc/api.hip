@@ -729,7 +729,7 @@ MultiWs multi_ws(int64_t d_out, int64_t d_in, int64_t M, int r, int n, bool bwd)
         w.bt = take(2 * static_cast<int64_t>(n) * r * d_out);
         w.grads = take(4 * qn::multi_grads_part_floats(d_out, d_in, M, n, r));      // dA, dB partials
     }
-    w.gpart = take(4 * (bwd ? qn::gemm_split_part_floats(M, d_in, d_out) : qn::gemm_split_part_floats(M, d_out, d_in)));
+    w.gpart = take(4 * (bwd ? qn::gemm_multi_part_floats(M, d_in, d_out) : qn::gemm_multi_part_floats(M, d_out, d_in)));
     w.bytes = off;
     return w;
 }

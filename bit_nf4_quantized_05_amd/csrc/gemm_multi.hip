@@ -19,8 +19,12 @@
 // meets its own adapter: zeros in place of the other rows would let an infinity or NaN in
 // one adapter's weights reach its neighbours' tokens, and this costs fewer MFMAs besides.
 //
-// With few tiles the K-steps are split as in the single-adapter GEMM (gemm_split), the rank
-// steps going to the last split; gemm_multi_reduce adds the partials.
+// The last round of tiles. With at most 64 tiles past a multiple of the 256 CUs their K-steps
+// are split as in the single-adapter GEMM (gemm_split), the rank steps going to the last
+// split; gemm_multi_reduce adds the partials. With 65 to 128 they are taken as twice as many
+// half tiles of 128 x 256, whole in K: a half tile's step takes about 0.6 of a whole one's
+// (as many MFMAs per wave again for two thirds of the LDS reads), and no partials are written
+// and read back.
 #include <hip/hip_runtime.h>
 
 #include "gemm_common.h"
@@ -49,31 +53,48 @@ struct MultiGemm {
     uint32_t bytesT, bytesR;                    // extents of T and of one adapter's R
 };
 
-template <bool kSplit>
-__device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg) {
+// LDS reads and MFMAs of a k16 sub-step in turn: one read, then PER MFMAs, N times
+#define QN_INTERLEAVE(N, PER)                                     \
+    _Pragma("unroll") for (int _i = 0; _i < (N); ++_i) {          \
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);        \
+        __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);      \
+    }
+
+// BMT rows per tile: 256, or 128 (the two halves of each of the last g.rem tiles)
+template <int BMT, bool kSplit>
+__device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
     const GemmArgs& g = mg.g;
-    constexpr int TM = BM / kWM / 32;           // 4 m sub-tiles per wave
+    constexpr bool kHalf = BMT < BM;
+    static_assert(!(kHalf && kSplit), "half tiles are whole in K");
+    constexpr int TM = BMT / kWM / 32;          // 4 (2) m sub-tiles per wave
     constexpr int TN = BN / kWN / 32;           // 2 n sub-tiles
-    constexpr int SEG = BM / (kWM * kWN) / 8;   // 4 8-row load segments per wave and operand
+    constexpr int SEGP = BMT / (kWM * kWN) / 8; // 4 (2) 8-row load segments of P per wave
+    constexpr int SEG = BN / (kWM * kWN) / 8;   // 4 of Q
+    constexpr int kPer = kHalf ? 1 : 2;         // MFMAs per LDS read
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / kWN, wn = wave % kWN;
     const int M = g.M, N = g.N;
 
-    const int bid = static_cast<int>(blockIdx.x);
     const bool split_wg = kSplit && bid >= g.full;
-    const int T = kSplit ? g.full : g.tiles_m * g.tiles_n;
+    const int T = kHalf ? 2 * g.rem : g.full;           // workgroups of this kind
     const int w = split_wg ? 0 : bid;
     const int sj = split_wg ? bid - g.full : 0;
     const int sk = split_wg ? sj / g.rem : 0;
-    const int logical = split_wg ? g.full + sj % g.rem : ((T % 8 == 0) ? (w & 7) * (T >> 3) + (w >> 3) : w);
+    const int place = (T % 8 == 0) ? (w & 7) * (T >> 3) + (w >> 3) : w;
+    const int logical = split_wg ? g.full + sj % g.rem : kHalf ? g.full + place / 2 : place;
     int tm, tn;
     tile_coords(g, logical, tm, tn);
-    const int m0 = tm * BM, n0 = tn * BN;
+    const int m0 = tm * BM + (kHalf ? (place & 1) * BMT : 0), n0 = tn * BN;
+    if (kHalf && m0 >= M) return;
 
     // this tile's adapters: used[k0 .. k1), `steps` rank steps in all (last split only)
-    const int2 kr = mg.plan.tile[tm];
+    int2 kr = mg.plan.tile[tm];
+    if constexpr (kHalf) {                      // the adapters of this half alone
+        while (kr.x < kr.y && mg.plan.start[mg.plan.used[kr.x] + 1] <= m0) ++kr.x;
+        while (kr.x < kr.y && mg.plan.start[mg.plan.used[kr.y - 1]] >= m0 + BMT) --kr.y;
+    }
     const int jsteps = (mg.r + BK - 1) / BK;
     const int steps = !split_wg || sk == g.splits - 1 ? (kr.y - kr.x) * jsteps : 0;
     int a_next = 0, lo_next = 0, hi_next = 0;   // adapter and positions of the step issued next
@@ -85,15 +106,18 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg) {
 
     const uint32_t kcE = static_cast<uint32_t>((lane & 7) ^ (lane >> 4)) * 16u;
     const uint32_t kcO = static_cast<uint32_t>((lane & 7) ^ (4 | (lane >> 4))) * 16u;
-    uint32_t voP[SEG], voQ[SEG];
+    uint32_t voP[SEGP], voQ[SEG];
+#pragma unroll
+    for (int j = 0; j < SEGP; ++j) {
+        const int rr = 8 * SEGP * wave + 8 * j + (lane >> 3);
+        const uint32_t rp = static_cast<uint32_t>(mg.plan.order[min(m0 + rr, M - 1)]);
+        voP[j] = rp * static_cast<uint32_t>(g.ldp * 2) + (((SEGP * wave + j) & 1) ? kcO : kcE);
+    }
 #pragma unroll
     for (int j = 0; j < SEG; ++j) {
         const int rr = 8 * SEG * wave + 8 * j + (lane >> 3);
-        const uint32_t kc16 = (((SEG * wave + j) & 1) ? kcO : kcE);
-        const uint32_t rp = static_cast<uint32_t>(mg.plan.order[min(m0 + rr, M - 1)]);
         const uint32_t rq = static_cast<uint32_t>(min(n0 + rr, N - 1));
-        voP[j] = rp * static_cast<uint32_t>(g.ldp * 2) + kc16;
-        voQ[j] = rq * static_cast<uint32_t>(g.ldq * 2) + kc16;
+        voQ[j] = rq * static_cast<uint32_t>(g.ldq * 2) + (((SEG * wave + j) & 1) ? kcO : kcE);
     }
     const __amdgpu_buffer_rsrc_t rsP = make_rsrc(g.P, g.bytesP);
     const __amdgpu_buffer_rsrc_t rsQ = make_rsrc(g.Q, g.bytesQ);
@@ -103,11 +127,12 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg) {
 
 #define QN_ISSUE(KTV, ST)                                                                         \
     {                                                                                             \
-        uint4* sp_ = (ST) + wave * (64 * SEG);                                                    \
-        uint4* sq_ = sp_ + kChunks;                                                               \
+        uint4* sp_ = (ST) + wave * (64 * SEGP);                                                   \
+        uint4* sq_ = (ST) + kChunks + wave * (64 * SEG);                                          \
         const int so_ = ((KTV) + kb) * (BK * 2);                                                  \
         _Pragma("unroll") for (int j = 0; j < SEG; ++j) {                                         \
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsP, (lds_ptr_t)(sp_ + 64 * j), 16, voP[j], so_, 0, 0); \
+            if (j < SEGP)                                                                         \
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsP, (lds_ptr_t)(sp_ + 64 * j), 16, voP[j < SEGP ? j : 0], so_, 0, 0); \
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsQ, (lds_ptr_t)(sq_ + 64 * j), 16, voQ[j], so_, 0, 0); \
         }                                                                                         \
     }
@@ -122,16 +147,21 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg) {
         const uint16_t* rb = mg.R + static_cast<int64_t>(a_next) * N * mg.r;
         const __amdgpu_buffer_rsrc_t rsT = make_rsrc(mg.T, mg.bytesT);
         const __amdgpu_buffer_rsrc_t rsR = make_rsrc(rb, mg.bytesR);
-        uint4* sp = st + wave * (64 * SEG);
-        uint4* sq = sp + kChunks;
+        uint4* sp = st + wave * (64 * SEGP);
+        uint4* sq = st + kChunks + wave * (64 * SEG);
         const int last = mg.r / 8 - 1 - j0 / 8;
+#pragma unroll
+        for (int j = 0; j < SEGP; ++j) {
+            const int rr = 8 * SEGP * wave + 8 * j + (ln >> 3);
+            const int c = min((ln & 7) ^ ((rr >> 1) & 7), last);
+            const uint32_t vp = (static_cast<uint32_t>(min(m0 + rr, M - 1)) * mg.r + 8 * c) * 2u;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsT, (lds_ptr_t)(sp + 64 * j), 16, vp, j0 * 2, 0, 0);
+        }
 #pragma unroll
         for (int j = 0; j < SEG; ++j) {
             const int rr = 8 * SEG * wave + 8 * j + (ln >> 3);
             const int c = min((ln & 7) ^ ((rr >> 1) & 7), last);
-            const uint32_t vp = (static_cast<uint32_t>(min(m0 + rr, M - 1)) * mg.r + 8 * c) * 2u;
             const uint32_t vq = (static_cast<uint32_t>(min(n0 + rr, N - 1)) * mg.r + 8 * c) * 2u;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsT, (lds_ptr_t)(sp + 64 * j), 16, vp, j0 * 2, 0, 0);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsR, (lds_ptr_t)(sq + 64 * j), 16, vq, j0 * 2, 0, 0);
         }
     };
@@ -167,19 +197,19 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg) {
         QN_FRAGS(CUR, chs[1], fb)                                              \
         __builtin_amdgcn_s_setprio(1);                                         \
         QN_MFMAS(fa)                                                           \
-        QN_INTERLEAVE_DS_MFMA((TM + TN));                                      \
+        QN_INTERLEAVE(TM + TN, kPer);                                         \
         QN_FRAGS(CUR, chs[2], fa)                                              \
         QN_MFMAS(fb)                                                           \
-        QN_INTERLEAVE_DS_MFMA((TM + TN));                                      \
+        QN_INTERLEAVE(TM + TN, kPer);                                         \
         QN_FRAGS(CUR, chs[3], fb)                                              \
         QN_MFMAS(fa)                                                           \
-        QN_INTERLEAVE_DS_MFMA((TM + TN));                                      \
+        QN_INTERLEAVE(TM + TN, kPer);                                         \
         __builtin_amdgcn_s_setprio(0);                                         \
         __builtin_amdgcn_s_waitcnt(0);                                         \
         QN_BARRIER();                                                          \
         NEXT_FRAGS                                                             \
         QN_MFMAS(fb)                                                           \
-        QN_INTERLEAVE_DS_MFMA((TM + TN));                                      \
+        QN_INTERLEAVE(TM + TN, kPer);                                         \
     }
 #define QN_MAIN(K, CUR, NXT) QN_STEP(QN_ISSUE((K) + 1, NXT), CUR, NXT, QN_FRAGS(NXT, chs[0], fa))
 #define QN_LAST(CUR, NXT) QN_STEP(if (steps > 0) issue_rank(0, NXT), CUR, NXT, )
@@ -300,7 +330,7 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg) {
     const int cj = tid & 31;
     constexpr int kRowsPerPass = kNT / 32;
 #pragma unroll 4
-    for (int i = 0; i < BM / kRowsPerPass; ++i) {
+    for (int i = 0; i < BMT / kRowsPerPass; ++i) {
         const int r = i * kRowsPerPass + (tid >> 5);
         const uint4* arr = (r >> 7) ? g_st1 : g_st0;
         const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(arr) + (r & 127) * 512 +
@@ -312,14 +342,24 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg) {
     }
 }
 
+// whole tiles
 __global__ __launch_bounds__(kNT, 1)
 void gemm_multi_kernel(MultiGemm mg) {
-    gemm_multi_body<false>(mg);
+    gemm_multi_body<BM, false>(mg, static_cast<int>(blockIdx.x));
 }
 
+// whole tiles, then the last ones split in K
 __global__ __launch_bounds__(kNT, 1)
 void gemm_multi_split(MultiGemm mg) {
-    gemm_multi_body<true>(mg);
+    gemm_multi_body<BM, true>(mg, static_cast<int>(blockIdx.x));
+}
+
+// whole tiles, then the last ones as half tiles
+__global__ __launch_bounds__(kNT, 1)
+void gemm_multi_half(MultiGemm mg) {
+    const int bid = static_cast<int>(blockIdx.x);
+    if (bid < mg.g.full) gemm_multi_body<BM, false>(mg, bid);
+    else gemm_multi_body<BM / 2, false>(mg, bid - mg.g.full);
 }
 
 // Split tiles: C[order[m], n..n+3] = bf16(sum of the tile's partials in split order)
@@ -348,6 +388,18 @@ void gemm_multi_reduce(MultiGemm mg) {
 
 }  // namespace
 
+namespace {
+// tiles past a multiple of 256 that are taken as half tiles
+int half_tiles(int64_t M, int64_t N) {
+    const int64_t rem = (M + BM - 1) / BM * ((N + BN - 1) / BN) % 256;
+    return rem > 64 && rem <= 128 ? static_cast<int>(rem) : 0;
+}
+}  // namespace
+
+int64_t gemm_multi_part_floats(int64_t M, int64_t N, int64_t K) {
+    return half_tiles(M, N) ? 0 : gemm_split_part_floats(M, N, K);
+}
+
 hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t K, const uint16_t* T,
                              const uint16_t* R, int r, const MultiPlan& plan, uint16_t* C, int64_t ldc, int64_t M,
                              int64_t N, float* part, hipStream_t st) {
@@ -362,14 +414,22 @@ hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, 
     mg.plan = plan; mg.T = T; mg.R = R; mg.r = r;
     mg.bytesT = static_cast<uint32_t>(2 * M * r);
     mg.bytesR = static_cast<uint32_t>(2 * N * r);
+    const int tiles = g.tiles_m * g.tiles_n;
+    g.part = part;
+    if (const int rem = half_tiles(M, N); rem > 0) {
+        g.full = tiles - rem;
+        g.rem = rem;
+        QN_LAUNCH("gemm_multi_half", st, gemm_multi_half, dim3(g.full + 2 * rem), dim3(kNT), 0, st, mg);
+        return hipGetLastError();
+    }
     const GemmSplit gs = gemm_split(M, N, K);
     g.splits = gs.splits;
     g.full = gs.full;
     g.rem = gs.rem;
     g.kper = (g.kt1 + g.splits - 1) / g.splits;
-    g.part = part;
     if (g.splits <= 1) {
-        QN_LAUNCH("gemm_multi_kernel", st, gemm_multi_kernel, dim3(g.tiles_m * g.tiles_n), dim3(kNT), 0, st, mg);
+        g.full = tiles;
+        QN_LAUNCH("gemm_multi_kernel", st, gemm_multi_kernel, dim3(tiles), dim3(kNT), 0, st, mg);
         return hipGetLastError();
     }
     QN_LAUNCH("gemm_multi_split", st, gemm_multi_split, dim3(g.full + g.rem * g.splits), dim3(kNT), 0, st, mg);

@@ -96,7 +96,8 @@ hipError_t launch_multi_reduce(const MultiPlan& plan, int64_t M, int r, int piec
 
 // ---- gemm_multi.hip ----
 // C[order[pos], :] = bf16( P[order[pos], K] Q[N, K]^T + T[pos, r] R_a[N, r]^T ), a the adapter
-// of the position (no second term without one); part as for gemm_nt.
+// of the position (no second term without one). part holds gemm_multi_part_floats floats.
+int64_t gemm_multi_part_floats(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t K, const uint16_t* T,
                              const uint16_t* R, int r, const MultiPlan& plan, uint16_t* C, int64_t ldc, int64_t M,
                              int64_t N, float* part, hipStream_t st);
