@@ -22,9 +22,16 @@
 // The last round of tiles. With at most 64 tiles past a multiple of the 256 CUs their K-steps
 // are split as in the single-adapter GEMM (gemm_split), the rank steps going to the last
 // split; gemm_multi_reduce adds the partials. With 65 to 128 they are taken as twice as many
-// half tiles of 128 x 256, whole in K: a half tile's step takes about 0.6 of a whole one's
-// (as many MFMAs per wave again for two thirds of the LDS reads), and no partials are written
-// and read back.
+// half tiles of 128 x 256, whole in K, which writes and reads back no partials: a half tile's
+// step takes 0.6 of a whole one's (4 LDS reads for 4 MFMAs, not 6 for 8), more than half, so
+// whole tiles stay the rule (4096 x 4096 at 4096 tokens: 119 us whole, 133 us in halves).
+// Alone they run on three stages of 48 KB, whose loads have two steps to arrive (1531 x 4096
+// x 4096, 96 tiles: 66 us; two stages 73; split in two 77 and 13 for the sums); after whole
+// tiles, in the same launch, on the two stages of those (11008 columns of 2048 tokens, 256 +
+// 88 tiles: 174 us; in two launches 124 + 58; split 170 + 12).
+// Dealing the last tiles' steps out evenly over all CUs, parts joined by the last workgroup
+// to finish, was slower than the split: 112 us for the 96 tiles (127 us with device-scope
+// fences in place of write-through stores), for 88 MB of partials.
 #include <hip/hip_runtime.h>
 
 #include "gemm_common.h"
@@ -40,6 +47,11 @@ namespace {
 
 __shared__ uint4 g_st0[2 * kChunks];
 __shared__ uint4 g_st1[2 * kChunks];
+// half tiles: three stages of [P 128 rows | Q 256 rows], distinct objects as above
+constexpr int kHalfStage = kChunks / 2 + kChunks;
+__shared__ uint4 g_h0[kHalfStage];
+__shared__ uint4 g_h1[kHalfStage];
+__shared__ uint4 g_h2[kHalfStage];
 
 constexpr int kWM = 2, kWN = 4;                 // waves
 constexpr int kNT = 64 * kWM * kWN;             // threads
@@ -60,17 +72,20 @@ struct MultiGemm {
         __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);      \
     }
 
-// BMT rows per tile: 256, or 128 (the two halves of each of the last g.rem tiles)
-template <int BMT, bool kSplit>
+// BMT rows per tile: 256, or 128 (the two halves of each of the last g.rem tiles); kThree: half
+// tiles on three LDS stages
+template <int BMT, bool kSplit, bool kThree>
 __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
     const GemmArgs& g = mg.g;
     constexpr bool kHalf = BMT < BM;
     static_assert(!(kHalf && kSplit), "half tiles are whole in K");
+    static_assert(kHalf || !kThree, "three stages hold half tiles only");
     constexpr int TM = BMT / kWM / 32;          // 4 (2) m sub-tiles per wave
     constexpr int TN = BN / kWN / 32;           // 2 n sub-tiles
     constexpr int SEGP = BMT / (kWM * kWN) / 8; // 4 (2) 8-row load segments of P per wave
     constexpr int SEG = BN / (kWM * kWN) / 8;   // 4 of Q
     constexpr int kPer = kHalf ? 1 : 2;         // MFMAs per LDS read
+    constexpr int kQ = kThree ? kChunks / 2 : kChunks;   // Q's place in a stage
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -128,7 +143,7 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
 #define QN_ISSUE(KTV, ST)                                                                         \
     {                                                                                             \
         uint4* sp_ = (ST) + wave * (64 * SEGP);                                                   \
-        uint4* sq_ = (ST) + kChunks + wave * (64 * SEG);                                          \
+        uint4* sq_ = (ST) + kQ + wave * (64 * SEG);                                          \
         const int so_ = ((KTV) + kb) * (BK * 2);                                                  \
         _Pragma("unroll") for (int j = 0; j < SEG; ++j) {                                         \
             if (j < SEGP)                                                                         \
@@ -148,7 +163,7 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
         const __amdgpu_buffer_rsrc_t rsT = make_rsrc(mg.T, mg.bytesT);
         const __amdgpu_buffer_rsrc_t rsR = make_rsrc(rb, mg.bytesR);
         uint4* sp = st + wave * (64 * SEGP);
-        uint4* sq = st + kChunks + wave * (64 * SEG);
+        uint4* sq = st + kQ + wave * (64 * SEG);
         const int last = mg.r / 8 - 1 - j0 / 8;
 #pragma unroll
         for (int j = 0; j < SEGP; ++j) {
@@ -169,7 +184,7 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
     const uint32_t frow = lane & 31;
     const uint32_t fsw = (frow >> 1) & 7;
     const uint32_t prow = (wm * (TM * 32) + frow) * 8;
-    const uint32_t qrow = kChunks + (wn * (TN * 32) + frow) * 8;
+    const uint32_t qrow = kQ + (wn * (TN * 32) + frow) * 8;
     uint32_t chs[4];
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) chs[kk] = (2 * kk + (lane >> 5)) ^ fsw;
@@ -214,6 +229,58 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
 #define QN_MAIN(K, CUR, NXT) QN_STEP(QN_ISSUE((K) + 1, NXT), CUR, NXT, QN_FRAGS(NXT, chs[0], fa))
 #define QN_LAST(CUR, NXT) QN_STEP(if (steps > 0) issue_rank(0, NXT), CUR, NXT, )
 
+    // the stage the first rank step is in: the last main step's successor
+    int stage = 0;
+    if constexpr (kThree) {
+        // Three stages: a step waits for its own stage only (the 6 loads of the next may be in
+        // flight), passes the barrier that certifies it for all waves and the stage of the step
+        // before as read, and sends the loads of the step after next into that one.
+#define QN_HALF(K, CUR, FREE, MORE)                                            \
+    {                                                                          \
+        if (MORE || (K) + 1 < KT) QN_WAIT_VM(SEGP + SEG); else QN_WAIT_VM(0);  \
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");        \
+        if (MORE || (K) + 2 < KT) QN_ISSUE((K) + 2, FREE)                      \
+        QN_FRAGS(CUR, chs[0], fa)                                              \
+        QN_FRAGS(CUR, chs[1], fb)                                              \
+        __builtin_amdgcn_s_setprio(1);                                         \
+        QN_MFMAS(fa)                                                           \
+        QN_FRAGS(CUR, chs[2], fa)                                              \
+        QN_INTERLEAVE(TM + TN, kPer)                                           \
+        QN_MFMAS(fb)                                                           \
+        QN_FRAGS(CUR, chs[3], fb)                                              \
+        QN_INTERLEAVE(TM + TN, kPer)                                           \
+        QN_MFMAS(fa)                                                           \
+        QN_MFMAS(fb)                                                           \
+        __builtin_amdgcn_s_setprio(0);                                         \
+    }
+        QN_ISSUE(0, g_h0)
+        if (KT > 1) QN_ISSUE(1, g_h1)
+        int k = 0;
+        // (no condition inside the loop: with one the compiler, not knowing how many loads are
+        // in flight, waited for nearly all of them; it still does once per turn, hence six
+        // steps to a turn)
+        for (; k + 8 <= KT; k += 6) {
+            QN_HALF(k, g_h0, g_h2, true)
+            QN_HALF(k + 1, g_h1, g_h0, true)
+            QN_HALF(k + 2, g_h2, g_h1, true)
+            QN_HALF(k + 3, g_h0, g_h2, true)
+            QN_HALF(k + 4, g_h1, g_h0, true)
+            QN_HALF(k + 5, g_h2, g_h1, true)
+        }
+        for (; k < KT; k += 3) {
+            QN_HALF(k, g_h0, g_h2, false)
+            if (k + 1 < KT) QN_HALF(k + 1, g_h1, g_h0, false)
+            if (k + 2 < KT) QN_HALF(k + 2, g_h2, g_h1, false)
+        }
+#undef QN_HALF
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (steps > 0) {
+            issue_rank(0, g_h0);
+            QN_WAIT_VM(0);
+            QN_BARRIER();
+        }
+    } else {
+    stage = KT & 1;
     QN_ISSUE(0, g_st0)
     QN_WAIT_VM(0);
     QN_BARRIER();
@@ -230,6 +297,7 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
         uint4* nxt = (KT & 1) ? g_st1 : g_st0;
         QN_LAST(cur, nxt)
     }
+    }
 #undef QN_LAST
 #undef QN_MAIN
 #undef QN_STEP
@@ -241,8 +309,10 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
     // (that step's wait and barrier). Each step: the next one's loads, this one's products,
     // then every wave's loads and LDS reads are waited for before the barrier.
     for (int s = 0; s < steps; ++s) {
-        const uint4* cur = ((KT + s) & 1) ? g_st1 : g_st0;
-        uint4* nxt = ((KT + s) & 1) ? g_st0 : g_st1;
+        uint4* const sa = kThree ? g_h0 : g_st0;
+        uint4* const sb = kThree ? g_h1 : g_st1;
+        const uint4* cur = ((stage + s) & 1) ? sb : sa;
+        uint4* nxt = ((stage + s) & 1) ? sa : sb;
         const int lo = lo_next, hi = hi_next;
         const int subs = min(BK, mg.r - (s % jsteps) * BK) / 16;
         if (s + 1 < steps) {
@@ -309,11 +379,12 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
     }
     // ---- epilogue: the bf16 tile through LDS (conflict-free, as the single-adapter GEMM),
     // then each row as 512 contiguous bytes to its token's row of C
+    constexpr int kRowsIn = (kThree ? 64 : 128) - 1;     // rows of the tile in one stage, less 1
 #pragma unroll
     for (int b = 0; b < TM; ++b) {
         const int rl = wm * (TM * 32) + b * 32 + static_cast<int>(frow);
-        uint4* arr = (rl >> 7) ? g_st1 : g_st0;
-        char* rowp = reinterpret_cast<char*>(arr) + (rl & 127) * 512;
+        uint4* arr = kThree ? ((rl >> 6) ? g_h1 : g_h0) : (rl >> 7) ? g_st1 : g_st0;
+        char* rowp = reinterpret_cast<char*>(arr) + (rl & kRowsIn) * 512;
 #pragma unroll
         for (int a = 0; a < TN; ++a) {
 #pragma unroll
@@ -332,8 +403,8 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
 #pragma unroll 4
     for (int i = 0; i < BMT / kRowsPerPass; ++i) {
         const int r = i * kRowsPerPass + (tid >> 5);
-        const uint4* arr = (r >> 7) ? g_st1 : g_st0;
-        const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(arr) + (r & 127) * 512 +
+        const uint4* arr = kThree ? ((r >> 6) ? g_h1 : g_h0) : (r >> 7) ? g_st1 : g_st0;
+        const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(arr) + (r & kRowsIn) * 512 +
                                                         ((cj ^ (r & 31)) << 4));
         const int m = m0 + r;
         const int n = n0 + cj * 8;
@@ -345,21 +416,27 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
 // whole tiles
 __global__ __launch_bounds__(kNT, 1)
 void gemm_multi_kernel(MultiGemm mg) {
-    gemm_multi_body<BM, false>(mg, static_cast<int>(blockIdx.x));
+    gemm_multi_body<BM, false, false>(mg, static_cast<int>(blockIdx.x));
 }
 
 // whole tiles, then the last ones split in K
 __global__ __launch_bounds__(kNT, 1)
 void gemm_multi_split(MultiGemm mg) {
-    gemm_multi_body<BM, true>(mg, static_cast<int>(blockIdx.x));
+    gemm_multi_body<BM, true, false>(mg, static_cast<int>(blockIdx.x));
 }
 
-// whole tiles, then the last ones as half tiles
+// whole tiles, then the last ones as half tiles on the same two stages
+__global__ __launch_bounds__(kNT, 1)
+void gemm_multi_mixed(MultiGemm mg) {
+    const int bid = static_cast<int>(blockIdx.x);
+    if (bid < mg.g.full) gemm_multi_body<BM, false, false>(mg, bid);
+    else gemm_multi_body<BM / 2, false, false>(mg, bid - mg.g.full);
+}
+
+// half tiles alone, on three stages
 __global__ __launch_bounds__(kNT, 1)
 void gemm_multi_half(MultiGemm mg) {
-    const int bid = static_cast<int>(blockIdx.x);
-    if (bid < mg.g.full) gemm_multi_body<BM, false>(mg, bid);
-    else gemm_multi_body<BM / 2, false>(mg, bid - mg.g.full);
+    gemm_multi_body<BM / 2, false, true>(mg, static_cast<int>(blockIdx.x));
 }
 
 // Split tiles: C[order[m], n..n+3] = bf16(sum of the tile's partials in split order)
@@ -419,7 +496,10 @@ hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, 
     if (const int rem = half_tiles(M, N); rem > 0) {
         g.full = tiles - rem;
         g.rem = rem;
-        QN_LAUNCH("gemm_multi_half", st, gemm_multi_half, dim3(g.full + 2 * rem), dim3(kNT), 0, st, mg);
+        if (g.full > 0)
+            QN_LAUNCH("gemm_multi_mixed", st, gemm_multi_mixed, dim3(g.full + 2 * rem), dim3(kNT), 0, st, mg);
+        else
+            QN_LAUNCH("gemm_multi_half", st, gemm_multi_half, dim3(2 * rem), dim3(kNT), 0, st, mg);
         return hipGetLastError();
     }
     const GemmSplit gs = gemm_split(M, N, K);
