@@ -702,7 +702,7 @@ int qlora_lora_grads(const uint16_t* A, const uint16_t* B, int r, float s, const
 namespace {
 
 struct MultiWs {
-    int64_t what, at, bt, pre0, pre1, t, u, gpart, grads, part, part_t, bytes;
+    int64_t what, pre0, pre1, t, u, gpart, grads, part, part_t, bytes;
     int splits0, splits1;
 };
 
@@ -725,8 +725,6 @@ MultiWs multi_ws(int64_t d_out, int64_t d_in, int64_t M, int r, int n, bool bwd)
     if (bwd) {
         w.pre1 = take(4 * static_cast<int64_t>(w.splits1) * M * r);                 // B^T dy, K-split
         w.u = take(2 * 3 * M * r);                                                  // U = s B^T dy
-        w.at = take(2 * static_cast<int64_t>(n) * r * d_in);                        // A^T, B^T of the adapters in use
-        w.bt = take(2 * static_cast<int64_t>(n) * r * d_out);
         w.grads = take(4 * qn::multi_grads_part_floats(d_out, d_in, M, n, r));      // dA, dB partials
     }
     w.gpart = take(4 * (bwd ? qn::gemm_multi_part_floats(M, d_in, d_out) : qn::gemm_multi_part_floats(M, d_out, d_in)));
@@ -827,7 +825,7 @@ int qlora_multi_fwd(const uint8_t* codes, const int8_t* qconst, const float* qsc
     if ((e = qn::launch_multi_reduce(pl, d_seq, r, 1, f32(mw.pre0), mw.splits0, u16(mw.t), nullptr, 0, nullptr, st)) !=
         hipSuccess)
         return hip_fail(e, "qlora_multi_fwd (A x)");
-    if ((e = qn::launch_gemm_multi(X, ldx, u16(mw.what), d_in, u16(mw.t), B, r, pl, Y, ldy, d_seq, d_out, f32(mw.gpart),
+    if ((e = qn::launch_gemm_multi(X, ldx, u16(mw.what), d_in, u16(mw.t), B, false, r, pl, Y, ldy, d_seq, d_out, f32(mw.gpart),
                                    st)) != hipSuccess)
         return hip_fail(e, "qlora_multi_fwd (gemm)");
     return 0;
@@ -851,18 +849,14 @@ int qlora_multi_bwd(const uint8_t* codes, const int8_t* qconst, const float* qsc
     auto u16 = [&](int64_t off) { return reinterpret_cast<uint16_t*>(ws + off); };
     const qn::MultiPlan pl = qn::multi_plan_at(plan, d_seq, n);
     hipError_t e;
-    // K-contiguous copies for the products: B^T [r, d_out] (B^T dy) and A^T [d_in, r] (dX)
-    if ((e = qn::launch_multi_transpose(pl, std::min<int64_t>(n, d_seq), A, r, d_in, u16(mw.at), B, d_out, r, u16(mw.bt),
-                                        st)) != hipSuccess)
-        return hip_fail(e, "qlora_multi_bwd (A^T, B^T)");
     if ((e = qn::launch_multi_prologue(codes, bc, d_out, d_in, true, u16(mw.what), pl, s, d_seq, n, r,
                                        qn::MultiPre{X, ldx, d_in, A, f32(mw.pre0)},
-                                       qn::MultiPre{dY, lddy, d_out, u16(mw.bt), f32(mw.pre1)}, st)) != hipSuccess)
+                                       qn::MultiPre{dY, lddy, d_out, B, f32(mw.pre1)}, st)) != hipSuccess)
         return hip_fail(e, "qlora_multi_bwd (prologue)");
     if ((e = qn::launch_multi_reduce(pl, d_seq, r, 3, f32(mw.pre0), mw.splits0, u16(mw.t), f32(mw.pre1), mw.splits1,
                                      u16(mw.u), st)) != hipSuccess)
         return hip_fail(e, "qlora_multi_bwd (A x, B^T dy)");
-    if ((e = qn::launch_gemm_multi(dY, lddy, u16(mw.what), d_out, u16(mw.u), u16(mw.at), r, pl, dX, lddx, d_seq, d_in,
+    if ((e = qn::launch_gemm_multi(dY, lddy, u16(mw.what), d_out, u16(mw.u), A, true, r, pl, dX, lddx, d_seq, d_in,
                                    f32(mw.gpart), st)) != hipSuccess)
         return hip_fail(e, "qlora_multi_bwd (gemm)");
     if ((e = qn::launch_multi_grads(pl, X, ldx, dY, lddy, u16(mw.t), u16(mw.u), d_out, d_in, d_seq, n, r, f32(mw.grads),

@@ -3,6 +3,8 @@
 // for the positions p of a batch sorted by adapter, a the adapter of position p:
 //     forward : P = X,  Q = W_hat,    T = s_a A_a x,    R_a = B_a
 //     dX      : P = dY, Q = W_hat^T,  T = s_a B_a^T dy, R_a = A_a^T
+// (A_a itself is read, rank-major: its rows go to LDS as they are and transposing reads hand
+// out the fragments).
 //
 // The main K-steps are those of the single-adapter GEMM (256 x 256 tiles, 8 waves of
 // 128 x 64, K-steps of 64 double-buffered in LDS by direct loads, swizzled rows; the
@@ -38,6 +40,7 @@
 #include "internal.h"
 #include "mfma_device.h"
 #include "multi.h"
+#include "multi_device.h"
 #include "nf4_device.h"
 
 #include <algorithm>
@@ -60,7 +63,7 @@ struct MultiGemm {
     GemmArgs g;                                 // P, Q, C, sizes, splits
     MultiPlan plan;
     const uint16_t* T;                          // [M, r]
-    const uint16_t* R;                          // [adapters, N, r]
+    const uint16_t* R;                          // [adapters, N, r], or [adapters, r, N]
     int r;
     uint32_t bytesT, bytesR;                    // extents of T and of one adapter's R
 };
@@ -74,7 +77,7 @@ struct MultiGemm {
 
 // BMT rows per tile: 256, or 128 (the two halves of each of the last g.rem tiles); kThree: half
 // tiles on three LDS stages
-template <int BMT, bool kSplit, bool kThree>
+template <int BMT, bool kSplit, bool kThree, bool kRankMajor>
 __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
     const GemmArgs& g = mg.g;
     constexpr bool kHalf = BMT < BM;
@@ -174,10 +177,18 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
         }
 #pragma unroll
         for (int j = 0; j < SEG; ++j) {
-            const int rr = 8 * SEG * wave + 8 * j + (ln >> 3);
-            const int c = min((ln & 7) ^ ((rr >> 1) & 7), last);
-            const uint32_t vq = (static_cast<uint32_t>(min(n0 + rr, N - 1)) * mg.r + 8 * c) * 2u;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsR, (lds_ptr_t)(sq + 64 * j), 16, vq, j0 * 2, 0, 0);
+            if constexpr (kRankMajor) {
+                // 2 rank rows of 256 columns a segment, 16-byte piece c of rank k at c ^ 2 (k % 4)
+                const int k = 2 * (SEG * wave + j) + (ln >> 5);
+                const int n = min(n0 + 8 * ((ln & 31) ^ (2 * (k & 3))), N - 8);
+                const uint32_t vq = (static_cast<uint32_t>(min(j0 + k, mg.r - 1)) * N + n) * 2u;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsR, (lds_ptr_t)(sq + 64 * j), 16, vq, 0, 0, 0);
+            } else {
+                const int rr = 8 * SEG * wave + 8 * j + (ln >> 3);
+                const int c = min((ln & 7) ^ ((rr >> 1) & 7), last);
+                const uint32_t vq = (static_cast<uint32_t>(min(n0 + rr, N - 1)) * mg.r + 8 * c) * 2u;
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsR, (lds_ptr_t)(sq + 64 * j), 16, vq, j0 * 2, 0, 0);
+            }
         }
     };
 
@@ -328,7 +339,17 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
         for (int kk = 0; kk < 4; ++kk)
             if (kk < subs) {
 #pragma unroll
-                for (int a = 0; a < TN; ++a) q[a][kk] = cur[qrow + a * 256 + chs[kk]];
+                for (int a = 0; a < TN; ++a) {
+                    if constexpr (kRankMajor) {
+                        const int k = 8 * (lane >> 5) + ((lane >> 2) & 3);       // + 16 kk, the same k % 4
+                        const int n = wn * (TN * 32) + a * 32 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+                        const char* q0 = reinterpret_cast<const char*>(cur + kQ) + k * 512 +
+                                         ((((n >> 3) ^ (2 * (k & 3))) << 4) | ((n & 7) << 1));
+                        q[a][kk] = lds_tr8(q0 + kk * (16 * 512), 4 * 512);
+                    } else {
+                        q[a][kk] = cur[qrow + a * 256 + chs[kk]];
+                    }
+                }
             }
 #pragma unroll
         for (int b = 0; b < TM; ++b) {
@@ -413,31 +434,29 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
     }
 }
 
-// whole tiles
-__global__ __launch_bounds__(kNT, 1)
-void gemm_multi_kernel(MultiGemm mg) {
-    gemm_multi_body<BM, false, false>(mg, static_cast<int>(blockIdx.x));
-}
-
-// whole tiles, then the last ones split in K
-__global__ __launch_bounds__(kNT, 1)
-void gemm_multi_split(MultiGemm mg) {
-    gemm_multi_body<BM, true, false>(mg, static_cast<int>(blockIdx.x));
-}
-
-// whole tiles, then the last ones as half tiles on the same two stages
-__global__ __launch_bounds__(kNT, 1)
-void gemm_multi_mixed(MultiGemm mg) {
-    const int bid = static_cast<int>(blockIdx.x);
-    if (bid < mg.g.full) gemm_multi_body<BM, false, false>(mg, bid);
-    else gemm_multi_body<BM / 2, false, false>(mg, bid - mg.g.full);
-}
-
-// half tiles alone, on three stages
-__global__ __launch_bounds__(kNT, 1)
-void gemm_multi_half(MultiGemm mg) {
-    gemm_multi_body<BM / 2, false, true>(mg, static_cast<int>(blockIdx.x));
-}
+// The kernels, for R as rows (forward) and rank-major (input gradient):
+//   kernel  whole tiles
+//   split   whole tiles, then the last ones split in K
+//   mixed   whole tiles, then the last ones as half tiles on the same two stages
+//   half    half tiles alone, on three stages
+#define QN_MULTI_KERNELS(SUFFIX, RANK_MAJOR)                                                          \
+    __global__ __launch_bounds__(kNT, 1) void gemm_multi_kernel##SUFFIX(MultiGemm mg) {                \
+        gemm_multi_body<BM, false, false, RANK_MAJOR>(mg, static_cast<int>(blockIdx.x));               \
+    }                                                                                                 \
+    __global__ __launch_bounds__(kNT, 1) void gemm_multi_split##SUFFIX(MultiGemm mg) {                 \
+        gemm_multi_body<BM, true, false, RANK_MAJOR>(mg, static_cast<int>(blockIdx.x));                \
+    }                                                                                                 \
+    __global__ __launch_bounds__(kNT, 1) void gemm_multi_mixed##SUFFIX(MultiGemm mg) {                 \
+        const int bid = static_cast<int>(blockIdx.x);                                                 \
+        if (bid < mg.g.full) gemm_multi_body<BM, false, false, RANK_MAJOR>(mg, bid);                   \
+        else gemm_multi_body<BM / 2, false, false, RANK_MAJOR>(mg, bid - mg.g.full);                   \
+    }                                                                                                 \
+    __global__ __launch_bounds__(kNT, 1) void gemm_multi_half##SUFFIX(MultiGemm mg) {                  \
+        gemm_multi_body<BM / 2, false, true, RANK_MAJOR>(mg, static_cast<int>(blockIdx.x));            \
+    }
+QN_MULTI_KERNELS(, false)
+QN_MULTI_KERNELS(_dx, true)
+#undef QN_MULTI_KERNELS
 
 // Split tiles: C[order[m], n..n+3] = bf16(sum of the tile's partials in split order)
 template <int SP>
@@ -478,7 +497,7 @@ int64_t gemm_multi_part_floats(int64_t M, int64_t N, int64_t K) {
 }
 
 hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t K, const uint16_t* T,
-                             const uint16_t* R, int r, const MultiPlan& plan, uint16_t* C, int64_t ldc, int64_t M,
+                             const uint16_t* R, bool rank_major, int r, const MultiPlan& plan, uint16_t* C, int64_t ldc, int64_t M,
                              int64_t N, float* part, hipStream_t st) {
     MultiGemm mg{};
     GemmArgs& g = mg.g;
@@ -493,13 +512,16 @@ hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, 
     mg.bytesR = static_cast<uint32_t>(2 * N * r);
     const int tiles = g.tiles_m * g.tiles_n;
     g.part = part;
+#define QN_GEMM(KERNEL, GRID)                                                                          \
+    do {                                                                                               \
+        if (rank_major) QN_LAUNCH(#KERNEL "_dx", st, KERNEL##_dx, dim3(GRID), dim3(kNT), 0, st, mg);     \
+        else QN_LAUNCH(#KERNEL, st, KERNEL, dim3(GRID), dim3(kNT), 0, st, mg);                          \
+    } while (0)
     if (const int rem = half_tiles(M, N); rem > 0) {
         g.full = tiles - rem;
         g.rem = rem;
-        if (g.full > 0)
-            QN_LAUNCH("gemm_multi_mixed", st, gemm_multi_mixed, dim3(g.full + 2 * rem), dim3(kNT), 0, st, mg);
-        else
-            QN_LAUNCH("gemm_multi_half", st, gemm_multi_half, dim3(2 * rem), dim3(kNT), 0, st, mg);
+        if (g.full > 0) QN_GEMM(gemm_multi_mixed, g.full + 2 * rem);
+        else QN_GEMM(gemm_multi_half, 2 * rem);
         return hipGetLastError();
     }
     const GemmSplit gs = gemm_split(M, N, K);
@@ -509,10 +531,11 @@ hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, 
     g.kper = (g.kt1 + g.splits - 1) / g.splits;
     if (g.splits <= 1) {
         g.full = tiles;
-        QN_LAUNCH("gemm_multi_kernel", st, gemm_multi_kernel, dim3(tiles), dim3(kNT), 0, st, mg);
+        QN_GEMM(gemm_multi_kernel, tiles);
         return hipGetLastError();
     }
-    QN_LAUNCH("gemm_multi_split", st, gemm_multi_split, dim3(g.full + g.rem * g.splits), dim3(kNT), 0, st, mg);
+    QN_GEMM(gemm_multi_split, g.full + g.rem * g.splits);
+#undef QN_GEMM
     const dim3 rgrid(static_cast<unsigned>(g.rem * 64));
     if (g.splits == 2) QN_LAUNCH("gemm_multi_reduce", st, gemm_multi_reduce<2>, rgrid, dim3(256), 0, st, mg);
     else if (g.splits == 3) QN_LAUNCH("gemm_multi_reduce", st, gemm_multi_reduce<3>, rgrid, dim3(256), 0, st, mg);

@@ -55,7 +55,11 @@ constexpr int kMultiMaxAdapters = 1024;
 constexpr int kMultiItem = 128;             // positions per work item at most
 constexpr int kMultiTile = 256;             // positions per GEMM tile
 
-struct MultiItem { int32_t adapter, pos, count, index; };   // index: of the item within its adapter
+// A run of at most 128 positions of one adapter: the first, how many are left from there to
+// the adapter's last, and the item's number within its adapter. adapter -1: no item (the list
+// is filled up with these, so that a kernel needs no count before it reads its item).
+struct MultiItem { int32_t adapter, pos, left, index; };
+__host__ __device__ inline int item_count(const MultiItem& it) { return it.left < kMultiItem ? it.left : kMultiItem; }
 struct MultiPlan {
     const int32_t* head;                    // [0] adapters in use, [1] items, [2] positions with an adapter
     const int32_t* order;                   // [M] token at each position
@@ -82,7 +86,7 @@ struct MultiPool {
 // ---- prologue.hip ----
 // Pre-passes of the multi-adapter calls, one launch: for every item and K-slice the fp32
 // partial s_a P[order[pos], kslice] R_a[r, kslice]^T into part[slice][pos][r]; R is [n, r, K]
-// row-major. Up to two products (R1 null: one), and the double dequantisation of the weight
+// row-major for the first product, [n, K, r] for the second (none if its R is null), and the double dequantisation of the weight
 // to what (transposed or not; null: none).
 struct MultiPre { const uint16_t* P; int64_t ldp; int64_t K; const uint16_t* R; float* part; };
 hipError_t launch_multi_prologue(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
@@ -95,11 +99,12 @@ hipError_t launch_multi_reduce(const MultiPlan& plan, int64_t M, int r, int piec
                                uint16_t* T0, const float* part1, int splits1, uint16_t* T1, hipStream_t st);
 
 // ---- gemm_multi.hip ----
-// C[order[pos], :] = bf16( P[order[pos], K] Q[N, K]^T + T[pos, r] R_a[N, r]^T ), a the adapter
+// C[order[pos], :] = bf16( P[order[pos], K] Q[N, K]^T + T[pos, r] R_a[N, r]^T ), R [n, N, r] or,
+// with rank_major, R_a^T given as [n, r, N]; a the adapter
 // of the position (no second term without one). part holds gemm_multi_part_floats floats.
 int64_t gemm_multi_part_floats(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t K, const uint16_t* T,
-                             const uint16_t* R, int r, const MultiPlan& plan, uint16_t* C, int64_t ldc, int64_t M,
+                             const uint16_t* R, bool rank_major, int r, const MultiPlan& plan, uint16_t* C, int64_t ldc, int64_t M,
                              int64_t N, float* part, hipStream_t st);
 
 // ---- skinny.hip, multi_small.hip ----
@@ -116,10 +121,6 @@ hipError_t launch_multi_small(const uint8_t* codes, const BlockConsts& bc, int64
                               hipStream_t st);
 
 // ---- multi_grads.hip ----
-// dst[a] [cols, rows] = src[a] [rows, cols]^T for the adapters in use (rows and cols multiples of 16)
-hipError_t launch_multi_transpose(const MultiPlan& plan, int64_t max_used, const uint16_t* src0, int64_t rows0,
-                                  int64_t cols0, uint16_t* dst0, const uint16_t* src1, int64_t rows1, int64_t cols1,
-                                  uint16_t* dst1, hipStream_t st);
 // dB[a] [d_out, r] = sum over a's positions of dY^T T, dA[a] [r, d_in] of U^T X (zeros for an
 // adapter without tokens); T, U [3][M][r]. part holds multi_grads_part_floats floats.
 int64_t multi_grads_part_floats(int64_t d_out, int64_t d_in, int64_t M, int n, int r);

@@ -1,5 +1,4 @@
-// Gradients of many adapters' factors in one batch on gfx950, and the transposed copies of
-// the factors that the backward's products read.
+// Gradients of many adapters' factors in one batch on gfx950.
 //
 // For the tokens t of adapter a (learn.ifs.name deck card 1: only the adapters are trained;
 // the derivatives of Y = W_hat x + s_a B_a A_a x):
@@ -9,14 +8,16 @@
 // outputs are float32, and with one bf16 term they would carry its 2^-9 for the sake of a
 // product that the reads of dY and X bound in any case.
 //
-// multi_grad_mfma: as the single-adapter kernel, a workgroup takes 128 columns of P = dY or
-// X (32 per wave), 64 (or 32) ranks and a slice of one adapter's positions; per step of 32
-// positions the gathered rows of P and the rows of the three terms go straight into LDS
-// (two stages), and ds_read_b64_tr_b16 hands each lane 4 consecutive rows of a column, the
-// MFMA's K order. A slice is `per` items (128 positions each) of the plan. An adapter whose
-// tokens fit one slice is written to dA, dB at once; the others leave one partial per
-// slice, added in slice order by multi_grad_reduce, which also writes the zeros of adapters
-// without tokens. Deterministic; rows of other adapters are never read.
+// multi_grad_mfma: as for one adapter, a workgroup takes 128 columns of P = dY or X (32 per
+// wave), 64 (or 32) ranks and a slice of one adapter's positions; per step of 32 positions the
+// gathered rows of P and the rows of the three terms go straight into LDS (two stages), and
+// transposing reads hand each lane 4 consecutive rows of a column, the MFMA's K order. A slice is `per` items (128 positions each)
+// of the plan. An adapter whose tokens fit one slice is written to dA, dB at once; the others
+// leave one partial per slice, added in slice order by multi_grad_reduce, which also writes
+// the zeros of adapters without tokens. Deterministic; rows of other adapters count nowhere.
+// Slice s of adapter a has slot first_item[a] / per + a + s: a's ceil(items / per) slots end
+// before the next adapter's begin, and there are at most items / per + n of them.
+// Bound by the reads of dY and X and, with many slices, of the partials.
 #include <hip/hip_runtime.h>
 
 #include "internal.h"
@@ -50,82 +51,106 @@ struct GradArgs {
     int M, r, jchunks, max_items, per;
 };
 
+// 16-byte piece c of row m sits at c ^ swz(m), so that the 4 rows of a transposing read fall in
+// different banks (rows of 64 bytes do without)
 __device__ __forceinline__ int swz(int m) { return 2 * (m & 3); }
 
+template <int JB>
 struct GradTile {
-    uint4 P[kGK * 16];               // 32 rows x 16 chunks of 8 columns
-    uint4 T[kTerms][kGK * 8];        // 32 rows x 8 chunks of 8 ranks
+    uint4 P[kGK * 16];               // 32 rows x 16 pieces of 8 columns
+    uint4 T[kTerms][kGK * 4 * JB];   // 32 rows x 4 JB pieces of 8 ranks
 };
 
-#define QN_TR(d, a, off) "ds_read_b64_tr_b16 %" #d ", %" #a " offset:" #off "\n\t"
+// Transposing reads, each asm block ending with its own wait. (The builtin form would have
+// the compiler wait for every load in flight, the next stage's too, before each read.) A
+// lane's reads are its rows +0, +4, +16 and +20: two 16-row MFMA steps.
+#define QN_TR(d, a, off) "ds_read_b64_tr_b16 %" #d ", %" #a " offset:%" #off "\n\t"
+#define QN_TR4(d0, d1, d2, d3, a, o0, o1, o2, o3) QN_TR(d0, a, o0) QN_TR(d1, a, o1) QN_TR(d2, a, o2) QN_TR(d3, a, o3)
+typedef unsigned long long u64;
 
-// 4 transposing reads of one operand (rows +0, +4, +16, +20 of the lane's block), waited for
-template <int kRow>      // bytes per row
-__device__ __forceinline__ void tr_read(uint32_t addr, unsigned long long (&v)[4]) {
-    static_assert(kRow == 256 || kRow == 128, "row pitch");
-    if constexpr (kRow == 256) {
-        asm volatile(QN_TR(0, 4, 0) QN_TR(1, 4, 1024) QN_TR(2, 4, 4096) QN_TR(3, 4, 5120) "s_waitcnt lgkmcnt(0)"
-                     : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]) : "v"(addr) : "memory");
+__device__ __forceinline__ uint4 fragment(u64 a, u64 b) {
+    return uint4{static_cast<uint32_t>(a), static_cast<uint32_t>(a >> 32), static_cast<uint32_t>(b),
+                 static_cast<uint32_t>(b >> 32)};
+}
+
+// rows past `valid` as zeros (they belong to other adapters); first row of the lane's 8 is mb
+__device__ __forceinline__ uint4 masked(const uint4& f, int mb, int valid) {
+    uint32_t w[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] &= (mb + 2 * i < valid ? 0xFFFFu : 0u) | (mb + 2 * i + 1 < valid ? 0xFFFF0000u : 0u);
+    return uint4{w[0], w[1], w[2], w[3]};
+}
+
+// the 4 reads of term kP at each of the JB rank blocks' addresses
+template <int JB, int kP>
+__device__ __forceinline__ void read_term(const uint32_t (&ta)[JB], u64 (&b)[JB][4]) {
+    constexpr int kRow = 64 * JB, kOff = kP * kGK * kRow;
+    if constexpr (JB == 1) {
+        asm volatile(QN_TR4(0, 1, 2, 3, 4, 5, 6, 7, 8) "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(b[0][0]), "=&v"(b[0][1]), "=&v"(b[0][2]), "=&v"(b[0][3])
+                     : "v"(ta[0]), "n"(kOff), "n"(kOff + 4 * kRow), "n"(kOff + 16 * kRow), "n"(kOff + 20 * kRow)
+                     : "memory");
     } else {
-        asm volatile(QN_TR(0, 4, 0) QN_TR(1, 4, 512) QN_TR(2, 4, 2048) QN_TR(3, 4, 2560) "s_waitcnt lgkmcnt(0)"
-                     : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]) : "v"(addr) : "memory");
+        asm volatile(QN_TR4(0, 1, 2, 3, 8, 10, 11, 12, 13) QN_TR4(4, 5, 6, 7, 9, 10, 11, 12, 13) "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(b[0][0]), "=&v"(b[0][1]), "=&v"(b[0][2]), "=&v"(b[0][3]), "=&v"(b[1][0]), "=&v"(b[1][1]),
+                       "=&v"(b[1][2]), "=&v"(b[1][3])
+                     : "v"(ta[0]), "v"(ta[1]), "n"(kOff), "n"(kOff + 4 * kRow), "n"(kOff + 16 * kRow),
+                       "n"(kOff + 20 * kRow)
+                     : "memory");
     }
 }
-#undef QN_TR
 
 template <int JB>
-__device__ __forceinline__ void grad_compute(const GradTile& t, int wave, int lane, int valid, f32x16 (&acc)[JB]) {
-    const int g4 = lane >> 4, r = (lane >> 2) & 3, bq = lane & 3;
-    const int m = 8 * (g4 >> 1) + r;
-    const int n = 32 * wave + 16 * (g4 & 1) + 4 * bq;
-    const uint32_t pa = lds_addr(t.P) + 2 * (m * 128 + ((((n >> 3) ^ swz(m)) << 3) | (n & 7)));
-    unsigned long long a[4];
-    tr_read<256>(pa, a);
-    uint4 A[2];
+__device__ __forceinline__ void grad_compute(const GradTile<JB>& t, int wave, int lane, int valid, f32x16 (&acc)[JB]) {
+    const int g4 = lane >> 4;
+    const int m = 8 * (g4 >> 1) + ((lane >> 2) & 3);
+    const int col = 16 * (g4 & 1) + 4 * (lane & 3);                    // of a 32-wide block
+    const int n = 32 * wave + col;
+    const uint32_t pa = lds_addr(t.P) + m * 256 + ((((n >> 3) ^ swz(m)) << 4) | ((n & 7) << 1));
+    uint32_t ta[JB];
 #pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-        const int mb = 16 * sub + 8 * (g4 >> 1);                       // first position of this lane's 8
-        uint32_t aw[4] = {static_cast<uint32_t>(a[2 * sub]), static_cast<uint32_t>(a[2 * sub] >> 32),
-                          static_cast<uint32_t>(a[2 * sub + 1]), static_cast<uint32_t>(a[2 * sub + 1] >> 32)};
-        if (valid < kGK) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t keep = (mb + 2 * i < valid ? 0xFFFFu : 0u) | (mb + 2 * i + 1 < valid ? 0xFFFF0000u : 0u);
-                aw[i] &= keep;
-            }
-        }
-        A[sub] = uint4{aw[0], aw[1], aw[2], aw[3]};
+    for (int jb = 0; jb < JB; ++jb) {
+        const int j = 32 * jb + col;
+        ta[jb] = lds_addr(t.T) + m * (64 * JB) + ((((j >> 3) ^ (JB == 2 ? swz(m) : 0)) << 4) | ((j & 7) << 1));
     }
+    u64 a[4];
+    asm volatile(QN_TR4(0, 1, 2, 3, 4, 5, 6, 7, 8) "s_waitcnt lgkmcnt(0)"
+                 : "=&v"(a[0]), "=&v"(a[1]), "=&v"(a[2]), "=&v"(a[3])
+                 : "v"(pa), "n"(0), "n"(4 * 256), "n"(16 * 256), "n"(20 * 256)
+                 : "memory");
+    const int mb = 8 * (lane >> 5);
+    uint4 A[2] = {fragment(a[0], a[1]), fragment(a[2], a[3])};
+    if (valid < kGK) {
+        A[0] = masked(A[0], mb, valid);
+        A[1] = masked(A[1], mb + 16, valid);
+    }
+    auto add = [&](const u64 (&b)[JB][4]) {
 #pragma unroll
-    for (int p = 0; p < kTerms; ++p) {
-#pragma unroll
-        for (int jb = 0; jb < JB; ++jb) {
-            const int j = 32 * jb + 16 * (g4 & 1) + 4 * bq;
-            unsigned long long b[4];
-            tr_read<128>(lds_addr(t.T[p]) + 2 * (m * 64 + ((((j >> 3) ^ swz(m)) << 3) | (j & 7))), b);
+        for (int jb = 0; jb < JB; ++jb)
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
-                uint32_t bw[4] = {static_cast<uint32_t>(b[2 * sub]), static_cast<uint32_t>(b[2 * sub] >> 32),
-                                  static_cast<uint32_t>(b[2 * sub + 1]), static_cast<uint32_t>(b[2 * sub + 1] >> 32)};
-                if (valid < kGK) {          // rows past the slice belong to others: their terms must not count either
-                    const int mb = 16 * sub + 8 * (g4 >> 1);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t keep = (mb + 2 * i < valid ? 0xFFFFu : 0u) |
-                                              (mb + 2 * i + 1 < valid ? 0xFFFF0000u : 0u);
-                        bw[i] &= keep;
-                    }
-                }
-                acc[jb] = mfma32(A[sub], uint4{bw[0], bw[1], bw[2], bw[3]}, acc[jb]);
+                uint4 B = fragment(b[jb][2 * sub], b[jb][2 * sub + 1]);
+                if (valid < kGK) B = masked(B, mb + 16 * sub, valid);
+                acc[jb] = mfma32(A[sub], B, acc[jb]);
             }
-        }
-    }
+    };
+    u64 b[JB][4];
+    read_term<JB, 0>(ta, b);
+    add(b);
+    read_term<JB, 1>(ta, b);
+    add(b);
+    read_term<JB, 2>(ta, b);
+    add(b);
+    static_assert(kTerms == 3, "three terms");
 }
+#undef QN_TR4
+#undef QN_TR
 
 template <int JB>   // 32-wide rank blocks per workgroup: 1 (r <= 32) or 2
 __global__ __launch_bounds__(256)
 void multi_grad_mfma(GradArgs g) {
-    __shared__ GradTile s0, s1;
+    __shared__ GradTile<JB> s0, s1;
     __shared__ int s_order[kMaxPer * kMultiItem];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -138,12 +163,10 @@ void multi_grad_mfma(GradArgs g) {
     b /= jb.tiles;
     const int item = b % g.max_items;
     const int j0 = (b / g.max_items) * kGJ;
-    if (item >= g.plan.head[1]) return;
     const MultiItem it = g.plan.items[item];
-    if (it.index % g.per != 0) return;
-    const int end = g.plan.start[it.adapter + 1];
-    const int m_lo = it.pos, m_hi = min(m_lo + g.per * kMultiItem, end);
-    const bool alone = it.index == 0 && m_hi == end;                   // the adapter's only slice
+    if (it.adapter < 0 || it.index % g.per != 0) return;
+    const int m_lo = it.pos, m_hi = m_lo + min(g.per * kMultiItem, it.left);
+    const bool alone = it.index == 0 && m_hi == m_lo + it.left;        // the adapter's only slice
     const int64_t n0 = static_cast<int64_t>(tile) * kGCols;
     const int steps = (m_hi - m_lo + kGK - 1) / kGK;
     const int64_t mr = static_cast<int64_t>(g.M) * g.r;
@@ -155,8 +178,11 @@ void multi_grad_mfma(GradArgs g) {
     // the slice's tokens, so that a step's loads wait for no index from memory
     for (int i = threadIdx.x; i < m_hi - m_lo; i += 256) s_order[i] = g.plan.order[m_lo + i];
     __syncthreads();
-    // rows 4 (2 w + q) + lane / 16 of P, row 8 w + lane / 8 of each term
-    auto issue = [&](GradTile& t, int m) {
+    // P: rows 4 (2 w + q) + lane / 16. T: JB = 2, row 8 w + lane / 8 of each term; JB = 1, the 6
+    // half terms (16 rows each) dealt to the waves, the last two to two waves each (the same
+    // bytes), so that every wave has as many loads in flight
+    constexpr int kTLoads = JB == 2 ? kTerms : 2;
+    auto issue = [&](GradTile<JB>& t, int m) {
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             const int row = 4 * (2 * wave + q) + (lane >> 4);
@@ -164,26 +190,40 @@ void multi_grad_mfma(GradArgs g) {
             const int64_t ng = min(n0 + 8 * ((lane & 15) ^ swz(row)), jb.N - 8);
             load_lds16(jb.P + tok * jb.ldp + ng, &t.P[(2 * wave + q) * 64]);
         }
-        const int row = 8 * wave + (lane >> 3);
-        const int64_t at = static_cast<int64_t>(min(m + row, m_hi - 1)) * g.r + min(j0 + 8 * ((lane & 7) ^ swz(row)), g.r - 8);
+        if constexpr (JB == 2) {
+            const int row = 8 * wave + (lane >> 3);
+            const int64_t at = static_cast<int64_t>(min(m + row, m_hi - 1)) * g.r +
+                               min(j0 + 8 * ((lane & 7) ^ swz(row)), g.r - 8);
 #pragma unroll
-        for (int p = 0; p < kTerms; ++p) load_lds16(jb.T + p * mr + at, &t.T[p][wave * 64]);
+            for (int p = 0; p < kTerms; ++p) load_lds16(jb.T + p * mr + at, &t.T[p][wave * 64]);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int half = h == 0 ? wave : 4 + (wave & 1);       // half term
+                const int p = half >> 1, row = 16 * (half & 1) + (lane >> 2);
+                const int64_t at = static_cast<int64_t>(min(m + row, m_hi - 1)) * g.r + min(8 * (lane & 3), g.r - 8);
+                load_lds16(jb.T + p * mr + at, &t.T[p][(half & 1) * 64]);
+            }
+        }
     };
 #define QN_GRAD_BARRIER() asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory")
+    constexpr int kLoads = 2 + kTLoads;
+    auto compute = [&](const GradTile<JB>& t, int s) {
+        grad_compute<JB>(t, wave, lane, min(kGK, m_hi - (m_lo + s * kGK)), acc);
+    };
+#define QN_GRAD(S, CUR, NXT)                                                                   \
+    if ((S) + 1 < steps) { issue(NXT, m_lo + ((S) + 1) * kGK); QN_WAIT_VM(kLoads); }           \
+    else QN_WAIT_VM(0);                                                                        \
+    QN_GRAD_BARRIER();                                                                         \
+    compute(CUR, S);                                                                           \
+    QN_GRAD_BARRIER();
     issue(s0, m_lo);
     for (int s = 0; s < steps; s += 2) {
-        if (s + 1 < steps) { issue(s1, m_lo + (s + 1) * kGK); QN_WAIT_VM(2 + kTerms); }
-        else QN_WAIT_VM(0);
-        QN_GRAD_BARRIER();
-        grad_compute<JB>(s0, wave, lane, min(kGK, m_hi - (m_lo + s * kGK)), acc);
-        QN_GRAD_BARRIER();
+        QN_GRAD(s, s0, s1)
         if (s + 1 >= steps) break;
-        if (s + 2 < steps) { issue(s0, m_lo + (s + 2) * kGK); QN_WAIT_VM(2 + kTerms); }
-        else QN_WAIT_VM(0);
-        QN_GRAD_BARRIER();
-        grad_compute<JB>(s1, wave, lane, min(kGK, m_hi - (m_lo + (s + 1) * kGK)), acc);
-        QN_GRAD_BARRIER();
+        QN_GRAD(s + 1, s1, s0)
     }
+#undef QN_GRAD
 #undef QN_GRAD_BARRIER
     // D of a 32 x 32 tile: lane l holds rows 8 (v / 4) + 4 (l / 32) + v % 4 of column l % 32
     const int64_t Nr = jb.N * g.r;
@@ -197,11 +237,14 @@ void multi_grad_mfma(GradArgs g) {
         for (int v = 0; v < 16; v += 4) {
             const int64_t n = n0 + 32 * wave + 8 * (v >> 2) + 4 * (lane >> 5);
             if (n >= jb.N) continue;                                   // N % 64 == 0: 4 columns in or out together
+            const float4 o = float4{acc[k][v], acc[k][v + 1], acc[k][v + 2], acc[k][v + 3]};
             if (alone && jb.rows) {
-                *reinterpret_cast<float4*>(dst + j * jb.N + n) = float4{acc[k][v], acc[k][v + 1], acc[k][v + 2], acc[k][v + 3]};
+                *reinterpret_cast<float4*>(dst + j * jb.N + n) = o;
             } else {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) dst[(n + e) * g.r + j] = acc[k][v + e];
+                dst[n * g.r + j] = o.x;
+                dst[(n + 1) * g.r + j] = o.y;
+                dst[(n + 2) * g.r + j] = o.z;
+                dst[(n + 3) * g.r + j] = o.w;
             }
         }
     }
@@ -245,50 +288,12 @@ void multi_grad_reduce(GradArgs g, int blocks0) {
     }
 }
 
-// dst[a] [cols, rows] = src[a] [rows, cols]^T in 64 x 64 tiles through LDS; adapter
-// used[blockIdx.y]. rows and cols are multiples of 16.
-struct TransposeJob { const uint16_t* src; uint16_t* dst; int rows, cols, tiles; };
-
-__global__ __launch_bounds__(256)
-void multi_transpose(TransposeJob j0, TransposeJob j1, const int32_t* __restrict__ head, const int32_t* __restrict__ used) {
-    __shared__ uint16_t t[64 * 66];
-    if (static_cast<int>(blockIdx.y) >= head[0]) return;
-    const bool second = static_cast<int>(blockIdx.x) >= j0.tiles;
-    const TransposeJob& j = second ? j1 : j0;
-    const int b = static_cast<int>(blockIdx.x) - (second ? j0.tiles : 0);
-    const int64_t base = static_cast<int64_t>(used[blockIdx.y]) * j.rows * j.cols;
-    const int ct = (j.cols + 63) / 64;
-    const int r0 = b / ct * 64, c0 = b % ct * 64;
-    const int tid = threadIdx.x;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int row = (tid >> 3) + 32 * q, c = 8 * (tid & 7);
-        if (r0 + row < j.rows && c0 + c < j.cols) {
-            const uint4 v = *reinterpret_cast<const uint4*>(j.src + base + static_cast<int64_t>(r0 + row) * j.cols + c0 + c);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) *reinterpret_cast<uint32_t*>(&t[row * 66 + c + 2 * e]) = w[e];
-        }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        const int col = (tid >> 3) + 32 * q, r = 8 * (tid & 7);
-        if (c0 + col < j.cols && r0 + r < j.rows) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                w[e] = t[(r + 2 * e) * 66 + col] | (static_cast<uint32_t>(t[(r + 2 * e + 1) * 66 + col]) << 16);
-            *reinterpret_cast<uint4*>(j.dst + base + static_cast<int64_t>(c0 + col) * j.rows + r0 + r) =
-                uint4{w[0], w[1], w[2], w[3]};
-        }
-    }
-}
-
 int jchunks_of(int r) { return (r + kGJ - 1) / kGJ; }
 
-// Items per slice: about 512 workgroups over both gradients if the tokens were evenly
-// spread, at most 1024 positions a slice.
+// Items per slice: about 512 workgroups over both gradients if the tokens were evenly spread,
+// at most 1024 positions a slice. (256 of twice the length: 31 against 23 us on 4096 x 4096,
+// 4096 tokens, r = 16, and 39 against 34 us on 11008 + 4096 columns, 2048 tokens, r = 64, whose
+// partials then take 8 instead of 12 us; 1024 of half of it: 26 us for the partials there.)
 int per_of(int64_t d_out, int64_t d_in, int64_t M, int r) {
     const int64_t tiles = ((d_out + kGCols - 1) / kGCols + (d_in + kGCols - 1) / kGCols) * jchunks_of(r);
     const int64_t items = (M + kMultiItem - 1) / kMultiItem;
@@ -296,20 +301,6 @@ int per_of(int64_t d_out, int64_t d_in, int64_t M, int r) {
 }
 
 }  // namespace
-
-hipError_t launch_multi_transpose(const MultiPlan& plan, int64_t max_used, const uint16_t* src0, int64_t rows0,
-                                  int64_t cols0, uint16_t* dst0, const uint16_t* src1, int64_t rows1, int64_t cols1,
-                                  uint16_t* dst1, hipStream_t st) {
-    auto job = [](const uint16_t* s, int64_t rows, int64_t cols, uint16_t* d) {
-        return TransposeJob{s, d, static_cast<int>(rows), static_cast<int>(cols),
-                            static_cast<int>(((rows + 63) / 64) * ((cols + 63) / 64))};
-    };
-    const TransposeJob j0 = job(src0, rows0, cols0, dst0), j1 = job(src1, rows1, cols1, dst1);
-    QN_LAUNCH("multi_transpose", st, multi_transpose,
-              dim3(static_cast<unsigned>(j0.tiles + j1.tiles), static_cast<unsigned>(max_used)), dim3(256), 0, st, j0, j1,
-              plan.head, plan.used);
-    return hipGetLastError();
-}
 
 namespace {
 int64_t slots_of(int64_t d_out, int64_t d_in, int64_t M, int n, int r) {

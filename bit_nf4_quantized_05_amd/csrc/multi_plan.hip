@@ -58,7 +58,7 @@ __device__ __forceinline__ unsigned long long same_key(int key, bool valid) {
 }
 
 __global__ __launch_bounds__(kPlanThreads)
-void multi_plan_kernel(const int32_t* __restrict__ ids, int M, int n, PlanOut out) {
+void multi_plan_kernel(const int32_t* __restrict__ ids, int M, int n, int max_items, PlanOut out) {
     __shared__ int hist[kPlanWaves * kKeys];
     __shared__ int ends[kMultiMaxAdapters];            // end position of each adapter in use
     __shared__ int tmp[kPlanWaves];
@@ -101,9 +101,10 @@ void multi_plan_kernel(const int32_t* __restrict__ ids, int M, int n, PlanOut ou
             out.used[at_used] = tid;
             ends[at_used] = first + count;
             for (int k = 0; k * kMultiItem < count; ++k)
-                out.items[at_item + k] = MultiItem{tid, first + k * kMultiItem, min(kMultiItem, count - k * kMultiItem), k};
+                out.items[at_item + k] = MultiItem{tid, first + k * kMultiItem, count - k * kMultiItem, k};
         }
     }
+    for (int i = n_items + tid; i < max_items; i += kPlanThreads) out.items[i] = MultiItem{-1, 0, 0, 0};
     if (tid == 0) {
         out.start[n] = total;
         int p = total;
@@ -184,7 +185,7 @@ hipError_t launch_multi_plan(const int32_t* ids, int64_t M, int n, void* buf, hi
     const PlanOut out{w, w + o.order, w + o.start, w + o.first_item, w + o.used,
                       reinterpret_cast<int2*>(w + o.tile), reinterpret_cast<MultiItem*>(w + o.items)};
     QN_LAUNCH("multi_plan_kernel", st, multi_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, ids,
-              static_cast<int>(M), n, out);
+              static_cast<int>(M), n, static_cast<int>(multi_max_items(M, n)), out);
     return hipGetLastError();
 }
 

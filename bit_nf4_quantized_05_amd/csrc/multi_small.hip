@@ -102,20 +102,21 @@ void multi_reduce_small(SmallArgs a) {
             const int k = k0 + kWaves * n;
             if (k >= items) break;                       // wave-uniform
             const MultiItem it = a.plan.items[k];
+            const int count = item_count(it);
 #pragma unroll
             for (int t = 0; t < TT; ++t) {
-                if (16 * t >= it.count) break;
+                if (16 * t >= count) break;
                 const int row = 16 * t + i;
                 f32x4 acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int c = 0; c < RC; ++c) {
                     const uint4 tv = *reinterpret_cast<const uint4*>(
-                        &s_t[(it.pos + min(row, it.count - 1)) * kPitch + 32 * c + 8 * g]);
+                        &s_t[(it.pos + min(row, count - 1)) * kPitch + 32 * c + 8 * g]);
                     acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, bw[n][c]),
                                                                   __builtin_bit_cast(bf16x8, tv), acc, 0, 0, 0);
                 }
                 // D of a 16 x 16 tile: lane l holds rows 4 (l / 16) .. + 3 of token l % 16
-                if (row < it.count) {
+                if (row < count) {
 #pragma unroll
                     for (int v = 0; v < 4; ++v) s_y[it.pos + row][4 * g + v] = acc[v];
                 }

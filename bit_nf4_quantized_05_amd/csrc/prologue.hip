@@ -1,8 +1,9 @@
 // Prologue of a QLoRA linear call on gfx950: the LoRA pre-pass (rank-r product of
 // the activations with A or B^T; up to two such products per launch), the adapter
 // layouts and the double dequantisation of the NF4 weight to bf16 W_hat or W_hat^T,
-// in one launch; the same for tokens of many adapters (multi_prologue_kernel); the reduction of K-split pre-pass partials; and the small transpose
-// of B that the input gradient uses when the pre-pass cannot read B itself.
+// in one launch; the same for tokens of many adapters (multi_prologue_kernel); the
+// reduction of K-split pre-pass partials; and the small transpose of B that the input
+// gradient uses when the pre-pass cannot read B itself.
 #include <hip/hip_runtime.h>
 
 #include "internal.h"
@@ -442,7 +443,7 @@ void prologue_kernel(PrologueArgs a, NF4Tables tab) {
 // ---------------------------------------------------------------------------
 struct MultiPreJob {
     const uint16_t* P; int64_t ldp; int K;
-    const uint16_t* R;               // [n, r, K]
+    const uint16_t* R;               // [n, r, K] (job 0) or [n, K, r] (job 1)
     float* part;                     // [psplits][M][r]
     int psplits, kper, n;            // K-slices, 64-wide K-chunks per slice, workgroups
 };
@@ -454,13 +455,18 @@ struct MultiPrologueArgs {
     int max_items;
 };
 
-template <int NT>
+// kMajor: R is [K, r] per adapter (B_a of the backward), fetched as 64 k-rows of 32 NT ranks
+// (pieces past r repeat the last one, their ranks are not stored) and gathered into fragments
+// by transposing reads; a row's 16-byte pieces are XORed with 2 (k % 4) where the pitch would
+// put the 4 rows of a read in the same banks (NT even). No transposed copy of B is made.
+template <int NT, bool kMajor>
 __device__ __forceinline__ void multi_pre_job(const MultiPreJob& j, const MultiPrologueArgs& a, int b,
                                               PreStage<NT>& s0, PreStage<NT>& s1) {
     constexpr int kLoads = 4 + NT;
     const int item = b % a.max_items, sp = b / a.max_items;
-    if (item >= a.plan.head[1]) return;
     const MultiItem it = a.plan.items[item];
+    if (it.adapter < 0) return;
+    const int count = item_count(it);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = a.d.r;
@@ -471,19 +477,61 @@ __device__ __forceinline__ void multi_pre_job(const MultiPreJob& j, const MultiP
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const int row = 32 * wave + 8 * u + (lane >> 3);
-        const int64_t tok = a.plan.order[it.pos + min(row, it.count - 1)];
+        const int64_t tok = a.plan.order[it.pos + min(row, count - 1)];
         prow[u] = j.P + tok * j.ldp + 8 * ((lane & 7) ^ ((row >> 1) & 7));
     }
+    const int64_t rstep = kMajor ? static_cast<int64_t>(64) * r : 64;          // R's elements per K-chunk
+    const auto swz = [](int k) { return NT % 2 == 0 ? 2 * (k & 3) : 0; };
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        const int row = 8 * (4 * i + wave) + (lane >> 3);
-        rrow[i] = j.R + (static_cast<int64_t>(it.adapter) * r + min(row, r - 1)) * j.K + 8 * ((lane & 7) ^ ((row >> 1) & 7));
+        if constexpr (kMajor) {
+            const int q = 64 * (4 * i + wave) + lane;
+            const int k = q / (4 * NT), c = (q % (4 * NT)) ^ swz(k);
+            rrow[i] = j.R + (static_cast<int64_t>(it.adapter) * j.K + k) * r + min(8 * c, r - 8);
+        } else {
+            const int row = 8 * (4 * i + wave) + (lane >> 3);
+            rrow[i] = j.R + (static_cast<int64_t>(it.adapter) * r + min(row, r - 1)) * j.K + 8 * ((lane & 7) ^ ((row >> 1) & 7));
+        }
     }
     auto issue = [&](PreStage<NT>& st, int kc) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) load_lds16(prow[u] + static_cast<int64_t>(kc) * 64, &st.x[(32 * wave + 8 * u) * 8]);
 #pragma unroll
-        for (int i = 0; i < NT; ++i) load_lds16(rrow[i] + static_cast<int64_t>(kc) * 64, &st.r[8 * (4 * i + wave) * 8]);
+        for (int i = 0; i < NT; ++i) load_lds16(rrow[i] + kc * rstep, &st.r[8 * (4 * i + wave) * 8]);
+    };
+    auto compute = [&](const PreStage<NT>& st, f32x16 (&acc)[NT]) {
+        if constexpr (!kMajor) {
+            pre_compute<NT, false>(st, wave, lane, acc);
+        } else {
+            constexpr int kPitch = 64 * NT;            // bytes per k-row
+            const int g4 = lane >> 4, fr = lane & 31;
+            const int k = 8 * (g4 >> 1) + ((lane >> 2) & 3);
+            const uint32_t rbase = lds_addr(st.r) + k * kPitch + 8 * (lane & 1);
+            uint4 xf[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) xf[u] = st.x[(32 * wave + fr) * 8 + ((2 * u + (lane >> 5)) ^ ((fr >> 1) & 7))];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                // rows k = 16 u + .. + 4 h (h = 0, 1) of the four k16 steps u, one asm block with its own wait
+                const uint32_t at = rbase + 16 * ((4 * t + 2 * (g4 & 1) + ((lane >> 1) & 1)) ^ swz(k));
+                unsigned long long v[8];
+                asm volatile("ds_read_b64_tr_b16 %0, %8 offset:%9\n\tds_read_b64_tr_b16 %1, %8 offset:%10\n\t"
+                             "ds_read_b64_tr_b16 %2, %8 offset:%11\n\tds_read_b64_tr_b16 %3, %8 offset:%12\n\t"
+                             "ds_read_b64_tr_b16 %4, %8 offset:%13\n\tds_read_b64_tr_b16 %5, %8 offset:%14\n\t"
+                             "ds_read_b64_tr_b16 %6, %8 offset:%15\n\tds_read_b64_tr_b16 %7, %8 offset:%16\n\t"
+                             "s_waitcnt lgkmcnt(0)"
+                             : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]),
+                               "=&v"(v[6]), "=&v"(v[7])
+                             : "v"(at), "n"(0), "n"(4 * kPitch), "n"(16 * kPitch), "n"(20 * kPitch), "n"(32 * kPitch),
+                               "n"(36 * kPitch), "n"(48 * kPitch), "n"(52 * kPitch)
+                             : "memory");
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    acc[t] = mfma32(uint4{static_cast<uint32_t>(v[2 * u]), static_cast<uint32_t>(v[2 * u] >> 32),
+                                          static_cast<uint32_t>(v[2 * u + 1]), static_cast<uint32_t>(v[2 * u + 1] >> 32)},
+                                    xf[u], acc[t]);
+            }
+        }
     };
     f32x16 acc[NT];
 #pragma unroll
@@ -493,17 +541,17 @@ __device__ __forceinline__ void multi_pre_job(const MultiPreJob& j, const MultiP
         if (kc + 1 < ke) { issue(s1, kc + 1); QN_WAIT_VM(kLoads); }
         else QN_WAIT_VM(0);
         QN_PRE_BARRIER();
-        pre_compute<NT, false>(s0, wave, lane, acc);
+        compute(s0, acc);
         QN_PRE_BARRIER();
         if (kc + 1 >= ke) break;
         if (kc + 2 < ke) { issue(s0, kc + 2); QN_WAIT_VM(kLoads); }
         else QN_WAIT_VM(0);
         QN_PRE_BARRIER();
-        pre_compute<NT, false>(s1, wave, lane, acc);
+        compute(s1, acc);
         QN_PRE_BARRIER();
     }
     const int row = 32 * wave + (lane & 31);
-    if (row >= it.count) return;
+    if (row >= count) return;
     const float s = a.s[it.adapter];
     float* out = j.part + (static_cast<int64_t>(sp) * a.d.M + it.pos + row) * r;
 #pragma unroll
@@ -552,12 +600,12 @@ void multi_prologue_kernel(MultiPrologueArgs a, NF4Tables tab) {
     __shared__ PreStage<NT> s0, s1;
     int b = blockIdx.x;
     if (b < a.pre[0].n) {
-        multi_pre_job<NT>(a.pre[0], a, b, s0, s1);
+        multi_pre_job<NT, false>(a.pre[0], a, b, s0, s1);
         return;
     }
     b -= a.pre[0].n;
     if (b < a.pre[1].n) {
-        multi_pre_job<NT>(a.pre[1], a, b, s0, s1);
+        multi_pre_job<NT, true>(a.pre[1], a, b, s0, s1);
         return;
     }
     dequant_jobs(a.d, b - a.pre[1].n, tab, reinterpret_cast<char*>(s1.x));

@@ -87,8 +87,9 @@ __device__ __forceinline__ void multi_ax_job(const MultiAx& m, const SkArgs& a, 
     b /= m.max_items;
     const int sp = b % m.splits;
     const int j0 = b / m.splits * 16;
-    if (item >= m.plan.head[1]) return;
     const MultiItem it = m.plan.items[item];
+    if (it.adapter < 0) return;
+    const int count = item_count(it);
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int i = lane & 15, g = lane >> 4;
@@ -97,7 +98,7 @@ __device__ __forceinline__ void multi_ax_job(const MultiAx& m, const SkArgs& a, 
     const uint16_t* xrow[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
-        const int64_t tok = m.plan.order[it.pos + min(16 * t + i, it.count - 1)];
+        const int64_t tok = m.plan.order[it.pos + min(16 * t + i, count - 1)];
         xrow[t] = a.X + tok * a.ldx + 16 * g;
     }
     f32x4 acc[TT];
@@ -117,7 +118,7 @@ __device__ __forceinline__ void multi_ax_job(const MultiAx& m, const SkArgs& a, 
         }
 #pragma unroll
         for (int t = 0; t < TT; ++t)
-            if (16 * t < it.count) {
+            if (16 * t < count) {
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -128,7 +129,7 @@ __device__ __forceinline__ void multi_ax_job(const MultiAx& m, const SkArgs& a, 
             if (k + u * NW < b1) {
 #pragma unroll
                 for (int t = 0; t < TT; ++t)
-                    if (16 * t < it.count) {
+                    if (16 * t < count) {
 #pragma unroll
                         for (int h = 0; h < 2; ++h) acc[t] = mfma16(av[u][h], xv[t][u][h], acc[t]);
                     }
@@ -144,7 +145,7 @@ __device__ __forceinline__ void multi_ax_job(const MultiAx& m, const SkArgs& a, 
 #pragma unroll
     for (int t = 0; t < TT; ++t) {
         const int row = 16 * t + i;
-        if (row >= it.count) continue;
+        if (row >= count) continue;
         f32x4 v = acc[t];
 #pragma unroll
         for (int q = 0; q < NW - 1; ++q) v = v + red[(q * TT + t) * 64 + lane];

@@ -115,8 +115,9 @@ def test_plan(M, n, kind):
     rows = []
     for a in act:
         assert first[a] == len(rows)
-        rows += [(a, start[a] + k, min(128, counts[a] - k), k // 128) for k in range(0, counts[a], 128)]
+        rows += [(a, start[a] + k, counts[a] - k, k // 128) for k in range(0, counts[a], 128)]
     assert head[1] == len(rows) and np.array_equal(items[:len(rows)].reshape(-1, 4), np.array(rows, int).reshape(-1, 4))
+    assert np.all(items[len(rows):] == [-1, 0, 0, 0])
     for t in range((M + 255) // 256):
         have = [a for k, a in enumerate(act) if start[a] < min(256 * t + 256, head[2]) and start[a + 1] > 256 * t]
         k0, k1 = tile[2 * t], tile[2 * t + 1]
@@ -134,7 +135,9 @@ SMALL = [(64, 64, 1, 16, 1, "one"), (256, 320, 1, 16, 4, "none"), (512, 4096, 3,
 LARGE = [(256, 256, 65, 16, 3, "mixed"), (320, 192, 300, 32, 5, "packed"), (512, 4096, 200, 48, 40, "mixed"),
          (1024, 1536, 1531, 16, 7, "packed"), (256, 512, 1024, 64, 4, "packed"), (64, 64, 257, 256, 2, "mixed"),
          (192, 128, 513, 80, 64, "outside"), (256, 320, 700, 112, 1, "one"), (256, 256, 600, 16, 9, "none"),
-         (128, 192, 2000, 16, 1000, "mixed"), (2048, 2048, 2100, 16, 3, "packed")]
+         (128, 192, 2000, 16, 1000, "mixed"), (2048, 2048, 2100, 16, 3, "packed"),
+         # 96 tiles (halves alone), 336 (whole ones and halves), 257 (whole ones and one split)
+         (4096, 128, 1531, 32, 30, "packed"), (4096, 64, 5200, 16, 5, "packed"), (4096, 1024, 4097, 16, 6, "mixed")]
 
 
 @pytest.mark.parametrize("d_out,d_in,M,r,n,kind", SMALL + LARGE)
@@ -252,7 +255,8 @@ def test_ranks_padded_by_the_pool():
 BWD = [(64, 64, 1, 16, 2, "one"), (256, 256, 203, 16, 3, "packed"), (320, 192, 40, 48, 6, "mixed"),
        (192, 320, 700, 32, 2, "packed"), (512, 1024, 1300, 16, 1, "one"), (128, 256, 900, 80, 5, "mixed"),
        (256, 192, 1500, 64, 3, "packed"), (64, 128, 300, 256, 4, "mixed"), (128, 128, 500, 16, 200, "mixed"),
-       (256, 256, 130, 16, 4, "none"), (1536, 1088, 640, 128, 3, "packed")]
+       (256, 256, 130, 16, 4, "none"), (1536, 1088, 640, 128, 3, "packed"),
+       (128, 4096, 1531, 48, 30, "packed"), (64, 4096, 5200, 16, 5, "packed"), (1024, 512, 2000, 240, 3, "mixed")]
 
 
 @pytest.mark.parametrize("d_out,d_in,M,r,n,kind", BWD)

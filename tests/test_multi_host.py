@@ -23,7 +23,7 @@ def test_sizes():
     # up to 64 tokens: partial sums only; above: W_hat as well
     assert qn.multi_linear_fwd_workspace_bytes(4096, 4096, 64, 16, 8) < 2 * 4096 * 4096
     assert qn.multi_linear_fwd_workspace_bytes(4096, 4096, 65, 16, 8) > 2 * 4096 * 4096
-    # the backward holds both transposed factors of the pool
+    # the backward keeps gradient partials that grow with the pool
     few, many = (qn.multi_linear_bwd_workspace_bytes(256, 256, 200, 16, n) for n in (1, 101))
     assert many - few >= 100 * 2 * 16 * 512
 
