@@ -159,17 +159,27 @@ __device__ __forceinline__ float gemv_half_block(const uint4 c, const uint4* xv,
 // chunks 4 l .. 4 l + 3; their order is XORed with bits 2..3 of l
 __device__ __forceinline__ int gv_xpos(int c) { return (c & ~3) | ((c & 3) ^ ((c >> 4) & 3)); }
 
+// The adapter of the token, read on the device (kSel): A, B and s are then those of adapter
+// *adapter of a pool ([n, r, d_in], [n, d_out, r], [n]), and a negative one has no rank term.
+struct GvSelect {
+    const int32_t* adapter;
+    const float* s;
+    int64_t a_stride, b_stride;     // elements of one adapter
+};
+
 // T tokens (1, 2 or 3; the ntok <= T real ones first, x rows past ntok read as zero and
 // their outputs not stored): each code-pair lookup serves all T tokens. T > 1 only with
 // the one-launch form (kAx); 4 tokens would need more than the 128 registers a lane has
 // at 16 waves per CU.
-template <int T, bool kAx>
+template <int T, bool kAx, bool kSel = false>
 __global__ __launch_bounds__(1024)
 void gemv_nf4_kernel(const uint4* __restrict__ codes, BlockConsts bc,
                      int d_out, int d_in, const uint16_t* __restrict__ x, int ldx, int ntok,
                      const uint16_t* __restrict__ B, int r, float s, const float* __restrict__ part,
-                     int nparts, const uint16_t* __restrict__ A, uint16_t* __restrict__ y, int ldy, NF4Tables tab) {
+                     int nparts, const uint16_t* __restrict__ A, uint16_t* __restrict__ y, int ldy, NF4Tables tab,
+                     GvSelect sel) {
     static_assert(T == 1 || kAx, "several tokens only in the one-launch form");
+    static_assert(!kSel || (T == 1 && kAx), "a selected adapter only in the one-token one-launch form");
     __shared__ uint4 lut4[256 * kLutCopies / 4];
     __shared__ uint4 xs[2][T][kGvSeg / 8];
     __shared__ float tvs[1024];
@@ -223,6 +233,15 @@ void gemv_nf4_kernel(const uint4* __restrict__ codes, BlockConsts bc,
 #pragma unroll
     for (int k = 0; k < T; ++k) st[k] = uint4{0, 0, 0, 0};
     stage_issue(st, 0);
+    bool ranked = true;
+    if constexpr (kSel) {
+        const int a = sel.adapter[0];
+        ranked = a >= 0;
+        const int64_t ai = ranked ? a : 0;
+        A += ai * sel.a_stride;
+        B += ai * sel.b_stride;
+        s = sel.s[ai];
+    }
     const int nval = nparts * r;                  // <= 1024
     uint4 tst = uint4{0, 0, 0, 0};
     // one-launch form: wave j loads row j of A (rows past r repeat row r - 1 and are not
@@ -396,7 +415,8 @@ void gemv_nf4_kernel(const uint4* __restrict__ codes, BlockConsts bc,
 #pragma unroll
     for (int k = 0; k < T; ++k) {
         float v = acc[k];
-        for (int j = lane; j < r; j += 64) v += bf16_to_f32(brow[j]) * s_t[16 * k + j];
+        for (int j = lane; j < r; j += 64)
+            if (!kSel || ranked) v += bf16_to_f32(brow[j]) * s_t[16 * k + j];
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
         if (lane == 0 && row0 + wave < d_out && k < ntok) y[static_cast<int64_t>(k) * ldy + row0 + wave] = bf16_bits(v);
@@ -447,12 +467,13 @@ struct GvUnit {
 // T = 1, 2 or 3 tokens (x and y rows at strides ldx, ldy): each code-pair lookup serves
 // every token, with per token the dot order of the one-token form; s (A x) per token
 // at s_t[16 t + j] (one-launch form) or s_t[t r + j] (from the T-token slice partials).
-template <int T, bool kAx, bool kPub>
+template <int T, bool kAx, bool kPub, bool kSel = false>
 __global__ __launch_bounds__(1024)
 void gemv_nf4_persist(const uint4* __restrict__ codes, BlockConsts bc, int d_out, int d_in,
                       const uint16_t* __restrict__ x, int64_t ldx, const uint16_t* __restrict__ B, int r, float s,
                       float* __restrict__ part, int nparts, int per, int ax_polls, const uint16_t* __restrict__ A,
-                      uint16_t* __restrict__ y, int64_t ldy, NF4Tables tab) {
+                      uint16_t* __restrict__ y, int64_t ldy, NF4Tables tab, GvSelect sel) {
+    static_assert(!kSel || (T == 1 && kAx), "a selected adapter only in the one-token one-launch form");
     constexpr int kBw = kAx ? 1 : 4;              // 64-entry pieces of a row of B (r <= 16 in the one-launch form)
     constexpr int kX = T == 1 ? kGvXMax : kGvXMaxT;
     constexpr int kXPer = kX / 8 / 1024;          // 16-byte x chunks per thread and token
@@ -504,6 +525,15 @@ void gemv_nf4_persist(const uint4* __restrict__ codes, BlockConsts bc, int d_out
     for (int t = 0; t < T; ++t)
 #pragma unroll
         for (int i = 0; i < kXPer; ++i) xr[t][i] = x4[t * (ldx / 8) + min(tid + 1024 * i, nch - 1)];
+    bool ranked = true;
+    if constexpr (kSel) {
+        const int a = sel.adapter[0];
+        ranked = a >= 0;
+        const int64_t ai = ranked ? a : 0;
+        A += ai * sel.a_stride;
+        B += ai * sel.b_stride;
+        s = sel.s[ai];
+    }
     uint4 av[8];
     uint4 tst = uint4{0, 0, 0, 0};
     if constexpr (kAx) {
@@ -687,7 +717,7 @@ void gemv_nf4_persist(const uint4* __restrict__ codes, BlockConsts bc, int d_out
 #pragma unroll
         for (int i = 0; i < kBw; ++i) {
             const int j = lane + 64 * i;
-            if (j < r) v += bf16_to_f32(bw[i]) * s_t[(kAx ? 16 : r) * k + j];
+            if (j < r && (!kSel || ranked)) v += bf16_to_f32(bw[i]) * s_t[(kAx ? 16 : r) * k + j];
         }
 #pragma unroll
         for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
@@ -816,7 +846,7 @@ hipError_t launch_gemv_nf4(const uint8_t* codes, const BlockConsts& bc, int64_t 
     const dim3 pgrid(static_cast<unsigned>(one_launch || nt != 1 ? want_wgs : std::max<int64_t>(want_wgs, nparts)));
 #define QN_GVP_LAUNCH(TT, AX, PUB, NP, PER) \
     QN_LAUNCH("gemv_nf4_persist", st, (gemv_nf4_persist<TT, AX, PUB>), pgrid, dim3(64 * kGvWaves), 0, st, c4, bc, dout, \
-              din, x, ldx, B, r, s, ws_part, NP, PER, g_ax_polls.load(std::memory_order_relaxed), A, y, ldy, tables())
+              din, x, ldx, B, r, s, ws_part, NP, PER, g_ax_polls.load(std::memory_order_relaxed), A, y, ldy, tables(), GvSelect{})
     if (persist && one_launch) {
         if (nt == 1) QN_GVP_LAUNCH(1, true, false, 0, 0);
         else if (nt == 2) QN_GVP_LAUNCH(2, true, false, 0, 0);
@@ -828,7 +858,7 @@ hipError_t launch_gemv_nf4(const uint8_t* codes, const BlockConsts& bc, int64_t 
 #define QN_GV_LAUNCH(TT) \
         QN_LAUNCH("gemv_nf4_kernel", st, (gemv_nf4_kernel<TT, true>), grid, dim3(64 * kGvWaves), 0, st, \
                   c4, bc, dout, din, x, static_cast<int>(ldx), nt, B, r, s, ws_part, 0, A, y, static_cast<int>(ldy), \
-                  tables())
+                  tables(), GvSelect{})
         if (nt == 1) QN_GV_LAUNCH(1);
         else if (nt == 2) QN_GV_LAUNCH(2);
         else QN_GV_LAUNCH(3);
@@ -855,7 +885,30 @@ hipError_t launch_gemv_nf4(const uint8_t* codes, const BlockConsts& bc, int64_t 
 #undef QN_GVP_LAUNCH
     if (nt != 1) return hipErrorInvalidValue;
     QN_LAUNCH("gemv_nf4_kernel", st, (gemv_nf4_kernel<1, false>), grid, dim3(64 * kGvWaves), 0, st, c4, bc, dout, din,
-              x, static_cast<int>(ldx), 1, B, r, s, ws_part, nparts, A, y, static_cast<int>(ldy), tables());
+              x, static_cast<int>(ldx), 1, B, r, s, ws_part, nparts, A, y, static_cast<int>(ldy), tables(), GvSelect{});
+    return hipGetLastError();
+}
+
+// One token whose adapter is read on the device (r <= 16 and d_in <= 4096: every workgroup
+// forms s A x itself).
+bool gemv_selects(int64_t d_in, int r) { return r <= kGvWaves && d_in <= kGvSeg; }
+
+hipError_t launch_gemv_nf4_select(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
+                                  const uint16_t* A, const uint16_t* B, const float* s, int r, const int32_t* adapter,
+                                  const uint16_t* x, uint16_t* y, hipStream_t st) {
+    if (!gemv_selects(d_in, r)) return hipErrorInvalidValue;
+    const int64_t ngroups = (d_out + kGvWaves - 1) / kGvWaves;
+    const uint4* c4 = reinterpret_cast<const uint4*>(codes);
+    const int dout = static_cast<int>(d_out), din = static_cast<int>(d_in);
+    const GvSelect sel{adapter, s, r * d_in, d_out * r};
+    if (ngroups > kGvPersistWgs)
+        QN_LAUNCH("gemv_nf4_persist", st, (gemv_nf4_persist<1, true, false, true>), dim3(kGvPersistWgs),
+                  dim3(64 * kGvWaves), 0, st, c4, bc, dout, din, x, d_in, B, r, 0.0f, nullptr, 0, 0, 0, A, y, d_out,
+                  tables(), sel);
+    else
+        QN_LAUNCH("gemv_nf4_kernel", st, (gemv_nf4_kernel<1, true, true>), dim3(static_cast<unsigned>(ngroups)),
+                  dim3(64 * kGvWaves), 0, st, c4, bc, dout, din, x, din, 1, B, r, 0.0f, nullptr, 0, A, y, dout,
+                  tables(), sel);
     return hipGetLastError();
 }
 

@@ -107,6 +107,14 @@ hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, 
                              const uint16_t* R, bool rank_major, int r, const MultiPlan& plan, uint16_t* C, int64_t ldc, int64_t M,
                              int64_t N, float* part, hipStream_t st);
 
+// ---- gemv.hip ----
+// One token with the adapter *adapter (none if negative) of a pool, in one launch: W_hat x +
+// s_a B_a (A_a x), for r <= 16 and d_in <= 4096 (gemv_selects).
+bool gemv_selects(int64_t d_in, int r);
+hipError_t launch_gemv_nf4_select(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
+                                  const uint16_t* A, const uint16_t* B, const float* s, int r, const int32_t* adapter,
+                                  const uint16_t* x, uint16_t* y, hipStream_t st);
+
 // ---- skinny.hip, multi_small.hip ----
 // Forward of up to kSkinnyMaxTokens tokens from the packed codes: the W_hat x partials
 // [skinny_splits(d_in, M)][M][d_out] by token and the s_a A_a x partials

@@ -4,7 +4,9 @@
 //   skinny_nf4<., true> (skinny.hip) streams the weight's packed codes once for all tokens
 //   into K-split partials of W_hat x, and beside them reads A of every adapter in use once
 //   for the partials of s_a A_a x;
-//   multi_reduce_small adds the partials and the rank term.
+//   multi_reduce_small adds the partials and the rank term;
+// or, for one token with r <= 16 and d_in <= 4096, in the streaming GEMV's one launch, which
+// reads the token's adapter from the plan (4096 x 4096: 10.9 -> 6.9 us per graph-replayed call).
 //
 // multi_reduce_small: a workgroup takes 16 rows of W and all tokens. It forms T = bf16(sum
 // of the A x partials in slice order) of every position in LDS; its waves take the plan's
@@ -156,6 +158,10 @@ hipError_t launch_multi_small(const uint8_t* codes, const BlockConsts& bc, int64
                               const MultiPool& pool, const uint16_t* X, int64_t ldx, int64_t M,
                               const MultiPlan& plan, float* part, float* part_t, uint16_t* Y, int64_t ldy,
                               hipStream_t st) {
+    // one token: the first item's adapter is its own (none: -1)
+    if (M == 1 && gemv_selects(d_in, pool.r))
+        return launch_gemv_nf4_select(codes, bc, d_out, d_in, pool.A, pool.B, pool.s, pool.r, &plan.items[0].adapter, X,
+                                      Y, st);
     const hipError_t e = launch_skinny_multi(codes, bc, d_out, d_in, pool, plan, X, ldx, M, part, part_t, st);
     if (e != hipSuccess) return e;
     SmallArgs a{};

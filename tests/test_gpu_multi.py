@@ -131,7 +131,10 @@ def test_plan(M, n, kind):
 SMALL = [(64, 64, 1, 16, 1, "one"), (256, 320, 1, 16, 4, "none"), (512, 4096, 3, 32, 3, "mixed"),
          (1024, 1088, 16, 16, 40, "mixed"), (320, 192, 17, 48, 2, "mixed"), (512, 2048, 33, 64, 33, "packed"),
          (192, 11008, 64, 80, 64, "mixed"), (4096, 512, 64, 256, 5, "mixed"), (256, 256, 64, 16, 1, "one"),
-         (128, 64, 40, 128, 300, "outside")]
+         (128, 64, 40, 128, 300, "outside"),
+         # one token on the streaming GEMV, up to 4096 rows and more, with an adapter and without
+         (4096, 4096, 1, 16, 3, "one"), (4160, 256, 1, 16, 3, "one"), (4160, 256, 1, 16, 3, "none"),
+         (128, 4160, 1, 16, 2, "one"), (128, 256, 1, 32, 2, "one")]
 LARGE = [(256, 256, 65, 16, 3, "mixed"), (320, 192, 300, 32, 5, "packed"), (512, 4096, 200, 48, 40, "mixed"),
          (1024, 1536, 1531, 16, 7, "packed"), (256, 512, 1024, 64, 4, "packed"), (64, 64, 257, 256, 2, "mixed"),
          (192, 128, 513, 80, 64, "outside"), (256, 320, 700, 112, 1, "one"), (256, 256, 600, 16, 9, "none"),
@@ -205,6 +208,22 @@ def test_adapters_do_not_reach_each_other(M, value):
     assert not torch.isfinite(Y[~other].float()).all() and not torch.isfinite(dX[~other].float()).all()
     keep = [a for a in range(6) if a != bad]
     assert torch.equal(dA[keep], rA[keep]) and torch.equal(dB[keep], rB[keep])
+
+
+@pytest.mark.parametrize("d_out", [256, 4160])
+@pytest.mark.parametrize("who", [-1, 1])
+def test_one_token_keeps_off_other_adapters(d_out, who):
+    _say(f"[multi] one token beside adapters of NaN, {d_out} rows, adapter {who}")
+    L = Layer(d_out, 256, 1, 16, 3, "one", seed=2)
+    plan = qn.multi_plan(torch.tensor([who], dtype=torch.int32, device=dev()), 3)
+    ref = qn.multi_linear_fwd(L.q, L.pool, plan, L.X)
+    for a in (0, 2):
+        L.pool.A[a] = float("nan")
+        L.pool.B[a] = float("inf")
+    L.pool.s[0] = float("nan")
+    Y = qn.multi_linear_fwd(L.q, L.pool, plan, L.X)
+    torch.cuda.synchronize()
+    assert torch.isfinite(ref.float()).all() and torch.equal(Y.view(torch.int16), ref.view(torch.int16))
 
 
 @pytest.mark.parametrize("M", [50, 400])
