@@ -14,16 +14,17 @@
 // use) pairs, however the requests came in.
 //
 // Rank steps. After the last main step a tile walks the adapters with tokens in it, 64
-// ranks a step, double-buffered in the same stages (the first one's loads go out under the
-// last main step). A 32-row MFMA tile skips an adapter that has none of its rows, adds
-// straight to its accumulators when all 32 rows are the adapter's, and otherwise forms the
-// product apart and adds it where the lane's row is the adapter's. So a row only ever
+// ranks a step (4 adapters of rank 16, 2 of 32), double-buffered in the same stages (the first
+// one's loads go out under the last main step). A 32-row MFMA tile skips an adapter that has
+// none of its rows, adds straight to its accumulators when all 32 rows are the adapter's, and
+// otherwise forms the product apart and adds it where the lane's row is the adapter's. So a row only ever
 // meets its own adapter: zeros in place of the other rows would let an infinity or NaN in
 // one adapter's weights reach its neighbours' tokens, and this costs fewer MFMAs besides.
 //
 // The last round of tiles. With at most 64 tiles past a multiple of the 256 CUs their K-steps
-// are split as in the single-adapter GEMM (gemm_split), the rank steps going to the last
-// split; gemm_multi_reduce adds the partials. With 65 to 128 they are taken as twice as many
+// are split as in the single-adapter GEMM (gemm_split), and so are their adapters (256 tokens
+// of 256 users, 16 tiles: 64 rank steps of 2.6 us would stand in one split's way);
+// gemm_multi_reduce adds the partials. With 65 to 128 they are taken as twice as many
 // half tiles of 128 x 256, whole in K, which writes and reads back no partials: a half tile's
 // step takes 0.6 of a whole one's (4 LDS reads for 4 MFMAs, not 6 for 8), more than half, so
 // whole tiles stay the rule (4096 x 4096 at 4096 tokens: 119 us whole, 133 us in halves).
@@ -40,7 +41,6 @@
 #include "internal.h"
 #include "mfma_device.h"
 #include "multi.h"
-#include "multi_device.h"
 #include "nf4_device.h"
 
 #include <algorithm>
@@ -55,6 +55,10 @@ constexpr int kHalfStage = kChunks / 2 + kChunks;
 __shared__ uint4 g_h0[kHalfStage];
 __shared__ uint4 g_h1[kHalfStage];
 __shared__ uint4 g_h2[kHalfStage];
+// the adapters with tokens in the tile: which, and their positions [lo, hi)
+__shared__ int g_ad[BM];
+__shared__ int g_lo[BM];
+__shared__ int g_hi[BM];
 
 constexpr int kWM = 2, kWN = 4;                 // waves
 constexpr int kNT = 64 * kWM * kWN;             // threads
@@ -65,7 +69,6 @@ struct MultiGemm {
     const uint16_t* T;                          // [M, r]
     const uint16_t* R;                          // [adapters, N, r], or [adapters, r, N]
     int r;
-    uint32_t bytesT, bytesR;                    // extents of T and of one adapter's R
 };
 
 // LDS reads and MFMAs of a k16 sub-step in turn: one read, then PER MFMAs, N times
@@ -107,19 +110,28 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
     const int m0 = tm * BM + (kHalf ? (place & 1) * BMT : 0), n0 = tn * BN;
     if (kHalf && m0 >= M) return;
 
-    // this tile's adapters: used[k0 .. k1), `steps` rank steps in all (last split only)
+    // this tile's adapters: used[k0 .. k1), `steps` rank steps in all
     int2 kr = mg.plan.tile[tm];
     if constexpr (kHalf) {                      // the adapters of this half alone
         while (kr.x < kr.y && mg.plan.start[mg.plan.used[kr.x] + 1] <= m0) ++kr.x;
         while (kr.x < kr.y && mg.plan.start[mg.plan.used[kr.y - 1]] >= m0 + BMT) --kr.y;
     }
+    // a rank step holds 64 ranks: of one adapter, or of 2 or 4 adapters of 32 or 16 (8 << sh ranks
+    // each); jsteps steps per adapter of more than 64
+    const int sh = mg.r == 16 ? 1 : mg.r == 32 ? 2 : 3;
+    const int per = 8 >> sh;
     const int jsteps = (mg.r + BK - 1) / BK;
-    const int steps = !split_wg || sk == g.splits - 1 ? (kr.y - kr.x) * jsteps : 0;
-    int a_next = 0, lo_next = 0, hi_next = 0;   // adapter and positions of the step issued next
-    if (steps > 0) {
-        a_next = mg.plan.used[kr.x];
-        lo_next = mg.plan.start[a_next];
-        hi_next = mg.plan.start[a_next + 1];
+    if (split_wg) {                             // this split's share of them
+        const int k = kr.y - kr.x;
+        kr = int2{kr.x + k * sk / g.splits, kr.x + k * (sk + 1) / g.splits};
+    }
+    const int used = kr.y - kr.x;
+    const int steps = (used + per - 1) / per * jsteps;
+    if (tid < used) {                           // at most one per row
+        const int a = mg.plan.used[kr.x + tid];
+        g_ad[tid] = a;
+        g_lo[tid] = mg.plan.start[a];
+        g_hi[tid] = mg.plan.start[a + 1];
     }
 
     const uint32_t kcE = static_cast<uint32_t>((lane & 7) ^ (lane >> 4)) * 16u;
@@ -155,25 +167,23 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
         }                                                                                         \
     }
 
-    // Rank step S into stage ST: ranks j0 .. of T's rows and of the rows of R of adapter
-    // a_next. Pieces past r re-read the last one (no MFMA reads them); the offsets are formed
+    // Rank step S into stage ST: ranks j0 .. of T's rows (the same 8 << sh ranks once per
+    // adapter of the step) and of the rows of R of its adapters. Pieces past r re-read the last
+    // one, adapters past the last re-read it (no MFMA reads either); the addresses are formed
     // from an opaque copy of the lane index, so they hold no registers through the main steps.
     auto issue_rank = [&](int s, uint4* st) {
-        const int j0 = (s % jsteps) * BK;
+        const int j0 = (s % jsteps) * BK, k0 = s / jsteps * per;
         int ln = lane;
         asm volatile("" : "+v"(ln));
-        const uint16_t* rb = mg.R + static_cast<int64_t>(a_next) * N * mg.r;
-        const __amdgpu_buffer_rsrc_t rsT = make_rsrc(mg.T, mg.bytesT);
-        const __amdgpu_buffer_rsrc_t rsR = make_rsrc(rb, mg.bytesR);
         uint4* sp = st + wave * (64 * SEGP);
         uint4* sq = st + kQ + wave * (64 * SEG);
         const int last = mg.r / 8 - 1 - j0 / 8;
 #pragma unroll
         for (int j = 0; j < SEGP; ++j) {
             const int rr = 8 * SEGP * wave + 8 * j + (ln >> 3);
-            const int c = min((ln & 7) ^ ((rr >> 1) & 7), last);
-            const uint32_t vp = (static_cast<uint32_t>(min(m0 + rr, M - 1)) * mg.r + 8 * c) * 2u;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rsT, (lds_ptr_t)(sp + 64 * j), 16, vp, j0 * 2, 0, 0);
+            const int c = (ln & 7) ^ ((rr >> 1) & 7);
+            const int64_t row = min(m0 + rr, M - 1);
+            load_lds16(mg.T + row * mg.r + j0 + 8 * min(c & ((1 << sh) - 1), last), sp + 64 * j);
         }
 #pragma unroll
         for (int j = 0; j < SEG; ++j) {
@@ -181,13 +191,13 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
                 // 2 rank rows of 256 columns a segment, 16-byte piece c of rank k at c ^ 2 (k % 4)
                 const int k = 2 * (SEG * wave + j) + (ln >> 5);
                 const int n = min(n0 + 8 * ((ln & 31) ^ (2 * (k & 3))), N - 8);
-                const uint32_t vq = (static_cast<uint32_t>(min(j0 + k, mg.r - 1)) * N + n) * 2u;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsR, (lds_ptr_t)(sq + 64 * j), 16, vq, 0, 0, 0);
+                const int64_t a = g_ad[min(k0 + (k >> (sh + 3)), used - 1)];
+                load_lds16(mg.R + (a * mg.r + min(j0 + (k & ((8 << sh) - 1)), mg.r - 1)) * N + n, sq + 64 * j);
             } else {
                 const int rr = 8 * SEG * wave + 8 * j + (ln >> 3);
-                const int c = min((ln & 7) ^ ((rr >> 1) & 7), last);
-                const uint32_t vq = (static_cast<uint32_t>(min(n0 + rr, N - 1)) * mg.r + 8 * c) * 2u;
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsR, (lds_ptr_t)(sq + 64 * j), 16, vq, j0 * 2, 0, 0);
+                const int c = (ln & 7) ^ ((rr >> 1) & 7);
+                const int64_t a = g_ad[min(k0 + (c >> sh), used - 1)];
+                load_lds16(mg.R + (a * N + min(n0 + rr, N - 1)) * mg.r + j0 + 8 * min(c & ((1 << sh) - 1), last), sq + 64 * j);
             }
         }
     };
@@ -293,7 +303,7 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
     } else {
     stage = KT & 1;
     QN_ISSUE(0, g_st0)
-    QN_WAIT_VM(0);
+    __builtin_amdgcn_s_waitcnt(0);              // (the adapter list's LDS writes too)
     QN_BARRIER();
     QN_FRAGS(g_st0, chs[0], fa)
     // the last main step stands outside the loop, which then has no branch in it
@@ -324,56 +334,56 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
         uint4* const sb = kThree ? g_h1 : g_st1;
         const uint4* cur = ((stage + s) & 1) ? sb : sa;
         uint4* nxt = ((stage + s) & 1) ? sa : sb;
-        const int lo = lo_next, hi = hi_next;
+        if (s + 1 < steps) issue_rank(s + 1, nxt);
+        const int k0 = s / jsteps * per;
         const int subs = min(BK, mg.r - (s % jsteps) * BK) / 16;
-        if (s + 1 < steps) {
-            if ((s + 1) % jsteps == 0) {
-                a_next = mg.plan.used[kr.x + (s + 1) / jsteps];
-                lo_next = mg.plan.start[a_next];
-                hi_next = mg.plan.start[a_next + 1];
-            }
-            issue_rank(s + 1, nxt);
-        }
-        uint4 q[TN][4];
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-            if (kk < subs) {
+        for (int kk = 0; kk < 4; ++kk) {
+            // sub-step kk: 16 ranks of adapter k0 + (kk >> (sh - 1))
+            const int k = k0 + (kk >> (sh - 1));
+            if (k >= used || (sh == 3 && kk >= subs)) continue;
+            const int lo = __builtin_amdgcn_readfirstlane(g_lo[k]), hi = __builtin_amdgcn_readfirstlane(g_hi[k]);
+            const int w0 = m0 + wm * (TM * 32);
+            if (w0 >= hi || w0 + TM * 32 <= lo) continue;                // none of the wave's positions
+            uint4 q[TN];
+            if constexpr (kRankMajor) {
+                const int kr0 = 16 * kk + 8 * (lane >> 5) + ((lane >> 2) & 3);
+                uint32_t qa[TN];
 #pragma unroll
                 for (int a = 0; a < TN; ++a) {
-                    if constexpr (kRankMajor) {
-                        const int k = 8 * (lane >> 5) + ((lane >> 2) & 3);       // + 16 kk, the same k % 4
-                        const int n = wn * (TN * 32) + a * 32 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
-                        const char* q0 = reinterpret_cast<const char*>(cur + kQ) + k * 512 +
-                                         ((((n >> 3) ^ (2 * (k & 3))) << 4) | ((n & 7) << 1));
-                        q[a][kk] = lds_tr8(q0 + kk * (16 * 512), 4 * 512);
-                    } else {
-                        q[a][kk] = cur[qrow + a * 256 + chs[kk]];
-                    }
+                    const int n = wn * (TN * 32) + a * 32 + 16 * ((lane >> 4) & 1) + 4 * (lane & 3);
+                    qa[a] = lds_addr(cur + kQ) + kr0 * 512 + ((((n >> 3) ^ (2 * (kr0 & 3))) << 4) | ((n & 7) << 1));
                 }
+                static_assert(TN == 2, "two column tiles");
+                unsigned long long v[4];
+                asm volatile("ds_read_b64_tr_b16 %0, %4\n\tds_read_b64_tr_b16 %1, %4 offset:2048\n\t"
+                             "ds_read_b64_tr_b16 %2, %5\n\tds_read_b64_tr_b16 %3, %5 offset:2048\n\t"
+                             "s_waitcnt lgkmcnt(0)"
+                             : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]) : "v"(qa[0]), "v"(qa[1]) : "memory");
+#pragma unroll
+                for (int a = 0; a < TN; ++a)
+                    q[a] = uint4{static_cast<uint32_t>(v[2 * a]), static_cast<uint32_t>(v[2 * a] >> 32),
+                                 static_cast<uint32_t>(v[2 * a + 1]), static_cast<uint32_t>(v[2 * a + 1] >> 32)};
+            } else {
+#pragma unroll
+                for (int a = 0; a < TN; ++a) q[a] = cur[qrow + a * 256 + chs[kk]];
             }
 #pragma unroll
-        for (int b = 0; b < TM; ++b) {
-            const int p0 = m0 + wm * (TM * 32) + b * 32;             // the sub-tile's positions p0 .. p0 + 31
-            if (p0 >= hi || p0 + 32 <= lo) continue;                 // wave-uniform
-            const bool whole = p0 >= lo && p0 + 32 <= hi;
-            const bool mine = p0 + static_cast<int>(frow) >= lo && p0 + static_cast<int>(frow) < hi;
-            uint4 p[4];
+            for (int b = 0; b < TM; ++b) {
+                const int p0 = w0 + b * 32;                              // the sub-tile's positions p0 .. p0 + 31
+                if (p0 >= hi || p0 + 32 <= lo) continue;                 // wave-uniform
+                const uint4 p = cur[prow + b * 256 + chs[kk]];
+                if (p0 >= lo && p0 + 32 <= hi) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-                if (kk < subs) p[kk] = cur[prow + b * 256 + chs[kk]];
-#pragma unroll
-            for (int a = 0; a < TN; ++a) {
-                if (whole) {
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        if (kk < subs) acc[a][b] = mfma32(q[a][kk], p[kk], acc[a][b]);
+                    for (int a = 0; a < TN; ++a) acc[a][b] = mfma32(q[a], p, acc[a][b]);
                 } else {
-                    f32x16 t = f32x16{};
+                    const bool mine = p0 + static_cast<int>(frow) >= lo && p0 + static_cast<int>(frow) < hi;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        if (kk < subs) t = mfma32(q[a][kk], p[kk], t);
+                    for (int a = 0; a < TN; ++a) {
+                        const f32x16 t = mfma32(q[a], p, f32x16{});
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) acc[a][b][e] = mine ? acc[a][b][e] + t[e] : acc[a][b][e];
+                        for (int e = 0; e < 16; ++e) acc[a][b][e] = mine ? acc[a][b][e] + t[e] : acc[a][b][e];
+                    }
                 }
             }
         }
@@ -508,8 +518,6 @@ hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, 
     g.bytesP = static_cast<uint32_t>(2 * ldp * M);
     g.bytesQ = static_cast<uint32_t>(2 * K * N);
     mg.plan = plan; mg.T = T; mg.R = R; mg.r = r;
-    mg.bytesT = static_cast<uint32_t>(2 * M * r);
-    mg.bytesR = static_cast<uint32_t>(2 * N * r);
     const int tiles = g.tiles_m * g.tiles_n;
     g.part = part;
 #define QN_GEMM(KERNEL, GRID)                                                                          \

@@ -90,8 +90,12 @@ void multi_reduce_small(SmallArgs a) {
         const int p = e / quads, j = e % quads * 4;
         uint2 v = uint2{0, 0};
         if (j < r) {
-            const float4 t = ordered_sum4<8>(a.part_t + static_cast<int64_t>(p) * r + j, static_cast<int64_t>(M) * r,
-                                             a.tsplits);
+            const float* pt = a.part_t + static_cast<int64_t>(p) * r + j;
+            const int64_t stride = static_cast<int64_t>(M) * r;
+            // as many loads as there are slices (uniform)
+            const float4 t = a.tsplits == 1 ? *reinterpret_cast<const float4*>(pt)
+                             : a.tsplits <= 4 ? ordered_sum4<4>(pt, stride, a.tsplits)
+                                              : ordered_sum4<8>(pt, stride, a.tsplits);
             v = uint2{pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w)};
         }
         *reinterpret_cast<uint2*>(&s_t[p * kPitch + j]) = v;
@@ -168,7 +172,7 @@ hipError_t launch_multi_small(const uint8_t* codes, const BlockConsts& bc, int64
     a.plan = plan; a.B = pool.B;
     a.d_out = static_cast<int>(d_out); a.M = static_cast<int>(M); a.r = pool.r;
     a.splits = skinny_splits(d_in, M);
-    a.tsplits = multi_small_splits(d_in);
+    a.tsplits = multi_small_splits(d_in, M, pool.n, pool.r);
     a.part = part; a.part_t = part_t; a.Y = Y; a.ldy = ldy;
     if (pool.r <= 32) return launch_reduce<1>(a, st);
     if (pool.r <= 64) return launch_reduce<2>(a, st);

@@ -483,12 +483,20 @@ hipError_t launch_stream(const SkArgs& a, const MultiAx& m, int n_ax, hipStream_
     return hipGetLastError();
 }
 
-// K-slices of A x: at most 8, of at least 16 blocks (two per wave)
-int ax_blocks(int64_t d_in) { return static_cast<int>(std::max<int64_t>(16, (d_in / 64 + 7) / 8)); }
+// 64-wide blocks per K-slice of A x: slices enough for about 256 workgroups of A x, but at
+// least 16 blocks (two per wave) each and at most 8 slices (every reader of the sums adds them)
+int ax_blocks(int64_t d_in, int64_t M, int n, int r) {
+    const int64_t nb = d_in / 64, jobs = multi_max_items(M, n) * (r / 16);
+    const int64_t want = std::max<int64_t>(1, std::min<int64_t>(8, (256 + jobs - 1) / jobs));
+    return static_cast<int>(std::max<int64_t>(16, (nb + want - 1) / want));
+}
 
 }  // namespace
 
-int multi_small_splits(int64_t d_in) { return static_cast<int>((d_in / 64 + ax_blocks(d_in) - 1) / ax_blocks(d_in)); }
+int multi_small_splits(int64_t d_in, int64_t M, int n, int r) {
+    const int per = ax_blocks(d_in, M, n, r);
+    return static_cast<int>((d_in / 64 + per - 1) / per);
+}
 
 hipError_t launch_skinny_multi(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
                                const MultiPool& pool, const MultiPlan& plan, const uint16_t* X, int64_t ldx,
@@ -501,8 +509,8 @@ hipError_t launch_skinny_multi(const uint8_t* codes, const BlockConsts& bc, int6
     MultiAx m{};
     m.plan = plan; m.pool = pool;
     m.max_items = static_cast<int>(multi_max_items(d_seq, pool.n));
-    m.splits = multi_small_splits(d_in);
-    m.bper = ax_blocks(d_in);
+    m.splits = multi_small_splits(d_in, d_seq, pool.n, pool.r);
+    m.bper = ax_blocks(d_in, d_seq, pool.n, pool.r);
     m.part = part_t;
     return launch_stream<true>(a, m, m.max_items * m.splits * (pool.r / 16), st);
 }
