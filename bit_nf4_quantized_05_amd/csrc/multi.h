@@ -10,7 +10,7 @@ namespace qn {
 
 // ---- adamw.hip ----
 constexpr int kAdamBlock = 256;             // elements per state block (one wave, 4 per lane)
-constexpr int kAdamChunkBlocks = 8;         // blocks per workgroup
+constexpr int kAdamChunkBlocks = 4;         // blocks per workgroup
 constexpr int kAdamChunk = kAdamBlock * kAdamChunkBlocks;
 
 // One tensor of a step's table; the table is an array of these, then one AdamChunk per

@@ -104,9 +104,9 @@ __device__ __forceinline__ void multi_ax_job(const MultiAx& m, const SkArgs& a, 
     f32x4 acc[TT];
 #pragma unroll
     for (int t = 0; t < TT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    // U blocks k, k + 8 at a time (past the slice: k again, not added); with 3 or 4 token tiles
-    // one, or the registers would leave room for one workgroup per CU instead of two
-    constexpr int U = TT <= 2 ? 2 : 1;
+    // U blocks k, k + 8 at a time (past the slice: k again, not added); with more than one
+    // token tile one, or the registers would leave room for a workgroup less per CU
+    constexpr int U = TT == 1 ? 2 : 1;
     for (int k = b0 + wave; k < b1; k += U * NW) {
         uint4 av[U][2], xv[TT][U][2];
         int64_t off[U];

@@ -29,7 +29,7 @@ def test_block_and_table_sizes():
     lib = _lib.lib()
     n = _i64(1, 256, 257, 0, 5000)
     assert lib.qlora_adamw_blocks(_at(n), 5) == 1 + 1 + 2 + 0 + 20
-    assert lib.qlora_adamw_table_bytes(_at(n), 5) == 5 * 48 + 8 * (1 + 1 + 1 + 0 + 3)
+    assert lib.qlora_adamw_table_bytes(_at(n), 5) == 5 * 48 + 8 * (1 + 1 + 1 + 0 + 5)
     assert lib.qlora_adamw_blocks(_at(_i64(-1)), 1) == -1
     assert lib.qlora_adamw_table_bytes(None, 2) == -1
     assert lib.qlora_adamw_blocks(None, 0) == 0
@@ -43,14 +43,14 @@ def test_table_entries_and_refusals():
     def table(p, g, c=None, flags=0):
         return lib.qlora_adamw_table(_at(p), _at(g), _at(c) if c else None, _at(n), 2, flags, buf.ctypes.data)
 
-    assert table(_ptrs(FAKE, FAKE + 4), _ptrs(FAKE, FAKE)) == 3
+    assert table(_ptrs(FAKE, FAKE + 4), _ptrs(FAKE, FAKE)) == 4
     rows = buf[:96].view(np.int64).reshape(2, 6)
     assert rows[0].tolist() == [FAKE, FAKE, 0, 3000, 0, 1]
     assert rows[1].tolist() == [FAKE + 4, FAKE, 0, 5, 12, 0]        # 4-byte aligned: no wide accesses
-    assert buf[96:].view(np.int32).tolist() == [0, 0, 0, 1, 1, 0]
+    assert buf[96:].view(np.int32).tolist() == [0, 0, 0, 1, 0, 2, 1, 0]
     assert table(_ptrs(FAKE, FAKE + 2), _ptrs(FAKE, FAKE)) == -1    # float32 at an odd half
     assert b"misaligned" in lib.qn_last_error()
-    assert table(_ptrs(FAKE, FAKE + 2), _ptrs(FAKE, FAKE), flags=4) == 3
+    assert table(_ptrs(FAKE, FAKE + 2), _ptrs(FAKE, FAKE), flags=4) == 4
     assert table(_ptrs(FAKE, None), _ptrs(FAKE, FAKE)) == -1
     assert table(_ptrs(FAKE, FAKE), _ptrs(FAKE, FAKE), flags=8) == -1
     assert table(_ptrs(FAKE, FAKE), _ptrs(FAKE, FAKE), _ptrs(FAKE, FAKE + 1)) == -1
