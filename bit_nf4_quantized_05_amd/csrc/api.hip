@@ -822,7 +822,7 @@ int qlora_multi_fwd(const uint8_t* codes, const int8_t* qconst, const float* qsc
     if ((e = qn::launch_multi_prologue(codes, bc, d_out, d_in, false, u16(mw.what), pl, s, d_seq, n, r,
                                        qn::MultiPre{X, ldx, d_in, A, f32(mw.pre0)}, qn::MultiPre{}, st)) != hipSuccess)
         return hip_fail(e, "qlora_multi_fwd (prologue)");
-    if ((e = qn::launch_multi_reduce(pl, d_seq, r, 1, f32(mw.pre0), mw.splits0, u16(mw.t), nullptr, 0, nullptr, st)) !=
+    if ((e = qn::launch_multi_reduce(d_seq, r, 1, f32(mw.pre0), mw.splits0, u16(mw.t), nullptr, 0, nullptr, st)) !=
         hipSuccess)
         return hip_fail(e, "qlora_multi_fwd (A x)");
     if ((e = qn::launch_gemm_multi(X, ldx, u16(mw.what), d_in, u16(mw.t), B, false, r, pl, Y, ldy, d_seq, d_out, f32(mw.gpart),
@@ -853,7 +853,7 @@ int qlora_multi_bwd(const uint8_t* codes, const int8_t* qconst, const float* qsc
                                        qn::MultiPre{X, ldx, d_in, A, f32(mw.pre0)},
                                        qn::MultiPre{dY, lddy, d_out, B, f32(mw.pre1)}, st)) != hipSuccess)
         return hip_fail(e, "qlora_multi_bwd (prologue)");
-    if ((e = qn::launch_multi_reduce(pl, d_seq, r, 3, f32(mw.pre0), mw.splits0, u16(mw.t), f32(mw.pre1), mw.splits1,
+    if ((e = qn::launch_multi_reduce(d_seq, r, 3, f32(mw.pre0), mw.splits0, u16(mw.t), f32(mw.pre1), mw.splits1,
                                      u16(mw.u), st)) != hipSuccess)
         return hip_fail(e, "qlora_multi_bwd (A x, B^T dy)");
     if ((e = qn::launch_gemm_multi(dY, lddy, u16(mw.what), d_out, u16(mw.u), A, true, r, pl, dX, lddx, d_seq, d_in,

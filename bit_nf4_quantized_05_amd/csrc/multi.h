@@ -95,7 +95,7 @@ hipError_t launch_multi_prologue(const uint8_t* codes, const BlockConsts& bc, in
 // T[piece][pos][r] = the slice partials added in slice order, in `pieces` bf16 terms (1:
 // rounded once; 3: the remainders too, 24 bits in all), for one or two products (part1
 // null: one)
-hipError_t launch_multi_reduce(const MultiPlan& plan, int64_t M, int r, int pieces, const float* part0, int splits0,
+hipError_t launch_multi_reduce(int64_t M, int r, int pieces, const float* part0, int splits0,
                                uint16_t* T0, const float* part1, int splits1, uint16_t* T1, hipStream_t st);
 
 // ---- gemm_multi.hip ----

@@ -38,7 +38,7 @@ constexpr int kWaves = 4;
 struct SmallArgs {
     MultiPlan plan;
     const uint16_t* B;                  // [n, d_out, r]
-    int d_out, M, r, splits, tsplits;
+    int d_out, M, r, splits, tsplits, max_items;
     const float* part;                  // [splits][M][d_out], by token
     const float* part_t;                // [tsplits][M][r], by position
     uint16_t* Y; int64_t ldy;
@@ -64,8 +64,10 @@ void multi_reduce_small(SmallArgs a) {
     auto load_b = [&](int k0, uint4 (&w)[kBatch][RC]) {
 #pragma unroll
         for (int n = 0; n < kBatch; ++n) {
-            const int k = min(k0 + kWaves * n, items - 1);
-            const uint16_t* row = a.B + (static_cast<int64_t>(a.plan.items[k].adapter) * a.d_out + o0 + i) * r;
+            // (no wait for the count: the list is full of items of adapter -1 past its end)
+            const int k = min(k0 + kWaves * n, a.max_items - 1);
+            const int64_t ad = max(a.plan.items[k].adapter, 0);
+            const uint16_t* row = a.B + (ad * a.d_out + o0 + i) * r;
 #pragma unroll
             for (int c = 0; c < RC; ++c) {
                 const uint4 v = *reinterpret_cast<const uint4*>(row + min(32 * c + 8 * g, r - 8));
@@ -74,7 +76,7 @@ void multi_reduce_small(SmallArgs a) {
         }
     };
     uint4 bw[kBatch][RC];
-    if (wave < items) load_b(wave, bw);
+    load_b(wave, bw);
     float pv[TT][SPL];
     int64_t tok[TT];
 #pragma unroll
@@ -173,6 +175,7 @@ hipError_t launch_multi_small(const uint8_t* codes, const BlockConsts& bc, int64
     a.d_out = static_cast<int>(d_out); a.M = static_cast<int>(M); a.r = pool.r;
     a.splits = skinny_splits(d_in, M);
     a.tsplits = multi_small_splits(d_in, M, pool.n, pool.r);
+    a.max_items = static_cast<int>(multi_max_items(M, pool.n));
     a.part = part; a.part_t = part_t; a.Y = Y; a.ldy = ldy;
     if (pool.r <= 32) return launch_reduce<1>(a, st);
     if (pool.r <= 64) return launch_reduce<2>(a, st);

@@ -567,17 +567,17 @@ __device__ __forceinline__ void multi_pre_job(const MultiPreJob& j, const MultiP
 }
 
 // T[piece][pos][r] = the slice partials added in slice order, as 1 or 3 bf16 terms; 4 ranks
-// per thread. The positions of a token without an adapter are not written.
+// per thread. Those of a token without an adapter come from sums that no slice wrote; nobody
+// reads them.
 struct MultiReduceJob { const float* part; uint16_t* T; int splits; };
 
 __global__ __launch_bounds__(256)
-void multi_reduce(MultiReduceJob j0, MultiReduceJob j1, int blocks0, const int32_t* __restrict__ head, int64_t M, int r,
-                  int pieces) {
+void multi_reduce(MultiReduceJob j0, MultiReduceJob j1, int blocks0, int64_t M, int r, int pieces) {
     const bool second = static_cast<int>(blockIdx.x) >= blocks0;
     const MultiReduceJob& jb = second ? j1 : j0;
     const int64_t idx = (static_cast<int64_t>(second ? blockIdx.x - blocks0 : blockIdx.x) * 256 + threadIdx.x) * 4;
-    if (idx >= static_cast<int64_t>(head[2]) * r) return;
     const int64_t total = M * r;
+    if (idx >= total) return;
     const float4 t = ordered_sum4<8>(jb.part + idx, total, jb.splits);
     float v[4] = {t.x, t.y, t.z, t.w};
     for (int p = 0; p < pieces; ++p) {
@@ -874,12 +874,12 @@ hipError_t launch_multi_prologue(const uint8_t* codes, const BlockConsts& bc, in
     return hipGetLastError();
 }
 
-hipError_t launch_multi_reduce(const MultiPlan& plan, int64_t M, int r, int pieces, const float* part0, int splits0,
+hipError_t launch_multi_reduce(int64_t M, int r, int pieces, const float* part0, int splits0,
                                uint16_t* T0, const float* part1, int splits1, uint16_t* T1, hipStream_t st) {
     const int blocks = static_cast<int>((M * r / 4 + 255) / 256);
     const MultiReduceJob j0{part0, T0, splits0}, j1{part1, T1, splits1};
     QN_LAUNCH("multi_reduce", st, multi_reduce, dim3(static_cast<unsigned>(part1 ? 2 * blocks : blocks)), dim3(256), 0,
-              st, j0, j1, blocks, plan.head, M, r, pieces);
+              st, j0, j1, blocks, M, r, pieces);
     return hipGetLastError();
 }
 

@@ -155,8 +155,9 @@ __device__ __forceinline__ void multi_ax_job(const MultiAx& m, const SkArgs& a, 
     }
 }
 
-// TT 16-token tiles; kMulti: the first m.n workgroups form A x of many adapters instead of
-// the rows of one A past the rows of W (a.r = 0)
+// TT 16-token tiles; kMulti: the last n_ax workgroups form A x of many adapters instead of the
+// rows of one A past the rows of W (a.r = 0). Last, since they are short: first, they kept
+// the longer ones waiting (24 tokens 14.3 -> 13.8 us, 64 tokens of 11008 x 4096 52.8 -> 50.6)
 template <int TT, bool kMulti>
 __global__ __launch_bounds__(kSkThreads)
 void skinny_nf4(SkArgs a, NF4Tables tab, MultiAx m, int n_ax) {
@@ -174,12 +175,13 @@ void skinny_nf4(SkArgs a, NF4Tables tab, MultiAx m, int n_ax) {
     const int kq = wave >> 2;                      // block pairs kq, kq + KQ, ... of each slice
     if constexpr (kMulti) {
         static_assert((NW - 1) * TT * 64 <= TT * 16 * kSkBlk * 8, "the sums of A x fit the x buffer");
-        if (static_cast<int>(blockIdx.x) < n_ax) {
-            multi_ax_job<TT>(m, a, static_cast<int>(blockIdx.x), reinterpret_cast<f32x4*>(xs));
+        const int b = static_cast<int>(blockIdx.x) - (static_cast<int>(gridDim.x) - n_ax);
+        if (b >= 0) {
+            multi_ax_job<TT>(m, a, b, reinterpret_cast<f32x4*>(xs));
             return;
         }
     }
-    const int bid = static_cast<int>(blockIdx.x) - (kMulti ? n_ax : 0);
+    const int bid = static_cast<int>(blockIdx.x);
     const int row_blocks = a.d_out / kSkRows;
     const int all_blocks = row_blocks + (a.r + kSkRows - 1) / kSkRows;
     const int rb = bid % all_blocks;
