@@ -155,12 +155,37 @@ __device__ __forceinline__ float gemv_half_block(const uint4 c, const uint4* xv,
     return part;
 }
 
+// The same half block with the weights themselves, bf16(c[code] * a_hat) as the dequantiser
+// rounds them: the table holds float32 pairs (8 bytes, 32 copies: lanes l and l + 32 share one,
+// 32 lanes of 8 bytes fill all banks), lane8 = 8 (lane % 32), the pair of byte i of w at
+// byte << 8 | lane8. For a token whose adapter comes from a pool: those calls give every
+// token the weights of the large-batch path whatever the batch, where the bf16 code book
+// above is off by another rounding (relative error 0.0026 of a 4096 x 4096 call's output
+// against 0.0017).
+__device__ __forceinline__ float gemv_half_block_exact(const uint4 c, const uint4* xv, const char* lut, uint32_t lane8,
+                                                       float a) {
+    const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+    float part = 0.0f;
+#pragma unroll
+    for (int w4 = 0; w4 < 4; ++w4) {
+        const uint32_t xw[4] = {xv[w4].x, xv[w4].y, xv[w4].z, xv[w4].w};
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const float2 f = *reinterpret_cast<const float2*>(lut + lut_addr(cw[w4], lane8, b));
+            part = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, pack_bf16x2(f.x * a, f.y * a)),
+                                                   __builtin_bit_cast(bf16x2, xw[b]), part, false);
+        }
+    }
+    return part;
+}
+
 // position of 16-byte x chunk c of a segment in LDS: lane l = (c >> 2) & 63 reads
 // chunks 4 l .. 4 l + 3; their order is XORed with bits 2..3 of l
 __device__ __forceinline__ int gv_xpos(int c) { return (c & ~3) | ((c & 3) ^ ((c >> 4) & 3)); }
 
 // The adapter of the token, read on the device (kSel): A, B and s are then those of adapter
-// *adapter of a pool ([n, r, d_in], [n, d_out, r], [n]), and a negative one has no rank term.
+// *adapter of a pool ([n, r, d_in], [n, d_out, r], [n]), a negative one has no rank term, and
+// the weights are the dequantiser's (gemv_half_block_exact).
 struct GvSelect {
     const int32_t* adapter;
     const float* s;
@@ -290,8 +315,10 @@ void gemv_nf4_kernel(const uint4* __restrict__ codes, BlockConsts bc,
             hi = (pr >> 4) == i ? tab.code[i] : hi;
         }
         const uint32_t v = pack_bf16x2(lo, hi);
+        const uint4 e = kSel ? uint4{__float_as_uint(lo), __float_as_uint(hi), __float_as_uint(lo), __float_as_uint(hi)}
+                             : uint4{v, v, v, v};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) lut4[pr * (kLutCopies / 4) + (tid & 3) * 4 + c] = uint4{v, v, v, v};
+        for (int c = 0; c < 4; ++c) lut4[pr * (kLutCopies / 4) + (tid & 3) * 4 + c] = e;
         if (tid < 256) qlut[tid] = dq_step(bc.fmt, static_cast<int8_t>(tid - 128));      // T[q] at q + 128
     }
     stage_store(st, 0);
@@ -359,7 +386,8 @@ void gemv_nf4_kernel(const uint4* __restrict__ codes, BlockConsts bc,
                 uint4 xv[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) xv[e] = xs[kb][0][h * 256 + 4 * lane + (e ^ ((lane >> 2) & 3))];
-                acc[0] += a * gemv_half_block(g.cw[h], xv, lut, lane4);
+                if constexpr (kSel) acc[0] += gemv_half_block_exact(g.cw[h], xv, lut, (lane4 & 124u) << 1, a);
+                else acc[0] += a * gemv_half_block(g.cw[h], xv, lut, lane4);
             } else {
                 // one code-pair lookup per byte for all tokens; per token the same dot
                 // order as the single-token form
@@ -592,8 +620,10 @@ void gemv_nf4_persist(const uint4* __restrict__ codes, BlockConsts bc, int d_out
             hi = (pr >> 4) == i ? tab.code[i] : hi;
         }
         const uint32_t v = pack_bf16x2(lo, hi);
+        const uint4 e = kSel ? uint4{__float_as_uint(lo), __float_as_uint(hi), __float_as_uint(lo), __float_as_uint(hi)}
+                             : uint4{v, v, v, v};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) lut4[pr * (kLutCopies / 4) + (tid & 3) * 4 + c] = uint4{v, v, v, v};
+        for (int c = 0; c < 4; ++c) lut4[pr * (kLutCopies / 4) + (tid & 3) * 4 + c] = e;
         if (tid < 256) qlut[tid] = dq_step(bc.fmt, static_cast<int8_t>(tid - 128));
     }
 #pragma unroll
@@ -741,7 +771,8 @@ void gemv_nf4_persist(const uint4* __restrict__ codes, BlockConsts bc, int d_out
                 uint4 xv[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) xv[e] = xs[0][S * 512 + h * 256 + 4 * lane + (e ^ ((lane >> 2) & 3))];
-                acc[0] += a * gemv_half_block(cur.cw[h], xv, lut, lane4);
+                if constexpr (kSel) acc[0] += gemv_half_block_exact(cur.cw[h], xv, lut, (lane4 & 124u) << 1, a);
+                else acc[0] += a * gemv_half_block(cur.cw[h], xv, lut, lane4);
             } else {
                 const uint32_t cw[4] = {cur.cw[h].x, cur.cw[h].y, cur.cw[h].z, cur.cw[h].w};
                 float pt[T];

@@ -154,8 +154,21 @@ def test_forward(d_out, d_in, M, r, n, kind):
     assert torch.equal(Y.view(torch.int16), again.view(torch.int16))
 
 
+@pytest.mark.parametrize("d_out,d_in", [(4096, 4096), (4160, 1024), (256, 4160)])
+@pytest.mark.parametrize("M", [1, 5, 64, 80])
+def test_weights_are_the_dequantisers(d_out, d_in, M):
+    """Whatever path a batch takes, its weights are the dequantised bf16 ones: what is left
+    is the output's own rounding, 2^-8 / sqrt(3) = 0.0023 of a value at its binade's start
+    and half of that at its end, 0.0017 over values spread evenly in log, and the rank
+    sum's, the same share of a smaller part: 0.0021 holds both."""
+    _say(f"[multi] weights, {d_out}x{d_in}, {M} tokens")
+    L = Layer(d_out, d_in, M, 16, 3, "mixed", seed=M)
+    Y, ref = _f64(qn.multi_linear_fwd(L.q, L.pool, L.plan, L.X)), L.forward()
+    assert np.linalg.norm(Y - ref) <= 0.0021 * np.linalg.norm(ref)
+
+
 @pytest.mark.parametrize("dq", ["fp8", "none"])
-@pytest.mark.parametrize("M", [20, 150])
+@pytest.mark.parametrize("M", [1, 20, 150])
 def test_second_level_formats(dq, M):
     _say(f"[multi] second level {dq}, {M} tokens")
     L = Layer(256, 320, M, 16, 4, "mixed", seed=5, dq=dq)
