@@ -37,7 +37,7 @@ constexpr int kTopM = 127, kTopV = 255;          // code of 1.0
 constexpr int kOneBits = 0x3F800000 >> 20;       // 1.0f's pattern with 3 mantissa bits
 constexpr int kWaves = 4;
 
-// 32-bit mixer (finaliser of MurmurHash3, A. Appleby)
+// 32-bit mixer: three xor-shifts around two odd multipliers (A. Appleby's constants)
 __device__ __forceinline__ uint32_t mix32(uint32_t h) {
     h ^= h >> 16;
     h *= 0x85EBCA6Bu;
@@ -56,10 +56,14 @@ __device__ __forceinline__ int level_code(float x, float inv, uint32_t bits16, i
     return max(static_cast<int>(b >> 20) - (kOneBits - top), 0);
 }
 
-__device__ __forceinline__ float wave_max(float v) {
+// largest magnitude of a block, a NaN above all (the patterns of magnitudes order as integers)
+__device__ __forceinline__ float block_max(const float (&x)[4]) {
+    uint32_t b = 0;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-    return v;
+    for (int e = 0; e < 4; ++e) b = max(b, __float_as_uint(fabsf(x[e])));
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) b = max(b, static_cast<uint32_t>(__shfl_xor(static_cast<int>(b), o)));
+    return __uint_as_float(b);
 }
 
 __device__ __forceinline__ float bf16_val(uint32_t u) { return __uint_as_float(u << 16); }
@@ -202,21 +206,20 @@ void adamw_kernel(AdamArgs a, Coefs hc) {
                 v0 = e == 0 ? v[k].x : e == 1 ? v[k].y : e == 2 ? v[k].z : v[k].w;
             }
             const float ge = gv[e] * gs;
-            mo[e] = m0 * c.b1 + ge * c.c1;
-            vo[e] = v0 * c.b2 + (ge * ge) * c.c2;
+            const bool in = i + e < t.n;                       // past the end: zeros whatever the scales
+            mo[e] = in ? m0 * c.b1 + ge * c.c1 : 0.0f;
+            vo[e] = in ? v0 * c.b2 + (ge * ge) * c.c2 : 0.0f;
             const float den = sqrtf(vo[e]) * c.inv_root + a.eps;
             po[e] = pv[e] * c.keep - c.step_size * (mo[e] / den);
         }
         store4<kParamBf16>(t.p, i, t.n, whole, po);
         if (t.copy) store4<true>(t.copy, i, t.n, whole, po);
         if constexpr (k8) {
-            float bm = fmaxf(fmaxf(fabsf(mo[0]), fabsf(mo[1])), fmaxf(fabsf(mo[2]), fabsf(mo[3])));
-            float bv = fmaxf(fmaxf(vo[0], vo[1]), fmaxf(vo[2], vo[3]));
-            bm = wave_max(bm);
-            bv = wave_max(bv);
-            // a block whose largest magnitude is below the normal numbers is kept as zeros
-            const bool um = bm >= 0x1p-126f, uv = bv >= 0x1p-126f;
-            const float im = um ? 1.0f / bm : 0.0f, iv = uv ? 1.0f / bv : 0.0f;
+            const float bm = block_max(mo), bv = block_max(vo);
+            // a block whose largest magnitude is below the normal numbers is kept as zeros; one
+            // with an infinity or NaN keeps that as its scale, which no level makes finite
+            const bool um = !(bm < 0x1p-126f), uv = !(bv < 0x1p-126f);
+            const float im = bm >= 0x1p-126f ? 1.0f / bm : 0.0f, iv = bv >= 0x1p-126f ? 1.0f / bv : 0.0f;
             uint32_t wm = 0, wv = 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {

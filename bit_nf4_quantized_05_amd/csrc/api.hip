@@ -763,7 +763,8 @@ int check_multi(const uint8_t* codes, const int8_t* qconst, const float* qscale,
     if (!nf4_counts(d_out, d_in, &cnt, &n_b, &n_g)) return fail(-2, "weight too large");
     // the GEMM addresses each operand with 32-bit byte offsets
     const int64_t kMaxBytes = int64_t{1} << 32;
-    if (2 * cnt >= kMaxBytes || 2 * d_seq * std::max<int64_t>({ldx, ldo, bwd ? lddy : 0, r}) >= kMaxBytes ||
+    const int64_t ld = std::max<int64_t>({ldx, ldo, bwd ? lddy : 0, r});
+    if (2 * cnt >= kMaxBytes || ld >= kMaxBytes || 2 * d_seq * ld >= kMaxBytes ||
         2 * std::max(d_in, d_out) * r >= kMaxBytes)
         return fail(-2, "an operand reaches 4 GiB");
     *mw = multi_ws(d_out, d_in, d_seq, r, n, bwd);
@@ -890,6 +891,9 @@ int64_t qlora_adamw_table(void* const* p, const void* const* g, uint16_t* const*
     if (count > 0 && (!p || !g)) return fail(-1, "null pointer argument");
     if (flags & ~7) return fail(-1, "unknown flags");
     if (qlora_adamw_blocks(n, count) < 0) return -1;
+    int64_t need = 0;
+    for (int i = 0; i < count; ++i) need += (n[i] + qn::kAdamChunk - 1) / qn::kAdamChunk;
+    if (need > qn::kAdamMaxChunks) return fail(-1, "too many elements");
     const bool gb = flags & QN_ADAMW_GRAD_BF16, pb = flags & QN_ADAMW_PARAM_BF16;
     auto* t = static_cast<qn::AdamTensor*>(table);
     auto* c = reinterpret_cast<qn::AdamChunk*>(t + count);
@@ -906,7 +910,6 @@ int64_t qlora_adamw_table(void* const* p, const void* const* g, uint16_t* const*
         for (int64_t k = 0; k < nc; ++k) c[chunks + k] = qn::AdamChunk{i, static_cast<int32_t>(k)};
         chunks += nc;
     }
-    if (chunks > INT32_MAX) return fail(-1, "too many elements");
     return chunks;
 }
 
@@ -914,11 +917,11 @@ int qlora_adamw_step(const void* table, int count, int64_t n_chunks, int flags, 
                      float* v_scale, int64_t step, const int64_t* step_dev, double lr, const float* lr_dev,
                      double beta1, double beta2, double eps, double weight_decay, const float* grad_scale,
                      uint32_t seed, void* stream) {
-    if (count < 0 || n_chunks < 0 || n_chunks > INT32_MAX) return fail(-1, "bad tensor list");
+    if (count < 0 || n_chunks < 0 || n_chunks > qn::kAdamMaxChunks) return fail(-1, "bad tensor list");
     if (flags & ~7) return fail(-1, "unknown flags");
     const bool s8 = flags & QN_ADAMW_STATES_8;
     if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return fail(-1, "betas must be in [0, 1)");
-    if (!(eps > 0.0)) return fail(-1, "eps must be > 0");
+    if (!(static_cast<float>(eps) > 0.0f)) return fail(-1, "eps must be > 0 as a float32");
     if (!step_dev && step < 1) return fail(-1, "step must be >= 1");
     if (n_chunks == 0) return 0;
     if (!table || !m || !v || (s8 && (!m_scale || !v_scale))) return fail(-1, "null pointer argument");
@@ -940,7 +943,7 @@ int qlora_adamw_step(const void* table, int count, int64_t n_chunks, int flags, 
 
 int qlora_adamw_moments(const uint8_t* m, const float* m_scale, const uint8_t* v, const float* v_scale,
                         int64_t blocks, float* m_out, float* v_out, void* stream) {
-    if (blocks < 0 || blocks > (int64_t{1} << 32)) return fail(-1, "bad block count");
+    if (blocks < 0 || blocks > qn::kAdamMaxChunks * qn::kAdamChunkBlocks) return fail(-1, "bad block count");
     if (blocks == 0) return 0;
     if (!m || !m_scale || !v || !v_scale || !m_out || !v_out) return fail(-1, "null pointer argument");
     if (!aligned(m, 4) || !aligned(v, 4) || !aligned(m_scale, 4) || !aligned(v_scale, 4) || !aligned(m_out, 16) ||

@@ -112,9 +112,12 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
 
     // this tile's adapters: used[k0 .. k1), `steps` rank steps in all
     int2 kr = mg.plan.tile[tm];
-    if constexpr (kHalf) {                      // the adapters of this half alone
-        while (kr.x < kr.y && mg.plan.start[mg.plan.used[kr.x] + 1] <= m0) ++kr.x;
-        while (kr.x < kr.y && mg.plan.start[mg.plan.used[kr.y - 1]] >= m0 + BMT) --kr.y;
+    if constexpr (kHalf) {                      // the adapters of this half alone, counted by all threads
+        const int a = mg.plan.used[min(kr.x + tid, max(kr.y, 1) - 1)];
+        const bool in = kr.x + tid < kr.y;
+        const int before = __syncthreads_count(in && mg.plan.start[a + 1] <= m0);
+        const int after = __syncthreads_count(in && mg.plan.start[a] >= m0 + BMT);
+        kr = int2{kr.x + before, kr.y - after};
     }
     // a rank step holds 64 ranks: of one adapter, or of 2 or 4 adapters of 32 or 16 (8 << sh ranks
     // each); jsteps steps per adapter of more than 64

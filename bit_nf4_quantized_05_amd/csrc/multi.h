@@ -12,6 +12,7 @@ namespace qn {
 constexpr int kAdamBlock = 256;             // elements per state block (one wave, 4 per lane)
 constexpr int kAdamChunkBlocks = 4;         // blocks per workgroup
 constexpr int kAdamChunk = kAdamBlock * kAdamChunkBlocks;
+constexpr int64_t kAdamMaxChunks = (int64_t{1} << 24) - 1;        // a launch has under 2^32 threads
 
 // One tensor of a step's table; the table is an array of these, then one AdamChunk per
 // workgroup.
@@ -86,8 +87,8 @@ struct MultiPool {
 // ---- prologue.hip ----
 // Pre-passes of the multi-adapter calls, one launch: for every item and K-slice the fp32
 // partial s_a P[order[pos], kslice] R_a[r, kslice]^T into part[slice][pos][r]; R is [n, r, K]
-// row-major for the first product, [n, K, r] for the second (none if its R is null), and the double dequantisation of the weight
-// to what (transposed or not; null: none).
+// row-major for the first product, [n, K, r] for the second (none if its R is null), and
+// the double dequantisation of the weight to what (transposed or not; null: none).
 struct MultiPre { const uint16_t* P; int64_t ldp; int64_t K; const uint16_t* R; float* part; };
 hipError_t launch_multi_prologue(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
                                  bool transposed, uint16_t* what, const MultiPlan& plan, const float* s, int64_t M,
@@ -100,12 +101,12 @@ hipError_t launch_multi_reduce(int64_t M, int r, int pieces, const float* part0,
 
 // ---- gemm_multi.hip ----
 // C[order[pos], :] = bf16( P[order[pos], K] Q[N, K]^T + T[pos, r] R_a[N, r]^T ), R [n, N, r] or,
-// with rank_major, R_a^T given as [n, r, N]; a the adapter
-// of the position (no second term without one). part holds gemm_multi_part_floats floats.
+// with rank_major, R_a^T given as [n, r, N]; a the adapter of the
+// position (no second term without one). part holds gemm_multi_part_floats floats.
 int64_t gemm_multi_part_floats(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t K, const uint16_t* T,
-                             const uint16_t* R, bool rank_major, int r, const MultiPlan& plan, uint16_t* C, int64_t ldc, int64_t M,
-                             int64_t N, float* part, hipStream_t st);
+                             const uint16_t* R, bool rank_major, int r, const MultiPlan& plan,
+                             uint16_t* C, int64_t ldc, int64_t M, int64_t N, float* part, hipStream_t st);
 
 // ---- gemv.hip ----
 // One token with the adapter *adapter (none if negative) of a pool, in one launch: W_hat x +

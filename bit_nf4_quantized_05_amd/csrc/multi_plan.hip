@@ -78,6 +78,7 @@ void multi_plan_kernel(const int32_t* __restrict__ ids, int M, int n, int max_it
         const int key = id >= 0 && id < n ? id : n;
         const unsigned long long same = same_key(key, ok);
         if (ok && (same & below) == 0) row[key] += __popcll(same);       // the first lane of each id
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");           // seen by the next one's
     }
     __syncthreads();
     // thread k < n: adapter k (n <= 1024 threads)
@@ -126,12 +127,15 @@ void multi_plan_kernel(const int32_t* __restrict__ ids, int M, int n, int max_it
         const unsigned long long same = same_key(key, ok);
         int base = 0;
         if (ok) base = row[key];
-        // every lane has read its base before the first lane of each id moves it on
+        // every lane has read its base before the first lane of each id moves it on, and every
+        // lane sees that before its next read
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         if (ok) {
             out.order[base + __popcll(same & below)] = t + lane;
             if ((same & below) == 0) row[key] = base + __popcll(same);
         }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
     }
     // tile t covers positions [256 t, 256 t + 256): the adapters in use whose end lies past

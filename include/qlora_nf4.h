@@ -423,8 +423,9 @@ int qlora_multi_bwd(const uint8_t* codes, const int8_t* qconst, const float* qsc
  *     are added to the part cut off, so its mean is kept; a v > 0 has at least k = 1, m and
  *     v below a block's smallest level become 0 (v: level 1), a block whose largest value
  *     is below 2^-126 becomes zeros. The random bits of the element at state index e are
- *     the low (m) and high (v) halves of mix(e ^ mix(t ^ mix(seed))), mix being the 32-bit
- *     finaliser of MurmurHash3, e and t taken mod 2^32. p is formed from m, v before that.
+ *     the low (m) and high (v) halves of mix(e ^ mix(t ^ mix(seed))), e and t taken mod 2^32,
+ *     mix(h): h ^= h >> 16, h *= 0x85EBCA6B, h ^= h >> 13, h *= 0xC2B2AE35, h ^= h >> 16
+ *     (A. Appleby's constants). p is formed from m, v before that.
  * A NaN or infinite gradient makes its element's p, m, v non-finite (with 8-bit states the
  * moments of its whole block).
  */
@@ -440,7 +441,8 @@ int64_t qlora_adamw_blocks(const int64_t* n, int count);
 int64_t qlora_adamw_table_bytes(const int64_t* n, int count);
 /* Fills `table` (host memory, qlora_adamw_table_bytes bytes) from host arrays of `count`
  * device pointers and sizes; flags as for the step. Returns the number of chunks (what
- * qlora_adamw_step needs), or -1 (null or misaligned pointer, bad size or flags). */
+ * qlora_adamw_step needs), or -1 (null or misaligned pointer, bad size or flags, or 2^24
+ * chunks of 1024 elements and more). */
 int64_t qlora_adamw_table(void* const* p, const void* const* g, uint16_t* const* copy, const int64_t* n, int count,
                           int flags, void* table);
 /* One step. `table` is the device copy of the table for `count` tensors and `n_chunks`

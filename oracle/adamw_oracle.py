@@ -9,7 +9,7 @@ TINY = 2.0 ** -126            # smallest normal float32
 
 
 def mix32(h):
-    """Finaliser of MurmurHash3 on uint32 arrays."""
+    """The format's 32-bit mixer (three xor-shifts, two odd multipliers) on uint32 arrays."""
     h = np.array(h, dtype=np.uint32)
     h ^= h >> np.uint32(16)
     h *= np.uint32(0x85EBCA6B)

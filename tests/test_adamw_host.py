@@ -56,6 +56,13 @@ def test_table_entries_and_refusals():
     assert table(_ptrs(FAKE, FAKE), _ptrs(FAKE, FAKE), _ptrs(FAKE, FAKE + 1)) == -1
 
 
+def test_table_refuses_more_than_a_launch_holds():
+    n = _i64((1 << 34) - 1024 + 1)
+    buf = np.zeros(64, np.uint8)
+    assert _lib.lib().qlora_adamw_table(_at(_ptrs(FAKE)), _at(_ptrs(FAKE)), None, _at(n), 1, 0, buf.ctypes.data) == -1
+    assert b"too many" in _lib.lib().qn_last_error()
+
+
 def test_step_refusals_without_device_work():
     lib = _lib.lib()
 
@@ -69,7 +76,8 @@ def test_step_refusals_without_device_work():
 
     assert step(step=0) == -1
     assert step(b1=1.0) == -1 and step(b2=-0.1) == -1 and step(b1=float("nan")) == -1
-    assert step(eps=0.0) == -1
+    assert step(eps=0.0) == -1 and step(eps=1e-50) == -1            # 0 in float32
+    assert step(chunks=1 << 24) == -1
     assert step(m=None) == -1 and step(table=None) == -1
     assert step(flags=1) == -1                                       # 8-bit states without scales
     assert step(flags=16) == -1 and step(m=FAKE + 4) == -1 and step(chunks=-1) == -1

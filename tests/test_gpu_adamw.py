@@ -222,3 +222,67 @@ def test_set_grads():
     _run_and_check(st, [2])
     with pytest.raises(TypeError):
         st.set_grads([g.bfloat16() for g in grads])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_nonfinite_gradients_show(bits, value):
+    """An element of NaN or infinity: its own p, m and v with 32-bit moments (and no other's),
+    the moments of its block with 8-bit ones; no other block and no other parameter."""
+    _say(f"[adamw] gradient of {value}, bits={bits}")
+    n, at = 700, 300
+    g = torch.randn(n, generator=torch.Generator(device=dev()).manual_seed(11), device=dev())
+    g[at] = value
+    st = qn.adamw_state([torch.ones(n, device=dev())], [g], bits=bits)
+    qn.adamw_step(st, 1, LR)
+    m, v = qn.adamw_moments(st)
+    p = st.params[0]
+    fine = torch.ones(n, dtype=torch.bool, device=dev())
+    fine[at] = False
+    assert torch.isfinite(p[fine]).all() and not torch.isfinite(p[at])
+    if bits == 8:
+        fine[256:512] = False
+    for x in (m[:n], v[:n]):
+        assert torch.isfinite(x[fine]).all() and not torch.isfinite(x[~fine]).any()
+    qn.adamw_step(st, 2, LR)                     # and it stays
+    for x in qn.adamw_moments(st):
+        assert torch.isfinite(x[:n][fine]).all() and not torch.isfinite(x[:n][~fine]).any()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_state_past_a_tensor_stays_zero(bits):
+    """Also under a gradient scale that is not finite."""
+    _say(f"[adamw] padding, bits={bits}")
+    st = qn.adamw_state([torch.ones(300, device=dev()), torch.ones(1, device=dev())],
+                        [torch.ones(300, device=dev()), torch.ones(1, device=dev())], bits=bits)
+    for t, gs in enumerate((1.0, float("inf"), float("nan"))):
+        qn.adamw_step(st, t + 1, LR, grad_scale=torch.tensor([gs], device=dev()))
+        for x in (st.m, st.v):
+            assert torch.all(x[300:512] == 0) and torch.all(x[513:] == 0), gs
+
+
+def test_more_than_2_32_elements():
+    """Windows at both ends and around 2^31 and 2^32 of one tensor; moments within a level."""
+    _say("[adamw] 2^32 + 1000 elements")
+    n = 2 ** 32 + 1000
+    p = torch.zeros(n, dtype=torch.bfloat16, device=dev())
+    g = torch.zeros(n, dtype=torch.bfloat16, device=dev())
+    spans = [(0, 600), (2 ** 31 - 512, 2 ** 31 + 512), (2 ** 32 - 512, 2 ** 32 + 512), (n - 232, n)]
+    gen = torch.Generator(device=dev()).manual_seed(12)
+    for a, b in spans:
+        p[a:b] = torch.randn(b - a, generator=gen, device=dev()).bfloat16()
+        g[a:b] = torch.randn(b - a, generator=gen, device=dev()).bfloat16()
+    was = [(_f64(p[a:b]), _f64(g[a:b])) for a, b in spans]
+    st = qn.adamw_state([p], [g], bits=8)
+    qn.adamw_step(st, 1, LR, eps=EPS, weight_decay=WD)
+    torch.cuda.synchronize()
+    for (a, b), (p0, g0) in zip(spans, was):
+        want, m, v = O.step(p0, g0, 0.0, 0.0, 1, LR, eps=EPS, weight_decay=WD)
+        assert np.all(np.abs(_f64(p[a:b]) - want) <= 2.0 ** -8 * np.abs(want) + 1e-6), a
+        lo, hi = a // 256 * 256, -(-b // 256) * 256
+        blocks = slice(lo // 256, hi // 256)
+        for x, code, scale, signed, floor in ((m, st.m, st.m_scale, True, 2.0 ** -16), (v, st.v, st.v_scale, False, 2.0 ** -32)):
+            sc = scale[blocks].cpu().numpy()
+            have = O.decode(code[lo:hi].cpu().numpy(), sc, signed)[a - lo:b - lo]
+            assert np.all(np.abs(have - x) <= 0.13 * np.abs(x) + 1.3 * floor * sc.max()), a
+    assert st.m_scale[4:2 ** 23 - 4].count_nonzero() == 0

@@ -307,6 +307,57 @@ def test_gradients(d_out, d_in, M, r, n, kind):
         assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("M", [7, 64, 150])
+def test_gradients_against_differences(M):
+    """<dY, Y> is linear in each of X, A and B alone, so a whole step D of one of them moves it
+    by the gradient's product with D. Y's two roundings leave noise of 2^-8 / sqrt(3) per
+    element and call (test_weights_are_the_dequantisers), the rank sum's less: 5 deviations of
+    0.0024 sqrt(2) |dY Y| per element; dX's own roundings 0.0024 |dX D| per element."""
+    _say(f"[multi] gradients against differences, {M} tokens")
+    L = Layer(320, 256, M, 16, 3, "mixed", seed=40 + M)
+    dX, dA, dB = (_f64(g) for g in qn.multi_linear_bwd(L.q, L.pool, L.plan, L.X, L.dY))
+    dY, Y0 = _f64(L.dY), _f64(qn.multi_linear_fwd(L.q, L.pool, L.plan, L.X))
+    for what, t, grad in (("X", L.X, dX), ("A", L.pool.A, dA), ("B", L.pool.B, dB)):
+        was = t.clone()
+        t += (torch.randn(t.shape, generator=L.gen, device=dev()) * t.float().std()).bfloat16()
+        D = _f64(t) - _f64(was)
+        Y1 = _f64(qn.multi_linear_fwd(L.q, L.pool, L.plan, L.X))
+        t.copy_(was)
+        noise = 0.0024 * np.sqrt(np.sum((dY * Y0) ** 2) + np.sum((dY * Y1) ** 2) + np.sum((grad * D) ** 2))
+        assert abs(np.sum(dY * (Y1 - Y0)) - np.sum(grad * D)) <= 5 * noise, what
+
+
+def test_pool_of_more_than_2_32_elements():
+    """Adapters on both sides of element 2^31 and 2^32 of the pool and of dA."""
+    n, r, d_out, d_in = 1024, 64, 64, 65536 + 64
+    _say(f"[multi] pool of {n} adapters, r={r}, {d_in} features")
+    L = Layer(d_out, d_in, 80, r, 1, "one", seed=77)
+    A = torch.full((n, r, d_in), float("nan"), dtype=torch.bfloat16, device=dev())
+    B = torch.full((n, d_out, r), float("nan"), dtype=torch.bfloat16, device=dev())
+    who = [0, 510, 513, 1023]
+    for a in who:
+        A[a] = (torch.randn(r, d_in, generator=L.gen, device=dev()) * 0.02).bfloat16()
+        B[a] = (torch.randn(d_out, r, generator=L.gen, device=dev()) * 0.02).bfloat16()
+    pool = qn.AdapterPool(A, B, torch.ones(n, device=dev()))
+    ids = np.array(who, np.int32)[np.random.default_rng(7).integers(0, 4, 80)]
+    small = np.searchsorted(who, ids)
+    nA, nB, X, dY = _f64(A[who]), _f64(B[who]), _f64(L.X), _f64(L.dY)
+    for M in (5, 80):
+        plan = qn.multi_plan(torch.from_numpy(ids[:M].copy()).to(dev()), n)
+        Y = qn.multi_linear_fwd(L.q, pool, plan, L.X[:M])
+        check_close(_f64(Y), MO.forward(L.W, nA, nB, np.ones(4), small[:M], X[:M]), f"forward, {M} tokens")
+    gX, gA, gB = qn.multi_linear_bwd(L.q, pool, plan, L.X, L.dY)
+    wX, wA, wB = MO.backward(L.W, nA, nB, np.ones(4), small, X, dY)
+    check_close(_f64(gX), wX, "dX")
+    for k, a in enumerate(who):
+        assert np.linalg.norm(_f64(gA[a]) - wA[k]) <= 5e-6 * np.linalg.norm(wA[k]), a
+        # T sums 65600 products: sqrt(65600) 2^-24 = 1.5e-5
+        assert np.linalg.norm(_f64(gB[a]) - wB[k]) <= 3e-5 * np.linalg.norm(wB[k]), a
+        gA[a] = 0
+        gB[a] = 0
+    assert all(gA[i:i + 64].count_nonzero() == 0 for i in range(0, n, 64)) and gB.count_nonzero() == 0
+
+
 # ---- streams and graphs ---------------------------------------------------------------
 
 @pytest.mark.parametrize("M", [24, 300])

@@ -52,7 +52,8 @@ def _bwd(**kw):
                                       (dict(X=FAKE + 2), -1), (dict(plan=FAKE + 4), -1), (dict(ws=FAKE + 16), -1),
                                       (dict(dq=3), -1), (dict(r=8), -2), (dict(r=40), -2), (dict(n=1025), -2),
                                       (dict(d_in=96, ldx=96), -2), (dict(d_out=96, ldy=96), -2),
-                                      (dict(M=1 << 25, ldx=64), -2), (dict(bytes=64), -3)])
+                                      (dict(M=1 << 25, ldx=64), -2),
+                                      (dict(ldx=1 << 62), -2), (dict(M=(1 << 31) - 1, ldy=1 << 40), -2), (dict(bytes=64), -3)])
 def test_forward_refusals(bad, code):
     assert _fwd(**bad) == code
     assert _lib.lib().qn_last_error()
