@@ -703,7 +703,6 @@ namespace {
 
 struct MultiWs {
     int64_t what, pre0, pre1, t, u, gpart, grads, part, part_t, bytes;
-    int splits0, splits1;
 };
 
 // Workspace of a multi-adapter call; regions a call does not use have size 0.
@@ -717,13 +716,16 @@ MultiWs multi_ws(int64_t d_out, int64_t d_in, int64_t M, int r, int n, bool bwd)
         w.bytes = off;
         return w;
     }
-    w.splits0 = qn::prepass_split(M, d_in).splits;
-    w.splits1 = qn::prepass_split(M, d_out).splits;
+    // float32 sums of a pre-pass of several K-slices
+    auto pre = [&](int64_t K) {
+        const int sp = qn::multi_pre_split(M, K).splits;
+        return take(sp > 1 ? 4 * static_cast<int64_t>(sp) * M * r : 0);
+    };
     w.what = take(2 * d_out * d_in);                                                // W_hat or W_hat^T
-    w.pre0 = take(4 * static_cast<int64_t>(w.splits0) * M * r);                     // A x, K-split
+    w.pre0 = pre(d_in);                                                             // A x
     w.t = take(2 * (bwd ? 3 : 1) * M * r);                                          // T = s A x
     if (bwd) {
-        w.pre1 = take(4 * static_cast<int64_t>(w.splits1) * M * r);                 // B^T dy, K-split
+        w.pre1 = pre(d_out);                                                        // B^T dy
         w.u = take(2 * 3 * M * r);                                                  // U = s B^T dy
         w.grads = take(4 * qn::multi_grads_part_floats(d_out, d_in, M, n, r));      // dA, dB partials
     }
@@ -820,14 +822,12 @@ int qlora_multi_fwd(const uint8_t* codes, const int8_t* qconst, const float* qsc
         if (e != hipSuccess) return hip_fail(e, "qlora_multi_fwd (small batch)");
         return 0;
     }
-    if ((e = qn::launch_multi_prologue(codes, bc, d_out, d_in, false, u16(mw.what), pl, s, d_seq, n, r,
-                                       qn::MultiPre{X, ldx, d_in, A, f32(mw.pre0)}, qn::MultiPre{}, st)) != hipSuccess)
-        return hip_fail(e, "qlora_multi_fwd (prologue)");
-    if ((e = qn::launch_multi_reduce(d_seq, r, 1, f32(mw.pre0), mw.splits0, u16(mw.t), nullptr, 0, nullptr, st)) !=
+    if ((e = qn::launch_multi_prologue(codes, bc, d_out, d_in, false, u16(mw.what), pl, s, d_seq, n, r, 1,
+                                       qn::MultiPre{X, ldx, d_in, A, f32(mw.pre0), u16(mw.t)}, qn::MultiPre{}, st)) !=
         hipSuccess)
-        return hip_fail(e, "qlora_multi_fwd (A x)");
-    if ((e = qn::launch_gemm_multi(X, ldx, u16(mw.what), d_in, u16(mw.t), B, false, r, pl, Y, ldy, d_seq, d_out, f32(mw.gpart),
-                                   st)) != hipSuccess)
+        return hip_fail(e, "qlora_multi_fwd (prologue)");
+    if ((e = qn::launch_gemm_multi(X, ldx, u16(mw.what), d_in, u16(mw.t), B, false, r, pl, Y, ldy, d_seq, d_out,
+                                   f32(mw.gpart), st)) != hipSuccess)
         return hip_fail(e, "qlora_multi_fwd (gemm)");
     return 0;
 }
@@ -850,13 +850,10 @@ int qlora_multi_bwd(const uint8_t* codes, const int8_t* qconst, const float* qsc
     auto u16 = [&](int64_t off) { return reinterpret_cast<uint16_t*>(ws + off); };
     const qn::MultiPlan pl = qn::multi_plan_at(plan, d_seq, n);
     hipError_t e;
-    if ((e = qn::launch_multi_prologue(codes, bc, d_out, d_in, true, u16(mw.what), pl, s, d_seq, n, r,
-                                       qn::MultiPre{X, ldx, d_in, A, f32(mw.pre0)},
-                                       qn::MultiPre{dY, lddy, d_out, B, f32(mw.pre1)}, st)) != hipSuccess)
+    if ((e = qn::launch_multi_prologue(codes, bc, d_out, d_in, true, u16(mw.what), pl, s, d_seq, n, r, 3,
+                                       qn::MultiPre{X, ldx, d_in, A, f32(mw.pre0), u16(mw.t)},
+                                       qn::MultiPre{dY, lddy, d_out, B, f32(mw.pre1), u16(mw.u)}, st)) != hipSuccess)
         return hip_fail(e, "qlora_multi_bwd (prologue)");
-    if ((e = qn::launch_multi_reduce(d_seq, r, 3, f32(mw.pre0), mw.splits0, u16(mw.t), f32(mw.pre1), mw.splits1,
-                                     u16(mw.u), st)) != hipSuccess)
-        return hip_fail(e, "qlora_multi_bwd (A x, B^T dy)");
     if ((e = qn::launch_gemm_multi(dY, lddy, u16(mw.what), d_out, u16(mw.u), A, true, r, pl, dX, lddx, d_seq, d_in,
                                    f32(mw.gpart), st)) != hipSuccess)
         return hip_fail(e, "qlora_multi_bwd (gemm)");

@@ -21,10 +21,10 @@
 // meets its own adapter: zeros in place of the other rows would let an infinity or NaN in
 // one adapter's weights reach its neighbours' tokens, and this costs fewer MFMAs besides.
 //
-// The last round of tiles. With at most 64 tiles past a multiple of the 256 CUs their K-steps
-// are split as in the single-adapter GEMM (gemm_split), and so are their adapters (256 tokens
-// of 256 users, 16 tiles: 64 rank steps of 2.6 us would stand in one split's way);
-// gemm_multi_reduce adds the partials. With 65 to 128 they are taken as twice as many
+// The last round of tiles. Few tiles past a multiple of the 256 CUs, with a long K, have their
+// K-steps split as in the single-adapter GEMM (gemm_split), and so are their adapters (256 tokens
+// of 256 users, 16 tiles: 64 rank steps of 2.6 us would stand in one split's way); up to 128
+// otherwise run as (the rule stands at half_tiles)
 // half tiles of 128 x 256, whole in K, which writes and reads back no partials: a half tile's
 // step takes 0.6 of a whole one's (4 LDS reads for 4 MFMAs, not 6 for 8), more than half, so
 // whole tiles stay the rule (4096 x 4096 at 4096 tokens: 119 us whole, 133 us in halves).
@@ -498,15 +498,24 @@ void gemm_multi_reduce(MultiGemm mg) {
 }  // namespace
 
 namespace {
-// tiles past a multiple of 256 that are taken as half tiles
-int half_tiles(int64_t M, int64_t N) {
+// Tiles past a multiple of 256 that are taken as half tiles (0: none). Of at most 128 such
+// tiles a half tile takes 0.6 of a whole step per K-step; split in s, a tile takes 1/s of
+// them and the launch that adds the partials 8 steps (of 1.5 us) and one for every 14
+// partials of 256 KB. (rem tiles, K-steps, s: half against split, whole calls. 16, 16, 2:
+// 25.5 against 35.3 us; 16, 32, 4: 36.3, 37.1; 64, 64, 4: 64.8, 70.3; 32, 64, 4: 70.5, 64.0;
+// 16, 64, 4: 62.8, 49.3.)
+int half_tiles(int64_t M, int64_t N, int64_t K) {
     const int64_t rem = (M + BM - 1) / BM * ((N + BN - 1) / BN) % 256;
-    return rem > 64 && rem <= 128 ? static_cast<int>(rem) : 0;
+    if (rem > 128) return 0;
+    const int s = gemm_split(M, N, K).splits;
+    const double steps = static_cast<double>(K / BK);
+    const bool half = s <= 1 || 0.6 * steps <= steps / s + 8.0 + rem * s / 14.0;
+    return half ? static_cast<int>(rem) : 0;
 }
 }  // namespace
 
 int64_t gemm_multi_part_floats(int64_t M, int64_t N, int64_t K) {
-    return half_tiles(M, N) ? 0 : gemm_split_part_floats(M, N, K);
+    return half_tiles(M, N, K) ? 0 : gemm_split_part_floats(M, N, K);
 }
 
 hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t K, const uint16_t* T,
@@ -528,7 +537,7 @@ hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, 
         if (rank_major) QN_LAUNCH(#KERNEL "_dx", st, KERNEL##_dx, dim3(GRID), dim3(kNT), 0, st, mg);     \
         else QN_LAUNCH(#KERNEL, st, KERNEL, dim3(GRID), dim3(kNT), 0, st, mg);                          \
     } while (0)
-    if (const int rem = half_tiles(M, N); rem > 0) {
+    if (const int rem = half_tiles(M, N, K); rem > 0) {
         g.full = tiles - rem;
         g.rem = rem;
         if (g.full > 0) QN_GEMM(gemm_multi_mixed, g.full + 2 * rem);

@@ -85,19 +85,21 @@ struct MultiPool {
 };
 
 // ---- prologue.hip ----
-// Pre-passes of the multi-adapter calls, one launch: for every item and K-slice the fp32
-// partial s_a P[order[pos], kslice] R_a[r, kslice]^T into part[slice][pos][r]; R is [n, r, K]
-// row-major for the first product, [n, K, r] for the second (none if its R is null), and
-// the double dequantisation of the weight to what (transposed or not; null: none).
-struct MultiPre { const uint16_t* P; int64_t ldp; int64_t K; const uint16_t* R; float* part; };
+// Pre-passes of the multi-adapter calls and the double dequantisation of the weight to what
+// (transposed or not; null: none) in one launch: T[piece][pos][r] = s_a P[order[pos], K]
+// R_a[r, K]^T in `pieces` bf16 terms (1: rounded once; 3: the remainders too, 24 bits in all),
+// R [n, r, K] for the first product, [n, K, r] for the second (none if its R is null). K is
+// cut in multi_pre_split(M, K).splits slices; with more than one, part holds their float32
+// sums [slice][pos][r] and a second launch adds them in slice order.
+struct MultiPre { const uint16_t* P; int64_t ldp; int64_t K; const uint16_t* R; float* part; uint16_t* T; };
+// A short K is one slice: the second launch costs 4.8 us, a K-chunk of 64 about 0.4 us (backward
+// of 203 tokens on 512 x 512: 29.3 us against 29.9 in two slices; on 1024 x 1024, where K
+// stays in four: 35.4 against 37.8 in one).
+constexpr int64_t kMultiWholeK = 512;
+PrepassSplit multi_pre_split(int64_t M, int64_t K);
 hipError_t launch_multi_prologue(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
                                  bool transposed, uint16_t* what, const MultiPlan& plan, const float* s, int64_t M,
-                                 int n, int r, const MultiPre& p0, const MultiPre& p1, hipStream_t st);
-// T[piece][pos][r] = the slice partials added in slice order, in `pieces` bf16 terms (1:
-// rounded once; 3: the remainders too, 24 bits in all), for one or two products (part1
-// null: one)
-hipError_t launch_multi_reduce(int64_t M, int r, int pieces, const float* part0, int splits0,
-                               uint16_t* T0, const float* part1, int splits1, uint16_t* T1, hipStream_t st);
+                                 int n, int r, int pieces, const MultiPre& p0, const MultiPre& p1, hipStream_t st);
 
 // ---- gemm_multi.hip ----
 // C[order[pos], :] = bf16( P[order[pos], K] Q[N, K]^T + T[pos, r] R_a[N, r]^T ), R [n, N, r] or,

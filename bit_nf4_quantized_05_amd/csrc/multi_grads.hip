@@ -14,7 +14,8 @@
 // transposing reads hand each lane 4 consecutive rows of a column, the MFMA's K order. A slice is `per` items (128 positions each)
 // of the plan. An adapter whose tokens fit one slice is written to dA, dB at once; the others
 // leave one partial per slice, added in slice order by multi_grad_reduce, which also writes
-// the zeros of adapters without tokens. Deterministic; rows of other adapters count nowhere.
+// the zeros of adapters without tokens. A batch of up to 512 tokens is one slice per adapter,
+// its last workgroups write the zeros, and there is no second launch. Deterministic; rows of other adapters count nowhere.
 // Slice s of adapter a has slot first_item[a] / per + a + s: a's ceil(items / per) slots end
 // before the next adapter's begin, and there are at most items / per + n of them.
 // Bound by the reads of dY and X and, with many slices, of the partials.
@@ -49,6 +50,7 @@ struct GradArgs {
     GradJob job[2];                  // 0: dB (P = dY), 1: dA (P = X)
     MultiPlan plan;
     int M, r, jchunks, max_items, per;
+    int zero_at, zero_blocks;        // workgroups from zero_at on: zeros, zero_blocks per adapter
 };
 
 // 16-byte piece c of row m sits at c ^ swz(m), so that the 4 rows of a transposing read fall in
@@ -147,6 +149,23 @@ __device__ __forceinline__ void grad_compute(const GradTile<JB>& t, int wave, in
 #undef QN_TR4
 #undef QN_TR
 
+constexpr int kZero = 4096;          // elements of dB_a, dA_a per workgroup that writes zeros
+
+// zeros for an adapter without tokens: chunk c of its dB_a, then dA_a (sizes multiples of 1024)
+__device__ __forceinline__ void zero_job(const GradArgs& g, int b) {
+    const int a = b / g.zero_blocks;
+    if (g.plan.start[a + 1] > g.plan.start[a]) return;
+    const int64_t n0 = g.job[0].N * g.r, n1 = g.job[1].N * g.r;
+    const int64_t at = static_cast<int64_t>(b % g.zero_blocks) * kZero + 4 * threadIdx.x;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int64_t i = at + 1024 * q;
+        if (i >= n0 + n1) return;
+        float* p = i < n0 ? g.job[0].out + a * n0 + i : g.job[1].out + a * n1 + (i - n0);
+        *reinterpret_cast<float4*>(p) = float4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+}
+
 template <int JB>   // 32-wide rank blocks per workgroup: 1 (r <= 32) or 2
 __global__ __launch_bounds__(256)
 void multi_grad_mfma(GradArgs g) {
@@ -155,6 +174,10 @@ void multi_grad_mfma(GradArgs g) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     int b = static_cast<int>(blockIdx.x);
+    if (b >= g.zero_at) {
+        zero_job(g, b - g.zero_at);
+        return;
+    }
     const int nb0 = g.job[0].tiles * g.max_items * g.jchunks;
     const bool second = b >= nb0;
     const GradJob jb = second ? g.job[1] : g.job[0];
@@ -294,7 +317,13 @@ int jchunks_of(int r) { return (r + kGJ - 1) / kGJ; }
 // at most 1024 positions a slice. (256 of twice the length: 31 against 23 us on 4096 x 4096,
 // 4096 tokens, r = 16, and 39 against 34 us on 11008 + 4096 columns, 2048 tokens, r = 64, whose
 // partials then take 8 instead of 12 us; 1024 of half of it: 26 us for the partials there.)
+// Up to 512 tokens one slice per adapter: a second launch costs 4.9 us, a step of 32 positions
+// about 0.4 us (203 tokens of 3 adapters on 256 x 256 23.4 us against 24.7, 512 of 8 on 4096 x
+// 4096 with r = 64 73.5 against 76.1; 512 of a single adapter on 1024 x 1024 45.5 against 41.1,
+// but how the tokens are spread is not known on the host).
+constexpr int64_t kOneSlice = 512;
 int per_of(int64_t d_out, int64_t d_in, int64_t M, int r) {
+    if (M <= kOneSlice) return static_cast<int>((M + kMultiItem - 1) / kMultiItem);
     const int64_t tiles = ((d_out + kGCols - 1) / kGCols + (d_in + kGCols - 1) / kGCols) * jchunks_of(r);
     const int64_t items = (M + kMultiItem - 1) / kMultiItem;
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kMaxPer, items * tiles / 512)));
@@ -309,7 +338,7 @@ int64_t slots_of(int64_t d_out, int64_t d_in, int64_t M, int n, int r) {
 }  // namespace
 
 int64_t multi_grads_part_floats(int64_t d_out, int64_t d_in, int64_t M, int n, int r) {
-    return slots_of(d_out, d_in, M, n, r) * (d_out + d_in) * r;
+    return M <= kOneSlice ? 0 : slots_of(d_out, d_in, M, n, r) * (d_out + d_in) * r;
 }
 
 hipError_t launch_multi_grads(const MultiPlan& plan, const uint16_t* X, int64_t ldx, const uint16_t* dY, int64_t lddy,
@@ -323,9 +352,13 @@ hipError_t launch_multi_grads(const MultiPlan& plan, const uint16_t* X, int64_t 
     auto tiles = [](int64_t N) { return static_cast<int>((N + kGCols - 1) / kGCols); };
     g.job[0] = GradJob{dY, d_out, lddy, T, part, dB, 0, tiles(d_out)};
     g.job[1] = GradJob{X, d_in, ldx, U, part + slots_of(d_out, d_in, M, n, r) * d_out * r, dA, 1, tiles(d_in)};
-    const dim3 grid(static_cast<unsigned>((g.job[0].tiles + g.job[1].tiles) * g.max_items * g.jchunks));
+    g.zero_at = (g.job[0].tiles + g.job[1].tiles) * g.max_items * g.jchunks;
+    g.zero_blocks = static_cast<int>(((d_out + d_in) * r + kZero - 1) / kZero);
+    const bool whole = M <= kOneSlice;
+    const dim3 grid(static_cast<unsigned>(whole ? g.zero_at + n * g.zero_blocks : g.zero_at));
     if (r <= 32) QN_LAUNCH("multi_grad_mfma", st, multi_grad_mfma<1>, grid, dim3(256), 0, st, g);
     else QN_LAUNCH("multi_grad_mfma", st, multi_grad_mfma<2>, grid, dim3(256), 0, st, g);
+    if (whole) return hipGetLastError();
     const int b0 = static_cast<int>(d_out / 64 * (r / 16)), b1 = static_cast<int>(d_in / 64 * (r / 16));
     QN_LAUNCH("multi_grad_reduce", st, multi_grad_reduce, dim3(static_cast<unsigned>(b0 + b1), static_cast<unsigned>(n)),
               dim3(256), 0, st, g, b0);

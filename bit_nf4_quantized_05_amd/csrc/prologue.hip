@@ -436,7 +436,7 @@ void prologue_kernel(PrologueArgs a, NF4Tables tab) {
 // most 128 positions of one adapter) and one K-slice, with the stages and fragments of
 // the pre-pass above; only the token rows are gathered, each lane keeping the addresses
 // of the 4 rows it fetches. Every slice writes its fp32 partial, already times s_a, and
-// multi_reduce adds them. Work is proportional to the tokens of each adapter rounded up
+// multi_reduce adds them; of a single slice (multi_pre_split) T itself is written. Work is proportional to the tokens of each adapter rounded up
 // to 128, whatever the number of adapters in the pool; items past the plan's count (the
 // grid is sized for the worst case) end at once. Bound by the reads of P (each row once)
 // and, with many adapters of few tokens, of R (each adapter once per 128 tokens).
@@ -445,14 +445,31 @@ struct MultiPreJob {
     const uint16_t* P; int64_t ldp; int K;
     const uint16_t* R;               // [n, r, K] (job 0) or [n, K, r] (job 1)
     float* part;                     // [psplits][M][r]
+    uint16_t* T;                     // or, of one slice, T itself
     int psplits, kper, n;            // K-slices, 64-wide K-chunks per slice, workgroups
 };
+
+// 4 neighbouring values of T as 1 or 3 bf16 terms, `stride` elements apart
+__device__ __forceinline__ void store_terms(const float4& t, int pieces, uint16_t* T, int64_t stride) {
+    float v[4] = {t.x, t.y, t.z, t.w};
+    for (int p = 0; p < pieces; ++p) {
+        uint16_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            h[e] = bf16_bits(v[e]);
+            const float f = bf16_to_f32(h[e]);
+            v[e] = fabsf(f) < __builtin_inff() ? v[e] - f : 0.0f;      // nothing is left of an infinity or NaN
+        }
+        *reinterpret_cast<uint2*>(T + p * stride) =
+            uint2{h[0] | (static_cast<uint32_t>(h[1]) << 16), h[2] | (static_cast<uint32_t>(h[3]) << 16)};
+    }
+}
 
 struct MultiPrologueArgs {
     PrologueArgs d;                  // the dequantisation's fields, M, r
     MultiPreJob pre[2];
     MultiPlan plan; const float* s;
-    int max_items;
+    int max_items, pieces;
 };
 
 // kMajor: R is [K, r] per adapter (B_a of the backward), fetched as 64 k-rows of 32 NT ranks
@@ -553,15 +570,17 @@ __device__ __forceinline__ void multi_pre_job(const MultiPreJob& j, const MultiP
     const int row = 32 * wave + (lane & 31);
     if (row >= count) return;
     const float s = a.s[it.adapter];
-    float* out = j.part + (static_cast<int64_t>(sp) * a.d.M + it.pos + row) * r;
+    const int64_t mr = static_cast<int64_t>(a.d.M) * r, at = static_cast<int64_t>(it.pos + row) * r;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
         for (int gq = 0; gq < 4; ++gq) {
             const int n = t * 32 + 8 * gq + 4 * (lane >> 5);          // r % 16 == 0: 4 ranks in or out together
-            if (n < r)
-                *reinterpret_cast<float4*>(out + n) = float4{s * acc[t][4 * gq], s * acc[t][4 * gq + 1],
-                                                             s * acc[t][4 * gq + 2], s * acc[t][4 * gq + 3]};
+            if (n >= r) continue;
+            const float4 v = float4{s * acc[t][4 * gq], s * acc[t][4 * gq + 1], s * acc[t][4 * gq + 2],
+                                    s * acc[t][4 * gq + 3]};
+            if (j.T) store_terms(v, a.pieces, j.T + at + n, mr);
+            else *reinterpret_cast<float4*>(j.part + sp * mr + at + n) = v;
         }
     }
 }
@@ -579,18 +598,7 @@ void multi_reduce(MultiReduceJob j0, MultiReduceJob j1, int blocks0, int64_t M, 
     const int64_t total = M * r;
     if (idx >= total) return;
     const float4 t = ordered_sum4<8>(jb.part + idx, total, jb.splits);
-    float v[4] = {t.x, t.y, t.z, t.w};
-    for (int p = 0; p < pieces; ++p) {
-        uint16_t h[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            h[e] = bf16_bits(v[e]);
-            const float f = bf16_to_f32(h[e]);
-            v[e] = fabsf(f) < __builtin_inff() ? v[e] - f : 0.0f;      // nothing is left of an infinity or NaN
-        }
-        *reinterpret_cast<uint2*>(jb.T + p * total + idx) =
-            uint2{h[0] | (static_cast<uint32_t>(h[1]) << 16), h[2] | (static_cast<uint32_t>(h[3]) << 16)};
-    }
+    store_terms(t, pieces, jb.T + idx, total);
 }
 #undef QN_PRE_BARRIER
 
@@ -846,20 +854,25 @@ hipError_t launch_prepass_pair(const uint16_t* P0, int64_t ldp0, int64_t K0, con
     return launch_prologue_args(a, false, r1_kmajor, st);
 }
 
+PrepassSplit multi_pre_split(int64_t M, int64_t K) {
+    if (K <= kMultiWholeK) return PrepassSplit{1, static_cast<int>(K / 64)};
+    return prepass_split(M, K);
+}
+
 hipError_t launch_multi_prologue(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
                                  bool transposed, uint16_t* what, const MultiPlan& plan, const float* s, int64_t M,
-                                 int n, int r, const MultiPre& p0, const MultiPre& p1, hipStream_t st) {
+                                 int n, int r, int pieces, const MultiPre& p0, const MultiPre& p1, hipStream_t st) {
     MultiPrologueArgs a{};
     a.d.codes = codes; a.d.bc = bc; a.d.M = static_cast<int>(M); a.d.r = r;
     set_dequant(a.d, d_out, d_in, transposed, what);
-    a.plan = plan; a.s = s;
+    a.plan = plan; a.s = s; a.pieces = pieces;
     a.max_items = static_cast<int>(multi_max_items(M, n));
     const MultiPre* in[2] = {&p0, &p1};
     for (int i = 0; i < 2; ++i) {
         if (in[i]->R == nullptr) continue;
-        const PrepassSplit ps = prepass_split(M, in[i]->K);
-        a.pre[i] = MultiPreJob{in[i]->P, in[i]->ldp, static_cast<int>(in[i]->K), in[i]->R, in[i]->part, ps.splits,
-                               ps.kper, a.max_items * ps.splits};
+        const PrepassSplit ps = multi_pre_split(M, in[i]->K);
+        a.pre[i] = MultiPreJob{in[i]->P, in[i]->ldp, static_cast<int>(in[i]->K), in[i]->R, in[i]->part,
+                               ps.splits == 1 ? in[i]->T : nullptr, ps.splits, ps.kper, a.max_items * ps.splits};
     }
     const dim3 grid(static_cast<unsigned>(a.pre[0].n + a.pre[1].n + a.d.n_deq));
     const NF4Tables& tab = tables();
@@ -871,15 +884,16 @@ hipError_t launch_multi_prologue(const uint8_t* codes, const BlockConsts& bc, in
 #undef QN_PRO_CASE
         default: return hipErrorInvalidValue;
     }
-    return hipGetLastError();
-}
-
-hipError_t launch_multi_reduce(int64_t M, int r, int pieces, const float* part0, int splits0,
-                               uint16_t* T0, const float* part1, int splits1, uint16_t* T1, hipStream_t st) {
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    // the products of several slices
+    MultiReduceJob jobs[2];
+    int count = 0;
+    for (int i = 0; i < 2; ++i)
+        if (a.pre[i].psplits > 1) jobs[count++] = MultiReduceJob{a.pre[i].part, in[i]->T, a.pre[i].psplits};
+    if (count == 0) return hipSuccess;
     const int blocks = static_cast<int>((M * r / 4 + 255) / 256);
-    const MultiReduceJob j0{part0, T0, splits0}, j1{part1, T1, splits1};
-    QN_LAUNCH("multi_reduce", st, multi_reduce, dim3(static_cast<unsigned>(part1 ? 2 * blocks : blocks)), dim3(256), 0,
-              st, j0, j1, blocks, M, r, pieces);
+    QN_LAUNCH("multi_reduce", st, multi_reduce, dim3(static_cast<unsigned>(count * blocks)), dim3(256), 0, st, jobs[0],
+              jobs[count - 1], blocks, M, r, pieces);
     return hipGetLastError();
 }
 

@@ -24,7 +24,7 @@ def test_sizes():
     assert qn.multi_linear_fwd_workspace_bytes(4096, 4096, 64, 16, 8) < 2 * 4096 * 4096
     assert qn.multi_linear_fwd_workspace_bytes(4096, 4096, 65, 16, 8) > 2 * 4096 * 4096
     # the backward keeps gradient partials that grow with the pool
-    few, many = (qn.multi_linear_bwd_workspace_bytes(256, 256, 200, 16, n) for n in (1, 101))
+    few, many = (qn.multi_linear_bwd_workspace_bytes(256, 256, 2000, 16, n) for n in (1, 101))
     assert many - few >= 100 * 2 * 16 * 512
 
 
