@@ -17,19 +17,21 @@
 // ranks a step (4 adapters of rank 16, 2 of 32), double-buffered in the same stages (the first
 // one's loads go out under the last main step). A 32-row MFMA tile skips an adapter that has
 // none of its rows, adds straight to its accumulators when all 32 rows are the adapter's, and
-// otherwise forms the product apart and adds it where the lane's row is the adapter's. So a row only ever
-// meets its own adapter: zeros in place of the other rows would let an infinity or NaN in
+// otherwise forms the product apart and adds it where the lane's row is the adapter's. So a row
+// only ever meets its own adapter: zeros in place of the other rows would let an infinity or NaN in
 // one adapter's weights reach its neighbours' tokens, and this costs fewer MFMAs besides.
 //
-// The last round of tiles. Few tiles past a multiple of the 256 CUs, with a long K, have their
-// K-steps split as in the single-adapter GEMM (gemm_split), and so are their adapters (256 tokens
-// of 256 users, 16 tiles: 64 rank steps of 2.6 us would stand in one split's way); up to 128
-// otherwise run as (the rule stands at half_tiles)
-// half tiles of 128 x 256, whole in K, which writes and reads back no partials: a half tile's
-// step takes 0.6 of a whole one's (4 LDS reads for 4 MFMAs, not 6 for 8), more than half, so
-// whole tiles stay the rule (4096 x 4096 at 4096 tokens: 119 us whole, 133 us in halves).
+// The last round of tiles, at most 128 past a multiple of the 256 CUs, as whole tiles would
+// leave half the CUs idle (last_tiles has the rule):
+//   half tiles of 128 x 256: a half tile's step takes 0.6 of a whole one's (4 LDS reads for 4
+//   MFMAs, not 6 for 8), more than half, so whole tiles stay the rule (4096 x 4096 at 4096
+//   tokens: 119 us whole, 133 us in halves);
+//   K split in up to 16, gemm_multi_reduce adding the partials, and so are the adapters (256
+//   tokens of 256 users, 16 tiles: 64 rank steps of 2.6 us would stand in one split's way).
+//   Each XCD takes a run of neighbouring tiles of one slice: dealt out in turn, 800 x 11008 x
+//   4096 took 166 us in place of 112.
 // Alone they run on three stages of 48 KB, whose loads have two steps to arrive (1531 x 4096
-// x 4096, 96 tiles: 66 us; two stages 73; split in two 77 and 13 for the sums); after whole
+// x 4096, 96 tiles: 59 us; two stages 73; whole, split in two 77 and 13 for the sums); after whole
 // tiles, in the same launch, on the two stages of those (11008 columns of 2048 tokens, 256 +
 // 88 tiles: 174 us; in two launches 124 + 58; split 170 + 12).
 // Dealing the last tiles' steps out evenly over all CUs, parts joined by the last workgroup
@@ -62,6 +64,7 @@ __shared__ int g_hi[BM];
 
 constexpr int kWM = 2, kWN = 4;                 // waves
 constexpr int kNT = 64 * kWM * kWN;             // threads
+constexpr int kMaxSplits = 16;                  // of a tile's K-steps
 
 struct MultiGemm {
     GemmArgs g;                                 // P, Q, C, sizes, splits
@@ -78,13 +81,13 @@ struct MultiGemm {
         __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);      \
     }
 
-// BMT rows per tile: 256, or 128 (the two halves of each of the last g.rem tiles); kThree: half
-// tiles on three LDS stages
+// BMT rows per tile: 256, or 128. Half tiles are the two halves of each of the last g.rem tiles
+// or, alone on three LDS stages (kThree), g.rem tiles of their own raster (g.tiles_m rows of 128)
 template <int BMT, bool kSplit, bool kThree, bool kRankMajor>
 __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
     const GemmArgs& g = mg.g;
     constexpr bool kHalf = BMT < BM;
-    static_assert(!(kHalf && kSplit), "half tiles are whole in K");
+    static_assert(!(kHalf && kSplit) || kThree, "half tiles split in K are alone");
     static_assert(kHalf || !kThree, "three stages hold half tiles only");
     constexpr int TM = BMT / kWM / 32;          // 4 (2) m sub-tiles per wave
     constexpr int TN = BN / kWN / 32;           // 2 n sub-tiles
@@ -99,19 +102,25 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
     const int M = g.M, N = g.N;
 
     const bool split_wg = kSplit && bid >= g.full;
-    const int T = kHalf ? 2 * g.rem : g.full;           // workgroups of this kind
-    const int w = split_wg ? 0 : bid;
-    const int sj = split_wg ? bid - g.full : 0;
-    const int sk = split_wg ? sj / g.rem : 0;
-    const int place = (T % 8 == 0) ? (w & 7) * (T >> 3) + (w >> 3) : w;
-    const int logical = split_wg ? g.full + sj % g.rem : kHalf ? g.full + place / 2 : place;
+    const int T = kHalf && !kThree ? 2 * g.rem : split_wg || kThree ? g.rem : g.full;   // tiles of this kind
+    // Workgroups go to the 8 XCDs in turn: each takes a run of neighbouring tiles (of one
+    // K-slice after the other), whose rows of P and Q its L2 then holds for all of them
+    // (g.full is a multiple of 256 here; past the last slice: nothing)
+    const int w = split_wg ? bid - g.full : bid;
+    const int units = split_wg ? T * g.splits : T;
+    const int run = split_wg ? (units + 7) >> 3 : units >> 3;
+    const int u = split_wg || T % 8 == 0 ? (w & 7) * run + (w >> 3) : w;
+    if (split_wg && u >= units) return;
+    const int sk = split_wg ? u / T : 0;
+    const int place = split_wg ? u % T : u;
+    const int logical = kHalf && !kThree ? g.full + place / 2 : split_wg ? g.full + place : place;
     int tm, tn;
     tile_coords(g, logical, tm, tn);
-    const int m0 = tm * BM + (kHalf ? (place & 1) * BMT : 0), n0 = tn * BN;
-    if (kHalf && m0 >= M) return;
+    const int m0 = kThree ? tm * BMT : tm * BM + (kHalf ? (place & 1) * BMT : 0), n0 = tn * BN;
+    if (kHalf && !kThree && m0 >= M) return;
 
     // this tile's adapters: used[k0 .. k1), `steps` rank steps in all
-    int2 kr = mg.plan.tile[tm];
+    int2 kr = mg.plan.tile[m0 / BM];
     if constexpr (kHalf) {                      // the adapters of this half alone, counted by all threads
         const int a = mg.plan.used[min(kr.x + tid, max(kr.y, 1) - 1)];
         const bool in = kr.x + tid < kr.y;
@@ -395,10 +404,11 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
     }
 
     if (split_wg) {
-        float* pt = g.part + (static_cast<int64_t>(sk) * g.rem + sj % g.rem) * (BM * BN);
+        float* pt = g.part + (static_cast<int64_t>(sk) * T + place) * (BMT * BN);
 #pragma unroll
         for (int b = 0; b < TM; ++b) {
             const int ml = wm * (TM * 32) + b * 32 + static_cast<int>(frow);
+            if (m0 + ml >= M) continue;
 #pragma unroll
             for (int a = 0; a < TN; ++a) {
 #pragma unroll
@@ -452,6 +462,7 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
 //   split   whole tiles, then the last ones split in K
 //   mixed   whole tiles, then the last ones as half tiles on the same two stages
 //   half    half tiles alone, on three stages
+//   half_split  these split in K
 #define QN_MULTI_KERNELS(SUFFIX, RANK_MAJOR)                                                          \
     __global__ __launch_bounds__(kNT, 1) void gemm_multi_kernel##SUFFIX(MultiGemm mg) {                \
         gemm_multi_body<BM, false, false, RANK_MAJOR>(mg, static_cast<int>(blockIdx.x));               \
@@ -466,56 +477,74 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
     }                                                                                                 \
     __global__ __launch_bounds__(kNT, 1) void gemm_multi_half##SUFFIX(MultiGemm mg) {                  \
         gemm_multi_body<BM / 2, false, true, RANK_MAJOR>(mg, static_cast<int>(blockIdx.x));            \
+    }                                                                                                 \
+    __global__ __launch_bounds__(kNT, 1) void gemm_multi_half_split##SUFFIX(MultiGemm mg) {            \
+        gemm_multi_body<BM / 2, true, true, RANK_MAJOR>(mg, static_cast<int>(blockIdx.x));             \
     }
 QN_MULTI_KERNELS(, false)
 QN_MULTI_KERNELS(_dx, true)
 #undef QN_MULTI_KERNELS
 
-// Split tiles: C[order[m], n..n+3] = bf16(sum of the tile's partials in split order)
-template <int SP>
+// Split tiles of `rows` rows (g.tiles_m counts those): C[order[m], n..n+3] = bf16(sum of the
+// tile's partials in split order), 4 rows per workgroup
 __global__ __launch_bounds__(256)
-void gemm_multi_reduce(MultiGemm mg) {
+void gemm_multi_reduce(MultiGemm mg, int rows) {
     const GemmArgs& g = mg.g;
-    const int j = static_cast<int>(blockIdx.x) / 64;
-    const int ml = (static_cast<int>(blockIdx.x) % 64) * 4 + (threadIdx.x >> 6);
+    const int per = rows / 4;
+    const int j = static_cast<int>(blockIdx.x) / per;
+    const int ml = (static_cast<int>(blockIdx.x) % per) * 4 + (threadIdx.x >> 6);
     const int nl = (threadIdx.x & 63) * 4;
     int tm, tn;
     tile_coords(g, g.full + j, tm, tn);
-    const int m = tm * BM + ml, n = tn * BN + nl;
+    const int m = tm * rows + ml, n = tn * BN + nl;
     if (m >= g.M || n >= g.N) return;
-    const float* p = g.part + static_cast<int64_t>(j) * (BM * BN) + ml * BN + nl;
-    const int64_t stride = static_cast<int64_t>(g.rem) * (BM * BN);
     const int64_t row = mg.plan.order[m];
-    float4 v[SP];
-#pragma unroll
-    for (int s = 0; s < SP; ++s) v[s] = *reinterpret_cast<const float4*>(p + s * stride);
-    float4 t = v[0];
-#pragma unroll
-    for (int s = 1; s < SP; ++s) { t.x += v[s].x; t.y += v[s].y; t.z += v[s].z; t.w += v[s].w; }
+    const float4 t = ordered_sum4<8>(g.part + (static_cast<int64_t>(j) * rows + ml) * BN + nl,
+                                     static_cast<int64_t>(g.rem) * rows * BN, g.splits);
     *reinterpret_cast<uint2*>(g.C + row * g.ldc + n) = uint2{pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w)};
 }
 
-}  // namespace
+// What becomes of the tiles past a multiple of 256 (if at most 128; more run whole): rem tiles
+// of `rows` rows, 256 or 128, with K split in `splits`; half tiles beside whole ones (full > 0)
+// stay pairs, and rem counts the pairs.
+struct LastTiles { int full, rem, rows, splits, kper; };
 
-namespace {
-// Tiles past a multiple of 256 that are taken as half tiles (0: none). Of at most 128 such
-// tiles a half tile takes 0.6 of a whole step per K-step; split in s, a tile takes 1/s of
-// them and the launch that adds the partials 8 steps (of 1.5 us) and one for every 14
-// partials of 256 KB. (rem tiles, K-steps, s: half against split, whole calls. 16, 16, 2:
-// 25.5 against 35.3 us; 16, 32, 4: 36.3, 37.1; 64, 64, 4: 64.8, 70.3; 32, 64, 4: 70.5, 64.0;
-// 16, 64, 4: 62.8, 49.3.)
-int half_tiles(int64_t M, int64_t N, int64_t K) {
-    const int64_t rem = (M + BM - 1) / BM * ((N + BN - 1) / BN) % 256;
-    if (rem > 128) return 0;
-    const int s = gemm_split(M, N, K).splits;
-    const double steps = static_cast<double>(K / BK);
-    const bool half = s <= 1 || 0.6 * steps <= steps / s + 8.0 + rem * s / 14.0;
-    return half ? static_cast<int>(rem) : 0;
+// Counted in K-steps of a whole tile (1.5 us): a half tile's takes 0.6; the launch that adds the
+// partials takes 8 (its start included) and one for every 14 partials of 256 KB. Half tiles are
+// split only where no whole tiles run beside them. (Calls at 4096 x 4096: 100 tokens 33.9 us in
+// split halves, 36.4 split whole, 47.0 whole in four; 256 tokens 39.1, 43.4 and 48.4; 1000 tokens
+// 60.5 either way, 70.3 whole in four. 1000 tokens on 1024 x 1024 25.5 in halves, 35.3 whole in two.)
+LastTiles last_tiles(int64_t M, int64_t N, int64_t K) {
+    const int64_t tm = (M + BM - 1) / BM, tn = (N + BN - 1) / BN, tiles = tm * tn;
+    const int64_t rem = tiles % 256, kt = K / BK;
+    LastTiles best{static_cast<int>(tiles), 0, BM, 1, static_cast<int>(kt)};
+    if (rem == 0 || rem > 128) return best;
+    double cost = 1e30;
+    for (const int rows : {BM / 2, BM}) {
+        const bool alone = tiles == rem;
+        const int64_t count = rows == BM || !alone ? rem : (M + rows - 1) / rows * tn;
+        const int64_t most = rows == BM || alone ? std::min<int64_t>({kMaxSplits, 256 / count, kt / 4}) : 1;
+        for (int64_t s = 1; s <= std::max<int64_t>(1, most); ++s) {
+            const int64_t kper = (kt + s - 1) / s;
+            if ((kt + kper - 1) / kper != s) continue;                  // a split would be empty
+            double c = (rows == BM ? 1.0 : 0.6) * static_cast<double>(kper);
+            if (s > 1) c += 8.0 + static_cast<double>(count * s * rows) / (14.0 * BM);
+            if (c < cost) {
+                cost = c;
+                best = LastTiles{static_cast<int>(tiles - rem), static_cast<int>(count), rows, static_cast<int>(s),
+                                 static_cast<int>(kper)};
+            }
+        }
+    }
+    if (best.rows == BM && best.splits == 1) best = LastTiles{static_cast<int>(tiles), 0, BM, 1, static_cast<int>(kt)};
+    return best;
 }
+
 }  // namespace
 
 int64_t gemm_multi_part_floats(int64_t M, int64_t N, int64_t K) {
-    return half_tiles(M, N, K) ? 0 : gemm_split_part_floats(M, N, K);
+    const LastTiles lt = last_tiles(M, N, K);
+    return lt.splits > 1 ? static_cast<int64_t>(lt.splits) * lt.rem * lt.rows * BN : 0;
 }
 
 hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t K, const uint16_t* T,
@@ -537,29 +566,20 @@ hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, 
         if (rank_major) QN_LAUNCH(#KERNEL "_dx", st, KERNEL##_dx, dim3(GRID), dim3(kNT), 0, st, mg);     \
         else QN_LAUNCH(#KERNEL, st, KERNEL, dim3(GRID), dim3(kNT), 0, st, mg);                          \
     } while (0)
-    if (const int rem = half_tiles(M, N, K); rem > 0) {
-        g.full = tiles - rem;
-        g.rem = rem;
-        if (g.full > 0) QN_GEMM(gemm_multi_mixed, g.full + 2 * rem);
-        else QN_GEMM(gemm_multi_half, 2 * rem);
-        return hipGetLastError();
+    const LastTiles lt = last_tiles(M, N, K);
+    g.full = lt.full; g.rem = lt.rem; g.splits = lt.splits; g.kper = lt.kper;
+    if (lt.rem == 0) QN_GEMM(gemm_multi_kernel, tiles);
+    else if (lt.rows == BM) QN_GEMM(gemm_multi_split, g.full + (g.rem * g.splits + 7) / 8 * 8);
+    else if (g.full > 0) QN_GEMM(gemm_multi_mixed, g.full + 2 * g.rem);
+    else {
+        g.tiles_m = static_cast<int>((M + lt.rows - 1) / lt.rows);
+        if (lt.splits > 1) QN_GEMM(gemm_multi_half_split, (g.rem * g.splits + 7) / 8 * 8);
+        else QN_GEMM(gemm_multi_half, g.rem);
     }
-    const GemmSplit gs = gemm_split(M, N, K);
-    g.splits = gs.splits;
-    g.full = gs.full;
-    g.rem = gs.rem;
-    g.kper = (g.kt1 + g.splits - 1) / g.splits;
-    if (g.splits <= 1) {
-        g.full = tiles;
-        QN_GEMM(gemm_multi_kernel, tiles);
-        return hipGetLastError();
-    }
-    QN_GEMM(gemm_multi_split, g.full + g.rem * g.splits);
 #undef QN_GEMM
-    const dim3 rgrid(static_cast<unsigned>(g.rem * 64));
-    if (g.splits == 2) QN_LAUNCH("gemm_multi_reduce", st, gemm_multi_reduce<2>, rgrid, dim3(256), 0, st, mg);
-    else if (g.splits == 3) QN_LAUNCH("gemm_multi_reduce", st, gemm_multi_reduce<3>, rgrid, dim3(256), 0, st, mg);
-    else QN_LAUNCH("gemm_multi_reduce", st, gemm_multi_reduce<4>, rgrid, dim3(256), 0, st, mg);
+    if (g.splits > 1)
+        QN_LAUNCH("gemm_multi_reduce", st, gemm_multi_reduce, dim3(static_cast<unsigned>(g.rem * (lt.rows / 4))),
+                  dim3(256), 0, st, mg, lt.rows);
     return hipGetLastError();
 }
 
