@@ -92,10 +92,10 @@ struct MultiPool {
 // cut in multi_pre_split(M, K).splits slices; with more than one, part holds their float32
 // sums [slice][pos][r] and a second launch adds them in slice order.
 struct MultiPre { const uint16_t* P; int64_t ldp; int64_t K; const uint16_t* R; float* part; uint16_t* T; };
-// A short K is one slice: the second launch costs 4.8 us, a K-chunk of 64 about 0.4 us (backward
-// of 203 tokens on 512 x 512: 29.3 us against 29.9 in two slices; on 1024 x 1024, where K
-// stays in four: 35.4 against 37.8 in one).
-constexpr int64_t kMultiWholeK = 512;
+// (A K of at most 512 is one slice: the second launch costs 4.8 us, a K-chunk of 64 about 0.4 us;
+// backward of 203 tokens on 512 x 512 29.3 us against 29.9 in two slices. Slices of 4 chunks: 26 us
+// in place of 22 with 256 adapters of one token on 4096 features, 14 as well with two; of 16:
+// 21 and 18.)
 PrepassSplit multi_pre_split(int64_t M, int64_t K);
 hipError_t launch_multi_prologue(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
                                  bool transposed, uint16_t* what, const MultiPlan& plan, const float* s, int64_t M,

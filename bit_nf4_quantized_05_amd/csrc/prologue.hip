@@ -510,13 +510,23 @@ __device__ __forceinline__ void multi_pre_job(const MultiPreJob& j, const MultiP
             rrow[i] = j.R + (static_cast<int64_t>(it.adapter) * r + min(row, r - 1)) * j.K + 8 * ((lane & 7) ^ ((row >> 1) & 7));
         }
     }
+    const bool live = 32 * wave < count;               // a wave without rows only helps to load R
     auto issue = [&](PreStage<NT>& st, int kc) {
+        if (live) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) load_lds16(prow[u] + static_cast<int64_t>(kc) * 64, &st.x[(32 * wave + 8 * u) * 8]);
+            for (int u = 0; u < 4; ++u)
+                load_lds16(prow[u] + static_cast<int64_t>(kc) * 64, &st.x[(32 * wave + 8 * u) * 8]);
+        }
 #pragma unroll
         for (int i = 0; i < NT; ++i) load_lds16(rrow[i] + kc * rstep, &st.r[8 * (4 * i + wave) * 8]);
     };
+    // until only the loads of the chunk after are in flight
+    auto wait_one = [&]() {
+        if (live) QN_WAIT_VM(kLoads);
+        else QN_WAIT_VM(NT);
+    };
     auto compute = [&](const PreStage<NT>& st, f32x16 (&acc)[NT]) {
+        if (!live) return;
         if constexpr (!kMajor) {
             pre_compute<NT, false>(st, wave, lane, acc);
         } else {
@@ -555,13 +565,13 @@ __device__ __forceinline__ void multi_pre_job(const MultiPreJob& j, const MultiP
     for (int t = 0; t < NT; ++t) acc[t] = f32x16{};
     issue(s0, kb);
     for (int kc = kb; kc < ke; kc += 2) {
-        if (kc + 1 < ke) { issue(s1, kc + 1); QN_WAIT_VM(kLoads); }
+        if (kc + 1 < ke) { issue(s1, kc + 1); wait_one(); }
         else QN_WAIT_VM(0);
         QN_PRE_BARRIER();
         compute(s0, acc);
         QN_PRE_BARRIER();
         if (kc + 1 >= ke) break;
-        if (kc + 2 < ke) { issue(s0, kc + 2); QN_WAIT_VM(kLoads); }
+        if (kc + 2 < ke) { issue(s0, kc + 2); wait_one(); }
         else QN_WAIT_VM(0);
         QN_PRE_BARRIER();
         compute(s1, acc);
@@ -855,8 +865,13 @@ hipError_t launch_prepass_pair(const uint16_t* P0, int64_t ldp0, int64_t K0, con
 }
 
 PrepassSplit multi_pre_split(int64_t M, int64_t K) {
-    if (K <= kMultiWholeK) return PrepassSplit{1, static_cast<int>(K / 64)};
-    return prepass_split(M, K);
+    // about a workgroup per CU with full items, slices of 8 chunks of 64 or little less at least
+    const int64_t tiles = (M + kMultiItem - 1) / kMultiItem, nk = K / 64;
+    const int64_t want = std::min<int64_t>((256 + tiles - 1) / tiles, (nk + 7) / 8);
+    PrepassSplit ps;
+    ps.kper = static_cast<int>((nk + want - 1) / want);
+    ps.splits = static_cast<int>((nk + ps.kper - 1) / ps.kper);
+    return ps;
 }
 
 hipError_t launch_multi_prologue(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
