@@ -363,6 +363,37 @@ def test_pool_of_more_than_2_32_elements():
     assert all(gA[i:i + 64].count_nonzero() == 0 for i in range(0, n, 64)) and gB.count_nonzero() == 0
 
 
+def test_operands_near_4_gib():
+    """131072 tokens of 16320 features: X and dX take 4.28 GB, the largest the calls accept.
+    dA sums 65536 tokens: sqrt(65536) 2^-24 = 1.5e-5 of the norm, twice that allowed."""
+    M, d_in, d_out, r, n = 131072, 16320, 64, 16, 2
+    _say(f"[multi] {M} tokens of {d_in} features")
+    L = Layer(d_out, d_in, 1, r, n, "one", seed=91)
+    X = torch.empty(M, d_in, dtype=torch.bfloat16, device=dev())
+    for i in range(0, M, 16384):
+        X[i:i + 16384] = torch.randn(16384, d_in, generator=L.gen, device=dev()).bfloat16()
+    dY = torch.randn(M, d_out, generator=L.gen, device=dev()).bfloat16()
+    ids = (torch.arange(M, device=dev()) % 3 - 1).int()
+    plan = qn.multi_plan(ids, n)
+    Y = qn.multi_linear_fwd(L.q, L.pool, plan, X)
+    dX, dA, dB = qn.multi_linear_bwd(L.q, L.pool, plan, X, dY)
+    torch.cuda.synchronize()
+    rows = np.unique(np.concatenate([np.arange(0, M, 4099), np.arange(M - 40, M), np.arange(65520, 65560)]))
+    at = torch.from_numpy(rows).to(dev())
+    who = ids[at].cpu().numpy()
+    check_close(_f64(Y[at]), MO.forward(L.W, L.A, L.B, L.s, who, _f64(X[at])), "forward")
+    check_close(_f64(dX[at]), MO.backward(L.W, L.A, L.B, L.s, who, _f64(X[at]), _f64(dY[at]))[0], "dX")
+    A, B, s = L.pool.A.double(), L.pool.B.double(), L.s
+    for a in range(n):
+        wA, wB = torch.zeros_like(A[a]), torch.zeros_like(B[a])
+        for i in range(0, M, 16384):
+            t = i + torch.nonzero(ids[i:i + 16384] == a).reshape(-1)
+            x, dy = X[t].double(), dY[t].double()
+            wA += s[a] * torch.mm(torch.mm(dy, B[a]).t().contiguous(), x)
+            wB += s[a] * torch.mm(dy.t().contiguous(), torch.mm(x, A[a].t().contiguous()))
+        assert (dA[a].double() - wA).norm() <= 3e-5 * wA.norm() and (dB[a].double() - wB).norm() <= 3e-5 * wB.norm(), a
+
+
 # ---- streams and graphs ---------------------------------------------------------------
 
 @pytest.mark.parametrize("M", [24, 300])
