@@ -119,32 +119,10 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
     const int m0 = kThree ? tm * BMT : tm * BM + (kHalf ? (place & 1) * BMT : 0), n0 = tn * BN;
     if (kHalf && !kThree && m0 >= M) return;
 
-    // this tile's adapters: used[k0 .. k1), `steps` rank steps in all
-    int2 kr = mg.plan.tile[m0 / BM];
-    if constexpr (kHalf) {                      // the adapters of this half alone, counted by all threads
-        const int a = mg.plan.used[min(kr.x + tid, max(kr.y, 1) - 1)];
-        const bool in = kr.x + tid < kr.y;
-        const int before = __syncthreads_count(in && mg.plan.start[a + 1] <= m0);
-        const int after = __syncthreads_count(in && mg.plan.start[a] >= m0 + BMT);
-        kr = int2{kr.x + before, kr.y - after};
-    }
-    // a rank step holds 64 ranks: of one adapter, or of 2 or 4 adapters of 32 or 16 (8 << sh ranks
-    // each); jsteps steps per adapter of more than 64
-    const int sh = mg.r == 16 ? 1 : mg.r == 32 ? 2 : 3;
-    const int per = 8 >> sh;
-    const int jsteps = (mg.r + BK - 1) / BK;
-    if (split_wg) {                             // this split's share of them
-        const int k = kr.y - kr.x;
-        kr = int2{kr.x + k * sk / g.splits, kr.x + k * (sk + 1) / g.splits};
-    }
-    const int used = kr.y - kr.x;
-    const int steps = (used + per - 1) / per * jsteps;
-    if (tid < used) {                           // at most one per row
-        const int a = mg.plan.used[kr.x + tid];
-        g_ad[tid] = a;
-        g_lo[tid] = mg.plan.start[a];
-        g_hi[tid] = mg.plan.start[a + 1];
-    }
+    // this tile's adapters, one a thread (at most one per row); sorted out below, under the
+    // first loads
+    const int2 kr = mg.plan.tile[m0 / BM];
+    const int mine = mg.plan.used[min(kr.x + tid, max(kr.y, 1) - 1)];
 
     const uint32_t kcE = static_cast<uint32_t>((lane & 7) ^ (lane >> 4)) * 16u;
     const uint32_t kcO = static_cast<uint32_t>((lane & 7) ^ (4 | (lane >> 4))) * 16u;
@@ -178,6 +156,42 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rsQ, (lds_ptr_t)(sq_ + 64 * j), 16, voQ[j], so_, 0, 0); \
         }                                                                                         \
     }
+
+    if constexpr (kThree) {
+        QN_ISSUE(0, g_h0)
+        if (KT > 1) QN_ISSUE(1, g_h1)
+    } else {
+        QN_ISSUE(0, g_st0)
+    }
+    // the list g_ad, g_lo, g_hi of the adapters with `steps` rank steps in all (seen by all after
+    // the first barrier)
+    int first = 0, used = kr.y - kr.x;
+    int lo_mine = 0, hi_mine = 0;
+    const bool in = tid < used;
+    if (in) {
+        lo_mine = mg.plan.start[mine];
+        hi_mine = mg.plan.start[mine + 1];
+    }
+    if constexpr (kHalf) {                      // those of this half alone
+        first = __syncthreads_count(in && hi_mine <= m0);
+        used -= first + __syncthreads_count(in && lo_mine >= m0 + BMT);
+    }
+    if (split_wg) {                             // this split's share of them
+        const int all = used;
+        first += all * sk / g.splits;
+        used = all * (sk + 1) / g.splits - all * sk / g.splits;
+    }
+    if (tid >= first && tid < first + used) {
+        g_ad[tid - first] = mine;
+        g_lo[tid - first] = lo_mine;
+        g_hi[tid - first] = hi_mine;
+    }
+    // a rank step holds 64 ranks: of one adapter, or of 2 or 4 adapters of 32 or 16 (8 << sh ranks
+    // each); jsteps steps per adapter of more than 64
+    const int sh = mg.r == 16 ? 1 : mg.r == 32 ? 2 : 3;
+    const int per = 8 >> sh;
+    const int jsteps = (mg.r + BK - 1) / BK;
+    const int steps = (used + per - 1) / per * jsteps;
 
     // Rank step S into stage ST: ranks j0 .. of T's rows (the same 8 << sh ranks once per
     // adapter of the step) and of the rows of R of its adapters. Pieces past r re-read the last
@@ -262,17 +276,19 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
 #define QN_MAIN(K, CUR, NXT) QN_STEP(QN_ISSUE((K) + 1, NXT), CUR, NXT, QN_FRAGS(NXT, chs[0], fa))
 #define QN_LAST(CUR, NXT) QN_STEP(if (steps > 0) issue_rank(0, NXT), CUR, NXT, )
 
-    // the stage the first rank step is in: the last main step's successor
-    int stage = 0;
+    int stage = 0;                              // the stage of rank step 0, of two
+    auto third = [&](int v) { return v % 3 == 0 ? g_h0 : v % 3 == 1 ? g_h1 : g_h2; };   // of step v, of three
     if constexpr (kThree) {
-        // Three stages: a step waits for its own stage only (the 6 loads of the next may be in
-        // flight), passes the barrier that certifies it for all waves and the stage of the step
-        // before as read, and sends the loads of the step after next into that one.
+        // Three stages, main and rank steps in one sequence: a step waits for its own stage only
+        // (the 6 loads of the next may be in flight), passes the barrier that certifies it for all
+        // waves and the stage of the step before as read, and sends the loads of the step after
+        // next into that one.
 #define QN_HALF(K, CUR, FREE, MORE)                                            \
     {                                                                          \
-        if (MORE || (K) + 1 < KT) QN_WAIT_VM(SEGP + SEG); else QN_WAIT_VM(0);  \
+        if (MORE || (K) + 1 < KT + steps) QN_WAIT_VM(SEGP + SEG); else QN_WAIT_VM(0); \
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");        \
         if (MORE || (K) + 2 < KT) QN_ISSUE((K) + 2, FREE)                      \
+        else if ((K) + 2 < KT + steps) issue_rank((K) + 2 - KT, FREE);         \
         QN_FRAGS(CUR, chs[0], fa)                                              \
         QN_FRAGS(CUR, chs[1], fb)                                              \
         __builtin_amdgcn_s_setprio(1);                                         \
@@ -286,8 +302,10 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
         QN_MFMAS(fb)                                                           \
         __builtin_amdgcn_s_setprio(0);                                         \
     }
-        QN_ISSUE(0, g_h0)
-        if (KT > 1) QN_ISSUE(1, g_h1)
+        if (KT == 1 && steps > 0) {             // step 1 is a rank step
+            __syncthreads();                    // (the list)
+            issue_rank(0, g_h1);
+        }
         int k = 0;
         // (no condition inside the loop: with one the compiler, not knowing how many loads are
         // in flight, waited for nearly all of them; it still does once per turn, hence six
@@ -306,15 +324,8 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
             if (k + 2 < KT) QN_HALF(k + 2, g_h2, g_h1, false)
         }
 #undef QN_HALF
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (steps > 0) {
-            issue_rank(0, g_h0);
-            QN_WAIT_VM(0);
-            QN_BARRIER();
-        }
     } else {
     stage = KT & 1;
-    QN_ISSUE(0, g_st0)
     __builtin_amdgcn_s_waitcnt(0);              // (the adapter list's LDS writes too)
     QN_BARRIER();
     QN_FRAGS(g_st0, chs[0], fa)
@@ -338,15 +349,21 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
 #undef QN_FRAGS
 #undef QN_ISSUE
 
-    // ---- rank steps. Step 0 is in the stage the last main step did not read, and complete
-    // (that step's wait and barrier). Each step: the next one's loads, this one's products,
-    // then every wave's loads and LDS reads are waited for before the barrier.
+    // ---- rank steps. Of three stages they go on as the main steps. Of two, step 0 is in the
+    // stage the last main step did not read, and complete (that step's wait and barrier); each
+    // step: the next one's loads, this one's products, then every wave's loads and LDS reads
+    // are waited for before the barrier.
     for (int s = 0; s < steps; ++s) {
-        uint4* const sa = kThree ? g_h0 : g_st0;
-        uint4* const sb = kThree ? g_h1 : g_st1;
-        const uint4* cur = ((stage + s) & 1) ? sb : sa;
-        uint4* nxt = ((stage + s) & 1) ? sa : sb;
-        if (s + 1 < steps) issue_rank(s + 1, nxt);
+        const uint4* cur;
+        if constexpr (kThree) {
+            if (s + 1 < steps) QN_WAIT_VM(SEGP + SEG); else QN_WAIT_VM(0);
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            if (s + 2 < steps) issue_rank(s + 2, third(KT + s + 2));
+            cur = third(KT + s);
+        } else {
+            cur = ((stage + s) & 1) ? g_st1 : g_st0;
+            if (s + 1 < steps) issue_rank(s + 1, ((stage + s) & 1) ? g_st0 : g_st1);
+        }
         const int k0 = s / jsteps * per;
         const int subs = min(BK, mg.r - (s % jsteps) * BK) / 16;
 #pragma unroll
@@ -399,9 +416,13 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
                 }
             }
         }
-        __builtin_amdgcn_s_waitcnt(0);
-        QN_BARRIER();
+        if constexpr (!kThree) {
+            __builtin_amdgcn_s_waitcnt(0);
+            QN_BARRIER();
+        }
     }
+    // (the last step's LDS reads, before the epilogue writes there)
+    if constexpr (kThree) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
     if (split_wg) {
         float* pt = g.part + (static_cast<int64_t>(sk) * T + place) * (BMT * BN);
