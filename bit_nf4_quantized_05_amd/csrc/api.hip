@@ -711,7 +711,7 @@ MultiWs multi_ws(int64_t d_out, int64_t d_in, int64_t M, int r, int n, bool bwd)
     int64_t off = 0;
     auto take = [&](int64_t bytes) { const int64_t at = off; off += align_up(bytes, 256); return at; };
     if (!bwd && M <= qn::kSkinnyMaxTokens) {
-        w.part = take(4 * static_cast<int64_t>(qn::skinny_splits(d_in, M)) * M * d_out);    // W_hat x, K-split
+        w.part = take(4 * static_cast<int64_t>(qn::multi_splits(d_out, d_in, M)) * M * d_out);    // W_hat x, K-split
         w.part_t = take(4 * static_cast<int64_t>(qn::multi_small_splits(d_in, M, n, r)) * M * r);    // A x, K-split
         w.bytes = off;
         return w;

@@ -223,7 +223,8 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
                 const int rr = 8 * SEG * wave + 8 * j + (ln >> 3);
                 const int c = (ln & 7) ^ ((rr >> 1) & 7);
                 const int64_t a = g_ad[min(k0 + (c >> sh), used - 1)];
-                load_lds16(mg.R + (a * N + min(n0 + rr, N - 1)) * mg.r + j0 + 8 * min(c & ((1 << sh) - 1), last), sq + 64 * j);
+                load_lds16(mg.R + (a * N + min(n0 + rr, N - 1)) * mg.r + j0 + 8 * min(c & ((1 << sh) - 1), last),
+                           sq + 64 * j);
             }
         }
     };
@@ -569,8 +570,8 @@ int64_t gemm_multi_part_floats(int64_t M, int64_t N, int64_t K) {
 }
 
 hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t K, const uint16_t* T,
-                             const uint16_t* R, bool rank_major, int r, const MultiPlan& plan, uint16_t* C, int64_t ldc, int64_t M,
-                             int64_t N, float* part, hipStream_t st) {
+                             const uint16_t* R, bool rank_major, int r, const MultiPlan& plan, uint16_t* C,
+                             int64_t ldc, int64_t M, int64_t N, float* part, hipStream_t st) {
     MultiGemm mg{};
     GemmArgs& g = mg.g;
     g.tiles_m = static_cast<int>((M + BM - 1) / BM);

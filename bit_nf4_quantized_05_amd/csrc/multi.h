@@ -120,8 +120,9 @@ hipError_t launch_gemv_nf4_select(const uint8_t* codes, const BlockConsts& bc, i
 
 // ---- skinny.hip, multi_small.hip ----
 // Forward of up to kSkinnyMaxTokens tokens from the packed codes: the W_hat x partials
-// [skinny_splits(d_in, M)][M][d_out] by token and the s_a A_a x partials
+// [multi_splits(d_out, d_in, M)][M][d_out] by token and the s_a A_a x partials
 // [multi_small_splits][M][r] by position in one launch, then Y from both.
+int multi_splits(int64_t d_out, int64_t d_in, int64_t M);
 int multi_small_splits(int64_t d_in, int64_t M, int n, int r);
 hipError_t launch_skinny_multi(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
                                const MultiPool& pool, const MultiPlan& plan, const uint16_t* X, int64_t ldx,

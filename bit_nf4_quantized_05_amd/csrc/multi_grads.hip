@@ -11,11 +11,12 @@
 // multi_grad_mfma: as for one adapter, a workgroup takes 128 columns of P = dY or X (32 per
 // wave), 64 (or 32) ranks and a slice of one adapter's positions; per step of 32 positions the
 // gathered rows of P and the rows of the three terms go straight into LDS (two stages), and
-// transposing reads hand each lane 4 consecutive rows of a column, the MFMA's K order. A slice is `per` items (128 positions each)
-// of the plan. An adapter whose tokens fit one slice is written to dA, dB at once; the others
-// leave one partial per slice, added in slice order by multi_grad_reduce, which also writes
-// the zeros of adapters without tokens. A batch of up to 512 tokens is one slice per adapter,
-// its last workgroups write the zeros, and there is no second launch. Deterministic; rows of other adapters count nowhere.
+// transposing reads hand each lane 4 consecutive rows of a column, the MFMA's K order. A slice is
+// `per` items (128 positions each) of the plan. An adapter whose tokens fit one slice is written
+// to dA, dB at once; the others leave one partial per slice, added in slice order by
+// multi_grad_reduce, which also writes the zeros of adapters without tokens. A batch of up to 512
+// tokens is one slice per adapter, its last workgroups write the zeros, and there is no second
+// launch. Deterministic; rows of other adapters count nowhere.
 // Slice s of adapter a has slot first_item[a] / per + a + s: a's ceil(items / per) slots end
 // before the next adapter's begin, and there are at most items / per + n of them.
 // Bound by the reads of dY and X and, with many slices, of the partials.

@@ -173,7 +173,7 @@ hipError_t launch_multi_small(const uint8_t* codes, const BlockConsts& bc, int64
     SmallArgs a{};
     a.plan = plan; a.B = pool.B;
     a.d_out = static_cast<int>(d_out); a.M = static_cast<int>(M); a.r = pool.r;
-    a.splits = skinny_splits(d_in, M);
+    a.splits = multi_splits(d_out, d_in, M);
     a.tsplits = multi_small_splits(d_in, M, pool.n, pool.r);
     a.max_items = static_cast<int>(multi_max_items(M, pool.n));
     a.part = part; a.part_t = part_t; a.Y = Y; a.ldy = ldy;

@@ -436,8 +436,8 @@ void prologue_kernel(PrologueArgs a, NF4Tables tab) {
 // most 128 positions of one adapter) and one K-slice, with the stages and fragments of
 // the pre-pass above; only the token rows are gathered, each lane keeping the addresses
 // of the 4 rows it fetches. Every slice writes its fp32 partial, already times s_a, and
-// multi_reduce adds them; of a single slice (multi_pre_split) T itself is written. Work is proportional to the tokens of each adapter rounded up
-// to 128, whatever the number of adapters in the pool; items past the plan's count (the
+// multi_reduce adds them; of a single slice (multi_pre_split) T itself is written. Work is
+// proportional to the tokens of each adapter rounded up to 128, whatever the number of adapters in the pool; items past the plan's count (the
 // grid is sized for the worst case) end at once. Bound by the reads of P (each row once)
 // and, with many adapters of few tokens, of R (each adapter once per 128 tokens).
 // ---------------------------------------------------------------------------
@@ -507,7 +507,8 @@ __device__ __forceinline__ void multi_pre_job(const MultiPreJob& j, const MultiP
             rrow[i] = j.R + (static_cast<int64_t>(it.adapter) * j.K + k) * r + min(8 * c, r - 8);
         } else {
             const int row = 8 * (4 * i + wave) + (lane >> 3);
-            rrow[i] = j.R + (static_cast<int64_t>(it.adapter) * r + min(row, r - 1)) * j.K + 8 * ((lane & 7) ^ ((row >> 1) & 7));
+            rrow[i] = j.R + (static_cast<int64_t>(it.adapter) * r + min(row, r - 1)) * j.K +
+                      8 * ((lane & 7) ^ ((row >> 1) & 7));
         }
     }
     const bool live = 32 * wave < count;               // a wave without rows only helps to load R

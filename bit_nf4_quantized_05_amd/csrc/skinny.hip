@@ -495,6 +495,23 @@ int ax_blocks(int64_t d_in, int64_t M, int n, int r) {
 
 }  // namespace
 
+// 8 or 4 K-splits up to 32 tokens: slices of 512 weights one after the other in a workgroup, times
+// the share of workgroups that do not fit the CUs at once (4, 3 a CU with one, two token
+// tiles), at 1.4 (1.9) us each, against the partials' way to memory and back at 1.5 TB/s. (24
+// tokens on 4096 x 4096 14.1 us with 8, 13.3 with 4; 32 on 11008 x 4096 29.3, 23.8; on 4096 x 11008
+// 23.8, 26.7; on 28672 x 8192 73.5, 65.2; 4 on 4096 x 4096 9.7, 10.5.)
+int multi_splits(int64_t d_out, int64_t d_in, int64_t M) {
+    const int most = skinny_splits(d_in, M);
+    if (M > kSkSplitTokens || most <= 4) return most;
+    const double slots = M <= 16 ? 1024.0 : 768.0, slice_us = M <= 16 ? 1.4 : 1.9;
+    const int64_t rows = d_out / kSkRows, nslices = (d_in / 64 + kSkBlk - 1) / kSkBlk;
+    auto cost = [&](int s) {
+        return std::max(1.0, static_cast<double>(rows * s) / slots) * static_cast<double>((nslices + s - 1) / s) * slice_us +
+               static_cast<double>(8 * s * M * d_out) / 1.5e6;
+    };
+    return cost(4) < cost(most) ? 4 : most;
+}
+
 int multi_small_splits(int64_t d_in, int64_t M, int n, int r) {
     const int per = ax_blocks(d_in, M, n, r);
     return static_cast<int>((d_in / 64 + per - 1) / per);
@@ -506,7 +523,7 @@ hipError_t launch_skinny_multi(const uint8_t* codes, const BlockConsts& bc, int6
     SkArgs a{};
     a.codes = codes; a.bc = bc;
     a.d_out = static_cast<int>(d_out); a.d_in = static_cast<int>(d_in); a.d_seq = static_cast<int>(d_seq);
-    a.splits = skinny_splits(d_in, d_seq);
+    a.splits = multi_splits(d_out, d_in, d_seq);
     a.X = X; a.ldx = ldx; a.part = part;
     MultiAx m{};
     m.plan = plan; m.pool = pool;

@@ -143,7 +143,9 @@ LARGE = [(256, 256, 65, 16, 3, "mixed"), (320, 192, 300, 32, 5, "packed"), (512,
          (4096, 128, 1531, 32, 30, "packed"), (4096, 64, 5200, 16, 5, "packed"), (4096, 1024, 4097, 16, 6, "mixed"),
          # a few tiles of a short K (halves) and of a long one (split), after whole ones too
          (512, 512, 203, 16, 3, "mixed"), (256, 4096, 300, 32, 3, "mixed"), (4096, 2560, 4097, 16, 6, "mixed"),
-         (448, 10112, 100, 64, 5, "mixed"), (448, 10112, 130, 64, 140, "mixed"), (1024, 8192, 900, 16, 30, "mixed")]
+         (448, 10112, 100, 64, 5, "mixed"), (448, 10112, 130, 64, 140, "mixed"), (1024, 8192, 900, 16, 30, "mixed"),
+         # 64 whole tiles split in four
+         (4096, 4864, 1000, 16, 6, "mixed")]
 
 
 @pytest.mark.parametrize("d_out,d_in,M,r,n,kind", SMALL + LARGE)
@@ -293,7 +295,8 @@ BWD = [(64, 64, 1, 16, 2, "one"), (256, 256, 203, 16, 3, "packed"), (320, 192, 4
        (256, 256, 130, 16, 4, "none"), (1536, 1088, 640, 128, 3, "packed"),
        (128, 4096, 1531, 48, 30, "packed"), (64, 4096, 5200, 16, 5, "packed"), (1024, 512, 2000, 240, 3, "mixed"),
        (512, 512, 512, 16, 3, "mixed"), (4096, 256, 300, 32, 3, "mixed"), (2560, 4096, 4097, 16, 6, "packed"),
-       (576, 640, 513, 32, 600, "mixed"), (5056, 320, 54, 64, 5, "packed"), (4160, 640, 200, 16, 100, "mixed")]
+       (576, 640, 513, 32, 600, "mixed"), (5056, 320, 54, 64, 5, "packed"), (4160, 640, 200, 16, 100, "mixed"),
+       (4864, 4096, 1000, 16, 6, "mixed")]
 
 
 @pytest.mark.parametrize("d_out,d_in,M,r,n,kind", BWD)
