@@ -577,6 +577,14 @@ def _multi_check(q: NF4Weight, pool: AdapterPool, plan: MultiPlan, d_seq: int, d
                          f"not {d_seq} and {pool.n} on {dev}")
 
 
+def _multi_workspace(workspace: torch.Tensor | None, need, d_out, d_in, d_seq, pool: AdapterPool, dev) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(max(need(d_out, d_in, d_seq, pool.r, pool.n), 1), dtype=torch.uint8, device=dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected contiguous memory on {dev}")
+    return workspace
+
+
 def multi_linear_fwd(q: NF4Weight, pool: AdapterPool, plan: MultiPlan, X: torch.Tensor,
                      out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """qlora_multi_fwd: Y[t] = W_hat x_t + s_a B_a (A_a x_t), a the adapter of token t in the
@@ -592,8 +600,7 @@ def multi_linear_fwd(q: NF4Weight, pool: AdapterPool, plan: MultiPlan, X: torch.
         o, ldy = X.new_empty((d_seq, d_out)), d_out
     else:
         o, ldy = out, _rows(out, torch.bfloat16, (d_seq, d_out), "out", dev)
-    ws = workspace if workspace is not None else torch.empty(
-        max(multi_linear_fwd_workspace_bytes(d_out, d_in, d_seq, pool.r, pool.n), 1), dtype=torch.uint8, device=dev)
+    ws = _multi_workspace(workspace, multi_linear_fwd_workspace_bytes, d_out, d_in, d_seq, pool, dev)
     rc = lib().qlora_multi_fwd(q.codes.data_ptr(), q.qconst.data_ptr(), q.qscale.data_ptr(), q.qmean.data_ptr(), d_out,
                                d_in, _dq_code(q.dq), pool.A.data_ptr(), pool.B.data_ptr(), pool.s.data_ptr(), pool.n,
                                pool.r, X.data_ptr(), ldx, d_seq, plan.buf.data_ptr(), o.data_ptr(), ldy, ws.data_ptr(),
@@ -626,8 +633,7 @@ def multi_linear_bwd(q: NF4Weight, pool: AdapterPool, plan: MultiPlan, X: torch.
         _need(ga, torch.float32, (n, r, d_in), "dA", dev)
     if dB is not None:
         _need(gb, torch.float32, (n, d_out, r), "dB", dev)
-    ws = workspace if workspace is not None else torch.empty(
-        max(multi_linear_bwd_workspace_bytes(d_out, d_in, d_seq, r, n), 1), dtype=torch.uint8, device=dev)
+    ws = _multi_workspace(workspace, multi_linear_bwd_workspace_bytes, d_out, d_in, d_seq, pool, dev)
     rc = lib().qlora_multi_bwd(q.codes.data_ptr(), q.qconst.data_ptr(), q.qscale.data_ptr(), q.qmean.data_ptr(), d_out,
                                d_in, _dq_code(q.dq), pool.A.data_ptr(), pool.B.data_ptr(), pool.s.data_ptr(), n, r,
                                X.data_ptr(), ldx, dY.data_ptr(), lddy, d_seq, plan.buf.data_ptr(), gx.data_ptr(), lddx,
@@ -669,12 +675,14 @@ class AdamWState:
         return self.m.device
 
     def set_grads(self, grads) -> None:
-        """Uses these gradients (same shapes and type) from the next step on; the table is
-        built again and copied to the device, so keep gradient buffers where possible."""
+        """Uses these gradients (same shapes and type) from the next step on the current stream
+        on, captured steps included; the table is filled again in place (a copy from the host,
+        so keep gradient buffers where possible)."""
         grads = list(grads)
         if _adamw_flags(self.params, grads, self.copies, self.bits) != self.flags:
             raise TypeError("the gradients' type must stay the same")
-        self.table, self.n_chunks = _adamw_table(self.params, grads, self.copies, self.flags, self.device)
+        host, self.n_chunks = _adamw_table(self.params, grads, self.copies, self.flags)
+        self.table.copy_(host)
         self.grads = grads
 
 
@@ -698,7 +706,8 @@ def _adamw_flags(params, grads, copies, bits) -> int:
             (_PARAM_BF16 if pt == torch.bfloat16 else 0))
 
 
-def _adamw_table(params, grads, copies, flags, device):
+def _adamw_table(params, grads, copies, flags):
+    """(the table in host memory, its chunks)."""
     k = len(params)
     n = (_c_i64 * k)(*[p.numel() for p in params])
     ptrs = [(ctypes.c_void_p * k)(*[t.data_ptr() if t is not None and t.numel() else None for t in ts])
@@ -710,7 +719,7 @@ def _adamw_table(params, grads, copies, flags, device):
     chunks = lib().qlora_adamw_table(*[ctypes.addressof(p) for p in ptrs], ctypes.addressof(n), k, flags, _ptr(host))
     if chunks < 0:
         _check(int(chunks), "qlora_adamw_table")
-    return host.to(device), int(chunks)
+    return host, int(chunks)
 
 
 def adamw_state(params, grads, copies=None, bits: int = 32) -> AdamWState:
@@ -728,9 +737,9 @@ def adamw_state(params, grads, copies=None, bits: int = 32) -> AdamWState:
     dt = torch.uint8 if bits == 8 else torch.float32
     m = torch.zeros(blocks * ADAMW_BLOCK, dtype=dt, device=dev)
     scales = [torch.zeros(blocks, dtype=torch.float32, device=dev) for _ in range(2)] if bits == 8 else [None, None]
-    table, n_chunks = _adamw_table(params, grads, copies, flags, dev)
-    return AdamWState(params, grads, copies, bits, m, torch.zeros_like(m), *scales, offsets, blocks, flags, table,
-                      n_chunks)
+    table, n_chunks = _adamw_table(params, grads, copies, flags)
+    return AdamWState(params, grads, copies, bits, m, torch.zeros_like(m), *scales, offsets, blocks, flags,
+                      table.to(dev), n_chunks)
 
 
 def _scalar(t: torch.Tensor, dtype, name: str, device) -> int:

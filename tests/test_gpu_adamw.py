@@ -224,6 +224,29 @@ def test_set_grads():
         st.set_grads([g.bfloat16() for g in grads])
 
 
+def test_captured_step_follows_set_grads():
+    _say("[adamw] other gradient tensors under a captured step")
+    gen = torch.Generator(device=dev()).manual_seed(9)
+    params, grads = _make([500, 257], gen, torch.float32, torch.float32)
+    twin = [p.clone() for p in params]
+    st, ref = qn.adamw_state(params, grads), qn.adamw_state(twin, grads)
+    t = torch.ones(1, dtype=torch.int64, device=dev())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        qn.adamw_step(st, t, LR)
+    other = [torch.randn(g.shape, generator=gen, device=dev()) for g in grads]
+    for k, g in ((1, grads), (2, other), (3, grads), (4, other)):
+        st.set_grads(g)
+        ref.set_grads(g)
+        t.fill_(k)
+        graph.replay()
+        torch.cuda.synchronize()
+        qn.adamw_step(ref, torch.tensor([k], device=dev()), LR)
+        torch.cuda.synchronize()
+        for a, b in zip(params + [st.m, st.v], twin + [ref.m, ref.v]):
+            assert torch.equal(a, b), k
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
 def test_nonfinite_gradients_show(bits, value):

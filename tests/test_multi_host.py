@@ -98,6 +98,8 @@ def test_binding_refusals():
     with pytest.raises(ValueError):
         qn.multi_linear_bwd(q, pool, plan, X, torch.zeros(4, 64, dtype=torch.bfloat16))
     with pytest.raises(ValueError):
+        qn.multi_linear_fwd(q, pool, plan, X, workspace=torch.zeros(64, 64, dtype=torch.uint8)[:, :8])
+    with pytest.raises(ValueError):
         pool.set(0, torch.zeros(17, 128), torch.zeros(64, 17), 1.0)
     with pytest.raises(TypeError):
         qn.multi_plan(torch.zeros(5, dtype=torch.int64), 3)
