@@ -159,6 +159,23 @@ def test_forward(d_out, d_in, M, r, n, kind):
     assert torch.equal(Y.view(torch.int16), again.view(torch.int16))
 
 
+@pytest.mark.parametrize("r", [16, 32, 48, 96, 112, 160, 208, 256])
+@pytest.mark.parametrize("d_in", [448, 1216])
+def test_adapters_of_few_and_many_tokens(r, d_in):
+    """Adapters of 1, 15, 16, 17 and 70 tokens in one batch, in one and in several K-slices."""
+    _say(f"[multi] few tokens per adapter, r={r}, {d_in} features")
+    counts = [1, 15, 16, 17, 70, 1, 1, 3]
+    L = Layer(128, d_in, sum(counts), r, len(counts) + 1, "one", seed=r + d_in)
+    L.ids_np = np.random.default_rng(r).permutation(np.repeat(np.arange(len(counts)), counts)).astype(np.int32)
+    L.plan = qn.multi_plan(torch.from_numpy(L.ids_np).to(dev()), len(counts) + 1)
+    check_close(_f64(qn.multi_linear_fwd(L.q, L.pool, L.plan, L.X)), L.forward(), "forward")
+    gX, gA, gB = qn.multi_linear_bwd(L.q, L.pool, L.plan, L.X, L.dY)
+    wX, wA, wB = L.backward()
+    check_close(_f64(gX), wX, "dX")
+    _close32(gA, wA, "dA")
+    _close32(gB, wB, "dB")
+
+
 @pytest.mark.parametrize("d_out,d_in", [(4096, 4096), (4160, 1024), (256, 4160)])
 @pytest.mark.parametrize("M", [1, 5, 64, 80])
 def test_weights_are_the_dequantisers(d_out, d_in, M):
