@@ -148,11 +148,11 @@ hipError_t launch_reduce(const SmallArgs& a, hipStream_t st) {
     const dim3 grid(static_cast<unsigned>(a.d_out / kRows));
 #define QN_RED(TT, SPL) \
     QN_LAUNCH("multi_reduce_small", st, (multi_reduce_small<RC, TT, SPL>), grid, dim3(64 * kWaves), 0, st, a)
-    // as many partial loads per output as the split count allows; above 32 tokens it is at most 4
+    // as many partial loads per output as the split count allows
     switch ((a.M + 15) / 16) {
         case 1: if (a.splits <= 4) QN_RED(1, 4); else QN_RED(1, 8); break;
         case 2: if (a.splits <= 4) QN_RED(2, 4); else QN_RED(2, 8); break;
-        default: if (a.splits > 4) return hipErrorInvalidValue; QN_RED(4, 4); break;
+        default: if (a.splits <= 4) QN_RED(4, 4); else QN_RED(4, 8); break;
     }
 #undef QN_RED
     return hipGetLastError();

@@ -495,16 +495,17 @@ int ax_blocks(int64_t d_in, int64_t M, int n, int r) {
 
 }  // namespace
 
-// 8 or 4 K-splits up to 32 tokens: slices of 512 weights one after the other in a workgroup, times
-// the share of workgroups that do not fit the CUs at once (4, 3 a CU with one, two token
-// tiles), at 1.4 (1.9) us each, against the partials' way to memory and back at 1.5 TB/s. (24
-// tokens on 4096 x 4096 14.1 us with 8, 13.3 with 4; 32 on 11008 x 4096 29.3, 23.8; on 4096 x 11008
-// 23.8, 26.7; on 28672 x 8192 73.5, 65.2; 4 on 4096 x 4096 9.7, 10.5.)
+// 8 or 4 K-splits: slices of 512 weights one after the other in a workgroup, times the share of
+// workgroups that do not fit the CUs at once (4, 3, 2 a CU with one, two, more token tiles), at
+// 1.4 to 3.4 us each, against the partials' way to memory and back at 1.5 TB/s. (Weights from HBM,
+// 8 and 4 splits: 4 tokens on 4096 x 4096 10.6, 11.9 us; 32 on 11008 x 4096 31.2, 27.1; on 4096 x
+// 11008 26.4, 29.3; on 28672 x 8192 85.9, 76.2; 64 on 4096 x 4096 27.6, 26.2; on 2048 x 8192 26.6, 32.3.)
 int multi_splits(int64_t d_out, int64_t d_in, int64_t M) {
-    const int most = skinny_splits(d_in, M);
-    if (M > kSkSplitTokens || most <= 4) return most;
-    const double slots = M <= 16 ? 1024.0 : 768.0, slice_us = M <= 16 ? 1.4 : 1.9;
     const int64_t rows = d_out / kSkRows, nslices = (d_in / 64 + kSkBlk - 1) / kSkBlk;
+    const int most = static_cast<int>(std::min<int64_t>(kSkSplits, nslices));
+    if (most <= 4) return most;
+    const double slots = M <= 16 ? 1024.0 : M <= 32 ? 768.0 : 512.0;
+    const double slice_us = M <= 16 ? 1.4 : M <= 32 ? 1.9 : M <= 48 ? 2.7 : 3.4;
     auto cost = [&](int s) {
         return std::max(1.0, static_cast<double>(rows * s) / slots) * static_cast<double>((nslices + s - 1) / s) * slice_us +
                static_cast<double>(8 * s * M * d_out) / 1.5e6;
