@@ -50,6 +50,7 @@ __global__ __launch_bounds__(64 * kWaves)
 void multi_reduce_small(SmallArgs a) {
     constexpr int kPitch = 32 * RC + 8;                  // bf16 per row of T: 16-byte rows, banks 4 apart
     constexpr int kBatch = RC >= 4 ? 2 : 8 / RC;         // items whose B a wave has in flight
+    constexpr bool kSkip = RC >= 2;
     __shared__ __align__(16) uint16_t s_t[16 * TT * kPitch];
     __shared__ float s_y[16 * TT][kRows + 1];
     const int tid = threadIdx.x;
@@ -62,12 +63,17 @@ void multi_reduce_small(SmallArgs a) {
 
     // rows o0 + i of B of items k0, k0 + 4, ..; ranks past r are zeros
     auto load_b = [&](int k0, uint4 (&w)[kBatch][RC]) {
+        int ad[kBatch];
+#pragma unroll
+        for (int n = 0; n < kBatch; ++n)
+            // (no wait for the count: the list is full of items of adapter -1 past its end)
+            ad[n] = a.plan.items[min(k0 + kWaves * n, a.max_items - 1)].adapter;
 #pragma unroll
         for (int n = 0; n < kBatch; ++n) {
-            // (no wait for the count: the list is full of items of adapter -1 past its end)
-            const int k = min(k0 + kWaves * n, a.max_items - 1);
-            const int64_t ad = max(a.plan.items[k].adapter, 0);
-            const uint16_t* row = a.B + (ad * a.d_out + o0 + i) * r;
+            // larger ranks: nothing is read for no item (64 tokens of 11008 x 4096, r = 64: a call
+            // 51.0 -> 49.7 us; at r = 16 the branch costs more, 64 of 4096 x 4096 20.6 -> 22.3)
+            if (kSkip && __builtin_amdgcn_readfirstlane(ad[n]) < 0) continue;
+            const uint16_t* row = a.B + (static_cast<int64_t>(max(ad[n], 0)) * a.d_out + o0 + i) * r;
 #pragma unroll
             for (int c = 0; c < RC; ++c) {
                 const uint4 v = *reinterpret_cast<const uint4*>(row + min(32 * c + 8 * g, r - 8));
