@@ -723,7 +723,7 @@ MultiWs multi_ws(int64_t d_out, int64_t d_in, int64_t M, int r, int n, bool bwd)
     };
     w.what = take(2 * d_out * d_in);                                                // W_hat or W_hat^T
     w.pre0 = pre(d_in);                                                             // A x
-    w.t = take(2 * (bwd ? 3 : 1) * M * r);                                          // T = s A x
+    w.t = take(2 * (bwd ? 3 : 2) * M * r);                                          // T = s A x
     if (bwd) {
         w.pre1 = pre(d_out);                                                        // B^T dy
         w.u = take(2 * 3 * M * r);                                                  // U = s B^T dy
@@ -822,7 +822,7 @@ int qlora_multi_fwd(const uint8_t* codes, const int8_t* qconst, const float* qsc
         if (e != hipSuccess) return hip_fail(e, "qlora_multi_fwd (small batch)");
         return 0;
     }
-    if ((e = qn::launch_multi_prologue(codes, bc, d_out, d_in, false, u16(mw.what), pl, s, d_seq, n, r, 1,
+    if ((e = qn::launch_multi_prologue(codes, bc, d_out, d_in, false, u16(mw.what), pl, s, d_seq, n, r, 2,
                                        qn::MultiPre{X, ldx, d_in, A, f32(mw.pre0), u16(mw.t)}, qn::MultiPre{}, st)) !=
         hipSuccess)
         return hip_fail(e, "qlora_multi_fwd (prologue)");

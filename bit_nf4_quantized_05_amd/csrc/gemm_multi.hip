@@ -4,7 +4,8 @@
 //     forward : P = X,  Q = W_hat,    T = s_a A_a x,    R_a = B_a
 //     dX      : P = dY, Q = W_hat^T,  T = s_a B_a^T dy, R_a = A_a^T
 // (A_a itself is read, rank-major: its rows go to LDS as they are and transposing reads hand
-// out the fragments).
+// out the fragments). T comes as two bf16 terms, 16 bits: with one term its 2^-9 would show in
+// the output, whose own rounding is no coarser.
 //
 // The main K-steps are those of the single-adapter GEMM (256 x 256 tiles, 8 waves of
 // 128 x 64, K-steps of 64 double-buffered in LDS by direct loads, swizzled rows; the
@@ -13,8 +14,8 @@
 // the adapters per tile few: over all tile rows there are at most (tile rows + adapters in
 // use) pairs, however the requests came in.
 //
-// Rank steps. After the last main step a tile walks the adapters with tokens in it, 64
-// ranks a step (4 adapters of rank 16, 2 of 32), double-buffered in the same stages (the first
+// Rank steps. After the last main step a tile walks the adapters with tokens in it, 16 ranks
+// of 4 adapters or 32 of 2 a step (as many loads as of one term and 64 ranks of one), double-buffered in the same stages (the first
 // one's loads go out under the last main step). A 32-row MFMA tile skips an adapter that has
 // none of its rows, adds straight to its accumulators when all 32 rows are the adapter's, and
 // otherwise forms the product apart and adds it where the lane's row is the adapter's. So a row
@@ -69,7 +70,7 @@ constexpr int kMaxSplits = 16;                  // of a tile's K-steps
 struct MultiGemm {
     GemmArgs g;                                 // P, Q, C, sizes, splits
     MultiPlan plan;
-    const uint16_t* T;                          // [M, r]
+    const uint16_t* T;                          // [2][M, r]: two bf16 terms
     const uint16_t* R;                          // [adapters, N, r], or [adapters, r, N]
     int r;
 };
@@ -186,19 +187,19 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
         g_lo[tid - first] = lo_mine;
         g_hi[tid - first] = hi_mine;
     }
-    // a rank step holds 64 ranks: of one adapter, or of 2 or 4 adapters of 32 or 16 (8 << sh ranks
-    // each); jsteps steps per adapter of more than 64
-    const int sh = mg.r == 16 ? 1 : mg.r == 32 ? 2 : 3;
+    // a rank step holds 64 rows of R: 16 ranks of 4 adapters or 32 of 2 (8 << sh ranks each), jsteps
+    // steps per adapter of more than 32; and beside them both terms of T at those ranks
+    const int sh = mg.r == 16 ? 1 : 2;
     const int per = 8 >> sh;
-    const int jsteps = (mg.r + BK - 1) / BK;
+    const int jsteps = (mg.r + (8 << sh) - 1) / (8 << sh);
     const int steps = (used + per - 1) / per * jsteps;
 
-    // Rank step S into stage ST: ranks j0 .. of T's rows (the same 8 << sh ranks once per
-    // adapter of the step) and of the rows of R of its adapters. Pieces past r re-read the last
+    // Rank step S into stage ST: ranks j0 .. of T's rows (8 << sh of the first term, then the
+    // second's, over and over) and of the rows of R of its adapters. Pieces past r re-read the last
     // one, adapters past the last re-read it (no MFMA reads either); the addresses are formed
     // from an opaque copy of the lane index, so they hold no registers through the main steps.
     auto issue_rank = [&](int s, uint4* st) {
-        const int j0 = (s % jsteps) * BK, k0 = s / jsteps * per;
+        const int j0 = (s % jsteps) * (8 << sh), k0 = s / jsteps * per;
         int ln = lane;
         asm volatile("" : "+v"(ln));
         uint4* sp = st + wave * (64 * SEGP);
@@ -208,7 +209,7 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
         for (int j = 0; j < SEGP; ++j) {
             const int rr = 8 * SEGP * wave + 8 * j + (ln >> 3);
             const int c = (ln & 7) ^ ((rr >> 1) & 7);
-            const int64_t row = min(m0 + rr, M - 1);
+            const int64_t row = min(m0 + rr, M - 1) + ((c >> sh) & 1 ? static_cast<int64_t>(M) : 0);
             load_lds16(mg.T + row * mg.r + j0 + 8 * min(c & ((1 << sh) - 1), last), sp + 64 * j);
         }
 #pragma unroll
@@ -366,12 +367,13 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
             if (s + 1 < steps) issue_rank(s + 1, ((stage + s) & 1) ? g_st0 : g_st1);
         }
         const int k0 = s / jsteps * per;
-        const int subs = min(BK, mg.r - (s % jsteps) * BK) / 16;
+        const int subs = min(8 << sh, mg.r - (s % jsteps) * (8 << sh)) / 16;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
-            // sub-step kk: 16 ranks of adapter k0 + (kk >> (sh - 1))
+            // sub-step kk: 16 ranks of adapter k0 + (kk >> (sh - 1)), both terms of T at them
             const int k = k0 + (kk >> (sh - 1));
-            if (k >= used || (sh == 3 && kk >= subs)) continue;
+            if (k >= used || (sh == 2 && (kk & 1) >= subs)) continue;
+            const uint32_t term0 = sh == 1 ? chs[0] : chs[kk & 1], term1 = sh == 1 ? chs[1] : chs[2 + (kk & 1)];
             const int lo = __builtin_amdgcn_readfirstlane(g_lo[k]), hi = __builtin_amdgcn_readfirstlane(g_hi[k]);
             const int w0 = m0 + wm * (TM * 32);
             if (w0 >= hi || w0 + TM * 32 <= lo) continue;                // none of the wave's positions
@@ -402,17 +404,17 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
             for (int b = 0; b < TM; ++b) {
                 const int p0 = w0 + b * 32;                              // the sub-tile's positions p0 .. p0 + 31
                 if (p0 >= hi || p0 + 32 <= lo) continue;                 // wave-uniform
-                const uint4 p = cur[prow + b * 256 + chs[kk]];
+                const uint4 p = cur[prow + b * 256 + term0], e = cur[prow + b * 256 + term1];
                 if (p0 >= lo && p0 + 32 <= hi) {
 #pragma unroll
-                    for (int a = 0; a < TN; ++a) acc[a][b] = mfma32(q[a], p, acc[a][b]);
+                    for (int a = 0; a < TN; ++a) acc[a][b] = mfma32(q[a], p, mfma32(q[a], e, acc[a][b]));
                 } else {
                     const bool mine = p0 + static_cast<int>(frow) >= lo && p0 + static_cast<int>(frow) < hi;
 #pragma unroll
                     for (int a = 0; a < TN; ++a) {
-                        const f32x16 t = mfma32(q[a], p, f32x16{});
+                        const f32x16 t = mfma32(q[a], p, mfma32(q[a], e, f32x16{}));
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) acc[a][b][e] = mine ? acc[a][b][e] + t[e] : acc[a][b][e];
+                        for (int i = 0; i < 16; ++i) acc[a][b][i] = mine ? acc[a][b][i] + t[i] : acc[a][b][i];
                     }
                 }
             }

@@ -87,7 +87,7 @@ struct MultiPool {
 // ---- prologue.hip ----
 // Pre-passes of the multi-adapter calls and the double dequantisation of the weight to what
 // (transposed or not; null: none) in one launch: T[piece][pos][r] = s_a P[order[pos], K]
-// R_a[r, K]^T in `pieces` bf16 terms (1: rounded once; 3: the remainders too, 24 bits in all),
+// R_a[r, K]^T in `pieces` bf16 terms, each what the ones before left (2: 16 bits; 3: 24 bits),
 // R [n, r, K] for the first product, [n, K, r] for the second (none if its R is null). K is
 // cut in multi_pre_split(M, K).splits slices; with more than one, part holds their float32
 // sums [slice][pos][r] and a second launch adds them in slice order.
@@ -102,8 +102,8 @@ hipError_t launch_multi_prologue(const uint8_t* codes, const BlockConsts& bc, in
                                  int n, int r, int pieces, const MultiPre& p0, const MultiPre& p1, hipStream_t st);
 
 // ---- gemm_multi.hip ----
-// C[order[pos], :] = bf16( P[order[pos], K] Q[N, K]^T + T[pos, r] R_a[N, r]^T ), R [n, N, r] or,
-// with rank_major, R_a^T given as [n, r, N]; a the adapter of the
+// C[order[pos], :] = bf16( P[order[pos], K] Q[N, K]^T + (T[0] + T[1])[pos, r] R_a[N, r]^T ), T
+// [2 or more][M, r] in bf16 terms, R [n, N, r] or, with rank_major, R_a^T given as [n, r, N]; a the adapter of the
 // position (no second term without one). part holds gemm_multi_part_floats floats.
 int64_t gemm_multi_part_floats(int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm_multi(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t K, const uint16_t* T,

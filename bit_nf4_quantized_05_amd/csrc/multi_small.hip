@@ -8,10 +8,11 @@
 // or, for one token with r <= 16 and d_in <= 4096, in the streaming GEMV's one launch, which
 // reads the token's adapter from the plan (4096 x 4096: 10.9 -> 6.9 us per graph-replayed call).
 //
-// multi_reduce_small: a workgroup takes 16 rows of W and all tokens. It forms T = bf16(sum
-// of the A x partials in slice order) of every position in LDS; its waves take the plan's
+// multi_reduce_small: a workgroup takes 16 rows of W and all tokens. It forms T = the sum
+// of the A x partials in slice order of every position in LDS, as two bf16 terms (16 bits: one
+// term's 2^-9 would show in the output); its waves take the plan's
 // items (the tokens of one adapter) in turn, v_mfma_f32_16x16x32_bf16 with the item's 16
-// rows of B_a, straight from memory, as one operand and 16 of its tokens' T as the other;
+// rows of B_a, straight from memory, as one operand and both terms of 16 of its tokens' T as the other;
 // the products go to LDS by position, and each output is the ordered sum of its W_hat x
 // partials plus its product, rounded once. Every byte of B is read by one wave, 64
 // contiguous bytes per 4 lanes (one thread per row and token read its row in eight strided
@@ -51,7 +52,7 @@ void multi_reduce_small(SmallArgs a) {
     constexpr int kPitch = 32 * RC + 8;                  // bf16 per row of T: 16-byte rows, banks 4 apart
     constexpr int kBatch = RC >= 4 ? 2 : 8 / RC;         // items whose B a wave has in flight
     constexpr bool kSkip = RC >= 2;
-    __shared__ __align__(16) uint16_t s_t[16 * TT * kPitch];
+    __shared__ __align__(16) uint16_t s_t[2][16 * TT * kPitch];
     __shared__ float s_y[16 * TT][kRows + 1];
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -96,7 +97,7 @@ void multi_reduce_small(SmallArgs a) {
     const int quads = 8 * RC;                            // per position
     for (int e = tid; e < live * quads; e += 64 * kWaves) {
         const int p = e / quads, j = e % quads * 4;
-        uint2 v = uint2{0, 0};
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (j < r) {
             const float* pt = a.part_t + static_cast<int64_t>(p) * r + j;
             const int64_t stride = static_cast<int64_t>(M) * r;
@@ -104,9 +105,10 @@ void multi_reduce_small(SmallArgs a) {
             const float4 t = a.tsplits == 1 ? *reinterpret_cast<const float4*>(pt)
                              : a.tsplits <= 4 ? ordered_sum4<4>(pt, stride, a.tsplits)
                                               : ordered_sum4<8>(pt, stride, a.tsplits);
-            v = uint2{pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w)};
+            v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
         }
-        *reinterpret_cast<uint2*>(&s_t[p * kPitch + j]) = v;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) *reinterpret_cast<uint2*>(&s_t[h][p * kPitch + j]) = take_bf16x4(v);
     }
     __syncthreads();
     for (int k0 = wave; k0 < items; k0 += kWaves * kBatch) {
@@ -123,12 +125,14 @@ void multi_reduce_small(SmallArgs a) {
                 const int row = 16 * t + i;
                 f32x4 acc = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int c = 0; c < RC; ++c) {
-                    const uint4 tv = *reinterpret_cast<const uint4*>(
-                        &s_t[(it.pos + min(row, count - 1)) * kPitch + 32 * c + 8 * g]);
-                    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, bw[n][c]),
-                                                                  __builtin_bit_cast(bf16x8, tv), acc, 0, 0, 0);
-                }
+                for (int c = 0; c < RC; ++c)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 tv = *reinterpret_cast<const uint4*>(
+                            &s_t[h][(it.pos + min(row, count - 1)) * kPitch + 32 * c + 8 * g]);
+                        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, bw[n][c]),
+                                                                      __builtin_bit_cast(bf16x8, tv), acc, 0, 0, 0);
+                    }
                 // D of a 16 x 16 tile: lane l holds rows 4 (l / 16) .. + 3 of token l % 16
                 if (row < count) {
 #pragma unroll

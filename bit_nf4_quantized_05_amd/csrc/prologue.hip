@@ -449,20 +449,10 @@ struct MultiPreJob {
     int psplits, kper, n;            // K-slices, 64-wide K-chunks per slice, workgroups
 };
 
-// 4 neighbouring values of T as 1 or 3 bf16 terms, `stride` elements apart
+// 4 neighbouring values of T as 2 or 3 bf16 terms, `stride` elements apart
 __device__ __forceinline__ void store_terms(const float4& t, int pieces, uint16_t* T, int64_t stride) {
     float v[4] = {t.x, t.y, t.z, t.w};
-    for (int p = 0; p < pieces; ++p) {
-        uint16_t h[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            h[e] = bf16_bits(v[e]);
-            const float f = bf16_to_f32(h[e]);
-            v[e] = fabsf(f) < __builtin_inff() ? v[e] - f : 0.0f;      // nothing is left of an infinity or NaN
-        }
-        *reinterpret_cast<uint2*>(T + p * stride) =
-            uint2{h[0] | (static_cast<uint32_t>(h[1]) << 16), h[2] | (static_cast<uint32_t>(h[3]) << 16)};
-    }
+    for (int p = 0; p < pieces; ++p) *reinterpret_cast<uint2*>(T + p * stride) = take_bf16x4(v);
 }
 
 struct MultiPrologueArgs {
@@ -668,7 +658,7 @@ __device__ __forceinline__ void multi_pre_job(const MultiPreJob& j, const MultiP
     }
 }
 
-// T[piece][pos][r] = the slice partials added in slice order, as 1 or 3 bf16 terms; 4 ranks
+// T[piece][pos][r] = the slice partials added in slice order, as 2 or 3 bf16 terms; 4 ranks
 // per thread. Those of a token without an adapter come from sums that no slice wrote; nobody
 // reads them.
 struct MultiReduceJob { const float* part; uint16_t* T; int splits; };

@@ -369,7 +369,8 @@ int64_t qlora_multi_bwd_workspace_bytes(int64_t d_out, int64_t d_in, int64_t d_s
  * qlora_multi_fwd - Y[t] = dequant(W) x_t + s_a B_a (A_a x_t), a the token's adapter; the
  * first term alone for a token without one. Shapes, strides, alignment and errors as
  * qlora_linear_fwd_ex (d_in, d_out multiples of 64; -2 for r not a multiple of 16 or n over
- * the limit). A_a x_t is rounded to bf16 once; accumulation in float32, one final rounding.
+ * the limit). s_a A_a x_t keeps 16 bits or more (two bf16 terms; float32 for one token with r = 16
+ * and d_in <= 4096); accumulation in float32, one final rounding.
  * A token's result depends on its own adapter only: an infinity or NaN in another's weights
  * does not reach it. Up to 64 tokens stream the packed codes (a decode batch); more run the
  * MFMA GEMM on W_hat dequantised into the workspace.
@@ -384,8 +385,8 @@ int qlora_multi_fwd(const uint8_t* codes, const int8_t* qconst, const float* qsc
  *   dX[t]  = dequant(W)^T dy_t + s_a A_a^T (B_a^T dy_t)         bf16 [d_seq, d_in]
  *   dA_a   = s_a sum over a's tokens of (B_a^T dy_t) x_t^T      float32 [n, r, d_in]
  *   dB_a   = s_a sum over a's tokens of dy_t (A_a x_t)^T        float32 [n, d_out, r]
- * dA, dB of an adapter without tokens are zeros. dX rounds B_a^T dy_t to bf16 once; dA and
- * dB use the rank products to 24 bits and accumulate in float32, in a fixed order.
+ * dA, dB of an adapter without tokens are zeros. dX uses s_a B_a^T dy_t to 16 bits (two bf16
+ * terms); dA and dB use the rank products to 24 bits and accumulate in float32, in a fixed order.
  */
 int qlora_multi_bwd(const uint8_t* codes, const int8_t* qconst, const float* qscale, const float* qmean,
                     int64_t d_out, int64_t d_in, int dq, const uint16_t* A, const uint16_t* B, const float* s, int n,
