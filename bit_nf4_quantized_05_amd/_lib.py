@@ -484,13 +484,14 @@ def qlr_linear_fwd(q: NF4Weight, Af: QFactor, Bf: QFactor, s: float, X: torch.Te
 # ---- many adapters on one layer ---------------------------------------------------
 
 MULTI_RANK_STEP = 16          # ranks of a pool come in this step
+MULTI_MAX_ADAPTERS = 1024
 
 
 @dataclass(frozen=True)
 class AdapterPool:
     """Adapters of one layer side by side: A bfloat16 [n, r, d_in], B bfloat16
-    [n, d_out, r], s float32 [n] (each adapter's LoRA scale); r a multiple of 16. Checked
-    when it is made; the tensors' contents may change, the tensors may not be replaced.
+    [n, d_out, r], s float32 [n] (each adapter's LoRA scale); n <= 1024, r a multiple of 16
+    up to 256. Checked when it is made; the tensors' contents may change, the tensors may not be replaced.
     ``alloc_pool`` and ``set`` make one from adapters of any rank up to r."""
     A: torch.Tensor
     B: torch.Tensor
@@ -509,6 +510,10 @@ class AdapterPool:
         _need(A, torch.bfloat16, (n, r, d_in), "pool.A", dev)
         _need(B, torch.bfloat16, (n, d_out, r), "pool.B", dev)
         _need(s, torch.float32, (n,), "pool.s", dev)
+        if not 1 <= n <= MULTI_MAX_ADAPTERS:
+            raise ValueError(f"a pool holds 1 to {MULTI_MAX_ADAPTERS} adapters, not {n}")
+        if not MULTI_RANK_STEP <= r <= 256 or r % MULTI_RANK_STEP:
+            raise ValueError(f"a pool's rank is a multiple of {MULTI_RANK_STEP} up to 256, not {r}")
         for name, v in (("n", n), ("r", r), ("d_in", d_in), ("d_out", d_out), ("device", dev)):
             object.__setattr__(self, name, v)
 
@@ -527,8 +532,8 @@ class AdapterPool:
 
 def alloc_pool(n: int, r: int, d_out: int, d_in: int, device) -> AdapterPool:
     """A pool of n adapters of rank up to r (rounded up to a multiple of 16), all zero."""
-    if n < 1 or not 1 <= r <= 256:
-        raise ValueError("n must be >= 1 and r in [1, 256]")
+    if not 1 <= n <= MULTI_MAX_ADAPTERS or not 1 <= r <= 256:
+        raise ValueError(f"n must be in [1, {MULTI_MAX_ADAPTERS}] and r in [1, 256]")
     rp = -(-r // MULTI_RANK_STEP) * MULTI_RANK_STEP
     return AdapterPool(torch.zeros(n, rp, d_in, dtype=torch.bfloat16, device=device),
                        torch.zeros(n, d_out, rp, dtype=torch.bfloat16, device=device),

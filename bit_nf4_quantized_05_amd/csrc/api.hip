@@ -734,8 +734,12 @@ MultiWs multi_ws(int64_t d_out, int64_t d_in, int64_t M, int r, int n, bool bwd)
     return w;
 }
 
+// Sizes that check_multi takes with rows as short as they can be.
 bool multi_sizes_ok(int64_t d_out, int64_t d_in, int64_t d_seq, int r, int n) {
-    return linear_sizes_ok(d_out, d_in, d_seq, r) && n >= 1 && n <= QN_MULTI_MAX_ADAPTERS;
+    if (!linear_sizes_ok(d_out, d_in, d_seq, r) || n < 1 || n > QN_MULTI_MAX_ADAPTERS) return false;
+    if (d_in % 64 != 0 || d_out % 64 != 0 || r % 16 != 0) return false;
+    const int64_t kMaxElems = int64_t{1} << 31, wide = std::max(d_in, d_out);
+    return d_out * d_in < kMaxElems && d_seq <= (kMaxElems - 1) / std::max<int64_t>(wide, r) && wide * r < kMaxElems;
 }
 
 static_assert(QN_MULTI_MAX_ADAPTERS == qn::kMultiMaxAdapters, "adapter limit");

@@ -361,7 +361,7 @@ int qlora_lora_grads(const uint16_t* A, const uint16_t* B, int r, float s,
 int64_t qlora_multi_plan_bytes(int64_t d_seq, int n);
 int qlora_multi_plan(const int32_t* ids, int64_t d_seq, int n, void* plan, int64_t plan_bytes, void* stream);
 
-/* Workspace bytes of the two calls (0 on bad sizes). */
+/* Workspace bytes of the two calls (0 on sizes that the calls refuse). */
 int64_t qlora_multi_fwd_workspace_bytes(int64_t d_out, int64_t d_in, int64_t d_seq, int r, int n);
 int64_t qlora_multi_bwd_workspace_bytes(int64_t d_out, int64_t d_in, int64_t d_seq, int r, int n);
 
