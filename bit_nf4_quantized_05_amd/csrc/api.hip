@@ -38,6 +38,10 @@ int64_t align_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
 constexpr int64_t kMaxBlocks = (int64_t{1} << 32) - 1;
 
+// Whether `rows` >= 1 rows of bf16 at stride ld >= 1 reach 4 GiB: the kernels address an
+// operand with 32-bit byte offsets. (A division, since the product can pass 64 bits.)
+bool reaches_4gib(int64_t rows, int64_t ld) { return ld > ((int64_t{1} << 31) - 1) / rows; }
+
 bool nf4_counts(int64_t d_out, int64_t d_in, int64_t* n, int64_t* n_b, int64_t* n_g) {
     if (d_out < 1 || d_in < 1) return false;
     if (d_out > (int64_t{1} << 40) / d_in) return false;
@@ -147,9 +151,7 @@ int check_linear(const uint8_t* codes, const int8_t* qconst, const float* qscale
     if (d_in > INT32_MAX || d_out > INT32_MAX || d_seq > INT32_MAX) return fail(-2, "dimension too large");
     int64_t n, n_b, n_g;
     if (!nf4_counts(d_out, d_in, &n, &n_b, &n_g)) return fail(-2, "weight too large");
-    // the GEMM addresses each operand with 32-bit byte offsets
-    const int64_t kMaxBytes = int64_t{1} << 32;
-    if (2 * n >= kMaxBytes || 2 * d_seq * std::max(ldi, ldo) >= kMaxBytes)
+    if (reaches_4gib(d_out, d_in) || reaches_4gib(d_seq, std::max(ldi, ldo)))
         return fail(-2, "an operand reaches 4 GiB");
     *lw = linear_ws(d_out, d_in, d_seq, r, bwd);
     if (ws_bytes < lw->bytes) return fail(-3, "workspace too small");
@@ -672,7 +674,7 @@ int qlora_lora_grads(const uint16_t* A, const uint16_t* B, int r, float s, const
         return fail(-1, "misaligned pointer (16 B for arrays, 256 B for the workspace)");
     if (d_in % 64 != 0 || d_out % 64 != 0) return fail(-2, "d_in and d_out must be multiples of 64");
     if (d_in > INT32_MAX || d_out > INT32_MAX || d_seq > INT32_MAX) return fail(-2, "dimension too large");
-    if (2 * d_seq * std::max(ldx, lddy) >= (int64_t{1} << 32)) return fail(-2, "an operand reaches 4 GiB");
+    if (reaches_4gib(d_seq, std::max(ldx, lddy))) return fail(-2, "an operand reaches 4 GiB");
     const GradWs gw = grad_ws(d_out, d_in, d_seq, r);
     if (workspace_bytes < gw.bytes) return fail(-3, "workspace too small");
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -738,8 +740,8 @@ MultiWs multi_ws(int64_t d_out, int64_t d_in, int64_t M, int r, int n, bool bwd)
 bool multi_sizes_ok(int64_t d_out, int64_t d_in, int64_t d_seq, int r, int n) {
     if (!linear_sizes_ok(d_out, d_in, d_seq, r) || n < 1 || n > QN_MULTI_MAX_ADAPTERS) return false;
     if (d_in % 64 != 0 || d_out % 64 != 0 || r % 16 != 0) return false;
-    const int64_t kMaxElems = int64_t{1} << 31, wide = std::max(d_in, d_out);
-    return d_out * d_in < kMaxElems && d_seq <= (kMaxElems - 1) / std::max<int64_t>(wide, r) && wide * r < kMaxElems;
+    const int64_t wide = std::max(d_in, d_out);
+    return !reaches_4gib(d_out, d_in) && !reaches_4gib(d_seq, std::max<int64_t>(wide, r)) && !reaches_4gib(wide, r);
 }
 
 static_assert(QN_MULTI_MAX_ADAPTERS == qn::kMultiMaxAdapters, "adapter limit");
@@ -767,11 +769,8 @@ int check_multi(const uint8_t* codes, const int8_t* qconst, const float* qscale,
     if (d_in > INT32_MAX || d_out > INT32_MAX || d_seq > INT32_MAX) return fail(-2, "dimension too large");
     int64_t cnt, n_b, n_g;
     if (!nf4_counts(d_out, d_in, &cnt, &n_b, &n_g)) return fail(-2, "weight too large");
-    // the GEMM addresses each operand with 32-bit byte offsets
-    const int64_t kMaxBytes = int64_t{1} << 32;
-    const int64_t ld = std::max<int64_t>({ldx, ldo, bwd ? lddy : 0, r});
-    if (2 * cnt >= kMaxBytes || ld >= kMaxBytes || 2 * d_seq * ld >= kMaxBytes ||
-        2 * std::max(d_in, d_out) * r >= kMaxBytes)
+    if (reaches_4gib(d_out, d_in) || reaches_4gib(d_seq, std::max<int64_t>({ldx, ldo, bwd ? lddy : 0, r})) ||
+        reaches_4gib(std::max(d_in, d_out), r))
         return fail(-2, "an operand reaches 4 GiB");
     *mw = multi_ws(d_out, d_in, d_seq, r, n, bwd);
     if (ws_bytes < mw->bytes) return fail(-3, "workspace too small");
