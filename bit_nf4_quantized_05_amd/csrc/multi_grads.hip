@@ -17,8 +17,11 @@
 // multi_grad_reduce, which also writes the zeros of adapters without tokens. A batch of up to 512
 // tokens is one slice per adapter, its last workgroups write the zeros, and there is no second
 // launch. Deterministic; rows of other adapters count nowhere.
-// Slice s of adapter a has slot first_item[a] / per + a + s: a's ceil(items / per) slots end
-// before the next adapter's begin, and there are at most items / per + n of them.
+// Slots of partials: only an adapter of more than one slice's tokens ("span", 128 per) has any,
+// c > span tokens ceil(c / span) of them, which is at most floor(2 c / span). So the first slot
+// floor(2 start[a] / span) leaves room for all of a's before the next adapter's, and there are at
+// most 2 M / span, whatever the pool holds. With few adapters first_item[a] / per + a is less and
+// does as well (at most items / per + n); the smaller of two such numbers does too.
 // Bound by the reads of dY and X and, with many slices, of the partials.
 #include <hip/hip_runtime.h>
 
@@ -150,6 +153,11 @@ __device__ __forceinline__ void grad_compute(const GradTile<JB>& t, int wave, in
 #undef QN_TR4
 #undef QN_TR
 
+// slot of the first slice of adapter a (of several), whose tokens begin at position `start`
+__device__ __forceinline__ int first_slot(const GradArgs& g, int a, int start) {
+    return min(2 * start / (g.per * kMultiItem), g.plan.first_item[a] / g.per + a);
+}
+
 constexpr int kZero = 4096;          // elements of dB_a, dA_a per workgroup that writes zeros
 
 // zeros for an adapter without tokens: chunk c of its dB_a, then dA_a (sizes multiples of 1024)
@@ -252,7 +260,7 @@ void multi_grad_mfma(GradArgs g) {
     // D of a 32 x 32 tile: lane l holds rows 8 (v / 4) + 4 (l / 32) + v % 4 of column l % 32
     const int64_t Nr = jb.N * g.r;
     float* dst = alone ? jb.out + it.adapter * Nr
-                       : jb.part + (g.plan.first_item[it.adapter] / g.per + it.adapter + it.index / g.per) * Nr;
+                       : jb.part + (first_slot(g, it.adapter, it.pos - it.index * kMultiItem) + it.index / g.per) * Nr;
 #pragma unroll
     for (int k = 0; k < JB; ++k) {
         const int j = j0 + 32 * k + (lane & 31);
@@ -294,7 +302,7 @@ void multi_grad_reduce(GradArgs g, int blocks0) {
     const int j0 = (b % jt) * 16;
     const int64_t Nr = jb.N * g.r;
     const int tid = threadIdx.x;
-    const float* p = jb.part + (slices ? g.plan.first_item[a] / g.per + a : 0) * Nr;
+    const float* p = jb.part + (slices ? first_slot(g, a, lo) : 0) * Nr;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
         const int col = (tid >> 4) + 16 * q, j = tid & 15;
@@ -334,12 +342,18 @@ int per_of(int64_t d_out, int64_t d_in, int64_t M, int r) {
 
 namespace {
 int64_t slots_of(int64_t d_out, int64_t d_in, int64_t M, int n, int r) {
-    return multi_max_items(M, n) / per_of(d_out, d_in, M, r) + n;
+    const int64_t per = per_of(d_out, d_in, M, r);
+    return std::min(2 * M / (per * kMultiItem), multi_max_items(M, n) / per + n);
 }
 }  // namespace
 
+// (Up to 4 MB a slot is counted for every adapter of the pool, used or not: small pools keep the
+// workspace they had when slots were numbered by adapter alone.)
 int64_t multi_grads_part_floats(int64_t d_out, int64_t d_in, int64_t M, int n, int r) {
-    return M <= kOneSlice ? 0 : slots_of(d_out, d_in, M, n, r) * (d_out + d_in) * r;
+    if (M <= kOneSlice) return 0;
+    const int64_t slot = (d_out + d_in) * r, kept = (int64_t{1} << 20) / slot;
+    const int64_t of_pool = multi_max_items(M, n) / per_of(d_out, d_in, M, r) + n;
+    return std::max(slots_of(d_out, d_in, M, n, r), std::min(of_pool, kept)) * slot;
 }
 
 hipError_t launch_multi_grads(const MultiPlan& plan, const uint16_t* X, int64_t ldx, const uint16_t* dY, int64_t lddy,

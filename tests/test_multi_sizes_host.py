@@ -73,3 +73,23 @@ def test_calls_refuse_what_the_queries_answer_0_to(d_out, d_in, d_seq, r, n):
     assert lib.qlora_multi_fwd(*ptrs, d_out, d_in, 0, *pool, FAKE, d_in, d_seq, FAKE, FAKE, d_out, FAKE, 1 << 60, None) == -2
     assert lib.qlora_multi_bwd(*ptrs, d_out, d_in, 0, *pool, FAKE, d_in, FAKE, d_out, d_seq, FAKE, FAKE, d_in, FAKE, FAKE,
                                FAKE, 1 << 60, None) == -2
+
+
+@pytest.mark.parametrize("d_out,d_in,r", [(11008, 4096, 64), (4096, 4096, 16), (256, 256, 16), (4096, 11008, 256), (64, 64, 256)])
+@pytest.mark.parametrize("d_seq", [513, 700, 2000, 4096, 20000])
+def test_backward_workspace_does_not_grow_with_the_pool(d_out, d_in, r, d_seq):
+    """Partial gradients are written by adapters of more than one slice (at least 128 tokens)
+    only: of c > 128 tokens ceil(c / 128) <= 2 c / 128 slices, 2 d_seq / 128 over all adapters,
+    and at most 4 MB are set aside past them."""
+    sizes = [qn.multi_linear_bwd_workspace_bytes(d_out, d_in, d_seq, r, n) for n in (1, 8, 100, 1024)]
+    slot = 4 * (d_out + d_in) * r
+    without = qn.multi_linear_bwd_workspace_bytes(d_out, d_in, 512, r, 1) * d_seq // 512      # all else is linear in d_seq at most
+    for size in sizes:
+        assert size <= without + 2 * d_seq // 128 * slot + (4 << 20) + 4096
+    assert sizes[-1] - sizes[0] <= max(2 * d_seq // 128 * slot, 4 << 20)
+
+
+def test_backward_workspace_of_one_token_more():
+    """512 tokens need no partial gradients; one more costs at most 8 slots of them."""
+    few, more = (qn.multi_linear_bwd_workspace_bytes(11008, 4096, m, 64, 1024) for m in (512, 513))
+    assert more - few <= 8 * 4 * (11008 + 4096) * 64 + (1 << 20)
