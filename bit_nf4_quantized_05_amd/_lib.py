@@ -757,7 +757,7 @@ def adamw_step(state: AdamWState, step, lr, beta1: float = 0.9, beta2: float = 0
                weight_decay: float = 0.01, grad_scale: torch.Tensor | None = None, seed: int = 0) -> None:
     """qlora_adamw_step: one AdamW step in place over all tensors of the state. step (1 for
     the first) and lr may be one-element device tensors (int64, float32), read when the step
-    runs, for calls captured in a graph; grad_scale is a one-element float32 device tensor
+    runs, for calls captured in a graph (a device step below 1 changes nothing); grad_scale is a one-element float32 device tensor
     that multiplies the gradients."""
     dev = state.device
     step_dev = _scalar(step, torch.int64, "step", dev) if isinstance(step, torch.Tensor) else None

@@ -152,6 +152,7 @@ void adamw_kernel(AdamArgs a, Coefs hc) {
     uint32_t step = static_cast<uint32_t>(a.step);
     if (a.step_dev || a.lr_dev) {
         const int64_t n = a.step_dev ? a.step_dev[0] : a.step;
+        if (n < 1) return;                              // 1 - beta^n would be 0 or less; nothing is written
         const double b2t = power(a.beta2, n);
         c = coefs_of(a.lr_dev ? static_cast<double>(a.lr_dev[0]) : a.lr, a.beta1, a.beta2, a.weight_decay,
                      power(a.beta1, n), b2t, sqrt(1.0 - b2t));

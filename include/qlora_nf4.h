@@ -448,7 +448,8 @@ int64_t qlora_adamw_table(void* const* p, const void* const* g, uint16_t* const*
                           int flags, void* table);
 /* One step. `table` is the device copy of the table for `count` tensors and `n_chunks`
  * chunks. step >= 1 and lr are used unless lr_dev / step_dev (device scalars, for calls
- * captured in a HIP graph) are given; 0 <= beta < 1, eps > 0. m, v 16-byte aligned. */
+ * captured in a HIP graph) are given; with *step_dev below 1 the call changes nothing.
+ * 0 <= beta < 1, eps > 0. m, v 16-byte aligned. */
 int qlora_adamw_step(const void* table, int count, int64_t n_chunks, int flags, void* m, void* v, float* m_scale,
                      float* v_scale, int64_t step, const int64_t* step_dev, double lr, const float* lr_dev,
                      double beta1, double beta2, double eps, double weight_decay, const float* grad_scale,
