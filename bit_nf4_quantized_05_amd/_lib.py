@@ -711,6 +711,17 @@ def _adamw_flags(params, grads, copies, bits) -> int:
             (_PARAM_BF16 if pt == torch.bfloat16 else 0))
 
 
+def _adamw_own_memory(params, copies) -> None:
+    """Every written element belongs to one tensor (a bfloat16 parameter may be its own copy)."""
+    spans = [(p.data_ptr(), p.data_ptr() + p.nbytes, f"params[{i}]") for i, p in enumerate(params)]
+    spans += [(c.data_ptr(), c.data_ptr() + c.nbytes, f"copies[{i}]") for i, c in enumerate(copies or [])
+              if c is not None and (c.data_ptr(), c.dtype) != (params[i].data_ptr(), params[i].dtype)]
+    spans = sorted(s for s in spans if s[1] > s[0])
+    for (_, end, a), (start, _, b) in zip(spans, spans[1:]):
+        if start < end:
+            raise ValueError(f"{a} and {b} share memory: one step would update it twice")
+
+
 def _adamw_table(params, grads, copies, flags):
     """(the table in host memory, its chunks)."""
     k = len(params)
@@ -734,6 +745,7 @@ def adamw_state(params, grads, copies=None, bits: int = 32) -> AdamWState:
     params, grads = list(params), list(grads)
     copies = list(copies) if copies is not None else None
     flags = _adamw_flags(params, grads, copies, bits)
+    _adamw_own_memory(params, copies)
     dev = params[0].device
     offsets, blocks = [], 0
     for p in params:

@@ -411,6 +411,7 @@ int qlora_multi_bwd(const uint8_t* codes, const int8_t* qconst, const float* qsc
  *   p[i], g[i]   parameters and gradient of tensor i, n[i] >= 0 elements, contiguous;
  *                float32 or bf16 as the step's flags say, aligned to their element
  *   copy[i]      bf16 copy of the new parameters, or NULL (copy itself may be NULL)
+ * The parameters and copies of a table must not overlap (a workgroup each updates them at once).
  * State arrays are shared by all tensors: tensor i has ceil(n[i] / 256) blocks of 256
  * elements, after those of the tensors before it, so element e of tensor i is at
  * 256 * (blocks before it) + e. State past a tensor's last element is kept at zero. All
