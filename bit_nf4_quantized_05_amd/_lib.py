@@ -590,6 +590,14 @@ def _multi_workspace(workspace: torch.Tensor | None, need, d_out, d_in, d_seq, p
     return workspace
 
 
+def _multi_output(t: torch.Tensor, shape, name: str, dev, *inputs: torch.Tensor) -> int:
+    """Row stride of an output that is none of the inputs (they are read while it is written)."""
+    ld = _rows(t, torch.bfloat16, shape, name, dev)
+    if any(t.data_ptr() == x.data_ptr() for x in inputs):
+        raise ValueError(f"{name} is an input of the call")
+    return ld
+
+
 def multi_linear_fwd(q: NF4Weight, pool: AdapterPool, plan: MultiPlan, X: torch.Tensor,
                      out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """qlora_multi_fwd: Y[t] = W_hat x_t + s_a B_a (A_a x_t), a the adapter of token t in the
@@ -604,7 +612,7 @@ def multi_linear_fwd(q: NF4Weight, pool: AdapterPool, plan: MultiPlan, X: torch.
     if out is None:
         o, ldy = X.new_empty((d_seq, d_out)), d_out
     else:
-        o, ldy = out, _rows(out, torch.bfloat16, (d_seq, d_out), "out", dev)
+        o, ldy = out, _multi_output(out, (d_seq, d_out), "out", dev, X)
     ws = _multi_workspace(workspace, multi_linear_fwd_workspace_bytes, d_out, d_in, d_seq, pool, dev)
     rc = lib().qlora_multi_fwd(q.codes.data_ptr(), q.qconst.data_ptr(), q.qscale.data_ptr(), q.qmean.data_ptr(), d_out,
                                d_in, _dq_code(q.dq), pool.A.data_ptr(), pool.B.data_ptr(), pool.s.data_ptr(), pool.n,
@@ -631,7 +639,7 @@ def multi_linear_bwd(q: NF4Weight, pool: AdapterPool, plan: MultiPlan, X: torch.
     if dX is None:
         gx, lddx = X.new_empty((d_seq, d_in)), d_in
     else:
-        gx, lddx = dX, _rows(dX, torch.bfloat16, (d_seq, d_in), "dX", dev)
+        gx, lddx = dX, _multi_output(dX, (d_seq, d_in), "dX", dev, X, dY)
     ga = dA if dA is not None else torch.empty(n, r, d_in, dtype=torch.float32, device=dev)
     gb = dB if dB is not None else torch.empty(n, d_out, r, dtype=torch.float32, device=dev)
     if dA is not None:

@@ -355,7 +355,8 @@ int qlora_lora_grads(const uint16_t* A, const uint16_t* B, int r, float s,
  *   ids   int32 [d_seq]: the adapter of each token, or any value outside [0, n) for none
  *   plan  qlora_multi_plan_bytes(d_seq, n) bytes of device memory: the tokens sorted by
  *         adapter (stable) and the work lists of the calls below
- * The calls below must be given a plan made for their d_seq and n.
+ * The calls below must be given a plan made for their d_seq and n. Their outputs and workspace
+ * must not overlap an input, or each other.
  */
 #define QN_MULTI_MAX_ADAPTERS 1024
 int64_t qlora_multi_plan_bytes(int64_t d_seq, int n);

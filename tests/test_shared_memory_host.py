@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import bit_nf4_quantized_05_amd as qn
+from bit_nf4_quantized_05_amd import _lib
 
 
 def test_parameters_that_overlap():
@@ -31,3 +32,19 @@ def test_tensors_side_by_side_are_taken():
     st = qn.adamw_state([buf[300:], buf[:300], buf[5:5]], [g[300:], g[300:600], g[:0]], copies=[c[:700], c[700:], None])
     assert st.blocks == 3 + 2
     assert qn.adamw_state([c[:300]], [g[:300]], copies=[c[:300]]).blocks == 2      # the parameters' own bfloat16
+
+
+def _batch(d_out=64, d_in=64, M=5):
+    q, pool = qn.alloc_weight(d_out, d_in, "cpu"), qn.alloc_pool(3, 16, d_out, d_in, "cpu")
+    return q, pool, _lib.MultiPlan(torch.zeros(4096, dtype=torch.uint8), M, 3), torch.zeros(M, d_in).bfloat16()
+
+
+def test_output_that_is_an_input():
+    q, pool, plan, X = _batch()
+    dY = torch.zeros_like(X)
+    with pytest.raises(ValueError, match="out"):
+        qn.multi_linear_fwd(q, pool, plan, X, out=X)
+    with pytest.raises(ValueError, match="dX"):
+        qn.multi_linear_bwd(q, pool, plan, X, dY, dX=X)
+    with pytest.raises(ValueError, match="dX"):
+        qn.multi_linear_bwd(q, pool, plan, X, dY, dX=dY)
