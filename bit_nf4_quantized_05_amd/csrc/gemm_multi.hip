@@ -327,22 +327,20 @@ __device__ __forceinline__ void gemm_multi_body(const MultiGemm& mg, int bid) {
         }
 #undef QN_HALF
     } else {
-    stage = KT & 1;
-    __builtin_amdgcn_s_waitcnt(0);              // (the adapter list's LDS writes too)
-    QN_BARRIER();
-    QN_FRAGS(g_st0, chs[0], fa)
-    // the last main step stands outside the loop, which then has no branch in it
-    int kt = 0;
-    for (; kt + 2 < KT; kt += 2) {
-        QN_MAIN(kt, g_st0, g_st1)
-        QN_MAIN(kt + 1, g_st1, g_st0)
-    }
-    if (kt + 1 < KT) QN_MAIN(kt, g_st0, g_st1)
-    {
+        stage = KT & 1;
+        __builtin_amdgcn_s_waitcnt(0);          // (the adapter list's LDS writes too)
+        QN_BARRIER();
+        QN_FRAGS(g_st0, chs[0], fa)
+        // the last main step stands outside the loop, which then has no branch in it
+        int kt = 0;
+        for (; kt + 2 < KT; kt += 2) {
+            QN_MAIN(kt, g_st0, g_st1)
+            QN_MAIN(kt + 1, g_st1, g_st0)
+        }
+        if (kt + 1 < KT) QN_MAIN(kt, g_st0, g_st1)
         const uint4* cur = (KT & 1) ? g_st0 : g_st1;
         uint4* nxt = (KT & 1) ? g_st1 : g_st0;
         QN_LAST(cur, nxt)
-    }
     }
 #undef QN_LAST
 #undef QN_MAIN

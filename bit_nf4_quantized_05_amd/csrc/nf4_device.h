@@ -105,18 +105,4 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
     return __builtin_bit_cast(uint16_t, static_cast<__bf16>(v));
 }
 
-// v rounded to bf16; v keeps what the rounding left (nothing of an infinity or NaN)
-__device__ __forceinline__ uint16_t take_bf16(float& v) {
-    const uint16_t h = bf16_bits(v);
-    const float f = __uint_as_float(static_cast<uint32_t>(h) << 16);
-    v = fabsf(f) < __builtin_inff() ? v - f : 0.0f;
-    return h;
-}
-
-// 4 values as their next bf16 terms; the values keep the remainders
-__device__ __forceinline__ uint2 take_bf16x4(float (&v)[4]) {
-    const uint32_t a = take_bf16(v[0]), b = take_bf16(v[1]), c = take_bf16(v[2]), d = take_bf16(v[3]);
-    return uint2{a | (b << 16), c | (d << 16)};
-}
-
 }  // namespace qn
