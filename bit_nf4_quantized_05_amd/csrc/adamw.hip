@@ -20,8 +20,8 @@
 // names tensor and place), one wave per block, 4 elements per lane: every access is 16
 // bytes a lane (4 for codes) and the block's largest magnitude is a wave reduction. Bound by
 // HBM: p, g, m, v are read and p, m, v and the bf16 copy written once. 160 M float32
-// parameters with float32 gradients: 870 us, 5.5 TB/s (a 1 GiB device copy runs at 5.1); with
-// 8-bit moments 565 us, 5.1 TB/s. Chunks of 8 blocks, two per wave: 908 and 540 us, but
+// parameters with float32 gradients and bf16 copies: 870 us, 5.5 TB/s (a 1 GiB device copy runs at
+// 5.1); with 8-bit moments 553 to 569 us, 5.2 TB/s. Chunks of 8 blocks, two per wave: 908 and 540 us, but
 // later to fill the chip with small sets (4 tensors of 8000 elements: 5.4 against 4.9 us a
 // graph-replayed call); of 16: 895 and 545 us.
 #include <hip/hip_runtime.h>
