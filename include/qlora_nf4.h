@@ -373,7 +373,7 @@ int64_t qlora_multi_bwd_workspace_bytes(int64_t d_out, int64_t d_in, int64_t d_s
  * the limit). s_a A_a x_t keeps 16 bits or more (two bf16 terms; float32 for one token with r = 16
  * and d_in <= 4096); accumulation in float32, one final rounding.
  * A token's result depends on its own adapter only: an infinity or NaN in another's weights
- * does not reach it. Up to 64 tokens stream the packed codes (a decode batch); more run the
+ * does not reach it (one in its own shows as an infinity or NaN). Up to 64 tokens stream the packed codes (a decode batch); more run the
  * MFMA GEMM on W_hat dequantised into the workspace.
  */
 int qlora_multi_fwd(const uint8_t* codes, const int8_t* qconst, const float* qscale, const float* qmean,
