@@ -74,6 +74,16 @@ SIGNATURES = {
     "qlora_adamw_step": (_c_int, [_c_vp, _c_int, _c_i64, _c_int, _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp, _c_double,
                                   _c_vp, _c_double, _c_double, _c_double, _c_double, _c_vp, ctypes.c_uint32, _c_vp]),
     "qlora_adamw_moments": (_c_int, [_c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp, _c_vp, _c_vp]),
+    "qlora_gated_fwd_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64, _c_int]),
+    "qlora_gated_bwd_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64, _c_int]),
+    "qlora_gated_fwd": (_c_int, [_c_vp] * 8 + [_c_i64, _c_i64, _c_int] + [_c_vp, _c_vp, _c_float] * 2 +
+                        [_c_int, _c_int, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp]),
+    "qlora_gated_bwd": (_c_int, [_c_vp] * 8 + [_c_i64, _c_i64, _c_int] + [_c_vp, _c_vp, _c_float] * 2 +
+                        [_c_int, _c_int, _c_vp, _c_i64, _c_vp, _c_i64, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp,
+                         _c_i64, _c_vp]),
+    "qlora_head_loss_workspace_bytes": (_c_i64, [_c_i64, _c_i64, _c_i64, _c_int, _c_int]),
+    "qlora_head_loss": (_c_int, [_c_vp, _c_i64, _c_vp, _c_vp, _c_vp, _c_vp, _c_int, _c_i64, _c_i64, _c_vp, _c_i64, _c_i64,
+                                 _c_vp, _c_vp, _c_vp, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp]),
     "qn_profile_enable": (_c_int, [_c_int]),
     "qn_profile_read": (_c_int, [_c_vp, _c_int, _c_vp, _c_vp, _c_int]),
     "qn_profile_durations": (_c_int, [ctypes.c_char_p, _c_vp, _c_int]),
@@ -654,6 +664,185 @@ def multi_linear_bwd(q: NF4Weight, pool: AdapterPool, plan: MultiPlan, X: torch.
     if rc:
         _check(rc, "qlora_multi_bwd")
     return gx, ga, gb
+
+
+# ---- the gated feed-forward block -------------------------------------------------
+
+ACT_CODES = {"silu": 0, "gelu": 1}      # the QN_ACT_* codes of the header
+
+
+@dataclass(frozen=True)
+class GatedLayer:
+    """A gated feed-forward block's two projections: NF4 weights gate and up, both
+    [d_ff, d_in] in one format, their adapters A bfloat16 [r, d_in], B bfloat16 [d_ff, r] and
+    scales s (one rank for both; all four tensors None: no adapters), and the activation of
+    the gate, "silu" or "gelu" (the tanh form). Checked when it is made; the tensors' contents
+    may change, the tensors may not be replaced."""
+    gate: NF4Weight
+    up: NF4Weight
+    A_gate: torch.Tensor | None = None
+    B_gate: torch.Tensor | None = None
+    s_gate: float = 1.0
+    A_up: torch.Tensor | None = None
+    B_up: torch.Tensor | None = None
+    s_up: float = 1.0
+    act: str = "silu"
+    r: int = field(init=False)
+    d_in: int = field(init=False)
+    d_ff: int = field(init=False)
+    device: torch.device = field(init=False)
+    weights: tuple = field(init=False, repr=False)     # the leading arguments of both calls
+
+    def __post_init__(self):
+        g, u = self.gate, self.up
+        if (g.d_out, g.d_in, g.dq) != (u.d_out, u.d_in, u.dq) or g.device != u.device:
+            raise ValueError("the gate and up weights must have one shape, format and device")
+        if self.act not in ACT_CODES:
+            raise ValueError(f"act must be one of {sorted(ACT_CODES)}, got {self.act!r}")
+        pairs = (("gate", self.A_gate, self.B_gate), ("up", self.A_up, self.B_up))
+        tensors = [t for _, *ab in pairs for t in ab]
+        r, dev = 0, g.codes.device
+        if any(t is not None for t in tensors):
+            if any(t is None for t in tensors):
+                raise ValueError("both projections need an adapter, or neither")
+            r = self.A_gate.shape[0]
+            for name, A, B in pairs:
+                _need(A, torch.bfloat16, (r, g.d_in), f"A_{name}", dev)
+                _need(B, torch.bfloat16, (g.d_out, r), f"B_{name}", dev)
+        ptr = [t.data_ptr() if t is not None else None for t in tensors]
+        weights = tuple(t.data_ptr() for w in (g, u) for t in (w.codes, w.qconst, w.qscale, w.qmean)) + (
+            g.d_out, g.d_in, _dq_code(g.dq), ptr[0], ptr[1], float(self.s_gate), ptr[2], ptr[3], float(self.s_up), r,
+            ACT_CODES[self.act])
+        for name, v in (("r", r), ("d_in", g.d_in), ("d_ff", g.d_out), ("device", dev), ("weights", weights)):
+            object.__setattr__(self, name, v)
+
+
+def gated_fwd_workspace_bytes(d_ff: int, d_in: int, d_seq: int, r: int) -> int:
+    return lib().qlora_gated_fwd_workspace_bytes(d_ff, d_in, d_seq, r)
+
+
+def gated_bwd_workspace_bytes(d_ff: int, d_in: int, d_seq: int, r: int) -> int:
+    return lib().qlora_gated_bwd_workspace_bytes(d_ff, d_in, d_seq, r)
+
+
+def _workspace(workspace: torch.Tensor | None, need, dev) -> torch.Tensor:
+    """The caller's workspace (contiguous memory on the device) or a new one of need() bytes."""
+    if workspace is None:
+        return torch.empty(max(need(), 1), dtype=torch.uint8, device=dev)
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace: expected contiguous memory on {dev}")
+    return workspace
+
+
+def _output(t: torch.Tensor | None, shape, name: str, dev, *inputs: torch.Tensor):
+    """(a new contiguous output or the given one, its row stride)."""
+    if t is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=dev), shape[1]
+    return t, _multi_output(t, shape, name, dev, *inputs)
+
+
+def gated_fwd(layer: GatedLayer, X: torch.Tensor, save: bool = False, out: torch.Tensor | None = None,
+              GU: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """qlora_gated_fwd: H [d_seq, d_ff] = act(G) * U. With save (or GU given) (H, GU), GU
+    [d_seq, 2 d_ff] holding G beside U for ``gated_bwd``. X, out and GU may be row views of
+    wider arrays."""
+    dev, d_ff, d_in = layer.device, layer.d_ff, layer.d_in
+    if X.dim() != 2 or X.shape[1] != d_in:
+        raise ValueError(f"input must be [d_seq, {d_in}]")
+    d_seq = X.shape[0]
+    ldx = _rows(X, torch.bfloat16, X.shape, "input", dev)
+    o, ldh = _output(out, (d_seq, d_ff), "out", dev, X)
+    gu, ldgu = _output(GU, (d_seq, 2 * d_ff), "GU", dev, X, o) if save or GU is not None else (None, 0)
+    ws = _workspace(workspace, lambda: gated_fwd_workspace_bytes(d_ff, d_in, d_seq, layer.r), dev)
+    rc = lib().qlora_gated_fwd(*layer.weights, X.data_ptr(), ldx, d_seq, o.data_ptr(), ldh,
+                               None if gu is None else gu.data_ptr(), ldgu, ws.data_ptr(), ws.nbytes, _stream(dev))
+    if rc:
+        _check(rc, "qlora_gated_fwd")
+    return o if gu is None else (o, gu)
+
+
+def gated_bwd(layer: GatedLayer, GU: torch.Tensor, dH: torch.Tensor, dX: torch.Tensor | None = None,
+              dGU: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """qlora_gated_bwd: (dX bfloat16 [d_seq, d_in], dGU bfloat16 [d_seq, 2 d_ff] = dG beside dU)
+    of ``gated_fwd`` for the loss gradient dH and the GU that it kept. dGU may be GU itself. The
+    adapters' gradients are ``lora_grads(A, B, s, X, half)`` with the halves dGU[:, :d_ff] (gate)
+    and dGU[:, d_ff:] (up)."""
+    dev, d_ff, d_in = layer.device, layer.d_ff, layer.d_in
+    if GU.dim() != 2 or dH.dim() != 2 or GU.shape[0] != dH.shape[0]:
+        raise ValueError("GU [d_seq, 2 d_ff] and dH [d_seq, d_ff] must share d_seq")
+    d_seq = GU.shape[0]
+    ldgu = _rows(GU, torch.bfloat16, (d_seq, 2 * d_ff), "GU", dev)
+    lddh = _rows(dH, torch.bfloat16, (d_seq, d_ff), "dH", dev)
+    if dGU is GU:
+        dgu, lddgu = GU, ldgu
+    else:
+        dgu, lddgu = _output(dGU, (d_seq, 2 * d_ff), "dGU", dev, GU, dH)
+    gx, lddx = _output(dX, (d_seq, d_in), "dX", dev, GU, dH, dgu)
+    ws = _workspace(workspace, lambda: gated_bwd_workspace_bytes(d_ff, d_in, d_seq, layer.r), dev)
+    rc = lib().qlora_gated_bwd(*layer.weights, GU.data_ptr(), ldgu, dH.data_ptr(), lddh, d_seq, dgu.data_ptr(), lddgu,
+                               gx.data_ptr(), lddx, ws.data_ptr(), ws.nbytes, _stream(dev))
+    if rc:
+        _check(rc, "qlora_gated_bwd")
+    return gx, dgu
+
+
+# ---- the loss over a large vocabulary ----------------------------------------------
+
+def head_loss_workspace_bytes(head, d_seq: int, grad: bool = False) -> int:
+    """Workspace of ``head_loss`` (grad: of ``head_loss_grad``) for d_seq tokens on this head."""
+    nf4 = isinstance(head, NF4Weight)
+    vocab, d_in = (head.d_out, head.d_in) if nf4 else head.shape
+    return lib().qlora_head_loss_workspace_bytes(vocab, d_in, d_seq, int(nf4), int(grad))
+
+
+def _head_loss(head, X, target, scale, grad, loss, dX, workspace):
+    if isinstance(head, NF4Weight):
+        vocab, d_in, dev = head.d_out, head.d_in, head.device
+        args = (None, 0, head.codes.data_ptr(), head.qconst.data_ptr(), head.qscale.data_ptr(), head.qmean.data_ptr(),
+                _dq_code(head.dq))
+    else:
+        if head.dim() != 2:
+            raise ValueError("head: expected bfloat16 [vocab, d_in] or an NF4Weight")
+        (vocab, d_in), dev = head.shape, head.device
+        args = (head.data_ptr(), _rows(head, torch.bfloat16, (vocab, d_in), "head", dev), None, None, None, None, 0)
+    if X.dim() != 2 or X.shape[1] != d_in:
+        raise ValueError(f"input must be [d_seq, {d_in}]")
+    d_seq = X.shape[0]
+    ldx = _rows(X, torch.bfloat16, X.shape, "input", dev)
+    _need(target, torch.int64, (d_seq,), "target", dev)
+    if scale is not None:
+        _need(scale, torch.float32, (d_seq,), "scale", dev)
+    if loss is None:
+        loss = torch.empty(d_seq, dtype=torch.float32, device=dev)
+    else:
+        _need(loss, torch.float32, (d_seq,), "loss", dev)
+        if scale is not None and loss.data_ptr() == scale.data_ptr():
+            raise ValueError("loss is an input of the call")
+    gx, lddx = _output(dX, (d_seq, d_in), "dX", dev, X) if grad else (None, 0)
+    ws = _workspace(workspace, lambda: head_loss_workspace_bytes(head, d_seq, grad), dev)
+    rc = lib().qlora_head_loss(*args, vocab, d_in, X.data_ptr(), ldx, d_seq, target.data_ptr(),
+                               None if scale is None else scale.data_ptr(), loss.data_ptr(),
+                               None if gx is None else gx.data_ptr(), lddx, ws.data_ptr(), ws.nbytes, _stream(dev))
+    if rc:
+        _check(rc, "qlora_head_loss")
+    return loss, gx
+
+
+def head_loss(head, X: torch.Tensor, target: torch.Tensor, loss: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """qlora_head_loss without the gradient: float32 [d_seq], the softmax cross entropy of each
+    token over a head of vocab rows (bfloat16 [vocab, d_in], or an NF4Weight) for X [d_seq, d_in]
+    and int64 targets; a target outside [0, vocab) is not counted (loss 0). The logits are never
+    kept."""
+    return _head_loss(head, X, target, None, False, loss, None, workspace)[0]
+
+
+def head_loss_grad(head, X: torch.Tensor, target: torch.Tensor, scale: torch.Tensor | None = None,
+                   loss: torch.Tensor | None = None, dX: torch.Tensor | None = None,
+                   workspace: torch.Tensor | None = None):
+    """qlora_head_loss: (loss, dX), dX bfloat16 [d_seq, d_in] the gradient of sum(scale * loss) to X
+    (scale float32 [d_seq], None: 1; zeros for a token that is not counted), in the same pass."""
+    return _head_loss(head, X, target, scale, True, loss, dX, workspace)
 
 
 # ---- AdamW over many tensors -----------------------------------------------------

@@ -1,8 +1,8 @@
 // extern "C" entry points of libqlora_nf4: argument checks, workspace layout and
 // kernel sequencing. Every step of the layer runs in the kernels of quantize.hip,
 // prologue.hip, gemm_nt.hip, gemv.hip, skinny.hip, lora_grads.hip, factors.hip,
-// multi_plan.hip, multi_small.hip, gemm_multi.hip, multi_grads.hip and adamw.hip; this file does
-// no arithmetic on the data.
+// multi_plan.hip, multi_small.hip, gemm_multi.hip, multi_grads.hip, adamw.hip, gated.hip and
+// head_loss.hip; this file does no arithmetic on the data.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -15,6 +15,8 @@
 #include <vector>
 
 #include "../../include/qlora_nf4.h"
+#include "gated.h"
+#include "head_loss.h"
 #include "internal.h"
 #include "multi.h"
 
@@ -297,6 +299,99 @@ GradWs grad_ws(int64_t d_out, int64_t d_in, int64_t d_seq, int r) {
     w.ppart1 = off; off += align_up(prepass_part_bytes(d_seq, d_out, r), 256);     // dY B K-split partials
     w.bytes = off;
     return w;
+}
+}  // namespace
+
+// workspaces of qlora_gated_fwd and qlora_gated_bwd
+namespace {
+struct GatedWs {
+    int64_t what, t, adapt, ppart[2], bt[2], part, bytes;
+};
+
+GatedWs gated_ws(int64_t d_ff, int64_t d_in, int64_t d_seq, int r, bool bwd) {
+    GatedWs w{};
+    int64_t off = 0;
+    auto take = [&off](int64_t bytes) {
+        const int64_t at = off;
+        off += align_up(bytes, 256);
+        return at;
+    };
+    w.what = take(4 * d_ff * d_in);                                                  // both weights
+    w.t = take(2 * d_seq * qn::gated_k2(r));                                         // both rank products
+    w.adapt = take(2 * (bwd ? d_in : 2 * d_ff) * qn::gated_k2(r));                   // both adapters
+    for (int i = 0; i < 2; ++i) {
+        w.ppart[i] = take(r > 0 ? prepass_part_bytes(d_seq, bwd ? d_ff : d_in, r) : 0);
+        w.bt[i] = take(bwd && !qn::prepass_takes_kmajor(r) ? 2 * static_cast<int64_t>(r) * d_ff : 0);
+    }
+    w.part = take(4 * (bwd ? qn::gemm_split_part_floats(d_seq, d_in, 2 * d_ff) : qn::gated_part_floats(d_seq, d_ff, d_in)));
+    w.bytes = off;
+    return w;
+}
+
+// Whether an operand that the call makes reaches 4 GiB (sizes >= 1): both weights, the rank
+// products or the adapters' layouts
+bool gated_too_large(int64_t d_ff, int64_t d_in, int64_t d_seq, int r) {
+    const int64_t k2 = std::max(1, qn::gated_k2(r));
+    return reaches_4gib(2 * d_ff, std::max(d_in, k2)) || reaches_4gib(std::max(d_seq, d_in), k2);
+}
+
+bool gated_sizes_ok(int64_t d_ff, int64_t d_in, int64_t d_seq, int r) {
+    return d_ff >= 1 && d_in >= 1 && d_seq >= 1 && r >= 0 && r <= 256 && d_ff % 64 == 0 && d_in % 64 == 0 &&
+           d_in <= INT32_MAX && d_ff <= INT32_MAX / 2 && d_seq <= INT32_MAX && !gated_too_large(d_ff, d_in, d_seq, r) &&
+           !reaches_4gib(d_seq, std::max(2 * d_ff, d_in));
+}
+
+// What both gated calls check; `rows` are the row strides of the call's activations, each at
+// least its row length.
+int check_gated(const uint8_t* const (&codes)[2], const int8_t* const (&qconst)[2], const float* const (&qscale)[2],
+                const float* const (&qmean)[2], int64_t d_ff, int64_t d_in, int dq, const uint16_t* const (&A)[2],
+                const uint16_t* const (&B)[2], const float (&s)[2], int r, int act, int64_t d_seq, qn::GatedCall* c) {
+    for (int i = 0; i < 2; ++i) {
+        if (int rc = make_consts(dq, codes[i], qconst[i], qscale[i], qmean[i], &c->bc[i])) return rc;
+        if (r > 0 && (!A[i] || !B[i])) return fail(-1, "null pointer argument");
+        if (!aligned(codes[i], 16) || !aligned(A[i], 16) || !aligned(B[i], 16))
+            return fail(-1, "misaligned pointer (16 B for arrays, 256 B for the workspace)");
+        c->codes[i] = codes[i]; c->A[i] = A[i]; c->B[i] = B[i]; c->s[i] = s[i];
+    }
+    if (d_ff < 1 || d_in < 1 || d_seq < 1) return fail(-1, "sizes must be >= 1");
+    if (r < 0 || r > 256) return fail(-1, "r must be in [0, 256]");
+    if (act != QN_ACT_SILU && act != QN_ACT_GELU) return fail(-1, "unknown activation");
+    if (d_in % 64 != 0 || d_ff % 64 != 0) return fail(-2, "d_in and d_ff must be multiples of 64");
+    if (d_in > INT32_MAX || d_ff > INT32_MAX / 2 || d_seq > INT32_MAX) return fail(-2, "dimension too large");
+    if (gated_too_large(d_ff, d_in, d_seq, r)) return fail(-2, "an operand reaches 4 GiB");
+    c->d_ff = d_ff; c->d_in = d_in; c->M = d_seq; c->r = r; c->act = act;
+    return 0;
+}
+
+static_assert(QN_ACT_SILU == qn::kActSilu && QN_ACT_GELU == qn::kActGelu, "activation codes");
+
+// one activation of a gated call: `cols` wide at row stride ld
+int check_rows(const uint16_t* p, int64_t rows, int64_t cols, int64_t ld) {
+    if (!p) return fail(-1, "null pointer argument");
+    if (!aligned(p, 16)) return fail(-1, "misaligned pointer (16 B for arrays, 256 B for the workspace)");
+    if (ld < cols) return fail(-1, "a leading dimension is smaller than its row");
+    if (ld % 8 != 0) return fail(-1, "leading dimensions must be multiples of 8 elements");
+    if (reaches_4gib(rows, ld)) return fail(-2, "an operand reaches 4 GiB");
+    return 0;
+}
+
+// The sizes of a qlora_head_loss call, and its plan.
+int head_sizes(int64_t vocab, int64_t d_in, int64_t d_seq, bool nf4, bool grad, qn::HeadPlan* p) {
+    if (vocab < 1 || d_in < 1 || d_seq < 1) return fail(-1, "sizes must be >= 1");
+    if (d_in % 64 != 0 || (nf4 && vocab % 64 != 0)) return fail(-2, "d_in (and an NF4 head's rows) must be multiples of 64");
+    if (d_in > INT32_MAX / 2 || vocab > INT32_MAX / 2 || d_seq > INT32_MAX / 2) return fail(-2, "dimension too large");
+    int64_t n, n_b, n_g;
+    if (!nf4_counts(vocab, d_in, &n, &n_b, &n_g)) return fail(-2, "weight too large");
+    if (reaches_4gib(d_seq, d_in) || !qn::head_plan(vocab, d_in, d_seq, nf4, grad, p))
+        return fail(-2, "an operand reaches 4 GiB");
+    return 0;
+}
+
+int check_workspace(const void* ws, int64_t given, int64_t need) {
+    if (!ws) return fail(-1, "null pointer argument");
+    if (!aligned(ws, 256)) return fail(-1, "misaligned pointer (16 B for arrays, 256 B for the workspace)");
+    if (given < need) return fail(-3, "workspace too small");
+    return 0;
 }
 }  // namespace
 
@@ -952,6 +1047,127 @@ int qlora_adamw_moments(const uint8_t* m, const float* m_scale, const uint8_t* v
     hipError_t e = qn::launch_adamw_moments(m, m_scale, v, v_scale, blocks, m_out, v_out,
                                             static_cast<hipStream_t>(stream));
     if (e != hipSuccess) return hip_fail(e, "qlora_adamw_moments");
+    return 0;
+}
+
+int64_t qlora_gated_fwd_workspace_bytes(int64_t d_ff, int64_t d_in, int64_t d_seq, int r) {
+    return gated_sizes_ok(d_ff, d_in, d_seq, r) ? gated_ws(d_ff, d_in, d_seq, r, false).bytes : 0;
+}
+
+int64_t qlora_gated_bwd_workspace_bytes(int64_t d_ff, int64_t d_in, int64_t d_seq, int r) {
+    return gated_sizes_ok(d_ff, d_in, d_seq, r) ? gated_ws(d_ff, d_in, d_seq, r, true).bytes : 0;
+}
+
+int qlora_gated_fwd(const uint8_t* codes_g, const int8_t* qconst_g, const float* qscale_g, const float* qmean_g,
+                    const uint8_t* codes_u, const int8_t* qconst_u, const float* qscale_u, const float* qmean_u,
+                    int64_t d_ff, int64_t d_in, int dq, const uint16_t* A_g, const uint16_t* B_g, float s_g,
+                    const uint16_t* A_u, const uint16_t* B_u, float s_u, int r, int act, const uint16_t* X, int64_t ldx,
+                    int64_t d_seq, uint16_t* H, int64_t ldh, uint16_t* GU, int64_t ldgu, void* workspace,
+                    int64_t workspace_bytes, void* stream) {
+    qn::GatedCall c{};
+    if (int rc = check_gated({codes_g, codes_u}, {qconst_g, qconst_u}, {qscale_g, qscale_u}, {qmean_g, qmean_u}, d_ff, d_in,
+                             dq, {A_g, A_u}, {B_g, B_u}, {s_g, s_u}, r, act, d_seq, &c))
+        return rc;
+    if (int rc = check_rows(X, d_seq, d_in, ldx)) return rc;
+    if (int rc = check_rows(H, d_seq, d_ff, ldh)) return rc;
+    if (GU != nullptr)
+        if (int rc = check_rows(GU, d_seq, 2 * d_ff, ldgu)) return rc;
+    const GatedWs w = gated_ws(d_ff, d_in, d_seq, r, false);
+    if (int rc = check_workspace(workspace, workspace_bytes, w.bytes)) return rc;
+    char* ws = static_cast<char*>(workspace);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    qn::GatedProlog o{};
+    o.what = reinterpret_cast<uint16_t*>(ws + w.what);
+    o.adapt = reinterpret_cast<uint16_t*>(ws + w.adapt);
+    o.pre_in = X; o.ld_in = ldx;
+    o.pre_out = reinterpret_cast<uint16_t*>(ws + w.t);
+    for (int i = 0; i < 2; ++i) o.ppart[i] = reinterpret_cast<float*>(ws + w.ppart[i]);
+    hipError_t e = qn::launch_gated_prologue(c, false, o, st);
+    if (e != hipSuccess) return hip_fail(e, "qlora_gated_fwd (prologue)");
+    e = qn::launch_gated_gemm(c, X, ldx, o.what, o.pre_out, o.adapt, H, ldh, GU, ldgu, reinterpret_cast<float*>(ws + w.part),
+                              st);
+    if (e != hipSuccess) return hip_fail(e, "qlora_gated_fwd (gemm)");
+    return 0;
+}
+
+int qlora_gated_bwd(const uint8_t* codes_g, const int8_t* qconst_g, const float* qscale_g, const float* qmean_g,
+                    const uint8_t* codes_u, const int8_t* qconst_u, const float* qscale_u, const float* qmean_u,
+                    int64_t d_ff, int64_t d_in, int dq, const uint16_t* A_g, const uint16_t* B_g, float s_g,
+                    const uint16_t* A_u, const uint16_t* B_u, float s_u, int r, int act, const uint16_t* GU, int64_t ldgu,
+                    const uint16_t* dH, int64_t lddh, int64_t d_seq, uint16_t* dGU, int64_t lddgu, uint16_t* dX,
+                    int64_t lddx, void* workspace, int64_t workspace_bytes, void* stream) {
+    qn::GatedCall c{};
+    if (int rc = check_gated({codes_g, codes_u}, {qconst_g, qconst_u}, {qscale_g, qscale_u}, {qmean_g, qmean_u}, d_ff, d_in,
+                             dq, {A_g, A_u}, {B_g, B_u}, {s_g, s_u}, r, act, d_seq, &c))
+        return rc;
+    if (int rc = check_rows(GU, d_seq, 2 * d_ff, ldgu)) return rc;
+    if (int rc = check_rows(dH, d_seq, d_ff, lddh)) return rc;
+    if (int rc = check_rows(dGU, d_seq, 2 * d_ff, lddgu)) return rc;
+    if (int rc = check_rows(dX, d_seq, d_in, lddx)) return rc;
+    const GatedWs w = gated_ws(d_ff, d_in, d_seq, r, true);
+    if (int rc = check_workspace(workspace, workspace_bytes, w.bytes)) return rc;
+    char* ws = static_cast<char*>(workspace);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    // the elementwise part beside the layouts, then the rank products of dG and dU, then dX
+    qn::GatedProlog o{};
+    o.what = reinterpret_cast<uint16_t*>(ws + w.what);
+    o.adapt = reinterpret_cast<uint16_t*>(ws + w.adapt);
+    o.grad = qn::GatedGradArgs{dH, lddh, GU, ldgu, dGU, lddgu, static_cast<int>(d_seq), static_cast<int>(d_ff), act};
+    hipError_t e = qn::launch_gated_prologue(c, true, o, st);
+    if (e != hipSuccess) return hip_fail(e, "qlora_gated_bwd (prologue)");
+    uint16_t* t = nullptr;
+    if (r > 0) {
+        qn::GatedProlog p{};
+        t = p.pre_out = reinterpret_cast<uint16_t*>(ws + w.t);
+        p.pre_in = dGU; p.ld_in = lddgu;
+        for (int i = 0; i < 2; ++i) {
+            p.ppart[i] = reinterpret_cast<float*>(ws + w.ppart[i]);
+            if (qn::prepass_takes_kmajor(r)) continue;
+            uint16_t* bt = reinterpret_cast<uint16_t*>(ws + w.bt[i]);
+            if ((e = qn::launch_transpose_pad(c.B[i], d_ff, r, bt, d_ff, st)) != hipSuccess)
+                return hip_fail(e, "qlora_gated_bwd (transpose)");
+            p.bt[i] = bt;
+        }
+        if ((e = qn::launch_gated_prologue(c, true, p, st)) != hipSuccess) return hip_fail(e, "qlora_gated_bwd (pre-pass)");
+    }
+    e = qn::launch_gemm_nt(dGU, lddgu, o.what, 2 * d_ff, 2 * d_ff, t, qn::gated_k2(r), o.adapt, qn::gated_k2(r),
+                           qn::gated_k2(r), dX, lddx, d_seq, d_in, reinterpret_cast<float*>(ws + w.part), st);
+    if (e != hipSuccess) return hip_fail(e, "qlora_gated_bwd (gemm)");
+    return 0;
+}
+
+int64_t qlora_head_loss_workspace_bytes(int64_t vocab, int64_t d_in, int64_t d_seq, int nf4, int grad) {
+    qn::HeadPlan p;
+    return head_sizes(vocab, d_in, d_seq, nf4 != 0, grad != 0, &p) == 0 ? p.bytes : 0;
+}
+
+int qlora_head_loss(const uint16_t* W, int64_t ldw, const uint8_t* codes, const int8_t* qconst, const float* qscale,
+                    const float* qmean, int dq, int64_t vocab, int64_t d_in, const uint16_t* X, int64_t ldx, int64_t d_seq,
+                    const int64_t* target, const float* scale, float* loss, uint16_t* dX, int64_t lddx, void* workspace,
+                    int64_t workspace_bytes, void* stream) {
+    qn::HeadCall c{};
+    qn::HeadPlan p;
+    if ((W == nullptr) == (codes == nullptr)) return fail(-1, "give the head as bf16 or as an NF4 weight");
+    if (!target || !loss) return fail(-1, "null pointer argument");
+    if (!aligned(target, 8) || !aligned(scale, 4) || !aligned(loss, 4)) return fail(-1, "misaligned pointer");
+    if (codes != nullptr) {
+        if (int rc = make_consts(dq, codes, qconst, qscale, qmean, &c.bc)) return rc;
+        if (!aligned(codes, 16)) return fail(-1, "misaligned pointer (16 B for arrays, 256 B for the workspace)");
+    }
+    if (int rc = head_sizes(vocab, d_in, d_seq, codes != nullptr, dX != nullptr, &p)) return rc;
+    if (W != nullptr) {
+        // a piece of the head is an operand; the head itself may be larger
+        if (int rc = check_rows(W, std::min(vocab, p.piece), d_in, ldw)) return rc;
+        if (ldw > (int64_t{1} << 46) / vocab) return fail(-2, "weight too large");
+    }
+    if (int rc = check_rows(X, d_seq, d_in, ldx)) return rc;
+    if (dX != nullptr)
+        if (int rc = check_rows(dX, d_seq, d_in, lddx)) return rc;
+    if (int rc = check_workspace(workspace, workspace_bytes, p.bytes)) return rc;
+    c.W = W; c.ldw = ldw; c.codes = codes; c.V = vocab; c.d = d_in;
+    c.X = X; c.ldx = ldx; c.target = target; c.T = d_seq; c.scale = scale; c.loss = loss; c.dX = dX; c.lddx = lddx;
+    const hipError_t e = qn::launch_head_loss(c, p, static_cast<char*>(workspace), static_cast<hipStream_t>(stream));
+    if (e != hipSuccess) return hip_fail(e, "qlora_head_loss");
     return 0;
 }
 

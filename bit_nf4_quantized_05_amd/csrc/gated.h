@@ -1,0 +1,138 @@
+// The gated feed-forward block's launches, shared by gated.hip, prologue.hip and api.hip.
+//   H = act(G) * U,  G = W_g x + s_g B_g (A_g x),  U = W_u x + s_u B_u (A_u x)
+// and its gradient. Index 0 is the gate projection, 1 the up projection.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "internal.h"
+#include "nf4_device.h"
+
+namespace qn {
+
+constexpr int kActSilu = 0, kActGelu = 1;
+
+struct GatedCall {
+    const uint8_t* codes[2]; BlockConsts bc[2];
+    int64_t d_ff, d_in;
+    const uint16_t* A[2];             // [r, d_in]
+    const uint16_t* B[2];             // [d_ff, r]
+    float s[2];
+    int r, act;                       // r 0: no adapters
+    int64_t M;
+};
+
+// Rank columns of one projection, and of both, whole K-steps of 64 (0 without adapters)
+inline int gated_pad(int r) { return (r + 31) / 32 * 32; }
+inline int gated_k2(int r) { return 2 * gated_pad(r); }
+
+// act(g), and its derivative. sigma(x) = 1 / (1 + 2^(-x log2 e)) with the hardware's 2^x and
+// 1/x (1 ulp each), 0 or 1 where 2^x leaves float32.
+__device__ __forceinline__ float gated_sigmoid(float x) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-1.44269504088896341f * x));
+}
+// silu: g sigma(g); gelu: g sigma(2 c (g + k g^3)), the tanh form g / 2 (1 + tanh(..)) without
+// its cancellation for negative g
+constexpr float kGeluC2 = 1.59576912160573071f, kGeluK = 0.044715f;      // 2 sqrt(2 / pi)
+__device__ __forceinline__ float gated_act(int act, float g) {
+    const float x = act == kActSilu ? g : kGeluC2 * (g + kGeluK * (g * g) * g);
+    return g * gated_sigmoid(x);
+}
+__device__ __forceinline__ float gated_act_grad(int act, float g, float& value) {
+    if (act == kActSilu) {
+        const float s = gated_sigmoid(g);
+        value = g * s;
+        return s * (1.0f + g * (1.0f - s));
+    }
+    const float s = gated_sigmoid(kGeluC2 * (g + kGeluK * (g * g) * g));
+    value = g * s;
+    // past |g| = 16, s (1 - s) is 0 in float32; the bound keeps g^2 from overflowing beside it
+    const float q = fminf(fmaxf(g, -16.0f), 16.0f);
+    return s + q * (s * (1.0f - s)) * (kGeluC2 * (1.0f + 3.0f * kGeluK * (q * q)));
+}
+
+// dG = dH U act'(G), dU = dH act(G), elementwise over [M, d_ff]; G | U and dG | dU stand side by
+// side in rows of GU and dGU.
+struct GatedGradArgs {
+    const uint16_t* dH; int64_t lddh;
+    const uint16_t* GU; int64_t ldgu;
+    uint16_t* dGU; int64_t lddgu;
+    int M, d_ff, act;
+};
+constexpr int kGradPer = 4;           // 8-wide pieces per thread, 256 apart
+inline int gated_grad_blocks(const GatedGradArgs& g) {
+    const int64_t pieces = static_cast<int64_t>(g.M) * (g.d_ff / 8);
+    return static_cast<int>((pieces + 256 * kGradPer - 1) / (256 * kGradPer));
+}
+
+__device__ __forceinline__ void gated_grad_job(const GatedGradArgs& a, int b) {
+    const int cpr = a.d_ff / 8;
+    const int64_t total = static_cast<int64_t>(a.M) * cpr;
+    const int64_t first = static_cast<int64_t>(b) * (256 * kGradPer) + threadIdx.x;
+    uint4 h[kGradPer], g[kGradPer], u[kGradPer];
+    int64_t row[kGradPer];
+    int col[kGradPer];
+#pragma unroll
+    for (int k = 0; k < kGradPer; ++k) {
+        const int64_t at = min(first + 256 * k, total - 1);
+        row[k] = at / cpr;
+        col[k] = static_cast<int>(at - row[k] * cpr) * 8;
+        h[k] = *reinterpret_cast<const uint4*>(a.dH + row[k] * a.lddh + col[k]);
+        g[k] = *reinterpret_cast<const uint4*>(a.GU + row[k] * a.ldgu + col[k]);
+        u[k] = *reinterpret_cast<const uint4*>(a.GU + row[k] * a.ldgu + a.d_ff + col[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kGradPer; ++k) {
+        if (first + 256 * k >= total) break;
+        const uint32_t hw[4] = {h[k].x, h[k].y, h[k].z, h[k].w};
+        const uint32_t gw[4] = {g[k].x, g[k].y, g[k].z, g[k].w};
+        const uint32_t uw[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+        uint32_t og[4], ou[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float dg[2], du[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float hv = __uint_as_float(e ? hw[q] & 0xFFFF0000u : hw[q] << 16);
+                const float gv = __uint_as_float(e ? gw[q] & 0xFFFF0000u : gw[q] << 16);
+                const float uv = __uint_as_float(e ? uw[q] & 0xFFFF0000u : uw[q] << 16);
+                float act;
+                const float slope = gated_act_grad(a.act, gv, act);
+                dg[e] = hv * uv * slope;
+                du[e] = hv * act;
+            }
+            og[q] = pack_bf16x2(dg[0], dg[1]);
+            ou[q] = pack_bf16x2(du[0], du[1]);
+        }
+        uint16_t* out = a.dGU + row[k] * a.lddgu + col[k];
+        *reinterpret_cast<uint4*>(out) = uint4{og[0], og[1], og[2], og[3]};
+        *reinterpret_cast<uint4*>(out + a.d_ff) = uint4{ou[0], ou[1], ou[2], ou[3]};
+    }
+}
+
+// ---- prologue.hip ----
+// The layouts (what not null): both weights dequantised side by side to what (forward: rows in
+// runs of 32 in turn, [2 d_ff, d_in]; gradient: transposed, [d_in, 2 d_ff]), both adapters to
+// adapt ([2 d_ff, k2] or [d_in, k2]) and, in the gradient, the elementwise part grad. And (pre_out
+// not null, r > 0) the rank products of pre_in: pre_out [M, k2] = s_w pre_in R_w^T, R = A of X or
+// B of the halves of dGU; bt: B^T [r, d_ff] where the pre-pass cannot read B itself.
+struct GatedProlog {
+    uint16_t* what; uint16_t* adapt;
+    const uint16_t* pre_in; int64_t ld_in; uint16_t* pre_out; float* ppart[2];
+    const uint16_t* bt[2];
+    GatedGradArgs grad;
+};
+hipError_t launch_gated_prologue(const GatedCall& c, bool backward, const GatedProlog& o, hipStream_t st);
+
+// W_hat [d_out, d_in] to rows and transposed to cols (row stride ld_cols); either may be null
+hipError_t launch_dequant_both(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
+                               uint16_t* rows, uint16_t* cols, int64_t ld_cols, hipStream_t st);
+
+// ---- gated.hip ----
+// H (and GU, if not null) from X, the paired weight what, the rank products t [M, k2] and the
+// adapters adapt [2 d_ff, k2]; part holds gated_part_floats(M, d_ff, d_in) floats.
+int64_t gated_part_floats(int64_t M, int64_t d_ff, int64_t d_in);
+hipError_t launch_gated_gemm(const GatedCall& c, const uint16_t* X, int64_t ldx, const uint16_t* what, const uint16_t* t,
+                             const uint16_t* adapt, uint16_t* H, int64_t ldh, uint16_t* GU, int64_t ldgu, float* part,
+                             hipStream_t st);
+
+}  // namespace qn

@@ -1,0 +1,545 @@
+// Softmax cross entropy over a large vocabulary, in pieces of it, and its gradient to the
+// hidden states, on gfx950. The logits are never kept.
+//
+//   loss_t = log sum_v exp(z_tv) - z_ty,   z = X W^T,  y the token's target
+//   dX_t   = scale_t (sum_v p_tv W_v - W_y),   p = softmax(z_t)
+//
+// The exponentials are taken relative to the target's own logit, which is one short dot product
+// per token known before the sweep: with l = sum over v != y of exp(z_v - z_y),
+//   loss = log(1 + l),    dX = scale / (1 + l) (sum_{v != y} exp(z_v - z_y) W_v - l W_y).
+// Nothing underflows that matters (the sum is at least 1), the loss of a sure token keeps its
+// digits, the gradient has no difference of nearly equal terms, and the sweep needs no maximum
+// first: each piece's exponentials (bf16, so that they can be an MFMA operand) are multiplied
+// with W in the same pass and the sums divided at the end. Two products where forming the
+// logits again for the gradient would take three. Where z_v - z_y is large (past kMaxLog2 in
+// powers of two) a 256-wide tile of a row is scaled down by a power of two, and head_join brings
+// the row to one scale: exact in every case, and no work where it does not happen.
+//
+// Tokens without a target (prompts, padding) are left out before the products: head_plan_kernel
+// numbers the others, the GEMM gathers their rows, and workgroups past the last one end at once.
+//
+// Per piece: W^T of the piece (gradient; an NF4 head is dequantised here, both ways),
+// head_logits (the product and its exponentials), head_join, head_grad (their product with W,
+// added to float32 sums). Then head_final. All sums are in fixed order.
+#include <hip/hip_runtime.h>
+
+#include "gated.h"
+#include "gemm_core.h"
+#include "head_loss.h"
+#include "nf4_device.h"
+
+#include <algorithm>
+
+namespace qn {
+namespace {
+
+constexpr int kWM = 2, kWN = 4;
+using Waves = GemmWaves<kWM, kWN>;
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+// 2^80 times 2^31 rows stays in float32
+constexpr float kMaxLog2 = 80.0f;
+
+// The numbering of the counted tokens and what is known of each (arrays of T)
+struct HeadRows {
+    int32_t* count;                           // [0]
+    int32_t* idx;                             // token of a counted position
+    int32_t* pos;                             // position of a token, -1: not counted
+    int32_t* tgt;                             // a position's target
+    float* zt;                                // its target's logit
+    float* shift;                             // powers of two taken off its exponentials
+    float* l;                                 // sum of 2^((z - zt) log2 e - shift), v != target
+};
+
+__host__ __device__ inline int64_t head_int_count(int64_t T) { return 16 + 6 * ((T + 3) / 4 * 4); }
+HeadRows head_rows(char* ws, int64_t T) {
+    const int64_t n = (T + 3) / 4 * 4;
+    int32_t* p = reinterpret_cast<int32_t*>(ws);
+    float* f = reinterpret_cast<float*>(p + 16 + 3 * n);
+    return HeadRows{p, p + 16, p + 16 + n, p + 16 + 2 * n, f, f + n, f + 2 * n};
+}
+
+// One workgroup: wave w takes a 16th of the tokens, 64 at a time; counts, then numbers them.
+__global__ __launch_bounds__(1024)
+void head_plan_kernel(const int64_t* __restrict__ target, int64_t T, int64_t V, HeadRows r) {
+    __shared__ int counts[16];
+    const int lane = threadIdx.x & 63;
+    const int wave = threadIdx.x >> 6;
+    const int64_t per = ((T + 15) / 16 + 63) / 64 * 64;
+    const int64_t t0 = wave * per, t1 = min(t0 + per, T);
+    int n = 0;
+    for (int64_t t = t0; t < t1; t += 64) {
+        const int64_t y = t + lane < t1 ? target[t + lane] : -1;
+        n += __popcll(__ballot(y >= 0 && y < V));
+    }
+    if (lane == 0) counts[wave] = n;
+    __syncthreads();
+    int at = 0, all = 0;
+    for (int w = 0; w < 16; ++w) {
+        at += w < wave ? counts[w] : 0;
+        all += counts[w];
+    }
+    for (int64_t t = t0; t < t1; t += 64) {
+        const int64_t y = t + lane < t1 ? target[t + lane] : -1;
+        const bool ok = y >= 0 && y < V;
+        const unsigned long long m = __ballot(ok);
+        const int p = at + __popcll(m & ((1ull << lane) - 1));
+        if (ok) {
+            r.idx[p] = static_cast<int32_t>(t + lane);
+            r.tgt[p] = static_cast<int32_t>(y);
+        }
+        if (t + lane < t1) r.pos[t + lane] = ok ? p : -1;
+        at += __popcll(m);
+    }
+    if (threadIdx.x == 0) r.count[0] = all;
+}
+
+// The target's logit of each counted token, a wave each; of an NF4 head also the target's row in
+// bf16 (wt, if not null).
+__global__ __launch_bounds__(256)
+void head_target_kernel(HeadCall c, HeadRows r, uint16_t* wt, NF4Tables tab) {
+    __shared__ float s_code[16];
+    if (threadIdx.x < 16) s_code[threadIdx.x] = tab.code[threadIdx.x];
+    __syncthreads();
+    const int m = static_cast<int>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    if (m >= r.count[0]) return;
+    const int lane = threadIdx.x & 63;
+    const int64_t y = r.tgt[m];
+    const uint16_t* x = c.X + r.idx[m] * c.ldx;
+    float sum = 0.0f;
+    for (int64_t k = 8 * lane; k < c.d; k += 512) {
+        const uint4 xv = *reinterpret_cast<const uint4*>(x + k);
+        uint4 wv;
+        if (c.codes == nullptr) {
+            wv = *reinterpret_cast<const uint4*>(c.W + y * c.ldw + k);
+        } else {
+            const int64_t e = y * c.d + k, blk = e >> 6;
+            const uint32_t word = *reinterpret_cast<const uint32_t*>(c.codes + (e >> 1));
+            const float a = block_constant(c.bc.fmt, c.bc.q[blk], c.bc.scale[blk >> c.bc.gshift], c.bc.mean[0]);
+            float w[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) w[q] = s_code[(word >> (4 * q)) & 0xFu] * a;
+            wv = uint4{pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7])};
+            if (wt != nullptr) *reinterpret_cast<uint4*>(wt + m * c.d + k) = wv;
+        }
+        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, ww[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            sum += __uint_as_float(xw[q] << 16) * __uint_as_float(ww[q] << 16);
+            sum += __uint_as_float(xw[q] & 0xFFFF0000u) * __uint_as_float(ww[q] & 0xFFFF0000u);
+        }
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o);
+    if (lane == 0) {
+        r.zt[m] = sum;
+        r.shift[m] = 0.0f;
+        r.l[m] = 0.0f;
+    }
+}
+
+// dst [d, ld] = src [rows, d]^T for columns below rows, zeros up to the next multiple of 64.
+// A workgroup takes 64 x 64; 16-byte loads and stores through LDS rows of odd pitch (in words).
+__global__ __launch_bounds__(256)
+void head_transpose_kernel(const uint16_t* __restrict__ src, int64_t ldw, int64_t rows, uint16_t* __restrict__ dst,
+                           int64_t ld) {
+    constexpr int kP = 66;
+    __shared__ uint16_t tile[64 * kP];
+    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 64;         // columns of src
+    const int64_t v0 = static_cast<int64_t>(blockIdx.y) * 64;         // rows of src
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int c = 256 * u + threadIdx.x;
+        const int v = c >> 3, q = c & 7;
+        uint4 w = uint4{0, 0, 0, 0};
+        if (v0 + v < rows) w = *reinterpret_cast<const uint4*>(src + (v0 + v) * ldw + i0 + 8 * q);
+        uint32_t* at = reinterpret_cast<uint32_t*>(&tile[v * kP + 8 * q]);
+        at[0] = w.x; at[1] = w.y; at[2] = w.z; at[3] = w.w;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int c = 256 * u + threadIdx.x;
+        const int i = c >> 3, q = c & 7;
+        uint32_t w[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+            w[h] = tile[(8 * q + 2 * h) * kP + i] | (static_cast<uint32_t>(tile[(8 * q + 2 * h + 1) * kP + i]) << 16);
+        *reinterpret_cast<uint4*>(dst + (i0 + i) * ld + v0 + 8 * q) = uint4{w[0], w[1], w[2], w[3]};
+    }
+}
+
+// Workgroup -> one of n items, contiguous ranges per XCD (-1: none)
+__device__ __forceinline__ int xcd_range(int bid, int n) {
+    const int x = bid & 7, i = bid >> 3;
+    const int q = n >> 3, rest = n & 7;
+    return i < q + (x < rest) ? x * q + min(x, rest) + i : -1;
+}
+
+struct HeadTile {
+    int v0, cols;                             // the piece's first row of the head, and its rows
+    int64_t T;
+    float2* part;                             // [tiles_n][T]: a tile's sum, and the power taken off
+    uint16_t* E; int64_t lde;                 // exponentials [T, lde] (gradient)
+};
+
+// 256 counted tokens x 256 rows of the piece: z in the accumulators, then the exponentials.
+template <bool kGrad>
+__global__ __launch_bounds__(Waves::NT, 1)
+void head_logits_kernel(GemmArgs g, HeadTile h, HeadRows r) {
+    constexpr int TM = Waves::TM, TN = Waves::TN;
+    __shared__ float s_top[4][BM], s_sum[4][BM];
+    const int count = r.count[0];
+    g.tiles_m = (count + BM - 1) / BM;
+    const int logical = xcd_range(static_cast<int>(blockIdx.x), g.tiles_m * g.tiles_n);
+    if (logical < 0) return;
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = tid >> 6;
+    const int wm = wave / kWN, wn = wave % kWN;
+    int tm, tn;
+    tile_coords(g, logical, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+    f32x16 acc[TN][TM];
+    gemm_core<kWM, kWN, false>(
+        g, [&](int i) { return static_cast<uint32_t>(r.idx[min(m0 + i, count - 1)]); },
+        [&](int i) { return static_cast<uint32_t>(min(n0 + i, h.cols - 1)); }, 0, g.kt1, false, acc);
+    // acc -> y = (z - zt) log2 e, -inf at the target and past the piece
+    const int base = wn * 64 + 4 * (lane >> 5);      // tile column of the lane's value (a, gq, e): base + 32 a + 8 gq + e
+    const int ml0 = wm * (TM * 32) + (lane & 31);    // tile row of its b: ml0 + 32 b
+    const bool edge = n0 + BN > h.cols;
+    float top[TM];
+    float sh[TM];
+#pragma unroll
+    for (int b = 0; b < TM; ++b) {
+        const int m = min(m0 + ml0 + 32 * b, count - 1);
+        const float zt = r.zt[m];
+        sh[b] = r.shift[m];
+        const int skip = r.tgt[m] - h.v0 - n0 - base;
+        float t = -__builtin_inff();
+#pragma unroll
+        for (int a = 0; a < TN; ++a)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int off = 32 * a + 8 * (v >> 2) + (v & 3);
+                float y = (acc[a][b][v] - zt) * kLog2e - sh[b];
+                if (off == skip || (edge && n0 + base + off >= h.cols)) y = -__builtin_inff();
+                acc[a][b][v] = y;
+                t = fmaxf(t, y);
+            }
+        top[b] = fmaxf(t, __shfl_xor(t, 32));
+        if (lane < 32) s_top[wn][ml0 + 32 * b] = top[b];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < TM; ++b) {
+        const int ml = ml0 + 32 * b;
+        const float t = fmaxf(fmaxf(s_top[0][ml], s_top[1][ml]), fmaxf(s_top[2][ml], s_top[3][ml]));
+        const float off = t > kMaxLog2 ? ceilf(t) : 0.0f;
+        float sum = 0.0f;
+#pragma unroll
+        for (int a = 0; a < TN; ++a)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const float e = __builtin_amdgcn_exp2f(acc[a][b][v] - off);
+                acc[a][b][v] = e;
+                sum += e;
+            }
+        sum += __shfl_xor(sum, 32);
+        if (lane < 32) s_sum[wn][ml] = sum;
+        top[b] = off;
+        if constexpr (kGrad) {
+            // the tile as 256 rows of 512 B, rows 0..127 in the first stage, 16-byte chunk j of
+            // row ml at j ^ (ml & 31)
+            char* rowp = reinterpret_cast<char*>((ml >> 7) ? g_st1 : g_st0) + (ml & 127) * 512;
+#pragma unroll
+            for (int a = 0; a < TN; ++a)
+#pragma unroll
+                for (int gq = 0; gq < 4; ++gq) {
+                    const int nl = base + 32 * a + 8 * gq;
+                    *reinterpret_cast<uint2*>(rowp + (((nl >> 3) ^ (ml & 31)) << 4) + ((nl & 7) << 1)) =
+                        uint2{pack_bf16x2(acc[a][b][4 * gq], acc[a][b][4 * gq + 1]),
+                              pack_bf16x2(acc[a][b][4 * gq + 2], acc[a][b][4 * gq + 3])};
+                }
+        }
+    }
+    __syncthreads();
+    if (tid < BM && m0 + tid < count) {
+        const float t = fmaxf(fmaxf(s_top[0][tid], s_top[1][tid]), fmaxf(s_top[2][tid], s_top[3][tid]));
+        h.part[tn * h.T + m0 + tid] = float2{(s_sum[0][tid] + s_sum[1][tid]) + (s_sum[2][tid] + s_sum[3][tid]),
+                                             t > kMaxLog2 ? ceilf(t) : 0.0f};
+    }
+    if constexpr (kGrad) {
+        const int cj = tid & 31;
+#pragma unroll
+        for (int i = 0; i < BM / (Waves::NT / 32); ++i) {
+            const int row = i * (Waves::NT / 32) + (tid >> 5);
+            const char* arr = reinterpret_cast<const char*>((row >> 7) ? g_st1 : g_st0);
+            const uint4 v = *reinterpret_cast<const uint4*>(arr + (row & 127) * 512 + ((cj ^ (row & 31)) << 4));
+            if (m0 + row < count) *reinterpret_cast<uint4*>(h.E + static_cast<int64_t>(m0 + row) * h.lde + n0 + cj * 8) = v;
+        }
+    }
+}
+
+// The gradient's product: its tiles, and the splits of their K-steps that fill `slots` workgroups
+struct HeadSplit { int tiles, splits, kper; };
+__device__ __forceinline__ HeadSplit head_split(int count, int tiles_n, int slots, int kt_first, int kt) {
+    HeadSplit s;
+    s.tiles = (count + BM - 1) / BM * tiles_n;
+    // at least 8 K-steps per split of the first (longest) piece, and no split of it without any
+    const int want = max(1, min(slots / max(1, s.tiles), kt_first / 8));
+    const int per = (kt_first + want - 1) / want;
+    s.splits = (kt_first + per - 1) / per;
+    s.kper = (kt + s.splits - 1) / s.splits;
+    return s;
+}
+
+// A piece's sums joined to the row's: l, and, where a tile was scaled down, the row brought to one
+// scale (its exponentials in E and the sums of earlier pieces in acc times exact powers of two).
+// 64 rows per workgroup, 4 threads a row.
+struct HeadJoin {
+    const float2* part; int tiles_n; int64_t T;
+    uint16_t* E; int64_t lde;                 // or null
+    float* acc; int acc_tiles_n, slots, kt_first;    // acc null: no earlier piece
+};
+
+__global__ __launch_bounds__(256)
+void head_join_kernel(HeadJoin j, HeadRows r) {
+    __shared__ float s_sum[4][64], s_top[4][64], s_off[64];
+    const int count = r.count[0];
+    const int m0 = static_cast<int>(blockIdx.x) * 64;
+    if (m0 >= count) return;
+    const int i = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const int m = min(m0 + i, count - 1);
+    float sum = 0.0f, top = 0.0f;
+#pragma unroll 8
+    for (int n = q; n < j.tiles_n; n += 4) {
+        const float2 p = j.part[n * j.T + m];
+        sum += p.x;
+        top = fmaxf(top, p.y);
+    }
+    s_sum[q][i] = sum;
+    s_top[q][i] = top;
+    __syncthreads();
+    if (q == 0) {
+        top = fmaxf(fmaxf(s_top[0][i], s_top[1][i]), fmaxf(s_top[2][i], s_top[3][i]));
+        s_off[i] = top;
+        if (m0 + i < count) {
+            float l = r.l[m];
+            if (top == 0.0f) {
+                l += (s_sum[0][i] + s_sum[1][i]) + (s_sum[2][i] + s_sum[3][i]);
+            } else {
+                l *= __builtin_amdgcn_exp2f(-top);
+                for (int n = 0; n < j.tiles_n; ++n) {
+                    const float2 p = j.part[n * j.T + m];
+                    l += p.x * __builtin_amdgcn_exp2f(p.y - top);
+                }
+                r.shift[m] += top;
+            }
+            r.l[m] = l;
+        }
+    }
+    __syncthreads();
+    if (j.E == nullptr) return;
+    for (int k = 0; k < 64 && m0 + k < count; ++k) {
+        const float off = s_off[k];
+        if (off == 0.0f) continue;                   // uniform
+        const int row = m0 + k;
+        uint16_t* e = j.E + static_cast<int64_t>(row) * j.lde;
+        for (int n = 0; n < j.tiles_n; ++n) {
+            const float f = __builtin_amdgcn_exp2f(j.part[n * j.T + row].y - off);
+            uint16_t* at = e + n * BN + threadIdx.x;
+            *at = bf16_bits(__uint_as_float(static_cast<uint32_t>(*at) << 16) * f);
+        }
+        if (j.acc != nullptr) {
+            const float f = __builtin_amdgcn_exp2f(-off);
+            const HeadSplit s = head_split(count, j.acc_tiles_n, j.slots, j.kt_first, j.kt_first);
+            for (int sp = 0; sp < s.splits; ++sp)
+                for (int tn = 0; tn < j.acc_tiles_n; ++tn) {
+                    // the tile's place in acc, as head_grad_kernel numbers them
+                    const int64_t slot = static_cast<int64_t>(sp) * s.tiles + (row / BM) * j.acc_tiles_n + tn;
+                    j.acc[slot * (BM * BN) + (row % BM) * BN + threadIdx.x] *= f;
+                }
+        }
+    }
+}
+
+// acc += E W of a piece (the first piece: =), 256 x 256 float32 tiles; tile (tm, tn) of split s is
+// slot s tiles + tm tiles_n + tn.
+struct HeadGrad { float* acc; int slots, kt_first, first; };
+
+__global__ __launch_bounds__(Waves::NT, 1)
+void head_grad_kernel(GemmArgs g, HeadGrad h, HeadRows r) {
+    constexpr int TM = Waves::TM, TN = Waves::TN;
+    const int count = r.count[0];
+    const HeadSplit s = head_split(count, g.tiles_n, h.slots, h.kt_first, g.kt1);
+    g.tiles_m = (count + BM - 1) / BM;
+    const int logical = xcd_range(static_cast<int>(blockIdx.x), s.tiles * s.splits);
+    if (logical < 0) return;
+    const int sp = logical / s.tiles;
+    const int kb = sp * s.kper, ke = min(kb + s.kper, g.kt1);
+    if (kb >= ke) return;                            // a later, shorter piece adds nothing here
+    const int tid = threadIdx.x;
+    const int lane = tid & 63;
+    const int wave = tid >> 6;
+    const int wm = wave / kWN, wn = wave % kWN;
+    int tm, tn;
+    tile_coords(g, logical % s.tiles, tm, tn);
+    const int m0 = tm * BM, n0 = tn * BN;
+    f32x16 acc[TN][TM];
+    gemm_core<kWM, kWN, false>(
+        g, [&](int i) { return static_cast<uint32_t>(min(m0 + i, count - 1)); },
+        [&](int i) { return static_cast<uint32_t>(min(n0 + i, g.N - 1)); }, kb, ke, false, acc);
+    float* pt = h.acc + (static_cast<int64_t>(sp) * s.tiles + tm * g.tiles_n + tn) * (BM * BN);
+#pragma unroll
+    for (int b = 0; b < TM; ++b) {
+        const int ml = wm * (TM * 32) + b * 32 + (lane & 31);
+#pragma unroll
+        for (int a = 0; a < TN; ++a)
+#pragma unroll
+            for (int gq = 0; gq < 4; ++gq) {
+                float4* at = reinterpret_cast<float4*>(pt + ml * BN + wn * 64 + a * 32 + 8 * gq + 4 * (lane >> 5));
+                float4 v = float4{acc[a][b][4 * gq], acc[a][b][4 * gq + 1], acc[a][b][4 * gq + 2], acc[a][b][4 * gq + 3]};
+                if (!h.first) {
+                    const float4 o = *at;
+                    v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+                }
+                *at = v;
+            }
+    }
+}
+
+// Per token: the loss, and dX from the sums (zeros for a token that is not counted).
+struct HeadFinal {
+    const float* acc; int tiles_n, slots, kt_first;
+    const uint16_t* wt;                       // the target's row of position m at wt + m d, or null: in W
+};
+
+template <bool kGrad>
+__global__ __launch_bounds__(256)
+void head_final_kernel(HeadCall c, HeadFinal f, HeadRows r) {
+    const int64_t t = kGrad ? static_cast<int64_t>(blockIdx.x) : static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (t >= c.T) return;
+    const int m = r.pos[t];
+    float l = 0.0f, one = 1.0f;
+    if (m >= 0) {
+        const float shift = r.shift[m];
+        l = r.l[m];
+        one = __builtin_amdgcn_exp2f(-shift);                  // exp(z_y - z_y) on the row's scale
+        if (!kGrad || threadIdx.x == 0) c.loss[t] = shift == 0.0f ? log1pf(l) : shift * kLn2 + logf(one + l);
+    } else if (!kGrad || threadIdx.x == 0) {
+        c.loss[t] = 0.0f;
+    }
+    if constexpr (kGrad) {
+        uint16_t* out = c.dX + t * c.lddx;
+        const int count = r.count[0];
+        const HeadSplit s = head_split(count, f.tiles_n, f.slots, f.kt_first, f.kt_first);
+        const float k = m < 0 ? 0.0f : (c.scale != nullptr ? c.scale[t] : 1.0f) / (one + l);
+        const uint16_t* w = m < 0 ? nullptr : f.wt != nullptr ? f.wt + m * c.d : c.W + r.tgt[m] * c.ldw;
+        for (int64_t n = 4 * threadIdx.x; n < c.d; n += 1024) {
+            uint2 o = uint2{0u, 0u};
+            if (m >= 0) {
+                const float* at = f.acc + static_cast<int64_t>((m / BM) * f.tiles_n + n / BN) * (BM * BN) + (m % BM) * BN + n % BN;
+                const float4 a = ordered_sum4<4>(at, static_cast<int64_t>(s.tiles) * (BM * BN), s.splits);
+                const uint2 wv = *reinterpret_cast<const uint2*>(w + n);
+                o.x = pack_bf16x2(k * (a.x - l * __uint_as_float(wv.x << 16)), k * (a.y - l * __uint_as_float(wv.x & 0xFFFF0000u)));
+                o.y = pack_bf16x2(k * (a.z - l * __uint_as_float(wv.y << 16)), k * (a.w - l * __uint_as_float(wv.y & 0xFFFF0000u)));
+            }
+            *reinterpret_cast<uint2*>(out + n) = o;
+        }
+    }
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+}  // namespace
+
+bool head_plan(int64_t V, int64_t d, int64_t T, bool nf4, bool grad, HeadPlan* p) {
+    constexpr int64_t kLimit = int64_t{1} << 31;     // elements of bf16 in 4 GiB
+    const bool keeps = grad || nf4;
+    // Pieces of up to 16384 rows where something of a piece is kept (its exponentials, W^T, the
+    // dequantised rows), fewer where T rows of exponentials would pass 2 GiB; else up to 65536.
+    int64_t most = keeps ? 16384 : 65536;
+    if (grad) most = std::min(most, std::max<int64_t>(256, kLimit / 2 / T / 256 * 256));
+    p->pieces = static_cast<int>(ceil_div(V, most));
+    p->piece = ceil_div(ceil_div(V, p->pieces), 256) * 256;
+    p->pieces = static_cast<int>(ceil_div(V, p->piece));
+    if (grad && p->piece >= kLimit / T) return false;
+    if (keeps && p->piece >= kLimit / d) return false;
+    const int64_t tm = ceil_div(T, BM), tn = ceil_div(d, BN), kt = p->piece / BK;
+    p->slots = !grad ? 0 : static_cast<int>(std::max(tm * tn, std::min<int64_t>(256, tm * tn * std::max<int64_t>(1, kt / 8))));
+    int64_t off = 0;
+    auto take = [&off](int64_t bytes) {
+        const int64_t at = off;
+        off += ceil_div(bytes, 256) * 256;
+        return at;
+    };
+    p->ints = take(4 * head_int_count(T));
+    p->part = take(8 * (p->piece / BN) * T);
+    p->E = take(grad ? 2 * T * p->piece : 0);
+    p->WT = take(grad ? 2 * d * p->piece : 0);
+    p->rows = take(nf4 ? 2 * d * p->piece : 0);
+    p->wt = take(nf4 && grad ? 2 * T * d : 0);
+    p->acc = take(static_cast<int64_t>(p->slots) * BM * BN * 4);
+    p->bytes = off;
+    return true;
+}
+
+hipError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t st) {
+    const bool grad = c.dX != nullptr, nf4 = c.codes != nullptr;
+    const HeadRows r = head_rows(ws + p.ints, c.T);
+    float2* part = reinterpret_cast<float2*>(ws + p.part);
+    uint16_t* E = grad ? reinterpret_cast<uint16_t*>(ws + p.E) : nullptr;
+    uint16_t* WT = grad ? reinterpret_cast<uint16_t*>(ws + p.WT) : nullptr;
+    uint16_t* rows = nf4 ? reinterpret_cast<uint16_t*>(ws + p.rows) : nullptr;
+    uint16_t* wt = nf4 && grad ? reinterpret_cast<uint16_t*>(ws + p.wt) : nullptr;
+    float* acc = grad ? reinterpret_cast<float*>(ws + p.acc) : nullptr;
+    const int tm = static_cast<int>(ceil_div(c.T, BM));
+    const int kt_first = static_cast<int>(ceil_div(std::min(p.piece, c.V), BK));
+    QN_LAUNCH("head_plan_kernel", st, head_plan_kernel, dim3(1), dim3(1024), 0, st, c.target, c.T, c.V, r);
+    QN_LAUNCH("head_target_kernel", st, head_target_kernel, dim3(static_cast<unsigned>(ceil_div(c.T, 4))), dim3(256), 0, st,
+              c, r, wt, tables());
+    hipError_t e = hipGetLastError();
+    for (int i = 0; i < p.pieces && e == hipSuccess; ++i) {
+        const int64_t v0 = i * p.piece, cols = std::min(p.piece, c.V - v0);
+        const uint16_t* W = nf4 ? rows : c.W + v0 * c.ldw;
+        const int64_t ldw = nf4 ? c.d : c.ldw;
+        if (nf4) {
+            // v0 d / 64 blocks is a multiple of 256 of them: whole groups of constants
+            BlockConsts bc = c.bc;
+            const int64_t blk = v0 * c.d / kBlock;
+            bc.q += bc.fmt == kDqNone ? 0 : blk;
+            bc.scale += blk >> bc.gshift;
+            if ((e = launch_dequant_both(c.codes + v0 * c.d / 2, bc, cols, c.d, rows, WT, p.piece, st)) != hipSuccess) return e;
+        } else if (grad) {
+            QN_LAUNCH("head_transpose_kernel", st, head_transpose_kernel,
+                      dim3(static_cast<unsigned>(c.d / 64), static_cast<unsigned>(ceil_div(cols, 64))), dim3(256), 0, st, W,
+                      ldw, cols, WT, p.piece);
+        }
+        const int tn = static_cast<int>(ceil_div(cols, BN));
+        const GemmArgs g = gemm_args(c.X, c.ldx, W, ldw, c.d, nullptr, 0, nullptr, 0, 0, nullptr, 0, c.T, cols, nullptr);
+        const HeadTile h{static_cast<int>(v0), static_cast<int>(cols), c.T, part, E, p.piece};
+        const dim3 lgrid(static_cast<unsigned>(ceil_div(tm * tn, 8) * 8));
+        if (grad) QN_LAUNCH("head_logits_kernel", st, head_logits_kernel<true>, lgrid, dim3(Waves::NT), 0, st, g, h, r);
+        else QN_LAUNCH("head_logits_kernel", st, head_logits_kernel<false>, lgrid, dim3(Waves::NT), 0, st, g, h, r);
+        const int dn = static_cast<int>(ceil_div(c.d, BN));
+        const HeadJoin j{part, tn, c.T, E, p.piece, i > 0 ? acc : nullptr, dn, p.slots, kt_first};
+        QN_LAUNCH("head_join_kernel", st, head_join_kernel, dim3(static_cast<unsigned>(ceil_div(c.T, 64))), dim3(256), 0, st,
+                  j, r);
+        if (grad) {
+            const GemmArgs q = gemm_args(E, p.piece, WT, p.piece, ceil_div(cols, BK) * BK, nullptr, 0, nullptr, 0, 0, nullptr, 0,
+                                         c.T, c.d, nullptr);
+            const HeadGrad hg{acc, p.slots, kt_first, i == 0};
+            QN_LAUNCH("head_grad_kernel", st, head_grad_kernel, dim3(static_cast<unsigned>(ceil_div(p.slots, 8) * 8)),
+                      dim3(Waves::NT), 0, st, q, hg, r);
+        }
+        e = hipGetLastError();
+    }
+    if (e != hipSuccess) return e;
+    const HeadFinal f{acc, static_cast<int>(ceil_div(c.d, BN)), p.slots, kt_first, wt};
+    if (grad) QN_LAUNCH("head_final_kernel", st, head_final_kernel<true>, dim3(static_cast<unsigned>(c.T)), dim3(256), 0, st, c, f, r);
+    else QN_LAUNCH("head_final_kernel", st, head_final_kernel<false>, dim3(static_cast<unsigned>(ceil_div(c.T, 256))), dim3(256),
+                   0, st, c, f, r);
+    return hipGetLastError();
+}
+
+}  // namespace qn

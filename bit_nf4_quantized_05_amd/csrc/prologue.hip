@@ -6,6 +6,7 @@
 // gradient uses when the pre-pass cannot read B itself.
 #include <hip/hip_runtime.h>
 
+#include "gated.h"
 #include "internal.h"
 #include "mfma_device.h"
 #include "multi.h"
@@ -37,25 +38,34 @@ namespace {
 struct PreJob {
     const uint16_t* P; int64_t ldp; int K;
     const uint16_t* R; int64_t ldr;  // R [r, K] row stride ldr, or k-major [K, r]
-    uint16_t* OUT;
+    uint16_t* OUT; int64_t ldo;      // r_pad columns at this row stride
+    float s;
     float* ppart;                    // [psplits][M][32 NT] fp32 partials when psplits > 1 and !cat
     int psplits, kper;               // K-slices and 64-wide K-chunks per slice
     int cat;                         // slice sp writes its own bf16 partial to OUT columns sp r .. sp r + r - 1
     int n;                           // workgroups of this job
 };
 
-struct PrologueArgs {
+// One double dequantisation: W_hat row-major [d_out, d_in], rows of it at their place in a
+// pair of weights (see dequant_rows_job), or W_hat^T [d_in, d_out] with row stride ldw.
+struct DeqJob {
     const uint8_t* codes; BlockConsts bc;
     int64_t d_out, d_in;
-    int transposed;                 // dequant to W_hat^T [d_in, d_out] instead of W_hat
-    uint16_t* what;
+    int transposed;                 // dequant to W_hat^T instead of W_hat
+    uint16_t* what; int64_t ldw;
+    int paired;                     // row-major: rows of one of two weights, 32 and 32 in turn
+    int trans_tiles;                // 64 x 64 tiles per transposed-dequant workgroup (1..4)
+    int n;                          // workgroups
+};
+
+struct PrologueArgs {
+    DeqJob deq;
     PreJob pre[2];
-    int M, r, r_pad; float s;
+    int M, r, r_pad;
     int adapt_mode;                 // 0 none, 1 pad columns, 2 transpose + pad
     int reps;                       // copies of the adapter's r columns side by side (one per slice of a cat job)
     const uint16_t* asrc; uint16_t* adst; int64_t arows, acols;
-    int n_pre, n_adapt, n_deq;      // n_pre = pre[0].n + pre[1].n
-    int trans_tiles;                // 64 x 64 tiles per transposed-dequant workgroup (1..4)
+    int n_pre, n_adapt;             // n_pre = pre[0].n + pre[1].n
 };
 
 constexpr int kDeqPerWG = 8192;                  // weights per row-major dequant workgroup (128 blocks)
@@ -198,7 +208,7 @@ __device__ __forceinline__ void prepass_job(const PreJob& j, const PrologueArgs&
     if (m >= a.M) return;
     if (j.cat) {
         // r % 4 == 0: each group of 4 ranks is wholly below r or wholly past it
-        uint16_t* orow = j.OUT + static_cast<int64_t>(m) * a.r_pad;
+        uint16_t* orow = j.OUT + static_cast<int64_t>(m) * j.ldo;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -206,8 +216,8 @@ __device__ __forceinline__ void prepass_job(const PreJob& j, const PrologueArgs&
                 const int n = t * 32 + 8 * gq + 4 * (lane >> 5);
                 if (n < a.r)
                     *reinterpret_cast<uint2*>(orow + sp * a.r + n) =
-                        uint2{pack_bf16x2(a.s * acc[t][4 * gq], a.s * acc[t][4 * gq + 1]),
-                              pack_bf16x2(a.s * acc[t][4 * gq + 2], a.s * acc[t][4 * gq + 3])};
+                        uint2{pack_bf16x2(j.s * acc[t][4 * gq], j.s * acc[t][4 * gq + 1]),
+                              pack_bf16x2(j.s * acc[t][4 * gq + 2], j.s * acc[t][4 * gq + 3])};
             }
         }
         if (sp == j.psplits - 1)
@@ -216,7 +226,7 @@ __device__ __forceinline__ void prepass_job(const PreJob& j, const PrologueArgs&
         return;
     }
     if (j.psplits == 1) {
-        uint16_t* orow = j.OUT + static_cast<int64_t>(m) * a.r_pad;
+        uint16_t* orow = j.OUT + static_cast<int64_t>(m) * j.ldo;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -224,7 +234,7 @@ __device__ __forceinline__ void prepass_job(const PreJob& j, const PrologueArgs&
                 const int n = t * 32 + 8 * gq + 4 * (lane >> 5);
                 float v[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = n + e < a.r ? a.s * acc[t][4 * gq + e] : 0.0f;
+                for (int e = 0; e < 4; ++e) v[e] = n + e < a.r ? j.s * acc[t][4 * gq + e] : 0.0f;
                 *reinterpret_cast<uint2*>(orow + n) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
             }
         }
@@ -247,10 +257,10 @@ __device__ __forceinline__ void prepass_job(const PreJob& j, const PrologueArgs&
 // OUT[m, j] = bf16(s * sum of the slice partials in slice order) for j < r, 0 for
 // r <= j < r_pad; a thread takes 4 consecutive columns. The first `blocks0` workgroups
 // reduce job 0, the rest job 1.
-struct ReduceJob { const float* part; uint16_t* OUT; int splits; };
+struct ReduceJob { const float* part; uint16_t* OUT; int64_t ldo; int splits; float s; };
 
 __global__ __launch_bounds__(256)
-void prepass_reduce(ReduceJob j0, ReduceJob j1, int blocks0, int M, int ncols, int r, int r_pad, float s) {
+void prepass_reduce(ReduceJob j0, ReduceJob j1, int blocks0, int M, int ncols, int r, int r_pad) {
     const bool second = static_cast<int>(blockIdx.x) >= blocks0;
     const ReduceJob& jb = second ? j1 : j0;
     const int64_t idx = static_cast<int64_t>(second ? blockIdx.x - blocks0 : blockIdx.x) * 256 + threadIdx.x;
@@ -264,8 +274,8 @@ void prepass_reduce(ReduceJob j0, ReduceJob j1, int blocks0, int M, int ncols, i
         v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = j + e < r ? s * v[e] : 0.0f;
-    *reinterpret_cast<uint2*>(jb.OUT + m * r_pad + j) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    for (int e = 0; e < 4; ++e) v[e] = j + e < r ? jb.s * v[e] : 0.0f;
+    *reinterpret_cast<uint2*>(jb.OUT + m * jb.ldo + j) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
 // Adapter layouts; destination is [rows, r_pad] (pad) or [acols, r_pad] (transpose).
@@ -302,8 +312,10 @@ __device__ __forceinline__ void adapt_job(const PrologueArgs& a, int b) {
 // Row-major dequantisation of kDeqPerWG = 8192 weights (128 blocks): threads 0..127
 // form a_hat of one block each into LDS (the constants are loaded once per block,
 // not per weight); thread t takes the 8-weight code words t + 256 q (q = 0..3), so
-// every load and 16-byte store of a wave is contiguous.
-__device__ __forceinline__ void dequant_rows_job(const PrologueArgs& a, int b, const float* s_code,
+// every load and 16-byte store of a wave is contiguous. Of a paired weight, row o goes to
+// row 64 (o / 32) + o % 32 of what: its 32-row runs alternate with the other weight's (whose
+// what starts 32 rows later), so that a 64-wide tile of their product has both for 32 outputs.
+__device__ __forceinline__ void dequant_rows_job(const DeqJob& a, int b, const float* s_code,
                                                  float* s_ahat) {
     constexpr int kWords = kDeqPerWG / 8 / 256;  // code words per thread
     const int tid = threadIdx.x;
@@ -328,7 +340,12 @@ __device__ __forceinline__ void dequant_rows_job(const PrologueArgs& a, int b, c
         float w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = s_code[(cw[q] >> (4 * e)) & 0xFu] * ahat;
-        *reinterpret_cast<uint4*>(a.what + e0) = uint4{pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]),
+        int64_t at = e0;
+        if (a.paired) {
+            const uint32_t o = static_cast<uint32_t>(e0) / static_cast<uint32_t>(a.d_in);   // n < 2^31
+            at = e0 + static_cast<int64_t>(o & ~31u) * a.d_in;
+        }
+        *reinterpret_cast<uint4*>(a.what + at) = uint4{pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]),
                                                       pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7])};
     }
 }
@@ -341,7 +358,7 @@ __device__ __forceinline__ void dequant_rows_job(const PrologueArgs& a, int b, c
 // dequantises into an LDS tile that is written out transposed as W_hat^T rows.
 constexpr int kTransTiles = 4;
 
-__device__ __forceinline__ void dequant_transposed_job(const PrologueArgs& a, int b, const float* s_code,
+__device__ __forceinline__ void dequant_transposed_job(const DeqJob& a, int b, const float* s_code,
                                                        float* s_ahat, uint16_t* tile) {
     const int tid = threadIdx.x;
     const int tiles_i = static_cast<int>(a.d_in / 64);
@@ -386,14 +403,14 @@ __device__ __forceinline__ void dequant_transposed_job(const PrologueArgs& a, in
             const int cc = c & 7;            // 16-byte chunk: output columns o0 + 8 cc .. + 7
             const int64_t i = static_cast<int64_t>(t0 + k) * 64 + il;
             if (o0 + 8 * cc < a.d_out)       // d_out % 64 == 0 on this path: whole chunks
-                *reinterpret_cast<uint4*>(a.what + i * a.d_out + o0 + 8 * cc) =
+                *reinterpret_cast<uint4*>(a.what + i * a.ldw + o0 + 8 * cc) =
                     *reinterpret_cast<const uint4*>(&tile[il * kTP + 8 * cc]);
         }
     }
 }
 
 // Workgroup bd of the double dequantisation, with 16 KB of LDS scratch.
-__device__ __forceinline__ void dequant_jobs(const PrologueArgs& a, int bd, const NF4Tables& tab, char* lds) {
+__device__ __forceinline__ void dequant_jobs(const DeqJob& a, int bd, const NF4Tables& tab, char* lds) {
     float* s_code = reinterpret_cast<float*>(lds);             // 16 floats
     float* s_ahat = reinterpret_cast<float*>(lds + 64);        // up to 256 floats
     if (threadIdx.x < 16) s_code[threadIdx.x] = tab.code[threadIdx.x];
@@ -401,7 +418,7 @@ __device__ __forceinline__ void dequant_jobs(const PrologueArgs& a, int bd, cons
         // Workgroups go to the 8 XCDs in turn; a code row's 128-byte line spans several
         // neighbouring regions, so each XCD takes a contiguous range of regions and a
         // line is fetched into one XCD's L2 rather than into several.
-        const int bl = (a.n_deq & 7) == 0 ? (bd & 7) * (a.n_deq >> 3) + (bd >> 3) : bd;
+        const int bl = (a.n & 7) == 0 ? (bd & 7) * (a.n >> 3) + (bd >> 3) : bd;
         dequant_transposed_job(a, bl, s_code, s_ahat, reinterpret_cast<uint16_t*>(lds + 64 + 1024));
     } else {
         dequant_rows_job(a, bd, s_code, s_ahat);
@@ -427,7 +444,81 @@ void prologue_kernel(PrologueArgs a, NF4Tables tab) {
         adapt_job(a, b - a.n_pre);
         return;
     }
-    dequant_jobs(a, b - a.n_pre - a.n_adapt, tab, lds);
+    dequant_jobs(a.deq, b - a.n_pre - a.n_adapt, tab, lds);
+}
+
+// ---------------------------------------------------------------------------
+// The gated block's two projections side by side (gated.hip): both weights' dequantisation,
+// both pre-passes and both adapters in one launch. The rank columns of the gate come first,
+// pad of them, then those of the up projection; an output row has its own projection's adapter
+// and zeros at the other's columns.
+// ---------------------------------------------------------------------------
+struct GatedPrologueArgs {
+    PrologueArgs p;                  // pre[0], pre[1], M, r, r_pad (pad); deq: the gate's
+    DeqJob deq_up;
+    GatedGradArgs grad;              // the gradient's elementwise part (n_grad workgroups)
+    const uint16_t* asrc[2];         // B_g, B_u [d_ff, r] (forward) or A_g, A_u [r, d_in] (gradient)
+    uint16_t* adst; int64_t arows;   // [arows, k2]
+    int k2, backward, n_adapt, n_grad;
+};
+
+// 8 entries of a row of the adapter layout: forward, row 64 k + 32 w + i is row 32 k + i of
+// projection w; gradient, row i is column i of both A.
+__device__ __forceinline__ void gated_adapt_job(const GatedPrologueArgs& a, int b) {
+    const int cpr = a.k2 / 8, r = a.p.r, pad = a.p.r_pad;
+    const int64_t c = static_cast<int64_t>(b) * 256 + threadIdx.x;
+    if (c >= a.arows * cpr) return;
+    const int64_t i = c / cpr;
+    const int j0 = static_cast<int>(c % cpr) * 8;
+    const int w = j0 >= pad ? 1 : 0, q0 = j0 - w * pad;      // pad % 8 == 0: a chunk is of one projection
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+    if (a.backward || static_cast<int>(i >> 5 & 1) == w) {
+        const uint16_t* src = a.asrc[w];
+        const int64_t row = a.backward ? i : (i >> 6) * 32 + (i & 31);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (q0 + e < r) {
+                const int64_t at = a.backward ? (q0 + e) * a.arows + row : row * r + q0 + e;
+                v[e >> 1] |= static_cast<uint32_t>(src[at]) << (16 * (e & 1));
+            }
+        }
+    }
+    *reinterpret_cast<uint4*>(a.adst + c * 8) = uint4{v[0], v[1], v[2], v[3]};
+}
+
+template <int NT, bool KM>
+__global__ __launch_bounds__(256)
+void gated_prologue_kernel(GatedPrologueArgs a, NF4Tables tab) {
+    __shared__ PreStage<NT> s0, s1;
+    int b = blockIdx.x;
+    if (b < a.p.n_pre) {
+        const bool up = b >= a.p.pre[0].n;
+        prepass_job<NT, KM>(a.p.pre[up], a.p, up ? b - a.p.pre[0].n : b, s0, s1);
+        return;
+    }
+    b -= a.p.n_pre;
+    if (b < a.n_grad) {
+        gated_grad_job(a.grad, b);
+        return;
+    }
+    b -= a.n_grad;
+    if (b < a.n_adapt) {
+        gated_adapt_job(a, b);
+        return;
+    }
+    b -= a.n_adapt;
+    char* lds = reinterpret_cast<char*>(s1.x);
+    if (b < a.p.deq.n) dequant_jobs(a.p.deq, b, tab, lds);
+    else dequant_jobs(a.deq_up, b - a.p.deq.n, tab, lds);
+}
+
+// One weight dequantised both ways (either may have no workgroups): a piece of a head
+__global__ __launch_bounds__(256)
+void dequant_both_kernel(DeqJob rows, DeqJob cols, NF4Tables tab) {
+    __shared__ uint4 lds[(64 + 1024 + 64 * kTP * sizeof(uint16_t) + 15) / 16];
+    const int b = blockIdx.x;
+    if (b < rows.n) dequant_jobs(rows, b, tab, reinterpret_cast<char*>(lds));
+    else dequant_jobs(cols, b - rows.n, tab, reinterpret_cast<char*>(lds));
 }
 
 // ---------------------------------------------------------------------------
@@ -689,7 +780,7 @@ void multi_prologue_kernel(MultiPrologueArgs a, NF4Tables tab) {
         multi_pre_job<NT, true>(a.pre[1], a, b, s0, s1);
         return;
     }
-    dequant_jobs(a.d, b - a.pre[1].n, tab, reinterpret_cast<char*>(s1.x));
+    dequant_jobs(a.d.deq, b - a.pre[1].n, tab, reinterpret_cast<char*>(s1.x));
 }
 
 // ---------------------------------------------------------------------------
@@ -823,8 +914,9 @@ namespace {
 // split it replaces (more than max(16, that split's) 64-wide K-chunks: the pre-pass
 // would outlast the rest of the launch); otherwise fp32 partials in ppart (if given).
 PreJob make_job(const uint16_t* P, int64_t ldp, int64_t M, int64_t K, const uint16_t* R, int64_t ldr,
-                uint16_t* OUT, float* ppart, int cat_max = 0) {
+                uint16_t* OUT, int64_t ldo, float s, float* ppart, int cat_max = 0) {
     PreJob j;
+    j.ldo = ldo; j.s = s;
     j.P = P; j.ldp = ldp; j.K = static_cast<int>(K); j.R = R; j.ldr = ldr; j.OUT = OUT; j.ppart = ppart;
     const PrepassSplit ps = prepass_split(M, K);
     const int64_t nk = K / 64;
@@ -845,14 +937,19 @@ PreJob make_job(const uint16_t* P, int64_t ldp, int64_t M, int64_t K, const uint
 }
 
 // The dequantisation of a launch: its sizes and workgroups (none if what is null).
-void set_dequant(PrologueArgs& a, int64_t d_out, int64_t d_in, bool transposed, uint16_t* what) {
+DeqJob make_dequant(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in, bool transposed,
+                    uint16_t* what) {
+    DeqJob a{};
+    a.codes = codes; a.bc = bc;
     a.d_out = d_out; a.d_in = d_in; a.transposed = transposed ? 1 : 0; a.what = what;
+    a.ldw = transposed ? d_out : d_in;
     const int64_t n = d_out * d_in;
     a.trans_tiles = static_cast<int>(std::min<int64_t>(kTransTiles, std::max<int64_t>(1, (n / 4096) / 2048)));
-    a.n_deq = what == nullptr ? 0   // pre-pass (and adapter layout) only
-                              : static_cast<int>(transposed ? (d_in / 64 + a.trans_tiles - 1) / a.trans_tiles *
-                                                                  ((d_out + 63) / 64)
-                                                            : (n + kDeqPerWG - 1) / kDeqPerWG);
+    a.n = what == nullptr ? 0   // pre-pass (and adapter layout) only
+                          : static_cast<int>(transposed ? (d_in / 64 + a.trans_tiles - 1) / a.trans_tiles *
+                                                              ((d_out + 63) / 64)
+                                                        : (n + kDeqPerWG - 1) / kDeqPerWG);
+    return a;
 }
 
 // Launch the prologue for a (pre[0].n, pre[1].n set; the dequant and adapter fields
@@ -860,7 +957,7 @@ void set_dequant(PrologueArgs& a, int64_t d_out, int64_t d_in, bool transposed, 
 hipError_t launch_prologue_args(PrologueArgs& a, bool km0, bool km1, hipStream_t st) {
     a.n_pre = a.pre[0].n + a.pre[1].n;
     const int NT = (a.r + 31) / 32;
-    const dim3 grid(static_cast<unsigned>(a.n_pre + a.n_adapt + a.n_deq));
+    const dim3 grid(static_cast<unsigned>(a.n_pre + a.n_adapt + a.deq.n));
     const NF4Tables& tab = tables();
     if (km0 || km1) {
         if (!prepass_takes_kmajor(a.r) || (km0 && km1)) return hipErrorInvalidValue;
@@ -881,10 +978,10 @@ hipError_t launch_prologue_args(PrologueArgs& a, bool km0, bool km1, hipStream_t
     const int blocks0 = a.pre[0].n > 0 && a.pre[0].psplits > 1 && !a.pre[0].cat ? static_cast<int>(per_job) : 0;
     const int blocks1 = a.pre[1].n > 0 && a.pre[1].psplits > 1 && !a.pre[1].cat ? static_cast<int>(per_job) : 0;
     if (blocks0 + blocks1 > 0) {
-        const ReduceJob r0{a.pre[0].ppart, a.pre[0].OUT, a.pre[0].psplits};
-        const ReduceJob r1{a.pre[1].ppart, a.pre[1].OUT, a.pre[1].psplits};
+        const ReduceJob r0{a.pre[0].ppart, a.pre[0].OUT, a.pre[0].ldo, a.pre[0].psplits, a.pre[0].s};
+        const ReduceJob r1{a.pre[1].ppart, a.pre[1].OUT, a.pre[1].ldo, a.pre[1].psplits, a.pre[1].s};
         QN_LAUNCH("prepass_reduce", st, prepass_reduce, dim3(static_cast<unsigned>(blocks0 + blocks1)), dim3(256), 0,
-                  st, r0, r1, blocks0, a.M, 32 * NT, a.r, a.r_pad, a.s);
+                  st, r0, r1, blocks0, a.M, 32 * NT, a.r, a.r_pad);
     }
     return hipGetLastError();
 }
@@ -898,19 +995,18 @@ hipError_t launch_prologue(const uint8_t* codes, const BlockConsts& bc, int64_t 
                            int r_pad, int adapt_mode, const uint16_t* asrc, uint16_t* adst, int64_t arows,
                            int64_t acols, float* ppart, hipStream_t st) {
     PrologueArgs a{};
-    a.codes = codes; a.bc = bc;
     // With the adapter laid out here (r < r_pad), the K-slices of the pre-pass can each
     // take r of the r_pad columns and the adapter repeat once per slice: the GEMM's
     // LoRA K-steps then add the slice partials, and no reduction pass is needed.
     const int cat_max = adapt_mode != 0 && r % 4 == 0 ? r_pad / r : 0;
-    a.pre[0] = make_job(P, ldp, M, K, R, ldr, OUT, ppart, cat_max);
+    a.pre[0] = make_job(P, ldp, M, K, R, ldr, OUT, r_pad, s, ppart, cat_max);
     a.pre[1] = PreJob{};
-    a.M = static_cast<int>(M); a.r = r; a.s = s; a.r_pad = r_pad;
+    a.M = static_cast<int>(M); a.r = r; a.r_pad = r_pad;
     a.adapt_mode = adapt_mode; a.asrc = asrc; a.adst = adst; a.arows = arows; a.acols = acols;
     a.reps = a.pre[0].cat ? a.pre[0].psplits : 1;
     const int64_t adapt_elems = adapt_mode == 0 ? 0 : (adapt_mode == 1 ? arows : acols) * r_pad;
     a.n_adapt = static_cast<int>((adapt_elems / 8 + 255) / 256);    // one 8-entry chunk per thread
-    set_dequant(a, d_out, d_in, transposed, what);
+    a.deq = make_dequant(codes, bc, d_out, d_in, transposed, what);
     static_assert(64 + 1024 + 64 * kTP * sizeof(uint16_t) <= sizeof(PreStage<1>::x), "dequant scratch fits a stage");
     return launch_prologue_args(a, r_kmajor, false, st);
 }
@@ -920,11 +1016,84 @@ hipError_t launch_prepass_pair(const uint16_t* P0, int64_t ldp0, int64_t K0, con
                                const uint16_t* R1, int64_t ldr1, bool r1_kmajor, uint16_t* OUT1, float* ppart1,
                                int64_t M, int r, float s, int r_pad, hipStream_t st) {
     PrologueArgs a{};
-    a.pre[0] = make_job(P0, ldp0, M, K0, R0, ldr0, OUT0, ppart0);
-    a.pre[1] = make_job(P1, ldp1, M, K1, R1, ldr1, OUT1, ppart1);
-    a.M = static_cast<int>(M); a.r = r; a.s = s; a.r_pad = r_pad;
-    a.n_adapt = 0; a.n_deq = 0; a.trans_tiles = 1; a.reps = 1;
+    a.pre[0] = make_job(P0, ldp0, M, K0, R0, ldr0, OUT0, r_pad, s, ppart0);
+    a.pre[1] = make_job(P1, ldp1, M, K1, R1, ldr1, OUT1, r_pad, s, ppart1);
+    a.M = static_cast<int>(M); a.r = r; a.r_pad = r_pad;
+    a.n_adapt = 0; a.reps = 1;
     return launch_prologue_args(a, false, r1_kmajor, st);
+}
+
+hipError_t launch_gated_prologue(const GatedCall& c, bool backward, const GatedProlog& o, hipStream_t st) {
+    GatedPrologueArgs a{};
+    const bool first = o.what != nullptr;            // the launch with the weights' and adapters' layouts
+    a.p.M = static_cast<int>(c.M); a.p.r = c.r; a.p.r_pad = gated_pad(c.r);
+    const int64_t K = backward ? c.d_ff : c.d_in;
+    if (c.r > 0 && o.pre_out != nullptr) {
+        for (int w = 0; w < 2; ++w) {
+            const bool km = backward && prepass_takes_kmajor(c.r);
+            const uint16_t* R = backward ? (km ? c.B[w] : o.bt[w]) : c.A[w];
+            const uint16_t* P = backward ? o.pre_in + w * c.d_ff : o.pre_in;
+            a.p.pre[w] = make_job(P, o.ld_in, c.M, K, R, K, o.pre_out + w * gated_pad(c.r), gated_k2(c.r), c.s[w],
+                                  o.ppart[w]);
+        }
+    }
+    a.p.n_pre = a.p.pre[0].n + a.p.pre[1].n;
+    if (first) {
+        for (int w = 0; w < 2; ++w) {
+            DeqJob& d = w == 0 ? a.p.deq : a.deq_up;
+            if (backward) {
+                d = make_dequant(c.codes[w], c.bc[w], c.d_ff, c.d_in, true, o.what + w * c.d_ff);
+                d.ldw = 2 * c.d_ff;
+            } else {
+                d = make_dequant(c.codes[w], c.bc[w], c.d_ff, c.d_in, false, o.what + w * 32 * c.d_in);
+                d.paired = 1;
+            }
+            a.asrc[w] = backward ? c.A[w] : c.B[w];
+        }
+        a.backward = backward ? 1 : 0;
+        a.k2 = gated_k2(c.r);
+        a.adst = o.adapt;
+        a.arows = backward ? c.d_in : 2 * c.d_ff;
+        a.n_adapt = static_cast<int>((a.arows * (a.k2 / 8) + 255) / 256);
+        if (backward) {
+            a.grad = o.grad;
+            a.n_grad = gated_grad_blocks(o.grad);
+        }
+    }
+    const dim3 grid(static_cast<unsigned>(a.p.n_pre + a.n_grad + a.n_adapt + a.p.deq.n + a.deq_up.n));
+    const NF4Tables& tab = tables();
+    const int NT = std::max(1, (c.r + 31) / 32);
+    if (backward && prepass_takes_kmajor(c.r)) {
+        QN_LAUNCH("gated_prologue_kernel", st, (gated_prologue_kernel<1, true>), grid, dim3(256), 0, st, a, tab);
+    } else {
+        switch (a.p.n_pre > 0 ? NT : 1) {
+#define QN_PRO_CASE(T) \
+            case T: QN_LAUNCH("gated_prologue_kernel", st, (gated_prologue_kernel<T, false>), grid, dim3(256), 0, st, \
+                              a, tab); break;
+            QN_PRO_CASE(1) QN_PRO_CASE(2) QN_PRO_CASE(3) QN_PRO_CASE(4)
+            QN_PRO_CASE(5) QN_PRO_CASE(6) QN_PRO_CASE(7) QN_PRO_CASE(8)
+#undef QN_PRO_CASE
+            default: return hipErrorInvalidValue;
+        }
+    }
+    if (a.p.pre[0].psplits > 1) {
+        const int blocks = static_cast<int>((c.M * (gated_pad(c.r) / 4) + 255) / 256);
+        const ReduceJob r0{a.p.pre[0].ppart, a.p.pre[0].OUT, a.p.pre[0].ldo, a.p.pre[0].psplits, a.p.pre[0].s};
+        const ReduceJob r1{a.p.pre[1].ppart, a.p.pre[1].OUT, a.p.pre[1].ldo, a.p.pre[1].psplits, a.p.pre[1].s};
+        QN_LAUNCH("prepass_reduce", st, prepass_reduce, dim3(static_cast<unsigned>(2 * blocks)), dim3(256), 0, st, r0, r1,
+                  blocks, a.p.M, 32 * NT, c.r, gated_pad(c.r));
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_dequant_both(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
+                               uint16_t* rows, uint16_t* cols, int64_t ld_cols, hipStream_t st) {
+    const DeqJob jr = make_dequant(codes, bc, d_out, d_in, false, rows);
+    DeqJob jc = make_dequant(codes, bc, d_out, d_in, true, cols);
+    jc.ldw = ld_cols;
+    QN_LAUNCH("dequant_both_kernel", st, dequant_both_kernel, dim3(static_cast<unsigned>(jr.n + jc.n)), dim3(256), 0, st,
+              jr, jc, tables());
+    return hipGetLastError();
 }
 
 PrepassSplit multi_pre_split(int64_t M, int64_t K) {
@@ -941,8 +1110,8 @@ hipError_t launch_multi_prologue(const uint8_t* codes, const BlockConsts& bc, in
                                  bool transposed, uint16_t* what, const MultiPlan& plan, const float* s, int64_t M,
                                  int n, int r, int pieces, const MultiPre& p0, const MultiPre& p1, hipStream_t st) {
     MultiPrologueArgs a{};
-    a.d.codes = codes; a.d.bc = bc; a.d.M = static_cast<int>(M); a.d.r = r;
-    set_dequant(a.d, d_out, d_in, transposed, what);
+    a.d.M = static_cast<int>(M); a.d.r = r;
+    a.d.deq = make_dequant(codes, bc, d_out, d_in, transposed, what);
     a.plan = plan; a.s = s; a.pieces = pieces;
     a.max_items = static_cast<int>(multi_max_items(M, n));
     const MultiPre* in[2] = {&p0, &p1};
@@ -952,7 +1121,7 @@ hipError_t launch_multi_prologue(const uint8_t* codes, const BlockConsts& bc, in
         a.pre[i] = MultiPreJob{in[i]->P, in[i]->ldp, static_cast<int>(in[i]->K), in[i]->R, in[i]->part,
                                ps.splits == 1 ? in[i]->T : nullptr, ps.splits, ps.kper, a.max_items * ps.splits};
     }
-    const dim3 grid(static_cast<unsigned>(a.pre[0].n + a.pre[1].n + a.d.n_deq));
+    const dim3 grid(static_cast<unsigned>(a.pre[0].n + a.pre[1].n + a.d.deq.n));
     const NF4Tables& tab = tables();
     switch ((r + 31) / 32) {
 #define QN_PRO_CASE(T) \

@@ -396,6 +396,83 @@ int qlora_multi_bwd(const uint8_t* codes, const int8_t* qconst, const float* qsc
                     int64_t workspace_bytes, void* stream);
 
 /*
+ * The gated feed-forward block: a gate and an up projection of one input, each a QLoRA linear
+ * layer with its own NF4 weight [d_ff, d_in] and adapter, the activation of the one times the other:
+ *   G = dequant(W_g) x + s_g B_g (A_g x),  U = dequant(W_u) x + s_u B_u (A_u x),  H = act(G) U
+ *   [P1 LoRA: y = W0 x + s B(A x), for both; P2 card 1; N. Shazeer, "GLU Variants Improve
+ *    Transformer", for the product]
+ *   QN_ACT_SILU  act(g) = g / (1 + exp(-g))
+ *   QN_ACT_GELU  act(g) = g / 2 (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3)))
+ * Both weights have one shape and one format dq; both adapters one rank, 0 <= r <= 256 (0: none, A
+ * and B may be NULL). d_in, d_ff multiples of 64 (-2 otherwise; also where both weights together
+ * reach 4 GiB as bf16). Strides, alignment and errors as qlora_linear_fwd_ex. Outputs and the
+ * workspace must not overlap an input, or each other.
+ */
+#define QN_ACT_SILU 0
+#define QN_ACT_GELU 1
+
+/* Workspace bytes of the two calls (0 on sizes that the calls refuse). */
+int64_t qlora_gated_fwd_workspace_bytes(int64_t d_ff, int64_t d_in, int64_t d_seq, int r);
+int64_t qlora_gated_bwd_workspace_bytes(int64_t d_ff, int64_t d_in, int64_t d_seq, int r);
+
+/*
+ * qlora_gated_fwd - H [d_seq, d_ff] bf16 from X [d_seq, d_in]. GU (NULL: not kept) receives G in
+ * columns 0 .. d_ff - 1 and U in the d_ff columns after, bf16 [d_seq, 2 d_ff], for the gradient.
+ * H is formed from the float32 sums of G and U and rounded once.
+ */
+int qlora_gated_fwd(const uint8_t* codes_g, const int8_t* qconst_g, const float* qscale_g, const float* qmean_g,
+                    const uint8_t* codes_u, const int8_t* qconst_u, const float* qscale_u, const float* qmean_u,
+                    int64_t d_ff, int64_t d_in, int dq, const uint16_t* A_g, const uint16_t* B_g, float s_g,
+                    const uint16_t* A_u, const uint16_t* B_u, float s_u, int r, int act, const uint16_t* X, int64_t ldx,
+                    int64_t d_seq, uint16_t* H, int64_t ldh, uint16_t* GU, int64_t ldgu, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+
+/*
+ * qlora_gated_bwd - for the loss gradient dH [d_seq, d_ff] and the G, U that the forward kept:
+ *   dG = dH U act'(G),  dU = dH act(G)        bf16, side by side in dGU [d_seq, 2 d_ff]
+ *   dX = W_g^T dG + s_g A_g^T (B_g^T dG) + W_u^T dU + s_u A_u^T (B_u^T dU)     bf16 [d_seq, d_in]
+ * dX is formed from dG and dU as rounded to bf16. The adapters' gradients are qlora_lora_grads of X
+ * and the two halves of dGU (dY = dGU or dGU + d_ff, lddy = lddgu). dGU may be GU itself (the same
+ * pointer and stride): its elements are read before they are written.
+ */
+int qlora_gated_bwd(const uint8_t* codes_g, const int8_t* qconst_g, const float* qscale_g, const float* qmean_g,
+                    const uint8_t* codes_u, const int8_t* qconst_u, const float* qscale_u, const float* qmean_u,
+                    int64_t d_ff, int64_t d_in, int dq, const uint16_t* A_g, const uint16_t* B_g, float s_g,
+                    const uint16_t* A_u, const uint16_t* B_u, float s_u, int r, int act, const uint16_t* GU, int64_t ldgu,
+                    const uint16_t* dH, int64_t lddh, int64_t d_seq, uint16_t* dGU, int64_t lddgu, uint16_t* dX,
+                    int64_t lddx, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Workspace bytes of qlora_head_loss for a head of `vocab` rows, bf16 or (nf4) an NF4 weight, with
+ * or without the gradient (0 on sizes that the call refuses). */
+int64_t qlora_head_loss_workspace_bytes(int64_t vocab, int64_t d_in, int64_t d_seq, int nf4, int grad);
+
+/*
+ * qlora_head_loss - softmax cross entropy of every token over a frozen head, and (dX not NULL) the
+ * gradient of sum_t scale_t loss_t to the hidden states, in one pass over the vocabulary in pieces;
+ * the logits are not kept.
+ *   [P2 card 1: only the adapters are trained, the gradients flow through the frozen weights: the
+ *    loss is where they begin]
+ *   z = W x_t,  loss_t = log(sum_v exp(z_v)) - z_y,
+ *   dX_t = scale_t (sum_v p_v W_v - W_y),  p = softmax(z), y = target_t
+ *   head    bf16 W [vocab, d_in] at row stride ldw (codes, qconst, qscale, qmean NULL), or an NF4
+ *           weight [vocab, d_in] in format dq (W NULL; vocab a multiple of 64), which is taken as
+ *           nf4_double_dequant_ex gives it
+ *   X       bf16 [d_seq, d_in]
+ *   target  int64 [d_seq]; outside [0, vocab): the token is not counted, its loss and dX are zeros
+ *   scale   float32 [d_seq] or NULL (1): e.g. 1 / counted tokens for a mean
+ *   loss    float32 [d_seq] (not scaled);  dX bf16 [d_seq, d_in] or NULL
+ * d_in a multiple of 64; any vocab of a bf16 head. The logits are float32 sums; dX multiplies the
+ * exponentials rounded to bf16 (float32 sums; the target's own column is kept apart in float32). An
+ * infinite or NaN logit makes its token's loss and dX NaN or infinite, no other's. The result is
+ * deterministic. Strides, alignment and errors as qlora_linear_fwd_ex; outputs and the workspace must
+ * not overlap an input, or each other.
+ */
+int qlora_head_loss(const uint16_t* W, int64_t ldw, const uint8_t* codes, const int8_t* qconst, const float* qscale,
+                    const float* qmean, int dq, int64_t vocab, int64_t d_in, const uint16_t* X, int64_t ldx, int64_t d_seq,
+                    const int64_t* target, const float* scale, float* loss, uint16_t* dX, int64_t lddx, void* workspace,
+                    int64_t workspace_bytes, void* stream);
+
+/*
  * AdamW over many tensors in one launch, with the moments in 32 bits or in 8: the step
  * that takes the adapter gradients (float32) to the adapters the linear calls read (bf16).
  *   [P2 card 1: only the adapters are trained; I. Loshchilov, F. Hutter, "Decoupled Weight
