@@ -323,7 +323,7 @@ GatedWs gated_ws(int64_t d_ff, int64_t d_in, int64_t d_seq, int r, bool bwd) {
         w.ppart[i] = take(r > 0 ? prepass_part_bytes(d_seq, bwd ? d_ff : d_in, r) : 0);
         w.bt[i] = take(bwd && !qn::prepass_takes_kmajor(r) ? 2 * static_cast<int64_t>(r) * d_ff : 0);
     }
-    w.part = take(4 * (bwd ? qn::gemm_split_part_floats(d_seq, d_in, 2 * d_ff) : qn::gated_part_floats(d_seq, d_ff, d_in)));
+    w.part = take(4 * (bwd ? qn::gated_dx_part_floats(d_seq, d_ff, d_in) : qn::gated_part_floats(d_seq, d_ff, d_in)));
     w.bytes = off;
     return w;
 }
@@ -1130,8 +1130,7 @@ int qlora_gated_bwd(const uint8_t* codes_g, const int8_t* qconst_g, const float*
         }
         if ((e = qn::launch_gated_prologue(c, true, p, st)) != hipSuccess) return hip_fail(e, "qlora_gated_bwd (pre-pass)");
     }
-    e = qn::launch_gemm_nt(dGU, lddgu, o.what, 2 * d_ff, 2 * d_ff, t, qn::gated_k2(r), o.adapt, qn::gated_k2(r),
-                           qn::gated_k2(r), dX, lddx, d_seq, d_in, reinterpret_cast<float*>(ws + w.part), st);
+    e = qn::launch_gated_dx(c, dGU, lddgu, o.what, t, o.adapt, dX, lddx, reinterpret_cast<float*>(ws + w.part), st);
     if (e != hipSuccess) return hip_fail(e, "qlora_gated_bwd (gemm)");
     return 0;
 }

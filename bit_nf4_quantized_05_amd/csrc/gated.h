@@ -110,8 +110,8 @@ __device__ __forceinline__ void gated_grad_job(const GatedGradArgs& a, int b) {
 }
 
 // ---- prologue.hip ----
-// The layouts (what not null): both weights dequantised side by side to what (forward: rows in
-// runs of 32 in turn, [2 d_ff, d_in]; gradient: transposed, [d_in, 2 d_ff]), both adapters to
+// The layouts (what not null): both weights dequantised to what (forward: gate above up, [2 d_ff,
+// d_in]; gradient: transposed, side by side, [d_in, 2 d_ff]), both adapters to
 // adapt ([2 d_ff, k2] or [d_in, k2]) and, in the gradient, the elementwise part grad. And (pre_out
 // not null, r > 0) the rank products of pre_in: pre_out [M, k2] = s_w pre_in R_w^T, R = A of X or
 // B of the halves of dGU; bt: B^T [r, d_ff] where the pre-pass cannot read B itself.
@@ -128,11 +128,15 @@ hipError_t launch_dequant_both(const uint8_t* codes, const BlockConsts& bc, int6
                                uint16_t* rows, uint16_t* cols, int64_t ld_cols, hipStream_t st);
 
 // ---- gated.hip ----
-// H (and GU, if not null) from X, the paired weight what, the rank products t [M, k2] and the
-// adapters adapt [2 d_ff, k2]; part holds gated_part_floats(M, d_ff, d_in) floats.
+// H (and GU, if not null) from X, the weights what, the rank products t [M, k2] and the adapters
+// adapt [2 d_ff, k2] (t, adapt unused without adapters); part holds gated_part_floats floats.
 int64_t gated_part_floats(int64_t M, int64_t d_ff, int64_t d_in);
 hipError_t launch_gated_gemm(const GatedCall& c, const uint16_t* X, int64_t ldx, const uint16_t* what, const uint16_t* t,
                              const uint16_t* adapt, uint16_t* H, int64_t ldh, uint16_t* GU, int64_t ldgu, float* part,
                              hipStream_t st);
+// dX from dGU, what [d_in, 2 d_ff], t [M, k2] and adapt [d_in, k2]; part: gated_dx_part_floats
+int64_t gated_dx_part_floats(int64_t M, int64_t d_ff, int64_t d_in);
+hipError_t launch_gated_dx(const GatedCall& c, const uint16_t* dGU, int64_t lddgu, const uint16_t* what, const uint16_t* t,
+                           const uint16_t* adapt, uint16_t* dX, int64_t lddx, float* part, hipStream_t st);
 
 }  // namespace qn

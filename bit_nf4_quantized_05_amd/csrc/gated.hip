@@ -3,186 +3,246 @@
 // (the gate and up projections of the MLP pair, each a QLoRA linear layer: whoami-wesleyyou.top
 // "LoRA", learn.ifs.name deck card 1).
 //
-// One MFMA contraction makes both: the weights are dequantised into one [2 d_ff, d_in] operand
-// in which runs of 32 gate rows and the 32 up rows of the same outputs alternate, so that the
-// 64-wide sub-tile of a wave (two 32 x 32 accumulators) has G in the first and U in the second,
-// for the same lane and register. The activation and the product are then register arithmetic
-// in the epilogue, G and U reach memory only where the gradient needs them, and X is read once.
-// The K loop is the linear layer's (gemm_core.h), with the same split of the last round's tiles.
+// One MFMA contraction makes both: the weights are dequantised into one [2 d_ff, d_in] operand, gate
+// above up, and a 256 x 256 tile takes 128 gate rows and the 128 up rows of the same outputs, so that
+// G and U of an output are sums of the same lane (gemm_turns.h: the two column halves of a tile).
+// The activation and the product are then register arithmetic in the epilogue, G and U reach memory
+// only where the gradient needs them, and X is read once.
 #include <hip/hip_runtime.h>
 
 #include "gated.h"
-#include "gemm_core.h"
+#include "gemm_turns.h"
 
 #include <algorithm>
 
 namespace qn {
 namespace {
 
-constexpr int kWM = 2, kWN = 4;
-using Waves = GemmWaves<kWM, kWN>;
-static_assert(Waves::TN == 2, "a wave's two column tiles are the gate's and the up projection's");
-
 struct GatedOut {
     uint16_t* H; int64_t ldh;
     uint16_t* GU; int64_t ldgu;       // or null
-    int d_ff, act;
+    int M, d_ff, act;
+    float* part;
 };
 
-template <bool kSplit>
-__global__ __launch_bounds__(Waves::NT, 1)
-void gated_gemm_kernel(GemmArgs g, GatedOut o) {
-    constexpr int TM = Waves::TM, TN = Waves::TN;
-    const int tid = threadIdx.x;
-    const int lane = tid & 63;
-    const int wave = tid >> 6;
-    const int wm = wave / kWN, wn = wave % kWN;
-    const int frow = lane & 31;
-    // tiles as in gemm_nt: contiguous ranges per XCD; on the split path [0, full) whole, then
-    // tile full + j % rem, split j / rem
-    const int bid = static_cast<int>(blockIdx.x);
-    const bool split_wg = kSplit && bid >= g.full;
-    const int T = kSplit ? g.full : g.tiles_m * g.tiles_n;
-    const int sj = split_wg ? bid - g.full : 0;
-    const int sk = split_wg ? sj / g.rem : 0;
-    const int logical = split_wg ? g.full + sj % g.rem : ((T % 8 == 0) ? (bid & 7) * (T >> 3) + (bid >> 3) : bid);
-    int tm, tn;
-    tile_coords(g, logical, tm, tn);
-    const int m0 = tm * BM, n0 = tn * BN;
-    const int kb = split_wg ? sk * g.kper : 0;
-    const int ke = split_wg ? min(kb + g.kper, g.kt1) : g.kt1;
-    f32x16 acc[TN][TM];
-    gemm_core<kWM, kWN, true>(
-        g, [&](int r) { return static_cast<uint32_t>(min(m0 + r, g.M - 1)); },
-        [&](int r) { return static_cast<uint32_t>(min(n0 + r, g.N - 1)); }, kb, ke, !split_wg || sk == g.splits - 1, acc);
-    if (split_wg) {
-        float* pt = g.part + (static_cast<int64_t>(sk) * g.rem + sj % g.rem) * (BM * BN);
+// A tile's 256 x 256 bf16 values from LDS to rows of C: columns col(c) .. + 7 for chunk c (0..31)
+template <class Col>
+__device__ __forceinline__ void store_rows(uint16_t* C, int64_t ldc, int m0, int M, int limit, const Col& col) {
+    const int c = threadIdx.x & 31;
+    const int n = col(c);
 #pragma unroll
-        for (int b = 0; b < TM; ++b) {
-            const int ml = wm * (TM * 32) + b * 32 + frow;
-#pragma unroll
-            for (int a = 0; a < TN; ++a)
-#pragma unroll
-                for (int gq = 0; gq < 4; ++gq) {
-                    const int nl = wn * 64 + a * 32 + 8 * gq + 4 * (lane >> 5);
-                    *reinterpret_cast<float4*>(pt + ml * BN + nl) =
-                        float4{acc[a][b][4 * gq], acc[a][b][4 * gq + 1], acc[a][b][4 * gq + 2], acc[a][b][4 * gq + 3]};
-                }
-        }
-        return;
-    }
-    const int h0 = tn * (BN / 2);                    // the tile's first output column
-    if (o.GU != nullptr) {
-        // G and U as a 256 x 512 B tile in LDS, rows 0..127 in the first stage, 16-byte chunk j of
-        // row r at j ^ (r & 31); out as 256-byte runs of G and of U
-#pragma unroll
-        for (int b = 0; b < TM; ++b) {
-            const int rl = wm * (TM * 32) + b * 32 + frow;
-            char* rowp = reinterpret_cast<char*>((rl >> 7) ? g_st1 : g_st0) + (rl & 127) * 512;
-#pragma unroll
-            for (int a = 0; a < TN; ++a)
-#pragma unroll
-                for (int gq = 0; gq < 4; ++gq) {
-                    const int nl = a * 128 + wn * 32 + 8 * gq + 4 * (lane >> 5);      // G first, then U
-                    *reinterpret_cast<uint2*>(rowp + (((nl >> 3) ^ (rl & 31)) << 4) + ((nl & 7) << 1)) =
-                        uint2{pack_bf16x2(acc[a][b][4 * gq], acc[a][b][4 * gq + 1]),
-                              pack_bf16x2(acc[a][b][4 * gq + 2], acc[a][b][4 * gq + 3])};
-                }
-        }
-        __syncthreads();
-        const int cj = tid & 31;
-        const int col = h0 + (cj & 15) * 8;
-#pragma unroll
-        for (int i = 0; i < BM / (Waves::NT / 32); ++i) {
-            const int r = i * (Waves::NT / 32) + (tid >> 5);
-            const char* arr = reinterpret_cast<const char*>((r >> 7) ? g_st1 : g_st0);
-            const uint4 v = *reinterpret_cast<const uint4*>(arr + (r & 127) * 512 + ((cj ^ (r & 31)) << 4));
-            if (m0 + r < g.M && col < o.d_ff)
-                *reinterpret_cast<uint4*>(o.GU + static_cast<int64_t>(m0 + r) * o.ldgu + (cj >> 4) * o.d_ff + col) = v;
-        }
-        __syncthreads();
-    }
-    // H as a 256 x 256 B tile in the first stage, chunk j of row r at j ^ (r & 15)
-#pragma unroll
-    for (int b = 0; b < TM; ++b) {
-        const int rl = wm * (TM * 32) + b * 32 + frow;
-        char* rowp = reinterpret_cast<char*>(g_st0) + rl * 256;
-#pragma unroll
-        for (int gq = 0; gq < 4; ++gq) {
-            const int nl = wn * 32 + 8 * gq + 4 * (lane >> 5);
-            float h[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) h[e] = gated_act(o.act, acc[0][b][4 * gq + e]) * acc[1][b][4 * gq + e];
-            *reinterpret_cast<uint2*>(rowp + (((nl >> 3) ^ (rl & 15)) << 4) + ((nl & 7) << 1)) =
-                uint2{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])};
-        }
-    }
-    __syncthreads();
-    const int cj = tid & 15;
-    const int col = h0 + cj * 8;
-#pragma unroll
-    for (int i = 0; i < BM / (Waves::NT / 16); ++i) {
-        const int r = i * (Waves::NT / 16) + (tid >> 4);
-        const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(g_st0) + r * 256 + ((cj ^ (r & 15)) << 4));
-        if (m0 + r < g.M && col < o.d_ff) *reinterpret_cast<uint4*>(o.H + static_cast<int64_t>(m0 + r) * o.ldh + col) = v;
+    for (int i = 0; i < 16; ++i) {
+        const int row = 16 * i + (threadIdx.x >> 5);
+        const uint4 v = turn_get<256>(row, c);
+        if (m0 + row < M && n < limit) *reinterpret_cast<uint4*>(C + static_cast<int64_t>(m0 + row) * ldc + n) = v;
     }
 }
 
-// Split tiles: G and U summed over the splits in order, then the activation and the product;
+template <bool kKeep>
+__global__ __launch_bounds__(kTurnThreads, 1)
+void gated_gemm_kernel(TurnArgs g, TurnSplit s, GatedOut o) {
+    const TurnPlace p = turn_place(s, static_cast<int>(blockIdx.x), g.kt1);
+    if (p.tile < 0) return;
+    const int m0 = p.tm * kTurnTile, h0 = p.tn * (kTurnTile / 2);
+    TurnSums acc;
+    gemm_turns<true>(
+        g, [&](int r) { return static_cast<uint32_t>(min(m0 + r, o.M - 1)); },
+        [&](int r) { return static_cast<uint32_t>((r < 128 ? 0 : o.d_ff) + min(h0 + (r & 127), o.d_ff - 1)); }, p.kb, p.ke,
+        p.share < 0 || p.share == s.splits - 1, acc);
+    if (p.share >= 0) {
+        turn_put_sums(o.part + (static_cast<int64_t>(p.share) * s.rem + p.tile) * (kTurnTile * kTurnTile), acc, false);
+        return;
+    }
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int row0 = 64 * (wave >> 2) + (lane & 15), col0 = 32 * (wave & 3) + 4 * (lane >> 4);
+    if constexpr (kKeep) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const f32x4t v = acc[h][q][i][j];
+                        turn_put<256>(128 * h + 16 * i + row0, 128 * q + 16 * j + col0, v[0], v[1], v[2], v[3]);
+                    }
+        __syncthreads();
+        // 256 bytes of G, then 256 of U, per row
+        store_rows(o.GU, o.ldgu, m0, o.M, 2 * o.d_ff, [&](int c) {
+            const int n = h0 + 8 * (c & 15);
+            return n < o.d_ff ? n + (c >> 4) * o.d_ff : 2 * o.d_ff;
+        });
+        __syncthreads();
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = gated_act(o.act, acc[h][0][i][j][e]) * acc[h][1][i][j][e];
+                turn_put<128>(128 * h + 16 * i + row0, 16 * j + col0, v[0], v[1], v[2], v[3]);
+            }
+    __syncthreads();
+    const int c = threadIdx.x & 15;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int row = 32 * i + (threadIdx.x >> 4);
+        const uint4 v = turn_get<128>(row, c);
+        if (m0 + row < o.M && h0 + 8 * c < o.d_ff)
+            *reinterpret_cast<uint4*>(o.H + static_cast<int64_t>(m0 + row) * o.ldh + h0 + 8 * c) = v;
+    }
+}
+
+// Split tiles: G and U summed over the shares in order, then the activation and the product;
 // 4 outputs per thread, 32 workgroups per tile (8 rows each).
 template <int SP>
 __global__ __launch_bounds__(256)
-void gated_split_reduce(GemmArgs g, GatedOut o) {
+void gated_split_reduce(TurnSplit s, GatedOut o) {
     const int j = static_cast<int>(blockIdx.x) / 32;
     const int ml = (static_cast<int>(blockIdx.x) % 32) * 8 + (threadIdx.x >> 5);
     const int q = (threadIdx.x & 31) * 4;                             // output column of the tile
     int tm, tn;
-    tile_coords(g, g.full + j, tm, tn);
-    const int m = tm * BM + ml, n = tn * (BN / 2) + q;
-    if (m >= g.M || n >= o.d_ff) return;
-    const float* p = g.part + static_cast<int64_t>(j) * (BM * BN) + ml * BN + (q >> 5) * 64 + (q & 31);
-    const int64_t stride = static_cast<int64_t>(g.rem) * (BM * BN);
-    float4 v[2][SP];
+    turn_tile(s.full + j, s.tiles_m, s.tiles_n, tm, tn);
+    const int m = tm * kTurnTile + ml, n = tn * (kTurnTile / 2) + q;
+    if (m >= o.M || n >= o.d_ff) return;
+    const float* p = o.part + static_cast<int64_t>(j) * (kTurnTile * kTurnTile) + ml * kTurnTile + q;
+    const int64_t stride = static_cast<int64_t>(s.rem) * (kTurnTile * kTurnTile);
+    f32x4t v[2][SP];
 #pragma unroll
-    for (int s = 0; s < SP; ++s)
+    for (int k = 0; k < SP; ++k)
 #pragma unroll
-        for (int w = 0; w < 2; ++w) v[w][s] = *reinterpret_cast<const float4*>(p + s * stride + 32 * w);
-    float4 t[2] = {v[0][0], v[1][0]};
+        for (int w = 0; w < 2; ++w) v[w][k] = *reinterpret_cast<const f32x4t*>(p + k * stride + 128 * w);
+    f32x4t t[2] = {v[0][0], v[1][0]};
 #pragma unroll
-    for (int s = 1; s < SP; ++s)
+    for (int k = 1; k < SP; ++k)
 #pragma unroll
-        for (int w = 0; w < 2; ++w) { t[w].x += v[w][s].x; t[w].y += v[w][s].y; t[w].z += v[w][s].z; t[w].w += v[w][s].w; }
+        for (int w = 0; w < 2; ++w) t[w] = t[w] + v[w][k];
     if (o.GU != nullptr) {
 #pragma unroll
         for (int w = 0; w < 2; ++w)
             *reinterpret_cast<uint2*>(o.GU + static_cast<int64_t>(m) * o.ldgu + w * o.d_ff + n) =
-                uint2{pack_bf16x2(t[w].x, t[w].y), pack_bf16x2(t[w].z, t[w].w)};
+                uint2{pack_bf16x2(t[w][0], t[w][1]), pack_bf16x2(t[w][2], t[w][3])};
     }
+    float h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) h[e] = gated_act(o.act, t[0][e]) * t[1][e];
     *reinterpret_cast<uint2*>(o.H + static_cast<int64_t>(m) * o.ldh + n) =
-        uint2{pack_bf16x2(gated_act(o.act, t[0].x) * t[1].x, gated_act(o.act, t[0].y) * t[1].y),
-              pack_bf16x2(gated_act(o.act, t[0].z) * t[1].z, gated_act(o.act, t[0].w) * t[1].w)};
+        uint2{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])};
+}
+
+// dX = dGU [W_g; W_u] + U' A: a plain product, bf16 out
+struct GatedDx {
+    uint16_t* C; int64_t ldc;
+    int M, N;
+    float* part;
+};
+
+__global__ __launch_bounds__(kTurnThreads, 1)
+void gated_dx_kernel(TurnArgs g, TurnSplit s, GatedDx o) {
+    const TurnPlace p = turn_place(s, static_cast<int>(blockIdx.x), g.kt1);
+    if (p.tile < 0) return;
+    const int m0 = p.tm * kTurnTile, n0 = p.tn * kTurnTile;
+    TurnSums acc;
+    gemm_turns<true>(
+        g, [&](int r) { return static_cast<uint32_t>(min(m0 + r, o.M - 1)); },
+        [&](int r) { return static_cast<uint32_t>(min(n0 + r, o.N - 1)); }, p.kb, p.ke,
+        p.share < 0 || p.share == s.splits - 1, acc);
+    if (p.share >= 0) {
+        turn_put_sums(o.part + (static_cast<int64_t>(p.share) * s.rem + p.tile) * (kTurnTile * kTurnTile), acc, false);
+        return;
+    }
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int row0 = 64 * (wave >> 2) + (lane & 15), col0 = 32 * (wave & 3) + 4 * (lane >> 4);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const f32x4t v = acc[h][q][i][j];
+                    turn_put<256>(128 * h + 16 * i + row0, 128 * q + 16 * j + col0, v[0], v[1], v[2], v[3]);
+                }
+    __syncthreads();
+    store_rows(o.C, o.ldc, m0, o.M, o.N, [&](int c) { return n0 + 8 * c; });
+}
+
+// Split tiles: the shares' sums in order; 4 outputs per thread, 64 workgroups per tile
+template <int SP>
+__global__ __launch_bounds__(256)
+void gated_dx_reduce(TurnSplit s, GatedDx o) {
+    const int j = static_cast<int>(blockIdx.x) / 64;
+    const int ml = (static_cast<int>(blockIdx.x) % 64) * 4 + (threadIdx.x >> 6);
+    const int nl = (threadIdx.x & 63) * 4;
+    int tm, tn;
+    turn_tile(s.full + j, s.tiles_m, s.tiles_n, tm, tn);
+    const int m = tm * kTurnTile + ml, n = tn * kTurnTile + nl;
+    if (m >= o.M || n >= o.N) return;
+    const float* p = o.part + static_cast<int64_t>(j) * (kTurnTile * kTurnTile) + ml * kTurnTile + nl;
+    const int64_t stride = static_cast<int64_t>(s.rem) * (kTurnTile * kTurnTile);
+    f32x4t v[SP];
+#pragma unroll
+    for (int k = 0; k < SP; ++k) v[k] = *reinterpret_cast<const f32x4t*>(p + k * stride);
+    f32x4t t = v[0];
+#pragma unroll
+    for (int k = 1; k < SP; ++k) t = t + v[k];
+    *reinterpret_cast<uint2*>(o.C + static_cast<int64_t>(m) * o.ldc + n) = uint2{pack_bf16x2(t[0], t[1]), pack_bf16x2(t[2], t[3])};
+}
+
+TurnSplit fwd_split(int64_t M, int64_t d_ff, int64_t d_in) {
+    return turn_split(M, (d_ff + kTurnTile / 2 - 1) / (kTurnTile / 2), d_in / kTurnK);
+}
+TurnSplit dx_split(int64_t M, int64_t d_ff, int64_t d_in) {
+    return turn_split(M, (d_in + kTurnTile - 1) / kTurnTile, 2 * d_ff / kTurnK);
+}
+
+// P2 Q2^T of a call with adapters
+void add_ranks(TurnArgs& g, const uint16_t* t, const uint16_t* adapt, int k2, int64_t M, int64_t N) {
+    if (k2 == 0) return;
+    g.P2 = t; g.ldp2 = k2; g.Q2 = adapt; g.ldq2 = k2;
+    g.bytesP2 = static_cast<uint32_t>(2 * static_cast<int64_t>(k2) * M);
+    g.bytesQ2 = static_cast<uint32_t>(2 * static_cast<int64_t>(k2) * N);
+    g.kt2 = k2 / kTurnK;
 }
 
 }  // namespace
 
-int64_t gated_part_floats(int64_t M, int64_t d_ff, int64_t d_in) { return gemm_split_part_floats(M, 2 * d_ff, d_in); }
+int64_t gated_part_floats(int64_t M, int64_t d_ff, int64_t d_in) { return turn_split_floats(fwd_split(M, d_ff, d_in)); }
+int64_t gated_dx_part_floats(int64_t M, int64_t d_ff, int64_t d_in) { return turn_split_floats(dx_split(M, d_ff, d_in)); }
 
 hipError_t launch_gated_gemm(const GatedCall& c, const uint16_t* X, int64_t ldx, const uint16_t* what, const uint16_t* t,
                              const uint16_t* adapt, uint16_t* H, int64_t ldh, uint16_t* GU, int64_t ldgu, float* part,
                              hipStream_t st) {
-    const int64_t N = 2 * c.d_ff;
-    GemmArgs g = gemm_args(X, ldx, what, c.d_in, c.d_in, c.r > 0 ? t : nullptr, gated_k2(c.r), adapt, gated_k2(c.r),
-                           gated_k2(c.r), nullptr, 0, c.M, N, part);
-    const GatedOut o{H, ldh, GU, ldgu, static_cast<int>(c.d_ff), c.act};
-    if (g.splits <= 1) {
-        QN_LAUNCH("gated_gemm_kernel", st, gated_gemm_kernel<false>, dim3(g.tiles_m * g.tiles_n), dim3(Waves::NT), 0, st, g, o);
-        return hipGetLastError();
-    }
-    QN_LAUNCH("gated_gemm_split", st, gated_gemm_kernel<true>, dim3(g.full + g.rem * g.splits), dim3(Waves::NT), 0, st, g, o);
-    const dim3 rgrid(static_cast<unsigned>(g.rem * 32));
-    if (g.splits == 2) QN_LAUNCH("gated_split_reduce", st, gated_split_reduce<2>, rgrid, dim3(256), 0, st, g, o);
-    else if (g.splits == 3) QN_LAUNCH("gated_split_reduce", st, gated_split_reduce<3>, rgrid, dim3(256), 0, st, g, o);
-    else QN_LAUNCH("gated_split_reduce", st, gated_split_reduce<4>, rgrid, dim3(256), 0, st, g, o);
+    TurnArgs g = turn_args(X, ldx, c.M, what, c.d_in, 2 * c.d_ff, c.d_in);
+    add_ranks(g, t, adapt, gated_k2(c.r), c.M, 2 * c.d_ff);
+    const TurnSplit s = fwd_split(c.M, c.d_ff, c.d_in);
+    const GatedOut o{H, ldh, GU, ldgu, static_cast<int>(c.M), static_cast<int>(c.d_ff), c.act, part};
+    const dim3 grid(turn_split_grid(s));
+    if (GU != nullptr) QN_LAUNCH("gated_gemm_kernel", st, gated_gemm_kernel<true>, grid, dim3(kTurnThreads), 0, st, g, s, o);
+    else QN_LAUNCH("gated_gemm_kernel", st, gated_gemm_kernel<false>, grid, dim3(kTurnThreads), 0, st, g, s, o);
+    const dim3 rgrid(static_cast<unsigned>(s.rem * 32));
+    if (s.splits == 2) QN_LAUNCH("gated_split_reduce", st, gated_split_reduce<2>, rgrid, dim3(256), 0, st, s, o);
+    else if (s.splits == 3) QN_LAUNCH("gated_split_reduce", st, gated_split_reduce<3>, rgrid, dim3(256), 0, st, s, o);
+    else if (s.splits == 4) QN_LAUNCH("gated_split_reduce", st, gated_split_reduce<4>, rgrid, dim3(256), 0, st, s, o);
+    return hipGetLastError();
+}
+
+hipError_t launch_gated_dx(const GatedCall& c, const uint16_t* dGU, int64_t lddgu, const uint16_t* what, const uint16_t* t,
+                           const uint16_t* adapt, uint16_t* dX, int64_t lddx, float* part, hipStream_t st) {
+    TurnArgs g = turn_args(dGU, lddgu, c.M, what, 2 * c.d_ff, c.d_in, 2 * c.d_ff);
+    add_ranks(g, t, adapt, gated_k2(c.r), c.M, c.d_in);
+    const TurnSplit s = dx_split(c.M, c.d_ff, c.d_in);
+    const GatedDx o{dX, lddx, static_cast<int>(c.M), static_cast<int>(c.d_in), part};
+    QN_LAUNCH("gated_dx_kernel", st, gated_dx_kernel, dim3(turn_split_grid(s)), dim3(kTurnThreads), 0, st, g, s, o);
+    const dim3 rgrid(static_cast<unsigned>(s.rem * 64));
+    if (s.splits == 2) QN_LAUNCH("gated_dx_reduce", st, gated_dx_reduce<2>, rgrid, dim3(256), 0, st, s, o);
+    else if (s.splits == 3) QN_LAUNCH("gated_dx_reduce", st, gated_dx_reduce<3>, rgrid, dim3(256), 0, st, s, o);
+    else if (s.splits == 4) QN_LAUNCH("gated_dx_reduce", st, gated_dx_reduce<4>, rgrid, dim3(256), 0, st, s, o);
     return hipGetLastError();
 }
 

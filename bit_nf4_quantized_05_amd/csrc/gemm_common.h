@@ -28,12 +28,6 @@ struct GemmArgs {
     uint32_t bytesC, bytesBq, bytesBs;           // extents of the codes, 8-bit constants, scales
 };
 
-// The arguments of a product from memory (gemm_nt.hip): those of launch_gemm_nt, the split path
-// taken where part is not null and gemm_split says so (else splits = 1).
-GemmArgs gemm_args(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t ldq, int64_t K1, const uint16_t* P2,
-                   int64_t ldp2, const uint16_t* Q2, int64_t ldq2, int64_t K2, uint16_t* C, int64_t ldc, int64_t M,
-                   int64_t N, float* part);
-
 // Launches the in-GEMM dequantising forward kernel (gemm_nf4.hip) on arguments set up
 // as for gemm_nt: whole tiles, or (split) full whole tiles then rem tiles split
 // `splits` ways whose fp32 partials gemm_split_reduce adds.

@@ -29,7 +29,7 @@
 // tile; gemm_split_reduce adds a tile's S partials in split order and rounds to bf16.
 #include <hip/hip_runtime.h>
 
-#include "gemm_core.h"
+#include "gemm_common.h"
 #include "internal.h"
 #include "mfma_device.h"
 #include "nf4_device.h"
@@ -42,15 +42,24 @@ namespace {
 // ---------------------------------------------------------------------------
 // Main NT GEMM
 // ---------------------------------------------------------------------------
+// Two LDS stages as distinct objects, so the compiler can tell that reads of one
+// stage do not depend on in-flight direct-to-LDS loads into the other. Each holds
+// [P tile | Q tile] = 2 x 2048 chunks = 64 KB.
+__shared__ uint4 g_st0[2 * kChunks];
+__shared__ uint4 g_st1[2 * kChunks];
+
+// WM x WN waves; each wave owns a (256/WM) x (256/WN) sub-tile of 32x32 MFMA tiles.
 template <int WM, int WN, bool kSplit>
 __device__ __forceinline__ void gemm_nt_body(const GemmArgs& g) {
-    using W = GemmWaves<WM, WN>;
-    constexpr int NT = W::NT, TM = W::TM, TN = W::TN;
+    constexpr int NW = WM * WN;                 // waves
+    constexpr int NT = 64 * NW;                 // threads
+    constexpr int TM = BM / WM / 32;            // m sub-tiles per wave
+    constexpr int TN = BN / WN / 32;            // n sub-tiles per wave
+    constexpr int SEG = BM / NW / 8;            // 8-row load segments per wave and operand
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = tid >> 6;
     const int wm = wave / WN, wn = wave % WN;
-    const uint32_t frow = lane & 31;
     const int M = g.M, N = g.N;
 
     // ---- tile assignment: contiguous logical ranges per XCD, grouped raster. On the
@@ -67,15 +76,134 @@ __device__ __forceinline__ void gemm_nt_body(const GemmArgs& g) {
     tile_coords(g, logical, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
 
-    // K-steps of this workgroup: main steps [kb, ke) of P Q^T, then (last split, or no split)
-    // the kt2 LoRA steps
+    // ---- global -> LDS with buffer_load ... lds (16 B per lane). A tile row is 64
+    // bf16 = 128 B = 8 chunks; chunk c of tile row r is stored at c ^ ((r >> 1) & 7).
+    // The LDS has 64 banks of 4 B, so two consecutive rows cover all banks once, and
+    // 16 lanes reading one logical chunk of 16 consecutive rows hit 16 distinct 4-bank
+    // groups. One load fills a 1 KB segment = 8 rows: lane i lands at row i/8,
+    // position i%8, so it fetches chunk (i%8) ^ ((r >> 1) & 7). Wave w fills rows
+    // 8*SEG*w .. of both operand tiles; the per-lane byte offsets are fixed for the
+    // whole K loop, the K position goes in the scalar offset.
+    // 128-B rows, chunk c of row r at c ^ ((r >> 1) & 7); segment j = 8 rows starting
+    // at 8 (SEG w + j): (r >> 1) & 7 = 4 ((SEG w + j) & 1) + i/16 for lane i.
+    const uint32_t kcE = static_cast<uint32_t>((lane & 7) ^ (lane >> 4)) * 16u;
+    const uint32_t kcO = static_cast<uint32_t>((lane & 7) ^ (4 | (lane >> 4))) * 16u;
+    uint32_t voP[SEG], voQ[SEG], voP2[SEG], voQ2[SEG];
+#pragma unroll
+    for (int j = 0; j < SEG; ++j) {
+        const int rr = 8 * SEG * wave + 8 * j + (lane >> 3);
+        const uint32_t kc16 = (((SEG * wave + j) & 1) ? kcO : kcE);
+        const uint32_t rp = static_cast<uint32_t>(min(m0 + rr, M - 1));
+        const uint32_t rq = static_cast<uint32_t>(min(n0 + rr, N - 1));
+        voP[j] = rp * static_cast<uint32_t>(g.ldp * 2) + kc16;
+        voQ[j] = rq * static_cast<uint32_t>(g.ldq * 2) + kc16;
+        voP2[j] = rp * static_cast<uint32_t>(g.ldp2 * 2) + kc16;
+        voQ2[j] = rq * static_cast<uint32_t>(g.ldq2 * 2) + kc16;
+    }
+    const __amdgpu_buffer_rsrc_t rsP = make_rsrc(g.P, g.bytesP);
+    const __amdgpu_buffer_rsrc_t rsQ = make_rsrc(g.Q, g.bytesQ);
+    const __amdgpu_buffer_rsrc_t rsP2 = make_rsrc(g.P2, g.bytesP2);
+    const __amdgpu_buffer_rsrc_t rsQ2 = make_rsrc(g.Q2, g.bytesQ2);
+    // K-steps of this workgroup: main steps [kb, ke) of P Q^T, then (last split, or no
+    // split) the kt2 LoRA steps; step k of the loop is global step kb + k while k < ke - kb
     const int kb = split_wg ? sk * g.kper : 0;
     const int ke = split_wg ? min(kb + g.kper, g.kt1) : g.kt1;
     const bool lora = !split_wg || sk == g.splits - 1;
+    const int KT = (ke - kb) + (lora ? g.kt2 : 0);
+    const int kshift = kb;                      // global main step = local + kshift
+    const int kmain = ke - kb;
+
+#define QN_ISSUE(KTV, ST)                                                                         \
+    {                                                                                             \
+        const int kl_ = (KTV);                                                                    \
+        uint4* sp_ = (ST) + wave * (64 * SEG);                                                    \
+        uint4* sq_ = sp_ + kChunks;                                                               \
+        if (kl_ < kmain) {                                                                        \
+            const int so_ = (kl_ + kshift) * (BK * 2);                                            \
+            _Pragma("unroll") for (int j = 0; j < SEG; ++j) {                                     \
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsP, (lds_ptr_t)(sp_ + 64 * j), 16, voP[j], so_, 0, 0); \
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsQ, (lds_ptr_t)(sq_ + 64 * j), 16, voQ[j], so_, 0, 0); \
+            }                                                                                     \
+        } else {                                                                                  \
+            const int so_ = (kl_ - kmain) * (BK * 2);                                             \
+            _Pragma("unroll") for (int j = 0; j < SEG; ++j) {                                     \
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsP2, (lds_ptr_t)(sp_ + 64 * j), 16, voP2[j], so_, 0, 0); \
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rsQ2, (lds_ptr_t)(sq_ + 64 * j), 16, voQ2[j], so_, 0, 0); \
+            }                                                                                     \
+        }                                                                                         \
+    }
+
+    // ---- fragments: 32-row x 16-K reads per k16 sub-step kk (0..3)
+    const uint32_t frow = lane & 31;
+    const uint32_t fsw = (frow >> 1) & 7;
+    const uint32_t prow = (wm * (TM * 32) + frow) * 8;
+    const uint32_t qrow = kChunks + (wn * (TN * 32) + frow) * 8;
+    uint32_t chs[4];
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) chs[kk] = (2 * kk + (lane >> 5)) ^ fsw;
+#define QN_FRAGS(ST, CH, F)                                             \
+    {                                                                   \
+        F[0] = (ST)[qrow + (CH)];                                       \
+        _Pragma("unroll") for (int i = 0; i < TM; ++i) F[TN + i] = (ST)[prow + i * 256 + (CH)]; \
+        _Pragma("unroll") for (int i = 1; i < TN; ++i) F[i] = (ST)[qrow + i * 256 + (CH)];      \
+    }
+
     f32x16 acc[TN][TM];
-    gemm_core<WM, WN, true>(
-        g, [&](int r) { return static_cast<uint32_t>(min(m0 + r, M - 1)); },
-        [&](int r) { return static_cast<uint32_t>(min(n0 + r, N - 1)); }, kb, ke, lora, acc);
+#pragma unroll
+    for (int a = 0; a < TN; ++a)
+#pragma unroll
+        for (int b = 0; b < TM; ++b) acc[a][b] = f32x16{};
+#define QN_MFMAS(F)                                                            \
+    _Pragma("unroll") for (int a = 0; a < TN; ++a)                             \
+        _Pragma("unroll") for (int b = 0; b < TM; ++b)                         \
+            acc[a][b] = mfma32(F[a], F[TN + b], acc[a][b]);
+
+    uint4 fa[TM + TN], fb[TM + TN];
+    // One K-step on stage CUR (its kk = 0 fragments already in fa) while NXT receives
+    // step k+1; NXT last held step k-1, whose reads all finished before the previous
+    // step's barrier. Before the last sub-step every wave waits for its own loads and
+    // the barrier certifies NXT complete, so NXT's first fragments are read under the
+    // last MFMAs; CUR's reads are all done by then, so the next step may refill it.
+    // A wave runs its first three sub-steps at raised issue priority and drops it for
+    // the barrier, the next step's loads and the sub-step after the barrier, so the
+    // waves of a SIMD that are still in their MFMA run go first (2-4 % faster on the
+    // 4096^2 layer than equal priority; the results do not change).
+#define QN_STEP(KTV, CUR, NXT)                                                 \
+    {                                                                          \
+        const int k_ = (KTV);                                                  \
+        if (k_ + 1 < KT) QN_ISSUE(k_ + 1, NXT)                                 \
+        QN_FRAGS(CUR, chs[1], fb)                                              \
+        __builtin_amdgcn_s_setprio(1);                                         \
+        QN_MFMAS(fa)                                                           \
+        QN_INTERLEAVE_DS_MFMA((TM + TN));                                      \
+        QN_FRAGS(CUR, chs[2], fa)                                              \
+        QN_MFMAS(fb)                                                           \
+        QN_INTERLEAVE_DS_MFMA((TM + TN));                                      \
+        QN_FRAGS(CUR, chs[3], fb)                                              \
+        QN_MFMAS(fa)                                                           \
+        QN_INTERLEAVE_DS_MFMA((TM + TN));                                      \
+        __builtin_amdgcn_s_setprio(0);                                         \
+        __builtin_amdgcn_s_waitcnt(0);                                         \
+        QN_BARRIER();                                                          \
+        if (k_ + 1 < KT) QN_FRAGS(NXT, chs[0], fa)                             \
+        QN_MFMAS(fb)                                                           \
+        QN_INTERLEAVE_DS_MFMA((TM + TN));                                      \
+    }
+
+    QN_ISSUE(0, g_st0)
+    QN_WAIT_VM(0);
+    QN_BARRIER();
+    QN_FRAGS(g_st0, chs[0], fa)
+    int kt = 0;
+    for (; kt + 2 <= KT; kt += 2) {
+        QN_STEP(kt, g_st0, g_st1)
+        QN_STEP(kt + 1, g_st1, g_st0)
+    }
+    if (kt < KT) QN_STEP(kt, g_st0, g_st1)
+#undef QN_STEP
+#undef QN_MFMAS
+#undef QN_FRAGS
+#undef QN_ISSUE
 
     if (split_wg) {
         // fp32 partial tile of this split, compact 256 x 256: the lane's 4 consecutive n
@@ -195,10 +323,23 @@ int64_t gemm_split_part_floats(int64_t M, int64_t N, int64_t K1) {
     return gs.splits > 1 ? static_cast<int64_t>(gs.splits) * gs.rem * BM * BN : 0;
 }
 
-GemmArgs gemm_args(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t ldq, int64_t K1, const uint16_t* P2,
-                   int64_t ldp2, const uint16_t* Q2, int64_t ldq2, int64_t K2, uint16_t* C, int64_t ldc, int64_t M,
-                   int64_t N, float* part) {
-    GemmArgs g{};
+hipError_t launch_gemm_nt(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t ldq, int64_t K1,
+                          const uint16_t* P2, int64_t ldp2, const uint16_t* Q2, int64_t ldq2,
+                          int64_t K2, uint16_t* C, int64_t ldc, int64_t M, int64_t N, float* part,
+                          hipStream_t st, const uint8_t* codes, const BlockConsts* bc) {
+    GemmArgs g;
+    const bool deq = codes != nullptr;              // Q = W_hat formed from the codes in the kernel
+    g.codes = codes;
+    g.bc = deq ? *bc : BlockConsts{nullptr, nullptr, nullptr, 0, 0};
+    {
+        const NF4Tables& tab = tables();
+        for (int i = 0; i < 16; ++i) g.code[i] = tab.code[i];
+    }
+    const int64_t nblk = deq ? N * (K1 / BK) : 0;   // NF4 blocks of the weight (K1 % 64 == 0)
+    g.bytesC = static_cast<uint32_t>(nblk * 32);
+    g.bytesBq = static_cast<uint32_t>(nblk);
+    g.bytesBs = static_cast<uint32_t>(deq ? 4 * (((nblk - 1) >> g.bc.gshift) + 1) : 0);
+    if (deq) { Q = P; ldq = ldp; }                  // no bf16 weight operand
     g.tiles_m = static_cast<int>((M + BM - 1) / BM);
     g.tiles_n = static_cast<int>((N + BN - 1) / BN);
     if (P2 == nullptr) { P2 = P; Q2 = Q; ldp2 = ldp; ldq2 = ldq; K2 = 0; }
@@ -211,32 +352,13 @@ GemmArgs gemm_args(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t ld
     g.bytesP2 = static_cast<uint32_t>(2 * ldp2 * M);
     g.bytesQ2 = static_cast<uint32_t>(2 * ldq2 * N);
     const GemmSplit gs = gemm_split(M, N, K1);
-    g.splits = part == nullptr ? 1 : gs.splits;
+    g.splits = gs.splits;
     g.full = gs.full;
     g.rem = gs.rem;
     g.kper = (g.kt1 + g.splits - 1) / g.splits;
     g.part = part;
-    return g;
-}
-
-hipError_t launch_gemm_nt(const uint16_t* P, int64_t ldp, const uint16_t* Q, int64_t ldq, int64_t K1,
-                          const uint16_t* P2, int64_t ldp2, const uint16_t* Q2, int64_t ldq2,
-                          int64_t K2, uint16_t* C, int64_t ldc, int64_t M, int64_t N, float* part,
-                          hipStream_t st, const uint8_t* codes, const BlockConsts* bc) {
-    const bool deq = codes != nullptr;              // Q = W_hat formed from the codes in the kernel
-    if (deq) { Q = P; ldq = ldp; }                  // no bf16 weight operand
-    GemmArgs g = gemm_args(P, ldp, Q, ldq, K1, P2, ldp2, Q2, ldq2, K2, C, ldc, M, N, part);
-    g.codes = codes;
-    g.bc = deq ? *bc : BlockConsts{nullptr, nullptr, nullptr, 0, 0};
-    {
-        const NF4Tables& tab = tables();
-        for (int i = 0; i < 16; ++i) g.code[i] = tab.code[i];
-    }
-    const int64_t nblk = deq ? N * (K1 / BK) : 0;   // NF4 blocks of the weight (K1 % 64 == 0)
-    g.bytesC = static_cast<uint32_t>(nblk * 32);
-    g.bytesBq = static_cast<uint32_t>(nblk);
-    g.bytesBs = static_cast<uint32_t>(deq ? 4 * (((nblk - 1) >> g.bc.gshift) + 1) : 0);
-    if (g.splits <= 1) {
+    if (g.splits <= 1 || part == nullptr) {
+        g.splits = 1;
         if (deq) return launch_gemm_nf4_body(g, false, st);
         QN_LAUNCH("gemm_nt_kernel", st, gemm_nt_kernel, dim3(g.tiles_m * g.tiles_n), dim3(64 * kGemmWM * kGemmWN), 0,
                   st, g);

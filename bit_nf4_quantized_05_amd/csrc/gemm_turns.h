@@ -1,0 +1,350 @@
+// The K loop of the gated block's and the head's BF16 MFMA contractions (gated.hip,
+// head_loss.hip): a 256 x 256 tile of P Q^T (+ P2 Q2^T), both operands row-major with K
+// contiguous, in the accumulators of a workgroup of 8 waves. The tile's place, its rows and what
+// becomes of the sums are the caller's.
+//
+// Two groups of 4 waves (one wave of each on every SIMD) take turns: between two barriers one
+// group runs 16 MFMAs of 16 x 16 x 32 while the other reads its next fragments from LDS and issues
+// loads, so the matrix pipe of a SIMD has one wave's run after the other's and no MFMA waits for
+// an LDS read of its own wave. A K-step of 64 has four such phases, one per quarter of the tile
+// (128 x 128, of which a wave has 64 x 32):
+//   phase   reads from LDS       issues loads of     multiplies
+//   0       P half 0 (8 x 16 B)  P half 1 of t + 1   P0 Q0
+//   1       Q half 1 (4)         Q half 0 of t + 2   P0 Q1
+//   2       P half 1 (8)         P half 0 of t + 2   P1 Q1
+//   3       Q half 0 of t + 1    Q half 1 of t + 2   P1 Q0
+// A half (128 rows x 64 k, 16 KB) is refilled two phases after it was read, which is the first
+// point where both groups' reads are known to be done, and a load has five phases to land: the
+// waits are for all but the 10 newest of a wave's loads and never empty the queue before the tile's
+// last steps. Eight halves, each an LDS object of its own (so that the compiler can tell the reads
+// of one from the loads into another), 128 KB.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include "internal.h"
+#include "mfma_device.h"
+#include "nf4_device.h"
+
+namespace qn {
+
+constexpr int kTurnTile = 256, kTurnK = 64, kTurnThreads = 512;
+
+struct TurnArgs {
+    const uint16_t* P; int64_t ldp;
+    const uint16_t* Q; int64_t ldq;
+    const uint16_t* P2; int64_t ldp2;
+    const uint16_t* Q2; int64_t ldq2;
+    uint32_t bytesP, bytesQ, bytesP2, bytesQ2;      // extents for the load descriptors
+    int kt1, kt2;                                   // K-steps of P Q^T, and of P2 Q2^T
+};
+
+// rowsP, rowsQ: rows of the operands (their extents: every operand is below 4 GiB)
+inline TurnArgs turn_args(const uint16_t* P, int64_t ldp, int64_t rowsP, const uint16_t* Q, int64_t ldq, int64_t rowsQ,
+                          int64_t K) {
+    TurnArgs g{};
+    g.P = P; g.ldp = ldp; g.Q = Q; g.ldq = ldq;
+    g.bytesP = static_cast<uint32_t>(2 * ldp * rowsP);
+    g.bytesQ = static_cast<uint32_t>(2 * ldq * rowsQ);
+    g.kt1 = static_cast<int>(K / kTurnK);
+    return g;
+}
+
+namespace {
+
+typedef float f32x4t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) void* turn_lds_t;
+
+// halves: stage, operand, rows 0..127 or 128..255 of the tile
+__shared__ uint4 g_p00[1024], g_p01[1024], g_q00[1024], g_q01[1024];
+__shared__ uint4 g_p10[1024], g_p11[1024], g_q10[1024], g_q11[1024];
+
+// The sums of a wave: acc[h][g][i][j], lane l, is C[m][n .. n + 3] with m = 128 h + 64 wm + 16 i +
+// l % 16 and n = 128 g + 32 wn + 16 j + 4 (l / 16), wm = wave / 4, wn = wave % 4.
+typedef f32x4t TurnSums[2][2][4][2];
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t turn_rsrc(const void* base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0), static_cast<int>(bytes),
+                                             0x00020000);
+}
+
+// A barrier that keeps memory accesses (clobber) and MFMAs (sched_barrier) on their side and
+// waits for no load; LDS reads in flight are waited for where their values are used.
+#define QN_TURN()                                  \
+    {                                              \
+        __builtin_amdgcn_sched_barrier(0);         \
+        asm volatile("s_barrier" ::: "memory");    \
+        __builtin_amdgcn_sched_barrier(0);         \
+    }
+
+#define QN_WAIT_LDS() __builtin_amdgcn_s_waitcnt(0xC07F)      // lgkmcnt(0), no other counter
+
+// acc = the K-steps [kb, ke) of P Q^T, then (kRank and rank) the g.kt2 steps of P2 Q2^T; at least
+// one step in all. rowP(r), rowQ(r): the row of P and P2 (Q and Q2) that tile row r takes (uint32,
+// inside the operand). On return every wave has finished its reads of LDS and no load is in flight.
+template <bool kRank, class RowP, class RowQ>
+__device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, const RowQ& rowQ, int kb, int ke, bool rank,
+                                           TurnSums& acc) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave >> 2, wn = wave & 3;
+
+    // A half's row is 64 bf16 = 128 B = 8 chunks of 16 B; chunk c of row r is stored at c ^ ((r >> 1) & 7):
+    // two rows cover the 64 banks once, and 16 lanes reading one chunk of 16 rows hit 16 distinct 4-bank
+    // groups. A load instruction fills 8 rows; wave w fills rows 16 w .. 16 w + 15 of every half, lane i
+    // the chunk that belongs at position i % 8 of row i / 8.
+    uint32_t voP[2][2], voQ[2][2];                  // half, instruction
+    __amdgpu_buffer_rsrc_t rsP, rsQ;
+    auto places = [&](int64_t ldp, int64_t ldq) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int r = 128 * h + 16 * wave + 8 * j + (lane >> 3);
+                const uint32_t chunk = static_cast<uint32_t>((lane & 7) ^ (4 * j + (lane >> 4))) * 16u;
+                voP[h][j] = rowP(r) * static_cast<uint32_t>(ldp * 2) + chunk;
+                voQ[h][j] = rowQ(r) * static_cast<uint32_t>(ldq * 2) + chunk;
+            }
+    };
+    places(g.ldp, g.ldq);
+    const int kmain = ke - kb;
+    const int KT = kmain + (kRank && rank ? g.kt2 : 0);
+    // Loads are issued for two steps past the last as well, so that the loop has no branch around a
+    // load (with one the compiler emptied the load queue before the LDS reads); their descriptors have
+    // no extent, so nothing is fetched.
+    int next = 0;                                   // the step whose loads are issued
+    int so = kb * (kTurnK * 2);                     // its byte offset in a row
+    auto enter = [&]() {                            // before the first load of step `next`
+        if (kRank && next == kmain) {
+            places(g.ldp2, g.ldq2);
+            so = 0;
+        }
+        const bool first = !kRank || next < kmain, none = next >= KT;
+        rsP = turn_rsrc(first ? g.P : g.P2, none ? 0u : first ? g.bytesP : g.bytesP2);
+        rsQ = turn_rsrc(first ? g.Q : g.Q2, none ? 0u : first ? g.bytesQ : g.bytesQ2);
+    };
+    auto leave = [&]() { ++next; so += kTurnK * 2; };
+#define QN_LOAD(OBJ, RS, VO)                                                                                             \
+    {                                                                                                                    \
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(RS, (turn_lds_t)((OBJ) + wave * 128), 16, (VO)[0], so, 0, 0);           \
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(RS, (turn_lds_t)((OBJ) + wave * 128 + 64), 16, (VO)[1], so, 0, 0);      \
+    }
+
+    // fragments: lane l has row l % 16, k 8 (l / 16) .. + 7 of each 32
+    const int fr = lane & 15;
+    const uint32_t c0 = static_cast<uint32_t>((lane >> 4) ^ ((fr >> 1) & 7)), c1 = c0 ^ 4u;    // chunks of k 0..31 and 32..63
+    const uint32_t prow = static_cast<uint32_t>(64 * wm + fr) * 8, qrow = static_cast<uint32_t>(32 * wn + fr) * 8;
+    uint4 a[4][2], bx[2][2], by[2][2];
+#define QN_READ_P(OBJ)                                                                  \
+    _Pragma("unroll") for (int k = 0; k < 2; ++k)                                       \
+        _Pragma("unroll") for (int i = 0; i < 4; ++i) a[i][k] = (OBJ)[prow + 128 * i + (k ? c1 : c0)];
+#define QN_READ_Q(OBJ, B)                                                               \
+    _Pragma("unroll") for (int k = 0; k < 2; ++k)                                       \
+        _Pragma("unroll") for (int j = 0; j < 2; ++j) B[j][k] = (OBJ)[qrow + 128 * j + (k ? c1 : c0)];
+#define QN_MULTIPLY(H, G, B)                                                            \
+    {                                                                                   \
+        __builtin_amdgcn_s_setprio(1);                                                  \
+        _Pragma("unroll") for (int k = 0; k < 2; ++k)                                   \
+            _Pragma("unroll") for (int i = 0; i < 4; ++i)                               \
+                _Pragma("unroll") for (int j = 0; j < 2; ++j)                           \
+                    acc[H][G][i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(          \
+                        __builtin_bit_cast(bf16x8, B[j][k]), __builtin_bit_cast(bf16x8, a[i][k]), acc[H][G][i][j], 0, 0, 0); \
+        __builtin_amdgcn_s_setprio(0);                                                  \
+    }
+    // One K-step on stage (P0, P1, Q0, Q1), NP1 and NQ0 halves of the other stage; B1st has Q half 0,
+    // B2nd is for the other half.
+#define QN_STEP(P0, P1, Q0, Q1, NP1, NQ0, B1st, B2nd)                                   \
+    {                                                                                   \
+        QN_READ_P(P0)                                                                   \
+        QN_LOAD(NP1, rsP, voP[1])                                                       \
+        leave();                                                                        \
+        QN_WAIT_VM(10);                                                                 \
+        QN_TURN()                                                                       \
+        QN_MULTIPLY(0, 0, B1st)                                                         \
+        QN_TURN()                                                                       \
+        QN_READ_Q(Q1, B2nd)                                                             \
+        enter();                                                                        \
+        QN_LOAD(Q0, rsQ, voQ[0])                                                        \
+        QN_WAIT_VM(10);                                                                 \
+        QN_TURN()                                                                       \
+        QN_MULTIPLY(0, 1, B2nd)                                                         \
+        QN_TURN()                                                                       \
+        QN_READ_P(P1)                                                                   \
+        QN_LOAD(P0, rsP, voP[0])                                                        \
+        QN_WAIT_VM(10);                                                                 \
+        QN_TURN()                                                                       \
+        QN_MULTIPLY(1, 1, B2nd)                                                         \
+        QN_TURN()                                                                       \
+        QN_READ_Q(NQ0, B2nd)                                                            \
+        QN_LOAD(Q1, rsQ, voQ[1])                                                        \
+        QN_WAIT_VM(10);                                                                 \
+        QN_TURN()                                                                       \
+        QN_MULTIPLY(1, 0, B1st)                                                         \
+        QN_WAIT_LDS();  /* B2nd, two phases before its half is refilled */              \
+        QN_TURN()                                                                       \
+    }
+
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[h][q][i][j] = f32x4t{0.0f, 0.0f, 0.0f, 0.0f};
+
+    enter();
+    QN_LOAD(g_q00, rsQ, voQ[0])
+    QN_LOAD(g_p00, rsP, voP[0])
+    QN_LOAD(g_q01, rsQ, voQ[1])
+    QN_LOAD(g_p01, rsP, voP[1])
+    leave();
+    enter();
+    QN_LOAD(g_q10, rsQ, voQ[0])
+    QN_LOAD(g_p10, rsP, voP[0])
+    QN_LOAD(g_q11, rsQ, voQ[1])
+    QN_WAIT_VM(10);
+    QN_TURN()
+    QN_READ_Q(g_q00, bx)
+    if (wm == 1) QN_TURN()                          // the second group starts one turn later
+    for (int left = KT;;) {
+        QN_STEP(g_p00, g_p01, g_q00, g_q01, g_p11, g_q10, bx, by)
+        if (--left == 0) break;
+        QN_STEP(g_p10, g_p11, g_q10, g_q11, g_p01, g_q00, by, bx)
+        if (--left == 0) break;
+    }
+    if (wm == 0) QN_TURN()
+    QN_WAIT_VM(0);                                  // the loads past the last step
+    QN_TURN()
+#undef QN_STEP
+#undef QN_MULTIPLY
+#undef QN_READ_Q
+#undef QN_READ_P
+#undef QN_LOAD
+}
+
+// ---- epilogue: a bf16 tile through LDS, so that it leaves in whole rows ----
+typedef uint32_t u32x2t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char* turn_bytes_t;
+
+// object `index` (0..7; a constant after unrolling, or uniform)
+__device__ __forceinline__ turn_bytes_t turn_object(int index) {
+    const turn_bytes_t lo = index & 2 ? (index & 1 ? (turn_bytes_t)g_q01 : (turn_bytes_t)g_q00)
+                                      : (index & 1 ? (turn_bytes_t)g_p01 : (turn_bytes_t)g_p00);
+    const turn_bytes_t hi = index & 2 ? (index & 1 ? (turn_bytes_t)g_q11 : (turn_bytes_t)g_q10)
+                                      : (index & 1 ? (turn_bytes_t)g_p11 : (turn_bytes_t)g_p10);
+    return index & 4 ? hi : lo;
+}
+
+// 4 neighbouring columns of a row: of a 256-column tile (32 rows of 512 B per object, 16-byte chunk j
+// of row r at j ^ (r & 31)) or of a 128-column one (64 rows of 256 B, j ^ (r & 15)). The rows are
+// 16 per wave instruction, so 16 distinct 4-bank groups.
+template <int kCols>
+__device__ __forceinline__ void turn_put(int row, int col, float a, float b, float c, float d) {
+    constexpr int kRows = 8192 / kCols;
+    const int uniform = __builtin_amdgcn_readfirstlane(row / kRows);
+    *(__attribute__((address_space(3))) u32x2t*)(turn_object(uniform) + (row % kRows) * (2 * kCols) +
+                                                (((col >> 3) ^ (row & (kCols / 8 - 1))) << 4) + ((col & 7) << 1)) =
+        u32x2t{pack_bf16x2(a, b), pack_bf16x2(c, d)};
+}
+
+// chunk (8 columns) c of row `row`; the rows of a wave lie in one object
+template <int kCols>
+__device__ __forceinline__ uint4 turn_get(int row, int c) {
+    constexpr int kRows = 8192 / kCols;
+    const int uniform = __builtin_amdgcn_readfirstlane(row / kRows);
+    const u32x4t v = *(__attribute__((address_space(3))) u32x4t*)(turn_object(uniform) + (row % kRows) * (2 * kCols) +
+                                                                 ((c ^ (row & (kCols / 8 - 1))) << 4));
+    return uint4{v.x, v.y, v.z, v.w};
+}
+
+// ---- places of the tiles ----
+// Workgroup -> one of n items, contiguous ranges per XCD (workgroups go to the 8 XCDs in turn), so
+// that each XCD's L2 sees neighbouring tiles; -1: none. The grid is at least 8 ceil(n / 8).
+__device__ __forceinline__ int turn_item(int bid, int n) {
+    const int x = bid & 7, i = bid >> 3;
+    const int q = n >> 3, rest = n & 7;
+    return i < q + (x < rest ? 1 : 0) ? x * q + min(x, rest) + i : -1;
+}
+
+// item -> (tile row, tile column): groups of 4 tile rows, column by column
+__device__ __forceinline__ void turn_tile(int item, int tiles_m, int tiles_n, int& tm, int& tn) {
+    const int size = 4 * tiles_n;
+    const int first = item / size * 4;
+    const int rows = min(tiles_m - first, 4);
+    tm = first + item % size % rows;
+    tn = item % size / rows;
+}
+
+}  // namespace
+
+// The K-steps of the last round of tiles split over several workgroups each where it would leave
+// most CUs idle: of T tiles the first full run whole, the K-steps of the rem others in `splits`
+// shares of kper whose float32 sums (256 x 256 a piece, share s of tile j at s rem + j) a second
+// kernel adds. Shares have 8 K-steps or more.
+struct TurnSplit { int tiles_m, tiles_n, splits, full, rem, kper; };
+inline TurnSplit turn_split(int64_t M, int64_t tiles_n, int64_t kt) {
+    TurnSplit s{};
+    s.tiles_m = static_cast<int>((M + kTurnTile - 1) / kTurnTile);
+    s.tiles_n = static_cast<int>(tiles_n);
+    const int T = s.tiles_m * s.tiles_n, rem = T % 256;
+    int want = rem == 0 || rem > 128 ? 1 : 256 / rem;
+    if (want > 4) want = 4;
+    if (want > kt / 8) want = static_cast<int>(kt / 8);
+    s.splits = want < 2 ? 1 : want;
+    s.full = s.splits > 1 ? T - rem : T;
+    s.rem = s.splits > 1 ? rem : 0;
+    s.kper = static_cast<int>((kt + s.splits - 1) / s.splits);
+    return s;
+}
+inline int64_t turn_split_floats(const TurnSplit& s) {
+    return s.splits > 1 ? static_cast<int64_t>(s.splits) * s.rem * kTurnTile * kTurnTile : 0;
+}
+inline unsigned turn_split_grid(const TurnSplit& s) {
+    return static_cast<unsigned>((s.full + 7) / 8 * 8 + s.rem * s.splits);
+}
+
+namespace {
+
+// A workgroup's tile and share (share -1: the whole tile; tile -1: none)
+struct TurnPlace { int tm, tn, tile, share, kb, ke; };
+__device__ __forceinline__ TurnPlace turn_place(const TurnSplit& s, int bid, int kt) {
+    TurnPlace p;
+    const int whole = (s.full + 7) / 8 * 8;
+    int item;
+    if (bid < whole) {
+        item = turn_item(bid, s.full);
+        p.tile = item;
+        p.share = -1;
+        p.kb = 0;
+        p.ke = kt;
+    } else {
+        p.tile = (bid - whole) % s.rem;
+        item = s.full + p.tile;
+        p.share = (bid - whole) / s.rem;
+        p.kb = p.share * s.kper;
+        p.ke = min(p.kb + s.kper, kt);
+    }
+    if (item >= 0) turn_tile(item, s.tiles_m, s.tiles_n, p.tm, p.tn);
+    return p;
+}
+
+// A share's sums to its 256 x 256 float32 piece
+__device__ __forceinline__ void turn_put_sums(float* piece, const TurnSums& acc, bool add) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    float* at = piece + (64 * (wave >> 2) + (lane & 15)) * kTurnTile + 32 * (wave & 3) + 4 * (lane >> 4);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    f32x4t* p = reinterpret_cast<f32x4t*>(at + (128 * h + 16 * i) * kTurnTile + 128 * q + 16 * j);
+                    *p = add ? *p + acc[h][q][i][j] : acc[h][q][i][j];
+                }
+}
+
+}  // namespace
+}  // namespace qn

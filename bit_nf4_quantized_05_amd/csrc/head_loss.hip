@@ -24,7 +24,7 @@
 #include <hip/hip_runtime.h>
 
 #include "gated.h"
-#include "gemm_core.h"
+#include "gemm_turns.h"
 #include "head_loss.h"
 #include "nf4_device.h"
 
@@ -33,8 +33,7 @@
 namespace qn {
 namespace {
 
-constexpr int kWM = 2, kWN = 4;
-using Waves = GemmWaves<kWM, kWN>;
+constexpr int BM = kTurnTile, BN = kTurnTile, BK = kTurnK;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 // 2^80 times 2^31 rows stays in float32
 constexpr float kMaxLog2 = 80.0f;
@@ -168,15 +167,8 @@ void head_transpose_kernel(const uint16_t* __restrict__ src, int64_t ldw, int64_
     }
 }
 
-// Workgroup -> one of n items, contiguous ranges per XCD (-1: none)
-__device__ __forceinline__ int xcd_range(int bid, int n) {
-    const int x = bid & 7, i = bid >> 3;
-    const int q = n >> 3, rest = n & 7;
-    return i < q + (x < rest) ? x * q + min(x, rest) + i : -1;
-}
-
 struct HeadTile {
-    int v0, cols;                             // the piece's first row of the head, and its rows
+    int v0, cols, tiles_n;                    // the piece's first row of the head, its rows and tiles
     int64_t T;
     float2* part;                             // [tiles_n][T]: a tile's sum, and the power taken off
     uint16_t* E; int64_t lde;                 // exponentials [T, lde] (gradient)
@@ -184,84 +176,77 @@ struct HeadTile {
 
 // 256 counted tokens x 256 rows of the piece: z in the accumulators, then the exponentials.
 template <bool kGrad>
-__global__ __launch_bounds__(Waves::NT, 1)
-void head_logits_kernel(GemmArgs g, HeadTile h, HeadRows r) {
-    constexpr int TM = Waves::TM, TN = Waves::TN;
+__global__ __launch_bounds__(kTurnThreads, 1)
+void head_logits_kernel(TurnArgs g, HeadTile h, HeadRows r) {
     __shared__ float s_top[4][BM], s_sum[4][BM];
     const int count = r.count[0];
-    g.tiles_m = (count + BM - 1) / BM;
-    const int logical = xcd_range(static_cast<int>(blockIdx.x), g.tiles_m * g.tiles_n);
-    if (logical < 0) return;
-    const int tid = threadIdx.x;
-    const int lane = tid & 63;
-    const int wave = tid >> 6;
-    const int wm = wave / kWN, wn = wave % kWN;
+    const int tiles_m = (count + BM - 1) / BM;
+    const int item = turn_item(static_cast<int>(blockIdx.x), tiles_m * h.tiles_n);
+    if (item < 0) return;
     int tm, tn;
-    tile_coords(g, logical, tm, tn);
+    turn_tile(item, tiles_m, h.tiles_n, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
-    f32x16 acc[TN][TM];
-    gemm_core<kWM, kWN, false>(
+    TurnSums acc;
+    gemm_turns<false>(
         g, [&](int i) { return static_cast<uint32_t>(r.idx[min(m0 + i, count - 1)]); },
         [&](int i) { return static_cast<uint32_t>(min(n0 + i, h.cols - 1)); }, 0, g.kt1, false, acc);
-    // acc -> y = (z - zt) log2 e, -inf at the target and past the piece
-    const int base = wn * 64 + 4 * (lane >> 5);      // tile column of the lane's value (a, gq, e): base + 32 a + 8 gq + e
-    const int ml0 = wm * (TM * 32) + (lane & 31);    // tile row of its b: ml0 + 32 b
+    // acc -> y = (z - zt) log2 e - shift, -inf at the target and past the piece. The lane has rows
+    // 128 hh + 64 wm + 16 i + lane % 16 and of each 16 columns, base + 128 q + 16 j + e.
+    const int tid = threadIdx.x;
+    const int lane = tid & 63, wave = tid >> 6;
+    const int wn = wave & 3;
+    const int row0 = 64 * (wave >> 2) + (lane & 15), base = 32 * wn + 4 * (lane >> 4);
     const bool edge = n0 + BN > h.cols;
-    float top[TM];
-    float sh[TM];
 #pragma unroll
-    for (int b = 0; b < TM; ++b) {
-        const int m = min(m0 + ml0 + 32 * b, count - 1);
-        const float zt = r.zt[m];
-        sh[b] = r.shift[m];
-        const int skip = r.tgt[m] - h.v0 - n0 - base;
-        float t = -__builtin_inff();
+    for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-        for (int a = 0; a < TN; ++a)
+        for (int i = 0; i < 4; ++i) {
+            const int ml = 128 * hh + 16 * i + row0;
+            const int m = min(m0 + ml, count - 1);
+            const float zt = r.zt[m], sh = r.shift[m];
+            const int skip = r.tgt[m] - h.v0 - n0 - base;
+            float t = -__builtin_inff();
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const int off = 32 * a + 8 * (v >> 2) + (v & 3);
-                float y = (acc[a][b][v] - zt) * kLog2e - sh[b];
-                if (off == skip || (edge && n0 + base + off >= h.cols)) y = -__builtin_inff();
-                acc[a][b][v] = y;
-                t = fmaxf(t, y);
-            }
-        top[b] = fmaxf(t, __shfl_xor(t, 32));
-        if (lane < 32) s_top[wn][ml0 + 32 * b] = top[b];
-    }
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int off = 128 * q + 16 * j + e;
+                        float y = (acc[hh][q][i][j][e] - zt) * kLog2e - sh;
+                        if (off == skip || (edge && n0 + base + off >= h.cols)) y = -__builtin_inff();
+                        acc[hh][q][i][j][e] = y;
+                        t = fmaxf(t, y);
+                    }
+            t = fmaxf(t, __shfl_xor(t, 16));
+            t = fmaxf(t, __shfl_xor(t, 32));
+            if (lane < 16) s_top[wn][ml] = t;
+        }
     __syncthreads();
 #pragma unroll
-    for (int b = 0; b < TM; ++b) {
-        const int ml = ml0 + 32 * b;
-        const float t = fmaxf(fmaxf(s_top[0][ml], s_top[1][ml]), fmaxf(s_top[2][ml], s_top[3][ml]));
-        const float off = t > kMaxLog2 ? ceilf(t) : 0.0f;
-        float sum = 0.0f;
+    for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-        for (int a = 0; a < TN; ++a)
+        for (int i = 0; i < 4; ++i) {
+            const int ml = 128 * hh + 16 * i + row0;
+            const float t = fmaxf(fmaxf(s_top[0][ml], s_top[1][ml]), fmaxf(s_top[2][ml], s_top[3][ml]));
+            const float off = t > kMaxLog2 ? ceilf(t) : 0.0f;
+            float sum = 0.0f;
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const float e = __builtin_amdgcn_exp2f(acc[a][b][v] - off);
-                acc[a][b][v] = e;
-                sum += e;
-            }
-        sum += __shfl_xor(sum, 32);
-        if (lane < 32) s_sum[wn][ml] = sum;
-        top[b] = off;
-        if constexpr (kGrad) {
-            // the tile as 256 rows of 512 B, rows 0..127 in the first stage, 16-byte chunk j of
-            // row ml at j ^ (ml & 31)
-            char* rowp = reinterpret_cast<char*>((ml >> 7) ? g_st1 : g_st0) + (ml & 127) * 512;
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int a = 0; a < TN; ++a)
+                for (int j = 0; j < 2; ++j) {
+                    f32x4t v = acc[hh][q][i][j];
 #pragma unroll
-                for (int gq = 0; gq < 4; ++gq) {
-                    const int nl = base + 32 * a + 8 * gq;
-                    *reinterpret_cast<uint2*>(rowp + (((nl >> 3) ^ (ml & 31)) << 4) + ((nl & 7) << 1)) =
-                        uint2{pack_bf16x2(acc[a][b][4 * gq], acc[a][b][4 * gq + 1]),
-                              pack_bf16x2(acc[a][b][4 * gq + 2], acc[a][b][4 * gq + 3])};
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = __builtin_amdgcn_exp2f(v[e] - off);
+                        sum += v[e];
+                    }
+                    if constexpr (kGrad) turn_put<256>(ml, base + 128 * q + 16 * j, v[0], v[1], v[2], v[3]);
                 }
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            if (lane < 16) s_sum[wn][ml] = sum;
         }
-    }
     __syncthreads();
     if (tid < BM && m0 + tid < count) {
         const float t = fmaxf(fmaxf(s_top[0][tid], s_top[1][tid]), fmaxf(s_top[2][tid], s_top[3][tid]));
@@ -269,13 +254,12 @@ void head_logits_kernel(GemmArgs g, HeadTile h, HeadRows r) {
                                              t > kMaxLog2 ? ceilf(t) : 0.0f};
     }
     if constexpr (kGrad) {
-        const int cj = tid & 31;
+        const int c = tid & 31;
 #pragma unroll
-        for (int i = 0; i < BM / (Waves::NT / 32); ++i) {
-            const int row = i * (Waves::NT / 32) + (tid >> 5);
-            const char* arr = reinterpret_cast<const char*>((row >> 7) ? g_st1 : g_st0);
-            const uint4 v = *reinterpret_cast<const uint4*>(arr + (row & 127) * 512 + ((cj ^ (row & 31)) << 4));
-            if (m0 + row < count) *reinterpret_cast<uint4*>(h.E + static_cast<int64_t>(m0 + row) * h.lde + n0 + cj * 8) = v;
+        for (int i = 0; i < 16; ++i) {
+            const int row = 16 * i + (tid >> 5);
+            const uint4 v = turn_get<256>(row, c);
+            if (m0 + row < count) *reinterpret_cast<uint4*>(h.E + static_cast<int64_t>(m0 + row) * h.lde + n0 + c * 8) = v;
         }
     }
 }
@@ -365,47 +349,25 @@ void head_join_kernel(HeadJoin j, HeadRows r) {
 
 // acc += E W of a piece (the first piece: =), 256 x 256 float32 tiles; tile (tm, tn) of split s is
 // slot s tiles + tm tiles_n + tn.
-struct HeadGrad { float* acc; int slots, kt_first, first; };
+struct HeadGrad { float* acc; int tiles_n, slots, kt_first, first; };
 
-__global__ __launch_bounds__(Waves::NT, 1)
-void head_grad_kernel(GemmArgs g, HeadGrad h, HeadRows r) {
-    constexpr int TM = Waves::TM, TN = Waves::TN;
+__global__ __launch_bounds__(kTurnThreads, 1)
+void head_grad_kernel(TurnArgs g, HeadGrad h, int d, HeadRows r) {
     const int count = r.count[0];
-    const HeadSplit s = head_split(count, g.tiles_n, h.slots, h.kt_first, g.kt1);
-    g.tiles_m = (count + BM - 1) / BM;
-    const int logical = xcd_range(static_cast<int>(blockIdx.x), s.tiles * s.splits);
-    if (logical < 0) return;
-    const int sp = logical / s.tiles;
+    const HeadSplit s = head_split(count, h.tiles_n, h.slots, h.kt_first, g.kt1);
+    const int item = turn_item(static_cast<int>(blockIdx.x), s.tiles * s.splits);
+    if (item < 0) return;
+    const int sp = item / s.tiles;
     const int kb = sp * s.kper, ke = min(kb + s.kper, g.kt1);
     if (kb >= ke) return;                            // a later, shorter piece adds nothing here
-    const int tid = threadIdx.x;
-    const int lane = tid & 63;
-    const int wave = tid >> 6;
-    const int wm = wave / kWN, wn = wave % kWN;
     int tm, tn;
-    tile_coords(g, logical % s.tiles, tm, tn);
+    turn_tile(item % s.tiles, (count + BM - 1) / BM, h.tiles_n, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
-    f32x16 acc[TN][TM];
-    gemm_core<kWM, kWN, false>(
+    TurnSums acc;
+    gemm_turns<false>(
         g, [&](int i) { return static_cast<uint32_t>(min(m0 + i, count - 1)); },
-        [&](int i) { return static_cast<uint32_t>(min(n0 + i, g.N - 1)); }, kb, ke, false, acc);
-    float* pt = h.acc + (static_cast<int64_t>(sp) * s.tiles + tm * g.tiles_n + tn) * (BM * BN);
-#pragma unroll
-    for (int b = 0; b < TM; ++b) {
-        const int ml = wm * (TM * 32) + b * 32 + (lane & 31);
-#pragma unroll
-        for (int a = 0; a < TN; ++a)
-#pragma unroll
-            for (int gq = 0; gq < 4; ++gq) {
-                float4* at = reinterpret_cast<float4*>(pt + ml * BN + wn * 64 + a * 32 + 8 * gq + 4 * (lane >> 5));
-                float4 v = float4{acc[a][b][4 * gq], acc[a][b][4 * gq + 1], acc[a][b][4 * gq + 2], acc[a][b][4 * gq + 3]};
-                if (!h.first) {
-                    const float4 o = *at;
-                    v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
-                }
-                *at = v;
-            }
-    }
+        [&](int i) { return static_cast<uint32_t>(min(n0 + i, d - 1)); }, kb, ke, false, acc);
+    turn_put_sums(h.acc + (static_cast<int64_t>(sp) * s.tiles + tm * h.tiles_n + tn) * (BM * BN), acc, !h.first);
 }
 
 // Per token: the loss, and dX from the sums (zeros for a token that is not counted).
@@ -516,21 +478,20 @@ hipError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, char* ws, hipS
                       ldw, cols, WT, p.piece);
         }
         const int tn = static_cast<int>(ceil_div(cols, BN));
-        const GemmArgs g = gemm_args(c.X, c.ldx, W, ldw, c.d, nullptr, 0, nullptr, 0, 0, nullptr, 0, c.T, cols, nullptr);
-        const HeadTile h{static_cast<int>(v0), static_cast<int>(cols), c.T, part, E, p.piece};
+        const TurnArgs g = turn_args(c.X, c.ldx, c.T, W, ldw, cols, c.d);
+        const HeadTile h{static_cast<int>(v0), static_cast<int>(cols), tn, c.T, part, E, p.piece};
         const dim3 lgrid(static_cast<unsigned>(ceil_div(tm * tn, 8) * 8));
-        if (grad) QN_LAUNCH("head_logits_kernel", st, head_logits_kernel<true>, lgrid, dim3(Waves::NT), 0, st, g, h, r);
-        else QN_LAUNCH("head_logits_kernel", st, head_logits_kernel<false>, lgrid, dim3(Waves::NT), 0, st, g, h, r);
+        if (grad) QN_LAUNCH("head_logits_kernel", st, head_logits_kernel<true>, lgrid, dim3(kTurnThreads), 0, st, g, h, r);
+        else QN_LAUNCH("head_logits_kernel", st, head_logits_kernel<false>, lgrid, dim3(kTurnThreads), 0, st, g, h, r);
         const int dn = static_cast<int>(ceil_div(c.d, BN));
         const HeadJoin j{part, tn, c.T, E, p.piece, i > 0 ? acc : nullptr, dn, p.slots, kt_first};
         QN_LAUNCH("head_join_kernel", st, head_join_kernel, dim3(static_cast<unsigned>(ceil_div(c.T, 64))), dim3(256), 0, st,
                   j, r);
         if (grad) {
-            const GemmArgs q = gemm_args(E, p.piece, WT, p.piece, ceil_div(cols, BK) * BK, nullptr, 0, nullptr, 0, 0, nullptr, 0,
-                                         c.T, c.d, nullptr);
-            const HeadGrad hg{acc, p.slots, kt_first, i == 0};
+            const TurnArgs q = turn_args(E, p.piece, c.T, WT, p.piece, c.d, ceil_div(cols, BK) * BK);
+            const HeadGrad hg{acc, dn, p.slots, kt_first, i == 0};
             QN_LAUNCH("head_grad_kernel", st, head_grad_kernel, dim3(static_cast<unsigned>(ceil_div(p.slots, 8) * 8)),
-                      dim3(Waves::NT), 0, st, q, hg, r);
+                      dim3(kTurnThreads), 0, st, q, hg, static_cast<int>(c.d), r);
         }
         e = hipGetLastError();
     }

@@ -46,14 +46,13 @@ struct PreJob {
     int n;                           // workgroups of this job
 };
 
-// One double dequantisation: W_hat row-major [d_out, d_in], rows of it at their place in a
-// pair of weights (see dequant_rows_job), or W_hat^T [d_in, d_out] with row stride ldw.
+// One double dequantisation: W_hat row-major [d_out, d_in], or W_hat^T [d_in, d_out] with row
+// stride ldw.
 struct DeqJob {
     const uint8_t* codes; BlockConsts bc;
     int64_t d_out, d_in;
     int transposed;                 // dequant to W_hat^T instead of W_hat
     uint16_t* what; int64_t ldw;
-    int paired;                     // row-major: rows of one of two weights, 32 and 32 in turn
     int trans_tiles;                // 64 x 64 tiles per transposed-dequant workgroup (1..4)
     int n;                          // workgroups
 };
@@ -312,9 +311,7 @@ __device__ __forceinline__ void adapt_job(const PrologueArgs& a, int b) {
 // Row-major dequantisation of kDeqPerWG = 8192 weights (128 blocks): threads 0..127
 // form a_hat of one block each into LDS (the constants are loaded once per block,
 // not per weight); thread t takes the 8-weight code words t + 256 q (q = 0..3), so
-// every load and 16-byte store of a wave is contiguous. Of a paired weight, row o goes to
-// row 64 (o / 32) + o % 32 of what: its 32-row runs alternate with the other weight's (whose
-// what starts 32 rows later), so that a 64-wide tile of their product has both for 32 outputs.
+// every load and 16-byte store of a wave is contiguous.
 __device__ __forceinline__ void dequant_rows_job(const DeqJob& a, int b, const float* s_code,
                                                  float* s_ahat) {
     constexpr int kWords = kDeqPerWG / 8 / 256;  // code words per thread
@@ -340,12 +337,7 @@ __device__ __forceinline__ void dequant_rows_job(const DeqJob& a, int b, const f
         float w[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[e] = s_code[(cw[q] >> (4 * e)) & 0xFu] * ahat;
-        int64_t at = e0;
-        if (a.paired) {
-            const uint32_t o = static_cast<uint32_t>(e0) / static_cast<uint32_t>(a.d_in);   // n < 2^31
-            at = e0 + static_cast<int64_t>(o & ~31u) * a.d_in;
-        }
-        *reinterpret_cast<uint4*>(a.what + at) = uint4{pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]),
+        *reinterpret_cast<uint4*>(a.what + e0) = uint4{pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]),
                                                       pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7])};
     }
 }
@@ -462,8 +454,8 @@ struct GatedPrologueArgs {
     int k2, backward, n_adapt, n_grad;
 };
 
-// 8 entries of a row of the adapter layout: forward, row 64 k + 32 w + i is row 32 k + i of
-// projection w; gradient, row i is column i of both A.
+// 8 entries of a row of the adapter layout: forward, the gate's d_ff rows, then the up
+// projection's; gradient, row i is column i of both A.
 __device__ __forceinline__ void gated_adapt_job(const GatedPrologueArgs& a, int b) {
     const int cpr = a.k2 / 8, r = a.p.r, pad = a.p.r_pad;
     const int64_t c = static_cast<int64_t>(b) * 256 + threadIdx.x;
@@ -472,9 +464,10 @@ __device__ __forceinline__ void gated_adapt_job(const GatedPrologueArgs& a, int 
     const int j0 = static_cast<int>(c % cpr) * 8;
     const int w = j0 >= pad ? 1 : 0, q0 = j0 - w * pad;      // pad % 8 == 0: a chunk is of one projection
     uint32_t v[4] = {0u, 0u, 0u, 0u};
-    if (a.backward || static_cast<int>(i >> 5 & 1) == w) {
+    const int64_t d_ff = a.arows / 2;                        // forward
+    if (a.backward || (i >= d_ff) == (w == 1)) {
         const uint16_t* src = a.asrc[w];
-        const int64_t row = a.backward ? i : (i >> 6) * 32 + (i & 31);
+        const int64_t row = a.backward ? i : i - w * d_ff;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             if (q0 + e < r) {
@@ -1045,8 +1038,7 @@ hipError_t launch_gated_prologue(const GatedCall& c, bool backward, const GatedP
                 d = make_dequant(c.codes[w], c.bc[w], c.d_ff, c.d_in, true, o.what + w * c.d_ff);
                 d.ldw = 2 * c.d_ff;
             } else {
-                d = make_dequant(c.codes[w], c.bc[w], c.d_ff, c.d_in, false, o.what + w * 32 * c.d_in);
-                d.paired = 1;
+                d = make_dequant(c.codes[w], c.bc[w], c.d_ff, c.d_in, false, o.what + w * c.d_ff * c.d_in);
             }
             a.asrc[w] = backward ? c.A[w] : c.B[w];
         }
