@@ -1,8 +1,8 @@
 // extern "C" entry points of libqlora_nf4: argument checks, workspace layout and
 // kernel sequencing. Every step of the layer runs in the kernels of quantize.hip,
 // prologue.hip, gemm_nt.hip, gemv.hip, skinny.hip, lora_grads.hip, factors.hip,
-// multi_plan.hip, multi_small.hip, gemm_multi.hip, multi_grads.hip, adamw.hip, gated.hip and
-// head_loss.hip; this file does no arithmetic on the data.
+// multi_plan.hip, multi_small.hip, gemm_multi.hip, multi_grads.hip, adamw.hip, gated.hip,
+// gated_small.hip and head_loss.hip; this file does no arithmetic on the data.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -316,6 +316,11 @@ GatedWs gated_ws(int64_t d_ff, int64_t d_in, int64_t d_seq, int r, bool bwd) {
         off += align_up(bytes, 256);
         return at;
     };
+    if (!bwd && d_seq <= qn::kGatedSmall) {                                          // the codes streamed: sums only
+        w.part = take(4 * qn::gated_small_part_floats(d_seq, d_ff, d_in, r));
+        w.bytes = off;
+        return w;
+    }
     w.what = take(4 * d_ff * d_in);                                                  // both weights
     w.t = take(2 * d_seq * qn::gated_k2(r));                                         // both rank products
     w.adapt = take(2 * (bwd ? d_in : 2 * d_ff) * qn::gated_k2(r));                   // both adapters
@@ -1076,6 +1081,10 @@ int qlora_gated_fwd(const uint8_t* codes_g, const int8_t* qconst_g, const float*
     if (int rc = check_workspace(workspace, workspace_bytes, w.bytes)) return rc;
     char* ws = static_cast<char*>(workspace);
     hipStream_t st = static_cast<hipStream_t>(stream);
+    if (d_seq <= qn::kGatedSmall) {
+        const hipError_t es = qn::launch_gated_small(c, X, ldx, H, ldh, GU, ldgu, reinterpret_cast<float*>(ws + w.part), st);
+        return es == hipSuccess ? 0 : hip_fail(es, "qlora_gated_fwd (small batch)");
+    }
     qn::GatedProlog o{};
     o.what = reinterpret_cast<uint16_t*>(ws + w.what);
     o.adapt = reinterpret_cast<uint16_t*>(ws + w.adapt);

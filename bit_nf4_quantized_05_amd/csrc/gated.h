@@ -139,4 +139,11 @@ int64_t gated_dx_part_floats(int64_t M, int64_t d_ff, int64_t d_in);
 hipError_t launch_gated_dx(const GatedCall& c, const uint16_t* dGU, int64_t lddgu, const uint16_t* what, const uint16_t* t,
                            const uint16_t* adapt, uint16_t* dX, int64_t lddx, float* part, hipStream_t st);
 
+// ---- gated_small.hip ----
+// The forward on up to kGatedSmall tokens; part holds gated_small_part_floats floats.
+constexpr int kGatedSmall = 64;
+int64_t gated_small_part_floats(int64_t M, int64_t d_ff, int64_t d_in, int r);
+hipError_t launch_gated_small(const GatedCall& c, const uint16_t* X, int64_t ldx, uint16_t* H, int64_t ldh, uint16_t* GU,
+                              int64_t ldgu, float* part, hipStream_t st);
+
 }  // namespace qn
