@@ -5,6 +5,7 @@
 #include <hip/hip_runtime.h>
 
 #include "internal.h"
+#include "mfma_device.h"
 #include "nf4_device.h"
 
 namespace qn {
@@ -100,8 +101,8 @@ __device__ __forceinline__ void gated_grad_job(const GatedGradArgs& a, int b) {
                 dg[e] = hv * uv * slope;
                 du[e] = hv * act;
             }
-            og[q] = pack_bf16x2(dg[0], dg[1]);
-            ou[q] = pack_bf16x2(du[0], du[1]);
+            og[q] = bf16_pair(dg[0], dg[1]);
+            ou[q] = bf16_pair(du[0], du[1]);
         }
         uint16_t* out = a.dGU + row[k] * a.lddgu + col[k];
         *reinterpret_cast<uint4*>(out) = uint4{og[0], og[1], og[2], og[3]};

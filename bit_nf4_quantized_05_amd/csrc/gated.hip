@@ -125,13 +125,13 @@ void gated_split_reduce(TurnSplit s, GatedOut o) {
 #pragma unroll
         for (int w = 0; w < 2; ++w)
             *reinterpret_cast<uint2*>(o.GU + static_cast<int64_t>(m) * o.ldgu + w * o.d_ff + n) =
-                uint2{pack_bf16x2(t[w][0], t[w][1]), pack_bf16x2(t[w][2], t[w][3])};
+                uint2{bf16_pair(t[w][0], t[w][1]), bf16_pair(t[w][2], t[w][3])};
     }
     float h[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) h[e] = gated_act(o.act, t[0][e]) * t[1][e];
     *reinterpret_cast<uint2*>(o.H + static_cast<int64_t>(m) * o.ldh + n) =
-        uint2{pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])};
+        uint2{bf16_pair(h[0], h[1]), bf16_pair(h[2], h[3])};
 }
 
 // dX = dGU [W_g; W_u] + U' A: a plain product, bf16 out
@@ -191,7 +191,7 @@ void gated_dx_reduce(TurnSplit s, GatedDx o) {
     f32x4t t = v[0];
 #pragma unroll
     for (int k = 1; k < SP; ++k) t = t + v[k];
-    *reinterpret_cast<uint2*>(o.C + static_cast<int64_t>(m) * o.ldc + n) = uint2{pack_bf16x2(t[0], t[1]), pack_bf16x2(t[2], t[3])};
+    *reinterpret_cast<uint2*>(o.C + static_cast<int64_t>(m) * o.ldc + n) = uint2{bf16_pair(t[0], t[1]), bf16_pair(t[2], t[3])};
 }
 
 TurnSplit fwd_split(int64_t M, int64_t d_ff, int64_t d_in) {

@@ -245,7 +245,7 @@ __device__ __forceinline__ void turn_put(int row, int col, float a, float b, flo
     const int uniform = __builtin_amdgcn_readfirstlane(row / kRows);
     *(__attribute__((address_space(3))) u32x2t*)(turn_object(uniform) + (row % kRows) * (2 * kCols) +
                                                 (((col >> 3) ^ (row & (kCols / 8 - 1))) << 4) + ((col & 7) << 1)) =
-        u32x2t{pack_bf16x2(a, b), pack_bf16x2(c, d)};
+        u32x2t{bf16_pair(a, b), bf16_pair(c, d)};
 }
 
 // chunk (8 columns) c of row `row`; the rows of a wave lie in one object

@@ -117,7 +117,7 @@ void head_target_kernel(HeadCall c, HeadRows r, uint16_t* wt, NF4Tables tab) {
             float w[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) w[q] = s_code[(word >> (4 * q)) & 0xFu] * a;
-            wv = uint4{pack_bf16x2(w[0], w[1]), pack_bf16x2(w[2], w[3]), pack_bf16x2(w[4], w[5]), pack_bf16x2(w[6], w[7])};
+            wv = uint4{bf16_pair(w[0], w[1]), bf16_pair(w[2], w[3]), bf16_pair(w[4], w[5]), bf16_pair(w[6], w[7])};
             if (wt != nullptr) *reinterpret_cast<uint4*>(wt + m * c.d + k) = wv;
         }
         const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, ww[4] = {wv.x, wv.y, wv.z, wv.w};
@@ -403,8 +403,8 @@ void head_final_kernel(HeadCall c, HeadFinal f, HeadRows r) {
                 const float* at = f.acc + static_cast<int64_t>((m / BM) * f.tiles_n + n / BN) * (BM * BN) + (m % BM) * BN + n % BN;
                 const float4 a = ordered_sum4<4>(at, static_cast<int64_t>(s.tiles) * (BM * BN), s.splits);
                 const uint2 wv = *reinterpret_cast<const uint2*>(w + n);
-                o.x = pack_bf16x2(k * (a.x - l * __uint_as_float(wv.x << 16)), k * (a.y - l * __uint_as_float(wv.x & 0xFFFF0000u)));
-                o.y = pack_bf16x2(k * (a.z - l * __uint_as_float(wv.y << 16)), k * (a.w - l * __uint_as_float(wv.y & 0xFFFF0000u)));
+                o.x = bf16_pair(k * (a.x - l * __uint_as_float(wv.x << 16)), k * (a.y - l * __uint_as_float(wv.x & 0xFFFF0000u)));
+                o.y = bf16_pair(k * (a.z - l * __uint_as_float(wv.y << 16)), k * (a.w - l * __uint_as_float(wv.y & 0xFFFF0000u)));
             }
             *reinterpret_cast<uint2*>(out + n) = o;
         }

@@ -22,7 +22,10 @@ F, B8, ACT = 2.0 ** -24, 2.0 ** -8, 100 * 2.0 ** -22
 CASES = [(64, 64, 1, 1, "silu", "int8"), (64, 128, 3, 0, "gelu", "int8"), (128, 320, 17, 9, "silu", "fp8"),
          (512, 256, 203, 8, "gelu", "int8"), (192, 1088, 65, 33, "silu", "none"), (64, 4096, 64, 16, "gelu", "int8"),
          (704, 1024, 300, 64, "silu", "int8"), (320, 4096, 130, 16, "gelu", "fp8"), (4160, 128, 1025, 100, "silu", "int8"),
-         (2752, 512, 1, 16, "silu", "none"), (1088, 2112, 24, 256, "gelu", "int8"), (128, 64, 257, 24, "silu", "int8")]
+         (2752, 512, 1, 16, "silu", "none"), (1088, 2112, 24, 256, "gelu", "int8"), (128, 64, 257, 24, "silu", "int8"),
+         (1024, 4032, 7, 16, "silu", "int8"), (192, 3968, 16, 5, "gelu", "none"), (9152, 64, 2, 11, "silu", "fp8"),
+         (64, 4160, 4, 16, "gelu", "int8"), (640, 640, 9, 17, "silu", "int8"), (128, 2048, 33, 16, "silu", "int8"),
+         (66624, 64, 3, 16, "silu", "int8")]
 IDS = ["x".join(map(str, c)) for c in CASES]
 
 
