@@ -1,7 +1,7 @@
 // The gated block on 1 to 64 tokens (decode batches) on gfx950: both weights' codes are streamed
 // once and dequantised in registers straight into MFMA operands; no bf16 copy is made.
 //
-// gated_small_kernel: the rows of W_g, W_u, A_g and A_u one after the other as tiles of 16; a
+// gated_small_kernel: the rows of A_g, A_u, W_g and W_u one after the other as tiles of 16; a
 // wave multiplies a tile with the tokens over its share of K (v_mfma_f32_16x16x32_bf16, the tile's
 // rows against up to four 16-token tiles). Lane l (row l % 16, group l / 16) takes 16 code bytes =
 // 32 weights of each 128, one 16-byte load, and forms bf16(code * a_hat) exactly as the dequantiser
@@ -36,7 +36,7 @@ struct SmallArgs {
     const uint16_t* A[2];
     const uint16_t* X; int64_t ldx;
     int T, d_ff, d_in, r;
-    int wtiles, tiles;                          // 16-row tiles of both weights, and of everything
+    int atiles, tiles;                          // 16-row tiles of both A (first), and of everything
     int splits, pairs;                          // slices of K, 128-wide pieces per slice
     float* part;                                // [splits][T][16 tiles]
 };
@@ -116,27 +116,21 @@ __device__ __forceinline__ uint4 piece_weights(const Piece& c, int st, float a_h
     return uint4{v[0], v[1], v[2], v[3]};
 }
 
-// How a workgroup's 16 waves share the tiles, by the number TT of 16-token tiles: KW waves a tile
-template <int TT>
-struct SmallShape {
-    static constexpr int KW = TT == 1 ? 16 : TT == 2 ? 2 : 1;
-    // bytes for the tokens' slice beside the tables and the waves' sums
-    static constexpr int kX = (TT == 1 ? 78 : TT == 2 ? 60 : 92) * 1024;
-};
-
-template <int TT>
+// KW of a workgroup's 16 waves share a tile (each a part of its K), TT 16-token tiles
+template <int TT, int KW>
 struct SmallLds {
+    // bytes for the tokens' slice beside the tables and the sums that the waves of a tile hand on
+    static constexpr int kX = (KW == 16 ? 78 : KW == 4 ? 70 : KW == 2 ? 60 : 92) * 1024;
     CodeTables tables;                          // first: their offsets fit an LDS read's 16 bits
-    // the sums that waves of a tile hand on
-    float red[TT == 1 ? 1 : 2][TT == 1 ? 16 : TT == 2 ? 8 : 1][TT == 1 ? 1 : TT == 2 ? 2 : 1][TT <= 2 ? 256 : 1];
-    uint4 x[SmallShape<TT>::kX / 16];           // [token][chunk of 8], chunks XORed with the token
+    float red[KW == 1 || KW == 16 ? 1 : 2][KW == 1 ? 1 : KW == 16 ? 16 : kWaves - kWaves / KW][KW == 1 ? 1 : TT * 256];
+    uint4 x[kX / 16];                           // [token][chunk of 8], chunks XORed with the token
 };
 
-template <int TT>
+template <int TT, int KW>
 __global__ __launch_bounds__(kThreads, 4)
 void gated_small_kernel(SmallArgs a, NF4Tables tab) {
-    constexpr int KW = SmallShape<TT>::KW, kTiles = kWaves / KW;
-    __shared__ SmallLds<TT> lds;
+    constexpr int kTiles = kWaves / KW;
+    __shared__ SmallLds<TT, KW> lds;
     static_assert(sizeof(lds) <= 160 * 1024, "a CU's LDS");
     const int tid = threadIdx.x;
     const int lane = tid & 63;
@@ -152,9 +146,9 @@ void gated_small_kernel(SmallArgs a, NF4Tables tab) {
     // the k-th piece of the wave's group: neighbouring pieces in twos, which are a 128-byte line of codes
     auto piece_at = [&](int group, int k) { return ((group * (kGroupPairs / 2) + (k >> 1)) * KW + kw) * 2 + (k & 1); };
     auto load = [&](Piece (&c)[kGroupPairs], int tile, int group) {
-        const bool live = tile < a.wtiles;
-        const int w = live && tile * 16 >= a.d_ff ? 1 : 0;
-        const uint32_t row = static_cast<uint32_t>(live ? tile * 16 - w * a.d_ff : 0) + i;
+        const bool live = tile >= a.atiles && tile < a.tiles;
+        const int at = live ? (tile - a.atiles) * 16 : 0, w = at >= a.d_ff ? 1 : 0;
+        const uint32_t row = static_cast<uint32_t>(at - w * a.d_ff) + i;
         const PieceSource src = piece_source(a, w, live);
 #pragma unroll
         for (int k = 0; k < kGroupPairs; ++k) {
@@ -163,14 +157,14 @@ void gated_small_kernel(SmallArgs a, NF4Tables tab) {
         }
     };
 
-    // the tokens' slice (before the codes' loads, which it would queue behind), a wave per token at a time
-    for (int t = wave; t < a.T; t += kWaves)
-        for (int c = lane; c < np * 16; c += 64) {
-            const int col = (p0 * 16 + c) * 8;
-            uint4 v = uint4{0, 0, 0, 0};
-            if (col < a.d_in) v = *reinterpret_cast<const uint4*>(a.X + t * a.ldx + col);
-            lds.x[t * chunks + (c ^ (t & 15))] = v;
-        }
+    // the tokens' slice (before the codes' loads, which it would queue behind)
+    for (int e = tid, per = np * 16; e < a.T * per; e += kThreads) {
+        const int t = e / per, c = e - t * per;
+        const int col = (p0 * 16 + c) * 8;
+        uint4 v = uint4{0, 0, 0, 0};
+        if (col < a.d_in) v = *reinterpret_cast<const uint4*>(a.X + t * a.ldx + col);
+        lds.x[t * chunks + (c ^ (t & 15))] = v;
+    }
     // every workgroup's waves make the same number of rounds (they meet at barriers)
     int base = static_cast<int>(blockIdx.x) * kTiles;
     Piece cur[kGroupPairs], nxt[kGroupPairs];
@@ -202,62 +196,78 @@ void gated_small_kernel(SmallArgs a, NF4Tables tab) {
         const int tile = base + tl;
 #pragma unroll
         for (int t = 0; t < TT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (tile < a.wtiles) {
-            const float m = mu[tile * 16 >= a.d_ff ? 1 : 0];
+        if (tile < a.atiles) {
+            // 16 rows of A (past r: the last one again, not read), two pieces' loads at a time
+            const int per = a.atiles / 2, w = tile >= per ? 1 : 0;
+            const uint16_t* row = a.A[w] + static_cast<int64_t>(min((tile - w * per) * 16 + i, a.r - 1)) * a.d_in;
+            for (int p = kw; p < np; p += 2 * KW) {
+                uint4 v[2][4];
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int st = 0; st < 4; ++st) {
+                        const int col = (p0 + min(p + k * KW, np - 1)) * 128 + 32 * g;
+                        v[k][st] = *reinterpret_cast<const uint4*>(row + min(col, a.d_in - 32) + 8 * st);
+                    }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int at = min(p + k * KW, np - 1);
+                    const uint32_t keep = p + k * KW < np && (p0 + at) * 128 + 32 * g < a.d_in ? ~0u : 0u;
+#pragma unroll
+                    for (int st = 0; st < 4; ++st)
+                        multiply(uint4{v[k][st].x & keep, v[k][st].y & keep, v[k][st].z & keep, v[k][st].w & keep}, at, st);
+                }
+            }
+            load(cur, tile + step, 0);
+        } else if (tile < a.tiles) {
+            const float m = mu[(tile - a.atiles) * 16 >= a.d_ff ? 1 : 0];
             for (int grp = 0; grp < groups; ++grp) {
                 // the next group's loads, or the next tile's
                 const bool more = grp + 1 < groups;
                 load(nxt, more ? tile : tile + step, more ? grp + 1 : 0);
 #pragma unroll
-                for (int k = 0; k < kGroupPairs; ++k) {
-                    // past the slice: the last piece again, times zero
-                    const int at = piece_at(grp, k), p = min(at, np - 1);
-                    const uint32_t keep = at < np && 2 * (p0 + p) + (g >> 1) < nb ? ~0u : 0u;
-                    const float ah = piece_constant(cur[k], lds.tables, m, keep);
+                for (int k2 = 0; k2 < kGroupPairs; k2 += 2) {
+                    if (piece_at(grp, k2) >= np) break;                // uniform
 #pragma unroll
-                    for (int st = 0; st < 4; ++st) multiply(piece_weights(cur[k], st, ah, lds.tables, lane8), p, st);
+                    for (int k = k2; k < k2 + 2; ++k) {
+                        // past the slice: the last piece again, times zero
+                        const int at = piece_at(grp, k), p = min(at, np - 1);
+                        const uint32_t keep = at < np && 2 * (p0 + p) + (g >> 1) < nb ? ~0u : 0u;
+                        const float ah = piece_constant(cur[k], lds.tables, m, keep);
+#pragma unroll
+                        for (int st = 0; st < 4; ++st) multiply(piece_weights(cur[k], st, ah, lds.tables, lane8), p, st);
+                    }
                 }
 #pragma unroll
                 for (int k = 0; k < kGroupPairs; ++k) cur[k] = nxt[k];
             }
-        } else if (tile < a.tiles) {
-            // 16 rows of A (past r: the last one again, not read)
-            const int at = tile - a.wtiles, per = (a.r + 15) / 16;
-            const int w = at >= per ? 1 : 0;
-            const uint16_t* row = a.A[w] + static_cast<int64_t>(min((at - w * per) * 16 + i, a.r - 1)) * a.d_in;
-            for (int p = kw; p < np; p += KW) {
-                const int col = (p0 + p) * 128 + 32 * g;
-                const bool ok = col < a.d_in;
-                uint4 v[4];
-#pragma unroll
-                for (int st = 0; st < 4; ++st) v[st] = *reinterpret_cast<const uint4*>(row + min(col, a.d_in - 32) + 8 * st);
-#pragma unroll
-                for (int st = 0; st < 4; ++st) multiply(ok ? v[st] : uint4{0, 0, 0, 0}, p, st);
-            }
         }
         if constexpr (KW == 1) {
             if (tile < a.tiles) store(tile);
-        } else if constexpr (KW == 2) {
-            // the second wave's sums to the first; the next tile's beside these: one barrier a tile
-            if (kw == 1) {
+        } else if constexpr (KW < 16) {
+            // the others' sums to the tile's first wave; the next tile's beside these: one barrier a tile
+            auto slot = [&](int k, int t) { return reinterpret_cast<f32x4*>(&lds.red[parity][tl * (KW - 1) + k - 1][256 * t + 4 * lane]); };
+            if (kw > 0) {
 #pragma unroll
-                for (int t = 0; t < TT; ++t) *reinterpret_cast<f32x4*>(&lds.red[parity][tl][t][4 * lane]) = acc[t];
+                for (int t = 0; t < TT; ++t) *slot(kw, t) = acc[t];
             }
             QN_LDS_BARRIER();
             if (kw == 0 && tile < a.tiles) {
 #pragma unroll
-                for (int t = 0; t < TT; ++t) acc[t] = acc[t] + *reinterpret_cast<const f32x4*>(&lds.red[parity][tl][t][4 * lane]);
+                for (int k = 1; k < KW; ++k)
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) acc[t] = acc[t] + *slot(k, t);
                 store(tile);
             }
             parity ^= 1;
         } else {
             static_assert(TT == 1, "16 waves a tile: one token tile");
-            *reinterpret_cast<f32x4*>(&lds.red[0][wave][0][4 * lane]) = acc[0];
+            *reinterpret_cast<f32x4*>(&lds.red[0][wave][4 * lane]) = acc[0];
             QN_LDS_BARRIER();
             if (tid < 256) {
                 float v = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kWaves; ++w) v += lds.red[0][w][0][tid];
+                for (int w = 0; w < kWaves; ++w) v += lds.red[0][w][tid];
                 const int t = (tid >> 2) & 15, row = 4 * (tid >> 6) + (tid & 3);
                 if (t < a.T)
                     a.part[(static_cast<int64_t>(split) * a.T + t) * (16 * a.tiles) + 16 * tile + row] = v;
@@ -515,7 +525,7 @@ void gated_few_kernel(FewArgs a, NF4Tables tab) {
 // H (and GU) of 64 outputs for all tokens: the slices' sums in order, G += s_g sum_j T_g[j] B_g[., j]
 // with T = the A tiles' sums, in float32, U likewise.
 struct JoinArgs {
-    const float* part; int splits, T, d_ff, r, wtiles, tiles;
+    const float* part; int splits, T, d_ff, r, atiles, tiles;
     const uint16_t* B[2]; float s[2];
     int act;
     uint16_t* H; int64_t ldh;
@@ -539,7 +549,7 @@ void gated_join_kernel(JoinArgs a) {
     for (int w = 0; w < 2; ++w)
 #pragma unroll
         for (int k = 0; k < PT; ++k)
-            v[w][k] = ordered_sum<4>(part + min(q + 4 * k, nt - 1) * pitch + w * a.d_ff + n0 + i, slice, a.splits);
+            v[w][k] = ordered_sum<4>(part + min(q + 4 * k, nt - 1) * pitch + 16 * a.atiles + w * a.d_ff + n0 + i, slice, a.splits);
     for (int j0 = 0; j0 < a.r; j0 += kJoinRanks) {
         const int nj = min(kJoinRanks, a.r - j0);
         if (j0 > 0) __syncthreads();
@@ -549,7 +559,7 @@ void gated_join_kernel(JoinArgs a) {
         }
         for (int e = threadIdx.x; e < 2 * nt * nj; e += 256) {
             const int w = e / (nt * nj), t = e / nj % nt, j = e % nj;
-            s_t[w][t][j] = a.s[w] * ordered_sum<4>(part + t * pitch + 16 * a.wtiles + w * rp + j0 + j, slice, a.splits);
+            s_t[w][t][j] = a.s[w] * ordered_sum<4>(part + t * pitch + w * rp + j0 + j, slice, a.splits);
         }
         __syncthreads();
 #pragma unroll
@@ -573,17 +583,34 @@ void gated_join_kernel(JoinArgs a) {
 }
 
 // Slices of K: as few as fit the LDS with T tokens
-struct SmallPlan { int splits, pairs, wtiles, tiles; };
+// With up to 16 tokens: 16 waves a tile where that leaves each 2 pieces or more (one token on 28672 x
+// 8192 81 us), else 4 (16 tokens there, whose slices have 16 pieces: 276 us with 16 waves a tile)
+struct SmallPlan { int splits, pairs, atiles, tiles, kw; };
 SmallPlan small_plan(int64_t M, int64_t d_ff, int64_t d_in, int r) {
     const int npair = static_cast<int>((d_in / 64 + 1) / 2);
-    const int bytes = M <= 16 ? SmallShape<1>::kX : M <= 32 ? SmallShape<2>::kX : SmallShape<3>::kX;
-    const int most = static_cast<int>(bytes / (256 * M));
+    int most = static_cast<int>(SmallLds<1, 16>::kX / (256 * M));
     SmallPlan s;
-    s.splits = (npair + most - 1) / most;
-    s.pairs = (npair + s.splits - 1) / s.splits;
-    s.splits = (npair + s.pairs - 1) / s.pairs;
-    s.wtiles = static_cast<int>(2 * d_ff / 16);
-    s.tiles = s.wtiles + 2 * ((r + 15) / 16);
+    s.kw = M > 32 ? 1 : M > 16 ? 2 : std::min(npair, most) >= 32 ? 16 : 4;
+    if (s.kw != 16) most = static_cast<int>((s.kw == 4 ? SmallLds<1, 4>::kX : s.kw == 2 ? SmallLds<2, 2>::kX : SmallLds<4, 1>::kX) / (256 * M));
+    s.atiles = 2 * ((r + 15) / 16);
+    s.tiles = s.atiles + static_cast<int>(2 * d_ff / 16);
+    // Of up to 4 times as many slices as must be: the fewest pieces that a wave takes one after the other
+    // (rounds of a workgroup over its tiles), about 0.9 us each, against the sums' way to memory and back.
+    // (17 tokens on 11008 x 4096: 3 slices 46.7 us, 4 35. With 16 waves a tile the barriers count, not
+    // the pieces: as few as must be.)
+    const int least = (npair + most - 1) / most, per = kWaves / s.kw;
+    double best = 0.0;
+    for (int n = least; n <= (s.kw == 16 ? least : std::min(npair, 4 * least)); ++n) {
+        const int pairs = (npair + n - 1) / n, slices = (npair + pairs - 1) / pairs;
+        const int walkers = std::max(1, std::min((s.tiles + per - 1) / per, 256 / slices)) * per;
+        const double us = 0.9 * ((s.tiles + walkers - 1) / walkers) * ((pairs + s.kw - 1) / s.kw) +
+                          static_cast<double>(slices) * static_cast<double>(M) * s.tiles * 128 / 4.0e6;
+        if (n == least || us < best) {
+            best = us;
+            s.splits = slices;
+            s.pairs = pairs;
+        }
+    }
     return s;
 }
 
@@ -632,18 +659,22 @@ hipError_t launch_gated_small(const GatedCall& c, const uint16_t* X, int64_t ldx
     }
     a.X = X; a.ldx = ldx;
     a.T = static_cast<int>(c.M); a.d_ff = static_cast<int>(c.d_ff); a.d_in = static_cast<int>(c.d_in); a.r = c.r;
-    a.wtiles = s.wtiles; a.tiles = s.tiles; a.splits = s.splits; a.pairs = s.pairs; a.part = part;
+    a.atiles = s.atiles; a.tiles = s.tiles; a.splits = s.splits; a.pairs = s.pairs; a.part = part;
     const NF4Tables& tab = tables();
     a.code_bytes = code_bytes; a.q_bytes = q_bytes; a.s_bytes = s_bytes;
     // a workgroup per CU: 256 / splits walk over the tiles of a slice
-    const int per = kWaves / (c.M <= 16 ? SmallShape<1>::KW : c.M <= 32 ? SmallShape<2>::KW : SmallShape<3>::KW);
+    const int per = kWaves / s.kw;
     const dim3 grid(static_cast<unsigned>(std::max(1, std::min((s.tiles + per - 1) / per, 256 / s.splits))),
                     static_cast<unsigned>(s.splits));
-    if (c.M <= 16) QN_LAUNCH("gated_small_kernel", st, gated_small_kernel<1>, grid, dim3(kThreads), 0, st, a, tab);
-    else if (c.M <= 32) QN_LAUNCH("gated_small_kernel", st, gated_small_kernel<2>, grid, dim3(kThreads), 0, st, a, tab);
-    else if (c.M <= 48) QN_LAUNCH("gated_small_kernel", st, gated_small_kernel<3>, grid, dim3(kThreads), 0, st, a, tab);
-    else QN_LAUNCH("gated_small_kernel", st, gated_small_kernel<4>, grid, dim3(kThreads), 0, st, a, tab);
-    j.part = part; j.splits = s.splits; j.T = a.T; j.d_ff = a.d_ff; j.r = c.r; j.wtiles = s.wtiles; j.tiles = s.tiles;
+#define QN_SMALL(TT, KW) \
+    QN_LAUNCH("gated_small_kernel", st, (gated_small_kernel<TT, KW>), grid, dim3(kThreads), 0, st, a, tab)
+    if (s.kw == 16) QN_SMALL(1, 16);
+    else if (s.kw == 4) QN_SMALL(1, 4);
+    else if (s.kw == 2) QN_SMALL(2, 2);
+    else if (c.M <= 48) QN_SMALL(3, 1);
+    else QN_SMALL(4, 1);
+#undef QN_SMALL
+    j.part = part; j.splits = s.splits; j.T = a.T; j.d_ff = a.d_ff; j.r = c.r; j.atiles = s.atiles; j.tiles = s.tiles;
     j.act = c.act; j.H = H; j.ldh = ldh; j.GU = GU; j.ldgu = ldgu;
     const unsigned jx = static_cast<unsigned>(c.d_ff / kJoinRows);
     if (c.M <= 4) QN_LAUNCH("gated_join_kernel", st, gated_join_kernel<1>, dim3(jx, 1), dim3(256), 0, st, j);
