@@ -52,7 +52,6 @@ inline TurnArgs turn_args(const uint16_t* P, int64_t ldp, int64_t rowsP, const u
 namespace {
 
 typedef float f32x4t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) void* turn_lds_t;
 
 // halves: stage, operand, rows 0..127 or 128..255 of the tile
 __shared__ uint4 g_p00[1024], g_p01[1024], g_q00[1024], g_q01[1024];
@@ -62,9 +61,22 @@ __shared__ uint4 g_p10[1024], g_p11[1024], g_q10[1024], g_q11[1024];
 // l % 16 and n = 128 g + 32 wn + 16 j + 4 (l / 16), wm = wave / 4, wn = wave % 4.
 typedef f32x4t TurnSums[2][2][4][2];
 
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t turn_rsrc(const void* base, uint32_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0), static_cast<int>(bytes),
-                                             0x00020000);
+typedef int32_t i32x4t __attribute__((ext_vector_type(4)));
+
+// (base, no stride, extent in bytes, raw): offsets at or past the extent read as zero
+__device__ __forceinline__ i32x4t turn_rsrc(const void* base, uint32_t bytes) {
+    const uint64_t at = reinterpret_cast<uint64_t>(base);
+    return i32x4t{static_cast<int>(at), static_cast<int>(at >> 32) & 0xFFFF, static_cast<int>(bytes), 0x00020000};
+}
+
+// 16 bytes per lane from a buffer at `offset` + `base` to LDS address `to` + 16 lane. The instruction
+// itself, since the compiler's own form made it wait for loads into other halves before some LDS
+// reads (after 2 of the phases a load has); the waits are this file's. It writes no register.
+__device__ __forceinline__ void turn_load(const i32x4t& rsrc, uint32_t to, uint32_t offset, int base) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+                 :
+                 : "s"(to), "v"(offset), "s"(rsrc), "s"(base)
+                 : "memory", "m0");
 }
 
 // A barrier that keeps memory accesses (clobber) and MFMAs (sched_barrier) on their side and
@@ -93,7 +105,7 @@ __device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, 
     // groups. A load instruction fills 8 rows; wave w fills rows 16 w .. 16 w + 15 of every half, lane i
     // the chunk that belongs at position i % 8 of row i / 8.
     uint32_t voP[2][2], voQ[2][2];                  // half, instruction
-    __amdgpu_buffer_rsrc_t rsP, rsQ;
+    i32x4t rsP, rsQ;
     auto places = [&](int64_t ldp, int64_t ldq) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -123,10 +135,11 @@ __device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, 
         rsQ = turn_rsrc(first ? g.Q : g.Q2, none ? 0u : first ? g.bytesQ : g.bytesQ2);
     };
     auto leave = [&]() { ++next; so += kTurnK * 2; };
-#define QN_LOAD(OBJ, RS, VO)                                                                                             \
-    {                                                                                                                    \
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(RS, (turn_lds_t)((OBJ) + wave * 128), 16, (VO)[0], so, 0, 0);           \
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(RS, (turn_lds_t)((OBJ) + wave * 128 + 64), 16, (VO)[1], so, 0, 0);      \
+#define QN_LOAD(OBJ, RS, VO)                                        \
+    {                                                               \
+        const uint32_t to_ = lds_addr(OBJ) + 2048 * wave;           \
+        turn_load(RS, to_, (VO)[0], so);                            \
+        turn_load(RS, to_ + 1024, (VO)[1], so);                     \
     }
 
     // fragments: lane l has row l % 16, k 8 (l / 16) .. + 7 of each 32

@@ -35,8 +35,9 @@ namespace {
 
 constexpr int BM = kTurnTile, BN = kTurnTile, BK = kTurnK;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
-// 2^80 times 2^31 rows stays in float32
-constexpr float kMaxLog2 = 80.0f;
+// a tile's sum past which its rows are looked at one by one, and the power of two that a row's
+// exponentials may reach (2^80 times 2^31 rows stays in float32)
+constexpr float kLargest = 0x1p80f, kMaxLog2 = 80.0f;
 
 // The numbering of the counted tokens and what is known of each (arrays of T)
 struct HeadRows {
@@ -190,46 +191,31 @@ void head_logits_kernel(TurnArgs g, HeadTile h, HeadRows r) {
     gemm_turns<false>(
         g, [&](int i) { return static_cast<uint32_t>(r.idx[min(m0 + i, count - 1)]); },
         [&](int i) { return static_cast<uint32_t>(min(n0 + i, h.cols - 1)); }, 0, g.kt1, false, acc);
-    // acc -> y = (z - zt) log2 e - shift, -inf at the target and past the piece. The lane has rows
-    // 128 hh + 64 wm + 16 i + lane % 16 and of each 16 columns, base + 128 q + 16 j + e.
+    // e = 2^((z - zt) log2 e - shift), 0 at the target and past the piece. The lane has rows 128 hh +
+    // 64 wm + 16 i + lane % 16 and of each 16 columns, base + 128 q + 16 j + e.
     const int tid = threadIdx.x;
     const int lane = tid & 63, wave = tid >> 6;
     const int wn = wave & 3;
     const int row0 = 64 * (wave >> 2) + (lane & 15), base = 32 * wn + 4 * (lane >> 4);
-    const bool edge = n0 + BN > h.cols;
+    const int columns = h.cols - n0 - base;          // of the lane's, those below are in the piece
+    // the tile's columns that stay out of the lane's row: its target's (none: outside 0..255)
+    auto target = [&](int m) { return r.tgt[m] - h.v0 - n0 - base; };
+    auto keep = [&](f32x4t v, int off, int skip, float out) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (off + e == skip || off + e >= columns) v[e] = out;
+        return v;
+    };
 #pragma unroll
     for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int ml = 128 * hh + 16 * i + row0;
             const int m = min(m0 + ml, count - 1);
-            const float zt = r.zt[m], sh = r.shift[m];
-            const int skip = r.tgt[m] - h.v0 - n0 - base;
-            float t = -__builtin_inff();
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int off = 128 * q + 16 * j + e;
-                        float y = (acc[hh][q][i][j][e] - zt) * kLog2e - sh;
-                        if (off == skip || (edge && n0 + base + off >= h.cols)) y = -__builtin_inff();
-                        acc[hh][q][i][j][e] = y;
-                        t = fmaxf(t, y);
-                    }
-            t = fmaxf(t, __shfl_xor(t, 16));
-            t = fmaxf(t, __shfl_xor(t, 32));
-            if (lane < 16) s_top[wn][ml] = t;
-        }
-    __syncthreads();
-#pragma unroll
-    for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int ml = 128 * hh + 16 * i + row0;
-            const float t = fmaxf(fmaxf(s_top[0][ml], s_top[1][ml]), fmaxf(s_top[2][ml], s_top[3][ml]));
-            const float off = t > kMaxLog2 ? ceilf(t) : 0.0f;
+            const float c = -r.zt[m] * kLog2e - r.shift[m];
+            const int skip = target(m);
+            // few groups of 16 rows have a target in the tile, one tile of a piece has an edge
+            const bool some = __any(skip >= 0 && skip < BN) || n0 + BN > h.cols;
             float sum = 0.0f;
 #pragma unroll
             for (int q = 0; q < 2; ++q)
@@ -237,10 +223,9 @@ void head_logits_kernel(TurnArgs g, HeadTile h, HeadRows r) {
                 for (int j = 0; j < 2; ++j) {
                     f32x4t v = acc[hh][q][i][j];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        v[e] = __builtin_amdgcn_exp2f(v[e] - off);
-                        sum += v[e];
-                    }
+                    for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], kLog2e, c));
+                    if (some) v = keep(v, 128 * q + 16 * j, skip, 0.0f);
+                    sum += (v[0] + v[1]) + (v[2] + v[3]);
                     if constexpr (kGrad) turn_put<256>(ml, base + 128 * q + 16 * j, v[0], v[1], v[2], v[3]);
                 }
             sum += __shfl_xor(sum, 16);
@@ -248,11 +233,70 @@ void head_logits_kernel(TurnArgs g, HeadTile h, HeadRows r) {
             if (lane < 16) s_sum[wn][ml] = sum;
         }
     __syncthreads();
+    auto total = [&](int row) { return (s_sum[0][row] + s_sum[1][row]) + (s_sum[2][row] + s_sum[3][row]); };
+    float sum = 0.0f, power = 0.0f;
+    bool large = false;
     if (tid < BM && m0 + tid < count) {
-        const float t = fmaxf(fmaxf(s_top[0][tid], s_top[1][tid]), fmaxf(s_top[2][tid], s_top[3][tid]));
-        h.part[tn * h.T + m0 + tid] = float2{(s_sum[0][tid] + s_sum[1][tid]) + (s_sum[2][tid] + s_sum[3][tid]),
-                                             t > kMaxLog2 ? ceilf(t) : 0.0f};
+        sum = total(tid);
+        large = !(sum <= kLargest);
     }
+    if (__syncthreads_or(large)) {
+        // a row far above its target (or not a number): the tile again, each row less its own power of
+        // two; the other rows' bits are those of above
+        auto relative = [&](f32x4t v, int off, int skip, int m) {
+            const float c = -r.zt[m] * kLog2e - r.shift[m];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(v[e], kLog2e, c);
+            return keep(v, off, skip, -__builtin_inff());
+        };
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int ml = 128 * hh + 16 * i + row0, m = min(m0 + ml, count - 1);
+                float t = -__builtin_inff();
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const f32x4t v = relative(hh == 0 ? acc[0][q][i][j] : acc[1][q][i][j], 128 * q + 16 * j, target(m), m);
+                        t = fmaxf(fmaxf(fmaxf(t, v[0]), fmaxf(v[1], v[2])), v[3]);
+                    }
+                t = fmaxf(t, __shfl_xor(t, 16));
+                t = fmaxf(t, __shfl_xor(t, 32));
+                if (lane < 16) s_top[wn][ml] = t;
+            }
+        __syncthreads();
+        auto off_of = [&](int row) {
+            const float t = fmaxf(fmaxf(s_top[0][row], s_top[1][row]), fmaxf(s_top[2][row], s_top[3][row]));
+            return t > kMaxLog2 ? ceilf(t) : 0.0f;
+        };
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int ml = 128 * hh + 16 * i + row0, m = min(m0 + ml, count - 1);
+                const float off = off_of(ml);
+                float s = 0.0f;
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        f32x4t v = relative(hh == 0 ? acc[0][q][i][j] : acc[1][q][i][j], 128 * q + 16 * j, target(m), m);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_exp2f(v[e] - off);
+                        s += (v[0] + v[1]) + (v[2] + v[3]);
+                        if constexpr (kGrad) turn_put<256>(ml, base + 128 * q + 16 * j, v[0], v[1], v[2], v[3]);
+                    }
+                s += __shfl_xor(s, 16);
+                s += __shfl_xor(s, 32);
+                if (lane < 16) s_sum[wn][ml] = s;
+            }
+        __syncthreads();
+        if (tid < BM) {
+            sum = total(tid);
+            power = off_of(tid);
+        }
+    }
+    if (tid < BM && m0 + tid < count) h.part[tn * h.T + m0 + tid] = float2{sum, power};
     if constexpr (kGrad) {
         const int c = tid & 31;
 #pragma unroll
