@@ -99,7 +99,6 @@ void gated_gemm_kernel(TurnArgs g, TurnSplit s, GatedOut o) {
 
 // Split tiles: G and U summed over the shares in order, then the activation and the product;
 // 4 outputs per thread, 32 workgroups per tile (8 rows each).
-template <int SP>
 __global__ __launch_bounds__(256)
 void gated_split_reduce(TurnSplit s, GatedOut o) {
     const int j = static_cast<int>(blockIdx.x) / 32;
@@ -111,27 +110,15 @@ void gated_split_reduce(TurnSplit s, GatedOut o) {
     if (m >= o.M || n >= o.d_ff) return;
     const float* p = o.part + static_cast<int64_t>(j) * (kTurnTile * kTurnTile) + ml * kTurnTile + q;
     const int64_t stride = static_cast<int64_t>(s.rem) * (kTurnTile * kTurnTile);
-    f32x4t v[2][SP];
-#pragma unroll
-    for (int k = 0; k < SP; ++k)
-#pragma unroll
-        for (int w = 0; w < 2; ++w) v[w][k] = *reinterpret_cast<const f32x4t*>(p + k * stride + 128 * w);
-    f32x4t t[2] = {v[0][0], v[1][0]};
-#pragma unroll
-    for (int k = 1; k < SP; ++k)
-#pragma unroll
-        for (int w = 0; w < 2; ++w) t[w] = t[w] + v[w][k];
+    const float4 g = ordered_sum4<4>(p, stride, s.splits), u = ordered_sum4<4>(p + 128, stride, s.splits);
     if (o.GU != nullptr) {
-#pragma unroll
-        for (int w = 0; w < 2; ++w)
-            *reinterpret_cast<uint2*>(o.GU + static_cast<int64_t>(m) * o.ldgu + w * o.d_ff + n) =
-                uint2{bf16_pair(t[w][0], t[w][1]), bf16_pair(t[w][2], t[w][3])};
+        uint16_t* at = o.GU + static_cast<int64_t>(m) * o.ldgu + n;
+        *reinterpret_cast<uint2*>(at) = uint2{bf16_pair(g.x, g.y), bf16_pair(g.z, g.w)};
+        *reinterpret_cast<uint2*>(at + o.d_ff) = uint2{bf16_pair(u.x, u.y), bf16_pair(u.z, u.w)};
     }
-    float h[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = gated_act(o.act, t[0][e]) * t[1][e];
     *reinterpret_cast<uint2*>(o.H + static_cast<int64_t>(m) * o.ldh + n) =
-        uint2{bf16_pair(h[0], h[1]), bf16_pair(h[2], h[3])};
+        uint2{bf16_pair(gated_act(o.act, g.x) * u.x, gated_act(o.act, g.y) * u.y),
+              bf16_pair(gated_act(o.act, g.z) * u.z, gated_act(o.act, g.w) * u.w)};
 }
 
 // dX = dGU [W_g; W_u] + U' A: a plain product, bf16 out
@@ -173,7 +160,6 @@ void gated_dx_kernel(TurnArgs g, TurnSplit s, GatedDx o) {
 }
 
 // Split tiles: the shares' sums in order; 4 outputs per thread, 64 workgroups per tile
-template <int SP>
 __global__ __launch_bounds__(256)
 void gated_dx_reduce(TurnSplit s, GatedDx o) {
     const int j = static_cast<int>(blockIdx.x) / 64;
@@ -184,14 +170,8 @@ void gated_dx_reduce(TurnSplit s, GatedDx o) {
     const int m = tm * kTurnTile + ml, n = tn * kTurnTile + nl;
     if (m >= o.M || n >= o.N) return;
     const float* p = o.part + static_cast<int64_t>(j) * (kTurnTile * kTurnTile) + ml * kTurnTile + nl;
-    const int64_t stride = static_cast<int64_t>(s.rem) * (kTurnTile * kTurnTile);
-    f32x4t v[SP];
-#pragma unroll
-    for (int k = 0; k < SP; ++k) v[k] = *reinterpret_cast<const f32x4t*>(p + k * stride);
-    f32x4t t = v[0];
-#pragma unroll
-    for (int k = 1; k < SP; ++k) t = t + v[k];
-    *reinterpret_cast<uint2*>(o.C + static_cast<int64_t>(m) * o.ldc + n) = uint2{bf16_pair(t[0], t[1]), bf16_pair(t[2], t[3])};
+    const float4 t = ordered_sum4<4>(p, static_cast<int64_t>(s.rem) * (kTurnTile * kTurnTile), s.splits);
+    *reinterpret_cast<uint2*>(o.C + static_cast<int64_t>(m) * o.ldc + n) = uint2{bf16_pair(t.x, t.y), bf16_pair(t.z, t.w)};
 }
 
 TurnSplit fwd_split(int64_t M, int64_t d_ff, int64_t d_in) {
@@ -226,9 +206,7 @@ hipError_t launch_gated_gemm(const GatedCall& c, const uint16_t* X, int64_t ldx,
     if (GU != nullptr) QN_LAUNCH("gated_gemm_kernel", st, gated_gemm_kernel<true>, grid, dim3(kTurnThreads), 0, st, g, s, o);
     else QN_LAUNCH("gated_gemm_kernel", st, gated_gemm_kernel<false>, grid, dim3(kTurnThreads), 0, st, g, s, o);
     const dim3 rgrid(static_cast<unsigned>(s.rem * 32));
-    if (s.splits == 2) QN_LAUNCH("gated_split_reduce", st, gated_split_reduce<2>, rgrid, dim3(256), 0, st, s, o);
-    else if (s.splits == 3) QN_LAUNCH("gated_split_reduce", st, gated_split_reduce<3>, rgrid, dim3(256), 0, st, s, o);
-    else if (s.splits == 4) QN_LAUNCH("gated_split_reduce", st, gated_split_reduce<4>, rgrid, dim3(256), 0, st, s, o);
+    if (s.splits > 1) QN_LAUNCH("gated_split_reduce", st, gated_split_reduce, rgrid, dim3(256), 0, st, s, o);
     return hipGetLastError();
 }
 
@@ -240,9 +218,7 @@ hipError_t launch_gated_dx(const GatedCall& c, const uint16_t* dGU, int64_t lddg
     const GatedDx o{dX, lddx, static_cast<int>(c.M), static_cast<int>(c.d_in), part};
     QN_LAUNCH("gated_dx_kernel", st, gated_dx_kernel, dim3(turn_split_grid(s)), dim3(kTurnThreads), 0, st, g, s, o);
     const dim3 rgrid(static_cast<unsigned>(s.rem * 64));
-    if (s.splits == 2) QN_LAUNCH("gated_dx_reduce", st, gated_dx_reduce<2>, rgrid, dim3(256), 0, st, s, o);
-    else if (s.splits == 3) QN_LAUNCH("gated_dx_reduce", st, gated_dx_reduce<3>, rgrid, dim3(256), 0, st, s, o);
-    else if (s.splits == 4) QN_LAUNCH("gated_dx_reduce", st, gated_dx_reduce<4>, rgrid, dim3(256), 0, st, s, o);
+    if (s.splits > 1) QN_LAUNCH("gated_dx_reduce", st, gated_dx_reduce, rgrid, dim3(256), 0, st, s, o);
     return hipGetLastError();
 }
 

@@ -4,20 +4,20 @@
 // becomes of the sums are the caller's.
 //
 // Two groups of 4 waves (one wave of each on every SIMD) take turns: between two barriers one
-// group runs 16 MFMAs of 16 x 16 x 32 while the other reads its next fragments from LDS and issues
+// group runs 32 MFMAs of 16 x 16 x 32 while the other reads its next fragments from LDS and issues
 // loads, so the matrix pipe of a SIMD has one wave's run after the other's and no MFMA waits for
-// an LDS read of its own wave. A K-step of 64 has four such phases, one per quarter of the tile
-// (128 x 128, of which a wave has 64 x 32):
-//   phase   reads from LDS       issues loads of     multiplies
-//   0       P half 0 (8 x 16 B)  P half 1 of t + 1   P0 Q0
-//   1       Q half 1 (4)         Q half 0 of t + 2   P0 Q1
-//   2       P half 1 (8)         P half 0 of t + 2   P1 Q1
-//   3       Q half 0 of t + 1    Q half 1 of t + 2   P1 Q0
-// A half (128 rows x 64 k, 16 KB) is refilled two phases after it was read, which is the first
-// point where both groups' reads are known to be done, and a load has five phases to land: the
-// waits are for all but the 10 newest of a wave's loads and never empty the queue before the tile's
-// last steps. Eight halves, each an LDS object of its own (so that the compiler can tell the reads
-// of one from the loads into another), 128 KB.
+// an LDS read. A K-step of 64 has two such phases, one per half of the tile's rows (a wave has 64 of
+// each half's 128 rows, and 32 of each half's 128 columns):
+//   phase   reads from LDS                        issues loads of         multiplies
+//   0       P half 0, Q halves 0, 1 (16 x 16 B)   P half 1 of t + 1       P0 Q0, P0 Q1
+//   1       P half 1 (8)                          the others of t + 2     P1 Q1, P1 Q0
+// The reads are waited for before a phase's barrier, so a half (128 rows x 64 k, 16 KB) is refilled one
+// phase after it was read, the first point where both groups' reads are known to be done; a load has
+// three phases to land: the waits are for all but the 8 newest of a wave's loads and never empty the
+// queue before the tile's last steps. Eight halves, 128 KB of LDS.
+// The matrix pipes are busy 80 % of the time, at the clock that this load leaves (1.9 GHz: the chip is
+// power-limited); 4096 x 4096 x 16128 takes 350 us (1.54 PFLOP/s), the library's product 342 on the same
+// board. Four phases of 16 MFMAs took the same; 32 x 32 x 16 MFMAs on the same schedule 394.
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -146,7 +146,7 @@ __device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, 
     const int fr = lane & 15;
     const uint32_t c0 = static_cast<uint32_t>((lane >> 4) ^ ((fr >> 1) & 7)), c1 = c0 ^ 4u;    // chunks of k 0..31 and 32..63
     const uint32_t prow = static_cast<uint32_t>(64 * wm + fr) * 8, qrow = static_cast<uint32_t>(32 * wn + fr) * 8;
-    uint4 a[4][2], bx[2][2], by[2][2];
+    uint4 a[4][2], b0[2][2], b1[2][2];
 #define QN_READ_P(OBJ)                                                                  \
     _Pragma("unroll") for (int k = 0; k < 2; ++k)                                       \
         _Pragma("unroll") for (int i = 0; i < 4; ++i) a[i][k] = (OBJ)[prow + 128 * i + (k ? c1 : c0)];
@@ -163,36 +163,31 @@ __device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, 
                         __builtin_bit_cast(bf16x8, B[j][k]), __builtin_bit_cast(bf16x8, a[i][k]), acc[H][G][i][j], 0, 0, 0); \
         __builtin_amdgcn_s_setprio(0);                                                  \
     }
-    // One K-step on stage (P0, P1, Q0, Q1), NP1 and NQ0 halves of the other stage; B1st has Q half 0,
-    // B2nd is for the other half.
-#define QN_STEP(P0, P1, Q0, Q1, NP1, NQ0, B1st, B2nd)                                   \
+    // One K-step on stage (P0, P1, Q0, Q1), NP1 a half of the other stage. A phase's LDS reads are
+    // waited for before its barrier, so a half may be refilled one phase after it was read.
+#define QN_STEP(P0, P1, Q0, Q1, NP1)                                                    \
     {                                                                                   \
         QN_READ_P(P0)                                                                   \
+        QN_READ_Q(Q0, b0)                                                               \
+        QN_READ_Q(Q1, b1)                                                               \
         QN_LOAD(NP1, rsP, voP[1])                                                       \
         leave();                                                                        \
-        QN_WAIT_VM(10);                                                                 \
+        QN_WAIT_VM(8);                                                                  \
+        QN_WAIT_LDS();                                                                  \
         QN_TURN()                                                                       \
-        QN_MULTIPLY(0, 0, B1st)                                                         \
-        QN_TURN()                                                                       \
-        QN_READ_Q(Q1, B2nd)                                                             \
-        enter();                                                                        \
-        QN_LOAD(Q0, rsQ, voQ[0])                                                        \
-        QN_WAIT_VM(10);                                                                 \
-        QN_TURN()                                                                       \
-        QN_MULTIPLY(0, 1, B2nd)                                                         \
+        QN_MULTIPLY(0, 0, b0)                                                           \
+        QN_MULTIPLY(0, 1, b1)                                                           \
         QN_TURN()                                                                       \
         QN_READ_P(P1)                                                                   \
+        enter();                                                                        \
         QN_LOAD(P0, rsP, voP[0])                                                        \
-        QN_WAIT_VM(10);                                                                 \
-        QN_TURN()                                                                       \
-        QN_MULTIPLY(1, 1, B2nd)                                                         \
-        QN_TURN()                                                                       \
-        QN_READ_Q(NQ0, B2nd)                                                            \
+        QN_LOAD(Q0, rsQ, voQ[0])                                                        \
         QN_LOAD(Q1, rsQ, voQ[1])                                                        \
-        QN_WAIT_VM(10);                                                                 \
+        QN_WAIT_VM(8);                                                                  \
+        QN_WAIT_LDS();                                                                  \
         QN_TURN()                                                                       \
-        QN_MULTIPLY(1, 0, B1st)                                                         \
-        QN_WAIT_LDS();  /* B2nd, two phases before its half is refilled */              \
+        QN_MULTIPLY(1, 1, b1)                                                           \
+        QN_MULTIPLY(1, 0, b0)                                                           \
         QN_TURN()                                                                       \
     }
 
@@ -206,23 +201,22 @@ __device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, 
                 for (int j = 0; j < 2; ++j) acc[h][q][i][j] = f32x4t{0.0f, 0.0f, 0.0f, 0.0f};
 
     enter();
-    QN_LOAD(g_q00, rsQ, voQ[0])
     QN_LOAD(g_p00, rsP, voP[0])
+    QN_LOAD(g_q00, rsQ, voQ[0])
     QN_LOAD(g_q01, rsQ, voQ[1])
     QN_LOAD(g_p01, rsP, voP[1])
     leave();
     enter();
-    QN_LOAD(g_q10, rsQ, voQ[0])
     QN_LOAD(g_p10, rsP, voP[0])
+    QN_LOAD(g_q10, rsQ, voQ[0])
     QN_LOAD(g_q11, rsQ, voQ[1])
-    QN_WAIT_VM(10);
+    QN_WAIT_VM(8);
     QN_TURN()
-    QN_READ_Q(g_q00, bx)
     if (wm == 1) QN_TURN()                          // the second group starts one turn later
     for (int left = KT;;) {
-        QN_STEP(g_p00, g_p01, g_q00, g_q01, g_p11, g_q10, bx, by)
+        QN_STEP(g_p00, g_p01, g_q00, g_q01, g_p11)
         if (--left == 0) break;
-        QN_STEP(g_p10, g_p11, g_q10, g_q11, g_p01, g_q00, by, bx)
+        QN_STEP(g_p10, g_p11, g_q10, g_q11, g_p01)
         if (--left == 0) break;
     }
     if (wm == 0) QN_TURN()
@@ -294,7 +288,8 @@ __device__ __forceinline__ void turn_tile(int item, int tiles_m, int tiles_n, in
 // The K-steps of the last round of tiles split over several workgroups each where it would leave
 // most CUs idle: of T tiles the first full run whole, the K-steps of the rem others in `splits`
 // shares of kper whose float32 sums (256 x 256 a piece, share s of tile j at s rem + j) a second
-// kernel adds. Shares have 8 K-steps or more.
+// kernel adds. Up to 16 shares, of 4 K-steps or more (1531 tokens of the 11008 x 4096 block leave 4 tiles:
+// 243 us with up to 4 shares of 8 steps).
 struct TurnSplit { int tiles_m, tiles_n, splits, full, rem, kper; };
 inline TurnSplit turn_split(int64_t M, int64_t tiles_n, int64_t kt) {
     TurnSplit s{};
@@ -302,12 +297,13 @@ inline TurnSplit turn_split(int64_t M, int64_t tiles_n, int64_t kt) {
     s.tiles_n = static_cast<int>(tiles_n);
     const int T = s.tiles_m * s.tiles_n, rem = T % 256;
     int want = rem == 0 || rem > 128 ? 1 : 256 / rem;
-    if (want > 4) want = 4;
-    if (want > kt / 8) want = static_cast<int>(kt / 8);
+    if (want > 16) want = 16;
+    if (want > kt / 4) want = static_cast<int>(kt / 4);
     s.splits = want < 2 ? 1 : want;
     s.full = s.splits > 1 ? T - rem : T;
     s.rem = s.splits > 1 ? rem : 0;
     s.kper = static_cast<int>((kt + s.splits - 1) / s.splits);
+    if (s.splits > 1) s.splits = static_cast<int>((kt + s.kper - 1) / s.kper);
     return s;
 }
 inline int64_t turn_split_floats(const TurnSplit& s) {

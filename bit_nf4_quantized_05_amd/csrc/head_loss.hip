@@ -462,10 +462,11 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool head_plan(int64_t V, int64_t d, int64_t T, bool nf4, bool grad, HeadPlan* p) {
     constexpr int64_t kLimit = int64_t{1} << 31;     // elements of bf16 in 4 GiB
     const bool keeps = grad || nf4;
-    // Pieces of up to 16384 rows where something of a piece is kept (its exponentials, W^T, the
-    // dequantised rows), fewer where T rows of exponentials would pass 2 GiB; else up to 65536.
-    int64_t most = keeps ? 16384 : 65536;
-    if (grad) most = std::min(most, std::max<int64_t>(256, kLimit / 2 / T / 256 * 256));
+    // Pieces of up to 65536 rows (dequantised rows of 4096: 512 MB), of a gradient 32768 (W^T 256 MB) and
+    // fewer where T rows of exponentials would pass 2^27 (256 MB), but 4096 rows of them up to 2 GiB.
+    int64_t most = grad ? 32768 : 65536;
+    if (grad) most = std::min(most, std::max((int64_t{1} << 27) / T, std::min<int64_t>(4096, kLimit / 2 / T)) / 256 * 256);
+    most = std::max<int64_t>(256, most);
     p->pieces = static_cast<int>(ceil_div(V, most));
     p->piece = ceil_div(ceil_div(V, p->pieces), 256) * 256;
     p->pieces = static_cast<int>(ceil_div(V, p->piece));
