@@ -124,10 +124,6 @@ struct GatedProlog {
 };
 hipError_t launch_gated_prologue(const GatedCall& c, bool backward, const GatedProlog& o, hipStream_t st);
 
-// W_hat [d_out, d_in] to rows and transposed to cols (row stride ld_cols); either may be null
-hipError_t launch_dequant_both(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
-                               uint16_t* rows, uint16_t* cols, int64_t ld_cols, hipStream_t st);
-
 // ---- gated.hip ----
 // H (and GU, if not null) from X, the weights what, the rank products t [M, k2] and the adapters
 // adapt [2 d_ff, k2] (t, adapt unused without adapters); part holds gated_part_floats floats.

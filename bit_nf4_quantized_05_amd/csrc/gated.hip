@@ -45,7 +45,7 @@ void gated_gemm_kernel(TurnArgs g, TurnSplit s, GatedOut o) {
     if (p.tile < 0) return;
     const int m0 = p.tm * kTurnTile, h0 = p.tn * (kTurnTile / 2);
     TurnSums acc;
-    gemm_turns<true>(
+    gemm_turns<true, false>(
         g, [&](int r) { return static_cast<uint32_t>(min(m0 + r, o.M - 1)); },
         [&](int r) { return static_cast<uint32_t>((r < 128 ? 0 : o.d_ff) + min(h0 + (r & 127), o.d_ff - 1)); }, p.kb, p.ke,
         p.share < 0 || p.share == s.splits - 1, acc);
@@ -134,7 +134,7 @@ void gated_dx_kernel(TurnArgs g, TurnSplit s, GatedDx o) {
     if (p.tile < 0) return;
     const int m0 = p.tm * kTurnTile, n0 = p.tn * kTurnTile;
     TurnSums acc;
-    gemm_turns<true>(
+    gemm_turns<true, false>(
         g, [&](int r) { return static_cast<uint32_t>(min(m0 + r, o.M - 1)); },
         [&](int r) { return static_cast<uint32_t>(min(n0 + r, o.N - 1)); }, p.kb, p.ke,
         p.share < 0 || p.share == s.splits - 1, acc);

@@ -1,7 +1,8 @@
 // The K loop of the gated block's and the head's BF16 MFMA contractions (gated.hip,
-// head_loss.hip): a 256 x 256 tile of P Q^T (+ P2 Q2^T), both operands row-major with K
-// contiguous, in the accumulators of a workgroup of 8 waves. The tile's place, its rows and what
-// becomes of the sums are the caller's.
+// head_loss.hip): a 256 x 256 tile of P Q^T (+ P2 Q2^T), P row-major with K contiguous, Q so or
+// with its rows along K (a weight as it lies, in the product for its input's gradient), in the
+// accumulators of a workgroup of 8 waves. The tile's place, its rows and what becomes of the sums
+// are the caller's.
 //
 // Two groups of 4 waves (one wave of each on every SIMD) take turns: between two barriers one
 // group runs 32 MFMAs of 16 x 16 x 32 while the other reads its next fragments from LDS and issues
@@ -17,7 +18,9 @@
 // queue before the tile's last steps. Eight halves, 128 KB of LDS.
 // The matrix pipes are busy 80 % of the time, at the clock that this load leaves (1.9 GHz: the chip is
 // power-limited); 4096 x 4096 x 16128 takes 350 us (1.54 PFLOP/s), the library's product 342 on the same
-// board. Four phases of 16 MFMAs took the same; 32 x 32 x 16 MFMAs on the same schedule 394.
+// board. Four phases of 16 MFMAs took the same; 32 x 32 x 16 MFMAs on the same schedule 394. With Q's
+// rows along K (8-byte LDS reads that transpose, twice as many) it takes 353: the transposed copy
+// that the other form needs cost 88 more.
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -36,6 +39,7 @@ struct TurnArgs {
     const uint16_t* Q2; int64_t ldq2;
     uint32_t bytesP, bytesQ, bytesP2, bytesQ2;      // extents for the load descriptors
     int kt1, kt2;                                   // K-steps of P Q^T, and of P2 Q2^T
+    int rowsQ;                                      // rows of Q
 };
 
 // rowsP, rowsQ: rows of the operands (their extents: every operand is below 4 GiB)
@@ -46,12 +50,22 @@ inline TurnArgs turn_args(const uint16_t* P, int64_t ldp, int64_t rowsP, const u
     g.bytesP = static_cast<uint32_t>(2 * ldp * rowsP);
     g.bytesQ = static_cast<uint32_t>(2 * ldq * rowsQ);
     g.kt1 = static_cast<int>(K / kTurnK);
+    g.rowsQ = static_cast<int>(rowsQ);
     return g;
 }
 
 namespace {
 
 typedef float f32x4t __attribute__((ext_vector_type(4)));
+
+typedef uint32_t u32x2t __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) char* turn_bytes_t;
+
+__device__ __forceinline__ u32x2t turn_read_cols(turn_bytes_t at) {
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    return __builtin_bit_cast(u32x2t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)at));
+}
 
 // halves: stage, operand, rows 0..127 or 128..255 of the tile
 __shared__ uint4 g_p00[1024], g_p01[1024], g_q00[1024], g_q01[1024];
@@ -92,8 +106,11 @@ __device__ __forceinline__ void turn_load(const i32x4t& rsrc, uint32_t to, uint3
 
 // acc = the K-steps [kb, ke) of P Q^T, then (kRank and rank) the g.kt2 steps of P2 Q2^T; at least
 // one step in all. rowP(r), rowQ(r): the row of P and P2 (Q and Q2) that tile row r takes (uint32,
-// inside the operand). On return every wave has finished its reads of LDS and no load is in flight.
-template <bool kRank, class RowP, class RowQ>
+// inside the operand). With kQCols, Q is K-major instead, [kt1 64, ..] with its rows along K:
+// rowQ(r) is then the column of tile row r, for r a multiple of 8 and the 7 after it, and rows from
+// g.rowsQ on are taken as that last row (P must be zero there). On return every wave has finished
+// its reads of LDS and no load is in flight.
+template <bool kRank, bool kQCols, class RowP, class RowQ>
 __device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, const RowQ& rowQ, int kb, int ke, bool rank,
                                            TurnSums& acc) {
     const int lane = threadIdx.x & 63;
@@ -114,10 +131,25 @@ __device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, 
                 const int r = 128 * h + 16 * wave + 8 * j + (lane >> 3);
                 const uint32_t chunk = static_cast<uint32_t>((lane & 7) ^ (4 * j + (lane >> 4))) * 16u;
                 voP[h][j] = rowP(r) * static_cast<uint32_t>(ldp * 2) + chunk;
-                voQ[h][j] = rowQ(r) * static_cast<uint32_t>(ldq * 2) + chunk;
+                if constexpr (!kQCols) voQ[h][j] = rowQ(r) * static_cast<uint32_t>(ldq * 2) + chunk;
+            }
+    };
+    // K-major Q: a half is 64 k-rows of 128 columns = 256 B = 8 units of 32 B; unit u of row k is stored
+    // at u ^ swz(k), which puts the 8 rows that 32 lanes of a transposing read take (4 of each of two
+    // 8-row groups) into 8 distinct units. A load instruction fills 4 rows; wave w fills 8 w .. 8 w + 7.
+    const auto swz = [](int k) { return (k & 3) | ((k >> 1) & 4); };
+    auto columns = [&](int first) {                 // the rows' first is k-row `first` of Q
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int k = 8 * wave + 4 * j + (lane >> 4), at = lane & 15;
+                const int n = 128 * h + 16 * ((at >> 1) ^ swz(k)) + 8 * (at & 1);
+                voQ[h][j] = static_cast<uint32_t>(min(k, g.rowsQ - 1 - first)) * static_cast<uint32_t>(g.ldq * 2) + rowQ(n) * 2u;
             }
     };
     places(g.ldp, g.ldq);
+    if constexpr (kQCols) columns(0);
     const int kmain = ke - kb;
     const int KT = kmain + (kRank && rank ? g.kt2 : 0);
     // Loads are issued for two steps past the last as well, so that the loop has no branch around a
@@ -125,22 +157,27 @@ __device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, 
     // no extent, so nothing is fetched.
     int next = 0;                                   // the step whose loads are issued
     int so = kb * (kTurnK * 2);                     // its byte offset in a row
+    const uint32_t qstep = static_cast<uint32_t>(g.ldq) * (kTurnK * 2);      // K-major: bytes of 64 rows
+    int sq = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(kb) * qstep));
     auto enter = [&]() {                            // before the first load of step `next`
         if (kRank && next == kmain) {
             places(g.ldp2, g.ldq2);
             so = 0;
         }
+        if (kQCols && kb + next == g.kt1 - 1) columns(64 * (g.kt1 - 1));     // rows past the last: the last again
         const bool first = !kRank || next < kmain, none = next >= KT;
         rsP = turn_rsrc(first ? g.P : g.P2, none ? 0u : first ? g.bytesP : g.bytesP2);
         rsQ = turn_rsrc(first ? g.Q : g.Q2, none ? 0u : first ? g.bytesQ : g.bytesQ2);
     };
-    auto leave = [&]() { ++next; so += kTurnK * 2; };
-#define QN_LOAD(OBJ, RS, VO)                                        \
+    auto leave = [&]() { ++next; so += kTurnK * 2; sq = __builtin_amdgcn_readfirstlane(static_cast<int>(sq + qstep)); };
+#define QN_LOAD(OBJ, RS, VO, SO)                                    \
     {                                                               \
         const uint32_t to_ = lds_addr(OBJ) + 2048 * wave;           \
-        turn_load(RS, to_, (VO)[0], so);                            \
-        turn_load(RS, to_ + 1024, (VO)[1], so);                     \
+        turn_load(RS, to_, (VO)[0], SO);                            \
+        turn_load(RS, to_ + 1024, (VO)[1], SO);                     \
     }
+#define QN_LOAD_P(OBJ, H) QN_LOAD(OBJ, rsP, voP[H], so)
+#define QN_LOAD_Q(OBJ, H) QN_LOAD(OBJ, rsQ, voQ[H], kQCols ? sq : so)
 
     // fragments: lane l has row l % 16, k 8 (l / 16) .. + 7 of each 32
     const int fr = lane & 15;
@@ -150,9 +187,25 @@ __device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, 
 #define QN_READ_P(OBJ)                                                                  \
     _Pragma("unroll") for (int k = 0; k < 2; ++k)                                       \
         _Pragma("unroll") for (int i = 0; i < 4; ++i) a[i][k] = (OBJ)[prow + 128 * i + (k ? c1 : c0)];
+    // K-major: a transposing read hands lane p of 16 column p of a 4 x 16 block whose row p / 4 the
+    // address of lanes 4 (p / 4) .. + 3 gives, 8 bytes a lane; two make the 8 k of a fragment
+    uint32_t qcol[2];                               // by k / 4 of the 8
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int k = 8 * (lane >> 4) + 4 * q + (fr >> 2);
+        qcol[q] = static_cast<uint32_t>(256 * k + 32 * ((2 * wn) ^ swz(k)) + 8 * (fr & 3));
+    }
 #define QN_READ_Q(OBJ, B)                                                               \
     _Pragma("unroll") for (int k = 0; k < 2; ++k)                                       \
-        _Pragma("unroll") for (int j = 0; j < 2; ++j) B[j][k] = (OBJ)[qrow + 128 * j + (k ? c1 : c0)];
+        _Pragma("unroll") for (int j = 0; j < 2; ++j) {                                 \
+            if constexpr (kQCols) {                                                     \
+                const turn_bytes_t at_ = (turn_bytes_t)(OBJ) + 8192 * k;                \
+                const u32x2t lo_ = turn_read_cols(at_ + (qcol[0] ^ (32u * j))), hi_ = turn_read_cols(at_ + (qcol[1] ^ (32u * j))); \
+                B[j][k] = uint4{lo_.x, lo_.y, hi_.x, hi_.y};                            \
+            } else {                                                                    \
+                B[j][k] = (OBJ)[qrow + 128 * j + (k ? c1 : c0)];                        \
+            }                                                                           \
+        }
 #define QN_MULTIPLY(H, G, B)                                                            \
     {                                                                                   \
         __builtin_amdgcn_s_setprio(1);                                                  \
@@ -170,7 +223,7 @@ __device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, 
         QN_READ_P(P0)                                                                   \
         QN_READ_Q(Q0, b0)                                                               \
         QN_READ_Q(Q1, b1)                                                               \
-        QN_LOAD(NP1, rsP, voP[1])                                                       \
+        QN_LOAD_P(NP1, 1)                                                               \
         leave();                                                                        \
         QN_WAIT_VM(8);                                                                  \
         QN_WAIT_LDS();                                                                  \
@@ -180,9 +233,9 @@ __device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, 
         QN_TURN()                                                                       \
         QN_READ_P(P1)                                                                   \
         enter();                                                                        \
-        QN_LOAD(P0, rsP, voP[0])                                                        \
-        QN_LOAD(Q0, rsQ, voQ[0])                                                        \
-        QN_LOAD(Q1, rsQ, voQ[1])                                                        \
+        QN_LOAD_P(P0, 0)                                                                \
+        QN_LOAD_Q(Q0, 0)                                                                \
+        QN_LOAD_Q(Q1, 1)                                                                \
         QN_WAIT_VM(8);                                                                  \
         QN_WAIT_LDS();                                                                  \
         QN_TURN()                                                                       \
@@ -201,15 +254,15 @@ __device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, 
                 for (int j = 0; j < 2; ++j) acc[h][q][i][j] = f32x4t{0.0f, 0.0f, 0.0f, 0.0f};
 
     enter();
-    QN_LOAD(g_p00, rsP, voP[0])
-    QN_LOAD(g_q00, rsQ, voQ[0])
-    QN_LOAD(g_q01, rsQ, voQ[1])
-    QN_LOAD(g_p01, rsP, voP[1])
+    QN_LOAD_P(g_p00, 0)
+    QN_LOAD_Q(g_q00, 0)
+    QN_LOAD_Q(g_q01, 1)
+    QN_LOAD_P(g_p01, 1)
     leave();
     enter();
-    QN_LOAD(g_p10, rsP, voP[0])
-    QN_LOAD(g_q10, rsQ, voQ[0])
-    QN_LOAD(g_q11, rsQ, voQ[1])
+    QN_LOAD_P(g_p10, 0)
+    QN_LOAD_Q(g_q10, 0)
+    QN_LOAD_Q(g_q11, 1)
     QN_WAIT_VM(8);
     QN_TURN()
     if (wm == 1) QN_TURN()                          // the second group starts one turn later
@@ -226,13 +279,12 @@ __device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, 
 #undef QN_MULTIPLY
 #undef QN_READ_Q
 #undef QN_READ_P
+#undef QN_LOAD_Q
+#undef QN_LOAD_P
 #undef QN_LOAD
 }
 
 // ---- epilogue: a bf16 tile through LDS, so that it leaves in whole rows ----
-typedef uint32_t u32x2t __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) char* turn_bytes_t;
 
 // object `index` (0..7; a constant after unrolling, or uniform)
 __device__ __forceinline__ turn_bytes_t turn_object(int index) {

@@ -24,7 +24,7 @@ struct HeadCall {
 struct HeadPlan {
     int64_t piece;                            // rows per piece, a multiple of 256
     int pieces, slots;                        // pieces; 256 x 256 sums of the gradient's product
-    int64_t ints, part, E, WT, rows, wt, acc, bytes;
+    int64_t ints, part, E, rows, wt, acc, bytes;
 };
 bool head_plan(int64_t V, int64_t d, int64_t T, bool nf4, bool grad, HeadPlan* p);
 

@@ -18,9 +18,9 @@
 // Tokens without a target (prompts, padding) are left out before the products: head_plan_kernel
 // numbers the others, the GEMM gathers their rows, and workgroups past the last one end at once.
 //
-// Per piece: W^T of the piece (gradient; an NF4 head is dequantised here, both ways),
-// head_logits (the product and its exponentials), head_join, head_grad (their product with W,
-// added to float32 sums). Then head_final. All sums are in fixed order.
+// Per piece: an NF4 head's rows dequantised; head_logits (the product and its exponentials),
+// head_join, head_grad (their product with W, whose rows are along K there: read by transposing
+// LDS reads, no transposed copy; added to float32 sums). Then head_final. All sums are in fixed order.
 #include <hip/hip_runtime.h>
 
 #include "gated.h"
@@ -137,37 +137,6 @@ void head_target_kernel(HeadCall c, HeadRows r, uint16_t* wt, NF4Tables tab) {
     }
 }
 
-// dst [d, ld] = src [rows, d]^T for columns below rows, zeros up to the next multiple of 64.
-// A workgroup takes 64 x 64; 16-byte loads and stores through LDS rows of odd pitch (in words).
-__global__ __launch_bounds__(256)
-void head_transpose_kernel(const uint16_t* __restrict__ src, int64_t ldw, int64_t rows, uint16_t* __restrict__ dst,
-                           int64_t ld) {
-    constexpr int kP = 66;
-    __shared__ uint16_t tile[64 * kP];
-    const int64_t i0 = static_cast<int64_t>(blockIdx.x) * 64;         // columns of src
-    const int64_t v0 = static_cast<int64_t>(blockIdx.y) * 64;         // rows of src
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int c = 256 * u + threadIdx.x;
-        const int v = c >> 3, q = c & 7;
-        uint4 w = uint4{0, 0, 0, 0};
-        if (v0 + v < rows) w = *reinterpret_cast<const uint4*>(src + (v0 + v) * ldw + i0 + 8 * q);
-        uint32_t* at = reinterpret_cast<uint32_t*>(&tile[v * kP + 8 * q]);
-        at[0] = w.x; at[1] = w.y; at[2] = w.z; at[3] = w.w;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int c = 256 * u + threadIdx.x;
-        const int i = c >> 3, q = c & 7;
-        uint32_t w[4];
-#pragma unroll
-        for (int h = 0; h < 4; ++h)
-            w[h] = tile[(8 * q + 2 * h) * kP + i] | (static_cast<uint32_t>(tile[(8 * q + 2 * h + 1) * kP + i]) << 16);
-        *reinterpret_cast<uint4*>(dst + (i0 + i) * ld + v0 + 8 * q) = uint4{w[0], w[1], w[2], w[3]};
-    }
-}
-
 struct HeadTile {
     int v0, cols, tiles_n;                    // the piece's first row of the head, its rows and tiles
     int64_t T;
@@ -188,7 +157,7 @@ void head_logits_kernel(TurnArgs g, HeadTile h, HeadRows r) {
     turn_tile(item, tiles_m, h.tiles_n, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
     TurnSums acc;
-    gemm_turns<false>(
+    gemm_turns<false, false>(
         g, [&](int i) { return static_cast<uint32_t>(r.idx[min(m0 + i, count - 1)]); },
         [&](int i) { return static_cast<uint32_t>(min(n0 + i, h.cols - 1)); }, 0, g.kt1, false, acc);
     // e = 2^((z - zt) log2 e - shift), 0 at the target and past the piece. The lane has rows 128 hh +
@@ -402,15 +371,15 @@ void head_grad_kernel(TurnArgs g, HeadGrad h, int d, HeadRows r) {
     const int item = turn_item(static_cast<int>(blockIdx.x), s.tiles * s.splits);
     if (item < 0) return;
     const int sp = item / s.tiles;
-    const int kb = sp * s.kper, ke = min(kb + s.kper, g.kt1);
+    const int kb = __builtin_amdgcn_readfirstlane(sp * s.kper), ke = min(kb + s.kper, g.kt1);
     if (kb >= ke) return;                            // a later, shorter piece adds nothing here
     int tm, tn;
     turn_tile(item % s.tiles, (count + BM - 1) / BM, h.tiles_n, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
     TurnSums acc;
-    gemm_turns<false>(
+    gemm_turns<false, true>(
         g, [&](int i) { return static_cast<uint32_t>(min(m0 + i, count - 1)); },
-        [&](int i) { return static_cast<uint32_t>(min(n0 + i, d - 1)); }, kb, ke, false, acc);
+        [&](int i) { return static_cast<uint32_t>(min(n0 + i, d - 8)); }, kb, ke, false, acc);
     turn_put_sums(h.acc + (static_cast<int64_t>(sp) * s.tiles + tm * h.tiles_n + tn) * (BM * BN), acc, !h.first);
 }
 
@@ -462,7 +431,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 bool head_plan(int64_t V, int64_t d, int64_t T, bool nf4, bool grad, HeadPlan* p) {
     constexpr int64_t kLimit = int64_t{1} << 31;     // elements of bf16 in 4 GiB
     const bool keeps = grad || nf4;
-    // Pieces of up to 65536 rows (dequantised rows of 4096: 512 MB), of a gradient 32768 (W^T 256 MB) and
+    // Pieces of up to 65536 rows (dequantised rows of 4096: 512 MB), of a gradient 32768 and
     // fewer where T rows of exponentials would pass 2^27 (256 MB), but 4096 rows of them up to 2 GiB.
     int64_t most = grad ? 32768 : 65536;
     if (grad) most = std::min(most, std::max((int64_t{1} << 27) / T, std::min<int64_t>(4096, kLimit / 2 / T)) / 256 * 256);
@@ -483,7 +452,6 @@ bool head_plan(int64_t V, int64_t d, int64_t T, bool nf4, bool grad, HeadPlan* p
     p->ints = take(4 * head_int_count(T));
     p->part = take(8 * (p->piece / BN) * T);
     p->E = take(grad ? 2 * T * p->piece : 0);
-    p->WT = take(grad ? 2 * d * p->piece : 0);
     p->rows = take(nf4 ? 2 * d * p->piece : 0);
     p->wt = take(nf4 && grad ? 2 * T * d : 0);
     p->acc = take(static_cast<int64_t>(p->slots) * BM * BN * 4);
@@ -496,7 +464,6 @@ hipError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, char* ws, hipS
     const HeadRows r = head_rows(ws + p.ints, c.T);
     float2* part = reinterpret_cast<float2*>(ws + p.part);
     uint16_t* E = grad ? reinterpret_cast<uint16_t*>(ws + p.E) : nullptr;
-    uint16_t* WT = grad ? reinterpret_cast<uint16_t*>(ws + p.WT) : nullptr;
     uint16_t* rows = nf4 ? reinterpret_cast<uint16_t*>(ws + p.rows) : nullptr;
     uint16_t* wt = nf4 && grad ? reinterpret_cast<uint16_t*>(ws + p.wt) : nullptr;
     float* acc = grad ? reinterpret_cast<float*>(ws + p.acc) : nullptr;
@@ -516,11 +483,7 @@ hipError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, char* ws, hipS
             const int64_t blk = v0 * c.d / kBlock;
             bc.q += bc.fmt == kDqNone ? 0 : blk;
             bc.scale += blk >> bc.gshift;
-            if ((e = launch_dequant_both(c.codes + v0 * c.d / 2, bc, cols, c.d, rows, WT, p.piece, st)) != hipSuccess) return e;
-        } else if (grad) {
-            QN_LAUNCH("head_transpose_kernel", st, head_transpose_kernel,
-                      dim3(static_cast<unsigned>(c.d / 64), static_cast<unsigned>(ceil_div(cols, 64))), dim3(256), 0, st, W,
-                      ldw, cols, WT, p.piece);
+            if ((e = launch_dequant_rows(c.codes + v0 * c.d / 2, bc, cols * c.d, rows, st)) != hipSuccess) return e;
         }
         const int tn = static_cast<int>(ceil_div(cols, BN));
         const TurnArgs g = turn_args(c.X, c.ldx, c.T, W, ldw, cols, c.d);
@@ -533,7 +496,7 @@ hipError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, char* ws, hipS
         QN_LAUNCH("head_join_kernel", st, head_join_kernel, dim3(static_cast<unsigned>(ceil_div(c.T, 64))), dim3(256), 0, st,
                   j, r);
         if (grad) {
-            const TurnArgs q = turn_args(E, p.piece, c.T, WT, p.piece, c.d, ceil_div(cols, BK) * BK);
+            const TurnArgs q = turn_args(E, p.piece, c.T, W, ldw, cols, ceil_div(cols, BK) * BK);
             const HeadGrad hg{acc, dn, p.slots, kt_first, i == 0};
             QN_LAUNCH("head_grad_kernel", st, head_grad_kernel, dim3(static_cast<unsigned>(ceil_div(p.slots, 8) * 8)),
                       dim3(kTurnThreads), 0, st, q, hg, static_cast<int>(c.d), r);

@@ -505,15 +505,6 @@ void gated_prologue_kernel(GatedPrologueArgs a, NF4Tables tab) {
     else dequant_jobs(a.deq_up, b - a.p.deq.n, tab, lds);
 }
 
-// One weight dequantised both ways (either may have no workgroups): a piece of a head
-__global__ __launch_bounds__(256)
-void dequant_both_kernel(DeqJob rows, DeqJob cols, NF4Tables tab) {
-    __shared__ uint4 lds[(64 + 1024 + 64 * kTP * sizeof(uint16_t) + 15) / 16];
-    const int b = blockIdx.x;
-    if (b < rows.n) dequant_jobs(rows, b, tab, reinterpret_cast<char*>(lds));
-    else dequant_jobs(cols, b - rows.n, tab, reinterpret_cast<char*>(lds));
-}
-
 // ---------------------------------------------------------------------------
 // Pre-passes of the calls with many adapters: T[pos] = s_a R_a P[order[pos]], the adapter
 // a of each token taken from the batch's plan. A workgroup takes one item of the plan (at
@@ -1075,16 +1066,6 @@ hipError_t launch_gated_prologue(const GatedCall& c, bool backward, const GatedP
         QN_LAUNCH("prepass_reduce", st, prepass_reduce, dim3(static_cast<unsigned>(2 * blocks)), dim3(256), 0, st, r0, r1,
                   blocks, a.p.M, 32 * NT, c.r, gated_pad(c.r));
     }
-    return hipGetLastError();
-}
-
-hipError_t launch_dequant_both(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in,
-                               uint16_t* rows, uint16_t* cols, int64_t ld_cols, hipStream_t st) {
-    const DeqJob jr = make_dequant(codes, bc, d_out, d_in, false, rows);
-    DeqJob jc = make_dequant(codes, bc, d_out, d_in, true, cols);
-    jc.ldw = ld_cols;
-    QN_LAUNCH("dequant_both_kernel", st, dequant_both_kernel, dim3(static_cast<unsigned>(jr.n + jc.n)), dim3(256), 0, st,
-              jr, jc, tables());
     return hipGetLastError();
 }
 
