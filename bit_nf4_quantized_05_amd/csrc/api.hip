@@ -317,7 +317,7 @@ GatedWs gated_ws(int64_t d_ff, int64_t d_in, int64_t d_seq, int r, bool bwd) {
         return at;
     };
     if (!bwd && d_seq <= qn::kGatedSmall) {                                          // the codes streamed: sums only
-        w.part = take(4 * qn::gated_small_part_floats(d_seq, d_ff, d_in, r));
+        w.part = take(std::max<int64_t>(1, 4 * qn::gated_small_part_floats(d_seq, d_ff, d_in, r)));   // 0: sizes refused
         w.bytes = off;
         return w;
     }

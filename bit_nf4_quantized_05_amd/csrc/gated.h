@@ -124,6 +124,10 @@ struct GatedProlog {
 };
 hipError_t launch_gated_prologue(const GatedCall& c, bool backward, const GatedProlog& o, hipStream_t st);
 
+// W_hat [d_out, d_in] bf16, row-major (d_in % 64 == 0)
+hipError_t launch_dequant_weight(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in, uint16_t* what,
+                                 hipStream_t st);
+
 // ---- gated.hip ----
 // H (and GU, if not null) from X, the weights what, the rank products t [M, k2] and the adapters
 // adapt [2 d_ff, k2] (t, adapt unused without adapters); part holds gated_part_floats floats.

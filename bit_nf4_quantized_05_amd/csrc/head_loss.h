@@ -23,7 +23,7 @@ struct HeadCall {
 // have size 0). false: a size that the kernels do not take (an operand of 4 GiB or more).
 struct HeadPlan {
     int64_t piece;                            // rows per piece, a multiple of 256
-    int pieces, slots;                        // pieces; 256 x 256 sums of the gradient's product
+    int pieces, lt, slots;                    // tiles of 1 << lt; tiles of sums of the gradient's product
     int64_t ints, part, E, rows, wt, acc, bytes;
 };
 bool head_plan(int64_t V, int64_t d, int64_t T, bool nf4, bool grad, HeadPlan* p);

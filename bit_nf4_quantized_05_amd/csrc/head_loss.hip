@@ -19,25 +19,39 @@
 // numbers the others, the GEMM gathers their rows, and workgroups past the last one end at once.
 //
 // Per piece: an NF4 head's rows dequantised; head_logits (the product and its exponentials),
-// head_join, head_grad (their product with W, whose rows are along K there: read by transposing
-// LDS reads, no transposed copy; added to float32 sums). Then head_final. All sums are in fixed order.
+// head_join (after the last piece the loss), head_grad (their product with W, whose rows are along K
+// there: read by transposing LDS reads, no transposed copy; added to float32 sums). Then head_final. All sums are in fixed order.
 #include <hip/hip_runtime.h>
 
 #include "gated.h"
+#include "gemm_few.h"
 #include "gemm_turns.h"
 #include "head_loss.h"
 #include "nf4_device.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace qn {
 namespace {
 
-constexpr int BM = kTurnTile, BN = kTurnTile, BK = kTurnK;
+constexpr int BK = kTurnK;
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 // a tile's sum past which its rows are looked at one by one, and the power of two that a row's
 // exponentials may reach (2^80 times 2^31 rows stays in float32)
 constexpr float kLargest = 0x1p80f, kMaxLog2 = 80.0f;
+
+// K-steps that a split of the gradient's product has at least, by its tiles' size (1 << lt)
+__host__ __device__ constexpr int head_steps(int lt) { return lt == 6 ? 4 : 8; }
+// Tiles of 64 are taken on up to kFewTokens tokens (17 on 32000 rows of 4096: loss 51 us against 79
+// with tiles of 256, with the gradient 107 / 154; 128: 66 / 80 and 158 / 163) and where there are up to
+// kFewMost tiles of 256 (256 tokens on 16128 rows, 63 of them: 63 / 77 and 131 / 135; 1024 on 8192, 128:
+// 104 / 78 and 229 / 154).
+constexpr int64_t kFewTokens = 128, kFewMost = 64;
+// Past this many tokens one workgroup numbers them in a launch of its own (on 4096 rows of 64, a
+// launch of its own and each workgroup counting for itself: 4096 tokens 24 us and 22, 16384 51 and 58,
+// 65536 172 and 362).
+constexpr int64_t kPlanFrom = 8192;
 
 // The numbering of the counted tokens and what is known of each (arrays of T)
 struct HeadRows {
@@ -60,7 +74,7 @@ HeadRows head_rows(char* ws, int64_t T) {
 
 // One workgroup: wave w takes a 16th of the tokens, 64 at a time; counts, then numbers them.
 __global__ __launch_bounds__(1024)
-void head_plan_kernel(const int64_t* __restrict__ target, int64_t T, int64_t V, HeadRows r) {
+void head_plan_kernel(const int64_t* __restrict__ target, int64_t T, int64_t V, float* __restrict__ loss, HeadRows r) {
     __shared__ int counts[16];
     const int lane = threadIdx.x & 63;
     const int wave = threadIdx.x >> 6;
@@ -87,45 +101,91 @@ void head_plan_kernel(const int64_t* __restrict__ target, int64_t T, int64_t V, 
             r.idx[p] = static_cast<int32_t>(t + lane);
             r.tgt[p] = static_cast<int32_t>(y);
         }
-        if (t + lane < t1) r.pos[t + lane] = ok ? p : -1;
+        if (t + lane < t1) {
+            r.pos[t + lane] = ok ? p : -1;
+            if (!ok) loss[t + lane] = 0.0f;
+        }
         at += __popcll(m);
     }
     if (threadIdx.x == 0) r.count[0] = all;
 }
 
 // The target's logit of each counted token, a wave each; of an NF4 head also the target's row in
-// bf16 (wt, if not null).
+// bf16 (wt, if not null). Without head_plan_kernel before it (planned 0), workgroup b takes tokens
+// 4 b .. 4 b + 3, counts the tokens before them itself and writes their numbering; else positions.
 __global__ __launch_bounds__(256)
-void head_target_kernel(HeadCall c, HeadRows r, uint16_t* wt, NF4Tables tab) {
+void head_target_kernel(HeadCall c, HeadRows r, uint16_t* wt, int planned, NF4Tables tab) {
     __shared__ float s_code[16];
+    __shared__ int s_before[4];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int t0 = static_cast<int>(blockIdx.x) * 4;
     if (threadIdx.x < 16) s_code[threadIdx.x] = tab.code[threadIdx.x];
-    __syncthreads();
-    const int m = static_cast<int>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-    if (m >= r.count[0]) return;
-    const int lane = threadIdx.x & 63;
-    const int64_t y = r.tgt[m];
-    const uint16_t* x = c.X + r.idx[m] * c.ldx;
-    float sum = 0.0f;
-    for (int64_t k = 8 * lane; k < c.d; k += 512) {
-        const uint4 xv = *reinterpret_cast<const uint4*>(x + k);
-        uint4 wv;
-        if (c.codes == nullptr) {
-            wv = *reinterpret_cast<const uint4*>(c.W + y * c.ldw + k);
-        } else {
-            const int64_t e = y * c.d + k, blk = e >> 6;
-            const uint32_t word = *reinterpret_cast<const uint32_t*>(c.codes + (e >> 1));
-            const float a = block_constant(c.bc.fmt, c.bc.q[blk], c.bc.scale[blk >> c.bc.gshift], c.bc.mean[0]);
-            float w[8];
+    int64_t t = 0, y = 0;
+    int m = t0 + wave;
+    if (!planned) {
+        auto counted = [&](int64_t v) { return v >= 0 && v < c.V; };
+        const int64_t own = lane < 4 && t0 + lane < c.T ? c.target[t0 + lane] : -1;
+        int n = 0;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < t0; i += 256) n += counted(c.target[i]) ? 1 : 0;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) w[q] = s_code[(word >> (4 * q)) & 0xFu] * a;
-            wv = uint4{bf16_pair(w[0], w[1]), bf16_pair(w[2], w[3]), bf16_pair(w[4], w[5]), bf16_pair(w[6], w[7])};
-            if (wt != nullptr) *reinterpret_cast<uint4*>(wt + m * c.d + k) = wv;
+        for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
+        if (lane == 0) s_before[wave] = n;
+        __syncthreads();
+        const unsigned long long here = __ballot(counted(own));
+        const int before = (s_before[0] + s_before[1]) + (s_before[2] + s_before[3]);
+        if (t0 + 4 >= c.T && threadIdx.x == 0) r.count[0] = before + __popcll(here);
+        t = t0 + wave;
+        y = __shfl(own, wave);
+        m = before + __popcll(here & ((1ull << wave) - 1));
+        if (t >= c.T) return;
+        if (lane == 0) {
+            r.pos[t] = counted(y) ? m : -1;
+            if (!counted(y)) {
+                c.loss[t] = 0.0f;
+            } else {
+                r.idx[m] = static_cast<int32_t>(t);
+                r.tgt[m] = static_cast<int32_t>(y);
+            }
         }
-        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, ww[4] = {wv.x, wv.y, wv.z, wv.w};
+        if (!counted(y)) return;
+    } else {
+        __syncthreads();
+        if (m >= r.count[0]) return;
+        t = r.idx[m];
+        y = r.tgt[m];
+    }
+    const uint16_t* x = c.X + t * c.ldx;
+    float sum = 0.0f;
+    for (int64_t k0 = 8 * lane; k0 < c.d; k0 += 2048) {
+        uint4 xv[4], wv[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            sum += __uint_as_float(xw[q] << 16) * __uint_as_float(ww[q] << 16);
-            sum += __uint_as_float(xw[q] & 0xFFFF0000u) * __uint_as_float(ww[q] & 0xFFFF0000u);
+        for (int p = 0; p < 4; ++p) {                // all loads first; past the end the last again
+            const int64_t k = min(k0 + 512 * p, c.d - 8);
+            xv[p] = *reinterpret_cast<const uint4*>(x + k);
+            if (c.codes == nullptr) {
+                wv[p] = *reinterpret_cast<const uint4*>(c.W + y * c.ldw + k);
+            } else {
+                const int64_t e = y * c.d + k, blk = e >> 6;
+                const uint32_t word = *reinterpret_cast<const uint32_t*>(c.codes + (e >> 1));
+                const float a = block_constant(c.bc.fmt, c.bc.q[blk], c.bc.scale[blk >> c.bc.gshift], c.bc.mean[0]);
+                float w[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) w[q] = s_code[(word >> (4 * q)) & 0xFu] * a;
+                wv[p] = uint4{bf16_pair(w[0], w[1]), bf16_pair(w[2], w[3]), bf16_pair(w[4], w[5]), bf16_pair(w[6], w[7])};
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const int64_t k = k0 + 512 * p;
+            if (k >= c.d) break;
+            if (wt != nullptr) *reinterpret_cast<uint4*>(wt + m * c.d + k) = wv[p];
+            const uint32_t xw[4] = {xv[p].x, xv[p].y, xv[p].z, xv[p].w}, ww[4] = {wv[p].x, wv[p].y, wv[p].z, wv[p].w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                sum += __uint_as_float(xw[q] << 16) * __uint_as_float(ww[q] << 16);
+                sum += __uint_as_float(xw[q] & 0xFFFF0000u) * __uint_as_float(ww[q] & 0xFFFF0000u);
+            }
         }
     }
 #pragma unroll
@@ -144,11 +204,14 @@ struct HeadTile {
     uint16_t* E; int64_t lde;                 // exponentials [T, lde] (gradient)
 };
 
-// 256 counted tokens x 256 rows of the piece: z in the accumulators, then the exponentials.
-template <bool kGrad>
-__global__ __launch_bounds__(kTurnThreads, 1)
+// A tile of counted tokens x rows of the piece: z in the accumulators, then the exponentials.
+// kFew: tiles of 64 x 64 (gemm_few.h), else of 256 x 256.
+template <bool kGrad, bool kFew>
+__global__ __launch_bounds__(kFew ? kFewThreads : kTurnThreads, kFew ? 2 : 1)
 void head_logits_kernel(TurnArgs g, HeadTile h, HeadRows r) {
-    __shared__ float s_top[4][BM], s_sum[4][BM];
+    constexpr int BM = kFew ? kFewTile : kTurnTile, BN = BM;
+    constexpr int kH = kFew ? 1 : 2, kI = kFew ? 2 : 4, kWn = kFew ? 2 : 4;      // halves, 16-row blocks, waves side by side
+    __shared__ float s_top[kWn][BM], s_sum[kWn][BM];
     const int count = r.count[0];
     const int tiles_m = (count + BM - 1) / BM;
     const int item = turn_item(static_cast<int>(blockIdx.x), tiles_m * h.tiles_n);
@@ -156,18 +219,25 @@ void head_logits_kernel(TurnArgs g, HeadTile h, HeadRows r) {
     int tm, tn;
     turn_tile(item, tiles_m, h.tiles_n, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
-    TurnSums acc;
-    gemm_turns<false, false>(
-        g, [&](int i) { return static_cast<uint32_t>(r.idx[min(m0 + i, count - 1)]); },
-        [&](int i) { return static_cast<uint32_t>(min(n0 + i, h.cols - 1)); }, 0, g.kt1, false, acc);
+    const auto row_p = [&](int i) { return static_cast<uint32_t>(r.idx[min(m0 + i, count - 1)]); };
+    const auto row_q = [&](int i) { return static_cast<uint32_t>(min(n0 + i, h.cols - 1)); };
+    std::conditional_t<kFew, FewSums, TurnSums> acc;
+    if constexpr (kFew) gemm_few<false, false>(g, row_p, row_q, 0, g.kt1, false, acc);
+    else gemm_turns<false, false>(g, row_p, row_q, 0, g.kt1, false, acc);
     // e = 2^((z - zt) log2 e - shift), 0 at the target and past the piece. The lane has rows 128 hh +
-    // 64 wm + 16 i + lane % 16 and of each 16 columns, base + 128 q + 16 j + e.
+    // row0 + 16 i and of each 16 columns, base + 128 q + 16 j + e.
     const int tid = threadIdx.x;
     const int lane = tid & 63, wave = tid >> 6;
-    const int wn = wave & 3;
-    const int row0 = 64 * (wave >> 2) + (lane & 15), base = 32 * wn + 4 * (lane >> 4);
+    const int wn = wave % kWn;
+    const int row0 = 16 * kI * (wave / kWn) + (lane & 15), base = 32 * wn + 4 * (lane >> 4);
     const int columns = h.cols - n0 - base;          // of the lane's, those below are in the piece
     // the tile's columns that stay out of the lane's row: its target's (none: outside 0..255)
+    auto put = [&](int row, int col, const f32x4t& v) {       // of the tile: four values of E
+        if constexpr (!kFew) turn_put<256>(row, col, v[0], v[1], v[2], v[3]);
+        else if (m0 + row < count)
+            *reinterpret_cast<uint2*>(h.E + static_cast<int64_t>(m0 + row) * h.lde + n0 + col) =
+                uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+    };
     auto target = [&](int m) { return r.tgt[m] - h.v0 - n0 - base; };
     auto keep = [&](f32x4t v, int off, int skip, float out) {
 #pragma unroll
@@ -176,9 +246,9 @@ void head_logits_kernel(TurnArgs g, HeadTile h, HeadRows r) {
         return v;
     };
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh)
+    for (int hh = 0; hh < kH; ++hh)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < kI; ++i) {
             const int ml = 128 * hh + 16 * i + row0;
             const int m = min(m0 + ml, count - 1);
             const float c = -r.zt[m] * kLog2e - r.shift[m];
@@ -187,7 +257,7 @@ void head_logits_kernel(TurnArgs g, HeadTile h, HeadRows r) {
             const bool some = __any(skip >= 0 && skip < BN) || n0 + BN > h.cols;
             float sum = 0.0f;
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+            for (int q = 0; q < kH; ++q)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     f32x4t v = acc[hh][q][i][j];
@@ -195,14 +265,17 @@ void head_logits_kernel(TurnArgs g, HeadTile h, HeadRows r) {
                     for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], kLog2e, c));
                     if (some) v = keep(v, 128 * q + 16 * j, skip, 0.0f);
                     sum += (v[0] + v[1]) + (v[2] + v[3]);
-                    if constexpr (kGrad) turn_put<256>(ml, base + 128 * q + 16 * j, v[0], v[1], v[2], v[3]);
+                    if constexpr (kGrad) put(ml, base + 128 * q + 16 * j, v);
                 }
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
             if (lane < 16) s_sum[wn][ml] = sum;
         }
     __syncthreads();
-    auto total = [&](int row) { return (s_sum[0][row] + s_sum[1][row]) + (s_sum[2][row] + s_sum[3][row]); };
+    auto total = [&](int row) {
+        const float two = s_sum[0][row] + s_sum[1][row];
+        return kFew ? two : two + (s_sum[kWn - 2][row] + s_sum[kWn - 1][row]);
+    };
     float sum = 0.0f, power = 0.0f;
     bool large = false;
     if (tid < BM && m0 + tid < count) {
@@ -218,16 +291,16 @@ void head_logits_kernel(TurnArgs g, HeadTile h, HeadRows r) {
             for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(v[e], kLog2e, c);
             return keep(v, off, skip, -__builtin_inff());
         };
-        for (int hh = 0; hh < 2; ++hh)
+        for (int hh = 0; hh < kH; ++hh)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kI; ++i) {
                 const int ml = 128 * hh + 16 * i + row0, m = min(m0 + ml, count - 1);
                 float t = -__builtin_inff();
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
+                for (int q = 0; q < kH; ++q)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const f32x4t v = relative(hh == 0 ? acc[0][q][i][j] : acc[1][q][i][j], 128 * q + 16 * j, target(m), m);
+                        const f32x4t v = relative(hh == 0 ? acc[0][q][i][j] : acc[kH - 1][q][i][j], 128 * q + 16 * j, target(m), m);
                         t = fmaxf(fmaxf(fmaxf(t, v[0]), fmaxf(v[1], v[2])), v[3]);
                     }
                 t = fmaxf(t, __shfl_xor(t, 16));
@@ -236,24 +309,24 @@ void head_logits_kernel(TurnArgs g, HeadTile h, HeadRows r) {
             }
         __syncthreads();
         auto off_of = [&](int row) {
-            const float t = fmaxf(fmaxf(s_top[0][row], s_top[1][row]), fmaxf(s_top[2][row], s_top[3][row]));
+            const float t = fmaxf(fmaxf(s_top[0][row], s_top[1][row]), fmaxf(s_top[kWn - 2][row], s_top[kWn - 1][row]));
             return t > kMaxLog2 ? ceilf(t) : 0.0f;
         };
-        for (int hh = 0; hh < 2; ++hh)
+        for (int hh = 0; hh < kH; ++hh)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kI; ++i) {
                 const int ml = 128 * hh + 16 * i + row0, m = min(m0 + ml, count - 1);
                 const float off = off_of(ml);
                 float s = 0.0f;
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
+                for (int q = 0; q < kH; ++q)
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        f32x4t v = relative(hh == 0 ? acc[0][q][i][j] : acc[1][q][i][j], 128 * q + 16 * j, target(m), m);
+                        f32x4t v = relative(hh == 0 ? acc[0][q][i][j] : acc[kH - 1][q][i][j], 128 * q + 16 * j, target(m), m);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) v[e] = __builtin_amdgcn_exp2f(v[e] - off);
                         s += (v[0] + v[1]) + (v[2] + v[3]);
-                        if constexpr (kGrad) turn_put<256>(ml, base + 128 * q + 16 * j, v[0], v[1], v[2], v[3]);
+                        if constexpr (kGrad) put(ml, base + 128 * q + 16 * j, v);
                     }
                 s += __shfl_xor(s, 16);
                 s += __shfl_xor(s, 32);
@@ -266,7 +339,7 @@ void head_logits_kernel(TurnArgs g, HeadTile h, HeadRows r) {
         }
     }
     if (tid < BM && m0 + tid < count) h.part[tn * h.T + m0 + tid] = float2{sum, power};
-    if constexpr (kGrad) {
+    if constexpr (kGrad && !kFew) {
         const int c = tid & 31;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -277,39 +350,51 @@ void head_logits_kernel(TurnArgs g, HeadTile h, HeadRows r) {
     }
 }
 
-// The gradient's product: its tiles, and the splits of their K-steps that fill `slots` workgroups
+// The gradient's float32 sums: tiles of 1 << lt, tiles_n of them across d, room for slots
+struct HeadAcc { float* acc; int lt, tiles_n, slots, kt_first; };
+
+// its product's tiles, and the splits of their K-steps that fill the slots
 struct HeadSplit { int tiles, splits, kper; };
-__device__ __forceinline__ HeadSplit head_split(int count, int tiles_n, int slots, int kt_first, int kt) {
+__device__ __forceinline__ HeadSplit head_split(const HeadAcc& a, int count, int kt) {
     HeadSplit s;
-    s.tiles = (count + BM - 1) / BM * tiles_n;
-    // at least 8 K-steps per split of the first (longest) piece, and no split of it without any
-    const int want = max(1, min(slots / max(1, s.tiles), kt_first / 8));
-    const int per = (kt_first + want - 1) / want;
-    s.splits = (kt_first + per - 1) / per;
+    s.tiles = ((count + (1 << a.lt) - 1) >> a.lt) * a.tiles_n;
+    // at least head_steps(lt) K-steps per split of the first (longest) piece, and no split of it without any
+    const int want = max(1, min(a.slots / max(1, s.tiles), a.kt_first / head_steps(a.lt)));
+    const int per = (a.kt_first + want - 1) / want;
+    s.splits = (a.kt_first + per - 1) / per;
     s.kper = (kt + s.splits - 1) / s.splits;
     return s;
 }
+// the sums of position m's row, column n, of split 0; the next split's are tiles << 2 lt further
+__device__ __forceinline__ float* head_sums(const HeadAcc& a, int m, int64_t n) {
+    const int in = (1 << a.lt) - 1;
+    const int64_t tile = static_cast<int64_t>(m >> a.lt) * a.tiles_n + (n >> a.lt);
+    return a.acc + (tile << (2 * a.lt)) + (static_cast<int64_t>(m & in) << a.lt) + (n & in);
+}
 
 // A piece's sums joined to the row's: l, and, where a tile was scaled down, the row brought to one
-// scale (its exponentials in E and the sums of earlier pieces in acc times exact powers of two).
-// 64 rows per workgroup, 4 threads a row.
+// scale (its exponentials in E and the sums of earlier pieces in acc times exact powers of two); after
+// the last piece the loss. 16 rows per workgroup, 16 threads a row (64 rows of 4 threads took 8 us of 17
+// tokens on 32000 rows, in trips to memory one after another).
 struct HeadJoin {
-    const float2* part; int tiles_n; int64_t T;
+    const float2* part; int tiles_n, lt; int64_t T;   // tiles 1 << lt wide
     uint16_t* E; int64_t lde;                 // or null
-    float* acc; int acc_tiles_n, slots, kt_first;    // acc null: no earlier piece
+    HeadAcc a;                                // acc null: no earlier piece
+    int64_t d;
+    float* loss;                              // null: more pieces follow
 };
 
 __global__ __launch_bounds__(256)
 void head_join_kernel(HeadJoin j, HeadRows r) {
-    __shared__ float s_sum[4][64], s_top[4][64], s_off[64];
+    __shared__ float s_sum[16][17], s_top[16][17], s_off[16];
     const int count = r.count[0];
-    const int m0 = static_cast<int>(blockIdx.x) * 64;
+    const int m0 = static_cast<int>(blockIdx.x) * 16;
     if (m0 >= count) return;
-    const int i = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const int i = threadIdx.x & 15, q = threadIdx.x >> 4;
     const int m = min(m0 + i, count - 1);
     float sum = 0.0f, top = 0.0f;
 #pragma unroll 8
-    for (int n = q; n < j.tiles_n; n += 4) {
+    for (int n = q; n < j.tiles_n; n += 16) {
         const float2 p = j.part[n * j.T + m];
         sum += p.x;
         top = fmaxf(top, p.y);
@@ -318,56 +403,60 @@ void head_join_kernel(HeadJoin j, HeadRows r) {
     s_top[q][i] = top;
     __syncthreads();
     if (q == 0) {
-        top = fmaxf(fmaxf(s_top[0][i], s_top[1][i]), fmaxf(s_top[2][i], s_top[3][i]));
+        sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            sum += s_sum[k][i];
+            top = fmaxf(top, s_top[k][i]);
+        }
         s_off[i] = top;
         if (m0 + i < count) {
-            float l = r.l[m];
+            float l = r.l[m], shift = r.shift[m];
             if (top == 0.0f) {
-                l += (s_sum[0][i] + s_sum[1][i]) + (s_sum[2][i] + s_sum[3][i]);
+                l += sum;
             } else {
                 l *= __builtin_amdgcn_exp2f(-top);
                 for (int n = 0; n < j.tiles_n; ++n) {
                     const float2 p = j.part[n * j.T + m];
                     l += p.x * __builtin_amdgcn_exp2f(p.y - top);
                 }
-                r.shift[m] += top;
+                shift += top;
+                r.shift[m] = shift;
             }
             r.l[m] = l;
+            // log(1 + l), where 1 = exp(z_y - z_y) is 2^-shift on the row's scale
+            if (j.loss != nullptr)
+                j.loss[r.idx[m]] = shift == 0.0f ? log1pf(l) : shift * kLn2 + logf(__builtin_amdgcn_exp2f(-shift) + l);
         }
     }
-    __syncthreads();
-    if (j.E == nullptr) return;
-    for (int k = 0; k < 64 && m0 + k < count; ++k) {
+    if (!__syncthreads_or(q == 0 && top != 0.0f) || j.E == nullptr) return;
+    for (int k = 0; k < 16 && m0 + k < count; ++k) {
         const float off = s_off[k];
         if (off == 0.0f) continue;                   // uniform
         const int row = m0 + k;
         uint16_t* e = j.E + static_cast<int64_t>(row) * j.lde;
-        for (int n = 0; n < j.tiles_n; ++n) {
-            const float f = __builtin_amdgcn_exp2f(j.part[n * j.T + row].y - off);
-            uint16_t* at = e + n * BN + threadIdx.x;
-            *at = bf16_bits(__uint_as_float(static_cast<uint32_t>(*at) << 16) * f);
+        for (int n = threadIdx.x; n < j.tiles_n << j.lt; n += 256) {
+            const float f = __builtin_amdgcn_exp2f(j.part[(n >> j.lt) * j.T + row].y - off);
+            e[n] = bf16_bits(__uint_as_float(static_cast<uint32_t>(e[n]) << 16) * f);
         }
-        if (j.acc != nullptr) {
+        if (j.a.acc != nullptr) {
             const float f = __builtin_amdgcn_exp2f(-off);
-            const HeadSplit s = head_split(count, j.acc_tiles_n, j.slots, j.kt_first, j.kt_first);
+            const HeadSplit s = head_split(j.a, count, j.a.kt_first);
             for (int sp = 0; sp < s.splits; ++sp)
-                for (int tn = 0; tn < j.acc_tiles_n; ++tn) {
-                    // the tile's place in acc, as head_grad_kernel numbers them
-                    const int64_t slot = static_cast<int64_t>(sp) * s.tiles + (row / BM) * j.acc_tiles_n + tn;
-                    j.acc[slot * (BM * BN) + (row % BM) * BN + threadIdx.x] *= f;
-                }
+                for (int64_t n = threadIdx.x; n < j.d; n += 256)
+                    head_sums(j.a, row, n)[static_cast<int64_t>(sp) * s.tiles << (2 * j.a.lt)] *= f;
         }
     }
 }
 
-// acc += E W of a piece (the first piece: =), 256 x 256 float32 tiles; tile (tm, tn) of split s is
-// slot s tiles + tm tiles_n + tn.
-struct HeadGrad { float* acc; int tiles_n, slots, kt_first, first; };
-
-__global__ __launch_bounds__(kTurnThreads, 1)
-void head_grad_kernel(TurnArgs g, HeadGrad h, int d, HeadRows r) {
+// acc += E W of a piece (the first piece: =), float32 tiles; tile (tm, tn) of split s is slot
+// s tiles + tm tiles_n + tn.
+template <bool kFew>
+__global__ __launch_bounds__(kFew ? kFewThreads : kTurnThreads, kFew ? 2 : 1)
+void head_grad_kernel(TurnArgs g, HeadAcc h, int first, int d, HeadRows r) {
+    constexpr int BM = kFew ? kFewTile : kTurnTile, BN = BM;
     const int count = r.count[0];
-    const HeadSplit s = head_split(count, h.tiles_n, h.slots, h.kt_first, g.kt1);
+    const HeadSplit s = head_split(h, count, g.kt1);
     const int item = turn_item(static_cast<int>(blockIdx.x), s.tiles * s.splits);
     if (item < 0) return;
     const int sp = item / s.tiles;
@@ -376,51 +465,41 @@ void head_grad_kernel(TurnArgs g, HeadGrad h, int d, HeadRows r) {
     int tm, tn;
     turn_tile(item % s.tiles, (count + BM - 1) / BM, h.tiles_n, tm, tn);
     const int m0 = tm * BM, n0 = tn * BN;
-    TurnSums acc;
-    gemm_turns<false, true>(
-        g, [&](int i) { return static_cast<uint32_t>(min(m0 + i, count - 1)); },
-        [&](int i) { return static_cast<uint32_t>(min(n0 + i, d - 8)); }, kb, ke, false, acc);
-    turn_put_sums(h.acc + (static_cast<int64_t>(sp) * s.tiles + tm * h.tiles_n + tn) * (BM * BN), acc, !h.first);
+    const auto row_p = [&](int i) { return static_cast<uint32_t>(min(m0 + i, count - 1)); };
+    const auto row_q = [&](int i) { return static_cast<uint32_t>(min(n0 + i, d - 8)); };
+    float* const at = h.acc + (static_cast<int64_t>(sp) * s.tiles + tm * h.tiles_n + tn) * (BM * BN);
+    std::conditional_t<kFew, FewSums, TurnSums> acc;
+    if constexpr (kFew) {
+        gemm_few<false, true>(g, row_p, row_q, kb, ke, false, acc);
+        few_put_sums(at, acc, !first);
+    } else {
+        gemm_turns<false, true>(g, row_p, row_q, kb, ke, false, acc);
+        turn_put_sums(at, acc, !first);
+    }
 }
 
-// Per token: the loss, and dX from the sums (zeros for a token that is not counted).
-struct HeadFinal {
-    const float* acc; int tiles_n, slots, kt_first;
-    const uint16_t* wt;                       // the target's row of position m at wt + m d, or null: in W
-};
-
-template <bool kGrad>
+// dX of a token from the sums (zeros for one that is not counted).
 __global__ __launch_bounds__(256)
-void head_final_kernel(HeadCall c, HeadFinal f, HeadRows r) {
-    const int64_t t = kGrad ? static_cast<int64_t>(blockIdx.x) : static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (t >= c.T) return;
+void head_final_kernel(HeadCall c, HeadAcc a, const uint16_t* wt, HeadRows r) {
+    const int64_t t = blockIdx.x;
     const int m = r.pos[t];
-    float l = 0.0f, one = 1.0f;
-    if (m >= 0) {
-        const float shift = r.shift[m];
-        l = r.l[m];
-        one = __builtin_amdgcn_exp2f(-shift);                  // exp(z_y - z_y) on the row's scale
-        if (!kGrad || threadIdx.x == 0) c.loss[t] = shift == 0.0f ? log1pf(l) : shift * kLn2 + logf(one + l);
-    } else if (!kGrad || threadIdx.x == 0) {
-        c.loss[t] = 0.0f;
+    const int count = r.count[0];
+    uint16_t* out = c.dX + t * c.lddx;
+    if (m < 0) {
+        for (int64_t n = 4 * threadIdx.x; n < c.d; n += 1024) *reinterpret_cast<uint2*>(out + n) = uint2{0u, 0u};
+        return;
     }
-    if constexpr (kGrad) {
-        uint16_t* out = c.dX + t * c.lddx;
-        const int count = r.count[0];
-        const HeadSplit s = head_split(count, f.tiles_n, f.slots, f.kt_first, f.kt_first);
-        const float k = m < 0 ? 0.0f : (c.scale != nullptr ? c.scale[t] : 1.0f) / (one + l);
-        const uint16_t* w = m < 0 ? nullptr : f.wt != nullptr ? f.wt + m * c.d : c.W + r.tgt[m] * c.ldw;
-        for (int64_t n = 4 * threadIdx.x; n < c.d; n += 1024) {
-            uint2 o = uint2{0u, 0u};
-            if (m >= 0) {
-                const float* at = f.acc + static_cast<int64_t>((m / BM) * f.tiles_n + n / BN) * (BM * BN) + (m % BM) * BN + n % BN;
-                const float4 a = ordered_sum4<4>(at, static_cast<int64_t>(s.tiles) * (BM * BN), s.splits);
-                const uint2 wv = *reinterpret_cast<const uint2*>(w + n);
-                o.x = bf16_pair(k * (a.x - l * __uint_as_float(wv.x << 16)), k * (a.y - l * __uint_as_float(wv.x & 0xFFFF0000u)));
-                o.y = bf16_pair(k * (a.z - l * __uint_as_float(wv.y << 16)), k * (a.w - l * __uint_as_float(wv.y & 0xFFFF0000u)));
-            }
-            *reinterpret_cast<uint2*>(out + n) = o;
-        }
+    const HeadSplit s = head_split(a, count, a.kt_first);
+    const float l = r.l[m];
+    const float k = (c.scale != nullptr ? c.scale[t] : 1.0f) / (__builtin_amdgcn_exp2f(-r.shift[m]) + l);
+    const uint16_t* w = wt != nullptr ? wt + m * c.d : c.W + r.tgt[m] * c.ldw;      // the target's row
+    for (int64_t n = 4 * threadIdx.x; n < c.d; n += 1024) {
+        const float4 v = ordered_sum4<4>(head_sums(a, m, n), static_cast<int64_t>(s.tiles) << (2 * a.lt), s.splits);
+        const uint2 wv = *reinterpret_cast<const uint2*>(w + n);
+        uint2 o;
+        o.x = bf16_pair(k * (v.x - l * __uint_as_float(wv.x << 16)), k * (v.y - l * __uint_as_float(wv.x & 0xFFFF0000u)));
+        o.y = bf16_pair(k * (v.z - l * __uint_as_float(wv.y << 16)), k * (v.w - l * __uint_as_float(wv.y & 0xFFFF0000u)));
+        *reinterpret_cast<uint2*>(out + n) = o;
     }
 }
 
@@ -441,8 +520,11 @@ bool head_plan(int64_t V, int64_t d, int64_t T, bool nf4, bool grad, HeadPlan* p
     p->pieces = static_cast<int>(ceil_div(V, p->piece));
     if (grad && p->piece >= kLimit / T) return false;
     if (keeps && p->piece >= kLimit / d) return false;
-    const int64_t tm = ceil_div(T, BM), tn = ceil_div(d, BN), kt = p->piece / BK;
-    p->slots = !grad ? 0 : static_cast<int>(std::max(tm * tn, std::min<int64_t>(256, tm * tn * std::max<int64_t>(1, kt / 8))));
+    p->lt = T <= kFewTokens || ceil_div(T, kTurnTile) * ceil_div(p->piece, kTurnTile) <= kFewMost ? 6 : 8;
+    const int64_t tile = int64_t{1} << p->lt;
+    const int64_t tm = ceil_div(T, tile), tn = ceil_div(d, tile), kt = p->piece / BK;
+    p->slots = !grad ? 0 : static_cast<int>(std::max(tm * tn, std::min<int64_t>(p->lt == 6 ? 512 : 256,
+                                                                                tm * tn * std::max<int64_t>(1, kt / head_steps(p->lt)))));
     int64_t off = 0;
     auto take = [&off](int64_t bytes) {
         const int64_t at = off;
@@ -450,11 +532,11 @@ bool head_plan(int64_t V, int64_t d, int64_t T, bool nf4, bool grad, HeadPlan* p
         return at;
     };
     p->ints = take(4 * head_int_count(T));
-    p->part = take(8 * (p->piece / BN) * T);
+    p->part = take(8 * (p->piece >> p->lt) * T);
     p->E = take(grad ? 2 * T * p->piece : 0);
     p->rows = take(nf4 ? 2 * d * p->piece : 0);
     p->wt = take(nf4 && grad ? 2 * T * d : 0);
-    p->acc = take(static_cast<int64_t>(p->slots) * BM * BN * 4);
+    p->acc = take((static_cast<int64_t>(p->slots) << (2 * p->lt)) * 4);
     p->bytes = off;
     return true;
 }
@@ -467,11 +549,16 @@ hipError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, char* ws, hipS
     uint16_t* rows = nf4 ? reinterpret_cast<uint16_t*>(ws + p.rows) : nullptr;
     uint16_t* wt = nf4 && grad ? reinterpret_cast<uint16_t*>(ws + p.wt) : nullptr;
     float* acc = grad ? reinterpret_cast<float*>(ws + p.acc) : nullptr;
-    const int tm = static_cast<int>(ceil_div(c.T, BM));
-    const int kt_first = static_cast<int>(ceil_div(std::min(p.piece, c.V), BK));
-    QN_LAUNCH("head_plan_kernel", st, head_plan_kernel, dim3(1), dim3(1024), 0, st, c.target, c.T, c.V, r);
+    const bool few = p.lt == 6;
+    const int64_t tile = int64_t{1} << p.lt;
+    const int tm = static_cast<int>(ceil_div(c.T, tile));
+    const dim3 threads(few ? kFewThreads : kTurnThreads);
+    const HeadAcc sums{acc, p.lt, static_cast<int>(ceil_div(c.d, tile)), p.slots,
+                       static_cast<int>(ceil_div(std::min(p.piece, c.V), BK))};
+    const bool planned = c.T > kPlanFrom;
+    if (planned) QN_LAUNCH("head_plan_kernel", st, head_plan_kernel, dim3(1), dim3(1024), 0, st, c.target, c.T, c.V, c.loss, r);
     QN_LAUNCH("head_target_kernel", st, head_target_kernel, dim3(static_cast<unsigned>(ceil_div(c.T, 4))), dim3(256), 0, st,
-              c, r, wt, tables());
+              c, r, wt, planned ? 1 : 0, tables());
     hipError_t e = hipGetLastError();
     for (int i = 0; i < p.pieces && e == hipSuccess; ++i) {
         const int64_t v0 = i * p.piece, cols = std::min(p.piece, c.V - v0);
@@ -483,31 +570,31 @@ hipError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, char* ws, hipS
             const int64_t blk = v0 * c.d / kBlock;
             bc.q += bc.fmt == kDqNone ? 0 : blk;
             bc.scale += blk >> bc.gshift;
-            if ((e = launch_dequant_rows(c.codes + v0 * c.d / 2, bc, cols * c.d, rows, st)) != hipSuccess) return e;
+            if ((e = launch_dequant_weight(c.codes + v0 * c.d / 2, bc, cols, c.d, rows, st)) != hipSuccess) return e;
         }
-        const int tn = static_cast<int>(ceil_div(cols, BN));
+        const int tn = static_cast<int>(ceil_div(cols, tile));
         const TurnArgs g = turn_args(c.X, c.ldx, c.T, W, ldw, cols, c.d);
         const HeadTile h{static_cast<int>(v0), static_cast<int>(cols), tn, c.T, part, E, p.piece};
         const dim3 lgrid(static_cast<unsigned>(ceil_div(tm * tn, 8) * 8));
-        if (grad) QN_LAUNCH("head_logits_kernel", st, head_logits_kernel<true>, lgrid, dim3(kTurnThreads), 0, st, g, h, r);
-        else QN_LAUNCH("head_logits_kernel", st, head_logits_kernel<false>, lgrid, dim3(kTurnThreads), 0, st, g, h, r);
-        const int dn = static_cast<int>(ceil_div(c.d, BN));
-        const HeadJoin j{part, tn, c.T, E, p.piece, i > 0 ? acc : nullptr, dn, p.slots, kt_first};
-        QN_LAUNCH("head_join_kernel", st, head_join_kernel, dim3(static_cast<unsigned>(ceil_div(c.T, 64))), dim3(256), 0, st,
+        if (grad && few) QN_LAUNCH("head_logits_kernel", st, (head_logits_kernel<true, true>), lgrid, threads, 0, st, g, h, r);
+        else if (grad) QN_LAUNCH("head_logits_kernel", st, (head_logits_kernel<true, false>), lgrid, threads, 0, st, g, h, r);
+        else if (few) QN_LAUNCH("head_logits_kernel", st, (head_logits_kernel<false, true>), lgrid, threads, 0, st, g, h, r);
+        else QN_LAUNCH("head_logits_kernel", st, (head_logits_kernel<false, false>), lgrid, threads, 0, st, g, h, r);
+        HeadJoin j{part, tn, p.lt, c.T, E, p.piece, sums, c.d, i == p.pieces - 1 ? c.loss : nullptr};
+        if (i == 0) j.a.acc = nullptr;
+        QN_LAUNCH("head_join_kernel", st, head_join_kernel, dim3(static_cast<unsigned>(ceil_div(c.T, 16))), dim3(256), 0, st,
                   j, r);
         if (grad) {
             const TurnArgs q = turn_args(E, p.piece, c.T, W, ldw, cols, ceil_div(cols, BK) * BK);
-            const HeadGrad hg{acc, dn, p.slots, kt_first, i == 0};
-            QN_LAUNCH("head_grad_kernel", st, head_grad_kernel, dim3(static_cast<unsigned>(ceil_div(p.slots, 8) * 8)),
-                      dim3(kTurnThreads), 0, st, q, hg, static_cast<int>(c.d), r);
+            const dim3 ggrid(static_cast<unsigned>(ceil_div(p.slots, 8) * 8));
+            const int first = i == 0, d = static_cast<int>(c.d);
+            if (few) QN_LAUNCH("head_grad_kernel", st, head_grad_kernel<true>, ggrid, threads, 0, st, q, sums, first, d, r);
+            else QN_LAUNCH("head_grad_kernel", st, head_grad_kernel<false>, ggrid, threads, 0, st, q, sums, first, d, r);
         }
         e = hipGetLastError();
     }
     if (e != hipSuccess) return e;
-    const HeadFinal f{acc, static_cast<int>(ceil_div(c.d, BN)), p.slots, kt_first, wt};
-    if (grad) QN_LAUNCH("head_final_kernel", st, head_final_kernel<true>, dim3(static_cast<unsigned>(c.T)), dim3(256), 0, st, c, f, r);
-    else QN_LAUNCH("head_final_kernel", st, head_final_kernel<false>, dim3(static_cast<unsigned>(ceil_div(c.T, 256))), dim3(256),
-                   0, st, c, f, r);
+    if (grad) QN_LAUNCH("head_final_kernel", st, head_final_kernel, dim3(static_cast<unsigned>(c.T)), dim3(256), 0, st, c, sums, wt, r);
     return hipGetLastError();
 }
 

@@ -417,6 +417,15 @@ __device__ __forceinline__ void dequant_jobs(const DeqJob& a, int bd, const NF4T
     }
 }
 
+// A weight's dequantisation alone, row-major (a piece of the loss's NF4 head). Bound by its writes:
+// 32000 rows of 4096 took 105 us with a thread per 8 weights.
+__global__ __launch_bounds__(256)
+void dequant_weight_kernel(DeqJob a, NF4Tables tab) {
+    __shared__ float s_code[16], s_ahat[kDeqPerWG / 64];
+    if (threadIdx.x < 16) s_code[threadIdx.x] = tab.code[threadIdx.x];
+    dequant_rows_job(a, static_cast<int>(blockIdx.x), s_code, s_ahat);
+}
+
 // KM0, KM1: whether pre-pass job 0 / 1 takes its R k-major
 template <int NT, bool KM0, bool KM1>
 __global__ __launch_bounds__(256)
@@ -993,6 +1002,13 @@ hipError_t launch_prologue(const uint8_t* codes, const BlockConsts& bc, int64_t 
     a.deq = make_dequant(codes, bc, d_out, d_in, transposed, what);
     static_assert(64 + 1024 + 64 * kTP * sizeof(uint16_t) <= sizeof(PreStage<1>::x), "dequant scratch fits a stage");
     return launch_prologue_args(a, r_kmajor, false, st);
+}
+
+hipError_t launch_dequant_weight(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, int64_t d_in, uint16_t* what,
+                                 hipStream_t st) {
+    const DeqJob a = make_dequant(codes, bc, d_out, d_in, false, what);
+    QN_LAUNCH("dequant_weight_kernel", st, dequant_weight_kernel, dim3(static_cast<unsigned>(a.n)), dim3(256), 0, st, a, tables());
+    return hipGetLastError();
 }
 
 hipError_t launch_prepass_pair(const uint16_t* P0, int64_t ldp0, int64_t K0, const uint16_t* R0, int64_t ldr0,

@@ -18,7 +18,8 @@ F, B8 = 2.0 ** -24, 2.0 ** -8
 # vocabulary, width, tokens, share without a target, head
 CASES = [(1, 64, 1, 0.0, "bf16"), (2, 64, 3, 0.0, "bf16"), (257, 64, 5, 0.0, "bf16"), (1001, 256, 203, 0.3, "bf16"),
          (64, 128, 70, 0.0, "int8"), (4160, 320, 300, 0.5, "fp8"), (20000, 128, 65, 0.0, "bf16"), (33000, 192, 513, 0.2, "bf16"),
-         (16448, 128, 257, 0.1, "none"), (50001, 64, 17, 0.0, "bf16"), (40000, 1088, 1, 0.0, "bf16"), (512, 64, 1025, 0.97, "bf16")]
+         (16448, 128, 257, 0.1, "none"), (50001, 64, 17, 0.0, "bf16"), (40000, 1088, 1, 0.0, "bf16"), (512, 64, 1025, 0.97, "bf16"),
+         (300, 64, 9001, 0.4, "bf16"), (33000, 64, 100, 0.2, "bf16"), (33024, 128, 128, 0.1, "int8"), (32000, 64, 300, 0.0, "int8")]
 IDS = ["x".join(map(str, c)) for c in CASES]
 
 
@@ -107,8 +108,9 @@ def test_logits_far_above_the_target(V, m, gain):
     check(full, X, t, scale, qn.head_loss(own, X, t), None)
 
 
-def test_a_later_piece_far_above_the_earlier_ones():
-    V, d, m = 33000, 64, 270
+@pytest.mark.parametrize("m", [101, 270])
+def test_a_later_piece_far_above_the_earlier_ones(m):
+    V, d = 33000, 64
     own, full, X, t, scale = make(V, d, m)
     own[20000:20003] = (X[:3].float() * 8).bfloat16()          # huge logits for some tokens, late in the vocabulary
     own[32999] = (X[100].float() * 16).bfloat16()
@@ -127,8 +129,9 @@ def test_no_token_counted():
     assert (qn.head_loss(own, X, t) == 0).all()
 
 
-def test_infinities_stay_with_their_token():
-    own, _, X, t, scale = make(3001, 128, 300)
+@pytest.mark.parametrize("V", [3001, 20001])
+def test_infinities_stay_with_their_token(V):
+    own, _, X, t, scale = make(V, 128, 300)
     loss, dX = qn.head_loss_grad(own, X, t, scale=scale)
     bad = X.clone()
     bad[5, 1], bad[128, 2], bad[299, 3] = float("inf"), float("nan"), float("-inf")
