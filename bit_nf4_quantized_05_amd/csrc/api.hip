@@ -1122,6 +1122,8 @@ int qlora_gated_bwd(const uint8_t* codes_g, const int8_t* qconst_g, const float*
     o.what = reinterpret_cast<uint16_t*>(ws + w.what);
     o.adapt = reinterpret_cast<uint16_t*>(ws + w.adapt);
     o.grad = qn::GatedGradArgs{dH, lddh, GU, ldgu, dGU, lddgu, static_cast<int>(d_seq), static_cast<int>(d_ff), act};
+    if (r > 0 && !qn::prepass_takes_kmajor(r))
+        for (int i = 0; i < 2; ++i) o.bt[i] = reinterpret_cast<uint16_t*>(ws + w.bt[i]);
     hipError_t e = qn::launch_gated_prologue(c, true, o, st);
     if (e != hipSuccess) return hip_fail(e, "qlora_gated_bwd (prologue)");
     uint16_t* t = nullptr;
@@ -1131,11 +1133,7 @@ int qlora_gated_bwd(const uint8_t* codes_g, const int8_t* qconst_g, const float*
         p.pre_in = dGU; p.ld_in = lddgu;
         for (int i = 0; i < 2; ++i) {
             p.ppart[i] = reinterpret_cast<float*>(ws + w.ppart[i]);
-            if (qn::prepass_takes_kmajor(r)) continue;
-            uint16_t* bt = reinterpret_cast<uint16_t*>(ws + w.bt[i]);
-            if ((e = qn::launch_transpose_pad(c.B[i], d_ff, r, bt, d_ff, st)) != hipSuccess)
-                return hip_fail(e, "qlora_gated_bwd (transpose)");
-            p.bt[i] = bt;
+            p.bt[i] = o.bt[i];
         }
         if ((e = qn::launch_gated_prologue(c, true, p, st)) != hipSuccess) return hip_fail(e, "qlora_gated_bwd (pre-pass)");
     }

@@ -111,15 +111,16 @@ __device__ __forceinline__ void gated_grad_job(const GatedGradArgs& a, int b) {
 }
 
 // ---- prologue.hip ----
-// The layouts (what not null): both weights dequantised to what (forward: gate above up, [2 d_ff,
-// d_in]; gradient: transposed, side by side, [d_in, 2 d_ff]), both adapters to
-// adapt ([2 d_ff, k2] or [d_in, k2]) and, in the gradient, the elementwise part grad. And (pre_out
-// not null, r > 0) the rank products of pre_in: pre_out [M, k2] = s_w pre_in R_w^T, R = A of X or
-// B of the halves of dGU; bt: B^T [r, d_ff] where the pre-pass cannot read B itself.
+// The layouts (what not null): both weights dequantised to what, gate above up, [2 d_ff, d_in];
+// both adapters to adapt (forward B, [2 d_ff, k2]; gradient A, [k2, d_in]); in the gradient also the
+// elementwise part grad and, where the pre-pass cannot read B itself, B^T [r, d_ff] to bt. And (pre_out
+// not null, r > 0) the rank products of pre_in: pre_out [M, k2] = s_w pre_in R_w^T, R = A of X or B of
+// the halves of dGU; rows of up to kGatedOneSlice are not cut (their partials' sum is a launch more).
+constexpr int64_t kGatedOneSlice = 512;
 struct GatedProlog {
     uint16_t* what; uint16_t* adapt;
     const uint16_t* pre_in; int64_t ld_in; uint16_t* pre_out; float* ppart[2];
-    const uint16_t* bt[2];
+    uint16_t* bt[2];
     GatedGradArgs grad;
 };
 hipError_t launch_gated_prologue(const GatedCall& c, bool backward, const GatedProlog& o, hipStream_t st);
@@ -135,7 +136,7 @@ int64_t gated_part_floats(int64_t M, int64_t d_ff, int64_t d_in);
 hipError_t launch_gated_gemm(const GatedCall& c, const uint16_t* X, int64_t ldx, const uint16_t* what, const uint16_t* t,
                              const uint16_t* adapt, uint16_t* H, int64_t ldh, uint16_t* GU, int64_t ldgu, float* part,
                              hipStream_t st);
-// dX from dGU, what [d_in, 2 d_ff], t [M, k2] and adapt [d_in, k2]; part: gated_dx_part_floats
+// dX from dGU, what [2 d_ff, d_in], t [M, k2] and adapt [k2, d_in]; part: gated_dx_part_floats
 int64_t gated_dx_part_floats(int64_t M, int64_t d_ff, int64_t d_in);
 hipError_t launch_gated_dx(const GatedCall& c, const uint16_t* dGU, int64_t lddgu, const uint16_t* what, const uint16_t* t,
                            const uint16_t* adapt, uint16_t* dX, int64_t lddx, float* part, hipStream_t st);

@@ -11,9 +11,11 @@
 #include <hip/hip_runtime.h>
 
 #include "gated.h"
+#include "gemm_few.h"
 #include "gemm_turns.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace qn {
 namespace {
@@ -36,6 +38,19 @@ __device__ __forceinline__ void store_rows(uint16_t* C, int64_t ldc, int m0, int
         const uint4 v = turn_get<256>(row, c);
         if (m0 + row < M && n < limit) *reinterpret_cast<uint4*>(C + static_cast<int64_t>(m0 + row) * ldc + n) = v;
     }
+}
+
+// 4 outputs n .. n + 3 of token m from their G and U
+template <bool kKeep>
+__device__ __forceinline__ void gated_store(const GatedOut& o, int m, int n, const f32x4t& g, const f32x4t& u) {
+    if constexpr (kKeep) {
+        uint16_t* at = o.GU + static_cast<int64_t>(m) * o.ldgu + n;
+        *reinterpret_cast<uint2*>(at) = uint2{bf16_pair(g[0], g[1]), bf16_pair(g[2], g[3])};
+        *reinterpret_cast<uint2*>(at + o.d_ff) = uint2{bf16_pair(u[0], u[1]), bf16_pair(u[2], u[3])};
+    }
+    *reinterpret_cast<uint2*>(o.H + static_cast<int64_t>(m) * o.ldh + n) =
+        uint2{bf16_pair(gated_act(o.act, g[0]) * u[0], gated_act(o.act, g[1]) * u[1]),
+              bf16_pair(gated_act(o.act, g[2]) * u[2], gated_act(o.act, g[3]) * u[3])};
 }
 
 template <bool kKeep>
@@ -97,94 +112,155 @@ void gated_gemm_kernel(TurnArgs g, TurnSplit s, GatedOut o) {
     }
 }
 
-// Split tiles: G and U summed over the shares in order, then the activation and the product;
-// 4 outputs per thread, 32 workgroups per tile (8 rows each).
-__global__ __launch_bounds__(256)
-void gated_split_reduce(TurnSplit s, GatedOut o) {
-    const int j = static_cast<int>(blockIdx.x) / 32;
-    const int ml = (static_cast<int>(blockIdx.x) % 32) * 8 + (threadIdx.x >> 5);
-    const int q = (threadIdx.x & 31) * 4;                             // output column of the tile
-    int tm, tn;
-    turn_tile(s.full + j, s.tiles_m, s.tiles_n, tm, tn);
-    const int m = tm * kTurnTile + ml, n = tn * (kTurnTile / 2) + q;
-    if (m >= o.M || n >= o.d_ff) return;
-    const float* p = o.part + static_cast<int64_t>(j) * (kTurnTile * kTurnTile) + ml * kTurnTile + q;
-    const int64_t stride = static_cast<int64_t>(s.rem) * (kTurnTile * kTurnTile);
-    const float4 g = ordered_sum4<4>(p, stride, s.splits), u = ordered_sum4<4>(p + 128, stride, s.splits);
-    if (o.GU != nullptr) {
-        uint16_t* at = o.GU + static_cast<int64_t>(m) * o.ldgu + n;
-        *reinterpret_cast<uint2*>(at) = uint2{bf16_pair(g.x, g.y), bf16_pair(g.z, g.w)};
-        *reinterpret_cast<uint2*>(at + o.d_ff) = uint2{bf16_pair(u.x, u.y), bf16_pair(u.z, u.w)};
+// The same on tiles of 64 tokens x 32 outputs (gemm_few.h): of every 32 columns of the tile the first
+// 16 are gate rows, the others the up rows of the same outputs, so that a lane has both.
+template <bool kKeep>
+__global__ __launch_bounds__(kFewThreads, 2)
+void gated_few_gemm_kernel(TurnArgs g, TurnSplit s, GatedOut o) {
+    const TurnPlace p = turn_place(s, static_cast<int>(blockIdx.x), g.kt1);
+    if (p.tile < 0) return;
+    const int m0 = p.tm * kFewTile, h0 = p.tn * (kFewTile / 2);
+    FewSums acc;
+    gemm_few<true, false>(
+        g, [&](int r) { return static_cast<uint32_t>(min(m0 + r, o.M - 1)); },
+        [&](int r) { return static_cast<uint32_t>((r & 16 ? o.d_ff : 0) + h0 + 16 * (r >> 5) + (r & 15)); }, p.kb, p.ke,
+        p.share < 0 || p.share == s.splits - 1, acc);
+    if (p.share >= 0) {
+        few_put_sums(o.part + (static_cast<int64_t>(p.share) * s.rem + p.tile) * (kFewTile * kFewTile), acc, false);
+        return;
     }
-    *reinterpret_cast<uint2*>(o.H + static_cast<int64_t>(m) * o.ldh + n) =
-        uint2{bf16_pair(gated_act(o.act, g.x) * u.x, gated_act(o.act, g.y) * u.y),
-              bf16_pair(gated_act(o.act, g.z) * u.z, gated_act(o.act, g.w) * u.w)};
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int n = h0 + 16 * (wave & 1) + 4 * (lane >> 4);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int m = m0 + 32 * (wave >> 1) + 16 * i + (lane & 15);
+        if (m < o.M) gated_store<kKeep>(o, m, n, acc[0][0][i][0], acc[0][0][i][1]);
+    }
 }
 
-// dX = dGU [W_g; W_u] + U' A: a plain product, bf16 out
+// Split tiles: G and U summed over the shares in order, then the activation and the product;
+// 4 outputs per thread, 2^(2 lt - 3) threads per tile.
+__global__ __launch_bounds__(256)
+void gated_split_reduce(TurnSplit s, GatedOut o) {
+    const int at = static_cast<int>(blockIdx.x) * 256 + threadIdx.x;
+    const int j = at >> (2 * s.lt - 3), in = at & ((1 << (2 * s.lt - 3)) - 1);
+    const int ml = in >> (s.lt - 3), q = (in & ((1 << (s.lt - 3)) - 1)) * 4;      // row and output of the tile
+    int tm, tn;
+    turn_tile(s.full + j, s.tiles_m, s.tiles_n, tm, tn);
+    const int m = (tm << s.lt) + ml, n = (tn << (s.lt - 1)) + q;
+    if (m >= o.M || n >= o.d_ff) return;
+    const bool few = s.lt == 6;
+    const float* p = o.part + (static_cast<int64_t>(j) << (2 * s.lt)) + (ml << s.lt) + (few ? 32 * (q >> 4) + (q & 15) : q);
+    const int64_t stride = static_cast<int64_t>(s.rem) << (2 * s.lt);
+    const float4 g = ordered_sum4<4>(p, stride, s.splits), u = ordered_sum4<4>(p + (few ? 16 : 128), stride, s.splits);
+    const f32x4t gv = {g.x, g.y, g.z, g.w}, uv = {u.x, u.y, u.z, u.w};
+    if (o.GU != nullptr) gated_store<true>(o, m, n, gv, uv);
+    else gated_store<false>(o, m, n, gv, uv);
+}
+
+// dX = dGU [W_g; W_u] + U' [A_g; A_u]: a plain product whose weights lie with their rows along K
+// (read by transposing LDS reads), bf16 out
 struct GatedDx {
     uint16_t* C; int64_t ldc;
     int M, N;
     float* part;
 };
 
-__global__ __launch_bounds__(kTurnThreads, 1)
+template <bool kFew>
+__global__ __launch_bounds__(kFew ? kFewThreads : kTurnThreads, kFew ? 2 : 1)
 void gated_dx_kernel(TurnArgs g, TurnSplit s, GatedDx o) {
+    constexpr int kTile = kFew ? kFewTile : kTurnTile;
     const TurnPlace p = turn_place(s, static_cast<int>(blockIdx.x), g.kt1);
     if (p.tile < 0) return;
-    const int m0 = p.tm * kTurnTile, n0 = p.tn * kTurnTile;
-    TurnSums acc;
-    gemm_turns<true, false>(
-        g, [&](int r) { return static_cast<uint32_t>(min(m0 + r, o.M - 1)); },
-        [&](int r) { return static_cast<uint32_t>(min(n0 + r, o.N - 1)); }, p.kb, p.ke,
-        p.share < 0 || p.share == s.splits - 1, acc);
-    if (p.share >= 0) {
-        turn_put_sums(o.part + (static_cast<int64_t>(p.share) * s.rem + p.tile) * (kTurnTile * kTurnTile), acc, false);
-        return;
-    }
+    const int m0 = p.tm * kTile, n0 = p.tn * kTile;
+    const int last_p = o.M - 1, last_q = o.N - 8;
+    const auto row_p = [=](int r) { return static_cast<uint32_t>(min(m0 + r, last_p)); };
+    const auto col_q = [=](int r) { return static_cast<uint32_t>(min(n0 + r, last_q)); };
+    const bool rank = p.share < 0 || p.share == s.splits - 1;
+    float* const piece = o.part + (static_cast<int64_t>(p.share) * s.rem + p.tile) * (kTile * kTile);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int row0 = 64 * (wave >> 2) + (lane & 15), col0 = 32 * (wave & 3) + 4 * (lane >> 4);
+    std::conditional_t<kFew, FewSums, TurnSums> acc;
+    if constexpr (kFew) {
+        gemm_few<true, true>(g, row_p, col_q, p.kb, p.ke, rank, acc);
+        if (p.share >= 0) {
+            few_put_sums(piece, acc, false);
+            return;
+        }
+        const int n = n0 + 32 * (wave & 1) + 4 * (lane >> 4);
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+        for (int i = 0; i < 2; ++i) {
+            const int m = m0 + 32 * (wave >> 1) + 16 * i + (lane & 15);
+            if (m >= o.M) continue;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < 2; ++j) {             // N % 64 == 0: whole tiles
+                const f32x4t v = acc[0][0][i][j];
+                *reinterpret_cast<uint2*>(o.C + static_cast<int64_t>(m) * o.ldc + n + 16 * j) =
+                    uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+            }
+        }
+    } else {
+        gemm_turns<true, true>(g, row_p, col_q, p.kb, p.ke, rank, acc);
+        if (p.share >= 0) {
+            turn_put_sums(piece, acc, false);
+            return;
+        }
+        const int row0 = 64 * (wave >> 2) + (lane & 15), col0 = 32 * (wave & 3) + 4 * (lane >> 4);
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const f32x4t v = acc[h][q][i][j];
-                    turn_put<256>(128 * h + 16 * i + row0, 128 * q + 16 * j + col0, v[0], v[1], v[2], v[3]);
-                }
-    __syncthreads();
-    store_rows(o.C, o.ldc, m0, o.M, o.N, [&](int c) { return n0 + 8 * c; });
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const f32x4t v = acc[h][q][i][j];
+                        turn_put<256>(128 * h + 16 * i + row0, 128 * q + 16 * j + col0, v[0], v[1], v[2], v[3]);
+                    }
+        __syncthreads();
+        store_rows(o.C, o.ldc, m0, o.M, o.N, [&](int c) { return n0 + 8 * c; });
+    }
 }
 
-// Split tiles: the shares' sums in order; 4 outputs per thread, 64 workgroups per tile
+// Split tiles: the shares' sums in order; 4 outputs per thread, 2^(2 lt - 2) threads per tile
 __global__ __launch_bounds__(256)
 void gated_dx_reduce(TurnSplit s, GatedDx o) {
-    const int j = static_cast<int>(blockIdx.x) / 64;
-    const int ml = (static_cast<int>(blockIdx.x) % 64) * 4 + (threadIdx.x >> 6);
-    const int nl = (threadIdx.x & 63) * 4;
+    const int at = static_cast<int>(blockIdx.x) * 256 + threadIdx.x;
+    const int j = at >> (2 * s.lt - 2), in = at & ((1 << (2 * s.lt - 2)) - 1);
+    const int ml = in >> (s.lt - 2), nl = (in & ((1 << (s.lt - 2)) - 1)) * 4;
     int tm, tn;
     turn_tile(s.full + j, s.tiles_m, s.tiles_n, tm, tn);
-    const int m = tm * kTurnTile + ml, n = tn * kTurnTile + nl;
+    const int m = (tm << s.lt) + ml, n = (tn << s.lt) + nl;
     if (m >= o.M || n >= o.N) return;
-    const float* p = o.part + static_cast<int64_t>(j) * (kTurnTile * kTurnTile) + ml * kTurnTile + nl;
-    const float4 t = ordered_sum4<4>(p, static_cast<int64_t>(s.rem) * (kTurnTile * kTurnTile), s.splits);
+    const float* p = o.part + (static_cast<int64_t>(j) << (2 * s.lt)) + (ml << s.lt) + nl;
+    const float4 t = ordered_sum4<4>(p, static_cast<int64_t>(s.rem) << (2 * s.lt), s.splits);
     *reinterpret_cast<uint2*>(o.C + static_cast<int64_t>(m) * o.ldc + n) = uint2{bf16_pair(t.x, t.y), bf16_pair(t.z, t.w)};
 }
 
-TurnSplit fwd_split(int64_t M, int64_t d_ff, int64_t d_in) {
-    return turn_split(M, (d_ff + kTurnTile / 2 - 1) / (kTurnTile / 2), d_in / kTurnK);
-}
-TurnSplit dx_split(int64_t M, int64_t d_ff, int64_t d_in) {
-    return turn_split(M, (d_in + kTurnTile - 1) / kTurnTile, 2 * d_ff / kTurnK);
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Tiles of 64 or of 256, by the number of 256-wide tiles. Forward, up to 96 (with tiles of 64 and of
+// 256: 203 tokens of the 512 x 256 block 15 and 20 us, 256 of 11008 x 4096, 86 tiles, 112 and 120; 70 of
+// 28672 x 8192, 224 tiles, 502 and 469). The gradient's sums are long and its tiles few, and shares of
+// them fill the chip: up to 64 tiles and 128 K-steps (128 tokens of 4096 x 4096 55 and 59; of 11008 x
+// 4096, 344 steps, 116 and 110; 256 of 5504 x 2048, 172 steps, 60 and 56).
+bool fwd_few(int64_t M, int64_t d_ff) { return ceil_div(M, kTurnTile) * ceil_div(2 * d_ff, kTurnTile) <= 96; }
+bool dx_few(int64_t M, int64_t d_ff, int64_t d_in) {
+    return ceil_div(M, kTurnTile) * ceil_div(d_in, kTurnTile) <= 64 && 2 * d_ff / kTurnK <= 128;
 }
 
-// P2 Q2^T of a call with adapters
-void add_ranks(TurnArgs& g, const uint16_t* t, const uint16_t* adapt, int k2, int64_t M, int64_t N) {
+TurnSplit fwd_split(int64_t M, int64_t d_ff, int64_t d_in) {
+    return fwd_few(M, d_ff) ? few_split(M, d_ff / (kFewTile / 2), d_in / kTurnK)
+                            : turn_split(M, ceil_div(d_ff, kTurnTile / 2), d_in / kTurnK);
+}
+TurnSplit dx_split(int64_t M, int64_t d_ff, int64_t d_in) {
+    return dx_few(M, d_ff, d_in) ? few_split(M, d_in / kFewTile, 2 * d_ff / kTurnK)
+                                 : turn_split(M, ceil_div(d_in, kTurnTile), 2 * d_ff / kTurnK);
+}
+
+// P2 Q2^T of a call with adapters: adapt's rows are ldq2 long
+void add_ranks(TurnArgs& g, const uint16_t* t, const uint16_t* adapt, int k2, int64_t ldq2, int64_t M, int64_t N) {
     if (k2 == 0) return;
-    g.P2 = t; g.ldp2 = k2; g.Q2 = adapt; g.ldq2 = k2;
+    g.P2 = t; g.ldp2 = k2; g.Q2 = adapt; g.ldq2 = ldq2;
     g.bytesP2 = static_cast<uint32_t>(2 * static_cast<int64_t>(k2) * M);
     g.bytesQ2 = static_cast<uint32_t>(2 * static_cast<int64_t>(k2) * N);
     g.kt2 = k2 / kTurnK;
@@ -199,25 +275,30 @@ hipError_t launch_gated_gemm(const GatedCall& c, const uint16_t* X, int64_t ldx,
                              const uint16_t* adapt, uint16_t* H, int64_t ldh, uint16_t* GU, int64_t ldgu, float* part,
                              hipStream_t st) {
     TurnArgs g = turn_args(X, ldx, c.M, what, c.d_in, 2 * c.d_ff, c.d_in);
-    add_ranks(g, t, adapt, gated_k2(c.r), c.M, 2 * c.d_ff);
+    add_ranks(g, t, adapt, gated_k2(c.r), gated_k2(c.r), c.M, 2 * c.d_ff);
     const TurnSplit s = fwd_split(c.M, c.d_ff, c.d_in);
     const GatedOut o{H, ldh, GU, ldgu, static_cast<int>(c.M), static_cast<int>(c.d_ff), c.act, part};
     const dim3 grid(turn_split_grid(s));
-    if (GU != nullptr) QN_LAUNCH("gated_gemm_kernel", st, gated_gemm_kernel<true>, grid, dim3(kTurnThreads), 0, st, g, s, o);
+    const bool few = s.lt == 6;
+    if (few && GU != nullptr) QN_LAUNCH("gated_few_gemm_kernel", st, gated_few_gemm_kernel<true>, grid, dim3(kFewThreads), 0, st, g, s, o);
+    else if (few) QN_LAUNCH("gated_few_gemm_kernel", st, gated_few_gemm_kernel<false>, grid, dim3(kFewThreads), 0, st, g, s, o);
+    else if (GU != nullptr) QN_LAUNCH("gated_gemm_kernel", st, gated_gemm_kernel<true>, grid, dim3(kTurnThreads), 0, st, g, s, o);
     else QN_LAUNCH("gated_gemm_kernel", st, gated_gemm_kernel<false>, grid, dim3(kTurnThreads), 0, st, g, s, o);
-    const dim3 rgrid(static_cast<unsigned>(s.rem * 32));
+    const dim3 rgrid(static_cast<unsigned>((s.rem << (2 * s.lt - 3)) / 256));
     if (s.splits > 1) QN_LAUNCH("gated_split_reduce", st, gated_split_reduce, rgrid, dim3(256), 0, st, s, o);
     return hipGetLastError();
 }
 
 hipError_t launch_gated_dx(const GatedCall& c, const uint16_t* dGU, int64_t lddgu, const uint16_t* what, const uint16_t* t,
                            const uint16_t* adapt, uint16_t* dX, int64_t lddx, float* part, hipStream_t st) {
-    TurnArgs g = turn_args(dGU, lddgu, c.M, what, 2 * c.d_ff, c.d_in, 2 * c.d_ff);
-    add_ranks(g, t, adapt, gated_k2(c.r), c.M, c.d_in);
+    TurnArgs g = turn_args(dGU, lddgu, c.M, what, c.d_in, 2 * c.d_ff, 2 * c.d_ff);
+    add_ranks(g, t, adapt, gated_k2(c.r), c.d_in, c.M, c.d_in);
     const TurnSplit s = dx_split(c.M, c.d_ff, c.d_in);
     const GatedDx o{dX, lddx, static_cast<int>(c.M), static_cast<int>(c.d_in), part};
-    QN_LAUNCH("gated_dx_kernel", st, gated_dx_kernel, dim3(turn_split_grid(s)), dim3(kTurnThreads), 0, st, g, s, o);
-    const dim3 rgrid(static_cast<unsigned>(s.rem * 64));
+    const dim3 grid(turn_split_grid(s));
+    if (s.lt == 6) QN_LAUNCH("gated_dx_kernel", st, gated_dx_kernel<true>, grid, dim3(kFewThreads), 0, st, g, s, o);
+    else QN_LAUNCH("gated_dx_kernel", st, gated_dx_kernel<false>, grid, dim3(kTurnThreads), 0, st, g, s, o);
+    const dim3 rgrid(static_cast<unsigned>((s.rem << (2 * s.lt - 2)) / 256));
     if (s.splits > 1) QN_LAUNCH("gated_dx_reduce", st, gated_dx_reduce, rgrid, dim3(256), 0, st, s, o);
     return hipGetLastError();
 }

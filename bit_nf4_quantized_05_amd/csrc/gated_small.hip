@@ -522,8 +522,10 @@ void gated_few_kernel(FewArgs a, NF4Tables tab) {
     }
 }
 
-// H (and GU) of 64 outputs for all tokens: the slices' sums in order, G += s_g sum_j T_g[j] B_g[., j]
-// with T = the A tiles' sums, in float32, U likewise.
+// H (and GU) of 64 outputs of 16 tokens: the slices' sums in order, G += s_g sum_j T_g[j] B_g[., j]
+// with T = the A tiles' sums, in float32, U likewise. A thread has 4 outputs of a token; what it costs
+// is trips to memory, so the first slices' loads are on their way while the ranks come to LDS (24
+// tokens of 11008 outputs: 10 us with a thread per output and its loads one after the other).
 struct JoinArgs {
     const float* part; int splits, T, d_ff, r, atiles, tiles;
     const uint16_t* B[2]; float s[2];
@@ -531,54 +533,78 @@ struct JoinArgs {
     uint16_t* H; int64_t ldh;
     uint16_t* GU; int64_t ldgu;
 };
-constexpr int kJoinRows = 64, kJoinRanks = 32;
+constexpr int kJoinRows = 64, kJoinTokens = 16, kJoinRanks = 32, kJoinFirst = 4;
 
-template <int PT>       // tokens per thread; a workgroup takes 4 PT
 __global__ __launch_bounds__(256)
 void gated_join_kernel(JoinArgs a) {
-    __shared__ float s_b[2][kJoinRows][kJoinRanks + 1];
-    __shared__ float s_t[2][4 * PT][kJoinRanks];
-    const int n0 = static_cast<int>(blockIdx.x) * kJoinRows, t0 = static_cast<int>(blockIdx.y) * (4 * PT);
-    const int nt = min(4 * PT, a.T - t0);
-    const int i = threadIdx.x & 63, q = threadIdx.x >> 6;
+    __shared__ float s_b[2][kJoinRanks][kJoinRows + 4];
+    __shared__ float s_t[2][kJoinTokens][kJoinRanks];
+    const int n0 = static_cast<int>(blockIdx.x) * kJoinRows, t0 = static_cast<int>(blockIdx.y) * kJoinTokens;
+    const int nt = min(kJoinTokens, a.T - t0);
+    const int tid = threadIdx.x, n = 4 * (tid & 15), q = tid >> 4;
     const int64_t pitch = 16 * a.tiles, slice = pitch * a.T;
     const int rp = (a.r + 15) / 16 * 16;
     const float* part = a.part + t0 * pitch;
-    float v[2][PT];
+    const float* own = part + min(q, nt - 1) * pitch + 16 * a.atiles + n0 + n;
+    f32x4 first[2][kJoinFirst];
 #pragma unroll
     for (int w = 0; w < 2; ++w)
 #pragma unroll
-        for (int k = 0; k < PT; ++k)
-            v[w][k] = ordered_sum<4>(part + min(q + 4 * k, nt - 1) * pitch + 16 * a.atiles + w * a.d_ff + n0 + i, slice, a.splits);
-    for (int j0 = 0; j0 < a.r; j0 += kJoinRanks) {
+        for (int k = 0; k < kJoinFirst; ++k)
+            first[w][k] = *reinterpret_cast<const f32x4*>(own + w * a.d_ff + min(k, a.splits - 1) * slice);
+    f32x4 v[2];
+    for (int j0 = 0; j0 < a.r || j0 == 0; j0 += kJoinRanks) {
         const int nj = min(kJoinRanks, a.r - j0);
         if (j0 > 0) __syncthreads();
-        for (int e = threadIdx.x; e < 2 * kJoinRows * nj; e += 256) {
-            const int w = e / (kJoinRows * nj), row = e / nj % kJoinRows, j = e % nj;
-            s_b[w][row][j] = bf16_to_f32(a.B[w][static_cast<int64_t>(n0 + row) * a.r + j0 + j]);
+        if ((a.r & 7) == 0) {
+            // 8 ranks of a row; neighbouring threads have neighbouring rows
+            for (int e = tid; e < 2 * kJoinRows * (nj / 8); e += 256) {
+                const int row = e % kJoinRows, w = e / kJoinRows & 1, j = e / (2 * kJoinRows) * 8;
+                const uint4 b = *reinterpret_cast<const uint4*>(a.B[w] + static_cast<int64_t>(n0 + row) * a.r + j0 + j);
+                const uint32_t words[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    s_b[w][j + 2 * k][row] = __uint_as_float(words[k] << 16);
+                    s_b[w][j + 2 * k + 1][row] = __uint_as_float(words[k] & 0xFFFF0000u);
+                }
+            }
+        } else {
+            for (int e = tid; e < 2 * kJoinRows * nj; e += 256) {
+                const int row = e % kJoinRows, w = e / kJoinRows & 1, j = e / (2 * kJoinRows);
+                s_b[w][j][row] = bf16_to_f32(a.B[w][static_cast<int64_t>(n0 + row) * a.r + j0 + j]);
+            }
         }
-        for (int e = threadIdx.x; e < 2 * nt * nj; e += 256) {
-            const int w = e / (nt * nj), t = e / nj % nt, j = e % nj;
-            s_t[w][t][j] = a.s[w] * ordered_sum<4>(part + t * pitch + w * rp + j0 + j, slice, a.splits);
+        for (int e = tid; e < 2 * kJoinTokens * nj; e += 256) {
+            const int w = e & 1, t = e / 2 % kJoinTokens, j = e / (2 * kJoinTokens);
+            s_t[w][t][j] = a.s[w] * ordered_sum<4>(part + min(t, nt - 1) * pitch + w * rp + j0 + j, slice, a.splits);
         }
         __syncthreads();
+        if (j0 == 0) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                v[w] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int k = 0; k < kJoinFirst; ++k)
+                    if (k < a.splits) v[w] = v[w] + first[w][k];
+                for (int k = kJoinFirst; k < a.splits; ++k)
+                    v[w] = v[w] + *reinterpret_cast<const f32x4*>(own + w * a.d_ff + k * slice);
+            }
+        }
 #pragma unroll
         for (int w = 0; w < 2; ++w)
-            for (int j = 0; j < nj; ++j) {
-                const float b = s_b[w][i][j];
-#pragma unroll
-                for (int k = 0; k < PT; ++k) v[w][k] += s_t[w][min(q + 4 * k, nt - 1)][j] * b;
-            }
+#pragma unroll 4
+            for (int j = 0; j < nj; ++j) v[w] = v[w] + s_t[w][q][j] * *reinterpret_cast<const f32x4*>(&s_b[w][j][n]);
     }
+    if (q >= nt) return;
+    const int64_t t = t0 + q;
+    *reinterpret_cast<uint2*>(a.H + t * a.ldh + n0 + n) =
+        uint2{bf16_pair(gated_act(a.act, v[0][0]) * v[1][0], gated_act(a.act, v[0][1]) * v[1][1]),
+              bf16_pair(gated_act(a.act, v[0][2]) * v[1][2], gated_act(a.act, v[0][3]) * v[1][3])};
+    if (a.GU != nullptr) {
 #pragma unroll
-    for (int k = 0; k < PT; ++k) {
-        if (q + 4 * k >= nt) break;
-        const int64_t t = t0 + q + 4 * k;
-        a.H[t * a.ldh + n0 + i] = bf16_bits(gated_act(a.act, v[0][k]) * v[1][k]);
-        if (a.GU != nullptr) {
-            a.GU[t * a.ldgu + n0 + i] = bf16_bits(v[0][k]);
-            a.GU[t * a.ldgu + a.d_ff + n0 + i] = bf16_bits(v[1][k]);
-        }
+        for (int w = 0; w < 2; ++w)
+            *reinterpret_cast<uint2*>(a.GU + t * a.ldgu + w * a.d_ff + n0 + n) =
+                uint2{bf16_pair(v[w][0], v[w][1]), bf16_pair(v[w][2], v[w][3])};
     }
 }
 
@@ -677,8 +703,8 @@ hipError_t launch_gated_small(const GatedCall& c, const uint16_t* X, int64_t ldx
     j.part = part; j.splits = s.splits; j.T = a.T; j.d_ff = a.d_ff; j.r = c.r; j.atiles = s.atiles; j.tiles = s.tiles;
     j.act = c.act; j.H = H; j.ldh = ldh; j.GU = GU; j.ldgu = ldgu;
     const unsigned jx = static_cast<unsigned>(c.d_ff / kJoinRows);
-    if (c.M <= 4) QN_LAUNCH("gated_join_kernel", st, gated_join_kernel<1>, dim3(jx, 1), dim3(256), 0, st, j);
-    else QN_LAUNCH("gated_join_kernel", st, gated_join_kernel<2>, dim3(jx, static_cast<unsigned>((c.M + 7) / 8)), dim3(256), 0, st, j);
+    QN_LAUNCH("gated_join_kernel", st, gated_join_kernel,
+              dim3(jx, static_cast<unsigned>((c.M + kJoinTokens - 1) / kJoinTokens)), dim3(256), 0, st, j);
     return hipGetLastError();
 }
 

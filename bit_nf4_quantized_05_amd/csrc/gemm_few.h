@@ -35,7 +35,7 @@ __device__ __forceinline__ void gemm_few(const TurnArgs& g, const RowP& rowP, co
     // transposing read take (4 of each of two 8-row groups) lie in 8 distinct 32-byte parts of the 64 banks.
     const auto swz = [](int k) { return ((k >> 1) & 1) | ((k >> 2) & 2); };
     uint32_t voP[2], voQ[2];
-    auto places = [&](int64_t ldp, int64_t ldq) {
+    auto places = [&](int64_t ldp, int64_t ldq) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int r = 16 * wave + 8 * j + (lane >> 3);
@@ -44,7 +44,7 @@ __device__ __forceinline__ void gemm_few(const TurnArgs& g, const RowP& rowP, co
             if constexpr (!kQCols) voQ[j] = rowQ(r) * static_cast<uint32_t>(ldq * 2) + chunk;
         }
     };
-    auto columns = [&](int64_t ldq, int last) {      // last: Q's last row, from the first of the step
+    auto columns = [&](int64_t ldq, int last) __attribute__((always_inline)) {      // last: Q's last row, from the first of the step
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int k = 16 * wave + 8 * j + (lane >> 3), at = lane & 7;
@@ -54,23 +54,26 @@ __device__ __forceinline__ void gemm_few(const TurnArgs& g, const RowP& rowP, co
     };
     places(g.ldp, g.ldq);
     if constexpr (kQCols) columns(g.ldq, g.rowsQ - 1);
+    // values, not members: the choice between two of them was made of their addresses, in scratch
+    const uint32_t bytesP = g.bytesP, bytesQ = g.bytesQ, bytesP2 = g.bytesP2, bytesQ2 = g.bytesQ2;
     const int kmain = ke - kb;
     const int KT = kmain + (kRank && rank ? g.kt2 : 0);
     int next = 0;                                    // the step whose loads are issued
     int so = kb * (kTurnK * 2);
     uint32_t qstep = static_cast<uint32_t>(g.ldq) * (kTurnK * 2);
     int sq = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(kb) * qstep));
-    auto issue = [&]() {                             // a step past the last: descriptors of no extent
+    auto issue = [&]() __attribute__((always_inline)) {                             // a step past the last: descriptors of no extent
         if (kRank && next == kmain) {
             places(g.ldp2, g.ldq2);
             if constexpr (kQCols) columns(g.ldq2, kTurnK - 1);
             qstep = static_cast<uint32_t>(g.ldq2) * (kTurnK * 2);
             so = sq = 0;
         }
-        if (kQCols && kb + next == g.kt1 - 1) columns(g.ldq, g.rowsQ - 1 - kTurnK * (g.kt1 - 1));
+        if (kQCols && (!kRank || next < kmain) && kb + next == g.kt1 - 1)     // rows past the last: the last again
+            columns(g.ldq, g.rowsQ - 1 - kTurnK * (g.kt1 - 1));
         const bool first = !kRank || next < kmain, none = next >= KT;
-        const i32x4t rsP = turn_rsrc(first ? g.P : g.P2, none ? 0u : first ? g.bytesP : g.bytesP2);
-        const i32x4t rsQ = turn_rsrc(first ? g.Q : g.Q2, none ? 0u : first ? g.bytesQ : g.bytesQ2);
+        const i32x4t rsP = turn_rsrc(first ? g.P : g.P2, none ? 0u : first ? bytesP : bytesP2);
+        const i32x4t rsQ = turn_rsrc(first ? g.Q : g.Q2, none ? 0u : first ? bytesQ : bytesQ2);
         const uint32_t to = lds + 16384u * (next & (kFewStages - 1)) + 2048u * wave;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
@@ -132,6 +135,14 @@ __device__ __forceinline__ void gemm_few(const TurnArgs& g, const RowP& rowP, co
     QN_WAIT_VM(0);
     QN_TURN()
 }
+
+}  // namespace
+
+// The split of the tiles' K-steps (turn_split): two workgroups fit a CU, and a share has 16 steps or
+// more, since the launch that adds the shares costs as much as 10.
+inline TurnSplit few_split(int64_t M, int64_t tiles_n, int64_t kt) { return turn_split_of(6, M, tiles_n, kt, 512, 16); }
+
+namespace {
 
 // The tile's sums to a 64 x 64 float32 piece
 __device__ __forceinline__ void few_put_sums(float* piece, const FewSums& acc, bool add) {

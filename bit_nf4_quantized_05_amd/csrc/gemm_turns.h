@@ -106,10 +106,10 @@ __device__ __forceinline__ void turn_load(const i32x4t& rsrc, uint32_t to, uint3
 
 // acc = the K-steps [kb, ke) of P Q^T, then (kRank and rank) the g.kt2 steps of P2 Q2^T; at least
 // one step in all. rowP(r), rowQ(r): the row of P and P2 (Q and Q2) that tile row r takes (uint32,
-// inside the operand). With kQCols, Q is K-major instead, [kt1 64, ..] with its rows along K:
-// rowQ(r) is then the column of tile row r, for r a multiple of 8 and the 7 after it, and rows from
-// g.rowsQ on are taken as that last row (P must be zero there). On return every wave has finished
-// its reads of LDS and no load is in flight.
+// inside the operand). With kQCols, Q and Q2 are K-major instead, their rows along K: rowQ(r) is
+// then the column of tile row r, for r a multiple of 8 and the 7 after it. Rows of Q from g.rowsQ on
+// are taken as the last one (P must be zero there); Q2 has whole steps of them. On return every wave
+// has finished its reads of LDS and no load is in flight.
 template <bool kRank, bool kQCols, class RowP, class RowQ>
 __device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, const RowQ& rowQ, int kb, int ke, bool rank,
                                            TurnSums& acc) {
@@ -123,7 +123,7 @@ __device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, 
     // the chunk that belongs at position i % 8 of row i / 8.
     uint32_t voP[2][2], voQ[2][2];                  // half, instruction
     i32x4t rsP, rsQ;
-    auto places = [&](int64_t ldp, int64_t ldq) {
+    auto places = [&](int64_t ldp, int64_t ldq) __attribute__((always_inline)) {
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -138,18 +138,20 @@ __device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, 
     // at u ^ swz(k), which puts the 8 rows that 32 lanes of a transposing read take (4 of each of two
     // 8-row groups) into 8 distinct units. A load instruction fills 4 rows; wave w fills 8 w .. 8 w + 7.
     const auto swz = [](int k) { return (k & 3) | ((k >> 1) & 4); };
-    auto columns = [&](int first) {                 // the rows' first is k-row `first` of Q
+    auto columns = [&](int64_t ldq, int last) __attribute__((always_inline)) {     // last: the operand's last row, from the first of the step
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int k = 8 * wave + 4 * j + (lane >> 4), at = lane & 15;
                 const int n = 128 * h + 16 * ((at >> 1) ^ swz(k)) + 8 * (at & 1);
-                voQ[h][j] = static_cast<uint32_t>(min(k, g.rowsQ - 1 - first)) * static_cast<uint32_t>(g.ldq * 2) + rowQ(n) * 2u;
+                voQ[h][j] = static_cast<uint32_t>(min(k, last)) * static_cast<uint32_t>(ldq * 2) + rowQ(n) * 2u;
             }
     };
     places(g.ldp, g.ldq);
-    if constexpr (kQCols) columns(0);
+    if constexpr (kQCols) columns(g.ldq, g.rowsQ - 1);
+    // values, not members: the choice between two of them was made of their addresses, in scratch
+    const uint32_t bytesP = g.bytesP, bytesQ = g.bytesQ, bytesP2 = g.bytesP2, bytesQ2 = g.bytesQ2;
     const int kmain = ke - kb;
     const int KT = kmain + (kRank && rank ? g.kt2 : 0);
     // Loads are issued for two steps past the last as well, so that the loop has no branch around a
@@ -157,17 +159,20 @@ __device__ __forceinline__ void gemm_turns(const TurnArgs& g, const RowP& rowP, 
     // no extent, so nothing is fetched.
     int next = 0;                                   // the step whose loads are issued
     int so = kb * (kTurnK * 2);                     // its byte offset in a row
-    const uint32_t qstep = static_cast<uint32_t>(g.ldq) * (kTurnK * 2);      // K-major: bytes of 64 rows
+    uint32_t qstep = static_cast<uint32_t>(g.ldq) * (kTurnK * 2);      // K-major: bytes of 64 rows
     int sq = __builtin_amdgcn_readfirstlane(static_cast<int>(static_cast<uint32_t>(kb) * qstep));
-    auto enter = [&]() {                            // before the first load of step `next`
+    auto enter = [&]() __attribute__((always_inline)) {                            // before the first load of step `next`
         if (kRank && next == kmain) {
             places(g.ldp2, g.ldq2);
-            so = 0;
+            if constexpr (kQCols) columns(g.ldq2, kTurnK - 1);
+            qstep = static_cast<uint32_t>(g.ldq2) * (kTurnK * 2);
+            so = sq = 0;
         }
-        if (kQCols && kb + next == g.kt1 - 1) columns(64 * (g.kt1 - 1));     // rows past the last: the last again
+        if (kQCols && (!kRank || next < kmain) && kb + next == g.kt1 - 1)     // rows past the last: the last again
+            columns(g.ldq, g.rowsQ - 1 - kTurnK * (g.kt1 - 1));
         const bool first = !kRank || next < kmain, none = next >= KT;
-        rsP = turn_rsrc(first ? g.P : g.P2, none ? 0u : first ? g.bytesP : g.bytesP2);
-        rsQ = turn_rsrc(first ? g.Q : g.Q2, none ? 0u : first ? g.bytesQ : g.bytesQ2);
+        rsP = turn_rsrc(first ? g.P : g.P2, none ? 0u : first ? bytesP : bytesP2);
+        rsQ = turn_rsrc(first ? g.Q : g.Q2, none ? 0u : first ? bytesQ : bytesQ2);
     };
     auto leave = [&]() { ++next; so += kTurnK * 2; sq = __builtin_amdgcn_readfirstlane(static_cast<int>(sq + qstep)); };
 #define QN_LOAD(OBJ, RS, VO, SO)                                    \
@@ -342,15 +347,16 @@ __device__ __forceinline__ void turn_tile(int item, int tiles_m, int tiles_n, in
 // shares of kper whose float32 sums (256 x 256 a piece, share s of tile j at s rem + j) a second
 // kernel adds. Up to 16 shares, of 4 K-steps or more (1531 tokens of the 11008 x 4096 block leave 4 tiles:
 // 243 us with up to 4 shares of 8 steps).
-struct TurnSplit { int tiles_m, tiles_n, splits, full, rem, kper; };
-inline TurnSplit turn_split(int64_t M, int64_t tiles_n, int64_t kt) {
+struct TurnSplit { int lt, tiles_m, tiles_n, splits, full, rem, kper; };       // tiles of 1 << lt
+inline TurnSplit turn_split_of(int lt, int64_t M, int64_t tiles_n, int64_t kt, int slots, int64_t steps) {
     TurnSplit s{};
-    s.tiles_m = static_cast<int>((M + kTurnTile - 1) / kTurnTile);
+    s.lt = lt;
+    s.tiles_m = static_cast<int>((M + (1 << lt) - 1) >> lt);
     s.tiles_n = static_cast<int>(tiles_n);
-    const int T = s.tiles_m * s.tiles_n, rem = T % 256;
-    int want = rem == 0 || rem > 128 ? 1 : 256 / rem;
+    const int T = s.tiles_m * s.tiles_n, rem = T % slots;
+    int want = rem == 0 || rem > slots / 2 ? 1 : slots / rem;
     if (want > 16) want = 16;
-    if (want > kt / 4) want = static_cast<int>(kt / 4);
+    if (want > kt / steps) want = static_cast<int>(kt / steps);
     s.splits = want < 2 ? 1 : want;
     s.full = s.splits > 1 ? T - rem : T;
     s.rem = s.splits > 1 ? rem : 0;
@@ -358,8 +364,9 @@ inline TurnSplit turn_split(int64_t M, int64_t tiles_n, int64_t kt) {
     if (s.splits > 1) s.splits = static_cast<int>((kt + s.kper - 1) / s.kper);
     return s;
 }
+inline TurnSplit turn_split(int64_t M, int64_t tiles_n, int64_t kt) { return turn_split_of(8, M, tiles_n, kt, 256, 4); }
 inline int64_t turn_split_floats(const TurnSplit& s) {
-    return s.splits > 1 ? static_cast<int64_t>(s.splits) * s.rem * kTurnTile * kTurnTile : 0;
+    return s.splits > 1 ? (static_cast<int64_t>(s.splits) * s.rem) << (2 * s.lt) : 0;
 }
 inline unsigned turn_split_grid(const TurnSplit& s) {
     return static_cast<unsigned>((s.full + 7) / 8 * 8 + s.rem * s.splits);

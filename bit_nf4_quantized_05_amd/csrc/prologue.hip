@@ -46,13 +46,12 @@ struct PreJob {
     int n;                           // workgroups of this job
 };
 
-// One double dequantisation: W_hat row-major [d_out, d_in], or W_hat^T [d_in, d_out] with row
-// stride ldw.
+// One double dequantisation: W_hat row-major [d_out, d_in], or W_hat^T [d_in, d_out].
 struct DeqJob {
     const uint8_t* codes; BlockConsts bc;
     int64_t d_out, d_in;
     int transposed;                 // dequant to W_hat^T instead of W_hat
-    uint16_t* what; int64_t ldw;
+    uint16_t* what;
     int trans_tiles;                // 64 x 64 tiles per transposed-dequant workgroup (1..4)
     int n;                          // workgroups
 };
@@ -395,7 +394,7 @@ __device__ __forceinline__ void dequant_transposed_job(const DeqJob& a, int b, c
             const int cc = c & 7;            // 16-byte chunk: output columns o0 + 8 cc .. + 7
             const int64_t i = static_cast<int64_t>(t0 + k) * 64 + il;
             if (o0 + 8 * cc < a.d_out)       // d_out % 64 == 0 on this path: whole chunks
-                *reinterpret_cast<uint4*>(a.what + i * a.ldw + o0 + 8 * cc) =
+                *reinterpret_cast<uint4*>(a.what + i * a.d_out + o0 + 8 * cc) =
                     *reinterpret_cast<const uint4*>(&tile[il * kTP + 8 * cc]);
         }
     }
@@ -451,41 +450,63 @@ void prologue_kernel(PrologueArgs a, NF4Tables tab) {
 // ---------------------------------------------------------------------------
 // The gated block's two projections side by side (gated.hip): both weights' dequantisation,
 // both pre-passes and both adapters in one launch. The rank columns of the gate come first,
-// pad of them, then those of the up projection; an output row has its own projection's adapter
-// and zeros at the other's columns.
+// pad of them, then those of the up projection.
 // ---------------------------------------------------------------------------
 struct GatedPrologueArgs {
     PrologueArgs p;                  // pre[0], pre[1], M, r, r_pad (pad); deq: the gate's
     DeqJob deq_up;
     GatedGradArgs grad;              // the gradient's elementwise part (n_grad workgroups)
-    const uint16_t* asrc[2];         // B_g, B_u [d_ff, r] (forward) or A_g, A_u [r, d_in] (gradient)
-    uint16_t* adst; int64_t arows;   // [arows, k2]
-    int k2, backward, n_adapt, n_grad;
+    const uint16_t* A[2]; const uint16_t* B[2];
+    uint16_t* adst;                  // forward [2 d_ff, k2], gradient [k2, d_in]
+    uint16_t* bt[2];                 // gradient: B^T [r, d_ff], or null
+    int64_t d_ff, d_in;
+    int k2, backward, n_adapt, n_bt, n_grad;
 };
 
-// 8 entries of a row of the adapter layout: forward, the gate's d_ff rows, then the up
-// projection's; gradient, row i is column i of both A.
+// 8 entries of a row of the adapters' layout. Forward: the gate's d_ff rows of B, then the up
+// projection's, each at its own rank columns with zeros at the other's. Gradient: the rows of A_g,
+// zeros up to pad, and so A_u.
 __device__ __forceinline__ void gated_adapt_job(const GatedPrologueArgs& a, int b) {
-    const int cpr = a.k2 / 8, r = a.p.r, pad = a.p.r_pad;
+    const int r = a.p.r, pad = a.p.r_pad;
     const int64_t c = static_cast<int64_t>(b) * 256 + threadIdx.x;
-    if (c >= a.arows * cpr) return;
-    const int64_t i = c / cpr;
-    const int j0 = static_cast<int>(c % cpr) * 8;
-    const int w = j0 >= pad ? 1 : 0, q0 = j0 - w * pad;      // pad % 8 == 0: a chunk is of one projection
-    uint32_t v[4] = {0u, 0u, 0u, 0u};
-    const int64_t d_ff = a.arows / 2;                        // forward
-    if (a.backward || (i >= d_ff) == (w == 1)) {
-        const uint16_t* src = a.asrc[w];
-        const int64_t row = a.backward ? i : i - w * d_ff;
+    uint4 v = uint4{0u, 0u, 0u, 0u};
+    if (a.backward) {
+        const int64_t cpr = a.d_in / 8;
+        if (c >= a.k2 * cpr) return;
+        const int j = static_cast<int>(c / cpr), w = j >= pad ? 1 : 0, q = j - w * pad;
+        if (q < r) v = *reinterpret_cast<const uint4*>(a.A[w] + q * a.d_in + (c % cpr) * 8);
+    } else {
+        const int cpr = a.k2 / 8;
+        if (c >= 2 * a.d_ff * cpr) return;
+        const int64_t i = c / cpr;
+        const int j0 = static_cast<int>(c % cpr) * 8;
+        const int w = j0 >= pad ? 1 : 0, q0 = j0 - w * pad;  // pad % 8 == 0: a chunk is of one projection
+        if ((i >= a.d_ff) == (w == 1)) {
+            const uint16_t* src = a.B[w] + (i - w * a.d_ff) * r + q0;
+            uint32_t e2[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (q0 + e < r) {
-                const int64_t at = a.backward ? (q0 + e) * a.arows + row : row * r + q0 + e;
-                v[e >> 1] |= static_cast<uint32_t>(src[at]) << (16 * (e & 1));
-            }
+            for (int e = 0; e < 8; ++e)
+                if (q0 + e < r) e2[e >> 1] |= static_cast<uint32_t>(src[e]) << (16 * (e & 1));
+            v = uint4{e2[0], e2[1], e2[2], e2[3]};
         }
     }
-    *reinterpret_cast<uint4*>(a.adst + c * 8) = uint4{v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<uint4*>(a.adst + c * 8) = v;
+}
+
+// 8 entries of a row of B_g^T or B_u^T, where the pre-pass does not read B as it is. The reads are
+// single entries of 8 rows; 0.7 million of them at rank 64 are lost beside the dequantisation.
+__device__ __forceinline__ void gated_bt_job(const GatedPrologueArgs& a, int b) {
+    const int64_t cpr = a.d_ff / 8;
+    int64_t c = static_cast<int64_t>(b) * 256 + threadIdx.x;
+    const int w = c >= a.p.r * cpr ? 1 : 0;
+    c -= w * a.p.r * cpr;
+    if (c >= a.p.r * cpr) return;
+    const int j = static_cast<int>(c % a.p.r);                // neighbouring lanes: one row of B
+    const int64_t k = c / a.p.r * 8;
+    uint32_t v[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e >> 1] |= static_cast<uint32_t>(a.B[w][(k + e) * a.p.r + j]) << (16 * (e & 1));
+    *reinterpret_cast<uint4*>(a.bt[w] + j * a.d_ff + k) = uint4{v[0], v[1], v[2], v[3]};
 }
 
 template <int NT, bool KM>
@@ -509,6 +530,11 @@ void gated_prologue_kernel(GatedPrologueArgs a, NF4Tables tab) {
         return;
     }
     b -= a.n_adapt;
+    if (b < a.n_bt) {
+        gated_bt_job(a, b);
+        return;
+    }
+    b -= a.n_bt;
     char* lds = reinterpret_cast<char*>(s1.x);
     if (b < a.p.deq.n) dequant_jobs(a.p.deq, b, tab, lds);
     else dequant_jobs(a.deq_up, b - a.p.deq.n, tab, lds);
@@ -935,7 +961,6 @@ DeqJob make_dequant(const uint8_t* codes, const BlockConsts& bc, int64_t d_out, 
     DeqJob a{};
     a.codes = codes; a.bc = bc;
     a.d_out = d_out; a.d_in = d_in; a.transposed = transposed ? 1 : 0; a.what = what;
-    a.ldw = transposed ? d_out : d_in;
     const int64_t n = d_out * d_in;
     a.trans_tiles = static_cast<int>(std::min<int64_t>(kTransTiles, std::max<int64_t>(1, (n / 4096) / 2048)));
     a.n = what == nullptr ? 0   // pre-pass (and adapter layout) only
@@ -1026,43 +1051,37 @@ hipError_t launch_prepass_pair(const uint16_t* P0, int64_t ldp0, int64_t K0, con
 hipError_t launch_gated_prologue(const GatedCall& c, bool backward, const GatedProlog& o, hipStream_t st) {
     GatedPrologueArgs a{};
     const bool first = o.what != nullptr;            // the launch with the weights' and adapters' layouts
+    const bool kmajor = backward && prepass_takes_kmajor(c.r);
     a.p.M = static_cast<int>(c.M); a.p.r = c.r; a.p.r_pad = gated_pad(c.r);
     const int64_t K = backward ? c.d_ff : c.d_in;
-    if (c.r > 0 && o.pre_out != nullptr) {
-        for (int w = 0; w < 2; ++w) {
-            const bool km = backward && prepass_takes_kmajor(c.r);
-            const uint16_t* R = backward ? (km ? c.B[w] : o.bt[w]) : c.A[w];
+    for (int w = 0; w < 2; ++w) {
+        a.A[w] = c.A[w]; a.B[w] = c.B[w]; a.bt[w] = o.bt[w];
+        if (c.r > 0 && o.pre_out != nullptr) {
+            const uint16_t* R = backward ? (kmajor ? c.B[w] : o.bt[w]) : c.A[w];
             const uint16_t* P = backward ? o.pre_in + w * c.d_ff : o.pre_in;
             a.p.pre[w] = make_job(P, o.ld_in, c.M, K, R, K, o.pre_out + w * gated_pad(c.r), gated_k2(c.r), c.s[w],
-                                  o.ppart[w]);
+                                  K <= kGatedOneSlice ? nullptr : o.ppart[w]);
         }
     }
     a.p.n_pre = a.p.pre[0].n + a.p.pre[1].n;
     if (first) {
-        for (int w = 0; w < 2; ++w) {
-            DeqJob& d = w == 0 ? a.p.deq : a.deq_up;
-            if (backward) {
-                d = make_dequant(c.codes[w], c.bc[w], c.d_ff, c.d_in, true, o.what + w * c.d_ff);
-                d.ldw = 2 * c.d_ff;
-            } else {
-                d = make_dequant(c.codes[w], c.bc[w], c.d_ff, c.d_in, false, o.what + w * c.d_ff * c.d_in);
-            }
-            a.asrc[w] = backward ? c.A[w] : c.B[w];
-        }
+        for (int w = 0; w < 2; ++w)
+            (w == 0 ? a.p.deq : a.deq_up) = make_dequant(c.codes[w], c.bc[w], c.d_ff, c.d_in, false, o.what + w * c.d_ff * c.d_in);
         a.backward = backward ? 1 : 0;
+        a.d_ff = c.d_ff; a.d_in = c.d_in;
         a.k2 = gated_k2(c.r);
         a.adst = o.adapt;
-        a.arows = backward ? c.d_in : 2 * c.d_ff;
-        a.n_adapt = static_cast<int>((a.arows * (a.k2 / 8) + 255) / 256);
+        a.n_adapt = static_cast<int>(((backward ? c.d_in : 2 * c.d_ff) * (a.k2 / 8) + 255) / 256);
         if (backward) {
             a.grad = o.grad;
             a.n_grad = gated_grad_blocks(o.grad);
+            if (c.r > 0 && !kmajor) a.n_bt = static_cast<int>((2 * c.r * (c.d_ff / 8) + 255) / 256);
         }
     }
-    const dim3 grid(static_cast<unsigned>(a.p.n_pre + a.n_grad + a.n_adapt + a.p.deq.n + a.deq_up.n));
+    const dim3 grid(static_cast<unsigned>(a.p.n_pre + a.n_grad + a.n_adapt + a.n_bt + a.p.deq.n + a.deq_up.n));
     const NF4Tables& tab = tables();
     const int NT = std::max(1, (c.r + 31) / 32);
-    if (backward && prepass_takes_kmajor(c.r)) {
+    if (kmajor) {
         QN_LAUNCH("gated_prologue_kernel", st, (gated_prologue_kernel<1, true>), grid, dim3(256), 0, st, a, tab);
     } else {
         switch (a.p.n_pre > 0 ? NT : 1) {
