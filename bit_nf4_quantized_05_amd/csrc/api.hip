@@ -325,8 +325,9 @@ GatedWs gated_ws(int64_t d_ff, int64_t d_in, int64_t d_seq, int r, bool bwd) {
     w.t = take(2 * d_seq * qn::gated_k2(r));                                         // both rank products
     w.adapt = take(2 * (bwd ? d_in : 2 * d_ff) * qn::gated_k2(r));                   // both adapters
     for (int i = 0; i < 2; ++i) {
-        w.ppart[i] = take(r > 0 ? prepass_part_bytes(d_seq, bwd ? d_ff : d_in, r) : 0);
-        w.bt[i] = take(bwd && !qn::prepass_takes_kmajor(r) ? 2 * static_cast<int64_t>(r) * d_ff : 0);
+        w.ppart[i] = take(bwd ? (i == 0 ? 4 * qn::gated_ranks_floats(d_seq, d_ff, r) : 0)
+                              : r > 0 ? prepass_part_bytes(d_seq, d_in, r) : 0);
+        w.bt[i] = take(bwd && !qn::gated_reads_b(r) ? 2 * static_cast<int64_t>(r) * d_ff : 0);
     }
     w.part = take(4 * (bwd ? qn::gated_dx_part_floats(d_seq, d_ff, d_in) : qn::gated_part_floats(d_seq, d_ff, d_in)));
     w.bytes = off;
@@ -1088,7 +1089,7 @@ int qlora_gated_fwd(const uint8_t* codes_g, const int8_t* qconst_g, const float*
     qn::GatedProlog o{};
     o.what = reinterpret_cast<uint16_t*>(ws + w.what);
     o.adapt = reinterpret_cast<uint16_t*>(ws + w.adapt);
-    o.pre_in = X; o.ld_in = ldx;
+    o.X = X; o.ldx = ldx;
     o.pre_out = reinterpret_cast<uint16_t*>(ws + w.t);
     for (int i = 0; i < 2; ++i) o.ppart[i] = reinterpret_cast<float*>(ws + w.ppart[i]);
     hipError_t e = qn::launch_gated_prologue(c, false, o, st);
@@ -1122,20 +1123,14 @@ int qlora_gated_bwd(const uint8_t* codes_g, const int8_t* qconst_g, const float*
     o.what = reinterpret_cast<uint16_t*>(ws + w.what);
     o.adapt = reinterpret_cast<uint16_t*>(ws + w.adapt);
     o.grad = qn::GatedGradArgs{dH, lddh, GU, ldgu, dGU, lddgu, static_cast<int>(d_seq), static_cast<int>(d_ff), act};
-    if (r > 0 && !qn::prepass_takes_kmajor(r))
+    if (!qn::gated_reads_b(r))
         for (int i = 0; i < 2; ++i) o.bt[i] = reinterpret_cast<uint16_t*>(ws + w.bt[i]);
     hipError_t e = qn::launch_gated_prologue(c, true, o, st);
     if (e != hipSuccess) return hip_fail(e, "qlora_gated_bwd (prologue)");
-    uint16_t* t = nullptr;
+    uint16_t* t = reinterpret_cast<uint16_t*>(ws + w.t);
     if (r > 0) {
-        qn::GatedProlog p{};
-        t = p.pre_out = reinterpret_cast<uint16_t*>(ws + w.t);
-        p.pre_in = dGU; p.ld_in = lddgu;
-        for (int i = 0; i < 2; ++i) {
-            p.ppart[i] = reinterpret_cast<float*>(ws + w.ppart[i]);
-            p.bt[i] = o.bt[i];
-        }
-        if ((e = qn::launch_gated_prologue(c, true, p, st)) != hipSuccess) return hip_fail(e, "qlora_gated_bwd (pre-pass)");
+        e = qn::launch_gated_ranks(c, dGU, lddgu, o.bt, t, reinterpret_cast<float*>(ws + w.ppart[0]), st);
+        if (e != hipSuccess) return hip_fail(e, "qlora_gated_bwd (rank products)");
     }
     e = qn::launch_gated_dx(c, dGU, lddgu, o.what, t, o.adapt, dX, lddx, reinterpret_cast<float*>(ws + w.part), st);
     if (e != hipSuccess) return hip_fail(e, "qlora_gated_bwd (gemm)");

@@ -448,8 +448,9 @@ void prologue_kernel(PrologueArgs a, NF4Tables tab) {
 }
 
 // ---------------------------------------------------------------------------
-// The gated block's two projections side by side (gated.hip): both weights' dequantisation,
-// both pre-passes and both adapters in one launch. The rank columns of the gate come first,
+// The gated block's two projections side by side (gated.hip): both weights' dequantisation, both
+// adapters and, forward, both pre-passes (rows of up to kGatedOneSlice in one slice: the sum of slices
+// is a launch more), in the gradient its elementwise part, in one launch. The rank columns of the gate come first,
 // pad of them, then those of the up projection.
 // ---------------------------------------------------------------------------
 struct GatedPrologueArgs {
@@ -493,8 +494,8 @@ __device__ __forceinline__ void gated_adapt_job(const GatedPrologueArgs& a, int 
     *reinterpret_cast<uint4*>(a.adst + c * 8) = v;
 }
 
-// 8 entries of a row of B_g^T or B_u^T, where the pre-pass does not read B as it is. The reads are
-// single entries of 8 rows; 0.7 million of them at rank 64 are lost beside the dequantisation.
+// 8 entries of a row of B_g^T or B_u^T, where the rank products cannot read B as it is (its rows of
+// r % 8 != 0 entries start off 16-byte boundaries). Single entries of 8 rows are read.
 __device__ __forceinline__ void gated_bt_job(const GatedPrologueArgs& a, int b) {
     const int64_t cpr = a.d_ff / 8;
     int64_t c = static_cast<int64_t>(b) * 256 + threadIdx.x;
@@ -509,14 +510,14 @@ __device__ __forceinline__ void gated_bt_job(const GatedPrologueArgs& a, int b) 
     *reinterpret_cast<uint4*>(a.bt[w] + j * a.d_ff + k) = uint4{v[0], v[1], v[2], v[3]};
 }
 
-template <int NT, bool KM>
+template <int NT>
 __global__ __launch_bounds__(256)
 void gated_prologue_kernel(GatedPrologueArgs a, NF4Tables tab) {
     __shared__ PreStage<NT> s0, s1;
     int b = blockIdx.x;
     if (b < a.p.n_pre) {
         const bool up = b >= a.p.pre[0].n;
-        prepass_job<NT, KM>(a.p.pre[up], a.p, up ? b - a.p.pre[0].n : b, s0, s1);
+        prepass_job<NT, false>(a.p.pre[up], a.p, up ? b - a.p.pre[0].n : b, s0, s1);
         return;
     }
     b -= a.p.n_pre;
@@ -1050,49 +1051,35 @@ hipError_t launch_prepass_pair(const uint16_t* P0, int64_t ldp0, int64_t K0, con
 
 hipError_t launch_gated_prologue(const GatedCall& c, bool backward, const GatedProlog& o, hipStream_t st) {
     GatedPrologueArgs a{};
-    const bool first = o.what != nullptr;            // the launch with the weights' and adapters' layouts
-    const bool kmajor = backward && prepass_takes_kmajor(c.r);
     a.p.M = static_cast<int>(c.M); a.p.r = c.r; a.p.r_pad = gated_pad(c.r);
-    const int64_t K = backward ? c.d_ff : c.d_in;
     for (int w = 0; w < 2; ++w) {
         a.A[w] = c.A[w]; a.B[w] = c.B[w]; a.bt[w] = o.bt[w];
-        if (c.r > 0 && o.pre_out != nullptr) {
-            const uint16_t* R = backward ? (kmajor ? c.B[w] : o.bt[w]) : c.A[w];
-            const uint16_t* P = backward ? o.pre_in + w * c.d_ff : o.pre_in;
-            a.p.pre[w] = make_job(P, o.ld_in, c.M, K, R, K, o.pre_out + w * gated_pad(c.r), gated_k2(c.r), c.s[w],
-                                  K <= kGatedOneSlice ? nullptr : o.ppart[w]);
-        }
+        if (c.r > 0 && !backward)
+            a.p.pre[w] = make_job(o.X, o.ldx, c.M, c.d_in, c.A[w], c.d_in, o.pre_out + w * gated_pad(c.r), gated_k2(c.r),
+                                  c.s[w], c.d_in <= kGatedOneSlice ? nullptr : o.ppart[w]);
+        (w == 0 ? a.p.deq : a.deq_up) = make_dequant(c.codes[w], c.bc[w], c.d_ff, c.d_in, false, o.what + w * c.d_ff * c.d_in);
     }
     a.p.n_pre = a.p.pre[0].n + a.p.pre[1].n;
-    if (first) {
-        for (int w = 0; w < 2; ++w)
-            (w == 0 ? a.p.deq : a.deq_up) = make_dequant(c.codes[w], c.bc[w], c.d_ff, c.d_in, false, o.what + w * c.d_ff * c.d_in);
-        a.backward = backward ? 1 : 0;
-        a.d_ff = c.d_ff; a.d_in = c.d_in;
-        a.k2 = gated_k2(c.r);
-        a.adst = o.adapt;
-        a.n_adapt = static_cast<int>(((backward ? c.d_in : 2 * c.d_ff) * (a.k2 / 8) + 255) / 256);
-        if (backward) {
-            a.grad = o.grad;
-            a.n_grad = gated_grad_blocks(o.grad);
-            if (c.r > 0 && !kmajor) a.n_bt = static_cast<int>((2 * c.r * (c.d_ff / 8) + 255) / 256);
-        }
+    a.backward = backward ? 1 : 0;
+    a.d_ff = c.d_ff; a.d_in = c.d_in;
+    a.k2 = gated_k2(c.r);
+    a.adst = o.adapt;
+    a.n_adapt = static_cast<int>(((backward ? c.d_in : 2 * c.d_ff) * (a.k2 / 8) + 255) / 256);
+    if (backward) {
+        a.grad = o.grad;
+        a.n_grad = gated_grad_blocks(o.grad);
+        if (o.bt[0] != nullptr) a.n_bt = static_cast<int>((2 * c.r * (c.d_ff / 8) + 255) / 256);
     }
     const dim3 grid(static_cast<unsigned>(a.p.n_pre + a.n_grad + a.n_adapt + a.n_bt + a.p.deq.n + a.deq_up.n));
     const NF4Tables& tab = tables();
-    const int NT = std::max(1, (c.r + 31) / 32);
-    if (kmajor) {
-        QN_LAUNCH("gated_prologue_kernel", st, (gated_prologue_kernel<1, true>), grid, dim3(256), 0, st, a, tab);
-    } else {
-        switch (a.p.n_pre > 0 ? NT : 1) {
+    const int NT = a.p.n_pre > 0 ? (c.r + 31) / 32 : 1;
+    switch (NT) {
 #define QN_PRO_CASE(T) \
-            case T: QN_LAUNCH("gated_prologue_kernel", st, (gated_prologue_kernel<T, false>), grid, dim3(256), 0, st, \
-                              a, tab); break;
-            QN_PRO_CASE(1) QN_PRO_CASE(2) QN_PRO_CASE(3) QN_PRO_CASE(4)
-            QN_PRO_CASE(5) QN_PRO_CASE(6) QN_PRO_CASE(7) QN_PRO_CASE(8)
+        case T: QN_LAUNCH("gated_prologue_kernel", st, gated_prologue_kernel<T>, grid, dim3(256), 0, st, a, tab); break;
+        QN_PRO_CASE(1) QN_PRO_CASE(2) QN_PRO_CASE(3) QN_PRO_CASE(4)
+        QN_PRO_CASE(5) QN_PRO_CASE(6) QN_PRO_CASE(7) QN_PRO_CASE(8)
 #undef QN_PRO_CASE
-            default: return hipErrorInvalidValue;
-        }
+        default: return hipErrorInvalidValue;
     }
     if (a.p.pre[0].psplits > 1) {
         const int blocks = static_cast<int>((c.M * (gated_pad(c.r) / 4) + 255) / 256);
