@@ -131,6 +131,14 @@ def _stream(dev: torch.device) -> int:
     return _raw_stream(dev.index)
 
 
+def _own_stream(dev: torch.device) -> int:
+    """_stream for a call whose tensors must lie on the current device: its default stream has no
+    device of its own, the launches would go to the current one."""
+    if torch.cuda.current_device() != dev.index:
+        raise ValueError(f"the tensors are on {dev}, which is not the current device")
+    return _stream(dev)
+
+
 def _ptr(t: torch.Tensor) -> int:
     return t.data_ptr()
 
@@ -745,7 +753,8 @@ def gated_fwd(layer: GatedLayer, X: torch.Tensor, save: bool = False, out: torch
               GU: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
     """qlora_gated_fwd: H [d_seq, d_ff] = act(G) * U. With save (or GU given) (H, GU), GU
     [d_seq, 2 d_ff] holding G beside U for ``gated_bwd``. X, out and GU may be row views of
-    wider arrays."""
+    wider arrays. The layer's device must be the current one, and calls that may run at once
+    need a workspace each (so too ``gated_bwd``, ``head_loss`` and ``head_loss_grad``)."""
     dev, d_ff, d_in = layer.device, layer.d_ff, layer.d_in
     if X.dim() != 2 or X.shape[1] != d_in:
         raise ValueError(f"input must be [d_seq, {d_in}]")
@@ -755,7 +764,7 @@ def gated_fwd(layer: GatedLayer, X: torch.Tensor, save: bool = False, out: torch
     gu, ldgu = _output(GU, (d_seq, 2 * d_ff), "GU", dev, X, o) if save or GU is not None else (None, 0)
     ws = _workspace(workspace, lambda: gated_fwd_workspace_bytes(d_ff, d_in, d_seq, layer.r), dev)
     rc = lib().qlora_gated_fwd(*layer.weights, X.data_ptr(), ldx, d_seq, o.data_ptr(), ldh,
-                               None if gu is None else gu.data_ptr(), ldgu, ws.data_ptr(), ws.nbytes, _stream(dev))
+                               None if gu is None else gu.data_ptr(), ldgu, ws.data_ptr(), ws.nbytes, _own_stream(dev))
     if rc:
         _check(rc, "qlora_gated_fwd")
     return o if gu is None else (o, gu)
@@ -780,7 +789,7 @@ def gated_bwd(layer: GatedLayer, GU: torch.Tensor, dH: torch.Tensor, dX: torch.T
     gx, lddx = _output(dX, (d_seq, d_in), "dX", dev, GU, dH, dgu)
     ws = _workspace(workspace, lambda: gated_bwd_workspace_bytes(d_ff, d_in, d_seq, layer.r), dev)
     rc = lib().qlora_gated_bwd(*layer.weights, GU.data_ptr(), ldgu, dH.data_ptr(), lddh, d_seq, dgu.data_ptr(), lddgu,
-                               gx.data_ptr(), lddx, ws.data_ptr(), ws.nbytes, _stream(dev))
+                               gx.data_ptr(), lddx, ws.data_ptr(), ws.nbytes, _own_stream(dev))
     if rc:
         _check(rc, "qlora_gated_bwd")
     return gx, dgu
@@ -822,7 +831,7 @@ def _head_loss(head, X, target, scale, grad, loss, dX, workspace):
     ws = _workspace(workspace, lambda: head_loss_workspace_bytes(head, d_seq, grad), dev)
     rc = lib().qlora_head_loss(*args, vocab, d_in, X.data_ptr(), ldx, d_seq, target.data_ptr(),
                                None if scale is None else scale.data_ptr(), loss.data_ptr(),
-                               None if gx is None else gx.data_ptr(), lddx, ws.data_ptr(), ws.nbytes, _stream(dev))
+                               None if gx is None else gx.data_ptr(), lddx, ws.data_ptr(), ws.nbytes, _own_stream(dev))
     if rc:
         _check(rc, "qlora_head_loss")
     return loss, gx

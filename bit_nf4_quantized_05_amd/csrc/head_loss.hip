@@ -514,7 +514,8 @@ bool head_plan(int64_t V, int64_t d, int64_t T, bool nf4, bool grad, HeadPlan* p
     // fewer where T rows of exponentials would pass 2^27 (256 MB), but 4096 rows of them up to 2 GiB.
     int64_t most = grad ? 32768 : 65536;
     if (grad) most = std::min(most, std::max((int64_t{1} << 27) / T, std::min<int64_t>(4096, kLimit / 2 / T)) / 256 * 256);
-    most = std::max<int64_t>(256, most);
+    // up to 2^22 tiles of a piece: a launch has less than 2^32 threads
+    most = std::max<int64_t>(256, std::min(most, (int64_t{1} << 22) / ceil_div(T, kTurnTile) * kTurnTile));
     p->pieces = static_cast<int>(ceil_div(V, most));
     p->piece = ceil_div(ceil_div(V, p->pieces), 256) * 256;
     p->pieces = static_cast<int>(ceil_div(V, p->piece));

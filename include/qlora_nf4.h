@@ -462,9 +462,9 @@ int64_t qlora_head_loss_workspace_bytes(int64_t vocab, int64_t d_in, int64_t d_s
  *   scale   float32 [d_seq] or NULL (1): e.g. 1 / counted tokens for a mean
  *   loss    float32 [d_seq] (not scaled);  dX bf16 [d_seq, d_in] or NULL
  * d_in a multiple of 64; any vocab of a bf16 head. The logits are float32 sums; dX multiplies the
- * exponentials rounded to bf16 (float32 sums; the target's own column is kept apart in float32). An
- * infinite or NaN logit makes its token's loss and dX NaN or infinite, no other's. The result is
- * deterministic. Strides, alignment and errors as qlora_linear_fwd_ex; outputs and the workspace must
+ * exponentials rounded to bf16 (float32 sums; the target's own column is kept apart in float32). A
+ * token with an infinite or NaN logit may have a NaN or infinite loss and dX; no other token is
+ * touched by it. The result is deterministic. Strides, alignment and errors as qlora_linear_fwd_ex; outputs and the workspace must
  * not overlap an input, or each other.
  */
 int qlora_head_loss(const uint16_t* W, int64_t ldw, const uint8_t* codes, const int8_t* qconst, const float* qscale,

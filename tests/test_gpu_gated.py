@@ -25,7 +25,7 @@ CASES = [(64, 64, 1, 1, "silu", "int8"), (64, 128, 3, 0, "gelu", "int8"), (128, 
          (2752, 512, 1, 16, "silu", "none"), (1088, 2112, 24, 256, "gelu", "int8"), (128, 64, 257, 24, "silu", "int8"),
          (1024, 4032, 7, 16, "silu", "int8"), (192, 3968, 16, 5, "gelu", "none"), (9152, 64, 2, 11, "silu", "fp8"),
          (64, 4160, 4, 16, "gelu", "int8"), (640, 640, 9, 17, "silu", "int8"), (128, 2048, 33, 16, "silu", "int8"),
-         (66624, 64, 3, 16, "silu", "int8")]
+         (66624, 64, 3, 16, "silu", "int8"), (2112, 1024, 1540, 40, "silu", "int8"), (64, 2816, 3000, 16, "gelu", "fp8")]
 IDS = ["x".join(map(str, c)) for c in CASES]
 
 
@@ -277,3 +277,31 @@ def test_replayed_from_a_graph(m):
         wx, wd = qn.gated_bwd(layer, wg, dH)
         for g, w in zip(got, (wh, wg, wx, wd)):
             assert torch.equal(g, w)
+
+
+@pytest.mark.parametrize("m", [3, 40, 70])
+def test_offsets_past_2_gib(m):
+    """Both weights together 3.76 GB in bf16: the last outputs of the forward, the last columns and the sums
+    over all rows of the gradient."""
+    f, d = 65536, 14336
+    layer, normal = make(f, d, 8, "silu")
+    rows = torch.tensor([0, 1, f // 2, f - 2, f - 1], device=dev())
+    cols = torch.tensor([0, 63, d - 64, d - 1], device=dev())
+    X, dH = normal(m, d).bfloat16(), normal(m, f).bfloat16()
+    H, GU = qn.gated_fwd(layer, X, save=True)
+    dX, dGU = qn.gated_bwd(layer, GU, dH)
+    x, want, mass = X.double(), 0.0, 0.0
+    for k, (w, A, B, s) in enumerate(((layer.gate, layer.A_gate, layer.B_gate, layer.s_gate),
+                                      (layer.up, layer.A_up, layer.B_up, layer.s_up))):
+        W = qn.double_dequant(w)
+        A, B = A.double(), B.double()
+        y, a = x @ W[rows].double().T + s * (x @ A.T) @ B[rows].T, x.abs() @ W[rows].double().abs().T
+        low = abs(s) * (x.abs() @ A.abs().T) @ B[rows].abs().T
+        # d float32 products; the rank product's rounding; the output's
+        within(GU[:, k * f:(k + 1) * f][:, rows], y, 2 * d * F * a + (2 * B8 + 2 * d * F) * low + B8 * y.abs(), "G or U")
+        dY = dGU[:, k * f:(k + 1) * f].double()
+        Wc = W[:, cols].double()
+        want = want + dY @ Wc + s * (dY @ B) @ A[:, cols]
+        mass = mass + 2 * f * F * (dY.abs() @ Wc.abs()) + (2 * B8 + 2 * f * F) * abs(s) * (dY.abs() @ B.abs()) @ A[:, cols].abs()
+        del W
+    within(dX[:, cols], want, 2 * mass + B8 * want.abs(), "dX")

@@ -215,3 +215,11 @@ def test_replayed_from_a_graph(V, m, head):
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         assert torch.equal(got[2], qn.head_loss(own, X, t))
         check(full, X, t, scale, got[0], got[1])
+
+
+@pytest.mark.parametrize("m", [20, 200])
+def test_offsets_past_2_gib(m):
+    V, d = 30000, 49152
+    own, _, X, t, scale = make(V, d, m, 0.1)
+    loss, dX = qn.head_loss_grad(own, X, t, scale=scale)
+    check(own.double(), X, t, scale, loss, dX)

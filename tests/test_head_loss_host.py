@@ -45,6 +45,21 @@ def test_sizes():
     assert f(256000, 4096, 4096, 0, 1) <= f(128000, 4096, 4096, 0, 1) * 1.1
 
 
+def test_a_launch_has_less_than_2_32_threads():
+    """Two words per token and tile of a piece are kept, and per token six more: that tells the tiles of
+    256 x 256, of 512 threads each."""
+    d_seq = 1 << 24
+    got = _lib.lib().qlora_head_loss_workspace_bytes(65536, 64, d_seq, 0, 0)
+    tiles = (got - 4 * 6 * d_seq) / (8 * d_seq) * (d_seq / 256)
+    assert 0 < tiles * 512 < 2 ** 32 and got > 0
+
+
+def test_tensors_off_the_current_device_are_refused(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="not the current device"):
+        _lib._own_stream(torch.device("cuda", 0))
+
+
 def test_call_checks():
     b = torch.bfloat16
     W, X, t = torch.zeros(100, 64, dtype=b), torch.zeros(5, 64, dtype=b), torch.zeros(5, dtype=torch.int64)
