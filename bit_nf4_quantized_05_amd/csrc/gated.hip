@@ -8,6 +8,8 @@
 // G and U of an output are sums of the same lane (gemm_turns.h: the two column halves of a tile).
 // The activation and the product are then register arithmetic in the epilogue, G and U reach memory
 // only where the gradient needs them, and X is read once.
+// Bound by the matrix pipes at the clock that they leave, and by whole rounds of tiles: 2048 tokens of
+// 11008 x 4096 (688 tiles on 256 CUs) take 282 us with G and U kept (1.32 PFLOP/s), dX there 250 (1.49).
 #include <hip/hip_runtime.h>
 
 #include "gated.h"
@@ -161,7 +163,8 @@ void gated_split_reduce(TurnSplit s, GatedOut o) {
 // The gradient's rank products: T_w = s_w dW_w B_w, dG for w = 0 and dU for w = 1, bf16 [M, k2] with w's
 // `pad` columns at w pad. Tiles of 64 tokens x 64 ranks over slices of K (their partial sums are added by
 // gated_ranks_reduce). kCols: B [d_ff, r] as it is, r % 8 == 0, its rows along K; else B^T.
-// Bound by the reads of dGU, which the launch before has just written.
+// Bound by the reads of dGU, which the launch before has just written: 90 MB in 30 us at 2048 tokens of
+// 11008 x 4096 (tiles of 128 tokens and their 32 ranks a wave took 32).
 struct GatedRanks {
     TurnArgs g[2];
     uint16_t* T; float* part;         // part [slices][M][2 pad] where there are several
