@@ -510,6 +510,13 @@ __device__ __forceinline__ void gated_bt_job(const GatedPrologueArgs& a, int b) 
     *reinterpret_cast<uint4*>(a.bt[w] + j * a.d_ff + k) = uint4{v[0], v[1], v[2], v[3]};
 }
 
+// Both weights' dequantisation, workgroup b of a.p.deq.n + a.deq_up.n
+__device__ __forceinline__ void gated_dequant_job(const GatedPrologueArgs& a, int b, const NF4Tables& tab, float* s_code, float* s_ahat) {
+    if (threadIdx.x < 16) s_code[threadIdx.x] = tab.code[threadIdx.x];
+    if (b < a.p.deq.n) dequant_rows_job(a.p.deq, b, s_code, s_ahat);
+    else dequant_rows_job(a.deq_up, b - a.p.deq.n, s_code, s_ahat);
+}
+
 template <int NT>
 __global__ __launch_bounds__(256)
 void gated_prologue_kernel(GatedPrologueArgs a, NF4Tables tab) {
@@ -521,6 +528,19 @@ void gated_prologue_kernel(GatedPrologueArgs a, NF4Tables tab) {
         return;
     }
     b -= a.p.n_pre;
+    if (b < a.n_adapt) {
+        gated_adapt_job(a, b);
+        return;
+    }
+    float* lds = reinterpret_cast<float*>(s1.x);
+    gated_dequant_job(a, b - a.n_adapt, tab, lds, lds + 16);
+}
+
+// The gradient's: no rank products here, so no LDS stages, and more workgroups fit a CU.
+__global__ __launch_bounds__(256)
+void gated_back_prologue_kernel(GatedPrologueArgs a, NF4Tables tab) {
+    __shared__ float s_code[16], s_ahat[kDeqPerWG / 64];
+    int b = blockIdx.x;
     if (b < a.n_grad) {
         gated_grad_job(a.grad, b);
         return;
@@ -535,10 +555,7 @@ void gated_prologue_kernel(GatedPrologueArgs a, NF4Tables tab) {
         gated_bt_job(a, b);
         return;
     }
-    b -= a.n_bt;
-    char* lds = reinterpret_cast<char*>(s1.x);
-    if (b < a.p.deq.n) dequant_jobs(a.p.deq, b, tab, lds);
-    else dequant_jobs(a.deq_up, b - a.p.deq.n, tab, lds);
+    gated_dequant_job(a, b - a.n_bt, tab, s_code, s_ahat);
 }
 
 // ---------------------------------------------------------------------------
@@ -1072,7 +1089,11 @@ hipError_t launch_gated_prologue(const GatedCall& c, bool backward, const GatedP
     }
     const dim3 grid(static_cast<unsigned>(a.p.n_pre + a.n_grad + a.n_adapt + a.n_bt + a.p.deq.n + a.deq_up.n));
     const NF4Tables& tab = tables();
-    const int NT = a.p.n_pre > 0 ? (c.r + 31) / 32 : 1;
+    if (backward) {
+        QN_LAUNCH("gated_back_prologue_kernel", st, gated_back_prologue_kernel, grid, dim3(256), 0, st, a, tab);
+        return hipGetLastError();
+    }
+    const int NT = std::max(1, (c.r + 31) / 32);
     switch (NT) {
 #define QN_PRO_CASE(T) \
         case T: QN_LAUNCH("gated_prologue_kernel", st, gated_prologue_kernel<T>, grid, dim3(256), 0, st, a, tab); break;
