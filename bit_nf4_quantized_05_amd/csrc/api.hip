@@ -305,7 +305,7 @@ GradWs grad_ws(int64_t d_out, int64_t d_in, int64_t d_seq, int r) {
 // workspaces of qlora_gated_fwd and qlora_gated_bwd
 namespace {
 struct GatedWs {
-    int64_t what, t, adapt, ppart[2], bt[2], part, bytes;
+    int64_t what, t, adapt, rpart, bt[2], part, bytes;
 };
 
 GatedWs gated_ws(int64_t d_ff, int64_t d_in, int64_t d_seq, int r, bool bwd) {
@@ -324,11 +324,8 @@ GatedWs gated_ws(int64_t d_ff, int64_t d_in, int64_t d_seq, int r, bool bwd) {
     w.what = take(4 * d_ff * d_in);                                                  // both weights
     w.t = take(2 * d_seq * qn::gated_k2(r));                                         // both rank products
     w.adapt = take(2 * (bwd ? d_in : 2 * d_ff) * qn::gated_k2(r));                   // both adapters
-    for (int i = 0; i < 2; ++i) {
-        w.ppart[i] = take(bwd ? (i == 0 ? 4 * qn::gated_ranks_floats(d_seq, d_ff, r) : 0)
-                              : r > 0 ? prepass_part_bytes(d_seq, d_in, r) : 0);
-        w.bt[i] = take(bwd && !qn::gated_reads_b(r) ? 2 * static_cast<int64_t>(r) * d_ff : 0);
-    }
+    w.rpart = take(4 * qn::gated_ranks_floats(d_seq, bwd ? d_ff : d_in, r));         // their partial sums
+    for (int i = 0; i < 2; ++i) w.bt[i] = take(bwd && !qn::gated_reads_b(r) ? 2 * static_cast<int64_t>(r) * d_ff : 0);
     w.part = take(4 * (bwd ? qn::gated_dx_part_floats(d_seq, d_ff, d_in) : qn::gated_part_floats(d_seq, d_ff, d_in)));
     w.bytes = off;
     return w;
@@ -1089,12 +1086,12 @@ int qlora_gated_fwd(const uint8_t* codes_g, const int8_t* qconst_g, const float*
     qn::GatedProlog o{};
     o.what = reinterpret_cast<uint16_t*>(ws + w.what);
     o.adapt = reinterpret_cast<uint16_t*>(ws + w.adapt);
-    o.X = X; o.ldx = ldx;
-    o.pre_out = reinterpret_cast<uint16_t*>(ws + w.t);
-    for (int i = 0; i < 2; ++i) o.ppart[i] = reinterpret_cast<float*>(ws + w.ppart[i]);
+    o.in = X; o.ld_in = ldx;
+    o.t = reinterpret_cast<uint16_t*>(ws + w.t);
+    o.part = reinterpret_cast<float*>(ws + w.rpart);
     hipError_t e = qn::launch_gated_prologue(c, false, o, st);
     if (e != hipSuccess) return hip_fail(e, "qlora_gated_fwd (prologue)");
-    e = qn::launch_gated_gemm(c, X, ldx, o.what, o.pre_out, o.adapt, H, ldh, GU, ldgu, reinterpret_cast<float*>(ws + w.part),
+    e = qn::launch_gated_gemm(c, X, ldx, o.what, o.t, o.adapt, H, ldh, GU, ldgu, reinterpret_cast<float*>(ws + w.part),
                               st);
     if (e != hipSuccess) return hip_fail(e, "qlora_gated_fwd (gemm)");
     return 0;
@@ -1118,21 +1115,19 @@ int qlora_gated_bwd(const uint8_t* codes_g, const int8_t* qconst_g, const float*
     if (int rc = check_workspace(workspace, workspace_bytes, w.bytes)) return rc;
     char* ws = static_cast<char*>(workspace);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    // the elementwise part beside the layouts, then the rank products of dG and dU, then dX
+    // the elementwise part beside the layouts, the rank products of dG and dU, dX
     qn::GatedProlog o{};
     o.what = reinterpret_cast<uint16_t*>(ws + w.what);
     o.adapt = reinterpret_cast<uint16_t*>(ws + w.adapt);
     o.grad = qn::GatedGradArgs{dH, lddh, GU, ldgu, dGU, lddgu, static_cast<int>(d_seq), static_cast<int>(d_ff), act};
+    o.in = dGU; o.ld_in = lddgu;
+    o.t = reinterpret_cast<uint16_t*>(ws + w.t);
+    o.part = reinterpret_cast<float*>(ws + w.rpart);
     if (!qn::gated_reads_b(r))
         for (int i = 0; i < 2; ++i) o.bt[i] = reinterpret_cast<uint16_t*>(ws + w.bt[i]);
     hipError_t e = qn::launch_gated_prologue(c, true, o, st);
     if (e != hipSuccess) return hip_fail(e, "qlora_gated_bwd (prologue)");
-    uint16_t* t = reinterpret_cast<uint16_t*>(ws + w.t);
-    if (r > 0) {
-        e = qn::launch_gated_ranks(c, dGU, lddgu, o.bt, t, reinterpret_cast<float*>(ws + w.ppart[0]), st);
-        if (e != hipSuccess) return hip_fail(e, "qlora_gated_bwd (rank products)");
-    }
-    e = qn::launch_gated_dx(c, dGU, lddgu, o.what, t, o.adapt, dX, lddx, reinterpret_cast<float*>(ws + w.part), st);
+    e = qn::launch_gated_dx(c, dGU, lddgu, o.what, o.t, o.adapt, dX, lddx, reinterpret_cast<float*>(ws + w.part), st);
     if (e != hipSuccess) return hip_fail(e, "qlora_gated_bwd (gemm)");
     return 0;
 }

@@ -111,16 +111,18 @@ __device__ __forceinline__ void gated_grad_job(const GatedGradArgs& a, int b) {
 }
 
 // ---- prologue.hip ----
-// Both weights dequantised to what, gate above up, [2 d_ff, d_in], and both adapters to adapt.
-// Forward: B, [2 d_ff, k2]; and (r > 0) the rank products pre_out [M, k2] = s_w X A_w^T, by partial sums
-// in ppart. Gradient: A, [k2, d_in]; the elementwise part grad and, where bt is not null, B^T [r, d_ff].
-constexpr int64_t kGatedOneSlice = 512;
+// Both weights dequantised to what, gate above up, [2 d_ff, d_in], and both adapters to adapt
+// (forward: B, [2 d_ff, k2]; gradient: A, [k2, d_in]); in the gradient the elementwise part grad and, where
+// bt is not null, B^T [r, d_ff]. Then (r > 0) the rank products of in: t [M, k2] = s_w X A_w^T, or
+// s_w (half w of dGU) B_w; part: gated_ranks_floats, K = d_in or d_ff.
 struct GatedProlog {
     uint16_t* what; uint16_t* adapt;
-    const uint16_t* X; int64_t ldx; uint16_t* pre_out; float* ppart[2];
-    uint16_t* bt[2];
+    const uint16_t* in; int64_t ld_in; uint16_t* t; float* part;
+    uint16_t* bt[2];                  // gradient: null where B itself can be read (gated_reads_b)
     GatedGradArgs grad;
 };
+inline bool gated_reads_b(int r) { return r % 8 == 0; }
+int64_t gated_ranks_floats(int64_t M, int64_t K, int r);
 hipError_t launch_gated_prologue(const GatedCall& c, bool backward, const GatedProlog& o, hipStream_t st);
 
 // W_hat [d_out, d_in] bf16, row-major (d_in % 64 == 0)
@@ -134,12 +136,6 @@ int64_t gated_part_floats(int64_t M, int64_t d_ff, int64_t d_in);
 hipError_t launch_gated_gemm(const GatedCall& c, const uint16_t* X, int64_t ldx, const uint16_t* what, const uint16_t* t,
                              const uint16_t* adapt, uint16_t* H, int64_t ldh, uint16_t* GU, int64_t ldgu, float* part,
                              hipStream_t st);
-// t [M, k2] = s_w (half w of dGU) B_w; bt: B^T of both, or null (r % 8 == 0: B itself is read); part:
-// gated_ranks_floats
-inline bool gated_reads_b(int r) { return r % 8 == 0; }
-int64_t gated_ranks_floats(int64_t M, int64_t d_ff, int r);
-hipError_t launch_gated_ranks(const GatedCall& c, const uint16_t* dGU, int64_t lddgu, uint16_t* const (&bt)[2], uint16_t* t,
-                              float* part, hipStream_t st);
 // dX from dGU, what [2 d_ff, d_in], t [M, k2] and adapt [k2, d_in]; part: gated_dx_part_floats
 int64_t gated_dx_part_floats(int64_t M, int64_t d_ff, int64_t d_in);
 hipError_t launch_gated_dx(const GatedCall& c, const uint16_t* dGU, int64_t lddgu, const uint16_t* what, const uint16_t* t,

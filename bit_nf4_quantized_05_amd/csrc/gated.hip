@@ -160,61 +160,6 @@ void gated_split_reduce(TurnSplit s, GatedOut o) {
     else gated_store<false>(o, m, n, gv, uv);
 }
 
-// The gradient's rank products: T_w = s_w dW_w B_w, dG for w = 0 and dU for w = 1, bf16 [M, k2] with w's
-// `pad` columns at w pad. Tiles of 64 tokens x 64 ranks over slices of K (their partial sums are added by
-// gated_ranks_reduce). kCols: B [d_ff, r] as it is, r % 8 == 0, its rows along K; else B^T.
-// Bound by the reads of dGU, which the launch before has just written: 90 MB in 30 us at 2048 tokens of
-// 11008 x 4096 (tiles of 128 tokens and their 32 ranks a wave took 32).
-struct GatedRanks {
-    TurnArgs g[2];
-    uint16_t* T; float* part;         // part [slices][M][2 pad] where there are several
-    float s[2];
-    int M, r, pad, slices, kper;
-};
-
-template <bool kCols>
-__global__ __launch_bounds__(kFewThreads, 2)
-void gated_ranks_kernel(GatedRanks o) {
-    const int tiles_m = (o.M + kFewTile - 1) / kFewTile, tiles_r = (o.pad + kFewTile - 1) / kFewTile;
-    int item = turn_item(static_cast<int>(blockIdx.x), 2 * tiles_m * tiles_r * o.slices);
-    if (item < 0) return;
-    const int n0 = item % tiles_r * kFewTile;
-    item /= tiles_r;
-    const int w = __builtin_amdgcn_readfirstlane(item & 1), m0 = (item >> 1) % tiles_m * kFewTile;
-    const int slice = __builtin_amdgcn_readfirstlane((item >> 1) / tiles_m);
-    const TurnArgs& g = o.g[w];
-    const int last_p = o.M - 1, last_q = o.r - (kCols ? 8 : 1);
-    const int kb = slice * o.kper, ke = min(kb + o.kper, g.kt1);
-    FewSums acc;
-    gemm_few<false, kCols>(
-        g, [=](int i) { return static_cast<uint32_t>(min(m0 + i, last_p)); },
-        [=](int i) { return static_cast<uint32_t>(min(n0 + i, last_q)); }, kb, ke, false, acc);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int m = m0 + 32 * (wave >> 1) + 16 * i + (lane & 15);
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int n = n0 + 32 * (wave & 1) + 16 * j + 4 * (lane >> 4);
-            if (m >= o.M || n >= o.pad) continue;
-            f32x4t v = acc[0][0][i][j];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = n + e < o.r ? o.s[w] * v[e] : 0.0f;
-            const int64_t at = static_cast<int64_t>(m) * (2 * o.pad) + w * o.pad + n;
-            if (o.slices == 1) *reinterpret_cast<uint2*>(o.T + at) = uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-            else *reinterpret_cast<f32x4t*>(o.part + static_cast<int64_t>(slice) * o.M * (2 * o.pad) + at) = v;
-        }
-    }
-}
-
-__global__ __launch_bounds__(256)
-void gated_ranks_reduce(const float* part, uint16_t* T, int64_t n, int slices) {
-    const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
-    if (at >= n) return;
-    const float4 v = ordered_sum4<8>(part + at, n, slices);
-    *reinterpret_cast<uint2*>(T + at) = uint2{bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
-}
-
 // dX = dGU [W_g; W_u] + U' [A_g; A_u]: a plain product whose weights lie with their rows along K
 // (read by transposing LDS reads), bf16 out
 struct GatedDx {
@@ -314,17 +259,6 @@ TurnSplit dx_split(int64_t M, int64_t d_ff, int64_t d_in) {
                                  : turn_split(M, ceil_div(d_in, kTurnTile), 2 * d_ff / kTurnK);
 }
 
-// Slices of the rank products' K: two workgroups a CU, 8 K-steps or more each
-struct RankSplit { int slices, kper; };
-RankSplit rank_split(int64_t M, int64_t d_ff, int r) {
-    const int64_t kt = d_ff / kTurnK, tiles = 2 * ceil_div(M, kFewTile) * ceil_div(gated_pad(r), kFewTile);
-    const int64_t want = std::max<int64_t>(1, std::min(512 / tiles, kt / 8));
-    RankSplit s;
-    s.kper = static_cast<int>(ceil_div(kt, want));
-    s.slices = static_cast<int>(ceil_div(kt, s.kper));
-    return s;
-}
-
 // P2 Q2^T of a call with adapters: adapt's rows are ldq2 long
 void add_ranks(TurnArgs& g, const uint16_t* t, const uint16_t* adapt, int k2, int64_t ldq2, int64_t M, int64_t N) {
     if (k2 == 0) return;
@@ -354,35 +288,6 @@ hipError_t launch_gated_gemm(const GatedCall& c, const uint16_t* X, int64_t ldx,
     else QN_LAUNCH("gated_gemm_kernel", st, gated_gemm_kernel<false>, grid, dim3(kTurnThreads), 0, st, g, s, o);
     const dim3 rgrid(static_cast<unsigned>((s.rem << (2 * s.lt - 3)) / 256));
     if (s.splits > 1) QN_LAUNCH("gated_split_reduce", st, gated_split_reduce, rgrid, dim3(256), 0, st, s, o);
-    return hipGetLastError();
-}
-
-int64_t gated_ranks_floats(int64_t M, int64_t d_ff, int r) {
-    const RankSplit s = rank_split(M, d_ff, std::max(r, 1));
-    return r > 0 && s.slices > 1 ? s.slices * M * gated_k2(r) : 0;
-}
-
-hipError_t launch_gated_ranks(const GatedCall& c, const uint16_t* dGU, int64_t lddgu, uint16_t* const (&bt)[2], uint16_t* t,
-                              float* part, hipStream_t st) {
-    const RankSplit s = rank_split(c.M, c.d_ff, c.r);
-    GatedRanks o{};
-    for (int w = 0; w < 2; ++w) {
-        const uint16_t* P = dGU + w * c.d_ff;
-        o.g[w] = bt[w] == nullptr ? turn_args(P, lddgu, c.M, c.B[w], c.r, c.d_ff, c.d_ff)
-                                  : turn_args(P, lddgu, c.M, bt[w], c.d_ff, c.r, c.d_ff);
-        o.s[w] = c.s[w];
-    }
-    o.T = t; o.part = part; o.M = static_cast<int>(c.M); o.r = c.r; o.pad = gated_pad(c.r);
-    o.slices = s.slices; o.kper = s.kper;
-    const int64_t items = 2 * ceil_div(c.M, kFewTile) * ceil_div(o.pad, kFewTile) * s.slices;
-    const dim3 grid(static_cast<unsigned>(ceil_div(items, 8) * 8));
-    if (bt[0] == nullptr) QN_LAUNCH("gated_ranks_kernel", st, gated_ranks_kernel<true>, grid, dim3(kFewThreads), 0, st, o);
-    else QN_LAUNCH("gated_ranks_kernel", st, gated_ranks_kernel<false>, grid, dim3(kFewThreads), 0, st, o);
-    if (s.slices > 1) {
-        const int64_t n = c.M * gated_k2(c.r);
-        QN_LAUNCH("gated_ranks_reduce", st, gated_ranks_reduce, dim3(static_cast<unsigned>(ceil_div(n, 1024))), dim3(256), 0,
-                  st, part, t, n, s.slices);
-    }
     return hipGetLastError();
 }
 

@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 
 #include "gated.h"
+#include "gemm_few.h"
 #include "internal.h"
 #include "mfma_device.h"
 #include "multi.h"
@@ -448,30 +449,92 @@ void prologue_kernel(PrologueArgs a, NF4Tables tab) {
 }
 
 // ---------------------------------------------------------------------------
-// The gated block's two projections side by side (gated.hip): both weights' dequantisation, both
-// adapters and, forward, both pre-passes (rows of up to kGatedOneSlice in one slice: the sum of slices
-// is a launch more), in the gradient its elementwise part, in one launch. The rank columns of the gate come first,
-// pad of them, then those of the up projection.
+// The gated block's two projections side by side (gated.hip): in one launch both weights'
+// dequantisation, both adapters' layouts and, in the gradient, its elementwise part; then the rank
+// products. The rank columns of the gate come first, pad of them, then those of the up projection.
 // ---------------------------------------------------------------------------
-struct GatedPrologueArgs {
-    PrologueArgs p;                  // pre[0], pre[1], M, r, r_pad (pad); deq: the gate's
-    DeqJob deq_up;
+
+// T_w = s_w P_w R_w^T, bf16 [M, k2] with w's `pad` columns at w pad. Forward: P = X, R = A [r, d_in].
+// Gradient: P = dG and dU, R^T = B [d_ff, r] as it is (kCols: its rows lie along K; r % 8 == 0) or R =
+// B^T. Tiles of 64 tokens x 64 ranks over slices of K, whose partial sums gated_ranks_reduce adds.
+// Bound by the reads of P: the gradient's, 90 MB that the launch before has written, take 30 us at 2048
+// tokens of 11008 x 4096 (tiles of 128 tokens, 32 a wave, 32).
+struct GatedRanks {
+    TurnArgs g[2];
+    uint16_t* T; float* part;         // part [slices][M][2 pad] where there are several
+    float s[2];
+    int M, r, pad, slices, kper;
+};
+__host__ __device__ inline int gated_rank_items(const GatedRanks& o) {
+    return 2 * ((o.M + kFewTile - 1) / kFewTile) * ((o.pad + kFewTile - 1) / kFewTile) * o.slices;
+}
+
+template <bool kCols>
+__device__ __forceinline__ void gated_ranks_job(const GatedRanks& o, int item) {
+    const int tiles_m = (o.M + kFewTile - 1) / kFewTile, tiles_r = (o.pad + kFewTile - 1) / kFewTile;
+    const int n0 = item % tiles_r * kFewTile;
+    item /= tiles_r;
+    const int w = __builtin_amdgcn_readfirstlane(item & 1), m0 = (item >> 1) % tiles_m * kFewTile;
+    const int slice = __builtin_amdgcn_readfirstlane((item >> 1) / tiles_m);
+    const TurnArgs& g = o.g[w];
+    const int last_p = o.M - 1, last_q = o.r - (kCols ? 8 : 1);
+    const int kb = slice * o.kper, ke = min(kb + o.kper, g.kt1);
+    FewSums acc;
+    gemm_few<false, kCols>(
+        g, [=](int i) { return static_cast<uint32_t>(min(m0 + i, last_p)); },
+        [=](int i) { return static_cast<uint32_t>(min(n0 + i, last_q)); }, kb, ke, false, acc);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int m = m0 + 32 * (wave >> 1) + 16 * i + (lane & 15);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int n = n0 + 32 * (wave & 1) + 16 * j + 4 * (lane >> 4);
+            if (m >= o.M || n >= o.pad) continue;
+            f32x4t v = acc[0][0][i][j];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = n + e < o.r ? o.s[w] * v[e] : 0.0f;
+            const int64_t at = static_cast<int64_t>(m) * (2 * o.pad) + w * o.pad + n;
+            if (o.slices == 1) *reinterpret_cast<uint2*>(o.T + at) = uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+            else *reinterpret_cast<f32x4t*>(o.part + static_cast<int64_t>(slice) * o.M * (2 * o.pad) + at) = v;
+        }
+    }
+}
+
+template <bool kCols>
+__global__ __launch_bounds__(kFewThreads, 2)
+void gated_ranks_kernel(GatedRanks o) {
+    const int item = turn_item(static_cast<int>(blockIdx.x), gated_rank_items(o));
+    if (item >= 0) gated_ranks_job<kCols>(o, item);
+}
+
+__global__ __launch_bounds__(256)
+void gated_ranks_reduce(const float* part, uint16_t* T, int64_t n, int slices) {
+    const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+    if (at >= n) return;
+    const float4 v = ordered_sum4<8>(part + at, n, slices);
+    *reinterpret_cast<uint2*>(T + at) = uint2{bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
+}
+
+struct GatedLayoutArgs {
+    DeqJob deq[2];
     GatedGradArgs grad;              // the gradient's elementwise part (n_grad workgroups)
     const uint16_t* A[2]; const uint16_t* B[2];
     uint16_t* adst;                  // forward [2 d_ff, k2], gradient [k2, d_in]
     uint16_t* bt[2];                 // gradient: B^T [r, d_ff], or null
     int64_t d_ff, d_in;
-    int k2, backward, n_adapt, n_bt, n_grad;
+    int r, pad, k2, n_ranks, n_adapt, n_bt, n_grad;
 };
 
 // 8 entries of a row of the adapters' layout. Forward: the gate's d_ff rows of B, then the up
 // projection's, each at its own rank columns with zeros at the other's. Gradient: the rows of A_g,
 // zeros up to pad, and so A_u.
-__device__ __forceinline__ void gated_adapt_job(const GatedPrologueArgs& a, int b) {
-    const int r = a.p.r, pad = a.p.r_pad;
+template <bool kBack>
+__device__ __forceinline__ void gated_adapt_job(const GatedLayoutArgs& a, int b) {
+    const int r = a.r, pad = a.pad;
     const int64_t c = static_cast<int64_t>(b) * 256 + threadIdx.x;
     uint4 v = uint4{0u, 0u, 0u, 0u};
-    if (a.backward) {
+    if constexpr (kBack) {
         const int64_t cpr = a.d_in / 8;
         if (c >= a.k2 * cpr) return;
         const int j = static_cast<int>(c / cpr), w = j >= pad ? 1 : 0, q = j - w * pad;
@@ -496,66 +559,53 @@ __device__ __forceinline__ void gated_adapt_job(const GatedPrologueArgs& a, int 
 
 // 8 entries of a row of B_g^T or B_u^T, where the rank products cannot read B as it is (its rows of
 // r % 8 != 0 entries start off 16-byte boundaries). Single entries of 8 rows are read.
-__device__ __forceinline__ void gated_bt_job(const GatedPrologueArgs& a, int b) {
+__device__ __forceinline__ void gated_bt_job(const GatedLayoutArgs& a, int b) {
     const int64_t cpr = a.d_ff / 8;
     int64_t c = static_cast<int64_t>(b) * 256 + threadIdx.x;
-    const int w = c >= a.p.r * cpr ? 1 : 0;
-    c -= w * a.p.r * cpr;
-    if (c >= a.p.r * cpr) return;
-    const int j = static_cast<int>(c % a.p.r);                // neighbouring lanes: one row of B
-    const int64_t k = c / a.p.r * 8;
+    const int w = c >= a.r * cpr ? 1 : 0;
+    c -= w * a.r * cpr;
+    if (c >= a.r * cpr) return;
+    const int j = static_cast<int>(c % a.r);                // neighbouring lanes: one row of B
+    const int64_t k = c / a.r * 8;
     uint32_t v[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e >> 1] |= static_cast<uint32_t>(a.B[w][(k + e) * a.p.r + j]) << (16 * (e & 1));
+    for (int e = 0; e < 8; ++e) v[e >> 1] |= static_cast<uint32_t>(a.B[w][(k + e) * a.r + j]) << (16 * (e & 1));
     *reinterpret_cast<uint4*>(a.bt[w] + j * a.d_ff + k) = uint4{v[0], v[1], v[2], v[3]};
 }
 
-// Both weights' dequantisation, workgroup b of a.p.deq.n + a.deq_up.n
-__device__ __forceinline__ void gated_dequant_job(const GatedPrologueArgs& a, int b, const NF4Tables& tab, float* s_code, float* s_ahat) {
-    if (threadIdx.x < 16) s_code[threadIdx.x] = tab.code[threadIdx.x];
-    if (b < a.p.deq.n) dequant_rows_job(a.p.deq, b, s_code, s_ahat);
-    else dequant_rows_job(a.deq_up, b - a.p.deq.n, s_code, s_ahat);
-}
-
-template <int NT>
+// kRanks: the rank products of the forward in the same launch (their LDS leaves two workgroups a CU)
+template <bool kBack, bool kRanks>
 __global__ __launch_bounds__(256)
-void gated_prologue_kernel(GatedPrologueArgs a, NF4Tables tab) {
-    __shared__ PreStage<NT> s0, s1;
-    int b = blockIdx.x;
-    if (b < a.p.n_pre) {
-        const bool up = b >= a.p.pre[0].n;
-        prepass_job<NT, false>(a.p.pre[up], a.p, up ? b - a.p.pre[0].n : b, s0, s1);
-        return;
-    }
-    b -= a.p.n_pre;
-    if (b < a.n_adapt) {
-        gated_adapt_job(a, b);
-        return;
-    }
-    float* lds = reinterpret_cast<float*>(s1.x);
-    gated_dequant_job(a, b - a.n_adapt, tab, lds, lds + 16);
-}
-
-// The gradient's: no rank products here, so no LDS stages, and more workgroups fit a CU.
-__global__ __launch_bounds__(256)
-void gated_back_prologue_kernel(GatedPrologueArgs a, NF4Tables tab) {
+void gated_layout_kernel(GatedLayoutArgs a, GatedRanks ranks, NF4Tables tab) {
     __shared__ float s_code[16], s_ahat[kDeqPerWG / 64];
     int b = blockIdx.x;
-    if (b < a.n_grad) {
-        gated_grad_job(a.grad, b);
-        return;
+    if constexpr (kRanks) {
+        if (b < a.n_ranks) {
+            gated_ranks_job<false>(ranks, b);
+            return;
+        }
+        b -= a.n_ranks;
     }
-    b -= a.n_grad;
+    if constexpr (kBack) {
+        if (b < a.n_grad) {
+            gated_grad_job(a.grad, b);
+            return;
+        }
+        b -= a.n_grad;
+        if (b < a.n_bt) {
+            gated_bt_job(a, b);
+            return;
+        }
+        b -= a.n_bt;
+    }
     if (b < a.n_adapt) {
-        gated_adapt_job(a, b);
+        gated_adapt_job<kBack>(a, b);
         return;
     }
     b -= a.n_adapt;
-    if (b < a.n_bt) {
-        gated_bt_job(a, b);
-        return;
-    }
-    gated_dequant_job(a, b - a.n_bt, tab, s_code, s_ahat);
+    if (threadIdx.x < 16) s_code[threadIdx.x] = tab.code[threadIdx.x];
+    const int w = b >= a.deq[0].n ? 1 : 0;
+    dequant_rows_job(a.deq[w], b - w * a.deq[0].n, s_code, s_ahat);
 }
 
 // ---------------------------------------------------------------------------
@@ -1066,48 +1116,68 @@ hipError_t launch_prepass_pair(const uint16_t* P0, int64_t ldp0, int64_t K0, con
     return launch_prologue_args(a, false, r1_kmajor, st);
 }
 
+namespace {
+// Slices of the rank products' K: two workgroups a CU, 8 K-steps or more each
+void rank_split(int64_t M, int64_t K, int r, int* slices, int* kper) {
+    const int64_t kt = K / kTurnK, tiles = 2 * ((M + kFewTile - 1) / kFewTile) * ((gated_pad(r) + kFewTile - 1) / kFewTile);
+    const int64_t want = std::max<int64_t>(1, std::min(512 / tiles, kt / 8));
+    *kper = static_cast<int>((kt + want - 1) / want);
+    *slices = static_cast<int>((kt + *kper - 1) / *kper);
+}
+// Up to this many weights (both projections) the rank products join the forward's layouts: a launch less,
+// but their LDS leaves the dequantisation two workgroups a CU (a joined launch and two: 512 tokens of
+// 2048 x 4096 44.7 and 48.6 us, 2048 of 4096 x 4096 124.9 and 121.3, of 11008 x 4096 332 and 309).
+constexpr int64_t kRanksWithin = int64_t{1} << 24;
+}  // namespace
+
+int64_t gated_ranks_floats(int64_t M, int64_t K, int r) {
+    if (r == 0) return 0;
+    int slices, kper;
+    rank_split(M, K, r, &slices, &kper);
+    return slices > 1 ? slices * M * gated_k2(r) : 0;
+}
+
 hipError_t launch_gated_prologue(const GatedCall& c, bool backward, const GatedProlog& o, hipStream_t st) {
-    GatedPrologueArgs a{};
-    a.p.M = static_cast<int>(c.M); a.p.r = c.r; a.p.r_pad = gated_pad(c.r);
+    GatedLayoutArgs a{};
+    GatedRanks q{};
+    a.r = c.r; a.pad = gated_pad(c.r); a.k2 = gated_k2(c.r);
+    a.d_ff = c.d_ff; a.d_in = c.d_in; a.adst = o.adapt;
+    const bool bcols = backward && o.bt[0] == nullptr;
+    const int64_t K = backward ? c.d_ff : c.d_in;
     for (int w = 0; w < 2; ++w) {
         a.A[w] = c.A[w]; a.B[w] = c.B[w]; a.bt[w] = o.bt[w];
-        if (c.r > 0 && !backward)
-            a.p.pre[w] = make_job(o.X, o.ldx, c.M, c.d_in, c.A[w], c.d_in, o.pre_out + w * gated_pad(c.r), gated_k2(c.r),
-                                  c.s[w], c.d_in <= kGatedOneSlice ? nullptr : o.ppart[w]);
-        (w == 0 ? a.p.deq : a.deq_up) = make_dequant(c.codes[w], c.bc[w], c.d_ff, c.d_in, false, o.what + w * c.d_ff * c.d_in);
+        a.deq[w] = make_dequant(c.codes[w], c.bc[w], c.d_ff, c.d_in, false, o.what + w * c.d_ff * c.d_in);
+        if (c.r > 0) {
+            const uint16_t* R = backward ? (bcols ? c.B[w] : o.bt[w]) : c.A[w];
+            const uint16_t* in = backward ? o.in + w * c.d_ff : o.in;
+            q.g[w] = bcols ? turn_args(in, o.ld_in, c.M, R, c.r, K, K) : turn_args(in, o.ld_in, c.M, R, K, c.r, K);
+            q.s[w] = c.s[w];
+        }
     }
-    a.p.n_pre = a.p.pre[0].n + a.p.pre[1].n;
-    a.backward = backward ? 1 : 0;
-    a.d_ff = c.d_ff; a.d_in = c.d_in;
-    a.k2 = gated_k2(c.r);
-    a.adst = o.adapt;
+    if (c.r > 0) {
+        q.T = o.t; q.part = o.part; q.M = static_cast<int>(c.M); q.r = c.r; q.pad = a.pad;
+        rank_split(c.M, K, c.r, &q.slices, &q.kper);
+    }
+    const bool within = !backward && c.r > 0 && 2 * c.d_ff * c.d_in <= kRanksWithin;
+    a.n_ranks = within ? gated_rank_items(q) : 0;
     a.n_adapt = static_cast<int>(((backward ? c.d_in : 2 * c.d_ff) * (a.k2 / 8) + 255) / 256);
     if (backward) {
         a.grad = o.grad;
         a.n_grad = gated_grad_blocks(o.grad);
-        if (o.bt[0] != nullptr) a.n_bt = static_cast<int>((2 * c.r * (c.d_ff / 8) + 255) / 256);
+        if (c.r > 0 && !bcols) a.n_bt = static_cast<int>((2 * c.r * (c.d_ff / 8) + 255) / 256);
     }
-    const dim3 grid(static_cast<unsigned>(a.p.n_pre + a.n_grad + a.n_adapt + a.n_bt + a.p.deq.n + a.deq_up.n));
-    const NF4Tables& tab = tables();
-    if (backward) {
-        QN_LAUNCH("gated_back_prologue_kernel", st, gated_back_prologue_kernel, grid, dim3(256), 0, st, a, tab);
-        return hipGetLastError();
-    }
-    const int NT = std::max(1, (c.r + 31) / 32);
-    switch (NT) {
-#define QN_PRO_CASE(T) \
-        case T: QN_LAUNCH("gated_prologue_kernel", st, gated_prologue_kernel<T>, grid, dim3(256), 0, st, a, tab); break;
-        QN_PRO_CASE(1) QN_PRO_CASE(2) QN_PRO_CASE(3) QN_PRO_CASE(4)
-        QN_PRO_CASE(5) QN_PRO_CASE(6) QN_PRO_CASE(7) QN_PRO_CASE(8)
-#undef QN_PRO_CASE
-        default: return hipErrorInvalidValue;
-    }
-    if (a.p.pre[0].psplits > 1) {
-        const int blocks = static_cast<int>((c.M * (gated_pad(c.r) / 4) + 255) / 256);
-        const ReduceJob r0{a.p.pre[0].ppart, a.p.pre[0].OUT, a.p.pre[0].ldo, a.p.pre[0].psplits, a.p.pre[0].s};
-        const ReduceJob r1{a.p.pre[1].ppart, a.p.pre[1].OUT, a.p.pre[1].ldo, a.p.pre[1].psplits, a.p.pre[1].s};
-        QN_LAUNCH("prepass_reduce", st, prepass_reduce, dim3(static_cast<unsigned>(2 * blocks)), dim3(256), 0, st, r0, r1,
-                  blocks, a.p.M, 32 * NT, c.r, gated_pad(c.r));
+    const dim3 grid(static_cast<unsigned>(a.n_ranks + a.n_grad + a.n_adapt + a.n_bt + a.deq[0].n + a.deq[1].n));
+    if (backward) QN_LAUNCH("gated_layout_kernel", st, (gated_layout_kernel<true, false>), grid, dim3(256), 0, st, a, q, tables());
+    else if (within) QN_LAUNCH("gated_layout_kernel", st, (gated_layout_kernel<false, true>), grid, dim3(256), 0, st, a, q, tables());
+    else QN_LAUNCH("gated_layout_kernel", st, (gated_layout_kernel<false, false>), grid, dim3(256), 0, st, a, q, tables());
+    if (c.r == 0) return hipGetLastError();
+    const dim3 rgrid(static_cast<unsigned>((gated_rank_items(q) + 7) / 8 * 8));
+    if (!within && bcols) QN_LAUNCH("gated_ranks_kernel", st, gated_ranks_kernel<true>, rgrid, dim3(kFewThreads), 0, st, q);
+    else if (!within) QN_LAUNCH("gated_ranks_kernel", st, gated_ranks_kernel<false>, rgrid, dim3(kFewThreads), 0, st, q);
+    if (q.slices > 1) {
+        const int64_t n = c.M * a.k2;
+        QN_LAUNCH("gated_ranks_reduce", st, gated_ranks_reduce, dim3(static_cast<unsigned>((n + 1023) / 1024)), dim3(256), 0,
+                  st, o.part, o.t, n, q.slices);
     }
     return hipGetLastError();
 }
