@@ -39,8 +39,7 @@ namespace {
 struct PreJob {
     const uint16_t* P; int64_t ldp; int K;
     const uint16_t* R; int64_t ldr;  // R [r, K] row stride ldr, or k-major [K, r]
-    uint16_t* OUT; int64_t ldo;      // r_pad columns at this row stride
-    float s;
+    uint16_t* OUT;
     float* ppart;                    // [psplits][M][32 NT] fp32 partials when psplits > 1 and !cat
     int psplits, kper;               // K-slices and 64-wide K-chunks per slice
     int cat;                         // slice sp writes its own bf16 partial to OUT columns sp r .. sp r + r - 1
@@ -60,7 +59,7 @@ struct DeqJob {
 struct PrologueArgs {
     DeqJob deq;
     PreJob pre[2];
-    int M, r, r_pad;
+    int M, r, r_pad; float s;
     int adapt_mode;                 // 0 none, 1 pad columns, 2 transpose + pad
     int reps;                       // copies of the adapter's r columns side by side (one per slice of a cat job)
     const uint16_t* asrc; uint16_t* adst; int64_t arows, acols;
@@ -207,7 +206,7 @@ __device__ __forceinline__ void prepass_job(const PreJob& j, const PrologueArgs&
     if (m >= a.M) return;
     if (j.cat) {
         // r % 4 == 0: each group of 4 ranks is wholly below r or wholly past it
-        uint16_t* orow = j.OUT + static_cast<int64_t>(m) * j.ldo;
+        uint16_t* orow = j.OUT + static_cast<int64_t>(m) * a.r_pad;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -215,8 +214,8 @@ __device__ __forceinline__ void prepass_job(const PreJob& j, const PrologueArgs&
                 const int n = t * 32 + 8 * gq + 4 * (lane >> 5);
                 if (n < a.r)
                     *reinterpret_cast<uint2*>(orow + sp * a.r + n) =
-                        uint2{pack_bf16x2(j.s * acc[t][4 * gq], j.s * acc[t][4 * gq + 1]),
-                              pack_bf16x2(j.s * acc[t][4 * gq + 2], j.s * acc[t][4 * gq + 3])};
+                        uint2{pack_bf16x2(a.s * acc[t][4 * gq], a.s * acc[t][4 * gq + 1]),
+                              pack_bf16x2(a.s * acc[t][4 * gq + 2], a.s * acc[t][4 * gq + 3])};
             }
         }
         if (sp == j.psplits - 1)
@@ -225,7 +224,7 @@ __device__ __forceinline__ void prepass_job(const PreJob& j, const PrologueArgs&
         return;
     }
     if (j.psplits == 1) {
-        uint16_t* orow = j.OUT + static_cast<int64_t>(m) * j.ldo;
+        uint16_t* orow = j.OUT + static_cast<int64_t>(m) * a.r_pad;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -233,7 +232,7 @@ __device__ __forceinline__ void prepass_job(const PreJob& j, const PrologueArgs&
                 const int n = t * 32 + 8 * gq + 4 * (lane >> 5);
                 float v[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = n + e < a.r ? j.s * acc[t][4 * gq + e] : 0.0f;
+                for (int e = 0; e < 4; ++e) v[e] = n + e < a.r ? a.s * acc[t][4 * gq + e] : 0.0f;
                 *reinterpret_cast<uint2*>(orow + n) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
             }
         }
@@ -256,10 +255,10 @@ __device__ __forceinline__ void prepass_job(const PreJob& j, const PrologueArgs&
 // OUT[m, j] = bf16(s * sum of the slice partials in slice order) for j < r, 0 for
 // r <= j < r_pad; a thread takes 4 consecutive columns. The first `blocks0` workgroups
 // reduce job 0, the rest job 1.
-struct ReduceJob { const float* part; uint16_t* OUT; int64_t ldo; int splits; float s; };
+struct ReduceJob { const float* part; uint16_t* OUT; int splits; };
 
 __global__ __launch_bounds__(256)
-void prepass_reduce(ReduceJob j0, ReduceJob j1, int blocks0, int M, int ncols, int r, int r_pad) {
+void prepass_reduce(ReduceJob j0, ReduceJob j1, int blocks0, int M, int ncols, int r, int r_pad, float s) {
     const bool second = static_cast<int>(blockIdx.x) >= blocks0;
     const ReduceJob& jb = second ? j1 : j0;
     const int64_t idx = static_cast<int64_t>(second ? blockIdx.x - blocks0 : blockIdx.x) * 256 + threadIdx.x;
@@ -273,8 +272,8 @@ void prepass_reduce(ReduceJob j0, ReduceJob j1, int blocks0, int M, int ncols, i
         v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = j + e < r ? jb.s * v[e] : 0.0f;
-    *reinterpret_cast<uint2*>(jb.OUT + m * jb.ldo + j) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    for (int e = 0; e < 4; ++e) v[e] = j + e < r ? s * v[e] : 0.0f;
+    *reinterpret_cast<uint2*>(jb.OUT + m * r_pad + j) = uint2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
 // Adapter layouts; destination is [rows, r_pad] (pad) or [acols, r_pad] (transpose).
@@ -1001,9 +1000,8 @@ namespace {
 // split it replaces (more than max(16, that split's) 64-wide K-chunks: the pre-pass
 // would outlast the rest of the launch); otherwise fp32 partials in ppart (if given).
 PreJob make_job(const uint16_t* P, int64_t ldp, int64_t M, int64_t K, const uint16_t* R, int64_t ldr,
-                uint16_t* OUT, int64_t ldo, float s, float* ppart, int cat_max = 0) {
+                uint16_t* OUT, float* ppart, int cat_max = 0) {
     PreJob j;
-    j.ldo = ldo; j.s = s;
     j.P = P; j.ldp = ldp; j.K = static_cast<int>(K); j.R = R; j.ldr = ldr; j.OUT = OUT; j.ppart = ppart;
     const PrepassSplit ps = prepass_split(M, K);
     const int64_t nk = K / 64;
@@ -1064,10 +1062,10 @@ hipError_t launch_prologue_args(PrologueArgs& a, bool km0, bool km1, hipStream_t
     const int blocks0 = a.pre[0].n > 0 && a.pre[0].psplits > 1 && !a.pre[0].cat ? static_cast<int>(per_job) : 0;
     const int blocks1 = a.pre[1].n > 0 && a.pre[1].psplits > 1 && !a.pre[1].cat ? static_cast<int>(per_job) : 0;
     if (blocks0 + blocks1 > 0) {
-        const ReduceJob r0{a.pre[0].ppart, a.pre[0].OUT, a.pre[0].ldo, a.pre[0].psplits, a.pre[0].s};
-        const ReduceJob r1{a.pre[1].ppart, a.pre[1].OUT, a.pre[1].ldo, a.pre[1].psplits, a.pre[1].s};
+        const ReduceJob r0{a.pre[0].ppart, a.pre[0].OUT, a.pre[0].psplits};
+        const ReduceJob r1{a.pre[1].ppart, a.pre[1].OUT, a.pre[1].psplits};
         QN_LAUNCH("prepass_reduce", st, prepass_reduce, dim3(static_cast<unsigned>(blocks0 + blocks1)), dim3(256), 0,
-                  st, r0, r1, blocks0, a.M, 32 * NT, a.r, a.r_pad);
+                  st, r0, r1, blocks0, a.M, 32 * NT, a.r, a.r_pad, a.s);
     }
     return hipGetLastError();
 }
@@ -1085,9 +1083,9 @@ hipError_t launch_prologue(const uint8_t* codes, const BlockConsts& bc, int64_t 
     // take r of the r_pad columns and the adapter repeat once per slice: the GEMM's
     // LoRA K-steps then add the slice partials, and no reduction pass is needed.
     const int cat_max = adapt_mode != 0 && r % 4 == 0 ? r_pad / r : 0;
-    a.pre[0] = make_job(P, ldp, M, K, R, ldr, OUT, r_pad, s, ppart, cat_max);
+    a.pre[0] = make_job(P, ldp, M, K, R, ldr, OUT, ppart, cat_max);
     a.pre[1] = PreJob{};
-    a.M = static_cast<int>(M); a.r = r; a.r_pad = r_pad;
+    a.M = static_cast<int>(M); a.r = r; a.s = s; a.r_pad = r_pad;
     a.adapt_mode = adapt_mode; a.asrc = asrc; a.adst = adst; a.arows = arows; a.acols = acols;
     a.reps = a.pre[0].cat ? a.pre[0].psplits : 1;
     const int64_t adapt_elems = adapt_mode == 0 ? 0 : (adapt_mode == 1 ? arows : acols) * r_pad;
@@ -1109,9 +1107,9 @@ hipError_t launch_prepass_pair(const uint16_t* P0, int64_t ldp0, int64_t K0, con
                                const uint16_t* R1, int64_t ldr1, bool r1_kmajor, uint16_t* OUT1, float* ppart1,
                                int64_t M, int r, float s, int r_pad, hipStream_t st) {
     PrologueArgs a{};
-    a.pre[0] = make_job(P0, ldp0, M, K0, R0, ldr0, OUT0, r_pad, s, ppart0);
-    a.pre[1] = make_job(P1, ldp1, M, K1, R1, ldr1, OUT1, r_pad, s, ppart1);
-    a.M = static_cast<int>(M); a.r = r; a.r_pad = r_pad;
+    a.pre[0] = make_job(P0, ldp0, M, K0, R0, ldr0, OUT0, ppart0);
+    a.pre[1] = make_job(P1, ldp1, M, K1, R1, ldr1, OUT1, ppart1);
+    a.M = static_cast<int>(M); a.r = r; a.s = s; a.r_pad = r_pad;
     a.n_adapt = 0; a.reps = 1;
     return launch_prologue_args(a, false, r1_kmajor, st);
 }
