@@ -1,4 +1,4 @@
-// The gated feed-forward block's launches, shared by gated.hip, prologue.hip and api.hip.
+// The gated feed-forward block's launches, shared by gated.hip, gated_small.hip, prologue.hip and api.hip.
 //   H = act(G) * U,  G = W_g x + s_g B_g (A_g x),  U = W_u x + s_u B_u (A_u x)
 // and its gradient. Index 0 is the gate projection, 1 the up projection.
 #pragma once

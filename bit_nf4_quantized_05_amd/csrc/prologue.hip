@@ -2,8 +2,9 @@
 // the activations with A or B^T; up to two such products per launch), the adapter
 // layouts and the double dequantisation of the NF4 weight to bf16 W_hat or W_hat^T,
 // in one launch; the same for tokens of many adapters (multi_prologue_kernel); the
-// reduction of K-split pre-pass partials; and the small transpose of B that the input
-// gradient uses when the pre-pass cannot read B itself.
+// reduction of K-split pre-pass partials; the small transpose of B that the input
+// gradient uses when the pre-pass cannot read B itself; and the layouts and rank products
+// of the gated block (gated_layout_kernel, gated_ranks_kernel).
 #include <hip/hip_runtime.h>
 
 #include "gated.h"
