@@ -129,6 +129,19 @@ def test_no_token_counted():
     assert (qn.head_loss(own, X, t) == 0).all()
 
 
+@pytest.mark.parametrize("V,m", [(3001, 100), (20001, 300), (300, 9001)])
+def test_rows_without_a_target_are_not_read(V, m):
+    """A padded batch: whatever the rows of the tokens that are not counted hold, and their scales."""
+    own, _, X, t, scale = make(V, 64, m, 0.5)
+    live = (t >= 0) & (t < V)
+    loss, dX = qn.head_loss_grad(own, X, t, scale=scale)
+    bad, wild = X.clone(), scale.clone()
+    bad[~live] = torch.tensor([float("nan"), float("inf")], device=dev()).repeat(32).bfloat16()
+    wild[~live] = float("nan")
+    l2, d2 = qn.head_loss_grad(own, bad, t, scale=wild)
+    assert torch.equal(l2, loss) and torch.equal(d2, dX) and torch.equal(qn.head_loss(own, bad, t), qn.head_loss(own, X, t))
+
+
 @pytest.mark.parametrize("V", [3001, 20001])
 def test_infinities_stay_with_their_token(V):
     own, _, X, t, scale = make(V, 128, 300)
