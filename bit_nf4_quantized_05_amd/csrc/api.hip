@@ -338,10 +338,12 @@ bool gated_too_large(int64_t d_ff, int64_t d_in, int64_t d_seq, int r) {
     return reaches_4gib(2 * d_ff, std::max(d_in, k2)) || reaches_4gib(std::max(d_seq, d_in), k2);
 }
 
-bool gated_sizes_ok(int64_t d_ff, int64_t d_in, int64_t d_seq, int r) {
+// The sizes that a call takes with its activations at their least row strides. The forward's GU counts where
+// the call keeps it.
+bool gated_sizes_ok(int64_t d_ff, int64_t d_in, int64_t d_seq, int r, bool bwd) {
     return d_ff >= 1 && d_in >= 1 && d_seq >= 1 && r >= 0 && r <= 256 && d_ff % 64 == 0 && d_in % 64 == 0 &&
            d_in <= INT32_MAX && d_ff <= INT32_MAX / 2 && d_seq <= INT32_MAX && !gated_too_large(d_ff, d_in, d_seq, r) &&
-           !reaches_4gib(d_seq, std::max(2 * d_ff, d_in));
+           !reaches_4gib(d_seq, std::max(bwd ? 2 * d_ff : d_ff, d_in));
 }
 
 // What both gated calls check; `rows` are the row strides of the call's activations, each at
@@ -1054,11 +1056,11 @@ int qlora_adamw_moments(const uint8_t* m, const float* m_scale, const uint8_t* v
 }
 
 int64_t qlora_gated_fwd_workspace_bytes(int64_t d_ff, int64_t d_in, int64_t d_seq, int r) {
-    return gated_sizes_ok(d_ff, d_in, d_seq, r) ? gated_ws(d_ff, d_in, d_seq, r, false).bytes : 0;
+    return gated_sizes_ok(d_ff, d_in, d_seq, r, false) ? gated_ws(d_ff, d_in, d_seq, r, false).bytes : 0;
 }
 
 int64_t qlora_gated_bwd_workspace_bytes(int64_t d_ff, int64_t d_in, int64_t d_seq, int r) {
-    return gated_sizes_ok(d_ff, d_in, d_seq, r) ? gated_ws(d_ff, d_in, d_seq, r, true).bytes : 0;
+    return gated_sizes_ok(d_ff, d_in, d_seq, r, true) ? gated_ws(d_ff, d_in, d_seq, r, true).bytes : 0;
 }
 
 int qlora_gated_fwd(const uint8_t* codes_g, const int8_t* qconst_g, const float* qscale_g, const float* qmean_g,

@@ -411,7 +411,8 @@ int qlora_multi_bwd(const uint8_t* codes, const int8_t* qconst, const float* qsc
 #define QN_ACT_SILU 0
 #define QN_ACT_GELU 1
 
-/* Workspace bytes of the two calls (0 on sizes that the calls refuse). */
+/* Workspace bytes of the two calls, 0 on sizes that they refuse (of the forward, without GU: a call
+ * that keeps it also needs d_seq ldgu below 2^31). */
 int64_t qlora_gated_fwd_workspace_bytes(int64_t d_ff, int64_t d_in, int64_t d_seq, int r);
 int64_t qlora_gated_bwd_workspace_bytes(int64_t d_ff, int64_t d_in, int64_t d_seq, int r);
 
