@@ -381,13 +381,13 @@ int check_rows(const uint16_t* p, int64_t rows, int64_t cols, int64_t ld) {
 }
 
 // The sizes of a qlora_head_loss call, and its plan.
-int head_sizes(int64_t vocab, int64_t d_in, int64_t d_seq, bool nf4, bool grad, qn::HeadPlan* p) {
+int head_sizes(int64_t vocab, int64_t d_in, int64_t ldw, int64_t d_seq, bool nf4, bool grad, qn::HeadPlan* p) {
     if (vocab < 1 || d_in < 1 || d_seq < 1) return fail(-1, "sizes must be >= 1");
     if (d_in % 64 != 0 || (nf4 && vocab % 64 != 0)) return fail(-2, "d_in (and an NF4 head's rows) must be multiples of 64");
     if (d_in > INT32_MAX / 2 || vocab > INT32_MAX / 2 || d_seq > INT32_MAX / 2) return fail(-2, "dimension too large");
     int64_t n, n_b, n_g;
     if (!nf4_counts(vocab, d_in, &n, &n_b, &n_g)) return fail(-2, "weight too large");
-    if (reaches_4gib(d_seq, d_in) || !qn::head_plan(vocab, d_in, d_seq, nf4, grad, p))
+    if (reaches_4gib(d_seq, d_in) || !qn::head_plan(vocab, d_in, ldw, d_seq, nf4, grad, p))
         return fail(-2, "an operand reaches 4 GiB");
     return 0;
 }
@@ -1136,7 +1136,7 @@ int qlora_gated_bwd(const uint8_t* codes_g, const int8_t* qconst_g, const float*
 
 int64_t qlora_head_loss_workspace_bytes(int64_t vocab, int64_t d_in, int64_t d_seq, int nf4, int grad) {
     qn::HeadPlan p;
-    return head_sizes(vocab, d_in, d_seq, nf4 != 0, grad != 0, &p) == 0 ? p.bytes : 0;
+    return head_sizes(vocab, d_in, d_in, d_seq, nf4 != 0, grad != 0, &p) == 0 ? p.bytes : 0;
 }
 
 int qlora_head_loss(const uint16_t* W, int64_t ldw, const uint8_t* codes, const int8_t* qconst, const float* qscale,
@@ -1152,7 +1152,7 @@ int qlora_head_loss(const uint16_t* W, int64_t ldw, const uint8_t* codes, const 
         if (int rc = make_consts(dq, codes, qconst, qscale, qmean, &c.bc)) return rc;
         if (!aligned(codes, 16)) return fail(-1, "misaligned pointer (16 B for arrays, 256 B for the workspace)");
     }
-    if (int rc = head_sizes(vocab, d_in, d_seq, codes != nullptr, dX != nullptr, &p)) return rc;
+    if (int rc = head_sizes(vocab, d_in, codes != nullptr ? d_in : ldw, d_seq, codes != nullptr, dX != nullptr, &p)) return rc;
     if (W != nullptr) {
         // a piece of the head is an operand; the head itself may be larger
         if (int rc = check_rows(W, std::min(vocab, p.piece), d_in, ldw)) return rc;

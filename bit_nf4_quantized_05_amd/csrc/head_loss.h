@@ -20,13 +20,14 @@ struct HeadCall {
 };
 
 // Pieces of the vocabulary and the workspace's parts (byte offsets; parts a call does not use
-// have size 0). false: a size that the kernels do not take (an operand of 4 GiB or more).
+// have size 0). false: a size that the kernels do not take (an operand of 4 GiB or more). ldw: the head's
+// row stride (d of an NF4 head); the workspace for ldw = d is enough for any.
 struct HeadPlan {
     int64_t piece;                            // rows per piece, a multiple of 256
     int pieces, lt, slots;                    // tiles of 1 << lt; tiles of sums of the gradient's product
     int64_t ints, part, E, rows, wt, acc, bytes;
 };
-bool head_plan(int64_t V, int64_t d, int64_t T, bool nf4, bool grad, HeadPlan* p);
+bool head_plan(int64_t V, int64_t d, int64_t ldw, int64_t T, bool nf4, bool grad, HeadPlan* p);
 
 hipError_t launch_head_loss(const HeadCall& c, const HeadPlan& p, char* ws, hipStream_t st);
 

@@ -509,21 +509,27 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-bool head_plan(int64_t V, int64_t d, int64_t T, bool nf4, bool grad, HeadPlan* p) {
+bool head_plan(int64_t V, int64_t d, int64_t ldw, int64_t T, bool nf4, bool grad, HeadPlan* p) {
     constexpr int64_t kLimit = int64_t{1} << 31;     // elements of bf16 in 4 GiB
-    const bool keeps = grad || nf4;
     // Pieces of up to 65536 rows (dequantised rows of 4096: 512 MB), of a gradient 32768 and
     // fewer where T rows of exponentials would pass 2^27 (256 MB), but 4096 rows of them up to 2 GiB.
     int64_t most = grad ? 32768 : 65536;
     if (grad) most = std::min(most, std::max((int64_t{1} << 27) / T, std::min<int64_t>(4096, kLimit / 2 / T)) / 256 * 256);
     // up to 2^22 tiles of a piece: a launch has less than 2^32 threads
-    most = std::max<int64_t>(256, std::min(most, (int64_t{1} << 22) / ceil_div(T, kTurnTile) * kTurnTile));
-    p->pieces = static_cast<int>(ceil_div(V, most));
-    p->piece = ceil_div(ceil_div(V, p->pieces), 256) * 256;
-    p->pieces = static_cast<int>(ceil_div(V, p->piece));
+    most = std::min(most, (int64_t{1} << 22) / ceil_div(T, kTurnTile) * kTurnTile);
+    auto cut = [&](int64_t ld) {                     // in even pieces that stay below 4 GiB at this row stride
+        most = std::max<int64_t>(256, std::min(most, (kLimit - 1) / ld / 256 * 256));
+        p->pieces = static_cast<int>(ceil_div(V, most));
+        p->piece = ceil_div(ceil_div(V, p->pieces), 256) * 256;
+        p->pieces = static_cast<int>(ceil_div(V, p->piece));
+    };
+    cut(d);
     if (grad && p->piece >= kLimit / T) return false;
-    if (keeps && p->piece >= kLimit / d) return false;
+    if (std::min(V, p->piece) > (kLimit - 1) / d) return false;
     p->lt = T <= kFewTokens || ceil_div(T, kTurnTile) * ceil_div(p->piece, kTurnTile) <= kFewMost ? 6 : 8;
+    // Rows further apart may need smaller pieces. The tiles stay as they are, and with them every part
+    // of the workspace is at most what it is for ldw = d.
+    if (ldw > d) cut(ldw);
     const int64_t tile = int64_t{1} << p->lt;
     const int64_t tm = ceil_div(T, tile), tn = ceil_div(d, tile), kt = p->piece / BK;
     p->slots = !grad ? 0 : static_cast<int>(std::max(tm * tn, std::min<int64_t>(p->lt == 6 ? 512 : 256,

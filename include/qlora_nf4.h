@@ -443,8 +443,8 @@ int qlora_gated_bwd(const uint8_t* codes_g, const int8_t* qconst_g, const float*
                     const uint16_t* dH, int64_t lddh, int64_t d_seq, uint16_t* dGU, int64_t lddgu, uint16_t* dX,
                     int64_t lddx, void* workspace, int64_t workspace_bytes, void* stream);
 
-/* Workspace bytes of qlora_head_loss for a head of `vocab` rows, bf16 or (nf4) an NF4 weight, with
- * or without the gradient (0 on sizes that the call refuses). */
+/* Workspace bytes of qlora_head_loss for a head of `vocab` rows, bf16 (at any row stride) or (nf4) an
+ * NF4 weight, with or without the gradient (0 on sizes that the call refuses). */
 int64_t qlora_head_loss_workspace_bytes(int64_t vocab, int64_t d_in, int64_t d_seq, int nf4, int grad);
 
 /*
@@ -462,7 +462,8 @@ int64_t qlora_head_loss_workspace_bytes(int64_t vocab, int64_t d_in, int64_t d_s
  *   target  int64 [d_seq]; outside [0, vocab): the token is not counted, its loss and dX are zeros
  *   scale   float32 [d_seq] or NULL (1): e.g. 1 / counted tokens for a mean
  *   loss    float32 [d_seq] (not scaled);  dX bf16 [d_seq, d_in] or NULL
- * d_in a multiple of 64; any vocab of a bf16 head. The logits are float32 sums; dX multiplies the
+ * d_in a multiple of 64; any vocab of a bf16 head; -2 where 256 rows (or all, of a smaller head) at
+ * their row stride reach 4 GiB. The logits are float32 sums; dX multiplies the
  * exponentials rounded to bf16 (float32 sums; the target's own column is kept apart in float32). A
  * token with an infinite or NaN logit may have a NaN or infinite loss and dX; no other token is
  * touched by it. The result is deterministic. Strides, alignment and errors as qlora_linear_fwd_ex; outputs and the workspace must
