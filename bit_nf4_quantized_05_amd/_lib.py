@@ -139,6 +139,9 @@ def _own_stream(dev: torch.device) -> int:
     return _stream(dev)
 
 
+_data_ptr = torch.Tensor.data_ptr
+
+
 def _ptr(t: torch.Tensor) -> int:
     return t.data_ptr()
 
@@ -684,8 +687,9 @@ class GatedLayer:
     """A gated feed-forward block's two projections: NF4 weights gate and up, both
     [d_ff, d_in] in one format, their adapters A bfloat16 [r, d_in], B bfloat16 [d_ff, r] and
     scales s (one rank for both; all four tensors None: no adapters), and the activation of
-    the gate, "silu" or "gelu" (the tanh form). Checked when it is made; the tensors' contents
-    may change, the tensors may not be replaced."""
+    the gate, "silu" or "gelu" (the tanh form). Checked when it is made, and again by a call that
+    finds a tensor's storage moved (``A.data = ...``, a checkpoint loaded in place). The tensors
+    themselves may not be replaced by others."""
     gate: NF4Weight
     up: NF4Weight
     A_gate: torch.Tensor | None = None
@@ -699,6 +703,8 @@ class GatedLayer:
     d_in: int = field(init=False)
     d_ff: int = field(init=False)
     device: torch.device = field(init=False)
+    tensors: tuple = field(init=False, repr=False)     # the weights' and the adapters'
+    addresses: list = field(init=False, repr=False)    # theirs, when they were checked
     weights: tuple = field(init=False, repr=False)     # the leading arguments of both calls
 
     def __post_init__(self):
@@ -710,6 +716,8 @@ class GatedLayer:
         pairs = (("gate", self.A_gate, self.B_gate), ("up", self.A_up, self.B_up))
         tensors = [t for _, *ab in pairs for t in ab]
         r, dev = 0, g.codes.device
+        if any(t.device != dev for w in (g, u) for t in (w.codes, w.qconst, w.qscale, w.qmean)):
+            raise ValueError(f"the weights' tensors must all be on {dev}")
         if any(t is not None for t in tensors):
             if any(t is None for t in tensors):
                 raise ValueError("both projections need an adapter, or neither")
@@ -717,12 +725,20 @@ class GatedLayer:
             for name, A, B in pairs:
                 _need(A, torch.bfloat16, (r, g.d_in), f"A_{name}", dev)
                 _need(B, torch.bfloat16, (g.d_out, r), f"B_{name}", dev)
-        ptr = [t.data_ptr() if t is not None else None for t in tensors]
-        weights = tuple(t.data_ptr() for w in (g, u) for t in (w.codes, w.qconst, w.qscale, w.qmean)) + (
-            g.d_out, g.d_in, _dq_code(g.dq), ptr[0], ptr[1], float(self.s_gate), ptr[2], ptr[3], float(self.s_up), r,
-            ACT_CODES[self.act])
-        for name, v in (("r", r), ("d_in", g.d_in), ("d_ff", g.d_out), ("device", dev), ("weights", weights)):
+        kept = tuple(t for w in (g, u) for t in (w.codes, w.qconst, w.qscale, w.qmean)) + tuple(t for t in tensors if r)
+        at = list(map(_data_ptr, kept))
+        ab = at[8:] or [None] * 4
+        weights = (*at[:8], g.d_out, g.d_in, _dq_code(g.dq), ab[0], ab[1], float(self.s_gate), ab[2], ab[3],
+                   float(self.s_up), r, ACT_CODES[self.act])
+        for name, v in (("r", r), ("d_in", g.d_in), ("d_ff", g.d_out), ("device", dev), ("tensors", kept),
+                        ("addresses", at), ("weights", weights)):
             object.__setattr__(self, name, v)
+
+    def arguments(self) -> tuple:
+        """The leading arguments of both calls, of the tensors where they are now."""
+        if list(map(_data_ptr, self.tensors)) != self.addresses:
+            self.__post_init__()
+        return self.weights
 
 
 def gated_fwd_workspace_bytes(d_ff: int, d_in: int, d_seq: int, r: int) -> int:
@@ -755,6 +771,7 @@ def gated_fwd(layer: GatedLayer, X: torch.Tensor, save: bool = False, out: torch
     [d_seq, 2 d_ff] holding G beside U for ``gated_bwd``. X, out and GU may be row views of
     wider arrays. The layer's device must be the current one, and calls that may run at once
     need a workspace each (so too ``gated_bwd``, ``head_loss`` and ``head_loss_grad``)."""
+    weights = layer.arguments()
     dev, d_ff, d_in = layer.device, layer.d_ff, layer.d_in
     if X.dim() != 2 or X.shape[1] != d_in:
         raise ValueError(f"input must be [d_seq, {d_in}]")
@@ -763,7 +780,7 @@ def gated_fwd(layer: GatedLayer, X: torch.Tensor, save: bool = False, out: torch
     o, ldh = _output(out, (d_seq, d_ff), "out", dev, X)
     gu, ldgu = _output(GU, (d_seq, 2 * d_ff), "GU", dev, X, o) if save or GU is not None else (None, 0)
     ws = _workspace(workspace, lambda: gated_fwd_workspace_bytes(d_ff, d_in, d_seq, layer.r), dev)
-    rc = lib().qlora_gated_fwd(*layer.weights, X.data_ptr(), ldx, d_seq, o.data_ptr(), ldh,
+    rc = lib().qlora_gated_fwd(*weights, X.data_ptr(), ldx, d_seq, o.data_ptr(), ldh,
                                None if gu is None else gu.data_ptr(), ldgu, ws.data_ptr(), ws.nbytes, _own_stream(dev))
     if rc:
         _check(rc, "qlora_gated_fwd")
@@ -776,6 +793,7 @@ def gated_bwd(layer: GatedLayer, GU: torch.Tensor, dH: torch.Tensor, dX: torch.T
     of ``gated_fwd`` for the loss gradient dH and the GU that it kept. dGU may be GU itself. The
     adapters' gradients are ``lora_grads(A, B, s, X, half)`` with the halves dGU[:, :d_ff] (gate)
     and dGU[:, d_ff:] (up)."""
+    weights = layer.arguments()
     dev, d_ff, d_in = layer.device, layer.d_ff, layer.d_in
     if GU.dim() != 2 or dH.dim() != 2 or GU.shape[0] != dH.shape[0]:
         raise ValueError("GU [d_seq, 2 d_ff] and dH [d_seq, d_ff] must share d_seq")
@@ -788,7 +806,7 @@ def gated_bwd(layer: GatedLayer, GU: torch.Tensor, dH: torch.Tensor, dX: torch.T
         dgu, lddgu = _output(dGU, (d_seq, 2 * d_ff), "dGU", dev, GU, dH)
     gx, lddx = _output(dX, (d_seq, d_in), "dX", dev, GU, dH, dgu)
     ws = _workspace(workspace, lambda: gated_bwd_workspace_bytes(d_ff, d_in, d_seq, layer.r), dev)
-    rc = lib().qlora_gated_bwd(*layer.weights, GU.data_ptr(), ldgu, dH.data_ptr(), lddh, d_seq, dgu.data_ptr(), lddgu,
+    rc = lib().qlora_gated_bwd(*weights, GU.data_ptr(), ldgu, dH.data_ptr(), lddh, d_seq, dgu.data_ptr(), lddgu,
                                gx.data_ptr(), lddx, ws.data_ptr(), ws.nbytes, _own_stream(dev))
     if rc:
         _check(rc, "qlora_gated_bwd")
