@@ -321,10 +321,11 @@ GatedWs gated_ws(int64_t d_ff, int64_t d_in, int64_t d_seq, int r, bool bwd) {
         w.bytes = off;
         return w;
     }
+    const int terms = qn::gated_terms(d_ff, d_in, d_seq, r), k2 = qn::gated_k2(r, terms);
     w.what = take(4 * d_ff * d_in);                                                  // both weights
-    w.t = take(2 * d_seq * qn::gated_k2(r));                                         // both rank products
-    w.adapt = take(2 * (bwd ? d_in : 2 * d_ff) * qn::gated_k2(r));                   // both adapters
-    w.rpart = take(4 * qn::gated_ranks_floats(d_seq, bwd ? d_ff : d_in, r));         // their partial sums
+    w.t = take(2 * d_seq * k2);                                                      // both rank products
+    w.adapt = take(2 * (bwd ? d_in : 2 * d_ff) * k2);                                // both adapters
+    w.rpart = take(4 * qn::gated_ranks_floats(d_seq, bwd ? d_ff : d_in, r, terms));  // their partial sums
     for (int i = 0; i < 2; ++i) w.bt[i] = take(bwd && !qn::gated_reads_b(r) ? 2 * static_cast<int64_t>(r) * d_ff : 0);
     w.part = take(4 * (bwd ? qn::gated_dx_part_floats(d_seq, d_ff, d_in) : qn::gated_part_floats(d_seq, d_ff, d_in)));
     w.bytes = off;
@@ -332,9 +333,9 @@ GatedWs gated_ws(int64_t d_ff, int64_t d_in, int64_t d_seq, int r, bool bwd) {
 }
 
 // Whether an operand that the call makes reaches 4 GiB (sizes >= 1): both weights, the rank
-// products or the adapters' layouts
+// products or the adapters' layouts (in one term; gated_terms)
 bool gated_too_large(int64_t d_ff, int64_t d_in, int64_t d_seq, int r) {
-    const int64_t k2 = std::max(1, qn::gated_k2(r));
+    const int64_t k2 = std::max(1, qn::gated_k2(r, 1));
     return reaches_4gib(2 * d_ff, std::max(d_in, k2)) || reaches_4gib(std::max(d_seq, d_in), k2);
 }
 
@@ -365,6 +366,7 @@ int check_gated(const uint8_t* const (&codes)[2], const int8_t* const (&qconst)[
     if (d_in > INT32_MAX || d_ff > INT32_MAX / 2 || d_seq > INT32_MAX) return fail(-2, "dimension too large");
     if (gated_too_large(d_ff, d_in, d_seq, r)) return fail(-2, "an operand reaches 4 GiB");
     c->d_ff = d_ff; c->d_in = d_in; c->M = d_seq; c->r = r; c->act = act;
+    c->terms = qn::gated_terms(d_ff, d_in, d_seq, r);
     return 0;
 }
 

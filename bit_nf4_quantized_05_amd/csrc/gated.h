@@ -20,11 +20,24 @@ struct GatedCall {
     float s[2];
     int r, act;                       // r 0: no adapters
     int64_t M;
+    int terms;                        // bf16 terms of the rank products past kGatedSmall tokens (gated_terms)
 };
 
-// Rank columns of one projection, and of both, whole K-steps of 64 (0 without adapters)
-inline int gated_pad(int r) { return (r + 31) / 32 * 32; }
-inline int gated_k2(int r) { return 2 * gated_pad(r); }
+// The rank products s A x and s B^T dY of one projection as `terms` bf16 terms, the second what the
+// first leaves (16 bits; with one term its 2^-9 shows in every output beside the output's own
+// rounding: 41 % of rank-dominated outputs were not the rounded result, 0.1 % with two): columns of one
+// term, of the projection, and of both, which are whole K-steps of 64 (0 without adapters). Up to rank 16
+// the second term takes room that the first leaves; at rank 64 it is two K-steps more (forward of 2048
+// tokens of 11008 x 4096 336 -> 345 us, the gradient 366 -> 368).
+inline int gated_term(int r, int terms) { return terms == 2 ? (r + 15) / 16 * 16 : (r + 31) / 32 * 32; }
+inline int gated_pad(int r, int terms) { return terms * gated_term(r, terms); }
+inline int gated_k2(int r, int terms) { return 2 * gated_pad(r, terms); }
+// Two terms, or one where an operand of them would reach 4 GiB (r > 128: a million rows of a layer or
+// two million tokens)
+inline int gated_terms(int64_t d_ff, int64_t d_in, int64_t M, int r) {
+    const int64_t rows = M > d_in ? M : d_in;
+    return r == 0 || (rows > 2 * d_ff ? rows : 2 * d_ff) <= ((int64_t{1} << 31) - 1) / gated_k2(r, 2) ? 2 : 1;
+}
 
 // act(g), and its derivative. sigma(x) = 1 / (1 + 2^(-x log2 e)) with the hardware's 2^x and
 // 1/x (1 ulp each), 0 or 1 where 2^x leaves float32.
@@ -114,7 +127,7 @@ __device__ __forceinline__ void gated_grad_job(const GatedGradArgs& a, int b) {
 // Both weights dequantised to what, gate above up, [2 d_ff, d_in], and both adapters to adapt
 // (forward: B, [2 d_ff, k2]; gradient: A, [k2, d_in]); in the gradient the elementwise part grad and, where
 // bt is not null, B^T [r, d_ff]. Then (r > 0) the rank products of in: t [M, k2] = s_w X A_w^T, or
-// s_w (half w of dGU) B_w; part: gated_ranks_floats, K = d_in or d_ff.
+// s_w (half w of dGU) B_w, in c.terms bf16 terms; part: gated_ranks_floats, K = d_in or d_ff.
 struct GatedProlog {
     uint16_t* what; uint16_t* adapt;
     const uint16_t* in; int64_t ld_in; uint16_t* t; float* part;
@@ -122,7 +135,7 @@ struct GatedProlog {
     GatedGradArgs grad;
 };
 inline bool gated_reads_b(int r) { return r % 8 == 0; }
-int64_t gated_ranks_floats(int64_t M, int64_t K, int r);
+int64_t gated_ranks_floats(int64_t M, int64_t K, int r, int terms);
 hipError_t launch_gated_prologue(const GatedCall& c, bool backward, const GatedProlog& o, hipStream_t st);
 
 // W_hat [d_out, d_in] bf16, row-major (d_in % 64 == 0)

@@ -277,7 +277,8 @@ hipError_t launch_gated_gemm(const GatedCall& c, const uint16_t* X, int64_t ldx,
                              const uint16_t* adapt, uint16_t* H, int64_t ldh, uint16_t* GU, int64_t ldgu, float* part,
                              hipStream_t st) {
     TurnArgs g = turn_args(X, ldx, c.M, what, c.d_in, 2 * c.d_ff, c.d_in);
-    add_ranks(g, t, adapt, gated_k2(c.r), gated_k2(c.r), c.M, 2 * c.d_ff);
+    const int k2 = gated_k2(c.r, c.terms);
+    add_ranks(g, t, adapt, k2, k2, c.M, 2 * c.d_ff);
     const TurnSplit s = fwd_split(c.M, c.d_ff, c.d_in);
     const GatedOut o{H, ldh, GU, ldgu, static_cast<int>(c.M), static_cast<int>(c.d_ff), c.act, part};
     const dim3 grid(turn_split_grid(s));
@@ -294,7 +295,7 @@ hipError_t launch_gated_gemm(const GatedCall& c, const uint16_t* X, int64_t ldx,
 hipError_t launch_gated_dx(const GatedCall& c, const uint16_t* dGU, int64_t lddgu, const uint16_t* what, const uint16_t* t,
                            const uint16_t* adapt, uint16_t* dX, int64_t lddx, float* part, hipStream_t st) {
     TurnArgs g = turn_args(dGU, lddgu, c.M, what, c.d_in, 2 * c.d_ff, 2 * c.d_ff);
-    add_ranks(g, t, adapt, gated_k2(c.r), c.d_in, c.M, c.d_in);
+    add_ranks(g, t, adapt, gated_k2(c.r, c.terms), c.d_in, c.M, c.d_in);
     const TurnSplit s = dx_split(c.M, c.d_ff, c.d_in);
     const GatedDx o{dX, lddx, static_cast<int>(c.M), static_cast<int>(c.d_in), part};
     const dim3 grid(turn_split_grid(s));

@@ -451,27 +451,36 @@ void prologue_kernel(PrologueArgs a, NF4Tables tab) {
 // ---------------------------------------------------------------------------
 // The gated block's two projections side by side (gated.hip): in one launch both weights'
 // dequantisation, both adapters' layouts and, in the gradient, its elementwise part; then the rank
-// products. The rank columns of the gate come first, pad of them, then those of the up projection.
+// products. The rank columns of the gate come first, pad of them (terms of `term` columns each, a
+// multiple of 16), then those of the up projection.
 // ---------------------------------------------------------------------------
 
-// T_w = s_w P_w R_w^T, bf16 [M, k2] with w's `pad` columns at w pad. Forward: P = X, R = A [r, d_in].
+// T_w = s_w P_w R_w^T in bf16 terms, [M, k2] with w's `pad` columns at w pad. Forward: P = X, R = A [r, d_in].
 // Gradient: P = dG and dU, R^T = B [d_ff, r] as it is (kCols: its rows lie along K; r % 8 == 0) or R =
 // B^T. Tiles of 64 tokens x 64 ranks over slices of K, whose partial sums gated_ranks_reduce adds.
 // Bound by the reads of P: the gradient's, 90 MB that the launch before has written, take 30 us at 2048
 // tokens of 11008 x 4096 (tiles of 128 tokens, 32 a wave, 32).
 struct GatedRanks {
     TurnArgs g[2];
-    uint16_t* T; float* part;         // part [slices][M][2 pad] where there are several
+    uint16_t* T; float* part;         // part [slices][M][2 term] where there are several
     float s[2];
-    int M, r, pad, slices, kper;
+    int M, r, term, pad, slices, kper;
 };
 __host__ __device__ inline int gated_rank_items(const GatedRanks& o) {
-    return 2 * ((o.M + kFewTile - 1) / kFewTile) * ((o.pad + kFewTile - 1) / kFewTile) * o.slices;
+    return 2 * ((o.M + kFewTile - 1) / kFewTile) * ((o.term + kFewTile - 1) / kFewTile) * o.slices;
+}
+
+// Ranks n .. n + 3 of projection w and token m in their terms (n + 3 < term; an infinity or NaN: in the first)
+__device__ __forceinline__ void gated_put_ranks(uint16_t* T, int term, int pad, int64_t m, int w, int n, const f32x4t& v) {
+    uint16_t* at = T + m * (2 * pad) + w * pad + n;
+    float left[4] = {v[0], v[1], v[2], v[3]};
+    *reinterpret_cast<uint2*>(at) = take_bf16x4(left);
+    if (pad > term) *reinterpret_cast<uint2*>(at + term) = take_bf16x4(left);
 }
 
 template <bool kCols>
 __device__ __forceinline__ void gated_ranks_job(const GatedRanks& o, int item) {
-    const int tiles_m = (o.M + kFewTile - 1) / kFewTile, tiles_r = (o.pad + kFewTile - 1) / kFewTile;
+    const int tiles_m = (o.M + kFewTile - 1) / kFewTile, tiles_r = (o.term + kFewTile - 1) / kFewTile;
     const int n0 = item % tiles_r * kFewTile;
     item /= tiles_r;
     const int w = __builtin_amdgcn_readfirstlane(item & 1), m0 = (item >> 1) % tiles_m * kFewTile;
@@ -490,13 +499,12 @@ __device__ __forceinline__ void gated_ranks_job(const GatedRanks& o, int item) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int n = n0 + 32 * (wave & 1) + 16 * j + 4 * (lane >> 4);
-            if (m >= o.M || n >= o.pad) continue;
+            if (m >= o.M || n >= o.term) continue;
             f32x4t v = acc[0][0][i][j];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = n + e < o.r ? o.s[w] * v[e] : 0.0f;
-            const int64_t at = static_cast<int64_t>(m) * (2 * o.pad) + w * o.pad + n;
-            if (o.slices == 1) *reinterpret_cast<uint2*>(o.T + at) = uint2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-            else *reinterpret_cast<f32x4t*>(o.part + static_cast<int64_t>(slice) * o.M * (2 * o.pad) + at) = v;
+            if (o.slices == 1) gated_put_ranks(o.T, o.term, o.pad, m, w, n, v);
+            else *reinterpret_cast<f32x4t*>(o.part + (static_cast<int64_t>(slice) * o.M + m) * (2 * o.term) + w * o.term + n) = v;
         }
     }
 }
@@ -509,11 +517,13 @@ void gated_ranks_kernel(GatedRanks o) {
 }
 
 __global__ __launch_bounds__(256)
-void gated_ranks_reduce(const float* part, uint16_t* T, int64_t n, int slices) {
+void gated_ranks_reduce(const float* part, uint16_t* T, int64_t n, int slices, int term, int pad) {
     const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
     if (at >= n) return;
     const float4 v = ordered_sum4<8>(part + at, n, slices);
-    *reinterpret_cast<uint2*>(T + at) = uint2{bf16_pair(v.x, v.y), bf16_pair(v.z, v.w)};
+    const uint32_t m = static_cast<uint32_t>(at) / (2 * term), q = static_cast<uint32_t>(at) % (2 * term);   // n < 2^31
+    const int w = q >= static_cast<uint32_t>(term) ? 1 : 0;
+    gated_put_ranks(T, term, pad, m, w, static_cast<int>(q) - w * term, f32x4t{v.x, v.y, v.z, v.w});
 }
 
 struct GatedLayoutArgs {
@@ -523,12 +533,12 @@ struct GatedLayoutArgs {
     uint16_t* adst;                  // forward [2 d_ff, k2], gradient [k2, d_in]
     uint16_t* bt[2];                 // gradient: B^T [r, d_ff], or null
     int64_t d_ff, d_in;
-    int r, pad, k2, n_ranks, n_adapt, n_bt, n_grad;
+    int r, term, pad, k2, n_ranks, n_adapt, n_bt, n_grad;
 };
 
 // 8 entries of a row of the adapters' layout. Forward: the gate's d_ff rows of B, then the up
-// projection's, each at its own rank columns with zeros at the other's. Gradient: the rows of A_g,
-// zeros up to pad, and so A_u.
+// projection's, each at its own rank columns, once per term, with zeros at the other's. Gradient: the
+// rows of A_g and zeros up to `term`, once per term, and so A_u.
 template <bool kBack>
 __device__ __forceinline__ void gated_adapt_job(const GatedLayoutArgs& a, int b) {
     const int r = a.r, pad = a.pad;
@@ -537,14 +547,14 @@ __device__ __forceinline__ void gated_adapt_job(const GatedLayoutArgs& a, int b)
     if constexpr (kBack) {
         const int64_t cpr = a.d_in / 8;
         if (c >= a.k2 * cpr) return;
-        const int j = static_cast<int>(c / cpr), w = j >= pad ? 1 : 0, q = j - w * pad;
+        const int j = static_cast<int>(c / cpr), w = j >= pad ? 1 : 0, q = (j - w * pad) % a.term;
         if (q < r) v = *reinterpret_cast<const uint4*>(a.A[w] + q * a.d_in + (c % cpr) * 8);
     } else {
         const int cpr = a.k2 / 8;
         if (c >= 2 * a.d_ff * cpr) return;
         const int64_t i = c / cpr;
         const int j0 = static_cast<int>(c % cpr) * 8;
-        const int w = j0 >= pad ? 1 : 0, q0 = j0 - w * pad;  // pad % 8 == 0: a chunk is of one projection
+        const int w = j0 >= pad ? 1 : 0, q0 = (j0 - w * pad) % a.term;   // term % 8 == 0: a chunk is of one term
         if ((i >= a.d_ff) == (w == 1)) {
             const uint16_t* src = a.B[w] + (i - w * a.d_ff) * r + q0;
             uint32_t e2[4] = {0u, 0u, 0u, 0u};
@@ -1119,7 +1129,7 @@ namespace {
 // Slices of the rank products' K: a workgroup a CU, 8 K-steps or more each (the gradient of 2048 tokens of
 // 11008 x 4096 with 1, 2 and 4 workgroups a CU 362, 364 and 367 us: the partial sums)
 void rank_split(int64_t M, int64_t K, int r, int* slices, int* kper) {
-    const int64_t kt = K / kTurnK, tiles = 2 * ((M + kFewTile - 1) / kFewTile) * ((gated_pad(r) + kFewTile - 1) / kFewTile);
+    const int64_t kt = K / kTurnK, tiles = 2 * ((M + kFewTile - 1) / kFewTile) * ((r + kFewTile - 1) / kFewTile);
     const int64_t want = std::max<int64_t>(1, std::min(256 / tiles, kt / 8));
     *kper = static_cast<int>((kt + want - 1) / want);
     *slices = static_cast<int>((kt + *kper - 1) / *kper);
@@ -1130,17 +1140,17 @@ void rank_split(int64_t M, int64_t K, int r, int* slices, int* kper) {
 constexpr int64_t kRanksWithin = int64_t{1} << 24;
 }  // namespace
 
-int64_t gated_ranks_floats(int64_t M, int64_t K, int r) {
+int64_t gated_ranks_floats(int64_t M, int64_t K, int r, int terms) {
     if (r == 0) return 0;
     int slices, kper;
     rank_split(M, K, r, &slices, &kper);
-    return slices > 1 ? slices * M * gated_k2(r) : 0;
+    return slices > 1 ? slices * M * 2 * gated_term(r, terms) : 0;
 }
 
 hipError_t launch_gated_prologue(const GatedCall& c, bool backward, const GatedProlog& o, hipStream_t st) {
     GatedLayoutArgs a{};
     GatedRanks q{};
-    a.r = c.r; a.pad = gated_pad(c.r); a.k2 = gated_k2(c.r);
+    a.r = c.r; a.term = gated_term(c.r, c.terms); a.pad = gated_pad(c.r, c.terms); a.k2 = gated_k2(c.r, c.terms);
     a.d_ff = c.d_ff; a.d_in = c.d_in; a.adst = o.adapt;
     const bool bcols = backward && o.bt[0] == nullptr;
     const int64_t K = backward ? c.d_ff : c.d_in;
@@ -1155,7 +1165,7 @@ hipError_t launch_gated_prologue(const GatedCall& c, bool backward, const GatedP
         }
     }
     if (c.r > 0) {
-        q.T = o.t; q.part = o.part; q.M = static_cast<int>(c.M); q.r = c.r; q.pad = a.pad;
+        q.T = o.t; q.part = o.part; q.M = static_cast<int>(c.M); q.r = c.r; q.term = a.term; q.pad = a.pad;
         rank_split(c.M, K, c.r, &q.slices, &q.kper);
     }
     const bool within = !backward && c.r > 0 && 2 * c.d_ff * c.d_in <= kRanksWithin;
@@ -1175,9 +1185,9 @@ hipError_t launch_gated_prologue(const GatedCall& c, bool backward, const GatedP
     if (!within && bcols) QN_LAUNCH("gated_ranks_kernel", st, gated_ranks_kernel<true>, rgrid, dim3(kFewThreads), 0, st, q);
     else if (!within) QN_LAUNCH("gated_ranks_kernel", st, gated_ranks_kernel<false>, rgrid, dim3(kFewThreads), 0, st, q);
     if (q.slices > 1) {
-        const int64_t n = c.M * a.k2;
+        const int64_t n = c.M * 2 * a.term;
         QN_LAUNCH("gated_ranks_reduce", st, gated_ranks_reduce, dim3(static_cast<unsigned>((n + 1023) / 1024)), dim3(256), 0,
-                  st, o.part, o.t, n, q.slices);
+                  st, o.part, o.t, n, q.slices, a.term, a.pad);
     }
     return hipGetLastError();
 }

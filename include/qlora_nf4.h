@@ -419,7 +419,9 @@ int64_t qlora_gated_bwd_workspace_bytes(int64_t d_ff, int64_t d_in, int64_t d_se
 /*
  * qlora_gated_fwd - H [d_seq, d_ff] bf16 from X [d_seq, d_in]. GU (NULL: not kept) receives G in
  * columns 0 .. d_ff - 1 and U in the d_ff columns after, bf16 [d_seq, 2 d_ff], for the gradient.
- * H is formed from the float32 sums of G and U and rounded once.
+ * H is formed from the float32 sums of G and U and rounded once. s A x keeps 16 bits or more (float32
+ * or two bf16 terms), as s B^T dY does in the gradient; 8 (one term) where two terms would reach 4 GiB:
+ * r above 128 with a million rows of a weight or two million tokens.
  */
 int qlora_gated_fwd(const uint8_t* codes_g, const int8_t* qconst_g, const float* qscale_g, const float* qmean_g,
                     const uint8_t* codes_u, const int8_t* qconst_u, const float* qscale_u, const float* qmean_u,
