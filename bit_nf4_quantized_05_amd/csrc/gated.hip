@@ -240,12 +240,17 @@ void gated_dx_reduce(TurnSplit s, GatedDx o) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tiles of 64 or of 256, by the number of 256-wide tiles. Forward, up to 96 (with tiles of 64 and of
-// 256: 203 tokens of the 512 x 256 block 15 and 20 us, 256 of 11008 x 4096, 86 tiles, 112 and 120; 70 of
-// 28672 x 8192, 224 tiles, 502 and 469). The gradient's sums are long and its tiles few, and shares of
+// Tiles of 64 or of 256, by their numbers. Forward, tiles of 64 where they are at most two rounds of the
+// chip, 1024, and the 256-wide ones at most 96 (us with tiles of 64 and of 256: 203 tokens of the 512 x 256
+// block 14 and 17; 512 of 2048 x 4096, 512 small tiles, 43 and 55; 512 of 4096 x 4096, 1024, 77 and 82 [75 and
+// 74 with the weights' copy in the Infinity Cache]; 768 there, 1536, 101 and 96 [99 and 82]; 128 of 11008 x
+// 4096, 688, 123 and 126; 256 there, 1376, 157 and 133 [117 and 106]; 70 of 28672 x 8192, 224 large tiles, 496
+// and 436). The gradient's sums are long and its tiles few, and shares of
 // them fill the chip: up to 64 tiles and 128 K-steps (128 tokens of 4096 x 4096 55 and 59; of 11008 x
 // 4096, 344 steps, 116 and 110; 256 of 5504 x 2048, 172 steps, 60 and 56).
-bool fwd_few(int64_t M, int64_t d_ff) { return ceil_div(M, kTurnTile) * ceil_div(2 * d_ff, kTurnTile) <= 96; }
+bool fwd_few(int64_t M, int64_t d_ff) {
+    return ceil_div(M, kFewTile) * (2 * d_ff / kFewTile) <= 1024 && ceil_div(M, kTurnTile) * ceil_div(2 * d_ff, kTurnTile) <= 96;
+}
 bool dx_few(int64_t M, int64_t d_ff, int64_t d_in) {
     return ceil_div(M, kTurnTile) * ceil_div(d_in, kTurnTile) <= 64 && 2 * d_ff / kTurnK <= 128;
 }
