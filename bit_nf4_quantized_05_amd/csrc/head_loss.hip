@@ -45,11 +45,13 @@ constexpr float kLargest = 0x1p80f, kMaxLog2 = 80.0f;
 
 // K-steps that a split of the gradient's product has at least, by its tiles' size (1 << lt)
 __host__ __device__ constexpr int head_steps(int lt) { return lt == 6 ? 4 : 8; }
-// Tiles of 64 are taken on up to kFewTokens tokens (17 on 32000 rows of 4096: loss 51 us against 79
-// with tiles of 256, with the gradient 107 / 154; 128: 66 / 80 and 158 / 163) and where there are up to
-// kFewMost tiles of 256 (256 tokens on 16128 rows, 63 of them: 63 / 77 and 131 / 135; 1024 on 8192, 128:
-// 104 / 78 and 229 / 154).
-constexpr int64_t kFewTokens = 128, kFewMost = 64;
+// Tiles of 64 are taken on up to 64 tokens (17 on 32000 rows of 4096: loss 61 us against 85 with tiles of
+// 256, with the gradient 120 / 170; 64: 66 / 85 and 130 / 174) and, where they are at most kFewSmall (two
+// rounds of the chip) in a piece, on up to kFewTokens tokens (65 on 32000 rows: 82 / 84 and 161 / 171, 128: 95 / 90
+// and 187 / 186; not 65 and 128 on 128000 rows, 2000 small tiles: loss 284 / 273 and 335 / 276) and for up to
+// kFewMost tiles of 256 (256 tokens on 16128 rows, 63 of them: 85 / 91 and 165 / 157; 512 on 8192, 64: 61 / 77
+// and 134 / 143; 1024 on 8192, 128: 108 / 80 and 244 / 167).
+constexpr int64_t kFewTokens = 128, kFewSmall = 1024, kFewMost = 64;
 // Past this many tokens one workgroup numbers them in a launch of its own (on 4096 rows of 64, a
 // launch of its own and each workgroup counting for itself: 4096 tokens 24 us and 22, 16384 51 and 58,
 // 65536 172 and 362).
@@ -526,7 +528,9 @@ bool head_plan(int64_t V, int64_t d, int64_t ldw, int64_t T, bool nf4, bool grad
     cut(d);
     if (grad && p->piece >= kLimit / T) return false;
     if (std::min(V, p->piece) > (kLimit - 1) / d) return false;
-    p->lt = T <= kFewTokens || ceil_div(T, kTurnTile) * ceil_div(p->piece, kTurnTile) <= kFewMost ? 6 : 8;
+    const int64_t large = ceil_div(T, kTurnTile) * ceil_div(p->piece, kTurnTile), rows = std::min(V, p->piece);
+    const bool two_rounds = ceil_div(T, kFewTile) * ceil_div(rows, kFewTile) <= kFewSmall;
+    p->lt = T <= kFewTile || (two_rounds && (T <= kFewTokens || large <= kFewMost)) ? 6 : 8;
     // Rows further apart may need smaller pieces. The tiles stay as they are, and with them every part
     // of the workspace is at most what it is for ldw = d.
     if (ldw > d) cut(ldw);
