@@ -25,7 +25,7 @@ struct GatedCall {
 
 // The rank products s A x and s B^T dY of one projection as `terms` bf16 terms, the second what the
 // first leaves (16 bits; with one term its 2^-9 shows in every output beside the output's own
-// rounding: 41 % of rank-dominated outputs were not the rounded result, 0.1 % with two): columns of one
+// rounding: 41 % of rank-dominated outputs were not the rounded result, 0.2 to 0.6 % with two): columns of one
 // term, of the projection, and of both, which are whole K-steps of 64 (0 without adapters). Up to rank 16
 // the second term takes room that the first leaves; at rank 64 it is two K-steps more (forward of 2048
 // tokens of 11008 x 4096 336 -> 345 us, the gradient 366 -> 368).
@@ -65,7 +65,9 @@ __device__ __forceinline__ float gated_act_grad(int act, float g, float& value) 
 }
 
 // dG = dH U act'(G), dU = dH act(G), elementwise over [M, d_ff]; G | U and dG | dU stand side by
-// side in rows of GU and dGU.
+// side in rows of GU and dGU. They are outputs in bf16, and dX is formed from these: of two bf16 terms it
+// would take a second product (another 250 us at 2048 tokens of 11008 x 4096) for an error of 0.0017 in
+// place of 0.0023, relative, beside the 0.0017 that dX's own rounding makes.
 struct GatedGradArgs {
     const uint16_t* dH; int64_t lddh;
     const uint16_t* GU; int64_t ldgu;

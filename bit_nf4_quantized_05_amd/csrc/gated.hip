@@ -9,7 +9,7 @@
 // The activation and the product are then register arithmetic in the epilogue, G and U reach memory
 // only where the gradient needs them, and X is read once.
 // Bound by the matrix pipes at the clock that they leave, and by whole rounds of tiles: 2048 tokens of
-// 11008 x 4096 (688 tiles on 256 CUs) take 282 us with G and U kept (1.32 PFLOP/s), dX there 250 (1.49).
+// 11008 x 4096 (688 tiles on 256 CUs) take 291 us with G and U kept (1.30 PFLOP/s), dX there 252 (1.49).
 #include <hip/hip_runtime.h>
 
 #include "gated.h"

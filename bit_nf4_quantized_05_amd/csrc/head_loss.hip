@@ -11,8 +11,9 @@
 // digits, the gradient has no difference of nearly equal terms, and the sweep needs no maximum
 // first: each piece's exponentials (bf16, so that they can be an MFMA operand) are multiplied
 // with W in the same pass and the sums divided at the end. Two products where forming the
-// logits again for the gradient would take three. Where z_v - z_y is large (past kMaxLog2 in
-// powers of two) a 256-wide tile of a row is scaled down by a power of two, and head_join brings
+// logits again for the gradient would take three. (The exponentials' rounding, 2^-9 at most of each of many
+// terms, moves dX by 0.0002 to 0.0007, relative, beside the 0.0017 of its own; a second term would be a
+// third product.) Where z_v - z_y is large (past kMaxLog2 in powers of two) a 256-wide tile of a row is scaled down by a power of two, and head_join brings
 // the row to one scale: exact in every case, and no work where it does not happen.
 //
 // Tokens without a target (prompts, padding) are left out before the products: head_plan_kernel
@@ -21,8 +22,9 @@
 // Per piece: an NF4 head's rows dequantised; head_logits (the product and its exponentials),
 // head_join (after the last piece the loss), head_grad (their product with W, whose rows are along K
 // there: read by transposing LDS reads, no transposed copy; added to float32 sums). Then head_final. All sums are in fixed order.
-// Bound by both products at the power-limited clock: 4096 tokens on 128000 rows of 4096 5.9 ms (1.46
-// PFLOP/s), and on few tokens by the head's stream: 17 on 32000 rows 48 us (5.5 TB/s).
+// Bound by both products at the power-limited clock: 4096 tokens on 128000 rows of 4096 5.9 to 6.2 ms by
+// the card (1.39 to 1.46 PFLOP/s), and on few tokens by the head's stream: 17 on 32000 rows 46 to 48 us,
+// as a plain read of its 262 MB (46 to 52).
 #include <hip/hip_runtime.h>
 
 #include "gated.h"
@@ -53,8 +55,8 @@ __host__ __device__ constexpr int head_steps(int lt) { return lt == 6 ? 4 : 8; }
 // and 134 / 143; 1024 on 8192, 128: 108 / 80 and 244 / 167).
 constexpr int64_t kFewTokens = 128, kFewSmall = 1024, kFewMost = 64;
 // Past this many tokens one workgroup numbers them in a launch of its own (on 4096 rows of 64, a
-// launch of its own and each workgroup counting for itself: 4096 tokens 24 us and 22, 16384 51 and 58,
-// 65536 172 and 362).
+// launch of its own and each workgroup counting for itself: 4096 tokens 22 us and 20, 16384 61 and 66,
+// 65536 212 and 400).
 constexpr int64_t kPlanFrom = 8192;
 
 // The numbering of the counted tokens and what is known of each (arrays of T)

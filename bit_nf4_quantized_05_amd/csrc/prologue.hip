@@ -1136,7 +1136,7 @@ void rank_split(int64_t M, int64_t K, int r, int* slices, int* kper) {
 }
 // Up to this many weights (both projections) the rank products join the forward's layouts: a launch less,
 // but their LDS leaves the dequantisation two workgroups a CU (a joined launch and two: 512 tokens of
-// 2048 x 4096 44.7 and 48.6 us, 2048 of 4096 x 4096 124.9 and 121.3, of 11008 x 4096 332 and 309).
+// 2048 x 4096 42 and 45 us, 2048 of 4096 x 4096 127 and 123, of 11008 x 4096 337 and 314).
 constexpr int64_t kRanksWithin = int64_t{1} << 24;
 }  // namespace
 
