@@ -1115,6 +1115,7 @@ int qlora_gated_bwd(const uint8_t* codes_g, const int8_t* qconst_g, const float*
     if (int rc = check_rows(dH, d_seq, d_ff, lddh)) return rc;
     if (int rc = check_rows(dGU, d_seq, 2 * d_ff, lddgu)) return rc;
     if (int rc = check_rows(dX, d_seq, d_in, lddx)) return rc;
+    if (dGU == GU && lddgu != ldgu && d_seq > 1) return fail(-1, "dGU in the place of GU needs GU's row stride");
     const GatedWs w = gated_ws(d_ff, d_in, d_seq, r, true);
     if (int rc = check_workspace(workspace, workspace_bytes, w.bytes)) return rc;
     char* ws = static_cast<char*>(workspace);

@@ -421,7 +421,8 @@ int64_t qlora_gated_bwd_workspace_bytes(int64_t d_ff, int64_t d_in, int64_t d_se
  * columns 0 .. d_ff - 1 and U in the d_ff columns after, bf16 [d_seq, 2 d_ff], for the gradient.
  * H is formed from the float32 sums of G and U and rounded once. s A x keeps 16 bits or more (float32
  * or two bf16 terms), as s B^T dY does in the gradient; 8 (one term) where two terms would reach 4 GiB:
- * r above 128 with a million rows of a weight or two million tokens.
+ * r above 128 with a million rows of a weight or two million tokens. An infinity or NaN in X stays in its
+ * token's row; one in an adapter may show as NaN in both G and U.
  */
 int qlora_gated_fwd(const uint8_t* codes_g, const int8_t* qconst_g, const float* qscale_g, const float* qmean_g,
                     const uint8_t* codes_u, const int8_t* qconst_u, const float* qscale_u, const float* qmean_u,
@@ -436,7 +437,7 @@ int qlora_gated_fwd(const uint8_t* codes_g, const int8_t* qconst_g, const float*
  *   dX = W_g^T dG + s_g A_g^T (B_g^T dG) + W_u^T dU + s_u A_u^T (B_u^T dU)     bf16 [d_seq, d_in]
  * dX is formed from dG and dU as rounded to bf16. The adapters' gradients are qlora_lora_grads of X
  * and the two halves of dGU (dY = dGU or dGU + d_ff, lddy = lddgu). dGU may be GU itself (the same
- * pointer and stride): its elements are read before they are written.
+ * pointer and stride; -1 with another stride): its elements are read before they are written.
  */
 int qlora_gated_bwd(const uint8_t* codes_g, const int8_t* qconst_g, const float* qscale_g, const float* qmean_g,
                     const uint8_t* codes_u, const int8_t* qconst_u, const float* qscale_u, const float* qmean_u,

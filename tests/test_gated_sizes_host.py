@@ -46,3 +46,14 @@ def test_queries_agree_with_the_calls(d_ff, d_in, m, r):
 def test_long_batches_that_keep_nothing_have_a_workspace():
     assert qn.gated_fwd_workspace_bytes(28672, 8192, 40000, 64) > 4 * 28672 * 8192
     assert qn.gated_fwd_workspace_bytes(11008, 4096, 100000, 16) > 4 * 11008 * 4096
+
+
+def test_the_gradient_in_place_at_another_stride_is_refused():
+    def call(GU, ldgu, dGU, lddgu, m):
+        return _lib.lib().qlora_gated_bwd(*WEIGHT, *WEIGHT, 64, 128, 0, *ADAPTERS, 8, 0, GU, ldgu, FAKE, 64, m, dGU, lddgu, FAKE,
+                                          128, FAKE, 0, None)
+
+    # -3: the sizes and strides are taken, the workspace is too small
+    assert call(2 * FAKE, 128, 2 * FAKE, 128, 3) == -3 and call(2 * FAKE, 160, 2 * FAKE, 160, 3) == -3
+    assert call(2 * FAKE, 160, 2 * FAKE, 128, 3) == -1 and call(2 * FAKE, 128, 2 * FAKE, 160, 3) == -1
+    assert call(2 * FAKE, 160, 2 * FAKE, 128, 1) == -3 and call(2 * FAKE, 160, 3 * FAKE, 128, 3) == -3
