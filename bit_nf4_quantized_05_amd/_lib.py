@@ -716,7 +716,7 @@ class GatedLayer:
         pairs = (("gate", self.A_gate, self.B_gate), ("up", self.A_up, self.B_up))
         tensors = [t for _, *ab in pairs for t in ab]
         r, dev = 0, g.codes.device
-        if any(t.device != dev for w in (g, u) for t in (w.codes, w.qconst, w.qscale, w.qmean)):
+        if any(t.device != dev and t.numel() for w in (g, u) for t in (w.codes, w.qconst, w.qscale, w.qmean)):
             raise ValueError(f"the weights' tensors must all be on {dev}")
         if any(t is not None for t in tensors):
             if any(t is None for t in tensors):

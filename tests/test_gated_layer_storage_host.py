@@ -89,3 +89,10 @@ def test_weights_apart_are_refused():
     w[1].qscale = w[1].qscale.to("meta")
     with pytest.raises(ValueError, match="must all be on"):
         qn.GatedLayer(w[0], w[1])
+
+
+def test_what_a_weight_does_not_have_may_be_anywhere():
+    """Without a second level the constants and their mean are empty, on whatever device."""
+    w = qn.alloc_weight(D_FF, D_IN, "cpu", "none")
+    w.qconst, w.qmean = w.qconst.to("meta"), w.qmean.to("meta")
+    assert qn.GatedLayer(w, w).d_ff == D_FF
