@@ -32,8 +32,8 @@ struct GatedCall {
 inline int gated_term(int r, int terms) { return terms == 2 ? (r + 15) / 16 * 16 : (r + 31) / 32 * 32; }
 inline int gated_pad(int r, int terms) { return terms * gated_term(r, terms); }
 inline int gated_k2(int r, int terms) { return 2 * gated_pad(r, terms); }
-// Two terms, or one where an operand of them would reach 4 GiB (r > 128: a million rows of a layer or
-// two million tokens)
+// Two terms, or one where an operand of them would reach 4 GiB (at rank 256 from 2^21 tokens, d_in or rows of
+// both weights on, at rank 64 from 2^23; up to rank 16 one term is as long)
 inline int gated_terms(int64_t d_ff, int64_t d_in, int64_t M, int r) {
     const int64_t rows = M > d_in ? M : d_in;
     return r == 0 || (rows > 2 * d_ff ? rows : 2 * d_ff) <= ((int64_t{1} << 31) - 1) / gated_k2(r, 2) ? 2 : 1;

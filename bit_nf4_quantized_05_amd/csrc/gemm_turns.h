@@ -18,10 +18,10 @@
 // queue before the tile's last steps. Eight halves, 128 KB of LDS.
 // In 4096 x 4096 x 16128, one round of tiles, the matrix pipes are busy 76 to 79 % of the kernel's cycles
 // (MfmaUtil; MFMA cycles over GRBM_GUI_ACTIVE) at the 1.8 GHz that this load leaves (the chip is
-// power-limited); with more rounds, each with its start and epilogue, 60 to 70 %. It takes 350 us (1.54 PFLOP/s), the library's product 342 on the same
-// board. Four phases of 16 MFMAs took the same; 32 x 32 x 16 MFMAs on the same schedule 394. With Q's
-// rows along K (8-byte LDS reads that transpose, twice as many) it takes 353: the transposed copy
-// that the other form needs cost 88 more.
+// power-limited); with more rounds, each with its start and epilogue, 60 to 70 %. It takes 350 us (1.54
+// PFLOP/s), the library's product 342 on the same board. Four phases of 16 MFMAs took the same; 32 x 32 x
+// 16 MFMAs on the same schedule 394. With Q's rows along K (8-byte LDS reads that transpose, twice as many)
+// it takes 353: the transposed copy that the other form needs cost 88 more.
 #pragma once
 #include <hip/hip_runtime.h>
 

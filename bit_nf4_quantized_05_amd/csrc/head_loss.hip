@@ -13,8 +13,9 @@
 // with W in the same pass and the sums divided at the end. Two products where forming the
 // logits again for the gradient would take three. (The exponentials' rounding, 2^-9 at most of each of many
 // terms, moves dX by 0.0002 to 0.0007, relative, beside the 0.0017 of its own; a second term would be a
-// third product.) Where z_v - z_y is large (past kMaxLog2 in powers of two) a 256-wide tile of a row is scaled down by a power of two, and head_join brings
-// the row to one scale: exact in every case, and no work where it does not happen.
+// third product.) Where z_v - z_y is large (past kMaxLog2 in powers of two) a tile of a row is scaled down
+// by a power of two, and head_join brings the row to one scale: exact in every case, and no work where it
+// does not happen.
 //
 // Tokens without a target (prompts, padding) are left out before the products: head_plan_kernel
 // numbers the others, the GEMM gathers their rows, and workgroups past the last one end at once.

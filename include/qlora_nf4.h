@@ -421,8 +421,8 @@ int64_t qlora_gated_bwd_workspace_bytes(int64_t d_ff, int64_t d_in, int64_t d_se
  * columns 0 .. d_ff - 1 and U in the d_ff columns after, bf16 [d_seq, 2 d_ff], for the gradient.
  * H is formed from the float32 sums of G and U and rounded once. s A x keeps 16 bits or more (float32
  * or two bf16 terms), as s B^T dY does in the gradient; 8 (one term) where two terms would reach 4 GiB:
- * r above 128 with a million rows of a weight or two million tokens. An infinity or NaN in X stays in its
- * token's row; one in an adapter may show as NaN in both G and U.
+ * from 2 million tokens (d_in, or rows of both weights) on at rank 256, 8 million at rank 64. An infinity
+ * or NaN in X stays in its token's row; one in an adapter may show as NaN in both G and U.
  */
 int qlora_gated_fwd(const uint8_t* codes_g, const int8_t* qconst_g, const float* qscale_g, const float* qmean_g,
                     const uint8_t* codes_u, const int8_t* qconst_u, const float* qscale_u, const float* qmean_u,
@@ -466,11 +466,11 @@ int64_t qlora_head_loss_workspace_bytes(int64_t vocab, int64_t d_in, int64_t d_s
  *   scale   float32 [d_seq] or NULL (1): e.g. 1 / counted tokens for a mean
  *   loss    float32 [d_seq] (not scaled);  dX bf16 [d_seq, d_in] or NULL
  * d_in a multiple of 64; any vocab of a bf16 head; -2 where 256 rows (or all, of a smaller head) at
- * their row stride reach 4 GiB. The logits are float32 sums; dX multiplies the
- * exponentials rounded to bf16 (float32 sums; the target's own column is kept apart in float32). A
- * token with an infinite or NaN logit may have a NaN or infinite loss and dX; no other token is
- * touched by it. The result is deterministic. Strides, alignment and errors as qlora_linear_fwd_ex; outputs and the workspace must
- * not overlap an input, or each other.
+ * their row stride reach 4 GiB. The logits are float32 sums; dX multiplies the exponentials rounded to
+ * bf16 (float32 sums; the target's own column is kept apart in float32). A token with an infinite or
+ * NaN logit may have a NaN or infinite loss and dX; no other token is touched by it. The result is
+ * deterministic. Strides, alignment and errors as qlora_linear_fwd_ex; outputs and the workspace must not
+ * overlap an input, or each other.
  */
 int qlora_head_loss(const uint16_t* W, int64_t ldw, const uint8_t* codes, const int8_t* qconst, const float* qscale,
                     const float* qmean, int dq, int64_t vocab, int64_t d_in, const uint16_t* X, int64_t ldx, int64_t d_seq,
